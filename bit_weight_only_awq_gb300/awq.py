@@ -24,12 +24,14 @@ lib = ctypes.CDLL(_LIB_PATH)
 
 STATUS = {0: "AWQ_OK", -1: "AWQ_EINVAL", -2: "AWQ_EALIGN", -3: "AWQ_EARCH", -4: "AWQ_ECUDA",
           -5: "AWQ_ETIMEOUT", -6: "AWQ_EWORKSPACE", -7: "AWQ_ENULL"}
+FP16, BF16 = 0, 1
 OP_GEMV, OP_GEMM, OP_W4A8_GEMM, OP_GEMV_PREPACKED, OP_GEMV_BF16, OP_GEMM_BF16, OP_W4A8_GROUPED = 0, 1, 2, 3, 4, 5, 6
 GROUP_SIZE = 128
 
 _p = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
+_f32 = ctypes.c_float
 _sz = ctypes.c_size_t
 
 _SIGS = {
@@ -55,6 +57,15 @@ _SIGS = {
     "awq_gemv_prepacked": (_i32, [_p, _p, _p, _i64, _i64, _i64, _i32, _p, _sz, _p]),
     "w4a8_gemm_grouped": (_i32, [_p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i32, _i32, _p, _sz, _p]),
     "w4a8_linear_grouped": (_i32, [_p, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i32, _i32, _p, _sz, _p]),
+    "w4a8_rmsnorm_quant": (_i32, [_p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, _f32, _i32, _p]),
+    "awq_rmsnorm": (_i32, [_p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, _f32, _i32, _p]),
+    "kv4_cache_bytes": (_sz, [_i64, _i32, _i32, _i32]),
+    "kv4_append": (_i32, [_p, _p, _p, _i64, _i64, _i64, _p, _p, _p, _i64, _i32, _i32, _p, _i64, _p, _i64, _i64, _i32,
+                          _i32, _i32, _i32, _i32, _p]),
+    "kv4_gather": (_i32, [_p, _p, _p, _p, _i64, _i64, _i32, _i32, _i32, _i32, _p]),
+    "kv4_attention_workspace_bytes": (_sz, [_i64, _i64, _i32, _i32, _i32, _i32]),
+    "kv4_attention": (_i32, [_p, _i64, _p, _p, _i64, _p, _p, _p, _p, _i64, _i64, _i32, _i32, _i32, _i32, _i64, _i32,
+                             _i32, _f32, _i32, _i32, _p, _sz, _p]),
     "awq_last_device_error": (_i32, [ctypes.POINTER(_i32)]),
     "awq_selftest_wait_timeout": (_i32, [_i64, _p]),
 }
@@ -68,7 +79,7 @@ def header_functions() -> list[str]:
     """Names of the functions declared in include/awq.h."""
     with open(_HEADER) as fh:
         text = fh.read()
-    return sorted(set(re.findall(r"^\s*(?:const\s+)?[a-z_0-9]+\s*\*?\s*((?:awq|w4a8)_[a-z0-9_]+)\s*\(", text, re.M)))
+    return sorted(set(re.findall(r"^\s*(?:const\s+)?[a-z_0-9]+\s*\*?\s*((?:awq|w4a8|kv4)_[a-z0-9_]+)\s*\(", text, re.M)))
 
 
 class AwqError(RuntimeError):
@@ -368,6 +379,203 @@ def w4a8_linear_grouped(x, wq, s3, s2, split_k: int = 0, out=None, acc_out=None,
                                                           _ptr(acc_out), _ptr(xq_out), _ptr(s_tok), M, K, N,
                                                           GROUP_SIZE, split_k, _ptr(ws), nbytes, _stream(stream)))
     return out, s_tok
+
+
+# ---- the operators between the linear layers of a decoder block
+
+_DTYPES = {torch.float16: FP16, torch.bfloat16: BF16}
+
+
+def _dtype16(name: str, *tensors) -> int:
+    """The awq_dtype shared by all given tensors."""
+    dtype = tensors[0].dtype
+    if dtype not in _DTYPES or any(t is not None and t.dtype != dtype for t in tensors):
+        raise TypeError(f"{name} takes fp16 or bf16 operands of one type")
+    return _DTYPES[dtype]
+
+
+def _need(name: str, dtype, *tensors) -> None:
+    for t in tensors:
+        if t is not None and (t.dtype != dtype or not t.is_contiguous()):
+            raise TypeError(f"{name}: expected a contiguous {dtype} tensor")
+
+
+def _row_stride(name: str, t) -> int:
+    """Elements from one row (token) to the next; inside a row everything is dense."""
+    inner = 1
+    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size != 1 and stride != inner:
+            raise ValueError(f"{name}: heads and channels of a token must be dense")
+        inner *= size
+    return max(t.stride(0), inner) if t.shape[0] <= 1 else t.stride(0)
+
+
+def _rmsnorm_args(name, x, weight, residual, res_out):
+    M, K = x.shape
+    dtype = _dtype16(name, x, weight, residual, res_out)
+    if weight.shape != (K,) or (residual is not None and residual.shape != x.shape):
+        raise ValueError(f"{name}: weight [K] and residual [M, K] go with x [M, K]")
+    if residual is not None and res_out is None:
+        res_out = torch.empty((M, K), dtype=x.dtype, device=x.device)
+    _need(name, x.dtype, weight, res_out)
+    rs = 0 if residual is None else _row_stride(name, residual)
+    return M, K, dtype, res_out, _row_stride(name, x), rs
+
+
+def w4a8_rmsnorm_quant(x, weight, residual=None, eps: float = 1e-6, res_out=None, y=None, xq=None, s_tok=None,
+                       stream=None):
+    """Residual addition, RMS norm and int8 codes of x [M, K]: (xq, s_tok, res_out), the first two as
+    w4a8_gemm takes them; res_out (x + residual) is None without a residual.  `y`, when given, receives the
+    normalized rows too.  res_out may be `x` or `residual` itself."""
+    M, K, dtype, res_out, xs, rs = _rmsnorm_args("w4a8_rmsnorm_quant", x, weight, residual, res_out)
+    if xq is None:
+        xq = torch.empty((M, K), dtype=torch.int8, device=x.device)
+    if s_tok is None:
+        s_tok = torch.empty((M,), dtype=torch.float32, device=x.device)
+    _check("w4a8_rmsnorm_quant", lib.w4a8_rmsnorm_quant(_ptr(x), _ptr(residual), _ptr(weight), _ptr(res_out), _ptr(y),
+                                                        _ptr(xq), _ptr(s_tok), M, K, xs, rs, eps, dtype,
+                                                        _stream(stream)))
+    return xq, s_tok, res_out
+
+
+def awq_rmsnorm(x, weight, residual=None, eps: float = 1e-6, res_out=None, out=None, stream=None):
+    """Residual addition and RMS norm of x [M, K] in its own type: (y, res_out), for the W4A16 layers."""
+    M, K, dtype, res_out, xs, rs = _rmsnorm_args("awq_rmsnorm", x, weight, residual, res_out)
+    if out is None:
+        out = torch.empty((M, K), dtype=x.dtype, device=x.device)
+    _check("awq_rmsnorm", lib.awq_rmsnorm(_ptr(x), _ptr(residual), _ptr(weight), _ptr(res_out), _ptr(out), M, K, xs,
+                                          rs, eps, dtype, _stream(stream)))
+    return out, res_out
+
+
+KV4_UNIT = 16  # tokens of a cache unit
+
+
+def kv4_cache(num_pages: int, kv_heads: int, head_dim: int, page_size: int = 64, device="cuda") -> torch.Tensor:
+    """A zeroed 4-bit cache of one layer: uint8 [num_pages, kv_heads, page_size / 16, 16 * head_dim + 128]
+    (units as include/awq.h lays them out).  The kv4_* calls read their sizes from this shape."""
+    if num_pages < 1 or lib.kv4_cache_bytes(num_pages, kv_heads, head_dim, page_size) == 0:
+        raise AwqError("kv4_cache", -1)
+    return torch.zeros((num_pages, kv_heads, page_size // KV4_UNIT, KV4_UNIT * head_dim + 128), dtype=torch.uint8,
+                       device=device)
+
+
+def _kv4_shape(name, cache):
+    """(num_pages, kv_heads, head_dim, page_size) of a cache tensor."""
+    if cache.dtype != torch.uint8 or cache.dim() != 4 or not cache.is_contiguous():
+        raise TypeError(f"{name}: the cache is a contiguous uint8 tensor [pages, kv_heads, page_size / 16, unit]")
+    pages, kv_heads, units, unit = cache.shape
+    return pages, kv_heads, (unit - 128) // KV4_UNIT if unit % KV4_UNIT == 0 else 0, units * KV4_UNIT
+
+
+def kv4_append(cache, k, v, positions, slots, table, q=None, interleaved: bool = False, q_out=None, stream=None):
+    """Rotates q and k (table fp32 [max_pos, rot_dim]: cosines, then sines; None for no rotation) and writes k
+    and v [T, kv_heads, D], quantized, to `slots` of the cache.  Returns the rotated queries (None without q)."""
+    pages, kv_heads, dim, page = _kv4_shape("kv4_append", cache)
+    dtype = _dtype16("kv4_append", k, v, q, q_out)
+    T = k.shape[0]
+    if k.shape != (T, kv_heads, dim) or v.shape != k.shape or slots.shape != (T,):
+        raise ValueError("kv4_append: k, v [T, kv_heads, head_dim] and slots [T] go with the cache")
+    _need("kv4_append", torch.int64, slots)
+    heads, rot, max_pos, qs, qos = 0, 0, 0, 0, 0
+    if q is not None:
+        heads = q.shape[1]
+        if q.shape != (T, heads, dim):
+            raise ValueError("kv4_append: q is [T, heads, head_dim]")
+        if q_out is None:
+            q_out = torch.empty((T, heads, dim), dtype=q.dtype, device=q.device)
+        elif q_out.shape != q.shape:
+            raise ValueError("kv4_append: q_out has another shape than q")
+        qs, qos = _row_stride("kv4_append", q), _row_stride("kv4_append", q_out)
+    if table is not None:
+        max_pos, rot = table.shape
+        _need("kv4_append", torch.float32, table)
+        _need("kv4_append", torch.int32, positions)
+        if positions.shape != (T,):
+            raise ValueError("kv4_append: positions is [T]")
+    _check("kv4_append", lib.kv4_append(
+        _ptr(q), _ptr(k), _ptr(v), qs, _row_stride("kv4_append", k), _row_stride("kv4_append", v), _ptr(positions),
+        _ptr(slots), _ptr(table), max_pos, rot, int(interleaved), _ptr(q_out), qos, _ptr(cache), pages, T, heads,
+        kv_heads, dim, page, dtype, _stream(stream)))
+    return q_out
+
+
+def kv4_gather(cache, slots, dtype=torch.float16, k=None, v=None, stream=None):
+    """The keys and values [T, kv_heads, head_dim] that the cache holds at `slots`."""
+    pages, kv_heads, dim, page = _kv4_shape("kv4_gather", cache)
+    T = slots.shape[0]
+    if k is None:
+        k = torch.empty((T, kv_heads, dim), dtype=dtype, device=cache.device)
+    if v is None:
+        v = torch.empty((T, kv_heads, dim), dtype=dtype, device=cache.device)
+    kind = _dtype16("kv4_gather", k, v)
+    _need("kv4_gather", torch.int64, slots)
+    _need("kv4_gather", k.dtype, k, v)
+    if k.shape != (T, kv_heads, dim) or v.shape != k.shape:
+        raise ValueError("kv4_gather: k and v are [T, kv_heads, head_dim]")
+    _check("kv4_gather", lib.kv4_gather(_ptr(cache), _ptr(slots), _ptr(k), _ptr(v), pages, T, kv_heads, dim, page,
+                                        kind, _stream(stream)))
+    return k, v
+
+
+# Workspaces of kv4_attention by device and stream (calls on one stream may share one), grown on demand.
+_kv4_workspaces: dict[tuple, torch.Tensor] = {}
+
+
+def _kv4_workspace(nbytes: int, device: torch.device, stream) -> torch.Tensor | None:
+    if nbytes == 0:
+        return None
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    key = (device.index, stream.cuda_stream)
+    ws = _kv4_workspaces.get(key)
+    if ws is None or ws.numel() < nbytes:
+        with torch.cuda.stream(stream):  # zeroed, and later freed, in the order of its own stream
+            ws = _kv4_workspaces[key] = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    return ws
+
+
+def kv4_attention_workspace_bytes(T: int, B: int, max_q: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib.kv4_attention_workspace_bytes(T, B, max_q, heads, kv_heads, head_dim))
+
+
+def kv4_attention(q, cache, block_table, kv_len, q_start=None, max_q: int = 1, scale: float | None = None,
+                  window: int = 0, out=None, lse=None, workspace=None, stream=None):
+    """Causal attention of q [T, heads, D] over the cached tokens of each sequence.
+
+    block_table int32 [B, max_pages], kv_len int32 [B] (new tokens included).  Without q_start every sequence
+    has one query (T = B); with q_start int32 [B + 1] sequence b has the queries q_start[b] .. q_start[b + 1] - 1,
+    at most max_q, which are its last tokens.  scale: 1 / sqrt(D) by default; window: 0 or the number of keys a
+    query looks back over, its own included.  `lse` fp32 [T, heads], when given, receives the log-sum-exp.
+    """
+    pages, kv_heads, dim, page = _kv4_shape("kv4_attention", cache)
+    T, heads, qd = q.shape
+    B, max_pages = block_table.shape
+    dtype = _dtype16("kv4_attention", q, out)
+    if qd != dim or kv_len.shape != (B,) or (q_start is not None and q_start.shape != (B + 1,)):
+        raise ValueError("kv4_attention: q [T, heads, head_dim], kv_len [B] and q_start [B + 1] go with the cache and block_table [B, pages]")
+    _need("kv4_attention", torch.int32, kv_len, q_start)
+    if block_table.dtype != torch.int32 or (max_pages > 1 and block_table.stride(1) != 1):
+        raise TypeError("kv4_attention: block_table is int32 with dense rows")
+    if out is None:
+        out = torch.empty((T, heads, dim), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("kv4_attention: out is dense and has q's shape")
+    if lse is not None:
+        _need("kv4_attention", torch.float32, lse)
+        if lse.shape != (T, heads):
+            raise ValueError("kv4_attention: lse is [T, heads]")
+    if scale is None:
+        scale = dim ** -0.5
+    ws = workspace
+    if ws is None:
+        ws = _kv4_workspace(kv4_attention_workspace_bytes(T, B, max_q, heads, kv_heads, dim), q.device, stream)
+    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check("kv4_attention", lib.kv4_attention(
+        _ptr(q), _row_stride("kv4_attention", q), _ptr(cache), _ptr(block_table),
+        max(block_table.stride(0), max_pages), _ptr(kv_len), _ptr(q_start), _ptr(out), _ptr(lse), T, B, max_q, heads,
+        kv_heads, dim, pages, page, max_pages, scale, window, dtype, _ptr(ws), nbytes, _stream(stream)))
+    return out
 
 
 def awq_last_device_error() -> int:

@@ -482,6 +482,135 @@ awq_status w4a8_linear_grouped(const uint16_t* x, const int32_t* wq, const uint1
                               stream);
 }
 
+static awq_status rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, uint16_t* res_out,
+                          uint16_t* y, int8_t* xq, float* s_tok, int64_t M, int64_t K, int64_t x_stride,
+                          int64_t res_stride, float eps, awq_dtype dtype, awq_stream_t stream) {
+  if (M < 0 || M > INT32_MAX || K < 8 || K > kNormMaxK || K % 8 != 0 || x_stride < K || x_stride % 8 != 0 ||
+      !(eps >= 0.f) || (dtype != AWQ_FP16 && dtype != AWQ_BF16))
+    return AWQ_EINVAL;
+  if (residual && (res_stride < K || res_stride % 8 != 0)) return AWQ_EINVAL;
+  if (M == 0) return AWQ_OK;
+  if (!x || !weight) return AWQ_ENULL;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(res_out) || !aligned16(y) ||
+      !aligned16(xq) || (reinterpret_cast<uintptr_t>(s_tok) & 3u) != 0)
+    return AWQ_EALIGN;
+  awq_status st = check_arch();
+  if (st != AWQ_OK) return st;
+  return from_cuda(launch_rmsnorm(x, residual, weight, res_out, y, xq, s_tok, M, K, x_stride, res_stride, eps,
+                                  dtype == AWQ_BF16, (cudaStream_t)stream));
+}
+
+awq_status w4a8_rmsnorm_quant(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, uint16_t* res_out,
+                              uint16_t* y, int8_t* xq, float* s_tok, int64_t M, int64_t K, int64_t x_stride,
+                              int64_t res_stride, float eps, awq_dtype dtype, awq_stream_t stream) {
+  if (M > 0 && (!xq || !s_tok)) return AWQ_ENULL;
+  return rmsnorm(x, residual, weight, res_out, y, xq, s_tok, M, K, x_stride, res_stride, eps, dtype, stream);
+}
+
+awq_status awq_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, uint16_t* res_out,
+                       uint16_t* y, int64_t M, int64_t K, int64_t x_stride, int64_t res_stride, float eps,
+                       awq_dtype dtype, awq_stream_t stream) {
+  if (M > 0 && !y) return AWQ_ENULL;
+  return rmsnorm(x, residual, weight, res_out, y, nullptr, nullptr, M, K, x_stride, res_stride, eps, dtype, stream);
+}
+
+static bool kv4_shape_ok(int64_t num_pages, int32_t kv_heads, int32_t dim, int32_t page_size) {
+  return num_pages >= 0 && num_pages <= INT32_MAX && kv_heads >= 1 && kv_heads <= 1024 && (dim == 64 || dim == 128) &&
+         page_size >= 16 && page_size <= 1024 && page_size % 16 == 0 && (64 % page_size == 0 || page_size % 64 == 0);
+}
+
+size_t kv4_cache_bytes(int64_t num_pages, int32_t kv_heads, int32_t head_dim, int32_t page_size) {
+  if (!kv4_shape_ok(num_pages, kv_heads, head_dim, page_size)) return 0;
+  return (size_t)num_pages * kv_heads * (page_size / kKv4Unit) * kv4_unit_bytes(head_dim);
+}
+
+awq_status kv4_append(const uint16_t* q, const uint16_t* k, const uint16_t* v, int64_t q_stride, int64_t k_stride,
+                      int64_t v_stride, const int32_t* positions, const int64_t* slots, const float* table,
+                      int64_t max_pos, int32_t rot_dim, int32_t interleaved, uint16_t* q_out, int64_t q_out_stride,
+                      void* cache, int64_t num_pages, int64_t T, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                      int32_t page_size, awq_dtype dtype, awq_stream_t stream) {
+  if (heads < 0 || heads > 1024 || kv_heads < 0 || !kv4_shape_ok(num_pages, kv_heads ? kv_heads : 1, head_dim, page_size))
+    return AWQ_EINVAL;
+  if (T < 0 || T > INT32_MAX || rot_dim < 0 || rot_dim > head_dim || rot_dim % 8 != 0 || max_pos < 0 ||
+      (dtype != AWQ_FP16 && dtype != AWQ_BF16))
+    return AWQ_EINVAL;
+  const int64_t qw = (int64_t)heads * head_dim, kw = (int64_t)kv_heads * head_dim;
+  if (heads && (q_stride < qw || q_stride % 8 != 0 || q_out_stride < qw || q_out_stride % 8 != 0)) return AWQ_EINVAL;
+  if (kv_heads && (k_stride < kw || k_stride % 8 != 0 || v_stride < kw || v_stride % 8 != 0)) return AWQ_EINVAL;
+  if (T == 0 || heads + kv_heads == 0) return AWQ_OK;
+  if ((heads && (!q || !q_out)) || (kv_heads && (!k || !v || !slots || !cache)) || (rot_dim && (!positions || !table)))
+    return AWQ_ENULL;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(cache) || !aligned16(table) ||
+      (reinterpret_cast<uintptr_t>(positions) & 3u) != 0 || (reinterpret_cast<uintptr_t>(slots) & 7u) != 0)
+    return AWQ_EALIGN;
+  awq_status st = check_arch();
+  if (st != AWQ_OK) return st;
+  const Kv4Rope rope{positions, table, max_pos, rot_dim, interleaved != 0};
+  return from_cuda(launch_kv4_append(q, k, v, q_stride, k_stride, v_stride, slots, rope, q_out, q_out_stride,
+                                     static_cast<uint8_t*>(cache), Kv4Shape{num_pages, kv_heads, head_dim, page_size}, T,
+                                     heads, dtype == AWQ_BF16, (cudaStream_t)stream));
+}
+
+awq_status kv4_gather(const void* cache, const int64_t* slots, uint16_t* k, uint16_t* v, int64_t num_pages, int64_t T,
+                      int32_t kv_heads, int32_t head_dim, int32_t page_size, awq_dtype dtype, awq_stream_t stream) {
+  if (!kv4_shape_ok(num_pages, kv_heads, head_dim, page_size) || T < 0 || T > INT32_MAX ||
+      (dtype != AWQ_FP16 && dtype != AWQ_BF16))
+    return AWQ_EINVAL;
+  if (T == 0 || (!k && !v)) return AWQ_OK;
+  if (!cache || !slots) return AWQ_ENULL;
+  if (!aligned16(cache) || !aligned16(k) || !aligned16(v) || (reinterpret_cast<uintptr_t>(slots) & 7u) != 0)
+    return AWQ_EALIGN;
+  awq_status st = check_arch();
+  if (st != AWQ_OK) return st;
+  return from_cuda(launch_kv4_gather(static_cast<const uint8_t*>(cache), slots, k, v,
+                                     Kv4Shape{num_pages, kv_heads, head_dim, page_size}, T, dtype == AWQ_BF16,
+                                     (cudaStream_t)stream));
+}
+
+static bool kv4_attention_shape_ok(int64_t T, int64_t B, int32_t max_q, int32_t heads, int32_t kv_heads, int32_t dim) {
+  return T >= 0 && T <= INT32_MAX && B >= 0 && B <= kKv4MaxSeqs && max_q >= 1 && heads >= 1 && heads <= 1024 &&
+         kv_heads >= 1 && heads % kv_heads == 0 && (dim == 64 || dim == 128);
+}
+
+size_t kv4_attention_workspace_bytes(int64_t T, int64_t B, int32_t max_q, int32_t heads, int32_t kv_heads,
+                                     int32_t head_dim) {
+  if (!kv4_attention_shape_ok(T, B, max_q, heads, kv_heads, head_dim)) return 0;
+  return kv4_attention_workspace(T, B, max_q, heads, kv_heads, head_dim);
+}
+
+awq_status kv4_attention(const uint16_t* q, int64_t q_stride, const void* cache, const int32_t* block_table,
+                         int64_t table_stride, const int32_t* kv_len, const int32_t* q_start, uint16_t* out, float* lse,
+                         int64_t T, int64_t B, int32_t max_q, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                         int64_t num_pages, int32_t page_size, int32_t max_pages, float scale, int32_t window,
+                         awq_dtype dtype, void* workspace, size_t workspace_bytes, awq_stream_t stream) {
+  if (!kv4_attention_shape_ok(T, B, max_q, heads, kv_heads, head_dim) ||
+      !kv4_shape_ok(num_pages, kv_heads, head_dim, page_size) || num_pages < 1)
+    return AWQ_EINVAL;
+  if (q_stride < (int64_t)heads * head_dim || q_stride % 8 != 0 || max_pages < 1 || table_stride < max_pages ||
+      (int64_t)max_pages * page_size > INT32_MAX - 1024 || !(scale - scale == 0.f) || window < 0 ||
+      (dtype != AWQ_FP16 && dtype != AWQ_BF16))
+    return AWQ_EINVAL;
+  if (!q_start && (T != B || max_q != 1)) return AWQ_EINVAL;
+  if (T == 0 || B == 0) return AWQ_OK;
+  if (!q || !cache || !block_table || !kv_len || !out) return AWQ_ENULL;
+  if (!aligned16(q) || !aligned16(cache) || !aligned16(out) || (reinterpret_cast<uintptr_t>(block_table) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(kv_len) & 3u) != 0 || (reinterpret_cast<uintptr_t>(q_start) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
+    return AWQ_EALIGN;
+  awq_status st = check_workspace(kv4_attention_workspace(T, B, max_q, heads, kv_heads, head_dim), workspace,
+                                  workspace_bytes);
+  if (st != AWQ_OK) return st;
+  st = check_arch();
+  if (st != AWQ_OK) return st;
+  int* err = device_error_ptr();
+  if (!err) return AWQ_ECUDA;
+  const Kv4AttnArgs a{q,     q_stride, static_cast<const uint8_t*>(cache), block_table, table_stride, kv_len,
+                      q_start, out,    lse,                                T,           (int)B,       max_q,
+                      heads, kv_heads, num_pages,                          page_size,   max_pages,    scale,
+                      window};
+  return from_cuda(launch_kv4_attention(a, head_dim, dtype == AWQ_BF16, workspace, err, (cudaStream_t)stream));
+}
+
 awq_status awq_last_device_error(int32_t* code) {
   if (!code) return AWQ_ENULL;
   *code = 0;

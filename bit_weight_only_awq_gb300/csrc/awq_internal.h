@@ -134,4 +134,63 @@ cudaError_t launch_quant_act(const uint16_t* x, int8_t* xq, float* s_tok, int64_
                              cudaStream_t s, uint16_t* x16 = nullptr);
 cudaError_t launch_i8_to_f16(const int8_t* xq, uint16_t* x16, int64_t count, cudaStream_t s);
 
+// ---- RMS norm with residual and int8 codes (w4a8_rmsnorm.cu); y, res_out, and xq with s_tok when not null
+constexpr int64_t kNormMaxK = 65536;
+cudaError_t launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, uint16_t* res_out,
+                           uint16_t* y, int8_t* xq, float* s_tok, int64_t M, int64_t K, int64_t x_stride,
+                           int64_t res_stride, float eps, bool bf16, cudaStream_t s);
+
+// ---- 4-bit paged cache (kv4_cache.cu, kv4_attention.cu).  Layout of a unit (16 tokens of one head): include/awq.h.
+constexpr int kKv4Unit = 16;
+constexpr int kKv4MaxSeqs = 4096;
+__host__ __device__ constexpr int kv4_unit_bytes(int dim) { return 16 * dim + 128; }
+// Byte offsets inside a unit: a token's key row, the 16-bit half of value channels 4c..4c+3, the token's four fp16.
+__host__ __device__ constexpr int kv4_key_offset(int dim, int token) { return token * (dim / 2); }
+__host__ __device__ constexpr int kv4_value_offset(int dim, int token, int channel) {
+  return 8 * dim +
+         ((((token / 8) * 8 + channel / (dim / 8)) * 4 + token % 8 / 2) * (dim / 32) + channel % (dim / 8) / 4) * 4 +
+         (token % 2) * 2;
+}
+__host__ __device__ constexpr int kv4_meta_offset(int dim, int token) { return 16 * dim + token * 8; }
+static_assert(kv4_value_offset(128, 15, 127) + 2 == 16 * 128 && kv4_value_offset(64, 15, 63) + 2 == 16 * 64,
+              "value halves fill their region");
+
+struct Kv4Shape {
+  int64_t num_pages;
+  int kv_heads, dim, page_size;
+};
+struct Kv4Rope {
+  const int32_t* positions;
+  const float* table;
+  int64_t max_pos;
+  int rot;
+  bool interleaved;
+};
+cudaError_t launch_kv4_append(const uint16_t* q, const uint16_t* k, const uint16_t* v, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride, const int64_t* slots, const Kv4Rope& rope,
+                              uint16_t* q_out, int64_t q_out_stride, uint8_t* cache, const Kv4Shape& c, int64_t T,
+                              int heads, bool bf16, cudaStream_t s);
+cudaError_t launch_kv4_gather(const uint8_t* cache, const int64_t* slots, uint16_t* k, uint16_t* v, const Kv4Shape& c,
+                              int64_t T, bool bf16, cudaStream_t s);
+
+struct Kv4AttnArgs {
+  const uint16_t* q;
+  int64_t q_stride;
+  const uint8_t* cache;
+  const int32_t* block_table;
+  int64_t table_stride;
+  const int32_t* kv_len;
+  const int32_t* q_start;  // nullptr: one query for each sequence
+  uint16_t* out;
+  float* lse;  // nullptr: not wanted
+  int64_t T;
+  int B, max_q, heads, kv_heads;
+  int64_t num_pages;
+  int page_size, max_pages;
+  float scale;
+  int window;
+};
+size_t kv4_attention_workspace(int64_t T, int64_t B, int max_q, int heads, int kv_heads, int dim);
+cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, int dim, bool bf16, void* ws, int* err, cudaStream_t s);
+
 }  // namespace awq

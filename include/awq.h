@@ -1,6 +1,7 @@
 /*
  * awq.h -- C ABI of libawq, a GB300 (sm_103a) implementation of the group-wise
- * INT4 weight-only quantized linear layer (AWQ W4A16) and its W4A8 variant.
+ * INT4 weight-only quantized linear layer (AWQ W4A16) and its W4A8 variant, with
+ * the operators that stand between such layers in a decoder block.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -381,6 +382,127 @@ awq_status w4a8_linear_grouped(const uint16_t *x, const int32_t *wq, const uint1
                                float *s_tok, int64_t M, int64_t K, int64_t N, int32_t group_size,
                                int32_t split_k, void *workspace, size_t workspace_bytes,
                                awq_stream_t stream);
+
+/*
+ * Operators between the quantized linear layers of a decoder block
+ * ----------------------------------------------------------------
+ * The norm that feeds a quantized linear layer, the append of new keys and values to a paged cache
+ * held in 4 bits, and attention over that cache.  `dtype` names the type of the 16-bit operands;
+ * statistics, rotations and sums are fp32.  Row strides are in elements; inside a row, heads and
+ * channels are dense.  The pages describe none of them: they name the models these layers sit in
+ * (Llama-2-7B, Mistral-7B, Llama-3.1-8B), whose block is norm - qkv - rotation - attention - o_proj.
+ */
+typedef enum { AWQ_FP16 = 0, AWQ_BF16 = 1 } awq_dtype;
+
+/*
+ * w4a8_rmsnorm_quant -- residual addition, root-mean-square norm and per-token int8 codes: the
+ * operands xq and s_tok of w4a8_gemm / w4a8_gemm_grouped, in one pass over the row.
+ *   h = x + residual (fp32; h = x when residual is NULL), res_out = RN(h)
+ *   y = h * w / sqrt(mean(h^2) + eps)
+ *   s_tok = max|y| / 127, xq = rint(y / s_tok)
+ * The norm's factor divides out of y / s_tok, so the codes are computed as rint(t / (max|t| / 127)) with
+ * t = h * w in fp32 (each operation rounded once): they do not depend on the order of the sum of squares.
+ * Unlike w4a8_quant_act's, the scale is not rounded to fp16: the row is never held in fp16.
+ * x [M, K] with row stride x_stride; residual [M, K] with row stride res_stride, or NULL; weight [K];
+ * res_out [M, K] dense (output; NULL to skip; may be x or residual itself when that is dense);
+ * y [M, K] dense (the norm's rows, rounded once; NULL to skip); xq int8 [M, K]; s_tok fp32 [M].
+ * A row of zeros gets s_tok = 0 and codes 0; a row holding a NaN or an infinity gets s_tok = NaN and
+ * codes 0, so that the product shows it.  K % 8 == 0, 8 <= K <= 65536, strides % 8 == 0 and >= K,
+ * eps >= 0.  M = 0 is a no-op.
+ */
+awq_status w4a8_rmsnorm_quant(const uint16_t *x, const uint16_t *residual, const uint16_t *weight,
+                              uint16_t *res_out, uint16_t *y, int8_t *xq, float *s_tok, int64_t M,
+                              int64_t K, int64_t x_stride, int64_t res_stride, float eps,
+                              awq_dtype dtype, awq_stream_t stream);
+
+/* awq_rmsnorm -- the same norm without codes, for awq_gemv / awq_gemm and their bf16 variants: writes y
+ * (required) and, when given, res_out. */
+awq_status awq_rmsnorm(const uint16_t *x, const uint16_t *residual, const uint16_t *weight,
+                       uint16_t *res_out, uint16_t *y, int64_t M, int64_t K, int64_t x_stride,
+                       int64_t res_stride, float eps, awq_dtype dtype, awq_stream_t stream);
+
+/*
+ * The 4-bit cache.  One layer's keys and values, in pages of page_size tokens, quantized for each token
+ * and head to codes u in 0..15 that stand for zero + u * scale (fp16 scale and zero, separate for key and
+ * value).  Layout: [num_pages][kv_heads][page_size / 16] units of 16 tokens of one head, each
+ * 16 * head_dim + 128 contiguous bytes:
+ *   - keys: token-major rows of head_dim / 2 bytes, the 32-bit words of eight channels in the AWQ order
+ *     (as awq_pack writes them);
+ *   - values: 16-bit halves of four channels, lowest nibble first, indexed [token / 8][channel / (D / 8)]
+ *     [token % 8 / 2][channel % (D / 8) / 4][token % 2] with D = head_dim;
+ *   - four fp16 for each token: key scale, key zero, value scale, value zero.
+ * A token's slot is page * page_size + its place in the page.  head_dim is 64 or 128, page_size a multiple
+ * of 16 up to 1024 that divides or is divided by 64.
+ *
+ * kv4_cache_bytes -- size of such a cache; 0 for a shape outside that.
+ */
+size_t kv4_cache_bytes(int64_t num_pages, int32_t kv_heads, int32_t head_dim, int32_t page_size);
+
+/*
+ * kv4_append -- rotates the queries and keys of T new tokens and writes the keys and values to the cache.
+ * q [T, heads, D], k, v [T, kv_heads, D] with token strides (they may be columns of one projection's
+ * output); q may be NULL with heads = 0, k and v NULL with kv_heads = 0 (no cache is touched then).
+ * positions int32 [T]; slots int64 [T]; table fp32 [max_pos, rot_dim]: for each position rot_dim / 2
+ * cosines, then rot_dim / 2 sines, so that every base, scaling and long-context rule is the caller's.
+ * rot_dim % 8 == 0, 0 <= rot_dim <= D: the first rot_dim channels of a head turn, in pairs (i, i +
+ * rot_dim / 2), or (2i, 2i + 1) when interleaved != 0; the others pass unchanged.  rot_dim = 0 needs no
+ * table and no positions.
+ *   a' = a c - b s, b' = b c + a s   (fp32, every operation rounded once)
+ *   scale = fp16_RN((max - min) / 15), zero = fp16_RN(min), u = clamp(rint((x - zero) / scale), 0, 15)
+ * over a head's D channels, from the unrounded fp32 x; scale and zero saturate at +-65504.  A head whose
+ * channels are all equal gets codes 0; one that holds a NaN or an infinity gets a NaN scale, so that what
+ * reads it shows it.
+ * q_out [T, heads, D] with token stride q_out_stride (may be q itself) receives the rotated queries.
+ * A token with slot < 0 (padding) or a slot beyond the cache writes no cache entry; one with a position
+ * outside [0, max_pos) writes none either, and its q_out row is zero.  Two tokens with the same slot in
+ * one call leave that entry unspecified.
+ */
+awq_status kv4_append(const uint16_t *q, const uint16_t *k, const uint16_t *v, int64_t q_stride,
+                      int64_t k_stride, int64_t v_stride, const int32_t *positions,
+                      const int64_t *slots, const float *table, int64_t max_pos, int32_t rot_dim,
+                      int32_t interleaved, uint16_t *q_out, int64_t q_out_stride, void *cache,
+                      int64_t num_pages, int64_t T, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                      int32_t page_size, awq_dtype dtype, awq_stream_t stream);
+
+/* kv4_gather -- reads the entries of `slots` int64 [T] back as k, v [T, kv_heads, head_dim] (dense; either
+ * may be NULL), zero + u * scale rounded once; zeros for a slot outside the cache. */
+awq_status kv4_gather(const void *cache, const int64_t *slots, uint16_t *k, uint16_t *v,
+                      int64_t num_pages, int64_t T, int32_t kv_heads, int32_t head_dim,
+                      int32_t page_size, awq_dtype dtype, awq_stream_t stream);
+
+/*
+ * kv4_attention -- softmax attention of T query tokens of B sequences over the cache.
+ * q [T, heads, D] with token stride q_stride; query head h reads cache head h / (heads / kv_heads).
+ * q_start int32 [B + 1]: sequence b's queries are tokens q_start[b] .. q_start[b + 1] - 1, at most max_q
+ * of them; NULL means one query for each sequence (T = B, max_q = 1).  kv_len int32 [B]: tokens of the
+ * sequence in the cache, the new ones included; the queries are its last ones, so query i of n sits at
+ * position p = kv_len - n + i and sees the keys j <= p, and j > p - window when window > 0.
+ * block_table int32 [B, max_pages] with row stride table_stride: the pages of each sequence in order.
+ *   S_j = scale * q . k_j,  out = sum_j exp(S_j) v_j / sum_j exp(S_j),  lse = ln sum_j exp(S_j)
+ * out [T, heads, D] dense, rounded once; lse fp32 [T, heads] or NULL.  A query that sees no key (p < 0, or
+ * kv_len = 0) gives zeros and lse = -inf.  What the cache holds at masked tokens, NaN included, does not
+ * matter.  Tokens that belong to no sequence are not written.
+ * Lengths, q_start and pages are read on the device only, so a captured graph follows them; lengths
+ * beyond max_pages * page_size and q_start beyond T are clamped, page numbers outside the cache read
+ * page 0: memory-safe, with unspecified results.  heads % kv_heads == 0, B <= 4096, finite scale,
+ * 0 <= window.
+ *
+ * The queries enter the tensor cores as fp16 after a power-of-two scaling of each row (exact for fp16 and
+ * bf16 down to 2^-24 of the row's largest), probabilities as fp16 times the value's scale, both with fp32
+ * sums; the result does not depend on timing or on other work on the GPU.
+ *
+ * Workspace: kv4_attention_workspace_bytes(), same contract as awq_gemv's (zero-filled once, each call
+ * leaves its counters at zero, calls that may run concurrently need separate ones).
+ */
+size_t kv4_attention_workspace_bytes(int64_t T, int64_t B, int32_t max_q, int32_t heads,
+                                     int32_t kv_heads, int32_t head_dim);
+awq_status kv4_attention(const uint16_t *q, int64_t q_stride, const void *cache,
+                         const int32_t *block_table, int64_t table_stride, const int32_t *kv_len,
+                         const int32_t *q_start, uint16_t *out, float *lse, int64_t T, int64_t B,
+                         int32_t max_q, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                         int64_t num_pages, int32_t page_size, int32_t max_pages, float scale,
+                         int32_t window, awq_dtype dtype, void *workspace, size_t workspace_bytes,
+                         awq_stream_t stream);
 
 /*
  * awq_last_device_error -- reads and clears the device-side error word of the

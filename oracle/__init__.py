@@ -33,3 +33,4 @@ from .awq_oracle import (  # noqa: F401
     PREPACK_UNIT_BYTES,
     prepack_gemv,
 )
+from . import block_oracle as block  # noqa: F401,E402  (the operators between the linear layers)

@@ -1,103 +1,697 @@
-// Attention over the 4-bit paged cache.
+// Attention over the 4-bit paged cache, one or a few new tokens for each sequence: HBM bound.
 //
 //   S_j = scale q . k_j,  out = sum_j exp(S_j - m) v_j / sum_j exp(S_j - m),  m the running maximum of S
 //
-// with keys and values zero + u * scale for each token and head (unit layout: include/awq.h).
+// with keys zk + u sk and values zv + u sv for each token and head (unit layout: include/awq.h), so that
+//
+//   S_j = scale (sk_j (q . u_j) + zk_j sum(q)),   sum_j p_j v_j = sum_j (p_j sv_j) u_j + sum_j p_j zv_j
+//
+// and only the products with the codes u need the tensor cores (mma.sync m16n8k16, fp32 sums).  A code in the low
+// bits of an fp16 half is the subnormal u 2^-24, exactly: one AND makes the operand register (two codes), with no
+// offset to subtract afterwards.  Every other register holds 16 u 2^-24 (the next nibble): for keys, the matching
+// query elements are divided by 16 beforehand; for values, the output rows are at the end.  The codes are the A
+// operand (16 tokens or 16 channels), the queries that share a cache head the 8 columns of B, so a column for
+// each of up to 8 query heads costs no more than one.
+//
+// Work.  The unit of work is a tile of 64 tokens of one (sequence, cache head, block of query columns).  All tiles
+// of the call, in that order, are cut into equal contiguous ranges, one for each warp of a persistent grid (one
+// CTA on each SM): the sequences' lengths are read on the device, and no warp waits for a longer one.  A warp
+// streams its tiles through its own ring of bulk copies.  Where a head's tiles are shared, the partial results
+// (maximum, sum, unnormalized output) are joined: inside a CTA after a barrier, across CTAs by the last one to
+// arrive, always in the order of the tiles, so that results do not depend on timing.
 #include <cmath>
 
 #include "awq_host.h"
 #include "awq_internal.h"
+#include "awq_ptx.cuh"
 #include "awq_types.cuh"
 
 namespace awq {
 namespace {
 
-constexpr int kSThreads = 128;  // keys of one step, and channels at most
+constexpr int kTile = 64;    // tokens of a tile: 4 units
+constexpr int kWarps = 12;   // three on each sub-partition
+constexpr int kThreads = 32 * kWarps;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kSThreads) kv4_attention_simple_kernel(Kv4AttnArgs a) {
-  __shared__ float qs[D];
-  __shared__ float red[4];
-  __shared__ float prob[kSThreads];
-  const int tid = threadIdx.x;
-  const int h = blockIdx.y, b = blockIdx.z;
-  const int begin = a.q_start ? min(max(a.q_start[b], 0), (int)a.T) : b;
-  const int end = a.q_start ? min(max(a.q_start[b + 1], begin), (int)a.T) : b + 1;
-  const int n = min(end - begin, a.max_q), i = blockIdx.x;
-  if (i >= n) return;
-  const int len = min(max(a.kv_len[b], 0), a.max_pages * a.page_size);
-  const int pos = len - n + i;
-  const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-  const int64_t row = (int64_t)(begin + i) * a.heads + h;
-  if (tid < D / 2) {
-    const float2 f = unpack2<BF16>(
-        reinterpret_cast<const uint32_t*>(a.q + (begin + i) * a.q_stride + h * D)[tid]);
-    qs[2 * tid] = f.x;
-    qs[2 * tid + 1] = f.y;
+template <int D>
+struct Geo {
+  static constexpr int kUnitBytes = kv4_unit_bytes(D);
+  static constexpr int kTileBytes = 4 * kUnitBytes;
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kRingBytes = kWarps * kStages * kTileBytes;
+  static constexpr int kSmemBytes = kRingBytes + 128;
+};
+
+// Floats of one partial result: the unnormalized output, then maximum and sum of every column.
+__host__ __device__ constexpr int part_floats(int dim, int cols) { return cols * (dim + 2); }
+
+// What a sequence asks for.
+struct Seq {
+  int begin, n;      // its query tokens
+  int len;           // cached tokens
+  int lo;            // the first token that any of its queries sees
+  int tiles, groups; // tiles of a (cache head, column block), and how many of those
+};
+
+template <int NT>
+__device__ __forceinline__ Seq seq_of(const Kv4AttnArgs& a, int b) {
+  Seq s;
+  s.begin = b;
+  s.n = 1;
+  if (a.q_start) {
+    s.begin = min(max(a.q_start[b], 0), (int)a.T);
+    s.n = min(min(max(a.q_start[b + 1], s.begin), (int)a.T) - s.begin, a.max_q);
   }
-  const int kvh = h / (a.heads / a.kv_heads), units = a.page_size / kKv4Unit;
-  const int* table = a.block_table + b * a.table_stride;
-  auto unit = [&](int j) {
-    int page = table[j / a.page_size];
-    if (page < 0 || page >= a.num_pages) page = 0;
-    return a.cache + (((int64_t)page * a.kv_heads + kvh) * units + j % a.page_size / kKv4Unit) * kv4_unit_bytes(D);
-  };
-  float m = -INFINITY, l = 0.f, acc = 0.f;
+  s.len = min(max(a.kv_len[b], 0), a.max_pages * a.page_size);
+  s.lo = a.window > 0 ? max(0, s.len - s.n + 1 - a.window) : 0;
+  s.lo = min(s.lo, s.len);
+  s.tiles = max(1, (s.len + kTile - 1) / kTile - s.lo / kTile);
+  const int per = a.heads / a.kv_heads;
+  s.groups = a.kv_heads * ((s.n * per + 8 * NT - 1) / (8 * NT));
+  return s;
+}
+
+// A position in the order of all tiles.
+struct Cursor {
+  int b, group, tile;
+  Seq s;
+};
+
+template <int NT>
+__device__ __forceinline__ void advance(const Kv4AttnArgs& a, Cursor& c) {
+  if (++c.tile < c.s.tiles) return;
+  c.tile = 0;
+  if (++c.group < c.s.groups) return;
+  c.group = 0;
+  do {
+    if (++c.b >= a.B) return;
+    c.s = seq_of<NT>(a, c.b);
+  } while (c.s.groups == 0);
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float col_max(float v) {  // over the 8 lanes that share columns
+  v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
+  v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
+  return fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
+}
+__device__ __forceinline__ float col_sum(float v) {
+  v += __shfl_xor_sync(0xFFFFFFFFu, v, 4);
+  v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
+  return v + __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+}
+template <int N>
+__device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  }
+}
+
+// Row `col` of a partial joins `total`: both rescaled to the larger maximum.
+struct Joined {
+  float m, l;
+  float4 o;
+};
+__device__ __forceinline__ void join(Joined& t, float m, float l, float4 o) {
+  const float top = fmaxf(t.m, m), base = top == -INFINITY ? 0.f : top;
+  const float x = ex2(t.m - base), y = ex2(m - base);
+  t.l = t.l * x + l * y;
+  t.o.x = t.o.x * x + o.x * y;
+  t.o.y = t.o.y * x + o.y * y;
+  t.o.z = t.o.z * x + o.z * y;
+  t.o.w = t.o.w * x + o.w * y;
+  t.m = top;
+}
+
+// The query token and head of a column, or false for a column beyond them.
+__device__ __forceinline__ bool row_of(const Kv4AttnArgs& a, const Seq& s, int kv_head, int col, int64_t& token, int& head) {
+  const int per = a.heads / a.kv_heads;
+  const int i = col / per;
+  token = s.begin + i;
+  head = kv_head * per + col - i * per;
+  return i < s.n;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store_joined(const Kv4AttnArgs& a, int dim, const Seq& s, int kv_head, int col, int c4,
+                                             const Joined& t) {
+  int64_t token;
+  int head;
+  if (!row_of(a, s, kv_head, col, token, head)) return;
+  const float inv = t.l == 0.f ? 0.f : 1.f / t.l;
+  const int64_t row = token * a.heads + head;
+  reinterpret_cast<uint2*>(a.out + row * dim)[c4] =
+      make_uint2(pack2<BF16>(t.o.x * inv, t.o.y * inv), pack2<BF16>(t.o.z * inv, t.o.w * inv));
+  if (a.lse && c4 == 0) a.lse[row] = t.l == 0.f ? -INFINITY : (t.m + log2f(t.l)) * kLn2;
+}
+
+// One partial of this CTA that does not cover its (sequence, head, column block).
+struct Desc {
+  long long first;  // the place of its tile 0 in the order of all tiles
+  int b, group;
+  const float* part;  // nullptr: none
+};
+
+template <int D, bool BF16, int NT>
+__global__ void __launch_bounds__(kThreads, 1)
+kv4_attention_kernel(const Kv4AttnArgs a, float* __restrict__ warp_parts, float* __restrict__ cta_parts, int* counters,
+                     int* err) {
+  using G = Geo<D>;
+  constexpr int kWords = D / 32;     // words of a lane for a token's keys, or for a token pair's values
+  constexpr int kCols = 8 * NT;
+  constexpr int kPart = part_floats(D, kCols);
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t bars[kWarps * G::kStages];
+  __shared__ long long before[kThreads];  // tiles before the sequences of each thread's share
+  __shared__ long long warp_total[kWarps];
+  __shared__ Desc desc[2 * kWarps];
+  __shared__ int abort_word, arrived;
+  volatile int* abort_flag = &abort_word;
+
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
+  uint8_t* ring = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u) + warp * G::kStages * G::kTileBytes;
+  if (lane < G::kStages) mbar_init(smem_u32(&bars[warp * G::kStages + lane]), 1);
+  if (lane < 2) desc[2 * warp + lane].part = nullptr;
+  if (tid == 0) abort_word = 0;
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // ---- the order of all tiles: thread i counts the tiles of sequences [i share, (i + 1) share)
+  const int share = (a.B + kThreads - 1) / kThreads;
+  long long mine = 0;
+  for (int b = tid * share; b < min(a.B, (tid + 1) * share); ++b) {
+    const Seq s = seq_of<NT>(a, b);
+    mine += (long long)s.tiles * s.groups;
+  }
+  long long upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 31) warp_total[warp] = upto;
   __syncthreads();
-  for (int j0 = lo / kSThreads * kSThreads; j0 <= pos; j0 += kSThreads) {
-    const int j = j0 + tid;
-    float s = -INFINITY;
-    if (j >= lo && j <= pos) {
-      const uint8_t* u = unit(j);
-      const float2 sz = unpack2<false>(*reinterpret_cast<const uint32_t*>(u + kv4_meta_offset(D, j % 16)));
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(u + kv4_key_offset(D, j % 16));
-      float dot = 0.f, sum = 0.f;
-      for (int c = 0; c < D; ++c) {
-        dot = fmaf(qs[c], (float)(w[c / 8] >> (4 * slot_of_col(c % 8)) & 15u), dot);
-        sum += qs[c];
-      }
-      s = a.scale * (sz.y * sum + sz.x * dot);
-    }
-    float top = s;
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    if (tid % 32 == 0) red[tid / 32] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])), m);
-    const float base = top == -INFINITY ? 0.f : top, old = expf(m - base);
-    prob[tid] = expf(s - base);
-    m = top;
-    __syncthreads();
-    l *= old;
-    acc *= old;
-    for (int t = 0; t < kSThreads; ++t) {
-      if (j0 + t < lo || j0 + t > pos) continue;  // the cache may hold anything there
-      l += prob[t];
-      if (tid < D) {
-        const uint8_t* u = unit(j0 + t);
-        const float2 sz = unpack2<false>(*reinterpret_cast<const uint32_t*>(u + kv4_meta_offset(D, (j0 + t) % 16) + 4));
-        const uint32_t half = *reinterpret_cast<const uint16_t*>(u + kv4_value_offset(D, (j0 + t) % 16, tid));
-        acc += prob[t] * (sz.y + sz.x * (float)(half >> (4 * (tid % 4)) & 15u));
-      }
-    }
-    __syncthreads();
+  long long total = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w == warp) before[tid] = total + upto - mine;
+    total += warp_total[w];
   }
-  if (tid < D) {
-    const uint32_t o = pack2<BF16>(l > 0.f || l != l ? acc / l : 0.f, 0.f);
-    a.out[row * D + tid] = (uint16_t)o;
+  __syncthreads();
+  const long long ctas = min((long long)gridDim.x, (total + kWarps - 1) / kWarps);
+  if (blockIdx.x >= ctas) return;
+
+  const long long warps = ctas * kWarps, me = (long long)blockIdx.x * kWarps + warp;
+  const long long u0 = me * total / warps, u1 = (me + 1) * total / warps;
+  const long long cta0 = (long long)blockIdx.x * total / ctas, cta1 = (long long)(blockIdx.x + 1) * total / ctas;
+  bool ok = true;
+
+  if (u0 < u1) {
+    // the sequence, head and tile of place u0
+    Cursor use;
+    {
+      int i = 0;
+#pragma unroll
+      for (int step = 256; step; step >>= 1)
+        if (i + step < kThreads && before[i + step] <= u0) i += step;
+      long long at = before[i];
+      use.b = i * share;
+      use.s = seq_of<NT>(a, use.b);
+      while (at + (long long)use.s.tiles * use.s.groups <= u0) {
+        at += (long long)use.s.tiles * use.s.groups;
+        use.s = seq_of<NT>(a, ++use.b);
+      }
+      const int rest = (int)(u0 - at);
+      use.group = rest / use.s.tiles;
+      use.tile = rest - use.group * use.s.tiles;
+    }
+    Cursor next = use;  // the tile to be copied next
+    const int count = (int)(u1 - u0);
+    const int units_page = a.page_size / kKv4Unit;
+    const int span = min(4, units_page);  // units that lie side by side in memory
+    const int per = a.heads / a.kv_heads;
+    const int blocks = next.s.groups / a.kv_heads;
+    int next_blocks = blocks;
+    const uint32_t bar0 = smem_u32(&bars[warp * G::kStages]);
+
+    // the page of lane i's unit (i < 4) of the tile at `next`
+    auto page_of = [&]() {
+      const int j = (next.s.lo / kTile + next.tile) * kTile + kKv4Unit * lane;
+      int page = 0;
+      if (lane < 4 && j < next.s.len) page = a.block_table[next.b * a.table_stride + j / a.page_size];
+      return page < 0 || page >= a.num_pages ? 0 : page;
+    };
+    int page = page_of();
+    auto issue = [&](int k) {  // copies tile k of this warp's range, the one at `next`
+      const int tile = next.s.lo / kTile + next.tile, j0 = tile * kTile;
+      const int first = max(0, (next.s.lo - j0) / kKv4Unit), last = min(4, (next.s.len - j0 + kKv4Unit - 1) / kKv4Unit);
+      const int st = k % G::kStages;
+      const uint32_t bar = bar0 + 8 * st;
+      if (lane == 0) mbar_arrive_tx(bar, max(0, last - first) * G::kUnitBytes);
+      __syncwarp();
+      const int from = max(lane, first), to = min(lane + span, last);
+      if (lane < 4 && lane % span == 0 && from < to) {
+        const int in_page = (j0 + kKv4Unit * from) % a.page_size / kKv4Unit;
+        const uint8_t* src = a.cache + (((int64_t)page * a.kv_heads + next.group / next_blocks) * units_page + in_page) * G::kUnitBytes;
+        bulk_load(smem_u32(ring + st * G::kTileBytes + from * G::kUnitBytes), src, (to - from) * G::kUnitBytes, bar);
+      }
+      const int b = next.b;
+      advance<NT>(a, next);
+      if (next.b != b && next.b < a.B) next_blocks = next.s.groups / a.kv_heads;
+      if (k + 1 < count) page = page_of();
+    };
+    int issued = 0;
+    while (issued < min(count, G::kStages)) issue(issued++);
+
+    // a head's state: queries, running maximum, sum, zero sum, output
+    uint32_t qf[NT][2 * kWords][2];
+    float qk[NT][2], qz[NT][2];    // per column: factor of the code product, of the key's zero (base 2)
+    int pos[NT][2];                // the last token it sees
+    float m[NT][2], l[NT][2], z[NT][2], o[NT][2 * kWords][4];
+    int vexp = 0;                  // probabilities enter fp16 as p sv 2^(13 - vexp)
+    int seg0 = 0;                  // the first tile of this warp in the current head
+
+    for (int k = 0; k < count; ++k) {
+      const int kv_head = use.group / (use.s.groups / a.kv_heads);
+      const int col0 = (use.group - kv_head * (use.s.groups / a.kv_heads)) * kCols;
+      if (k == 0 || use.tile == 0) {
+        seg0 = use.tile;
+        vexp = -16;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          // lane (g, t) loads channels [t D / 4, (t + 1) D / 4) of column g
+          int64_t token;
+          int head;
+          const bool in = row_of(a, use.s, kv_head, col0 + 8 * n + g, token, head);
+          float x[8 * kWords];
+          const uint4* src = reinterpret_cast<const uint4*>(a.q + token * a.q_stride + head * D + t * (D / 4));
+#pragma unroll
+          for (int i = 0; i < kWords; ++i) {
+            const uint4 v = in ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+              const float2 f = unpack2<BF16>(w[p]);
+              x[8 * i + 2 * p] = f.x;
+              x[8 * i + 2 * p + 1] = f.y;
+            }
+          }
+          float top = 0.f, sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8 * kWords; ++i) {
+            top = fmaxf(top, fabsf(x[i]));
+            sum += x[i];
+          }
+          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+          sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+          sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+          // a power of two takes the largest element to [2^10, 2^11): exact in fp16 down to 2^-24 of it
+          const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 127);
+          const float up = __uint_as_float((uint32_t)(127 + 10 - e) << 23);
+#pragma unroll
+          for (int i = 0; i < kWords; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float* y = x + 8 * i + 4 * h;
+              qf[n][2 * i + h][0] = pack2<false>(y[0] * up, y[1] * up);
+              qf[n][2 * i + h][1] = pack2<false>(y[2] * up * 0.0625f, y[3] * up * 0.0625f);
+            }
+          const float down = __uint_as_float((uint32_t)max(127 + e - 10, 1) << 23) * 16777216.f;
+          // the accumulator's columns of this lane are 2t and 2t + 1
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float d = __shfl_sync(0xFFFFFFFFu, down, 8 * t + 4 * c);
+            const float s = __shfl_sync(0xFFFFFFFFu, sum, 8 * t + 4 * c);
+            qk[n][c] = d * (a.scale * kLog2e);
+            qz[n][c] = s * (a.scale * kLog2e);
+            const int i = (col0 + 8 * n + 2 * t + c) / per;
+            pos[n][c] = i < use.s.n ? use.s.len - use.s.n + i : -1;
+            m[n][c] = -INFINITY;
+            l[n][c] = z[n][c] = 0.f;
+          }
+#pragma unroll
+          for (int i = 0; i < 2 * kWords; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[n][i][c] = 0.f;
+        }
+      }
+
+      const int st = k % G::kStages;
+      if (!__all_sync(0xFFFFFFFFu, wait_bounded(bar0 + 8 * st, (uint32_t)(k / G::kStages) & 1u, abort_flag, err, 601))) {
+        ok = false;
+        break;
+      }
+      const uint8_t* tile = ring + st * G::kTileBytes;
+      const int j0 = (use.s.lo / kTile + use.tile) * kTile;
+
+      // ---- scores: S[token][column], 16 tokens a unit
+      float s[NT][4][4];
+      uint2 meta[4][2];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint8_t* unit = tile + u * G::kUnitBytes;
+        uint32_t ka[kWords], kb[kWords];
+        lds_words<kWords>(unit + g * (D / 2) + t * (4 * kWords), ka);
+        lds_words<kWords>(unit + (g + 8) * (D / 2) + t * (4 * kWords), kb);
+        meta[u][0] = *reinterpret_cast<const uint2*>(unit + 16 * D + 8 * g);
+        meta[u][1] = *reinterpret_cast<const uint2*>(unit + 16 * D + 8 * (g + 8));
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[n][u][c] = 0.f;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t x = ka[i] >> (8 * h), y = kb[i] >> (8 * h);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              mma16816(s[n][u], x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u, qf[n][2 * i + h][0],
+                       qf[n][2 * i + h][1]);
+          }
+      }
+      // a tile that some column does not see whole: scales and zeros of tokens outside the sequence may be anything
+      const int pos_lo = use.s.len - use.s.n;  // the position of the first query
+      const bool edge = j0 + kTile > pos_lo + 1 || (a.window > 0 && j0 < use.s.len - a.window) || j0 < use.s.lo;
+      if (edge) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int j = j0 + 16 * u + 8 * r + g;
+            if (j < use.s.lo || j >= use.s.len) meta[u][r] = make_uint2(0u, 0u);
+          }
+      }
+      uint32_t vtop = 0;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float2 key = unpack2<false>(meta[u][r].x);
+          vtop = max(vtop, meta[u][r].y & 0x7FFFu);
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float& v = s[n][u][2 * r + c];
+              v = fmaf(key.x, v * qk[n][c], key.y * qz[n][c]);
+            }
+        }
+      if (edge) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int j = j0 + 16 * u + 8 * r + g;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                if (j > pos[n][c] || (a.window > 0 && j <= pos[n][c] - a.window)) s[n][u][2 * r + c] = -INFINITY;
+          }
+      }
+
+      // ---- running maximum; the largest value scale, rounded up to a power of two
+      vtop = __reduce_max_sync(0xFFFFFFFFu, vtop);
+      const int ve = max(vexp, (int)(vtop >> 10) - 14);
+      bool grown = ve != vexp;
+      float keep[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float top = m[n][c];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) top = fmaxf(top, fmaxf(s[n][u][c], s[n][u][2 + c]));
+          top = col_max(top);
+          grown |= top > m[n][c];
+          keep[n][c] = m[n][c];
+          m[n][c] = top;
+        }
+      if (__any_sync(0xFFFFFFFFu, grown)) {
+        const float shrink = __uint_as_float((uint32_t)(127 + vexp - ve) << 23);
+        vexp = ve;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float f = m[n][c] == -INFINITY ? 1.f : ex2(keep[n][c] - m[n][c]);
+            l[n][c] *= f;
+            z[n][c] *= f;
+#pragma unroll
+            for (int i = 0; i < 2 * kWords; ++i) {
+              o[n][i][c] *= f * shrink;
+              o[n][i][2 + c] *= f * shrink;
+            }
+          }
+      }
+
+      // ---- probabilities, and their products with the values' scales as the B operand [token][column]
+      const float vup = __uint_as_float((uint32_t)(127 + 13 - vexp) << 23);
+      float base[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) base[n][c] = m[n][c] == -INFINITY ? 0.f : m[n][c];
+      uint32_t pf[NT][4][2];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float2 val = unpack2<false>(meta[u][r].y);
+          const float w = val.x * vup;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float w0 = w, w1 = w, z0 = val.y, z1 = val.y;
+            if (edge) {  // a token hidden from one column and seen by another may hold a NaN
+              if (s[n][u][2 * r] == -INFINITY) w0 = z0 = 0.f;
+              if (s[n][u][2 * r + 1] == -INFINITY) w1 = z1 = 0.f;
+            }
+            const float p0 = ex2(s[n][u][2 * r] - base[n][0]), p1 = ex2(s[n][u][2 * r + 1] - base[n][1]);
+            l[n][0] += p0;
+            l[n][1] += p1;
+            z[n][0] = fmaf(p0, z0, z[n][0]);
+            z[n][1] = fmaf(p1, z1, z[n][1]);
+            pf[n][u][r] = transpose8x8(pack2<false>(p0 * w0, p1 * w1));
+          }
+        }
+
+      // ---- output: O[channel][column]
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint8_t* unit = tile + u * G::kUnitBytes + 8 * D;
+        uint32_t va[kWords], vb[kWords];
+        lds_words<kWords>(unit + lane * (4 * kWords), va);
+        lds_words<kWords>(unit + (32 + lane) * (4 * kWords), vb);
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t x = va[i] >> (8 * h), y = vb[i] >> (8 * h);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              mma16816(o[n][2 * i + h], x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u, pf[n][u][0],
+                       pf[n][u][1]);
+          }
+      }
+      __syncwarp();  // every lane has read the stage
+      const bool last = use.tile + 1 == use.s.tiles || k + 1 == count;
+      if (issued < count) issue(issued++);
+
+      if (last) {
+        const bool whole = seg0 == 0 && use.tile + 1 == use.s.tiles;
+        const float back = __uint_as_float((uint32_t)(127 + vexp - 13) << 23) * 16777216.f;
+        float* part = nullptr;
+        if (!whole) {
+          // the last partial of the range goes where the ring was, an earlier one to global memory
+          const bool end = k + 1 == count;
+          part = end ? reinterpret_cast<float*>(ring) : warp_parts + me * kPart;
+          if (lane == 0) {
+            Desc& d = desc[2 * warp + (end ? 1 : 0)];
+            d.first = u0 + k - use.tile;
+            d.b = use.b;
+            d.group = use.group;
+            d.part = part;
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float ls = col_sum(l[n][c]), zs = col_sum(z[n][c]);
+            const int col = 8 * n + 2 * t + c;
+            // this lane's channels are [g D / 8, (g + 1) D / 8)
+            if (whole) {
+              int64_t token;
+              int head;
+              if (row_of(a, use.s, kv_head, col0 + col, token, head)) {
+                const float inv = ls == 0.f ? 0.f : 1.f / ls;
+                const int64_t row = token * a.heads + head;
+                uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + row * D + g * (D / 8));
+                uint32_t w[2 * kWords];
+#pragma unroll
+                for (int i = 0; i < 2 * kWords; ++i)
+                  w[i] = pack2<BF16>((o[n][i][c] * back + zs) * inv, (o[n][i][2 + c] * (back * 0.0625f) + zs) * inv);
+#pragma unroll
+                for (int i = 0; i < kWords / 2; ++i)
+                  reinterpret_cast<uint4*>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                if (a.lse && g == 0) a.lse[row] = ls == 0.f ? -INFINITY : (m[n][c] + log2f(ls)) * kLn2;
+              }
+            } else {
+              float* dst = part + col * D + g * (D / 8);
+#pragma unroll
+              for (int i = 0; i < kWords; ++i)
+                reinterpret_cast<float4*>(dst)[i] =
+                    make_float4(o[n][2 * i][c] * back + zs, o[n][2 * i][2 + c] * (back * 0.0625f) + zs,
+                                o[n][2 * i + 1][c] * back + zs, o[n][2 * i + 1][2 + c] * (back * 0.0625f) + zs);
+              if (g == 0) {
+                part[kCols * D + col] = m[n][c];
+                part[kCols * D + kCols + col] = ls;
+              }
+            }
+          }
+      }
+      advance<NT>(a, use);
+    }
+    if (!ok) {
+      // leave no copy in flight behind: each one is waited for, with the same limit
+      int quiet = 0;
+      for (int k = max(0, issued - G::kStages); k < issued; ++k)
+        wait_bounded(bar0 + 8 * (k % G::kStages), (uint32_t)(k / G::kStages) & 1u, &quiet, err, 602);
+    }
   }
-  if (a.lse && tid == 0) a.lse[row] = l > 0.f || l != l ? m + logf(l) : -INFINITY;
+
+  // ---- the CTA's partials, in the order of the tiles
+  __syncthreads();
+  for (int i = 0; i < 2 * kWarps;) {
+    if (!desc[i].part) {
+      ++i;
+      continue;
+    }
+    const Desc d = desc[i];
+    int end = i + 1;
+    while (end < 2 * kWarps && (!desc[end].part || desc[end].first == d.first)) ++end;
+    const Seq s = seq_of<NT>(a, d.b);
+    const int blocks = s.groups / a.kv_heads;
+    const int kv_head = d.group / blocks, col0 = (d.group - kv_head * blocks) * kCols;
+    const long long d1 = d.first + s.tiles;
+    const bool whole = d.first >= cta0 && d1 <= cta1;
+    // a head shared with other CTAs: slot 1 when it goes on after this one, slot 0 when it ends here
+    float* out = cta_parts + (2 * blockIdx.x + (d1 > cta1 ? 1 : 0)) * (long long)kPart;
+    for (int e = tid; e < kCols * (D / 4); e += kThreads) {
+      const int col = e / (D / 4), c4 = e - col * (D / 4);
+      Joined j{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+      for (int p = i; p < end; ++p) {
+        const float* part = desc[p].part;
+        if (part)
+          join(j, part[kCols * D + col], part[kCols * D + kCols + col],
+               *reinterpret_cast<const float4*>(part + col * D + 4 * c4));
+      }
+      if (whole) {
+        store_joined<BF16>(a, D, s, kv_head, col0 + col, c4, j);
+      } else {
+        *reinterpret_cast<float4*>(out + col * D + 4 * c4) = j.o;
+        if (c4 == 0) {
+          out[kCols * D + col] = j.m;
+          out[kCols * D + kCols + col] = j.l;
+        }
+      }
+    }
+    if (!whole) {
+      const int c_first = (int)cta_of_unit(d.first, total, ctas), c_last = (int)cta_of_unit(d1 - 1, total, ctas);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        const int was = atomicAdd(&counters[c_first], 1);
+        arrived = was == c_last - c_first;
+        if (arrived) counters[c_first] = 0;  // for the next call
+        __threadfence();
+      }
+      __syncthreads();
+      if (arrived) {
+        for (int e = tid; e < kCols * (D / 4); e += kThreads) {
+          const int col = e / (D / 4), c4 = e - col * (D / 4);
+          Joined j{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll 4
+          for (int c = c_first; c <= c_last; ++c) {
+            const float* part = cta_parts + (2 * c + (c < c_last ? 1 : 0)) * (long long)kPart;
+            join(j, __ldcg(part + kCols * D + col), __ldcg(part + kCols * D + kCols + col),
+                 __ldcg(reinterpret_cast<const float4*>(part + col * D + 4 * c4)));
+          }
+          store_joined<BF16>(a, D, s, kv_head, col0 + col, c4, j);
+        }
+      }
+      __syncthreads();  // `arrived` is read before the next one is written
+    }
+    i = end;
+  }
+}
+
+// Eight columns hold a cache head's queries, or sixteen.
+bool narrow(int max_q, int heads, int kv_heads) { return (int64_t)max_q * (heads / kv_heads) <= 8; }
+
+template <int D, bool BF16, int NT>
+cudaError_t launch(const Kv4AttnArgs& a, void* ws, int* err, cudaStream_t s) {
+  const void* fn = reinterpret_cast<const void*>(kv4_attention_kernel<D, BF16, NT>);
+  cudaError_t e = set_smem_once(fn, Geo<D>::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  const int ctas = device_sm_count();
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  float* warp_parts = reinterpret_cast<float*>(base + kCounterBytes);
+  float* cta_parts = warp_parts + (size_t)ctas * kWarps * part_floats(D, 8 * NT);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Geo<D>::kSmemBytes;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kv4_attention_kernel<D, BF16, NT>, a, warp_parts, cta_parts, reinterpret_cast<int*>(base), err);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t kv4_attention_workspace(int64_t, int64_t, int, int, int, int) { return 0; }
+// Counters, a partial for each warp, and two for each CTA.
+size_t kv4_attention_workspace(int64_t, int64_t, int max_q, int heads, int kv_heads, int dim) {
+  const size_t part = sizeof(float) * part_floats(dim, narrow(max_q, heads, kv_heads) ? 8 : 16);
+  return kCounterBytes + align256((size_t)device_sm_count() * (kWarps + 2) * part);
+}
 
-cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, int dim, bool bf16, void*, int*, cudaStream_t s) {
-  const auto fn = dim == 128 ? (bf16 ? kv4_attention_simple_kernel<128, true> : kv4_attention_simple_kernel<128, false>)
-                             : (bf16 ? kv4_attention_simple_kernel<64, true> : kv4_attention_simple_kernel<64, false>);
-  const int64_t most = a.max_q < a.T ? a.max_q : a.T;
-  fn<<<dim3((unsigned)most, (unsigned)a.heads, (unsigned)a.B), kSThreads, 0, s>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, int dim, bool bf16, void* ws, int* err, cudaStream_t s) {
+  if (narrow(a.max_q, a.heads, a.kv_heads)) {
+    if (dim == 128) return bf16 ? launch<128, true, 1>(a, ws, err, s) : launch<128, false, 1>(a, ws, err, s);
+    return bf16 ? launch<64, true, 1>(a, ws, err, s) : launch<64, false, 1>(a, ws, err, s);
+  }
+  if (dim == 128) return bf16 ? launch<128, true, 2>(a, ws, err, s) : launch<128, false, 2>(a, ws, err, s);
+  return bf16 ? launch<64, true, 2>(a, ws, err, s) : launch<64, false, 2>(a, ws, err, s);
 }
 
 }  // namespace awq

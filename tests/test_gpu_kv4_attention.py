@@ -166,6 +166,26 @@ def test_a_visible_nan_shows_and_a_hidden_one_does_not(awq, new):
         assert np.isfinite(out.float().cpu().numpy()).all()
 
 
+@pytest.mark.parametrize("heads", [2, 6])
+@pytest.mark.parametrize("new", [2, 4, 120])
+def test_a_nan_value_shows_only_where_it_is_seen(awq, new, heads):
+    """The last token's value and the first token's key and value are NaN: all but the last query, or with a
+    window the last one too, do not see them."""
+    p = Problem([200], [new], heads, 2, 64, 16, seed=17)
+    nan = np.array([np.nan], np.float16).view(np.uint8)
+    page = p.table[0, 199 // 16]
+    p.cache[page, 1, 0, 16 * 64 + 8 * (199 % 16) + 4:][:2] = nan
+    out = p.run(awq)[0].float().cpu().numpy()
+    half = heads // 2
+    assert np.isnan(out[-1, half:]).all() and np.isfinite(out[:-1]).all() and np.isfinite(out[-1, :half]).all()
+    first = p.table[0, 0]
+    for at in (0, 4):
+        p.cache[first, :, 0, 16 * 64 + at:][..., :2] = nan
+    out = p.run(awq, window=80 - new // 2)[0].float().cpu().numpy()
+    sees = np.arange(200 - new, 200) - (80 - new // 2) < 0
+    assert np.isnan(out[sees]).all() and np.isfinite(out[~sees][:-1]).all()
+
+
 def test_strided_queries_table_rows_and_explicit_scale(awq):
     p = Problem([90, 40], [2, 1], 4, 2, 64, 16, seed=11)
     q = torch.zeros(3, 6, 64, dtype=torch.float16, device="cuda")

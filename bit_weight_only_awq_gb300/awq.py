@@ -394,6 +394,11 @@ def _dtype16(name: str, *tensors) -> int:
     return _DTYPES[dtype]
 
 
+def _raw_stream(stream, device: torch.device) -> int:
+    """The handle of `stream`, or of the device's current stream (without building a Stream object)."""
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
 def _need(name: str, dtype, *tensors) -> None:
     for t in tensors:
         if t is not None and (t.dtype != dtype or not t.is_contiguous()):
@@ -434,7 +439,7 @@ def w4a8_rmsnorm_quant(x, weight, residual=None, eps: float = 1e-6, res_out=None
         s_tok = torch.empty((M,), dtype=torch.float32, device=x.device)
     _check("w4a8_rmsnorm_quant", lib.w4a8_rmsnorm_quant(_ptr(x), _ptr(residual), _ptr(weight), _ptr(res_out), _ptr(y),
                                                         _ptr(xq), _ptr(s_tok), M, K, xs, rs, eps, dtype,
-                                                        _stream(stream)))
+                                                        _raw_stream(stream, x.device)))
     return xq, s_tok, res_out
 
 
@@ -444,7 +449,7 @@ def awq_rmsnorm(x, weight, residual=None, eps: float = 1e-6, res_out=None, out=N
     if out is None:
         out = torch.empty((M, K), dtype=x.dtype, device=x.device)
     _check("awq_rmsnorm", lib.awq_rmsnorm(_ptr(x), _ptr(residual), _ptr(weight), _ptr(res_out), _ptr(out), M, K, xs,
-                                          rs, eps, dtype, _stream(stream)))
+                                          rs, eps, dtype, _raw_stream(stream, x.device)))
     return out, res_out
 
 
@@ -496,7 +501,7 @@ def kv4_append(cache, k, v, positions, slots, table, q=None, interleaved: bool =
     _check("kv4_append", lib.kv4_append(
         _ptr(q), _ptr(k), _ptr(v), qs, _row_stride("kv4_append", k), _row_stride("kv4_append", v), _ptr(positions),
         _ptr(slots), _ptr(table), max_pos, rot, int(interleaved), _ptr(q_out), qos, _ptr(cache), pages, T, heads,
-        kv_heads, dim, page, dtype, _stream(stream)))
+        kv_heads, dim, page, dtype, _raw_stream(stream, cache.device)))
     return q_out
 
 
@@ -514,24 +519,26 @@ def kv4_gather(cache, slots, dtype=torch.float16, k=None, v=None, stream=None):
     if k.shape != (T, kv_heads, dim) or v.shape != k.shape:
         raise ValueError("kv4_gather: k and v are [T, kv_heads, head_dim]")
     _check("kv4_gather", lib.kv4_gather(_ptr(cache), _ptr(slots), _ptr(k), _ptr(v), pages, T, kv_heads, dim, page,
-                                        kind, _stream(stream)))
+                                        kind, _raw_stream(stream, cache.device)))
     return k, v
 
 
-# Workspaces of kv4_attention by device and stream (calls on one stream may share one), grown on demand.
+# Workspaces of kv4_attention by device, stream (calls on one stream may share one) and the sizes that they go by.
 _kv4_workspaces: dict[tuple, torch.Tensor] = {}
 
 
-def _kv4_workspace(nbytes: int, device: torch.device, stream) -> torch.Tensor | None:
-    if nbytes == 0:
-        return None
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    key = (device.index, stream.cuda_stream)
+def _kv4_workspace(handle: int, device: torch.device, sizes: tuple, stream) -> torch.Tensor:
+    key = (device.index, handle, *sizes)
     ws = _kv4_workspaces.get(key)
-    if ws is None or ws.numel() < nbytes:
-        with torch.cuda.stream(stream):  # zeroed, and later freed, in the order of its own stream
-            ws = _kv4_workspaces[key] = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    if ws is None:
+        nbytes = kv4_attention_workspace_bytes(*sizes)
+        same = (device.index, handle)
+        ws = _kv4_workspaces.get(same)
+        if ws is None or ws.numel() < nbytes:
+            with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
+                # zeroed, and later freed, in the order of its own stream
+                ws = _kv4_workspaces[same] = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+        _kv4_workspaces[key] = ws
     return ws
 
 
@@ -567,14 +574,16 @@ def kv4_attention(q, cache, block_table, kv_len, q_start=None, max_q: int = 1, s
             raise ValueError("kv4_attention: lse is [T, heads]")
     if scale is None:
         scale = dim ** -0.5
+    device = q.device
+    handle = _raw_stream(stream, device)
     ws = workspace
     if ws is None:
-        ws = _kv4_workspace(kv4_attention_workspace_bytes(T, B, max_q, heads, kv_heads, dim), q.device, stream)
-    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+        ws = _kv4_workspace(handle, device, (T, B, max_q, heads, kv_heads, dim), stream)
+    nbytes = ws.numel() * ws.element_size()
     _check("kv4_attention", lib.kv4_attention(
         _ptr(q), _row_stride("kv4_attention", q), _ptr(cache), _ptr(block_table),
         max(block_table.stride(0), max_pages), _ptr(kv_len), _ptr(q_start), _ptr(out), _ptr(lse), T, B, max_q, heads,
-        kv_heads, dim, pages, page, max_pages, scale, window, dtype, _ptr(ws), nbytes, _stream(stream)))
+        kv_heads, dim, pages, page, max_pages, scale, window, dtype, _ptr(ws), nbytes, handle))
     return out
 
 

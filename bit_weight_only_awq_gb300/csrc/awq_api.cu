@@ -587,7 +587,7 @@ awq_status kv4_attention(const uint16_t* q, int64_t q_stride, const void* cache,
       !kv4_shape_ok(num_pages, kv_heads, head_dim, page_size) || num_pages < 1)
     return AWQ_EINVAL;
   if (q_stride < (int64_t)heads * head_dim || q_stride % 8 != 0 || max_pages < 1 || table_stride < max_pages ||
-      (int64_t)max_pages * page_size > INT32_MAX - 1024 || !(scale - scale == 0.f) || window < 0 ||
+      (int64_t)max_pages * page_size > (1 << 30) || !(scale - scale == 0.f) || window < 0 ||
       (dtype != AWQ_FP16 && dtype != AWQ_BF16))
     return AWQ_EINVAL;
   if (!q_start && (T != B || max_q != 1)) return AWQ_EINVAL;

@@ -20,6 +20,7 @@
 // (maximum, sum, unnormalized output) are joined: inside a CTA after a barrier, across CTAs by the last one to
 // arrive, always in the order of the tiles, so that results do not depend on timing.
 #include <cmath>
+#include <type_traits>
 
 #include "awq_host.h"
 #include "awq_internal.h"
@@ -44,6 +45,12 @@ struct Geo {
   static constexpr int kSmemBytes = kRingBytes + 128;
 };
 
+struct Args : Kv4AttnArgs {
+  int per;             // query heads of a cache head
+  int units_page;      // units of a page
+  uint32_t page_magic; // unit / units_page = high word of unit * page_magic (0: one unit a page)
+};
+
 // Floats of one partial result: the unnormalized output, then maximum and sum of every column.
 __host__ __device__ constexpr int part_floats(int dim, int cols) { return cols * (dim + 2); }
 
@@ -52,11 +59,13 @@ struct Seq {
   int begin, n;      // its query tokens
   int len;           // cached tokens
   int lo;            // the first token that any of its queries sees
-  int tiles, groups; // tiles of a (cache head, column block), and how many of those
+  int tile0, tiles;  // the first tile, and the tiles, of a (cache head, column block)
+  int blocks;        // column blocks of a cache head
+  int groups;        // (cache head, column block) pairs
 };
 
 template <int NT>
-__device__ __forceinline__ Seq seq_of(const Kv4AttnArgs& a, int b) {
+__device__ __forceinline__ Seq seq_of(const Args& a, int b) {
   Seq s;
   s.begin = b;
   s.n = 1;
@@ -67,9 +76,10 @@ __device__ __forceinline__ Seq seq_of(const Kv4AttnArgs& a, int b) {
   s.len = min(max(a.kv_len[b], 0), a.max_pages * a.page_size);
   s.lo = a.window > 0 ? max(0, s.len - s.n + 1 - a.window) : 0;
   s.lo = min(s.lo, s.len);
-  s.tiles = max(1, (s.len + kTile - 1) / kTile - s.lo / kTile);
-  const int per = a.heads / a.kv_heads;
-  s.groups = a.kv_heads * ((s.n * per + 8 * NT - 1) / (8 * NT));
+  s.tile0 = s.lo / kTile;
+  s.tiles = max(1, (s.len + kTile - 1) / kTile - s.tile0);
+  s.blocks = (s.n * a.per + 8 * NT - 1) / (8 * NT);
+  s.groups = a.kv_heads * s.blocks;
   return s;
 }
 
@@ -80,7 +90,7 @@ struct Cursor {
 };
 
 template <int NT>
-__device__ __forceinline__ void advance(const Kv4AttnArgs& a, Cursor& c) {
+__device__ __forceinline__ void advance(const Args& a, Cursor& c) {
   if (++c.tile < c.s.tiles) return;
   c.tile = 0;
   if (++c.group < c.s.groups) return;
@@ -146,16 +156,15 @@ __device__ __forceinline__ void join(Joined& t, float m, float l, float4 o) {
 }
 
 // The query token and head of a column, or false for a column beyond them.
-__device__ __forceinline__ bool row_of(const Kv4AttnArgs& a, const Seq& s, int kv_head, int col, int64_t& token, int& head) {
-  const int per = a.heads / a.kv_heads;
-  const int i = col / per;
+__device__ __forceinline__ bool row_of(const Args& a, const Seq& s, int kv_head, int col, int64_t& token, int& head) {
+  const int i = col / a.per;
   token = s.begin + i;
-  head = kv_head * per + col - i * per;
+  head = kv_head * a.per + col - i * a.per;
   return i < s.n;
 }
 
 template <bool BF16>
-__device__ __forceinline__ void store_joined(const Kv4AttnArgs& a, int dim, const Seq& s, int kv_head, int col, int c4,
+__device__ __forceinline__ void store_joined(const Args& a, int dim, const Seq& s, int kv_head, int col, int c4,
                                              const Joined& t) {
   int64_t token;
   int head;
@@ -167,6 +176,18 @@ __device__ __forceinline__ void store_joined(const Kv4AttnArgs& a, int dim, cons
   if (a.lse && c4 == 0) a.lse[row] = t.l == 0.f ? -INFINITY : (t.m + log2f(t.l)) * kLn2;
 }
 
+// Part i of n equal contiguous parts of `total` tiles begins at i total / n; the part that holds a tile.  Divided
+// in 32 bits where that is enough, as it mostly is.
+__device__ __forceinline__ long long part_begin(long long i, long long total, long long n) {
+  const unsigned long long x = (unsigned long long)i * (unsigned long long)total;
+  return (x >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)n) : (long long)(x / (unsigned long long)n);
+}
+__device__ __forceinline__ int part_of(long long tile, long long total, long long n) {
+  const unsigned long long x = (unsigned long long)(tile + 1) * (unsigned long long)n + (unsigned long long)(total - 1);
+  return ((x | (unsigned long long)total) >> 32) == 0 ? (int)((uint32_t)x / (uint32_t)total) - 1
+                                                      : (int)(x / (unsigned long long)total) - 1;
+}
+
 // One partial of this CTA that does not cover its (sequence, head, column block).
 struct Desc {
   long long first;  // the place of its tile 0 in the order of all tiles
@@ -176,7 +197,7 @@ struct Desc {
 
 template <int D, bool BF16, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
-kv4_attention_kernel(const Kv4AttnArgs a, float* __restrict__ warp_parts, float* __restrict__ cta_parts, int* counters,
+kv4_attention_kernel(const Args a, float* __restrict__ warp_parts, float* __restrict__ cta_parts, int* counters,
                      int* err) {
   using G = Geo<D>;
   constexpr int kWords = D / 32;     // words of a lane for a token's keys, or for a token pair's values
@@ -224,8 +245,8 @@ kv4_attention_kernel(const Kv4AttnArgs a, float* __restrict__ warp_parts, float*
   if (blockIdx.x >= ctas) return;
 
   const long long warps = ctas * kWarps, me = (long long)blockIdx.x * kWarps + warp;
-  const long long u0 = me * total / warps, u1 = (me + 1) * total / warps;
-  const long long cta0 = (long long)blockIdx.x * total / ctas, cta1 = (long long)(blockIdx.x + 1) * total / ctas;
+  const long long u0 = part_begin(me, total, warps), u1 = part_begin(me + 1, total, warps);
+  const long long cta0 = part_begin(blockIdx.x, total, ctas), cta1 = part_begin(blockIdx.x + 1, total, ctas);
   bool ok = true;
 
   if (u0 < u1) {
@@ -249,54 +270,59 @@ kv4_attention_kernel(const Kv4AttnArgs a, float* __restrict__ warp_parts, float*
     }
     Cursor next = use;  // the tile to be copied next
     const int count = (int)(u1 - u0);
-    const int units_page = a.page_size / kKv4Unit;
-    const int span = min(4, units_page);  // units that lie side by side in memory
-    const int per = a.heads / a.kv_heads;
-    const int blocks = next.s.groups / a.kv_heads;
-    int next_blocks = blocks;
+    const int span = min(4, a.units_page);  // units that lie side by side in memory
+    int next_head = next.group / next.s.blocks;
     const uint32_t bar0 = smem_u32(&bars[warp * G::kStages]);
 
-    // the page of lane i's unit (i < 4) of the tile at `next`
-    auto page_of = [&]() {
-      const int j = (next.s.lo / kTile + next.tile) * kTile + kKv4Unit * lane;
-      int page = 0;
-      if (lane < 4 && j < next.s.len) page = a.block_table[next.b * a.table_stride + j / a.page_size];
-      return page < 0 || page >= a.num_pages ? 0 : page;
+    // lane i < 4 looks after unit i of the tile at `next`: its page, and its unit in that
+    int page = 0, in_page = 0;
+    auto look_up = [&]() {
+      const int unit = (next.s.tile0 + next.tile) * 4 + lane;
+      const int p = a.page_magic ? (int)__umulhi((uint32_t)unit, a.page_magic) : unit;
+      in_page = unit - p * a.units_page;
+      page = 0;
+      if (lane < 4 && unit * kKv4Unit < next.s.len) page = a.block_table[next.b * a.table_stride + p];
     };
-    int page = page_of();
+    look_up();
     auto issue = [&](int k) {  // copies tile k of this warp's range, the one at `next`
-      const int tile = next.s.lo / kTile + next.tile, j0 = tile * kTile;
+      const int j0 = (next.s.tile0 + next.tile) * kTile;
       const int first = max(0, (next.s.lo - j0) / kKv4Unit), last = min(4, (next.s.len - j0 + kKv4Unit - 1) / kKv4Unit);
       const int st = k % G::kStages;
       const uint32_t bar = bar0 + 8 * st;
       if (lane == 0) mbar_arrive_tx(bar, max(0, last - first) * G::kUnitBytes);
       __syncwarp();
-      const int from = max(lane, first), to = min(lane + span, last);
-      if (lane < 4 && lane % span == 0 && from < to) {
-        const int in_page = (j0 + kKv4Unit * from) % a.page_size / kKv4Unit;
-        const uint8_t* src = a.cache + (((int64_t)page * a.kv_heads + next.group / next_blocks) * units_page + in_page) * G::kUnitBytes;
-        bulk_load(smem_u32(ring + st * G::kTileBytes + from * G::kUnitBytes), src, (to - from) * G::kUnitBytes, bar);
+      const int skip = max(first - lane, 0), to = min(lane + span, last);  // units of the span before the first one
+      if (lane < 4 && (lane & (span - 1)) == 0 && lane + skip < to) {
+        const int64_t p = (uint32_t)page < (uint32_t)a.num_pages ? page : 0;
+        const uint8_t* src = a.cache + ((p * a.kv_heads + next_head) * a.units_page + in_page + skip) * G::kUnitBytes;
+        bulk_load(smem_u32(ring + st * G::kTileBytes + (lane + skip) * G::kUnitBytes), src,
+                  (to - lane - skip) * G::kUnitBytes, bar);
       }
-      const int b = next.b;
+      const int b = next.b, group = next.group;
       advance<NT>(a, next);
-      if (next.b != b && next.b < a.B) next_blocks = next.s.groups / a.kv_heads;
-      if (k + 1 < count) page = page_of();
+      if ((next.b != b || next.group != group) && next.b < a.B) next_head = next.group / next.s.blocks;
+      if (k + 1 < count) look_up();
     };
     int issued = 0;
     while (issued < min(count, G::kStages)) issue(issued++);
 
+    // Scores are kept as T = S / qk with qk > 0, so that one multiply-add gives the exponent: the sign of the scale
+    // goes into the queries, and a scale of zero makes them zero.
+    const float sign = a.scale > 0.f ? 1.f : a.scale < 0.f ? -1.f : 0.f;
+    const float factor = a.scale == 0.f ? kLog2e : fabsf(a.scale) * kLog2e;
     // a head's state: queries, running maximum, sum, zero sum, output
     uint32_t qf[NT][2 * kWords][2];
-    float qk[NT][2], qz[NT][2];    // per column: factor of the code product, of the key's zero (base 2)
+    float qk[NT][2], qr[NT][2];    // per column: the score's factor (base 2), and sum(q) over it
     int pos[NT][2];                // the last token it sees
     float m[NT][2], l[NT][2], z[NT][2], o[NT][2 * kWords][4];
     int vexp = 0;                  // probabilities enter fp16 as p sv 2^(13 - vexp)
     int seg0 = 0;                  // the first tile of this warp in the current head
+    int kv_head = 0, col0 = 0;
 
     for (int k = 0; k < count; ++k) {
-      const int kv_head = use.group / (use.s.groups / a.kv_heads);
-      const int col0 = (use.group - kv_head * (use.s.groups / a.kv_heads)) * kCols;
       if (k == 0 || use.tile == 0) {
+        kv_head = use.group / use.s.blocks;
+        col0 = (use.group - kv_head * use.s.blocks) * kCols;
         seg0 = use.tile;
         vexp = -16;
 #pragma unroll
@@ -314,8 +340,8 @@ kv4_attention_kernel(const Kv4AttnArgs a, float* __restrict__ warp_parts, float*
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
               const float2 f = unpack2<BF16>(w[p]);
-              x[8 * i + 2 * p] = f.x;
-              x[8 * i + 2 * p + 1] = f.y;
+              x[8 * i + 2 * p] = f.x * sign;
+              x[8 * i + 2 * p + 1] = f.y * sign;
             }
           }
           float top = 0.f, sum = 0.f;
@@ -343,11 +369,9 @@ kv4_attention_kernel(const Kv4AttnArgs a, float* __restrict__ warp_parts, float*
           // the accumulator's columns of this lane are 2t and 2t + 1
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const float d = __shfl_sync(0xFFFFFFFFu, down, 8 * t + 4 * c);
-            const float s = __shfl_sync(0xFFFFFFFFu, sum, 8 * t + 4 * c);
-            qk[n][c] = d * (a.scale * kLog2e);
-            qz[n][c] = s * (a.scale * kLog2e);
-            const int i = (col0 + 8 * n + 2 * t + c) / per;
+            qk[n][c] = __shfl_sync(0xFFFFFFFFu, down, 8 * t + 4 * c) * factor;
+            qr[n][c] = __shfl_sync(0xFFFFFFFFu, sum * (up * 5.9604644775390625e-8f), 8 * t + 4 * c);
+            const int i = (col0 + 8 * n + 2 * t + c) / a.per;
             pos[n][c] = i < use.s.n ? use.s.len - use.s.n + i : -1;
             m[n][c] = -INFINITY;
             l[n][c] = z[n][c] = 0.f;
@@ -365,7 +389,7 @@ kv4_attention_kernel(const Kv4AttnArgs a, float* __restrict__ warp_parts, float*
         break;
       }
       const uint8_t* tile = ring + st * G::kTileBytes;
-      const int j0 = (use.s.lo / kTile + use.tile) * kTile;
+      const int j0 = (use.s.tile0 + use.tile) * kTile;
 
       // ---- scores: S[token][column], 16 tokens a unit
       float s[NT][4][4];
@@ -411,13 +435,13 @@ kv4_attention_kernel(const Kv4AttnArgs a, float* __restrict__ warp_parts, float*
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const float2 key = unpack2<false>(meta[u][r].x);
-          vtop = max(vtop, meta[u][r].y & 0x7FFFu);
+          vtop = __vmaxu2(vtop, meta[u][r].y);
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               float& v = s[n][u][2 * r + c];
-              v = fmaf(key.x, v * qk[n][c], key.y * qz[n][c]);
+              v = fmaf(key.x, v, key.y * qr[n][c]);
             }
         }
       if (edge) {
@@ -435,7 +459,7 @@ kv4_attention_kernel(const Kv4AttnArgs a, float* __restrict__ warp_parts, float*
       }
 
       // ---- running maximum; the largest value scale, rounded up to a power of two
-      vtop = __reduce_max_sync(0xFFFFFFFFu, vtop);
+      vtop = __reduce_max_sync(0xFFFFFFFFu, vtop & 0x7FFFu);
       const int ve = max(vexp, (int)(vtop >> 10) - 14);
       bool grown = ve != vexp;
       float keep[NT][2];
@@ -458,7 +482,7 @@ kv4_attention_kernel(const Kv4AttnArgs a, float* __restrict__ warp_parts, float*
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const float f = m[n][c] == -INFINITY ? 1.f : ex2(keep[n][c] - m[n][c]);
+            const float f = m[n][c] == -INFINITY ? 1.f : ex2((keep[n][c] - m[n][c]) * qk[n][c]);
             l[n][c] *= f;
             z[n][c] *= f;
 #pragma unroll
@@ -475,29 +499,35 @@ kv4_attention_kernel(const Kv4AttnArgs a, float* __restrict__ warp_parts, float*
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) base[n][c] = m[n][c] == -INFINITY ? 0.f : m[n][c];
+        for (int c = 0; c < 2; ++c) base[n][c] = m[n][c] == -INFINITY ? 0.f : -m[n][c] * qk[n][c];
       uint32_t pf[NT][4][2];
+      auto weigh = [&](auto hides) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < 4; ++u)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float2 val = unpack2<false>(meta[u][r].y);
-          const float w = val.x * vup;
+          for (int r = 0; r < 2; ++r) {
+            const float2 val = unpack2<false>(meta[u][r].y);
+            const float w = val.x * vup;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            float w0 = w, w1 = w, z0 = val.y, z1 = val.y;
-            if (edge) {  // a token hidden from one column and seen by another may hold a NaN
-              if (s[n][u][2 * r] == -INFINITY) w0 = z0 = 0.f;
-              if (s[n][u][2 * r + 1] == -INFINITY) w1 = z1 = 0.f;
+            for (int n = 0; n < NT; ++n) {
+              float p[2];
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const float v = s[n][u][2 * r + c], e = ex2(fmaf(v, qk[n][c], base[n][c]));
+                // a token hidden from one column and seen by another may hold a NaN
+                const bool hidden = decltype(hides)::value && v == -INFINITY;
+                l[n][c] += e;
+                z[n][c] = fmaf(e, hidden ? 0.f : val.y, z[n][c]);
+                p[c] = e * (hidden ? 0.f : w);
+              }
+              pf[n][u][r] = transpose8x8(pack2<false>(p[0], p[1]));
             }
-            const float p0 = ex2(s[n][u][2 * r] - base[n][0]), p1 = ex2(s[n][u][2 * r + 1] - base[n][1]);
-            l[n][0] += p0;
-            l[n][1] += p1;
-            z[n][0] = fmaf(p0, z0, z[n][0]);
-            z[n][1] = fmaf(p1, z1, z[n][1]);
-            pf[n][u][r] = transpose8x8(pack2<false>(p0 * w0, p1 * w1));
           }
-        }
+      };
+      if (edge)
+        weigh(std::true_type{});
+      else
+        weigh(std::false_type{});
 
       // ---- output: O[channel][column]
 #pragma unroll
@@ -558,7 +588,7 @@ kv4_attention_kernel(const Kv4AttnArgs a, float* __restrict__ warp_parts, float*
 #pragma unroll
                 for (int i = 0; i < kWords / 2; ++i)
                   reinterpret_cast<uint4*>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-                if (a.lse && g == 0) a.lse[row] = ls == 0.f ? -INFINITY : (m[n][c] + log2f(ls)) * kLn2;
+                if (a.lse && g == 0) a.lse[row] = ls == 0.f ? -INFINITY : (m[n][c] * qk[n][c] + log2f(ls)) * kLn2;
               }
             } else {
               float* dst = part + col * D + g * (D / 8);
@@ -568,7 +598,7 @@ kv4_attention_kernel(const Kv4AttnArgs a, float* __restrict__ warp_parts, float*
                     make_float4(o[n][2 * i][c] * back + zs, o[n][2 * i][2 + c] * (back * 0.0625f) + zs,
                                 o[n][2 * i + 1][c] * back + zs, o[n][2 * i + 1][2 + c] * (back * 0.0625f) + zs);
               if (g == 0) {
-                part[kCols * D + col] = m[n][c];
+                part[kCols * D + col] = m[n][c] * qk[n][c];
                 part[kCols * D + kCols + col] = ls;
               }
             }
@@ -595,8 +625,7 @@ kv4_attention_kernel(const Kv4AttnArgs a, float* __restrict__ warp_parts, float*
     int end = i + 1;
     while (end < 2 * kWarps && (!desc[end].part || desc[end].first == d.first)) ++end;
     const Seq s = seq_of<NT>(a, d.b);
-    const int blocks = s.groups / a.kv_heads;
-    const int kv_head = d.group / blocks, col0 = (d.group - kv_head * blocks) * kCols;
+    const int kv_head = d.group / s.blocks, col0 = (d.group - kv_head * s.blocks) * kCols;
     const long long d1 = d.first + s.tiles;
     const bool whole = d.first >= cta0 && d1 <= cta1;
     // a head shared with other CTAs: slot 1 when it goes on after this one, slot 0 when it ends here
@@ -621,7 +650,7 @@ kv4_attention_kernel(const Kv4AttnArgs a, float* __restrict__ warp_parts, float*
       }
     }
     if (!whole) {
-      const int c_first = (int)cta_of_unit(d.first, total, ctas), c_last = (int)cta_of_unit(d1 - 1, total, ctas);
+      const int c_first = part_of(d.first, total, ctas), c_last = part_of(d1 - 1, total, ctas);
       __threadfence();
       __syncthreads();
       if (tid == 0) {
@@ -654,11 +683,17 @@ kv4_attention_kernel(const Kv4AttnArgs a, float* __restrict__ warp_parts, float*
 bool narrow(int max_q, int heads, int kv_heads) { return (int64_t)max_q * (heads / kv_heads) <= 8; }
 
 template <int D, bool BF16, int NT>
-cudaError_t launch(const Kv4AttnArgs& a, void* ws, int* err, cudaStream_t s) {
+cudaError_t launch(const Kv4AttnArgs& args, void* ws, int* err, cudaStream_t s) {
   const void* fn = reinterpret_cast<const void*>(kv4_attention_kernel<D, BF16, NT>);
   cudaError_t e = set_smem_once(fn, Geo<D>::kSmemBytes);
   if (e != cudaSuccess) return e;
   const int ctas = device_sm_count();
+  Args a;
+  static_cast<Kv4AttnArgs&>(a) = args;
+  a.per = args.heads / args.kv_heads;
+  a.units_page = args.page_size / kKv4Unit;
+  // exact for units below 2^32 / units_page >= 2^26: lengths are at most 2^30 tokens
+  a.page_magic = a.units_page == 1 ? 0u : (uint32_t)(((1ull << 32) + a.units_page - 1) / a.units_page);
   uint8_t* base = static_cast<uint8_t*>(ws);
   float* warp_parts = reinterpret_cast<float*>(base + kCounterBytes);
   float* cta_parts = warp_parts + (size_t)ctas * kWarps * part_floats(D, 8 * NT);

@@ -33,6 +33,7 @@ namespace {
 constexpr int kTile = 64;    // tokens of a tile: 4 units
 constexpr int kWarps = 12;   // three on each sub-partition
 constexpr int kThreads = 32 * kWarps;
+constexpr int kFewParts = 12;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -64,16 +65,22 @@ struct Seq {
   int groups;        // (cache head, column block) pairs
 };
 
-template <int NT>
-__device__ __forceinline__ Seq seq_of(const Args& a, int b) {
-  Seq s;
-  s.begin = b;
-  s.n = 1;
+// Query tokens and length of sequence b, as the device memory has them.
+__device__ __forceinline__ int3 read_seq(const Args& a, int b) {
+  int begin = b, n = 1;
   if (a.q_start) {
-    s.begin = min(max(a.q_start[b], 0), (int)a.T);
-    s.n = min(min(max(a.q_start[b + 1], s.begin), (int)a.T) - s.begin, a.max_q);
+    begin = min(max(a.q_start[b], 0), (int)a.T);
+    n = min(min(max(a.q_start[b + 1], begin), (int)a.T) - begin, a.max_q);
   }
-  s.len = min(max(a.kv_len[b], 0), a.max_pages * a.page_size);
+  return make_int3(begin, n, min(max(a.kv_len[b], 0), a.max_pages * a.page_size));
+}
+
+template <int NT>
+__device__ __forceinline__ Seq seq_of(const Args& a, const int3 v) {
+  Seq s;
+  s.begin = v.x;
+  s.n = v.y;
+  s.len = v.z;
   s.lo = a.window > 0 ? max(0, s.len - s.n + 1 - a.window) : 0;
   s.lo = min(s.lo, s.len);
   s.tile0 = s.lo / kTile;
@@ -81,6 +88,11 @@ __device__ __forceinline__ Seq seq_of(const Args& a, int b) {
   s.blocks = (s.n * a.per + 8 * NT - 1) / (8 * NT);
   s.groups = a.kv_heads * s.blocks;
   return s;
+}
+// The first kThreads sequences are kept in shared memory.
+template <int NT>
+__device__ __forceinline__ Seq seq_of(const Args& a, const int3* kept, int b) {
+  return seq_of<NT>(a, b < kThreads ? kept[b] : read_seq(a, b));
 }
 
 // A position in the order of all tiles.
@@ -90,14 +102,14 @@ struct Cursor {
 };
 
 template <int NT>
-__device__ __forceinline__ void advance(const Args& a, Cursor& c) {
+__device__ __forceinline__ void advance(const Args& a, const int3* kept, Cursor& c) {
   if (++c.tile < c.s.tiles) return;
   c.tile = 0;
   if (++c.group < c.s.groups) return;
   c.group = 0;
   do {
     if (++c.b >= a.B) return;
-    c.s = seq_of<NT>(a, c.b);
+    c.s = seq_of<NT>(a, kept, c.b);
   } while (c.s.groups == 0);
 }
 
@@ -139,39 +151,77 @@ __device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
   }
 }
 
-// Row `col` of a partial joins `total`: both rescaled to the larger maximum.
+// Four channels of a column's partial result.
 struct Joined {
-  float m, l;
-  float4 o;
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 };
-__device__ __forceinline__ void join(Joined& t, float m, float l, float4 o) {
-  const float top = fmaxf(t.m, m), base = top == -INFINITY ? 0.f : top;
-  const float x = ex2(t.m - base), y = ex2(m - base);
-  t.l = t.l * x + l * y;
-  t.o.x = t.o.x * x + o.x * y;
-  t.o.y = t.o.y * x + o.y * y;
-  t.o.z = t.o.z * x + o.z * y;
-  t.o.w = t.o.w * x + o.w * y;
-  t.m = top;
+// Joins element (col, channels 4 c4..) of N partials of COLS columns: all are read first, and rescaled to the
+// largest maximum.  part(i) gives partial i < n; FAR: other CTAs wrote them.
+template <int D, int COLS, int N, bool FAR, typename F>
+__device__ __forceinline__ void join_parts(Joined& j, int n, int col, int c4, F part) {
+  float m[N], l[N];
+  float4 o[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+    o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < n) {
+      const float* p = part(i);
+      const float *pm = p + COLS * D + col, *pl = pm + COLS;
+      const float4* po = reinterpret_cast<const float4*>(p + col * D + 4 * c4);
+      m[i] = FAR ? __ldcg(pm) : *pm;
+      l[i] = FAR ? __ldcg(pl) : *pl;
+      o[i] = FAR ? __ldcg(po) : *po;
+    }
+  }
+  float top = j.m;
+#pragma unroll
+  for (int i = 0; i < N; ++i) top = fmaxf(top, m[i]);
+  const float base = top == -INFINITY ? 0.f : top, x = ex2(j.m - base);
+  j.l *= x;
+  j.o = make_float4(j.o.x * x, j.o.y * x, j.o.z * x, j.o.w * x);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float y = ex2(m[i] - base);
+    j.l = fmaf(l[i], y, j.l);
+    j.o = make_float4(fmaf(o[i].x, y, j.o.x), fmaf(o[i].y, y, j.o.y), fmaf(o[i].z, y, j.o.z), fmaf(o[i].w, y, j.o.w));
+  }
+  j.m = top;
+}
+template <int D, int COLS>
+__device__ __forceinline__ void store_part(float* part, int col, int c4, const Joined& j) {
+  *reinterpret_cast<float4*>(part + col * D + 4 * c4) = j.o;
+  if (c4 == 0) {
+    part[COLS * D + col] = j.m;
+    part[COLS * D + COLS + col] = j.l;
+  }
 }
 
 // The query token and head of a column, or false for a column beyond them.
-__device__ __forceinline__ bool row_of(const Args& a, const Seq& s, int kv_head, int col, int64_t& token, int& head) {
+__device__ __forceinline__ bool row_of(const Args& a, int begin, int n, int kv_head, int col, int64_t& token, int& head) {
   const int i = col / a.per;
-  token = s.begin + i;
+  token = begin + i;
   head = kv_head * a.per + col - i * a.per;
-  return i < s.n;
+  return i < n;
 }
 
-template <bool BF16>
-__device__ __forceinline__ void store_joined(const Args& a, int dim, const Seq& s, int kv_head, int col, int c4,
-                                             const Joined& t) {
+// One partial of a warp that does not cover its (sequence, head, column block).
+struct Desc {
+  long long first;  // the place of its tile 0 in the order of all tiles
+  const float* part;
+  int tiles, begin, n, kv_head, col0;
+};
+
+template <int D, bool BF16>
+__device__ __forceinline__ void store_joined(const Args& a, const Desc& d, int col, int c4, const Joined& t) {
   int64_t token;
   int head;
-  if (!row_of(a, s, kv_head, col, token, head)) return;
+  if (!row_of(a, d.begin, d.n, d.kv_head, d.col0 + col, token, head)) return;
   const float inv = t.l == 0.f ? 0.f : 1.f / t.l;
   const int64_t row = token * a.heads + head;
-  reinterpret_cast<uint2*>(a.out + row * dim)[c4] =
+  reinterpret_cast<uint2*>(a.out + row * D)[c4] =
       make_uint2(pack2<BF16>(t.o.x * inv, t.o.y * inv), pack2<BF16>(t.o.z * inv, t.o.w * inv));
   if (a.lse && c4 == 0) a.lse[row] = t.l == 0.f ? -INFINITY : (t.m + log2f(t.l)) * kLn2;
 }
@@ -188,16 +238,9 @@ __device__ __forceinline__ int part_of(long long tile, long long total, long lon
                                                       : (int)(x / (unsigned long long)total) - 1;
 }
 
-// One partial of this CTA that does not cover its (sequence, head, column block).
-struct Desc {
-  long long first;  // the place of its tile 0 in the order of all tiles
-  int b, group;
-  const float* part;  // nullptr: none
-};
-
 template <int D, bool BF16, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
-kv4_attention_kernel(const Args a, float* __restrict__ warp_parts, float* __restrict__ cta_parts, int* counters,
+kv4_attention_kernel(const Args a, float* warp_parts, float* cta_parts, int* counters,
                      int* err) {
   using G = Geo<D>;
   constexpr int kWords = D / 32;     // words of a lane for a token's keys, or for a token pair's values
@@ -207,8 +250,10 @@ kv4_attention_kernel(const Args a, float* __restrict__ warp_parts, float* __rest
   __shared__ uint64_t bars[kWarps * G::kStages];
   __shared__ long long before[kThreads];  // tiles before the sequences of each thread's share
   __shared__ long long warp_total[kWarps];
-  __shared__ Desc desc[2 * kWarps];
-  __shared__ int abort_word, arrived;
+  __shared__ int3 kept[kThreads];         // the first sequences
+  __shared__ Desc desc[2 * kWarps];       // of each warp: an earlier partial, the last one
+  __shared__ int2 arrived[2];  // of a shared head whose last part came from here: its first CTA, its parts
+  __shared__ int abort_word;
   volatile int* abort_flag = &abort_word;
 
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
@@ -222,9 +267,10 @@ kv4_attention_kernel(const Args a, float* __restrict__ warp_parts, float* __rest
 
   // ---- the order of all tiles: thread i counts the tiles of sequences [i share, (i + 1) share)
   const int share = (a.B + kThreads - 1) / kThreads;
+  if (tid < a.B) kept[tid] = read_seq(a, tid);
   long long mine = 0;
   for (int b = tid * share; b < min(a.B, (tid + 1) * share); ++b) {
-    const Seq s = seq_of<NT>(a, b);
+    const Seq s = seq_of<NT>(a, share == 1 ? kept[tid] : read_seq(a, b));
     mine += (long long)s.tiles * s.groups;
   }
   long long upto = mine;
@@ -233,36 +279,39 @@ kv4_attention_kernel(const Args a, float* __restrict__ warp_parts, float* __rest
     const long long v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
     if (lane >= o) upto += v;
   }
+  before[tid] = upto - mine;  // in this warp so far
   if (lane == 31) warp_total[warp] = upto;
   __syncthreads();
-  long long total = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    if (w == warp) before[tid] = total + upto - mine;
-    total += warp_total[w];
+  // lane w: the tiles before warp w's sequences
+  long long ahead = lane < kWarps ? warp_total[lane] : 0;
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) {
+    const long long v = __shfl_up_sync(0xFFFFFFFFu, ahead, o);
+    if (lane >= o) ahead += v;
   }
-  __syncthreads();
+  const long long total = __shfl_sync(0xFFFFFFFFu, ahead, kWarps - 1);
+  ahead -= lane < kWarps ? warp_total[lane] : 0;
   const long long ctas = min((long long)gridDim.x, (total + kWarps - 1) / kWarps);
   if (blockIdx.x >= ctas) return;
 
   const long long warps = ctas * kWarps, me = (long long)blockIdx.x * kWarps + warp;
   const long long u0 = part_begin(me, total, warps), u1 = part_begin(me + 1, total, warps);
-  const long long cta0 = part_begin(blockIdx.x, total, ctas), cta1 = part_begin(blockIdx.x + 1, total, ctas);
   bool ok = true;
 
   if (u0 < u1) {
     // the sequence, head and tile of place u0
     Cursor use;
     {
-      int i = 0;
-#pragma unroll
-      for (int step = 256; step; step >>= 1)
-        if (i + step < kThreads && before[i + step] <= u0) i += step;
-      long long at = before[i];
-      use.b = i * share;
-      use.s = seq_of<NT>(a, use.b);
+      // the last warp's, then the last thread's, share that begins at or before u0
+      const int w = __popc(__ballot_sync(0xFFFFFFFFu, lane < kWarps && ahead <= u0)) - 1;
+      long long at = __shfl_sync(0xFFFFFFFFu, ahead, w);
+      const int i = __popc(__ballot_sync(0xFFFFFFFFu, at + before[32 * w + lane] <= u0)) - 1;
+      at += before[32 * w + i];
+      use.b = (32 * w + i) * share;
+      use.s = seq_of<NT>(a, kept, use.b);
       while (at + (long long)use.s.tiles * use.s.groups <= u0) {
         at += (long long)use.s.tiles * use.s.groups;
-        use.s = seq_of<NT>(a, ++use.b);
+        use.s = seq_of<NT>(a, kept, ++use.b);
       }
       const int rest = (int)(u0 - at);
       use.group = rest / use.s.tiles;
@@ -299,7 +348,7 @@ kv4_attention_kernel(const Args a, float* __restrict__ warp_parts, float* __rest
                   (to - lane - skip) * G::kUnitBytes, bar);
       }
       const int b = next.b, group = next.group;
-      advance<NT>(a, next);
+      advance<NT>(a, kept, next);
       if ((next.b != b || next.group != group) && next.b < a.B) next_head = next.group / next.s.blocks;
       if (k + 1 < count) look_up();
     };
@@ -319,6 +368,22 @@ kv4_attention_kernel(const Args a, float* __restrict__ warp_parts, float* __rest
     int seg0 = 0;                  // the first tile of this warp in the current head
     int kv_head = 0, col0 = 0;
 
+    // The queries of a head as they lie in memory: lane (g, t) reads channels [t D / 4, (t + 1) D / 4) of column g.
+    uint4 raw[NT][kWords];
+    auto read_q = [&](const Cursor& c) {
+      const int head0 = c.group / c.s.blocks, first = (c.group - head0 * c.s.blocks) * kCols;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        int64_t token;
+        int head;
+        const bool in = row_of(a, c.s.begin, c.s.n, head0, first + 8 * n + g, token, head);
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + token * a.q_stride + head * D + t * (D / 4));
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) raw[n][i] = in ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    read_q(use);
+
     for (int k = 0; k < count; ++k) {
       if (k == 0 || use.tile == 0) {
         kv_head = use.group / use.s.blocks;
@@ -327,16 +392,10 @@ kv4_attention_kernel(const Args a, float* __restrict__ warp_parts, float* __rest
         vexp = -16;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          // lane (g, t) loads channels [t D / 4, (t + 1) D / 4) of column g
-          int64_t token;
-          int head;
-          const bool in = row_of(a, use.s, kv_head, col0 + 8 * n + g, token, head);
           float x[8 * kWords];
-          const uint4* src = reinterpret_cast<const uint4*>(a.q + token * a.q_stride + head * D + t * (D / 4));
 #pragma unroll
           for (int i = 0; i < kWords; ++i) {
-            const uint4 v = in ? src[i] : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            const uint32_t w[4] = {raw[n][i].x, raw[n][i].y, raw[n][i].z, raw[n][i].w};
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
               const float2 f = unpack2<BF16>(w[p]);
@@ -529,6 +588,11 @@ kv4_attention_kernel(const Args a, float* __restrict__ warp_parts, float* __rest
       else
         weigh(std::false_type{});
 
+      const bool last = use.tile + 1 == use.s.tiles || k + 1 == count;
+      const Cursor was = use;
+      advance<NT>(a, kept, use);
+      if (last && k + 1 < count) read_q(use);  // arrives during the products below
+
       // ---- output: O[channel][column]
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -548,11 +612,10 @@ kv4_attention_kernel(const Args a, float* __restrict__ warp_parts, float* __rest
           }
       }
       __syncwarp();  // every lane has read the stage
-      const bool last = use.tile + 1 == use.s.tiles || k + 1 == count;
       if (issued < count) issue(issued++);
 
       if (last) {
-        const bool whole = seg0 == 0 && use.tile + 1 == use.s.tiles;
+        const bool whole = seg0 == 0 && was.tile + 1 == was.s.tiles;
         const float back = __uint_as_float((uint32_t)(127 + vexp - 13) << 23) * 16777216.f;
         float* part = nullptr;
         if (!whole) {
@@ -561,10 +624,13 @@ kv4_attention_kernel(const Args a, float* __restrict__ warp_parts, float* __rest
           part = end ? reinterpret_cast<float*>(ring) : warp_parts + me * kPart;
           if (lane == 0) {
             Desc& d = desc[2 * warp + (end ? 1 : 0)];
-            d.first = u0 + k - use.tile;
-            d.b = use.b;
-            d.group = use.group;
+            d.first = u0 + k - was.tile;
             d.part = part;
+            d.tiles = was.s.tiles;
+            d.begin = was.s.begin;
+            d.n = was.s.n;
+            d.kv_head = kv_head;
+            d.col0 = col0;
           }
         }
 #pragma unroll
@@ -577,7 +643,7 @@ kv4_attention_kernel(const Args a, float* __restrict__ warp_parts, float* __rest
             if (whole) {
               int64_t token;
               int head;
-              if (row_of(a, use.s, kv_head, col0 + col, token, head)) {
+              if (row_of(a, was.s.begin, was.s.n, kv_head, col0 + col, token, head)) {
                 const float inv = ls == 0.f ? 0.f : 1.f / ls;
                 const int64_t row = token * a.heads + head;
                 uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + row * D + g * (D / 8));
@@ -604,7 +670,6 @@ kv4_attention_kernel(const Args a, float* __restrict__ warp_parts, float* __rest
             }
           }
       }
-      advance<NT>(a, use);
     }
     if (!ok) {
       // leave no copy in flight behind: each one is waited for, with the same limit
@@ -616,66 +681,90 @@ kv4_attention_kernel(const Args a, float* __restrict__ warp_parts, float* __rest
 
   // ---- the CTA's partials, in the order of the tiles
   __syncthreads();
-  for (int i = 0; i < 2 * kWarps;) {
-    if (!desc[i].part) {
-      ++i;
-      continue;
-    }
-    const Desc d = desc[i];
-    int end = i + 1;
-    while (end < 2 * kWarps && (!desc[end].part || desc[end].first == d.first)) ++end;
-    const Seq s = seq_of<NT>(a, d.b);
-    const int kv_head = d.group / s.blocks, col0 = (d.group - kv_head * s.blocks) * kCols;
-    const long long d1 = d.first + s.tiles;
-    const bool whole = d.first >= cta0 && d1 <= cta1;
-    // a head shared with other CTAs: slot 1 when it goes on after this one, slot 0 when it ends here
-    float* out = cta_parts + (2 * blockIdx.x + (d1 > cta1 ? 1 : 0)) * (long long)kPart;
-    for (int e = tid; e < kCols * (D / 4); e += kThreads) {
-      const int col = e / (D / 4), c4 = e - col * (D / 4);
-      Joined j{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-      for (int p = i; p < end; ++p) {
-        const float* part = desc[p].part;
-        if (part)
-          join(j, part[kCols * D + col], part[kCols * D + kCols + col],
-               *reinterpret_cast<const float4*>(part + col * D + 4 * c4));
-      }
-      if (whole) {
-        store_joined<BF16>(a, D, s, kv_head, col0 + col, c4, j);
-      } else {
-        *reinterpret_cast<float4*>(out + col * D + 4 * c4) = j.o;
-        if (c4 == 0) {
-          out[kCols * D + col] = j.m;
-          out[kCols * D + kCols + col] = j.l;
+  const long long cta0 = part_begin(blockIdx.x, total, ctas), cta1 = part_begin(blockIdx.x + 1, total, ctas);
+  // lane i looks after partial i; a group is the partials of one head
+  const bool some = lane < 2 * kWarps && desc[lane].part != nullptr;
+  const uint32_t parts = __ballot_sync(0xFFFFFFFFu, some);
+  const uint32_t below = parts & ((1u << lane) - 1u);
+  const bool leads = some && (below == 0 || desc[31 - __clz(below)].first != desc[lane].first);
+  const uint32_t leaders = __ballot_sync(0xFFFFFFFFu, leads);
+  const bool shared = leads && (desc[lane].first < cta0 || desc[lane].first + desc[lane].tiles > cta1);
+  const uint32_t open = __ballot_sync(0xFFFFFFFFu, shared);  // groups that other CTAs have a part of: two at most
+  // A head shared with other CTAs has slot 1 of this CTA when it goes on after it, slot 0 when it ends here.
+  auto slot = [&](int cta, bool goes_on) { return cta_parts + (2 * cta + (goes_on ? 1 : 0)) * (long long)kPart; };
+
+  constexpr int kLanes = D / 4, kAtOnce = 32 / kLanes;  // lanes of a column, columns of a warp at once
+  const int c4 = lane % kLanes;
+  {
+    uint32_t todo = leaders;
+    for (int item = warp * kAtOnce + lane / kLanes, k = 0; todo; todo &= todo - 1, ++k) {
+      const int lead = __ffs(todo) - 1;
+      const uint32_t rest = todo & (todo - 1);
+      const uint32_t members = parts & ~((1u << lead) - 1u) & (rest ? (rest & (0u - rest)) - 1u : 0xFFFFFFFFu);
+      const Desc& d = desc[lead];
+      for (; item < (k + 1) * kCols; item += kWarps * kAtOnce) {
+        const int col = item - k * kCols;
+        Joined j;
+        for (uint32_t m = members; m;) {
+          const int n = __popc(m);
+          join_parts<D, kCols, 4, false>(j, n, col, c4, [&](int) {
+            const float* p = desc[__ffs(m) - 1].part;
+            m &= m - 1;
+            return p;
+          });
         }
+        if (open >> lead & 1u)
+          store_part<D, kCols>(slot(blockIdx.x, d.first + d.tiles > cta1), col, c4, j);
+        else
+          store_joined<D, BF16>(a, d, col, c4, j);
       }
     }
-    if (!whole) {
-      const int c_first = part_of(d.first, total, ctas), c_last = part_of(d1 - 1, total, ctas);
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const int was = atomicAdd(&counters[c_first], 1);
-        arrived = was == c_last - c_first;
-        if (arrived) counters[c_first] = 0;  // for the next call
-        __threadfence();
-      }
-      __syncthreads();
-      if (arrived) {
-        for (int e = tid; e < kCols * (D / 4); e += kThreads) {
-          const int col = e / (D / 4), c4 = e - col * (D / 4);
-          Joined j{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-#pragma unroll 4
-          for (int c = c_first; c <= c_last; ++c) {
-            const float* part = cta_parts + (2 * c + (c < c_last ? 1 : 0)) * (long long)kPart;
-            join(j, __ldcg(part + kCols * D + col), __ldcg(part + kCols * D + kCols + col),
-                 __ldcg(reinterpret_cast<const float4*>(part + col * D + 4 * c4)));
-          }
-          store_joined<BF16>(a, D, s, kv_head, col0 + col, c4, j);
-        }
-      }
-      __syncthreads();  // `arrived` is read before the next one is written
+  }
+  if (!open) return;
+
+  // ---- heads shared with other CTAs: the last CTA to arrive joins all parts
+  const int opens = __popc(open);
+  auto open_desc = [&](int i) -> const Desc& { return desc[i == 0 ? __ffs(open) - 1 : 31 - __clz(open)]; };
+  __syncthreads();
+  if (tid < opens) {
+    const Desc& d = open_desc(tid);
+    const int first = part_of(d.first, total, ctas), n = part_of(d.first + d.tiles - 1, total, ctas) - first + 1;
+    __threadfence();  // the CTA's parts, before its arrival
+    const bool last = atomicAdd(&counters[first], 1) == n - 1;
+    if (last) counters[first] = 0;  // for the next call
+    arrived[tid] = last ? make_int2(first, n) : make_int2(0, 0);
+    __threadfence();
+  }
+  __syncthreads();
+  // few parts: a warp joins a column of them
+  for (int item = warp * kAtOnce + lane / kLanes; item < opens * kCols; item += kWarps * kAtOnce) {
+    const int i = item / kCols, col = item - i * kCols, first = arrived[i].x, n = arrived[i].y;
+    if (n == 0 || n > kFewParts) continue;
+    Joined j;
+    for (int p = 0; p < n; p += 4)
+      join_parts<D, kCols, 4, true>(j, n - p, col, c4, [&](int q) { return slot(first + p + q, p + q + 1 < n); });
+    store_joined<D, BF16>(a, open_desc(i), col, c4, j);
+  }
+  // many: each warp joins an equal share of them, then the shares are joined
+  for (int i = 0; i < opens; ++i) {
+    const int first = arrived[i].x, n = arrived[i].y;
+    if (n <= kFewParts) continue;
+    const int p0 = n * warp / kWarps, p1 = n * (warp + 1) / kWarps;
+    for (int col = lane / kLanes; col < kCols; col += kAtOnce) {
+      Joined j;
+      for (int p = p0; p < p1; p += 4)
+        join_parts<D, kCols, 4, true>(j, p1 - p, col, c4, [&](int q) { return slot(first + p + q, p + q + 1 < n); });
+      store_part<D, kCols>(reinterpret_cast<float*>(ring), col, c4, j);
     }
-    i = end;
+    __syncthreads();
+    for (int col = warp * kAtOnce + lane / kLanes; col < kCols; col += kWarps * kAtOnce) {
+      Joined j;
+      join_parts<D, kCols, kWarps, false>(j, kWarps, col, c4, [&](int w) {
+        return reinterpret_cast<const float*>(ring + (w - warp) * (G::kStages * G::kTileBytes));
+      });
+      store_joined<D, BF16>(a, open_desc(i), col, c4, j);
+    }
+    __syncthreads();  // the ring is written again
   }
 }
 

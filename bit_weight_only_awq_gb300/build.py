@@ -19,7 +19,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libawq.so")
 
 SOURCES = ("awq_api.cu", "awq_elementwise.cu", "awq_gemv.cu", "awq_gemv_pp.cu", "awq_gemm_tc.cu", "w4a8_act.cu",
-           "awq_noalloc.cu", "awq_selftest.cu", "w4a8_rmsnorm.cu", "kv4_cache.cu", "kv4_attention.cu")
+           "awq_noalloc.cu", "awq_selftest.cu", "w4a8_rmsnorm.cu", "kv4_cache.cu", "kv4_attention.cu",
+           "kv4_prefill.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]

@@ -26,6 +26,7 @@
 #include "awq_internal.h"
 #include "awq_ptx.cuh"
 #include "awq_types.cuh"
+#include "kv4_attention.cuh"
 
 namespace awq {
 namespace {
@@ -34,8 +35,6 @@ constexpr int kTile = 64;    // tokens of a tile: 4 units
 constexpr int kWarps = 12;   // three on each sub-partition
 constexpr int kThreads = 32 * kWarps;
 constexpr int kFewParts = 12;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 template <int D>
 struct Geo {
@@ -44,12 +43,6 @@ struct Geo {
   static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kRingBytes = kWarps * kStages * kTileBytes;
   static constexpr int kSmemBytes = kRingBytes + 128;
-};
-
-struct Args : Kv4AttnArgs {
-  int per;             // query heads of a cache head
-  int units_page;      // units of a page
-  uint32_t page_magic; // unit / units_page = high word of unit * page_magic (0: one unit a page)
 };
 
 // Floats of one partial result: the unnormalized output, then maximum and sum of every column.
@@ -64,16 +57,6 @@ struct Seq {
   int blocks;        // column blocks of a cache head
   int groups;        // (cache head, column block) pairs
 };
-
-// Query tokens and length of sequence b, as the device memory has them.
-__device__ __forceinline__ int3 read_seq(const Args& a, int b) {
-  int begin = b, n = 1;
-  if (a.q_start) {
-    begin = min(max(a.q_start[b], 0), (int)a.T);
-    n = min(min(max(a.q_start[b + 1], begin), (int)a.T) - begin, a.max_q);
-  }
-  return make_int3(begin, n, min(max(a.kv_len[b], 0), a.max_pages * a.page_size));
-}
 
 template <int NT>
 __device__ __forceinline__ Seq seq_of(const Args& a, const int3 v) {
@@ -123,11 +106,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
-  return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 __device__ __forceinline__ float col_max(float v) {  // over the 8 lanes that share columns
@@ -777,12 +755,7 @@ cudaError_t launch(const Kv4AttnArgs& args, void* ws, int* err, cudaStream_t s) 
   cudaError_t e = set_smem_once(fn, Geo<D>::kSmemBytes);
   if (e != cudaSuccess) return e;
   const int ctas = device_sm_count();
-  Args a;
-  static_cast<Kv4AttnArgs&>(a) = args;
-  a.per = args.heads / args.kv_heads;
-  a.units_page = args.page_size / kKv4Unit;
-  // exact for units below 2^32 / units_page >= 2^26: lengths are at most 2^30 tokens
-  a.page_magic = a.units_page == 1 ? 0u : (uint32_t)(((1ull << 32) + a.units_page - 1) / a.units_page);
+  const Args a = make_args(args);
   uint8_t* base = static_cast<uint8_t*>(ws);
   float* warp_parts = reinterpret_cast<float*>(base + kCounterBytes);
   float* cta_parts = warp_parts + (size_t)ctas * kWarps * part_floats(D, 8 * NT);
@@ -803,13 +776,22 @@ cudaError_t launch(const Kv4AttnArgs& args, void* ws, int* err, cudaStream_t s) 
 
 }  // namespace
 
-// Counters, a partial for each warp, and two for each CTA.
-size_t kv4_attention_workspace(int64_t, int64_t, int max_q, int heads, int kv_heads, int dim) {
+// From this many query rows of a cache head on, the tcgen05 kernel takes the call.
+constexpr int64_t kPrefillRows = 64;
+bool many(int64_t T, int max_q, int heads, int kv_heads) {
+  return (max_q < T ? max_q : T) * (heads / kv_heads) >= kPrefillRows;
+}
+
+// Counters, a partial for each warp, and two for each CTA; or the other kernel's partials after the counters.
+size_t kv4_attention_workspace(int64_t T, int64_t B, int max_q, int heads, int kv_heads, int dim) {
+  if (many(T, max_q, heads, kv_heads)) return kCounterBytes + align256(kv4_prefill_workspace(T, B, max_q, heads, kv_heads, dim));
   const size_t part = sizeof(float) * part_floats(dim, narrow(max_q, heads, kv_heads) ? 8 : 16);
   return kCounterBytes + align256((size_t)device_sm_count() * (kWarps + 2) * part);
 }
 
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, int dim, bool bf16, void* ws, int* err, cudaStream_t s) {
+  if (many(a.T, a.max_q, a.heads, a.kv_heads))
+    return launch_kv4_prefill(a, dim, bf16, static_cast<uint8_t*>(ws) + kCounterBytes, err, s);
   if (narrow(a.max_q, a.heads, a.kv_heads)) {
     if (dim == 128) return bf16 ? launch<128, true, 1>(a, ws, err, s) : launch<128, false, 1>(a, ws, err, s);
     return bf16 ? launch<64, true, 1>(a, ws, err, s) : launch<64, false, 1>(a, ws, err, s);

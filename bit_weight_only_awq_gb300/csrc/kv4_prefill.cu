@@ -8,14 +8,15 @@
 //
 // A CTA takes 256 query rows (query token, head) of one cache head in two tiles of 128, and goes over the cache in
 // tiles of 128 tokens.  tcgen05.mma kind::f16, M = 128:
-//   S[row][token] = Q' U_k^T   A = queries, B = key codes, both K-major in shared memory, N = 128
+//   S[row][token] = Q' U_k^T   A = queries, B = key codes, both K-major in shared memory, N = 64
 //   O[row][channel] += W U_v   A = weights, in tensor memory where S was, B = value codes, K-major, N = D
 // The codes become fp16 halves with one AND for two of them: u 2^-24 in the lowest nibble, 16 u 2^-24 in the next.
 // The factor 16 is taken out of the queries (channels 2, 3 of four) and of the output (odd channels).
 //
 // Roles: warps 0-3 and 4-7 are the softmax of the two row tiles (a thread has a row), warp 8 issues the products,
 // warp 9 copies units, warps 10-13 turn codes into operands.  While one row tile's softmax runs, the other's products
-// do.  The output stays in tensor memory; it is rescaled only when a row's maximum has grown by more than 2^8, so the
+// do; a tile's two halves of 64 tokens have an S each, so that a row tile's next scores are there before it is done
+// with the present ones.  The output stays in tensor memory; it is rescaled only when a row's maximum has grown by more than 2^8, so the
 // weights are at most 2^8 and enter fp16 as p sv 2^(5 - e), 2^e the largest value scale so far.
 #include <cmath>
 #include <type_traits>
@@ -49,7 +50,7 @@ struct Geo {
   static constexpr int kMetaBytes = 4 * kTok * 4 + 16;  // key scale, key zero, value scale, value zero; largest exponents
   static constexpr int kRawAt = kMeta + 2 * kMetaBytes;
   static constexpr int kSmem = kRawAt + kRaw * kRawBytes + 1024;
-  static constexpr uint32_t kIdescS = (1u << 4) | ((kTok / 8) << 17) | ((128 / 16) << 24);
+  static constexpr uint32_t kIdescS = (1u << 4) | ((kHalf / 8) << 17) | ((128 / 16) << 24);
   static constexpr uint32_t kIdescO = (1u << 4) | ((D / 8) << 17) | ((128 / 16) << 24);
   static_assert(kSmem <= 227 * 1024 - 512, "shared memory");
 };
@@ -64,23 +65,32 @@ __device__ __forceinline__ void wait_loaded(uint32_t (&r)[16]) {
 }
 
 struct Bars {
-  uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2][2],
+  uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[2][2], k_empty[2], v_full[2], v_empty[2], s_full[2][2], p_full[2][2],
       o_done[2][2], q_full, done;
 };
 
+// The products and commits are executed by the whole warp, with the same operands in every lane, and issued by
+// the one that elect.sync chooses (always the same): operands that the compiler sees as uniform need no moves between
+// register files before each product, which cost more than the product itself.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "{\n .reg .pred p, q;\n elect.sync _|q, 0xFFFFFFFF;\n setp.ne.b32 p, %4, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
 // A in tensor memory: a lane for each row, two halves a column.
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "{\n .reg .pred p, q;\n elect.sync _|q, 0xFFFFFFFF;\n setp.ne.b32 p, %4, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xFFFFFFFF;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -183,11 +193,13 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
       mbar_init(smem_u32(&bars.raw_empty[i]), kDqThreads);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&bars.k_full[i]), 2 * kDqThreads);
+      mbar_init(smem_u32(&bars.k_full[i][0]), kDqThreads);
+      mbar_init(smem_u32(&bars.k_full[i][1]), kDqThreads);
       mbar_init(smem_u32(&bars.v_full[i]), 2 * kDqThreads);
       mbar_init(smem_u32(&bars.k_empty[i]), 1);
       mbar_init(smem_u32(&bars.v_empty[i]), 1);
-      mbar_init(smem_u32(&bars.s_full[i]), 1);
+      mbar_init(smem_u32(&bars.s_full[i][0]), 1);
+      mbar_init(smem_u32(&bars.s_full[i][1]), 1);
       mbar_init(smem_u32(&bars.o_done[i][0]), 1);
       mbar_init(smem_u32(&bars.o_done[i][1]), 1);
       mbar_init(smem_u32(&bars.p_full[i][0]), 128);
@@ -259,15 +271,15 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
     const F2 qr2(qr, qr), qk2(qk, qk);
     for (int j = 0; j < count && ok; ++j) {
       const int b = j & 1;
-      ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bars.s_full[m]), j & 1, abort_flag, err, 621));
-      // the scales and zeros are read with the tile's codes ready: keys' before S, values' before O
-      ok = ok && __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bars.v_full[b]), (j >> 1) & 1, abort_flag, err, 622));
-      if (!ok) break;
-      tc_fence_after();
       const uint8_t* meta = smem + G::kMeta + b * G::kMetaBytes;
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         const int j0 = (job.tile0 + j) * kTok + h * kHalf;
+        // the scales and zeros are there with the keys
+        ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bars.k_full[b][h]), (j >> 1) & 1, abort_flag, err, 622)) &&
+             __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bars.s_full[m][h]), j & 1, abort_flag, err, 621));
+        if (!ok) break;
+        tc_fence_after();
         uint32_t raw[4][16];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld16_nowait(s_addr + h * kHalf + 16 * c, raw[c]);
@@ -311,8 +323,8 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
           l *= f;
           z *= f;
           if (j > 0 || h > 0) {
-            // the products into O so far: those of the tiles before have completed with this S, the first half's may run
-            if (h > 0) ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bars.o_done[m][0]), j & 1, abort_flag, err, 623));
+            // the products into O so far: the last ones, of the half before, may still run
+            ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bars.o_done[m][h ^ 1]), (j - 1 + h) & 1, abort_flag, err, 623));
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
@@ -419,62 +431,59 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
       }
     }
   } else if (warp == 8) {
-    // ------------------------------------------------ products, issued by one thread
-    if (lane == 0) {
-      bool ok = wait_bounded(smem_u32(&bars.q_full), 0, abort_flag, err, 611);
-      auto scores = [&](int m, int j) {
-        const int b = j & 1;
-        const uint64_t qa = smem_desc_sw128(sm + G::kQ + m * G::kQTile, 16, 1024);
-        const uint64_t kb = smem_desc_sw128(sm + G::kK + b * G::kKTile, 16, 1024);
+    // ------------------------------------------------ products
+    bool ok = true;
+    auto wait = [&](uint64_t& bar, uint32_t parity, int id) {
+      return __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bar), parity, abort_flag, err, id)) != 0;
+    };
+    ok = wait(bars.q_full, 0, 611);
+    auto scores = [&](int m, int j, int h) {
+      const uint64_t qa = smem_desc_sw128(sm + G::kQ + m * G::kQTile, 16, 1024);
+      const uint64_t kb = smem_desc_sw128(sm + G::kK + (j & 1) * G::kKTile + h * (kHalf * 128), 16, 1024);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t at = (uint64_t)((k / 4) * (16384 >> 4) + (k % 4) * 2);
-          mma_ss(tmem + 128 * m, qa + at, kb + at, G::kIdescS, k > 0 ? 1u : 0u);
-        }
-        mma_commit(smem_u32(&bars.s_full[m]));
-      };
-      auto begin_scores = [&](int j) {  // the first row tile that has tile j waits for its keys
-        ok = ok && wait_bounded(smem_u32(&bars.k_full[j & 1]), (j >> 1) & 1, abort_flag, err, 612);
-        if (ok) tc_fence_after();
-        return ok;
-      };
-      if (job.total > 0 && begin_scores(0)) {
-        for (int m = 0; m < 2; ++m)
-          if (job.count[m] > 0) scores(m, 0);
-        mma_commit(smem_u32(&bars.k_empty[0]));
-        for (int j = 0; j < job.total && ok; ++j) {
-          const int b = j & 1;
-          const uint64_t vb = smem_desc_sw128(sm + G::kV + b * G::kVTile, 16, 1024);
-          bool keys = false;
-          for (int m = 0; m < 2 && ok; ++m) {
-            if (j < job.count[m]) {
-              for (int h = 0; h < 2 && ok; ++h) {
-                ok = wait_bounded(smem_u32(&bars.p_full[m][h]), j & 1, abort_flag, err, 613);
-                if (ok && h == 0) ok = wait_bounded(smem_u32(&bars.v_full[b]), (j >> 1) & 1, abort_flag, err, 614);
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  mma_ts(tmem + 256 + 128 * m, tmem + 128 * m + h * kHalf + 8 * k,
-                         vb + (uint64_t)(h * ((D * 128) >> 4) + k * 2), G::kIdescO, (j | h | k) ? 1u : 0u);
-                mma_commit(smem_u32(&bars.o_done[m][h]));
-              }
-            }
-            if (ok && j + 1 < job.count[m]) {
-              if (!keys) keys = begin_scores(j + 1);
-              if (ok) scores(m, j + 1);
-            }
-          }
-          if (!ok) break;
-          mma_commit(smem_u32(&bars.v_empty[b]));
-          if (j + 1 < job.total) mma_commit(smem_u32(&bars.k_empty[(j + 1) & 1]));
-        }
+      for (int k = 0; k < D / 16; ++k) {
+        const uint64_t at = (uint64_t)((k / 4) * (16384 >> 4) + (k % 4) * 2);
+        mma_ss(tmem + 128 * m + kHalf * h, qa + at, kb + at, G::kIdescS, k > 0 ? 1u : 0u);
       }
-      // every product has completed before tensor memory is given back
-      mma_commit(smem_u32(&bars.done));
-      volatile int no_abort = 0;
-      wait_bounded(smem_u32(&bars.done), 0, &no_abort, err, 615);
+      commit(smem_u32(&bars.s_full[m][h]));
+    };
+    auto have_keys = [&](int j, int h) {
+      ok = ok && wait(bars.k_full[j & 1][h], (j >> 1) & 1, 612);
+      if (ok) tc_fence_after();
+      return ok;
+    };
+    for (int h = 0; h < 2 && job.total > 0; ++h)
+      if (have_keys(0, h))
+        for (int m = 0; m < 2; ++m)
+          if (job.count[m] > 0) scores(m, 0, h);
+    if (ok && job.total > 0) commit(smem_u32(&bars.k_empty[0]));
+    for (int j = 0; j < job.total && ok; ++j) {
+      const int b = j & 1;
+      const uint64_t vb = smem_desc_sw128(sm + G::kV + b * G::kVTile, 16, 1024);
+      for (int h = 0; h < 2 && ok; ++h)
+        for (int m = 0; m < 2 && ok; ++m) {
+          if (j < job.count[m]) {
+            ok = wait(bars.p_full[m][h], j & 1, 613) &&
+                 wait(bars.v_full[b], (j >> 1) & 1, 614);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ts(tmem + 256 + 128 * m, tmem + 128 * m + h * kHalf + 8 * k,
+                     vb + (uint64_t)(h * ((D * 128) >> 4) + k * 2), G::kIdescO, (j | h | k) ? 1u : 0u);
+            commit(smem_u32(&bars.o_done[m][h]));
+          }
+          // the half's scores of the next tile go where its weights were
+          if (j + 1 < job.count[m] && have_keys(j + 1, h)) scores(m, j + 1, h);
+        }
+      if (!ok) break;
+      commit(smem_u32(&bars.v_empty[b]));
+      if (j + 1 < job.total) commit(smem_u32(&bars.k_empty[(j + 1) & 1]));
     }
+    // every product has completed before tensor memory is given back
+    commit(smem_u32(&bars.done));
+    volatile int no_abort = 0;
+    wait_bounded(smem_u32(&bars.done), 0, &no_abort, err, 615);
   } else if (warp == 9) {
     // ------------------------------------------------ copies: lane u takes unit u of a half tile
     const int halves = 2 * job.total;
@@ -542,7 +551,7 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
                x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u);
       }
       fence_async();
-      mbar_arrive(smem_u32(&bars.k_full[b]));
+      mbar_arrive(smem_u32(&bars.k_full[b][h]));
       // values: eight tokens of a channel are one chunk of its row.  Thread: eight tokens tc, channels [g D / 8, ...),
       // a part of its quads; odd eights read their words pair by pair the other way round, so that the reads of
       // eight lanes fall into different banks.

@@ -33,6 +33,10 @@ namespace {
 constexpr int kRows = 256;   // query rows of a CTA
 constexpr int kTok = 128;    // tokens of a tile
 constexpr int kHalf = 64;    // tokens of a raw slot, and of one step of the softmax
+constexpr int kBufs = 4;     // operand buffers of a step's keys, and of its values
+// Scales and zeros of a step stay until its weights are made.  A step's keys are made at the earliest when the values
+// of the one before it are, which is after the weights of five steps before: six buffers.
+constexpr int kMetas = 6;
 constexpr int kRaw = 3;      // raw slots
 constexpr int kDqThreads = 128;
 constexpr int kThreads = 448;
@@ -44,11 +48,11 @@ struct Geo {
   static constexpr int kUnitStride = kUnitBytes + 32;  // units 32 bytes apart in the banks: the value words' reads
   static constexpr int kRawBytes = 4 * kUnitStride;
   static constexpr int kQTile = 128 * D * 2;           // one row tile, D / 64 blocks of 128 rows x 128 bytes
-  static constexpr int kKTile = kTok * D * 2;          // likewise
-  static constexpr int kVTile = kTok * D * 2;          // 2 blocks (64 tokens) of D rows x 128 bytes
-  static constexpr int kQ = 0, kK = kQ + 2 * kQTile, kV = kK + 2 * kKTile, kMeta = kV + 2 * kVTile;
-  static constexpr int kMetaBytes = 4 * kTok * 4 + 16;  // key scale, key zero, value scale, value zero; largest exponents
-  static constexpr int kRawAt = kMeta + 2 * kMetaBytes;
+  static constexpr int kKStep = kHalf * D * 2;         // a step's keys, D / 64 blocks of 64 rows x 128 bytes
+  static constexpr int kVStep = kHalf * D * 2;         // a step's values, D rows x 128 bytes
+  static constexpr int kQ = 0, kK = kQ + 2 * kQTile, kV = kK + kBufs * kKStep, kMeta = kV + kBufs * kVStep;
+  static constexpr int kMetaBytes = 4 * kHalf * 4 + 16;  // key scale, key zero, value scale, value zero; largest exponents
+  static constexpr int kRawAt = kMeta + kMetas * kMetaBytes;
   static constexpr int kSmem = kRawAt + kRaw * kRawBytes + 1024;
   static constexpr uint32_t kIdescS = (1u << 4) | ((kHalf / 8) << 17) | ((128 / 16) << 24);
   static constexpr uint32_t kIdescO = (1u << 4) | ((D / 8) << 17) | ((128 / 16) << 24);
@@ -65,7 +69,7 @@ __device__ __forceinline__ void wait_loaded(uint32_t (&r)[16]) {
 }
 
 struct Bars {
-  uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[2][2], k_empty[2], v_full[2], v_empty[2], s_full[2][2], p_full[2][2],
+  uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[kBufs], k_empty[kBufs], v_full[kBufs], v_empty[kBufs], s_full[2][2], p_full[2][2],
       o_done[2][2], q_full, done;
 };
 
@@ -177,7 +181,7 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   volatile int* abort_flag = &abort_word;
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid / 32, 0), lane = tid % 32;
   const int split = blockIdx.x % splits;
   // the blocks that see the most tokens first
   const int row_block = (int)(gridDim.x / splits) - 1 - blockIdx.x / splits;
@@ -192,12 +196,13 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
       mbar_init(smem_u32(&bars.raw_full[i]), 1);
       mbar_init(smem_u32(&bars.raw_empty[i]), kDqThreads);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&bars.k_full[i][0]), kDqThreads);
-      mbar_init(smem_u32(&bars.k_full[i][1]), kDqThreads);
-      mbar_init(smem_u32(&bars.v_full[i]), 2 * kDqThreads);
+    for (int i = 0; i < kBufs; ++i) {
+      mbar_init(smem_u32(&bars.k_full[i]), kDqThreads);
+      mbar_init(smem_u32(&bars.v_full[i]), kDqThreads);
       mbar_init(smem_u32(&bars.k_empty[i]), 1);
       mbar_init(smem_u32(&bars.v_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&bars.s_full[i][0]), 1);
       mbar_init(smem_u32(&bars.s_full[i][1]), 1);
       mbar_init(smem_u32(&bars.o_done[i][0]), 1);
@@ -270,13 +275,13 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
     const int count = job.count[m];
     const F2 qr2(qr, qr), qk2(qk, qk);
     for (int j = 0; j < count && ok; ++j) {
-      const int b = j & 1;
-      const uint8_t* meta = smem + G::kMeta + b * G::kMetaBytes;
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         const int j0 = (job.tile0 + j) * kTok + h * kHalf;
         // the scales and zeros are there with the keys
-        ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bars.k_full[b][h]), (j >> 1) & 1, abort_flag, err, 622)) &&
+        const int step = 2 * j + h;
+        const uint8_t* meta = smem + G::kMeta + step % kMetas * G::kMetaBytes;
+        ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bars.k_full[step % kBufs]), step / kBufs & 1, abort_flag, err, 622)) &&
              __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bars.s_full[m][h]), j & 1, abort_flag, err, 621));
         if (!ok) break;
         tc_fence_after();
@@ -285,11 +290,11 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
         for (int c = 0; c < 4; ++c) tmem_ld16_nowait(s_addr + h * kHalf + 16 * c, raw[c]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) wait_loaded(raw[c]);
-        const float4* ks = reinterpret_cast<const float4*>(meta + h * kHalf * 4);
-        const float4* kz = reinterpret_cast<const float4*>(meta + kTok * 4 + h * kHalf * 4);
-        const float4* vs = reinterpret_cast<const float4*>(meta + 2 * kTok * 4 + h * kHalf * 4);
-        const float4* vz = reinterpret_cast<const float4*>(meta + 3 * kTok * 4 + h * kHalf * 4);
-        const int2 ve2 = *reinterpret_cast<const int2*>(meta + 4 * kTok * 4 + h * 8);
+        const float4* ks = reinterpret_cast<const float4*>(meta + 0 * kHalf * 4);
+        const float4* kz = reinterpret_cast<const float4*>(meta + 1 * kHalf * 4);
+        const float4* vs = reinterpret_cast<const float4*>(meta + 2 * kHalf * 4);
+        const float4* vz = reinterpret_cast<const float4*>(meta + 3 * kHalf * 4);
+        const int2 ve2 = *reinterpret_cast<const int2*>(meta + 4 * kHalf * 4);
         F2 t[32];
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
@@ -437,48 +442,48 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
       return __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bar), parity, abort_flag, err, id)) != 0;
     };
     ok = wait(bars.q_full, 0, 611);
-    auto scores = [&](int m, int j, int h) {
+    // step: 64 tokens; a row tile's scores of steps 2j and 2j + 1 have an S each
+    auto scores = [&](int m, int step) {
       const uint64_t qa = smem_desc_sw128(sm + G::kQ + m * G::kQTile, 16, 1024);
-      const uint64_t kb = smem_desc_sw128(sm + G::kK + (j & 1) * G::kKTile + h * (kHalf * 128), 16, 1024);
+      const uint64_t kb = smem_desc_sw128(sm + G::kK + step % kBufs * G::kKStep, 16, 1024);
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint64_t at = (uint64_t)((k / 4) * (16384 >> 4) + (k % 4) * 2);
-        mma_ss(tmem + 128 * m + kHalf * h, qa + at, kb + at, G::kIdescS, k > 0 ? 1u : 0u);
-      }
-      commit(smem_u32(&bars.s_full[m][h]));
+      for (int k = 0; k < D / 16; ++k)
+        mma_ss(tmem + 128 * m + step % 2 * kHalf, qa + (uint64_t)((k / 4) * (16384 >> 4) + (k % 4) * 2),
+               kb + (uint64_t)((k / 4) * (kHalf * 128 >> 4) + (k % 4) * 2), G::kIdescS, k > 0 ? 1u : 0u);
+      commit(smem_u32(&bars.s_full[m][step % 2]));
     };
-    auto have_keys = [&](int j, int h) {
-      ok = ok && wait(bars.k_full[j & 1][h], (j >> 1) & 1, 612);
+    auto have_keys = [&](int step) {
+      ok = ok && wait(bars.k_full[step % kBufs], step / kBufs & 1, 612);
       if (ok) tc_fence_after();
       return ok;
     };
-    for (int h = 0; h < 2 && job.total > 0; ++h)
-      if (have_keys(0, h))
+    const int steps = 2 * job.total;
+    for (int step = 0; step < 2 && step < steps; ++step)
+      if (have_keys(step)) {
         for (int m = 0; m < 2; ++m)
-          if (job.count[m] > 0) scores(m, 0, h);
-    if (ok && job.total > 0) commit(smem_u32(&bars.k_empty[0]));
-    for (int j = 0; j < job.total && ok; ++j) {
-      const int b = j & 1;
-      const uint64_t vb = smem_desc_sw128(sm + G::kV + b * G::kVTile, 16, 1024);
-      for (int h = 0; h < 2 && ok; ++h)
-        for (int m = 0; m < 2 && ok; ++m) {
-          if (j < job.count[m]) {
-            ok = wait(bars.p_full[m][h], j & 1, 613) &&
-                 wait(bars.v_full[b], (j >> 1) & 1, 614);
-            if (!ok) break;
-            tc_fence_after();
+          if (job.count[m] > 0) scores(m, step);
+        commit(smem_u32(&bars.k_empty[step]));
+      }
+    for (int step = 0; step < steps && ok; ++step) {
+      const int j = step / 2, h = step % 2;
+      const uint64_t vb = smem_desc_sw128(sm + G::kV + step % kBufs * G::kVStep, 16, 1024);
+      for (int m = 0; m < 2 && ok; ++m) {
+        if (j < job.count[m]) {
+          ok = wait(bars.p_full[m][h], j & 1, 613) && wait(bars.v_full[step % kBufs], step / kBufs & 1, 614);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_ts(tmem + 256 + 128 * m, tmem + 128 * m + h * kHalf + 8 * k,
-                     vb + (uint64_t)(h * ((D * 128) >> 4) + k * 2), G::kIdescO, (j | h | k) ? 1u : 0u);
-            commit(smem_u32(&bars.o_done[m][h]));
-          }
-          // the half's scores of the next tile go where its weights were
-          if (j + 1 < job.count[m] && have_keys(j + 1, h)) scores(m, j + 1, h);
+          for (int k = 0; k < 4; ++k)
+            mma_ts(tmem + 256 + 128 * m, tmem + 128 * m + h * kHalf + 8 * k, vb + (uint64_t)(k * 2), G::kIdescO,
+                   (step | k) ? 1u : 0u);
+          commit(smem_u32(&bars.o_done[m][h]));
         }
+        // the scores of the step after the next go where these weights were
+        if (j + 1 < job.count[m] && have_keys(step + 2)) scores(m, step + 2);
+      }
       if (!ok) break;
-      commit(smem_u32(&bars.v_empty[b]));
-      if (j + 1 < job.total) commit(smem_u32(&bars.k_empty[(j + 1) & 1]));
+      commit(smem_u32(&bars.v_empty[step % kBufs]));
+      if (step + 2 < steps) commit(smem_u32(&bars.k_empty[(step + 2) % kBufs]));
     }
     // every product has completed before tensor memory is given back
     commit(smem_u32(&bars.done));
@@ -517,41 +522,43 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
     const int d = tid - 320, w = d / 32;
     bool ok = true;
     for (int k = 0; k < 2 * job.total && ok; ++k) {
-      const int j = k / 2, h = k % 2, b = j & 1, st = k % kRaw;
+      const int st = k % kRaw, buf = k % kBufs;
       ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bars.raw_full[st]), (uint32_t)(k / kRaw) & 1u, abort_flag, err, 631));
-      if (ok && h == 0 && j >= 2) {
-        ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bars.k_empty[b]), (uint32_t)(j / 2 - 1) & 1u, abort_flag, err, 632)) &&
-             __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bars.v_empty[b]), (uint32_t)(j / 2 - 1) & 1u, abort_flag, err, 633));
-      }
+      if (ok && k >= kBufs)
+        ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bars.k_empty[buf]), (uint32_t)(k / kBufs - 1) & 1u, abort_flag, err, 632));
       if (!ok) break;
       const uint8_t* raw = smem + G::kRawAt + st * G::kRawBytes;
       // scales and zeros as fp32, zeros for tokens outside the sequence: their bytes may be anything
       if (d < kHalf) {
-        const int at = (job.tile0 + j) * kTok + h * kHalf + d;
+        const int at = job.tile0 * kTok + k * kHalf + d;
         uint2 mt = *reinterpret_cast<const uint2*>(raw + (d / 16) * G::kUnitStride + 16 * D + (d % 16) * 8);
         if (at < job.lo || at >= job.len) mt = make_uint2(0u, 0u);
         const float2 ksz = unpack2<false>(mt.x), vsz = unpack2<false>(mt.y);
-        uint8_t* meta = smem + G::kMeta + b * G::kMetaBytes;
-        float* f = reinterpret_cast<float*>(meta) + h * kHalf + d;
+        uint8_t* meta = smem + G::kMeta + k % kMetas * G::kMetaBytes;
+        float* f = reinterpret_cast<float*>(meta) + d;
         f[0] = ksz.x;
-        f[kTok] = ksz.y;
-        f[2 * kTok] = vsz.x;
-        f[3 * kTok] = vsz.y;
+        f[kHalf] = ksz.y;
+        f[2 * kHalf] = vsz.x;
+        f[3 * kHalf] = vsz.y;
         // the value scales of these 32 tokens are below 2^(that)
         const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, mt.y & 0x7FFFu);
-        if (lane == 0) *reinterpret_cast<int*>(meta + 4 * kTok * 4 + h * 8 + 4 * w) = (int)(most >> 10) - 14;
+        if (lane == 0) *reinterpret_cast<int*>(meta + 4 * kHalf * 4 + 4 * w) = (int)(most >> 10) - 14;
       }
       // keys: a word is eight channels of a token, one 16-byte chunk of its row
 #pragma unroll 4
       for (int i = d; i < kHalf * (D / 8); i += kDqThreads) {
-        const int tok = i / (D / 8), c = i % (D / 8), row = h * kHalf + tok;
+        const int tok = i / (D / 8), c = i % (D / 8);
         const uint32_t x = *reinterpret_cast<const uint32_t*>(raw + (tok / 16) * G::kUnitStride + (tok % 16) * (D / 2) + 4 * c);
         const uint32_t y = x >> 8;
-        sts128(sm + G::kK + b * G::kKTile + (c / 8) * 16384 + row * 128 + ((c % 8) ^ (row % 8)) * 16, x & 0x000F000Fu,
+        sts128(sm + G::kK + buf * G::kKStep + (c / 8) * (kHalf * 128) + tok * 128 + ((c % 8) ^ (tok % 8)) * 16, x & 0x000F000Fu,
                x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u);
       }
       fence_async();
-      mbar_arrive(smem_u32(&bars.k_full[b][h]));
+      mbar_arrive(smem_u32(&bars.k_full[buf]));
+      if (k >= kBufs) {
+        ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bars.v_empty[buf]), (uint32_t)(k / kBufs - 1) & 1u, abort_flag, err, 633));
+        if (!ok) break;
+      }
       // values: eight tokens of a channel are one chunk of its row.  Thread: eight tokens tc, channels [g D / 8, ...),
       // a part of its quads; odd eights read their words pair by pair the other way round, so that the reads of
       // eight lanes fall into different banks.
@@ -579,12 +586,12 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
             const int ch = g * (D / 8) + 4 * (q0 + q) + e;
             const uint32_t mask = e % 2 ? 0x00F000F0u : 0x000F000Fu;
             const int sh = e / 2 * 8;
-            sts128(sm + G::kV + b * G::kVTile + h * (D * 128) + ch * 128 + (tc ^ (ch % 8)) * 16, x[0][q] >> sh & mask,
+            sts128(sm + G::kV + buf * G::kVStep + ch * 128 + (tc ^ (ch % 8)) * 16, x[0][q] >> sh & mask,
                    x[1][q] >> sh & mask, x[2][q] >> sh & mask, x[3][q] >> sh & mask);
           }
       }
       fence_async();
-      mbar_arrive(smem_u32(&bars.v_full[b]));
+      mbar_arrive(smem_u32(&bars.v_full[buf]));
       mbar_arrive(smem_u32(&bars.raw_empty[st]));
     }
   }

@@ -13,8 +13,8 @@
 // The codes become fp16 halves with one AND for two of them: u 2^-24 in the lowest nibble, 16 u 2^-24 in the next.
 // The factor 16 is taken out of the queries (channels 2, 3 of four) and of the output (odd channels).
 //
-// Roles: warps 0-3 and 4-7 are the softmax of the two row tiles (a thread has a row), warp 8 issues the products,
-// warp 9 copies units, warps 10-13 turn codes into operands.  While one row tile's softmax runs, the other's products
+// Roles: warps 0-3 and 4-7 are the softmax of the two row tiles (a thread has a row), warps 8 and 9 issue their
+// products, warp 10 copies units, warps 11-14 turn codes into operands.  While one row tile's softmax runs, the other's products
 // do; a tile's two halves of 64 tokens have an S each, so that a row tile's next scores are there before it is done
 // with the present ones.  The output stays in tensor memory; it is rescaled only when a row's maximum has grown by more than 2^8, so the
 // weights are at most 2^8 and enter fp16 as p sv 2^(5 - e), 2^e the largest value scale so far.
@@ -39,7 +39,7 @@ constexpr int kBufs = 4;     // operand buffers of a step's keys, and of its val
 constexpr int kMetas = 6;
 constexpr int kRaw = 3;      // raw slots
 constexpr int kDqThreads = 128;
-constexpr int kThreads = 448;
+constexpr int kThreads = 480;
 constexpr float kGrow = 8.f;  // growth of the maximum (base 2) that rescales the output
 
 template <int D>
@@ -199,8 +199,8 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
     for (int i = 0; i < kBufs; ++i) {
       mbar_init(smem_u32(&bars.k_full[i]), kDqThreads);
       mbar_init(smem_u32(&bars.v_full[i]), kDqThreads);
-      mbar_init(smem_u32(&bars.k_empty[i]), 1);
-      mbar_init(smem_u32(&bars.v_empty[i]), 1);
+      mbar_init(smem_u32(&bars.k_empty[i]), 2);
+      mbar_init(smem_u32(&bars.v_empty[i]), 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&bars.s_full[i][0]), 1);
@@ -211,7 +211,7 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
       mbar_init(smem_u32(&bars.p_full[i][1]), 128);
     }
     mbar_init(smem_u32(&bars.q_full), 256);
-    mbar_init(smem_u32(&bars.done), 1);
+    mbar_init(smem_u32(&bars.done), 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async();
   }
@@ -435,61 +435,54 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
         a.lse[row] = l == 0.f ? -INFINITY : (high + log2f(l * unit)) * kLn2;
       }
     }
-  } else if (warp == 8) {
-    // ------------------------------------------------ products
-    bool ok = true;
+  } else if (warp < 10) {
+    // ------------------------------------------------ products: a warp for each row tile
+    const int m = warp - 8, mine = 2 * job.count[m], steps = 2 * job.total;
     auto wait = [&](uint64_t& bar, uint32_t parity, int id) {
       return __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bar), parity, abort_flag, err, id)) != 0;
     };
-    ok = wait(bars.q_full, 0, 611);
-    // step: 64 tokens; a row tile's scores of steps 2j and 2j + 1 have an S each
-    auto scores = [&](int m, int step) {
-      const uint64_t qa = smem_desc_sw128(sm + G::kQ + m * G::kQTile, 16, 1024);
-      const uint64_t kb = smem_desc_sw128(sm + G::kK + step % kBufs * G::kKStep, 16, 1024);
+    bool ok = wait(bars.q_full, 0, 611);
+    const uint64_t qa = smem_desc_sw128(sm + G::kQ + m * G::kQTile, 16, 1024);
+    const uint64_t kb = smem_desc_sw128(sm + G::kK, 16, 1024), vb = smem_desc_sw128(sm + G::kV, 16, 1024);
+    // step: 64 tokens; the scores of even and odd steps have an S each
+    auto scores = [&](int step) {
+      const int buf = step % kBufs;
+      ok = ok && wait(bars.k_full[buf], step / kBufs & 1, 612);
+      if (!ok) return;
+      tc_fence_after();
+      if (step < mine) {
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        mma_ss(tmem + 128 * m + step % 2 * kHalf, qa + (uint64_t)((k / 4) * (16384 >> 4) + (k % 4) * 2),
-               kb + (uint64_t)((k / 4) * (kHalf * 128 >> 4) + (k % 4) * 2), G::kIdescS, k > 0 ? 1u : 0u);
-      commit(smem_u32(&bars.s_full[m][step % 2]));
-    };
-    auto have_keys = [&](int step) {
-      ok = ok && wait(bars.k_full[step % kBufs], step / kBufs & 1, 612);
-      if (ok) tc_fence_after();
-      return ok;
-    };
-    const int steps = 2 * job.total;
-    for (int step = 0; step < 2 && step < steps; ++step)
-      if (have_keys(step)) {
-        for (int m = 0; m < 2; ++m)
-          if (job.count[m] > 0) scores(m, step);
-        commit(smem_u32(&bars.k_empty[step]));
+        for (int k = 0; k < D / 16; ++k)
+          mma_ss(tmem + 128 * m + step % 2 * kHalf, qa + (uint64_t)((k / 4) * (16384 >> 4) + (k % 4) * 2),
+                 kb + (uint64_t)(buf * (G::kKStep >> 4) + (k / 4) * (kHalf * 128 >> 4) + (k % 4) * 2), G::kIdescS, k > 0 ? 1u : 0u);
+        commit(smem_u32(&bars.s_full[m][step % 2]));
       }
+      commit(smem_u32(&bars.k_empty[buf]));
+    };
+    for (int step = 0; step < 2 && step < steps; ++step) scores(step);
     for (int step = 0; step < steps && ok; ++step) {
-      const int j = step / 2, h = step % 2;
-      const uint64_t vb = smem_desc_sw128(sm + G::kV + step % kBufs * G::kVStep, 16, 1024);
-      for (int m = 0; m < 2 && ok; ++m) {
-        if (j < job.count[m]) {
-          ok = wait(bars.p_full[m][h], j & 1, 613) && wait(bars.v_full[step % kBufs], step / kBufs & 1, 614);
-          if (!ok) break;
-          tc_fence_after();
+      const int buf = step % kBufs;
+      ok = wait(bars.v_full[buf], step / kBufs & 1, 614);
+      if (ok && step < mine) {
+        ok = wait(bars.p_full[m][step % 2], step / 2 & 1, 613);
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_ts(tmem + 256 + 128 * m, tmem + 128 * m + h * kHalf + 8 * k, vb + (uint64_t)(k * 2), G::kIdescO,
-                   (step | k) ? 1u : 0u);
-          commit(smem_u32(&bars.o_done[m][h]));
-        }
-        // the scores of the step after the next go where these weights were
-        if (j + 1 < job.count[m] && have_keys(step + 2)) scores(m, step + 2);
+        for (int k = 0; k < 4; ++k)
+          mma_ts(tmem + 256 + 128 * m, tmem + 128 * m + step % 2 * kHalf + 8 * k,
+                 vb + (uint64_t)(buf * (G::kVStep >> 4) + k * 2), G::kIdescO, (step | k) ? 1u : 0u);
+        commit(smem_u32(&bars.o_done[m][step % 2]));
       }
       if (!ok) break;
-      commit(smem_u32(&bars.v_empty[step % kBufs]));
-      if (step + 2 < steps) commit(smem_u32(&bars.k_empty[(step + 2) % kBufs]));
+      commit(smem_u32(&bars.v_empty[buf]));
+      // the scores of the step after the next go where these weights were
+      if (step + 2 < steps) scores(step + 2);
     }
     // every product has completed before tensor memory is given back
     commit(smem_u32(&bars.done));
     volatile int no_abort = 0;
     wait_bounded(smem_u32(&bars.done), 0, &no_abort, err, 615);
-  } else if (warp == 9) {
+  } else if (warp == 10) {
     // ------------------------------------------------ copies: lane u takes unit u of a half tile
     const int halves = 2 * job.total;
     int issued = 0;
@@ -519,7 +512,7 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
       wait_bounded(smem_u32(&bars.raw_full[k % kRaw]), (uint32_t)(k / kRaw) & 1u, &no_abort, err, 602);
   } else {
     // ------------------------------------------------ operands from codes
-    const int d = tid - 320, w = d / 32;
+    const int d = tid - 352, w = d / 32;
     bool ok = true;
     for (int k = 0; k < 2 * job.total && ok; ++k) {
       const int st = k % kRaw, buf = k % kBufs;
@@ -544,14 +537,20 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
         const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, mt.y & 0x7FFFu);
         if (lane == 0) *reinterpret_cast<int*>(meta + 4 * kHalf * 4 + 4 * w) = (int)(most >> 10) - 14;
       }
-      // keys: a word is eight channels of a token, one 16-byte chunk of its row
-#pragma unroll 4
-      for (int i = d; i < kHalf * (D / 8); i += kDqThreads) {
-        const int tok = i / (D / 8), c = i % (D / 8);
-        const uint32_t x = *reinterpret_cast<const uint32_t*>(raw + (tok / 16) * G::kUnitStride + (tok % 16) * (D / 2) + 4 * c);
-        const uint32_t y = x >> 8;
-        sts128(sm + G::kK + buf * G::kKStep + (c / 8) * (kHalf * 128) + tok * 128 + ((c % 8) ^ (tok % 8)) * 16, x & 0x000F000Fu,
-               x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u);
+      // keys: a word is eight channels of a token, one 16-byte chunk of its row.  A thread has one chunk of every
+      // kPass-th token, so that all its addresses are two bases and constants.
+      {
+        constexpr int kChunks = D / 8, kPass = kDqThreads / kChunks;
+        const int c = d % kChunks, tok = d / kChunks;
+        const uint8_t* src = raw + tok * (D / 2) + 4 * c;
+        const uint32_t dst = sm + G::kK + buf * G::kKStep + (c / 8) * (kHalf * 128) + tok * 128 + ((c % 8) ^ (tok % 8)) * 16;
+#pragma unroll
+        for (int i = 0; i < kHalf / kPass; ++i) {
+          const int t = i * kPass;  // a multiple of 8
+          const uint32_t x = *reinterpret_cast<const uint32_t*>(src + (t / 16) * G::kUnitStride + (t % 16) * (D / 2));
+          const uint32_t y = x >> 8;
+          sts128(dst + t * 128, x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u);
+        }
       }
       fence_async();
       mbar_arrive(smem_u32(&bars.k_full[buf]));
@@ -579,16 +578,22 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
             x[t][0] = *reinterpret_cast<const uint32_t*>(at);
           }
         }
+        // channel g D / 8 + 4 (q0 + q) + e: rows of 128 bytes, their chunks swizzled by the channel's last three bits
+        const uint32_t dst = sm + G::kV + buf * G::kVStep + (g * (D / 8) + 4 * q0) * 128 + tc * 16;
+        const uint32_t swap = kEach == 1 ? 64u * (uint32_t)(q0 % 2) : 0u;
 #pragma unroll
-        for (int q = 0; q < kEach; ++q)
+        for (int q = 0; q < kEach; ++q) {
+          uint32_t y[4];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) y[t] = x[t][q] >> 8;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int ch = g * (D / 8) + 4 * (q0 + q) + e;
             const uint32_t mask = e % 2 ? 0x00F000F0u : 0x000F000Fu;
-            const int sh = e / 2 * 8;
-            sts128(sm + G::kV + buf * G::kVStep + ch * 128 + (tc ^ (ch % 8)) * 16, x[0][q] >> sh & mask,
-                   x[1][q] >> sh & mask, x[2][q] >> sh & mask, x[3][q] >> sh & mask);
+            const bool v = e / 2 != 0;
+            sts128((dst ^ (uint32_t)((4 * q + e) % 8 * 16) ^ swap) + (4 * q + e) * 128, (v ? y[0] : x[0][q]) & mask,
+                   (v ? y[1] : x[1][q]) & mask, (v ? y[2] : x[2][q]) & mask, (v ? y[3] : x[3][q]) & mask);
           }
+        }
       }
       fence_async();
       mbar_arrive(smem_u32(&bars.v_full[buf]));

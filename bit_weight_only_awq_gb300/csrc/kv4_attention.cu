@@ -778,8 +778,10 @@ cudaError_t launch(const Kv4AttnArgs& args, void* ws, int* err, cudaStream_t s) 
 
 // From this many query rows of a cache head on, the tcgen05 kernel takes the call.
 constexpr int64_t kPrefillRows = 64;
+constexpr int64_t kPrefillMaxRows = 1 << 20;  // its grid's second dimension: 4096 row blocks, 16 shares of the cache at most
 bool many(int64_t T, int max_q, int heads, int kv_heads) {
-  return (max_q < T ? max_q : T) * (heads / kv_heads) >= kPrefillRows;
+  const int64_t rows = (max_q < T ? max_q : T) * (heads / kv_heads);
+  return rows >= kPrefillRows && rows <= kPrefillMaxRows;
 }
 
 // Counters, a partial for each warp, and two for each CTA; or the other kernel's partials after the counters.

@@ -182,10 +182,11 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
   __shared__ int abort_word;
   volatile int* abort_flag = &abort_word;
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid / 32, 0), lane = tid % 32;
-  const int split = blockIdx.x % splits;
-  // the blocks that see the most tokens first
-  const int row_block = (int)(gridDim.x / splits) - 1 - blockIdx.x / splits;
-  const Job job = job_of(a, row_block, blockIdx.y, blockIdx.z, split, splits);
+  // heads of a row block first, then the row blocks from the one that sees the most tokens down: CTAs start in the
+  // order of their work, and the short ones fill what the long ones leave
+  const int split = blockIdx.y % splits, row_blocks = gridDim.y / splits;
+  const int row_block = row_blocks - 1 - blockIdx.y / splits;
+  const Job job = job_of(a, row_block, blockIdx.x, blockIdx.z, split, splits);
   if (job.row0 >= job.n * a.per) return;
   uint8_t* smem = align_smem_1024(smem_raw);
   const uint32_t sm = smem_u32(smem);
@@ -313,12 +314,17 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
             t[q] = F2(at > pos || at < from ? -INFINITY : v.x, at + 1 > pos || at + 1 < from ? -INFINITY : v.y);
           }
         }
-        float high = top;
+        float highs[8] = {top, top, top, top, top, top, top, top};
 #pragma unroll
         for (int q = 0; q < 32; ++q) {
           const float2 v = t[q].get();
-          high = fmaxf(high, fmaxf(v.x, v.y));
+          highs[q % 8] = fmaxf(highs[q % 8], fmaxf(v.x, v.y));
         }
+#pragma unroll
+        for (int q = 4; q; q /= 2)
+#pragma unroll
+          for (int k = 0; k < q; ++k) highs[k] = fmaxf(highs[k], highs[k + q]);
+        const float high = highs[0];
         const int ve = max(vexp, max(ve2.x, ve2.y));
         const bool grown = ve != vexp || (high > top && !((high - top) * qk <= kGrow));
         if (__any_sync(0xFFFFFFFFu, grown)) {
@@ -396,7 +402,7 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
     const float unit = __uint_as_float((uint32_t)(127 + vexp - 5) << 23);
     const int64_t row = token * a.heads + head;
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    float* part = parts + ((((long long)blockIdx.z * a.kv_heads + blockIdx.y) * (gridDim.x / splits) + row_block) * splits + split) * part_floats(D);
+    float* part = parts + ((((long long)blockIdx.z * a.kv_heads + blockIdx.x) * row_blocks + row_block) * splits + split) * part_floats(D);
     const int pr = 128 * m + r;
     if (ok) {
 #pragma unroll 1
@@ -564,7 +570,8 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
       {
         constexpr int kQuads = D / 32;               // quads of a group of D / 8 channels
         constexpr int kEach = kQuads / 2;            // of a thread
-        const int tc = lane % 8, s = tc % 2, g = 4 * (w % 2) + lane / 8, q0 = (w / 2) * kEach;
+        const int tc = lane % 8, s = tc % 2, g = 4 * (w % 2) + lane / 8;
+        const int q0 = ((w / 2) ^ (kEach == 2 ? g % 2 : 0)) * kEach;  // two groups of a half-warp: different banks
         const uint8_t* src = raw + (tc / 2) * G::kUnitStride + 8 * D + ((s * 8 + g) * 4 * kQuads + q0) * 4;
         uint32_t x[4][kEach];
 #pragma unroll
@@ -652,6 +659,7 @@ Plan plan_of(int64_t T, int64_t B, int max_q, int heads, int kv_heads) {
   const int64_t ctas = (blocks * B < T * per / kRows + B ? blocks * B : T * per / kRows + B) * kv_heads;
   int64_t splits = 2 * ctas > sms ? 1 : sms / ctas;
   if (splits * blocks * B * kv_heads > 4 * sms) splits = 4 * sms / (blocks * B * kv_heads);
+  if (splits > 16) splits = 16;
   return {(int)blocks, (int)(splits < 1 ? 1 : splits)};
 }
 
@@ -662,7 +670,7 @@ cudaError_t launch(const Kv4AttnArgs& args, float* parts, int* err, cudaStream_t
   if (e != cudaSuccess) return e;
   const Plan p = plan_of(args.T, args.B, args.max_q, args.heads, args.kv_heads);
   const Args a = make_args(args);
-  kv4_prefill_kernel<D, BF16><<<dim3((unsigned)(p.blocks * p.splits), (unsigned)a.kv_heads, (unsigned)a.B), kThreads,
+  kv4_prefill_kernel<D, BF16><<<dim3((unsigned)a.kv_heads, (unsigned)(p.blocks * p.splits), (unsigned)a.B), kThreads,
                                 Geo<D>::kSmem, s>>>(a, p.splits, parts, err);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.splits == 1) return e;

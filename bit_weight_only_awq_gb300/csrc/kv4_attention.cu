@@ -32,15 +32,18 @@ namespace awq {
 namespace {
 
 constexpr int kTile = 64;    // tokens of a tile: 4 units
-constexpr int kWarps = 12;   // three on each sub-partition
-constexpr int kThreads = 32 * kWarps;
 constexpr int kFewParts = 12;
 
-template <int D>
+// Eight query columns: twelve warps of 168 registers, three on each sub-partition.  Sixteen: eight warps of 255; twelve
+// spilled (16 columns of 32 x 8192 tokens: 140 us).
+constexpr int warps_of(int nt) { return nt == 1 ? 12 : 8; }
+
+template <int D, int NT>
 struct Geo {
+  static constexpr int kWarps = warps_of(NT);
   static constexpr int kUnitBytes = kv4_unit_bytes(D);
   static constexpr int kTileBytes = 4 * kUnitBytes;
-  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kStages = (D == 128 ? 2 : 4) * 12 / kWarps;
   static constexpr int kRingBytes = kWarps * kStages * kTileBytes;
   static constexpr int kSmemBytes = kRingBytes + 128;
 };
@@ -72,10 +75,10 @@ __device__ __forceinline__ Seq seq_of(const Args& a, const int3 v) {
   s.groups = a.kv_heads * s.blocks;
   return s;
 }
-// The first kThreads sequences are kept in shared memory.
+// The first sequences, one for each thread, are kept in shared memory.
 template <int NT>
 __device__ __forceinline__ Seq seq_of(const Args& a, const int3* kept, int b) {
-  return seq_of<NT>(a, b < kThreads ? kept[b] : read_seq(a, b));
+  return seq_of<NT>(a, b < 32 * warps_of(NT) ? kept[b] : read_seq(a, b));
 }
 
 // A position in the order of all tiles.
@@ -217,10 +220,11 @@ __device__ __forceinline__ int part_of(long long tile, long long total, long lon
 }
 
 template <int D, bool BF16, int NT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(32 * warps_of(NT), 1)
 kv4_attention_kernel(const Args a, float* warp_parts, float* cta_parts, int* counters,
                      int* err) {
-  using G = Geo<D>;
+  using G = Geo<D, NT>;
+  constexpr int kWarps = G::kWarps, kThreads = 32 * kWarps;
   constexpr int kWords = D / 32;     // words of a lane for a token's keys, or for a token pair's values
   constexpr int kCols = 8 * NT;
   constexpr int kPart = part_floats(D, kCols);
@@ -234,7 +238,8 @@ kv4_attention_kernel(const Args a, float* warp_parts, float* cta_parts, int* cou
   __shared__ int abort_word;
   volatile int* abort_flag = &abort_word;
 
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
+  // the shuffle tells the compiler that a warp's number is the same in all its lanes
+  const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid / 32, 0), lane = tid % 32, g = lane / 4, t = lane % 4;
   uint8_t* ring = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u) + warp * G::kStages * G::kTileBytes;
   if (lane < G::kStages) mbar_init(smem_u32(&bars[warp * G::kStages + lane]), 1);
   if (lane < 2) desc[2 * warp + lane].part = nullptr;
@@ -728,11 +733,15 @@ kv4_attention_kernel(const Args a, float* warp_parts, float* cta_parts, int* cou
     const int first = arrived[i].x, n = arrived[i].y;
     if (n <= kFewParts) continue;
     const int p0 = n * warp / kWarps, p1 = n * (warp + 1) / kWarps;
-    for (int col = lane / kLanes; col < kCols; col += kAtOnce) {
-      Joined j;
-      for (int p = p0; p < p1; p += 4)
-        join_parts<D, kCols, 4, true>(j, p1 - p, col, c4, [&](int q) { return slot(first + p + q, p + q + 1 < n); });
-      store_part<D, kCols>(reinterpret_cast<float*>(ring), col, c4, j);
+    for (int col = lane / kLanes; col < kCols; col += 4 * kAtOnce) {  // the reads of four columns in flight
+      Joined j[4];
+      for (int p = p0; p < p1; p += 2)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          join_parts<D, kCols, 2, true>(j[x], p1 - p, col + x * kAtOnce, c4,
+                                        [&](int q) { return slot(first + p + q, p + q + 1 < n); });
+#pragma unroll
+      for (int x = 0; x < 4; ++x) store_part<D, kCols>(reinterpret_cast<float*>(ring), col + x * kAtOnce, c4, j[x]);
     }
     __syncthreads();
     for (int col = warp * kAtOnce + lane / kLanes; col < kCols; col += kWarps * kAtOnce) {
@@ -752,20 +761,20 @@ bool narrow(int max_q, int heads, int kv_heads) { return (int64_t)max_q * (heads
 template <int D, bool BF16, int NT>
 cudaError_t launch(const Kv4AttnArgs& args, void* ws, int* err, cudaStream_t s) {
   const void* fn = reinterpret_cast<const void*>(kv4_attention_kernel<D, BF16, NT>);
-  cudaError_t e = set_smem_once(fn, Geo<D>::kSmemBytes);
+  cudaError_t e = set_smem_once(fn, Geo<D, NT>::kSmemBytes);
   if (e != cudaSuccess) return e;
   const int ctas = device_sm_count();
   const Args a = make_args(args);
   uint8_t* base = static_cast<uint8_t*>(ws);
   float* warp_parts = reinterpret_cast<float*>(base + kCounterBytes);
-  float* cta_parts = warp_parts + (size_t)ctas * kWarps * part_floats(D, 8 * NT);
+  float* cta_parts = warp_parts + (size_t)ctas * warps_of(NT) * part_floats(D, 8 * NT);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Geo<D>::kSmemBytes;
+  cfg.blockDim = dim3(32 * warps_of(NT));
+  cfg.dynamicSmemBytes = Geo<D, NT>::kSmemBytes;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -776,23 +785,25 @@ cudaError_t launch(const Kv4AttnArgs& args, void* ws, int* err, cudaStream_t s) 
 
 }  // namespace
 
-// From this many query rows of a cache head on, the tcgen05 kernel takes the call.
-constexpr int64_t kPrefillRows = 64;
-constexpr int64_t kPrefillMaxRows = 1 << 20;  // its grid's second dimension: 4096 row blocks, 16 shares of the cache at most
-bool many(int64_t T, int max_q, int heads, int kv_heads) {
+// From which number of query rows of a cache head on the tcgen05 kernel takes the call: it makes operands of a tile
+// once for 256 rows, where this one goes over the cache again for every 16.  us at 8 x 8192 tokens, 8 cache heads of 128
+// channels, here / there: 16 rows 34 / 81, 32 rows 52 / 82, 64 rows 90 / 83; at 16 x 4096, 64 channels: 32 rows 37 / 71,
+// 64 rows 61 / 71.
+constexpr int64_t kPrefillMaxRows = 1 << 20;  // its grid's second dimension: 4096 row blocks, 16 shares of the cache
+bool many(int64_t T, int max_q, int heads, int kv_heads, int dim) {
   const int64_t rows = (max_q < T ? max_q : T) * (heads / kv_heads);
-  return rows >= kPrefillRows && rows <= kPrefillMaxRows;
+  return rows > (dim == 128 ? 48 : 64) && rows <= kPrefillMaxRows;
 }
 
 // Counters, a partial for each warp, and two for each CTA; or the other kernel's partials after the counters.
 size_t kv4_attention_workspace(int64_t T, int64_t B, int max_q, int heads, int kv_heads, int dim) {
-  if (many(T, max_q, heads, kv_heads)) return kCounterBytes + align256(kv4_prefill_workspace(T, B, max_q, heads, kv_heads, dim));
-  const size_t part = sizeof(float) * part_floats(dim, narrow(max_q, heads, kv_heads) ? 8 : 16);
-  return kCounterBytes + align256((size_t)device_sm_count() * (kWarps + 2) * part);
+  if (many(T, max_q, heads, kv_heads, dim)) return kCounterBytes + align256(kv4_prefill_workspace(T, B, max_q, heads, kv_heads, dim));
+  const int nt = narrow(max_q, heads, kv_heads) ? 1 : 2;
+  return kCounterBytes + align256((size_t)device_sm_count() * (warps_of(nt) + 2) * sizeof(float) * part_floats(dim, 8 * nt));
 }
 
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, int dim, bool bf16, void* ws, int* err, cudaStream_t s) {
-  if (many(a.T, a.max_q, a.heads, a.kv_heads))
+  if (many(a.T, a.max_q, a.heads, a.kv_heads, dim))
     return launch_kv4_prefill(a, dim, bf16, static_cast<uint8_t*>(ws) + kCounterBytes, err, s);
   if (narrow(a.max_q, a.heads, a.kv_heads)) {
     if (dim == 128) return bf16 ? launch<128, true, 1>(a, ws, err, s) : launch<128, false, 1>(a, ws, err, s);

@@ -4,8 +4,11 @@
 //
 // with keys zk + u sk and values zv + u sv for each token and head (unit layout: include/awq.h), so that
 //
-//   S_j = scale (sk_j (q . u_j) + zk_j sum(q)),   sum_j p_j v_j = sum_j (p_j sv_j) u_j + sum_j p_j zv_j
+//   S_j = scale (sk_j (q . u_j) + zk_j sum(q)),
+//   sum_j p_j v_j = sum_j w_j u_j - 8 sum_j w_j + sum_j p_j (zv_j + 8 sv_j),  w_j = p_j sv_j rounded to fp16
 //
+// The middle term takes the rounding of w in with its code's distance from the middle, 8, not from 0: a third of
+// the error.
 // and only the products with the codes u need the tensor cores (mma.sync m16n8k16, fp32 sums).  A code in the low
 // bits of an fp16 half is the subnormal u 2^-24, exactly: one AND makes the operand register (two codes), with no
 // offset to subtract afterwards.  Every other register holds 16 u 2^-24 (the next nibble): for keys, the matching
@@ -537,6 +540,7 @@ kv4_attention_kernel(const Args a, float* warp_parts, float* cta_parts, int* cou
 
       // ---- probabilities, and their products with the values' scales as the B operand [token][column]
       const float vup = __uint_as_float((uint32_t)(127 + 13 - vexp) << 23);
+      const float middle = __uint_as_float((uint32_t)(127 + vexp - 13) << 23) * -8.f;
       float base[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -549,7 +553,7 @@ kv4_attention_kernel(const Args a, float* warp_parts, float* cta_parts, int* cou
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             const float2 val = unpack2<false>(meta[u][r].y);
-            const float w = val.x * vup;
+            const float w = val.x * vup, zero = fmaf(8.f, val.x, val.y);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               float p[2];
@@ -559,10 +563,14 @@ kv4_attention_kernel(const Args a, float* warp_parts, float* cta_parts, int* cou
                 // a token hidden from one column and seen by another may hold a NaN
                 const bool hidden = decltype(hides)::value && v == -INFINITY;
                 l[n][c] += e;
-                z[n][c] = fmaf(e, hidden ? 0.f : val.y, z[n][c]);
+                z[n][c] = fmaf(e, hidden ? 0.f : zero, z[n][c]);
                 p[c] = e * (hidden ? 0.f : w);
               }
-              pf[n][u][r] = transpose8x8(pack2<false>(p[0], p[1]));
+              const uint32_t rounded = pack2<false>(p[0], p[1]);
+              const float2 back8 = unpack2<false>(rounded);
+              z[n][0] = fmaf(back8.x, middle, z[n][0]);
+              z[n][1] = fmaf(back8.y, middle, z[n][1]);
+              pf[n][u][r] = transpose8x8(rounded);
             }
           }
       };

@@ -1,7 +1,8 @@
 // Attention of many new tokens over the 4-bit paged cache on the 5th-generation tensor cores.
 //
 // The mathematics is kv4_attention.cu's: with keys zk + u sk and values zv + u sv,
-//   T_j = sk_j (q' . u_j) + zk_j r,  p_j = 2^(qk T_j - base),  out = (sum_j (p_j sv_j) u_j + sum_j p_j zv_j) / sum_j p_j
+//   T_j = sk_j (q' . u_j) + zk_j r,  p_j = 2^(qk T_j - base),
+//   out = (sum_j (p_j sv_j) (u_j - 8) + sum_j p_j (zv_j + 8 sv_j)) / sum_j p_j
 // where q' is the query row times a power of two, exact in fp16, and qk, r carry that factor, the scale and sum(q).
 // Only codes and exact fp16 queries enter the score's products, so the scores are as exact as fp32 sums are; the
 // weights p sv are rounded to fp16 once.
@@ -10,8 +11,9 @@
 // tiles of 128 tokens.  tcgen05.mma kind::f16, M = 128:
 //   S[row][token] = Q' U_k^T   A = queries, B = key codes, both K-major in shared memory, N = 64
 //   O[row][channel] += W U_v   A = weights, in tensor memory where S was, B = value codes, K-major, N = D
-// The codes become fp16 halves with one AND for two of them: u 2^-24 in the lowest nibble, 16 u 2^-24 in the next.
-// The factor 16 is taken out of the queries (channels 2, 3 of four) and of the output (odd channels).
+// A key's codes become fp16 halves with one AND for two of them: u 2^-24 in the lowest nibble, 16 u 2^-24 in the next
+// (the factor 16 is taken out of the queries' channels 2, 3 of four).  A value's become u - 8, with one operation more,
+// so that the rounding of the weights counts by the code's distance from the middle: a third of the error.
 //
 // Roles: warps 0-3 and 4-7 are the softmax of the two row tiles (a thread has a row), warps 8 and 9 issue their
 // products, warp 10 copies units, warps 11-14 turn codes into operands.  While one row tile's softmax runs, the other's products
@@ -101,6 +103,15 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Two codes of a word as exact halves u - 8: nibbles 0 and 4 (odd = 0), or 1 and 5.
+__device__ __forceinline__ uint32_t centred(int odd, uint32_t w) {
+  // 1024 + u, or 1024 + 16 u
+  const uint32_t b = (w & (odd ? 0x00F000F0u : 0x000F000Fu)) | 0x64006400u;
+  const __half2 h = *reinterpret_cast<const __half2*>(&b);
+  const __half2 r = odd ? __hfma2(h, __float2half2_rn(0.0625f), __float2half2_rn(-72.f)) : __hsub2(h, __float2half2_rn(1032.f));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 
 // Two fp32 values in one register pair, one instruction for both.
 struct F2 {
@@ -416,7 +427,7 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
         }
         float v[16];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] = fmaf(__uint_as_float(o[k]), k % 2 ? 1048576.f : 16777216.f, z);
+        for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(o[k]) + z;
         if (splits == 1) {
           if (in) {
             uint32_t w[8];
@@ -538,7 +549,7 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
         f[0] = ksz.x;
         f[kHalf] = ksz.y;
         f[2 * kHalf] = vsz.x;
-        f[3 * kHalf] = vsz.y;
+        f[3 * kHalf] = fmaf(8.f, vsz.x, vsz.y);
         // the value scales of these 32 tokens are below 2^(that)
         const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, mt.y & 0x7FFFu);
         if (lane == 0) *reinterpret_cast<int*>(meta + 4 * kHalf * 4 + 4 * w) = (int)(most >> 10) - 14;
@@ -595,10 +606,9 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
           for (int t = 0; t < 4; ++t) y[t] = x[t][q] >> 8;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint32_t mask = e % 2 ? 0x00F000F0u : 0x000F000Fu;
             const bool v = e / 2 != 0;
-            sts128((dst ^ (uint32_t)((4 * q + e) % 8 * 16) ^ swap) + (4 * q + e) * 128, (v ? y[0] : x[0][q]) & mask,
-                   (v ? y[1] : x[1][q]) & mask, (v ? y[2] : x[2][q]) & mask, (v ? y[3] : x[3][q]) & mask);
+            sts128((dst ^ (uint32_t)((4 * q + e) % 8 * 16) ^ swap) + (4 * q + e) * 128, centred(e % 2, v ? y[0] : x[0][q]),
+                   centred(e % 2, v ? y[1] : x[1][q]), centred(e % 2, v ? y[2] : x[2][q]), centred(e % 2, v ? y[3] : x[3][q]));
           }
         }
       }

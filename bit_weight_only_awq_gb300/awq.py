@@ -10,6 +10,7 @@ there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -386,12 +387,16 @@ def w4a8_linear_grouped(x, wq, s3, s2, split_k: int = 0, out=None, acc_out=None,
 _DTYPES = {torch.float16: FP16, torch.bfloat16: BF16}
 
 
-def _dtype16(name: str, *tensors) -> int:
-    """The awq_dtype shared by all given tensors."""
-    dtype = tensors[0].dtype
-    if dtype not in _DTYPES or any(t is not None and t.dtype != dtype for t in tensors):
-        raise TypeError(f"{name} takes fp16 or bf16 operands of one type")
-    return _DTYPES[dtype]
+def _dtype16(name: str, first, *others) -> int:
+    """The awq_dtype that all given tensors share; they are on a GPU."""
+    dtype = first.dtype
+    kind = _DTYPES.get(dtype)
+    if kind is None or not first.is_cuda:
+        raise TypeError(f"{name} takes fp16 or bf16 operands of one type on a GPU")
+    for t in others:
+        if t is not None and (t.dtype is not dtype or not t.is_cuda):
+            raise TypeError(f"{name} takes fp16 or bf16 operands of one type on a GPU")
+    return kind
 
 
 def _raw_stream(stream, device: torch.device) -> int:
@@ -401,30 +406,33 @@ def _raw_stream(stream, device: torch.device) -> int:
 
 def _need(name: str, dtype, *tensors) -> None:
     for t in tensors:
-        if t is not None and (t.dtype != dtype or not t.is_contiguous()):
-            raise TypeError(f"{name}: expected a contiguous {dtype} tensor")
+        if t is not None and (t.dtype is not dtype or not t.is_cuda or not t.is_contiguous()):
+            raise TypeError(f"{name}: expected a contiguous {dtype} tensor on a GPU")
 
 
-def _row_stride(name: str, t) -> int:
-    """Elements from one row (token) to the next; inside a row everything is dense."""
-    inner = 1
+def _row_stride(name: str, t, inner: int) -> int:
+    """Elements from one row (token) to the next; the `inner` elements of a row are dense."""
+    if t.is_contiguous():
+        return inner
+    dense = 1
     for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if size != 1 and stride != inner:
+        if size != 1 and stride != dense:
             raise ValueError(f"{name}: heads and channels of a token must be dense")
-        inner *= size
+        dense *= size
     return max(t.stride(0), inner) if t.shape[0] <= 1 else t.stride(0)
 
 
 def _rmsnorm_args(name, x, weight, residual, res_out):
     M, K = x.shape
     dtype = _dtype16(name, x, weight, residual, res_out)
-    if weight.shape != (K,) or (residual is not None and residual.shape != x.shape):
-        raise ValueError(f"{name}: weight [K] and residual [M, K] go with x [M, K]")
+    if weight.shape != (K,) or (residual is not None and residual.shape != x.shape) or \
+            (res_out is not None and res_out.shape != x.shape):
+        raise ValueError(f"{name}: weight [K], residual and res_out [M, K] go with x [M, K]")
     if residual is not None and res_out is None:
         res_out = torch.empty((M, K), dtype=x.dtype, device=x.device)
     _need(name, x.dtype, weight, res_out)
-    rs = 0 if residual is None else _row_stride(name, residual)
-    return M, K, dtype, res_out, _row_stride(name, x), rs
+    rs = 0 if residual is None else _row_stride(name, residual, K)
+    return M, K, dtype, res_out, _row_stride(name, x, K), rs
 
 
 def w4a8_rmsnorm_quant(x, weight, residual=None, eps: float = 1e-6, res_out=None, y=None, xq=None, s_tok=None,
@@ -437,6 +445,11 @@ def w4a8_rmsnorm_quant(x, weight, residual=None, eps: float = 1e-6, res_out=None
         xq = torch.empty((M, K), dtype=torch.int8, device=x.device)
     if s_tok is None:
         s_tok = torch.empty((M,), dtype=torch.float32, device=x.device)
+    _need("w4a8_rmsnorm_quant", torch.int8, xq)
+    _need("w4a8_rmsnorm_quant", torch.float32, s_tok)
+    _need("w4a8_rmsnorm_quant", x.dtype, y)
+    if xq.shape != (M, K) or s_tok.shape != (M,) or (y is not None and y.shape != (M, K)):
+        raise ValueError("w4a8_rmsnorm_quant: xq and y are [M, K], s_tok is [M]")
     _check("w4a8_rmsnorm_quant", lib.w4a8_rmsnorm_quant(_ptr(x), _ptr(residual), _ptr(weight), _ptr(res_out), _ptr(y),
                                                         _ptr(xq), _ptr(s_tok), M, K, xs, rs, eps, dtype,
                                                         _raw_stream(stream, x.device)))
@@ -448,6 +461,10 @@ def awq_rmsnorm(x, weight, residual=None, eps: float = 1e-6, res_out=None, out=N
     M, K, dtype, res_out, xs, rs = _rmsnorm_args("awq_rmsnorm", x, weight, residual, res_out)
     if out is None:
         out = torch.empty((M, K), dtype=x.dtype, device=x.device)
+    else:
+        _need("awq_rmsnorm", x.dtype, out)
+        if out.shape != (M, K):
+            raise ValueError("awq_rmsnorm: out is [M, K]")
     _check("awq_rmsnorm", lib.awq_rmsnorm(_ptr(x), _ptr(residual), _ptr(weight), _ptr(res_out), _ptr(out), M, K, xs,
                                           rs, eps, dtype, _raw_stream(stream, x.device)))
     return out, res_out
@@ -467,9 +484,10 @@ def kv4_cache(num_pages: int, kv_heads: int, head_dim: int, page_size: int = 64,
 
 def _kv4_shape(name, cache):
     """(num_pages, kv_heads, head_dim, page_size) of a cache tensor."""
-    if cache.dtype != torch.uint8 or cache.dim() != 4 or not cache.is_contiguous():
-        raise TypeError(f"{name}: the cache is a contiguous uint8 tensor [pages, kv_heads, page_size / 16, unit]")
-    pages, kv_heads, units, unit = cache.shape
+    shape = cache.shape
+    if cache.dtype is not torch.uint8 or len(shape) != 4 or not cache.is_cuda or not cache.is_contiguous():
+        raise TypeError(f"{name}: the cache is a contiguous uint8 tensor [pages, kv_heads, page_size / 16, unit] on a GPU")
+    pages, kv_heads, units, unit = shape
     return pages, kv_heads, (unit - 128) // KV4_UNIT if unit % KV4_UNIT == 0 else 0, units * KV4_UNIT
 
 
@@ -491,7 +509,8 @@ def kv4_append(cache, k, v, positions, slots, table, q=None, interleaved: bool =
             q_out = torch.empty((T, heads, dim), dtype=q.dtype, device=q.device)
         elif q_out.shape != q.shape:
             raise ValueError("kv4_append: q_out has another shape than q")
-        qs, qos = _row_stride("kv4_append", q), _row_stride("kv4_append", q_out)
+        inner = heads * dim
+        qs, qos = _row_stride("kv4_append", q, inner), _row_stride("kv4_append", q_out, inner)
     if table is not None:
         max_pos, rot = table.shape
         _need("kv4_append", torch.float32, table)
@@ -499,7 +518,8 @@ def kv4_append(cache, k, v, positions, slots, table, q=None, interleaved: bool =
         if positions.shape != (T,):
             raise ValueError("kv4_append: positions is [T]")
     _check("kv4_append", lib.kv4_append(
-        _ptr(q), _ptr(k), _ptr(v), qs, _row_stride("kv4_append", k), _row_stride("kv4_append", v), _ptr(positions),
+        _ptr(q), _ptr(k), _ptr(v), qs, _row_stride("kv4_append", k, kv_heads * dim),
+        _row_stride("kv4_append", v, kv_heads * dim), _ptr(positions),
         _ptr(slots), _ptr(table), max_pos, rot, int(interleaved), _ptr(q_out), qos, _ptr(cache), pages, T, heads,
         kv_heads, dim, page, dtype, _raw_stream(stream, cache.device)))
     return q_out
@@ -523,27 +543,23 @@ def kv4_gather(cache, slots, dtype=torch.float16, k=None, v=None, stream=None):
     return k, v
 
 
-# Workspaces of kv4_attention by device, stream (calls on one stream may share one) and the sizes that they go by.
+@functools.lru_cache(maxsize=4096)
+def kv4_attention_workspace_bytes(T: int, B: int, max_q: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib.kv4_attention_workspace_bytes(T, B, max_q, heads, kv_heads, head_dim))
+
+
+# One workspace of kv4_attention for each device and stream (calls on one stream may share it), grown on demand.
 _kv4_workspaces: dict[tuple, torch.Tensor] = {}
 
 
-def _kv4_workspace(handle: int, device: torch.device, sizes: tuple, stream) -> torch.Tensor:
-    key = (device.index, handle, *sizes)
+def _kv4_workspace(handle: int, device: torch.device, nbytes: int, stream) -> torch.Tensor:
+    key = (device.index, handle)
     ws = _kv4_workspaces.get(key)
-    if ws is None:
-        nbytes = kv4_attention_workspace_bytes(*sizes)
-        same = (device.index, handle)
-        ws = _kv4_workspaces.get(same)
-        if ws is None or ws.numel() < nbytes:
-            with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
-                # zeroed, and later freed, in the order of its own stream
-                ws = _kv4_workspaces[same] = torch.zeros(nbytes, dtype=torch.uint8, device=device)
-        _kv4_workspaces[key] = ws
+    if ws is None or ws.numel() < nbytes:
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
+            # zeroed, and the old one freed, in the order of its own stream
+            ws = _kv4_workspaces[key] = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
     return ws
-
-
-def kv4_attention_workspace_bytes(T: int, B: int, max_q: int, heads: int, kv_heads: int, head_dim: int) -> int:
-    return int(lib.kv4_attention_workspace_bytes(T, B, max_q, heads, kv_heads, head_dim))
 
 
 def kv4_attention(q, cache, block_table, kv_len, q_start=None, max_q: int = 1, scale: float | None = None,
@@ -554,19 +570,24 @@ def kv4_attention(q, cache, block_table, kv_len, q_start=None, max_q: int = 1, s
     has one query (T = B); with q_start int32 [B + 1] sequence b has the queries q_start[b] .. q_start[b + 1] - 1,
     at most max_q, which are its last tokens.  scale: 1 / sqrt(D) by default; window: 0 or the number of keys a
     query looks back over, its own included.  `lse` fp32 [T, heads], when given, receives the log-sum-exp.
+    Without `workspace` the calls of a stream share one that grows; a call to be captured in a graph takes one of
+    its own (kv4_attention_workspace_bytes, zeroed once).
     """
     pages, kv_heads, dim, page = _kv4_shape("kv4_attention", cache)
-    T, heads, qd = q.shape
+    shape = q.shape
+    T, heads, qd = shape
     B, max_pages = block_table.shape
     dtype = _dtype16("kv4_attention", q, out)
     if qd != dim or kv_len.shape != (B,) or (q_start is not None and q_start.shape != (B + 1,)):
-        raise ValueError("kv4_attention: q [T, heads, head_dim], kv_len [B] and q_start [B + 1] go with the cache and block_table [B, pages]")
+        raise ValueError("kv4_attention: q [T, heads, head_dim], kv_len [B] and q_start [B + 1] go with the cache and "
+                         "block_table [B, pages]")
     _need("kv4_attention", torch.int32, kv_len, q_start)
-    if block_table.dtype != torch.int32 or (max_pages > 1 and block_table.stride(1) != 1):
-        raise TypeError("kv4_attention: block_table is int32 with dense rows")
+    table_stride, inner = block_table.stride()
+    if block_table.dtype is not torch.int32 or not block_table.is_cuda or (inner != 1 and max_pages > 1):
+        raise TypeError("kv4_attention: block_table is int32 with dense rows, on a GPU")
     if out is None:
-        out = torch.empty((T, heads, dim), dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape or not out.is_contiguous():
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+    elif out.shape != shape or not out.is_contiguous():
         raise ValueError("kv4_attention: out is dense and has q's shape")
     if lse is not None:
         _need("kv4_attention", torch.float32, lse)
@@ -576,14 +597,13 @@ def kv4_attention(q, cache, block_table, kv_len, q_start=None, max_q: int = 1, s
         scale = dim ** -0.5
     device = q.device
     handle = _raw_stream(stream, device)
-    ws = workspace
-    if ws is None:
-        ws = _kv4_workspace(handle, device, (T, B, max_q, heads, kv_heads, dim), stream)
-    nbytes = ws.numel() * ws.element_size()
+    if workspace is None:
+        workspace = _kv4_workspace(handle, device, kv4_attention_workspace_bytes(T, B, max_q, heads, kv_heads, dim), stream)
     _check("kv4_attention", lib.kv4_attention(
-        _ptr(q), _row_stride("kv4_attention", q), _ptr(cache), _ptr(block_table),
-        max(block_table.stride(0), max_pages), _ptr(kv_len), _ptr(q_start), _ptr(out), _ptr(lse), T, B, max_q, heads,
-        kv_heads, dim, pages, page, max_pages, scale, window, dtype, _ptr(ws), nbytes, handle))
+        q.data_ptr(), _row_stride("kv4_attention", q, heads * dim), cache.data_ptr(), block_table.data_ptr(),
+        table_stride if table_stride > max_pages else max_pages, kv_len.data_ptr(), _ptr(q_start), out.data_ptr(),
+        _ptr(lse), T, B, max_q, heads, kv_heads, dim, pages, page, max_pages, scale, window, dtype,
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle))
     return out
 
 

@@ -8,13 +8,15 @@
 namespace awq {
 namespace {
 
-// Both kernels: a CTA for each token, D / 8 lanes for each of its heads, eight channels a lane: one 16-byte
-// access, one AWQ word of the keys, two halves of the values.  HBM bound where there are many tokens; what the
-// SMs have to do for each byte comes close to it (rotation and codes are about nine operations a channel, the
-// reductions over a head four shuffles each for two or four heads at once).
+// Both kernels: one or more warps for each token, D / 8 lanes for each of its heads, eight channels a lane: one 16-byte
+// access, one AWQ word of the keys, two halves of the values.  The floor is HBM's: 8165 tokens of 32 + 32 + 32 heads move
+// 305 MB in 83 us, 3.7 TB/s, and are bound by the instructions (reductions over a head by shuffles, about twenty
+// operations for a code); reading back moves 169 MB in 37 us, 4.5 TB/s.  64 tokens of 32 + 8 + 8 heads take 4 us.
 constexpr int kAThreads = 256;
 constexpr int kAWarps = kAThreads / 32;
-constexpr int kTeamWarps = 256;  // warps that each SM should get
+// Warps that each SM should get: a warp's work on a token before its first head (page, rotation) costs as much as two
+// rounds of heads.  64 / 256 / 512 at 8165 tokens: 80 / 86 / 99 us.
+constexpr int kTeamWarps = 64;
 
 template <bool BF16>
 __device__ __forceinline__ void widen8(const uint4& v, float (&x)[8]) {
@@ -31,13 +33,15 @@ __device__ __forceinline__ uint4 narrow8(const float (&f)[8]) {
   return make_uint4(pack2<BF16>(f[0], f[1]), pack2<BF16>(f[2], f[3]), pack2<BF16>(f[4], f[5]), pack2<BF16>(f[6], f[7]));
 }
 
-// The rotation of a lane's eight channels, the same for every head of a token.  Every product and sum is rounded
-// by itself (no fused multiply-add), so the codes made from the result are a function of the inputs alone.
+// The rotation of a lane's eight channels, the same for every head of a token: x c + partner s, with the sine's sign
+// that of the channel's half (a c + b (-s) rounds as a c - b s).  Every product and sum is rounded by itself, so the codes
+// made from the result are a function of the inputs alone (mul.rn.f32x2 with add.rn.f32x2 would not do: the pair was
+// seen to come out as one fused operation).
 template <int LANES>
 struct Turn {
-  float c[8], s[8];  // cosines and sines; interleaved: four of each
-  int src[2];        // pairs (i, i + rot / 2): the lane that holds the partners of each four channels
-  bool in[2], first[2];
+  float c[8], s[8];
+  int src[2];   // pairs (i, i + rot / 2): the lane that holds the partners of each four channels
+  bool in[2];   // of each four channels: whether they turn
   int rot, odd;
   bool interleaved;
 
@@ -46,72 +50,62 @@ struct Turn {
     interleaved = inter;
     const int half = rot / 2;
     odd = half / 4 % 2;
-    if (interleaved) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool on = 8 * lane < rot;
-        c[i] = on ? row[4 * lane + i] : 0.f;
-        s[i] = on ? row[half + 4 * lane + i] : 0.f;
-      }
-      return;
-    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int at = 8 * lane + 4 * h;
       in[h] = at < rot;
-      first[h] = at < half;
-      const int partner = !in[h] ? at : first[h] ? at + half : at - half;
-      src[h] = partner / 8;
-      const int i = first[h] ? at : partner;
-      const float4 cv = in[h] ? *reinterpret_cast<const float4*>(row + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-      const float4 sv = in[h] ? *reinterpret_cast<const float4*>(row + half + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-      c[4 * h] = cv.x, c[4 * h + 1] = cv.y, c[4 * h + 2] = cv.z, c[4 * h + 3] = cv.w;
-      // a first half turns by - b s, a second one by + a s
-      const float sg = first[h] ? -1.f : 1.f;  // a c + (-b s) rounds as a c - b s
-      s[4 * h] = sg * sv.x, s[4 * h + 1] = sg * sv.y, s[4 * h + 2] = sg * sv.z, s[4 * h + 3] = sg * sv.w;
+      src[h] = lane;
+      if (interleaved) {
+        const float2 cv = in[h] ? *reinterpret_cast<const float2*>(row + at / 2) : make_float2(0.f, 0.f);
+        const float2 sv = in[h] ? *reinterpret_cast<const float2*>(row + half + at / 2) : make_float2(0.f, 0.f);
+        c[4 * h] = c[4 * h + 1] = cv.x;
+        c[4 * h + 2] = c[4 * h + 3] = cv.y;
+        s[4 * h] = -sv.x, s[4 * h + 1] = sv.x, s[4 * h + 2] = -sv.y, s[4 * h + 3] = sv.y;
+      } else {
+        const bool first = at < half;
+        const int partner = !in[h] ? at : first ? at + half : at - half;
+        src[h] = partner / 8;
+        const int i = first ? at : partner;
+        const float4 cv = in[h] ? *reinterpret_cast<const float4*>(row + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 sv = in[h] ? *reinterpret_cast<const float4*>(row + half + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float sg = first ? -1.f : 1.f;
+        c[4 * h] = cv.x, c[4 * h + 1] = cv.y, c[4 * h + 2] = cv.z, c[4 * h + 3] = cv.w;
+        s[4 * h] = sg * sv.x, s[4 * h + 1] = sg * sv.y, s[4 * h + 2] = sg * sv.z, s[4 * h + 3] = sg * sv.w;
+      }
     }
   }
   // every lane of the warp takes part
   __device__ __forceinline__ void apply(float (&x)[8], int lane) const {
     if (rot == 0) return;
-    if (interleaved) {
-      if (8 * lane < rot) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = x[2 * i], b = x[2 * i + 1];
-          x[2 * i] = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, s[i]));
-          x[2 * i + 1] = __fadd_rn(__fmul_rn(b, c[i]), __fmul_rn(a, s[i]));
-        }
-      }
-      return;
-    }
     float other[8];
+    if (interleaved) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) other[j] = x[j];
-    if (odd) {  // with an odd number of fours in a half, the partners are the other four of their lane
+      for (int j = 0; j < 8; ++j) other[j] = x[j ^ 1];
+    } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) other[j] = x[j ^ 4];
+      for (int j = 0; j < 8; ++j) other[j] = x[j];
+      if (odd) {  // with an odd number of fours in a half, the partners are the other four of their lane
+#pragma unroll
+        for (int j = 0; j < 8; ++j) other[j] = x[j ^ 4];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) other[j] = __shfl_sync(0xFFFFFFFFu, other[j], src[j / 4], LANES);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) other[j] = __shfl_sync(0xFFFFFFFFu, other[j], src[j / 4], LANES);
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if (in[h]) {
-#pragma unroll
-        for (int j = 4 * h; j < 4 * h + 4; ++j) x[j] = __fadd_rn(__fmul_rn(x[j], c[j]), __fmul_rn(other[j], s[j]));
-      }
+    for (int j = 0; j < 8; ++j)
+      if (in[j / 4]) x[j] = __fadd_rn(__fmul_rn(x[j], c[j]), __fmul_rn(other[j], s[j]));
   }
 };
 
-// Minimum and maximum that keep a NaN.
-__device__ __forceinline__ float min_nan(float a, float b) {
+// Minimum and maximum of three that keep a NaN.
+__device__ __forceinline__ float min_nan(float a, float b, float c) {
   float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
@@ -120,16 +114,13 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 constexpr float kMagic = 12582912.f;
 template <int LANES>
 __device__ __forceinline__ uint32_t quantize8(const float (&x)[8], uint32_t (&u)[8]) {
-  float low = x[0], high = x[0];
-#pragma unroll
-  for (int j = 1; j < 8; ++j) {
-    low = min_nan(low, x[j]);
-    high = max_nan(high, x[j]);
-  }
+  float low = min_nan(min_nan(x[0], x[1], x[2]), min_nan(x[3], x[4], x[5]), min_nan(x[6], x[7], x[7]));
+  float high = max_nan(max_nan(x[0], x[1], x[2]), max_nan(x[3], x[4], x[5]), max_nan(x[6], x[7], x[7]));
 #pragma unroll
   for (int o = LANES / 2; o > 0; o >>= 1) {
-    low = min_nan(low, __shfl_xor_sync(0xFFFFFFFFu, low, o, LANES));
-    high = max_nan(high, __shfl_xor_sync(0xFFFFFFFFu, high, o, LANES));
+    const float l = __shfl_xor_sync(0xFFFFFFFFu, low, o, LANES), h = __shfl_xor_sync(0xFFFFFFFFu, high, o, LANES);
+    low = min_nan(low, l, l);
+    high = max_nan(high, h, h);
   }
   const __half zero = __float2half_rn(fminf(fmaxf(low, -65504.f), 65504.f));
   const __half scale = __float2half_rn(fminf(__fdiv_rn(__fsub_rn(high, low), 15.0f), 65504.f));
@@ -141,11 +132,14 @@ __device__ __forceinline__ uint32_t quantize8(const float (&x)[8], uint32_t (&u)
   // differ; there, and where the rounding of zero and scale puts a code outside 0..15, the slow way is taken.
   // Adding 1.5 * 2^23 rounds to the nearest integer, ties to even.
   float far = fmaxf(-(low - z) * inv, (high - z) * inv - 15.f);
+  const F2 minus_z(-z, -z), inv2(inv, inv), magic(kMagic, kMagic), minus(-1.f, -1.f);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float d = __fsub_rn(x[j], z), m = fmaf(d, inv, kMagic);
-    far = fmaxf(far, fabsf(fmaf(d, inv, kMagic - m)));
-    u[j] = __float_as_uint(m);
+  for (int p = 0; p < 4; ++p) {
+    const F2 d = add2(F2(x[2 * p], x[2 * p + 1]), minus_z), m = fma2(d, inv2, magic);
+    const float2 e = fma2(d, inv2, fma2(m, minus, magic)).get(), w = m.get();
+    far = fmaxf(far, fmaxf(fabsf(e.x), fabsf(e.y)));
+    u[2 * p] = __float_as_uint(w.x);
+    u[2 * p + 1] = __float_as_uint(w.y);
   }
   const bool finite = low >= -FLT_MAX && high <= FLT_MAX;
   if (!(far < 0.4999f && finite)) {
@@ -192,65 +186,78 @@ __global__ void __launch_bounds__(kAThreads, 4) kv4_append_kernel(const AppendAr
   const int team = a.team;
   const int64_t t = blockIdx.x * (int64_t)(kAWarps / team) + warp / team;
   if (t >= a.T) return;
-  // rounds of HEADS heads: queries, then keys, then values
+  // rounds of HEADS heads: queries, then keys, then values, dealt out to the token's warps in turn
   const int q_rounds = (a.heads + HEADS - 1) / HEADS, kv_rounds = (a.c.kv_heads + HEADS - 1) / HEADS;
-  const int rounds = q_rounds + 2 * kv_rounds, stride = team * gridDim.y;
-  int r = blockIdx.y * team + warp % team;
-  if (r >= rounds) return;
+  const int stride = team * gridDim.y, me = blockIdx.y * team + warp % team;
+  const int k_first = (me + stride - q_rounds % stride) % stride, v_first = (k_first + stride - kv_rounds % stride) % stride;
   const int own = sub * D + 8 * lane;  // this lane's place in a round
-  const uint16_t* q_row = a.q + t * a.q_stride + own;
-  const uint16_t* k_row = a.k + t * a.k_stride + own;
-  const uint16_t* v_row = a.v + t * a.v_stride + own;
-  auto read = [&](int i) {
-    const int kr = i - q_rounds, vr = kr - kv_rounds;
-    const uint16_t* at = kr < 0 ? q_row + i * (HEADS * D) : vr < 0 ? k_row + kr * (HEADS * D) : v_row + vr * (HEADS * D);
-    const int h = (kr < 0 ? i : vr < 0 ? kr : vr) * HEADS + sub;
-    return i < rounds && h < (kr < 0 ? a.heads : a.c.kv_heads) ? *reinterpret_cast<const uint4*>(at)
-                                                               : make_uint4(0u, 0u, 0u, 0u);
-  };
-  uint4 next = read(r);
+  const int step = stride * HEADS * D;
+
   const int64_t pos = a.rope.rot ? a.rope.positions[t] : 0;
   const bool pos_ok = !a.rope.rot || (pos >= 0 && pos < a.rope.max_pos);
   const int64_t slot = a.c.kv_heads ? a.slots[t] : -1;
+  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+  auto read = [&](const uint16_t* at, bool in) { return in ? *reinterpret_cast<const uint4*>(at) : none; };
   Turn<LANES> turn;
-  turn.load(a.rope.table + (pos_ok ? pos * a.rope.rot : 0), pos_ok ? a.rope.rot : 0, a.rope.interleaved, lane);
-  const bool keep = pos_ok && slot >= 0 && slot < a.c.num_pages * a.c.page_size;
-  int in_page;
-  const int64_t page = page_of(keep ? slot : 0, a.c.page_size, in_page);
-  const int units = a.c.page_size / kKv4Unit, token = in_page % kKv4Unit;
-  const int head_bytes = units * kv4_unit_bytes(D);
-  uint8_t* unit0 = a.cache + (page * a.c.kv_heads * units + in_page / kKv4Unit) * kv4_unit_bytes(D);
-  const int key_at = kv4_key_offset(D, token) + 4 * lane, value_at = kv4_value_offset(D, token, 8 * lane);
-  const int meta_at = kv4_meta_offset(D, token);
-  for (; r < rounds; r += stride) {
-    float x[8];
-    widen8<BF16>(next, x);
-    next = read(r + stride);
-    const int kr = r - q_rounds, vr = kr - kv_rounds;
-    if (kr < 0) {
+  {
+    const uint16_t* src = a.q + t * a.q_stride + me * (HEADS * D) + own;
+    uint16_t* dst = a.q_out + t * a.q_out_stride + me * (HEADS * D) + own;
+    int h = me * HEADS + sub;
+    uint4 next = read(src, h < a.heads);
+    turn.load(a.rope.table + (pos_ok ? pos * a.rope.rot : 0), pos_ok ? a.rope.rot : 0, a.rope.interleaved, lane);
+    for (int r = me; r < q_rounds; r += stride) {
+      float x[8];
+      widen8<BF16>(next, x);
+      const bool mine = h < a.heads;
+      h += stride * HEADS;
+      src += step;
+      next = read(src, h < a.heads);
       turn.apply(x, lane);
-      if (r * HEADS + sub < a.heads)
-        *reinterpret_cast<uint4*>(a.q_out + t * a.q_out_stride + r * (HEADS * D) + own) =
-            pos_ok ? narrow8<BF16>(x) : make_uint4(0u, 0u, 0u, 0u);
-      continue;
+      if (mine) *reinterpret_cast<uint4*>(dst) = pos_ok ? narrow8<BF16>(x) : none;
+      dst += step;
     }
-    if (vr < 0) turn.apply(x, lane);
-    uint32_t u[8];
-    const uint32_t meta = quantize8<LANES>(x, u);
-    const int h = (vr < 0 ? kr : vr) * HEADS + sub;
-    if (!keep || h >= a.c.kv_heads) continue;  // after the last shuffle of the round
-    uint8_t* unit = unit0 + (int64_t)h * head_bytes;
-    if (vr < 0) {  // AWQ order: 0, 2, 4, 6, 1, 3, 5, 7; the upper bits of the floats are taken off the sum
-      constexpr uint32_t kOff = 0x4B400000u * 0x11111111u;
-      *reinterpret_cast<uint32_t*>(unit + key_at) = u[0] + (u[2] << 4) + (u[4] << 8) + (u[6] << 12) + (u[1] << 16) +
-                                                    (u[3] << 20) + (u[5] << 24) + (u[7] << 28) - kOff;
-    } else {  // the channels of a lane are two halves, four bytes apart
+  }
+  const bool keep = pos_ok && slot >= 0 && slot < a.c.num_pages * a.c.page_size;
+  if (!keep) return;  // the whole warp
+  int in_page;
+  const int64_t page = page_of(slot, a.c.page_size, in_page);
+  const int units = a.c.page_size / kKv4Unit, token = in_page % kKv4Unit;
+  const int64_t head_bytes = units * kv4_unit_bytes(D);
+  uint8_t* unit0 = a.cache + (page * a.c.kv_heads * units + in_page / kKv4Unit) * kv4_unit_bytes(D);
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
-        *reinterpret_cast<uint16_t*>(unit + value_at + 4 * p) =
-            (uint16_t)(u[4 * p] + (u[4 * p + 1] << 4) + (u[4 * p + 2] << 8) + (u[4 * p + 3] << 12));
+  for (int is_v = 0; is_v < 2; ++is_v) {
+    const int first = is_v ? v_first : k_first;
+    int h = first * HEADS + sub;
+    const uint16_t* src = (is_v ? a.v + t * a.v_stride : a.k + t * a.k_stride) + first * (HEADS * D) + own;
+    uint8_t* unit = unit0 + h * head_bytes;
+    const int code_at = is_v ? kv4_value_offset(D, token, 8 * lane) : kv4_key_offset(D, token) + 4 * lane;
+    const int meta_at = kv4_meta_offset(D, token) + 4 * is_v;
+    uint4 next = read(src, h < a.c.kv_heads);
+    for (int r = first; r < kv_rounds; r += stride) {
+      float x[8];
+      widen8<BF16>(next, x);
+      const bool mine = h < a.c.kv_heads;
+      h += stride * HEADS;
+      src += step;
+      next = read(src, h < a.c.kv_heads);
+      if (!is_v) turn.apply(x, lane);
+      uint32_t u[8];
+      const uint32_t meta = quantize8<LANES>(x, u);
+      if (mine) {
+        if (is_v) {  // the channels of a lane are two halves, four bytes apart
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+            *reinterpret_cast<uint16_t*>(unit + code_at + 4 * p) =
+                (uint16_t)(u[4 * p] + (u[4 * p + 1] << 4) + (u[4 * p + 2] << 8) + (u[4 * p + 3] << 12));
+        } else {  // AWQ order: 0, 2, 4, 6, 1, 3, 5, 7; the upper bits of the floats are taken off the sum
+          constexpr uint32_t kOff = 0x4B400000u * 0x11111111u;
+          *reinterpret_cast<uint32_t*>(unit + code_at) = u[0] + (u[2] << 4) + (u[4] << 8) + (u[6] << 12) + (u[1] << 16) +
+                                                         (u[3] << 20) + (u[5] << 24) + (u[7] << 28) - kOff;
+        }
+        if (lane == 0) *reinterpret_cast<uint32_t*>(unit + meta_at) = meta;
+      }
+      unit += stride * HEADS * head_bytes;
     }
-    if (lane == 0) *reinterpret_cast<uint32_t*>(unit + meta_at + (vr < 0 ? 0 : 4)) = meta;
   }
 }
 

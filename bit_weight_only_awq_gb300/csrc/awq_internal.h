@@ -191,9 +191,9 @@ struct Kv4AttnArgs {
   int window;
 };
 size_t kv4_attention_workspace(int64_t T, int64_t B, int max_q, int heads, int kv_heads, int dim);
-// many query rows of a cache head (kv4_prefill.cu); ws: kv4_prefill_workspace bytes
+// sequences with more than min_rows query rows of a cache head (kv4_prefill.cu); ws: kv4_prefill_workspace bytes
 size_t kv4_prefill_workspace(int64_t T, int64_t B, int max_q, int heads, int kv_heads, int dim);
-cudaError_t launch_kv4_prefill(const Kv4AttnArgs& a, int dim, bool bf16, void* ws, int* err, cudaStream_t s);
+cudaError_t launch_kv4_prefill(const Kv4AttnArgs& a, int min_rows, int dim, bool bf16, void* ws, int* err, cudaStream_t s);
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, int dim, bool bf16, void* ws, int* err, cudaStream_t s);
 
 }  // namespace awq

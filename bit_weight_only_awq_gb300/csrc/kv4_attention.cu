@@ -74,7 +74,7 @@ __device__ __forceinline__ Seq seq_of(const Args& a, const int3 v) {
   s.lo = min(s.lo, s.len);
   s.tile0 = s.lo / kTile;
   s.tiles = max(1, (s.len + kTile - 1) / kTile - s.tile0);
-  s.blocks = (s.n * a.per + 8 * NT - 1) / (8 * NT);
+  s.blocks = s.n * a.per > a.rows ? 0 : (s.n * a.per + 8 * NT - 1) / (8 * NT);
   s.groups = a.kv_heads * s.blocks;
   return s;
 }
@@ -763,16 +763,14 @@ kv4_attention_kernel(const Args a, float* warp_parts, float* cta_parts, int* cou
   }
 }
 
-// Eight columns hold a cache head's queries, or sixteen.
-bool narrow(int max_q, int heads, int kv_heads) { return (int64_t)max_q * (heads / kv_heads) <= 8; }
-
 template <int D, bool BF16, int NT>
-cudaError_t launch(const Kv4AttnArgs& args, void* ws, int* err, cudaStream_t s) {
+cudaError_t launch(const Kv4AttnArgs& args, int max_rows, void* ws, int* err, cudaStream_t s) {
   const void* fn = reinterpret_cast<const void*>(kv4_attention_kernel<D, BF16, NT>);
   cudaError_t e = set_smem_once(fn, Geo<D, NT>::kSmemBytes);
   if (e != cudaSuccess) return e;
   const int ctas = device_sm_count();
-  const Args a = make_args(args);
+  Args a = make_args(args);
+  a.rows = max_rows;
   uint8_t* base = static_cast<uint8_t*>(ws);
   float* warp_parts = reinterpret_cast<float*>(base + kCounterBytes);
   float* cta_parts = warp_parts + (size_t)ctas * warps_of(NT) * part_floats(D, 8 * NT);
@@ -791,34 +789,55 @@ cudaError_t launch(const Kv4AttnArgs& args, void* ws, int* err, cudaStream_t s) 
   return cudaGetLastError();
 }
 
-}  // namespace
+// Up to how many query rows of a cache head this kernel takes a sequence; the tcgen05 kernel, which makes operands of a
+// tile once for 256 rows where this one goes over the cache again for every 8 or 16, takes longer ones.  us at 8 x 8192
+// tokens, 8 cache heads of 128 channels, here / there: 16 rows 34 / 81, 32 rows 52 / 82, 64 rows 90 / 83; at 16 x 4096,
+// 64 channels: 32 rows 37 / 71, 64 rows 61 / 71.
+int rows_here(int dim) { return dim == 128 ? 48 : 64; }
+constexpr int64_t kPrefillMaxRows = 1 << 20;  // of the other's grid: 4096 row blocks, 16 shares of the cache
 
-// From which number of query rows of a cache head on the tcgen05 kernel takes the call: it makes operands of a tile
-// once for 256 rows, where this one goes over the cache again for every 16.  us at 8 x 8192 tokens, 8 cache heads of 128
-// channels, here / there: 16 rows 34 / 81, 32 rows 52 / 82, 64 rows 90 / 83; at 16 x 4096, 64 channels: 32 rows 37 / 71,
-// 64 rows 61 / 71.
-constexpr int64_t kPrefillMaxRows = 1 << 20;  // its grid's second dimension: 4096 row blocks, 16 shares of the cache
-bool many(int64_t T, int max_q, int heads, int kv_heads, int dim) {
-  const int64_t rows = (max_q < T ? max_q : T) * (heads / kv_heads);
-  return rows > (dim == 128 ? 48 : 64) && rows <= kPrefillMaxRows;
+// What a call takes: this kernel, with eight or sixteen columns, the other, or each for its sequences.  Sequences of
+// different length (T < B max_q) may be of both kinds: 31 single tokens and 512 of a prompt, 8192 cached each, take 251 us
+// so, and 413 us on the other kernel alone.
+struct Route {
+  bool here, there;
+  int nt;
+};
+Route route_of(int64_t T, int64_t B, int max_q, int heads, int kv_heads, int dim) {
+  const int64_t per = heads / kv_heads, rows = (max_q < T ? max_q : T) * per;
+  Route r;
+  r.there = rows > rows_here(dim) && rows <= kPrefillMaxRows;
+  r.here = !r.there || (T < B * max_q && per <= rows_here(dim));
+  r.nt = (r.there ? per : rows) <= 8 ? 1 : 2;
+  return r;
 }
 
-// Counters, a partial for each warp, and two for each CTA; or the other kernel's partials after the counters.
+// Counters, a partial for each warp, and two for each CTA; then the other kernel's partials.
+size_t workspace_here(int nt, int dim) {
+  return align256((size_t)device_sm_count() * (warps_of(nt) + 2) * sizeof(float) * part_floats(dim, 8 * nt));
+}
+
+}  // namespace
+
 size_t kv4_attention_workspace(int64_t T, int64_t B, int max_q, int heads, int kv_heads, int dim) {
-  if (many(T, max_q, heads, kv_heads, dim)) return kCounterBytes + align256(kv4_prefill_workspace(T, B, max_q, heads, kv_heads, dim));
-  const int nt = narrow(max_q, heads, kv_heads) ? 1 : 2;
-  return kCounterBytes + align256((size_t)device_sm_count() * (warps_of(nt) + 2) * sizeof(float) * part_floats(dim, 8 * nt));
+  const Route r = route_of(T, B, max_q, heads, kv_heads, dim);
+  return kCounterBytes + (r.here ? workspace_here(r.nt, dim) : 0) +
+         (r.there ? align256(kv4_prefill_workspace(T, B, max_q, heads, kv_heads, dim)) : 0);
 }
 
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, int dim, bool bf16, void* ws, int* err, cudaStream_t s) {
-  if (many(a.T, a.max_q, a.heads, a.kv_heads, dim))
-    return launch_kv4_prefill(a, dim, bf16, static_cast<uint8_t*>(ws) + kCounterBytes, err, s);
-  if (narrow(a.max_q, a.heads, a.kv_heads)) {
-    if (dim == 128) return bf16 ? launch<128, true, 1>(a, ws, err, s) : launch<128, false, 1>(a, ws, err, s);
-    return bf16 ? launch<64, true, 1>(a, ws, err, s) : launch<64, false, 1>(a, ws, err, s);
+  const Route r = route_of(a.T, a.B, a.max_q, a.heads, a.kv_heads, dim);
+  if (r.here) {
+    const int rows = r.there ? rows_here(dim) : INT32_MAX;
+    const auto fn = r.nt == 1 ? (dim == 128 ? (bf16 ? launch<128, true, 1> : launch<128, false, 1>)
+                                            : (bf16 ? launch<64, true, 1> : launch<64, false, 1>))
+                              : (dim == 128 ? (bf16 ? launch<128, true, 2> : launch<128, false, 2>)
+                                            : (bf16 ? launch<64, true, 2> : launch<64, false, 2>));
+    const cudaError_t e = fn(a, rows, ws, err, s);
+    if (e != cudaSuccess || !r.there) return e;
   }
-  if (dim == 128) return bf16 ? launch<128, true, 2>(a, ws, err, s) : launch<128, false, 2>(a, ws, err, s);
-  return bf16 ? launch<64, true, 2>(a, ws, err, s) : launch<64, false, 2>(a, ws, err, s);
+  uint8_t* parts = static_cast<uint8_t*>(ws) + kCounterBytes + (r.here ? workspace_here(r.nt, dim) : 0);
+  return launch_kv4_prefill(a, r.here ? rows_here(dim) : 0, dim, bf16, parts, err, s);
 }
 
 }  // namespace awq

@@ -11,6 +11,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 struct Args : Kv4AttnArgs {
   int per;             // query heads of a cache head
+  int rows;            // the sequences of this launch: at most so many query rows of a cache head, or more than that
   int units_page;      // units of a page
   uint32_t page_magic; // unit / units_page = high word of unit * page_magic (0: one unit a page)
 };

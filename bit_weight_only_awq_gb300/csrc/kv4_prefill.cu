@@ -133,7 +133,10 @@ __device__ __forceinline__ Job job_of(const Args& a, int row_block, int kv_head,
   j.tile0 = 0;
   j.count[0] = j.count[1] = j.total = 0;
   const int rows = s.y * a.per;
-  if (j.row0 >= rows) return j;
+  if (j.row0 >= rows || rows <= a.rows) {
+    j.n = 0;  // nothing to do here
+    return j;
+  }
   const int first = s.z - s.y + j.row0 / a.per;  // the first row's position
   j.lo = a.window > 0 ? min(max(0, first - a.window + 1), s.z) : 0;
   const int base = j.lo / kTok;
@@ -606,7 +609,7 @@ __global__ void __launch_bounds__(256) kv4_prefill_join_kernel(const Args a, int
   const int pr = blockIdx.x % (kRows / 8) * 8 + warp;
   const int3 s = read_seq(a, blockIdx.z);
   const int col = row_block * kRows + pr, i = col / a.per;
-  if (i >= s.y) return;
+  if (i >= s.y || s.y * a.per <= a.rows) return;
   const float* part = parts + (((long long)blockIdx.z * a.kv_heads + blockIdx.y) * blocks + row_block) * splits * part_floats(D);
   float top = -INFINITY;
   for (int k = 0; k < splits; ++k) top = fmaxf(top, part[k * part_floats(D) + (long long)kRows * D + pr]);
@@ -647,12 +650,13 @@ Plan plan_of(int64_t T, int64_t B, int max_q, int heads, int kv_heads) {
 }
 
 template <int D, bool BF16>
-cudaError_t launch(const Kv4AttnArgs& args, float* parts, int* err, cudaStream_t s) {
+cudaError_t launch(const Kv4AttnArgs& args, int min_rows, float* parts, int* err, cudaStream_t s) {
   const void* fn = reinterpret_cast<const void*>(kv4_prefill_kernel<D, BF16>);
   cudaError_t e = set_smem_once(fn, Geo<D>::kSmem);
   if (e != cudaSuccess) return e;
   const Plan p = plan_of(args.T, args.B, args.max_q, args.heads, args.kv_heads);
-  const Args a = make_args(args);
+  Args a = make_args(args);
+  a.rows = min_rows;
   kv4_prefill_kernel<D, BF16><<<dim3((unsigned)a.kv_heads, (unsigned)(p.blocks * p.splits), (unsigned)a.B), kThreads,
                                 Geo<D>::kSmem, s>>>(a, p.splits, parts, err);
   e = cudaGetLastError();
@@ -670,10 +674,10 @@ size_t kv4_prefill_workspace(int64_t T, int64_t B, int max_q, int heads, int kv_
   return p.splits == 1 ? 0 : sizeof(float) * (size_t)p.blocks * p.splits * kv_heads * B * (size_t)part_floats(dim);
 }
 
-cudaError_t launch_kv4_prefill(const Kv4AttnArgs& a, int dim, bool bf16, void* ws, int* err, cudaStream_t s) {
+cudaError_t launch_kv4_prefill(const Kv4AttnArgs& a, int min_rows, int dim, bool bf16, void* ws, int* err, cudaStream_t s) {
   float* parts = static_cast<float*>(ws);
-  if (dim == 128) return bf16 ? launch<128, true>(a, parts, err, s) : launch<128, false>(a, parts, err, s);
-  return bf16 ? launch<64, true>(a, parts, err, s) : launch<64, false>(a, parts, err, s);
+  if (dim == 128) return bf16 ? launch<128, true>(a, min_rows, parts, err, s) : launch<128, false>(a, min_rows, parts, err, s);
+  return bf16 ? launch<64, true>(a, min_rows, parts, err, s) : launch<64, false>(a, min_rows, parts, err, s);
 }
 
 }  // namespace awq

@@ -114,6 +114,10 @@ MULTI = [  # (lens, new tokens), heads, kv_heads, dim, page, bf16, window
     (([400], [400]), 8, 8, 128, 128, True, 0), (([600, 31], [100, 1]), 5, 1, 128, 32, False, 17),
     (([3], [200]), 4, 2, 128, 16, False, 0), (([1100, 700, 65], [300, 129, 2]), 8, 2, 128, 64, False, 0),
     (([257], [256]), 7, 7, 64, 64, True, 1), (([0], [70]), 8, 2, 64, 16, False, 0),
+    # single tokens, a few, and prompts in one call
+    (([900, 500, 64, 1, 0, 200, 33], [300, 1, 5, 1, 1, 200, 13]), 8, 2, 128, 64, False, 0),
+    (([700, 500, 64, 2, 200, 900], [100, 1, 40, 2, 0, 33]), 4, 2, 64, 16, True, 90),
+    (([300, 77, 1000], [120, 1, 2]), 64, 1, 128, 32, False, 0), (([300, 77], [60, 1]), 12, 1, 64, 32, False, 0),
 ]
 
 

@@ -190,6 +190,23 @@ def test_a_nan_value_shows_only_where_it_is_seen(awq, new, heads):
     assert np.isnan(out[sees]).all() and np.isfinite(out[~sees][:-1]).all()
 
 
+@pytest.mark.parametrize("new", [1, 2, 12, 40])
+@pytest.mark.parametrize("scale,q_scale", [(1e-40, 2.0), (-1e-30, 0.0), (1e-44, 1e-3), (0.0, 2.0)])
+def test_scales_next_to_zero_give_the_mean(awq, new, scale, q_scale):
+    """Scores that vanish: the weights are equal, and masked keys have none (the module's bound with delta = 0)."""
+    p = Problem([150, 30], [new, min(new, 30)], 8, 2, 128, 64, bf16=True, seed=21, q_scale=q_scale)
+    for window in (0, 33):
+        out, lse = p.run(awq, window=window, scale=scale)
+        want, want_lse, mag, _ = block.kv4_attention(p.q, p.cache, p.table, p.lens, p.start, scale, window)
+        got = out.float().cpu().numpy()
+        bound = mag * (2.0 ** -11 + 2.0 ** -17) + 2.0 ** -8 * np.abs(want) + 2.0 ** -24 * (1 + mag.max())
+        seen = ~np.isneginf(want_lse)
+        assert np.all(np.abs(got - want) <= bound)
+        got_lse = lse.cpu().numpy()
+        assert np.array_equal(~np.isneginf(got_lse), seen)
+        assert np.all(np.abs(got_lse - want_lse)[seen] <= 2.0 ** -17 + 2.0 ** -22 * np.abs(want_lse)[seen])
+
+
 def test_strided_queries_table_rows_and_explicit_scale(awq):
     p = Problem([90, 40], [2, 1], 4, 2, 64, 16, seed=11)
     q = torch.zeros(3, 6, 64, dtype=torch.float16, device="cuda")

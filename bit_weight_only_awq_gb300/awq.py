@@ -515,7 +515,7 @@ def kv4_append(cache, k, v, positions, slots, table, q=None, interleaved: bool =
         max_pos, rot = table.shape
         _need("kv4_append", torch.float32, table)
         _need("kv4_append", torch.int32, positions)
-        if positions.shape != (T,):
+        if positions is None or positions.shape != (T,):
             raise ValueError("kv4_append: positions is [T]")
     _check("kv4_append", lib.kv4_append(
         _ptr(q), _ptr(k), _ptr(v), qs, _row_stride("kv4_append", k, kv_heads * dim),
@@ -548,8 +548,10 @@ def kv4_attention_workspace_bytes(T: int, B: int, max_q: int, heads: int, kv_hea
     return int(lib.kv4_attention_workspace_bytes(T, B, max_q, heads, kv_heads, head_dim))
 
 
-# One workspace of kv4_attention for each device and stream (calls on one stream may share it), grown on demand.
+# One workspace of kv4_attention for each device and stream (calls on one stream may share it), grown on demand, by
+# half at least.  Outgrown ones stay: a graph captured on their stream may still use them.
 _kv4_workspaces: dict[tuple, torch.Tensor] = {}
+_kv4_outgrown: list[torch.Tensor] = []
 
 
 def _kv4_workspace(handle: int, device: torch.device, nbytes: int, stream) -> torch.Tensor:
@@ -557,7 +559,12 @@ def _kv4_workspace(handle: int, device: torch.device, nbytes: int, stream) -> to
     ws = _kv4_workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
-            # zeroed, and the old one freed, in the order of its own stream
+            if torch.cuda.is_current_stream_capturing():
+                # it would belong to the graph's memory, and be zeroed at its replays only
+                raise RuntimeError("kv4_attention: a captured call takes a workspace of its own")
+            if ws is not None:
+                _kv4_outgrown.append(ws)
+                nbytes = max(nbytes, ws.numel() + ws.numel() // 2)
             ws = _kv4_workspaces[key] = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
     return ws
 
@@ -571,7 +578,8 @@ def kv4_attention(q, cache, block_table, kv_len, q_start=None, max_q: int = 1, s
     at most max_q, which are its last tokens.  scale: 1 / sqrt(D) by default; window: 0 or the number of keys a
     query looks back over, its own included.  `lse` fp32 [T, heads], when given, receives the log-sum-exp.
     Without `workspace` the calls of a stream share one that grows; a call to be captured in a graph takes one of
-    its own (kv4_attention_workspace_bytes, zeroed once).
+    its own (kv4_attention_workspace_bytes, zeroed once).  After awq_last_device_error reports a wait that expired, a
+    workspace is zeroed again before its next use, as include/awq.h says of all of them.
     """
     pages, kv_heads, dim, page = _kv4_shape("kv4_attention", cache)
     shape = q.shape

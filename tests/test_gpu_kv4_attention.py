@@ -190,6 +190,34 @@ def test_a_nan_value_shows_only_where_it_is_seen(awq, new, heads):
     assert np.isnan(out[sees]).all() and np.isfinite(out[~sees][:-1]).all()
 
 
+def test_capture_takes_a_workspace_of_its_own(awq):
+    """A shared workspace made during a capture would live in the graph's memory; one outgrown later stays valid."""
+    p = Problem([500, 300], [1, 1], 8, 2, 128, 64, seed=22, junk=False)
+    q = torch.from_numpy(p.q).cuda().half()
+    cache, table, lens = (torch.from_numpy(a).cuda() for a in (p.cache, p.table, p.lens))
+    out = torch.empty_like(q)
+    want = awq.kv4_attention(q, cache, table, lens)
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    handle = (q.device.index, stream.cuda_stream)
+    kept = awq._kv4_workspaces.pop(handle, None)  # streams come from a pool: an earlier test may have used it
+    torch.cuda.synchronize()
+    with pytest.raises(RuntimeError, match="workspace"):
+        with torch.cuda.graph(graph, stream=stream):
+            out.zero_()
+            awq.kv4_attention(q, cache, table, lens, out=out)
+    assert handle not in awq._kv4_workspaces
+    with torch.cuda.stream(stream):
+        awq.kv4_attention(q, cache, table, lens, out=out)
+        first = awq._kv4_workspaces[handle]
+        awq._kv4_workspace(stream.cuda_stream, q.device, first.numel() + 1, None)
+        assert awq._kv4_workspaces[handle].numel() > first.numel() and any(w is first for w in awq._kv4_outgrown)
+        out.zero_()
+        awq.kv4_attention(q, cache, table, lens, out=out)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    del kept
+
+
 @pytest.mark.parametrize("new", [1, 2, 12, 40])
 @pytest.mark.parametrize("scale,q_scale", [(1e-40, 2.0), (-1e-30, 0.0), (1e-44, 1e-3), (0.0, 2.0)])
 def test_scales_next_to_zero_give_the_mean(awq, new, scale, q_scale):

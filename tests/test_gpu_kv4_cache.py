@@ -78,6 +78,37 @@ def test_append_and_gather(awq, T, heads, kv_heads, dim, page, rot, interleaved,
         assert np.array_equal(host(gv)[:, h], block.round16(block.kv4_dequant(vu, vs, vz), bf16))
 
 
+@pytest.mark.parametrize("T,heads,kv_heads,dim,rot,interleaved", [
+    (6001, 1, 1, 64, 64, False), (6001, 2, 1, 64, 64, True), (300, 40, 23, 128, 48, False), (3000, 0, 3, 128, 128, False),
+    (5000, 9, 0, 64, 32, True)])
+def test_long_calls_are_their_pieces(awq, T, heads, kv_heads, dim, rot, interleaved):
+    """Calls whose warps take parts of several tokens, some of them padding, against short calls of the same tokens."""
+    gen = torch.Generator(device="cuda").manual_seed(T + heads)
+    page, pages = 32, T // 32 + 9
+    q, k, v = (torch.randn(T, h, dim, generator=gen, device="cuda").half() for h in (heads, kv_heads, kv_heads))
+    positions = torch.randint(-5, 300, (T,), generator=gen, device="cuda", dtype=torch.int32)
+    slots = torch.randperm(pages * page, generator=gen, device="cuda")[:T].contiguous()
+    slots[torch.randint(0, T, (T // 10,), generator=gen, device="cuda")] = -1
+    table = torch.from_numpy(block.rope_table(290, rot)).cuda()
+    caches, outs = [], []
+    for piece in (T, 64):
+        cache = awq.kv4_cache(pages, max(kv_heads, 1), dim, page)
+        out = torch.full_like(q, 7.0)
+        for at in range(0, T, piece):
+            to = min(T, at + piece)
+            if kv_heads:
+                awq.kv4_append(cache, k[at:to], v[at:to], positions[at:to], slots[at:to], table,
+                               q=q[at:to] if heads else None, q_out=out[at:to] if heads else None, interleaved=interleaved)
+            else:
+                awq.lib.kv4_append(q[at:to].data_ptr(), None, None, heads * dim, 0, 0, positions[at:to].data_ptr(), None,
+                                   table.data_ptr(), 290, rot, int(interleaved), out[at:to].data_ptr(), heads * dim, None,
+                                   0, to - at, heads, 0, dim, page, 0, torch.cuda.current_stream().cuda_stream)
+        caches.append(cache)
+        outs.append(out)
+    assert torch.equal(caches[0], caches[1]) and torch.equal(outs[0], outs[1])
+    assert caches[0].any() == (kv_heads > 0) and (not heads or not (outs[0] == 7.0).all(dim=2).any())
+
+
 def test_consecutive_prompt_tokens_from_one_projection(awq):
     """Columns of one qkv projection, queries in place, tokens of one page and across pages, an odd first slot."""
     rng = np.random.default_rng(1)

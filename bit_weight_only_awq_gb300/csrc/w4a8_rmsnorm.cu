@@ -45,7 +45,7 @@ __device__ __forceinline__ uint2 codes8(const F2 (&t)[4], float step, float inv)
     b[2 * p] = __float_as_uint(w.x);
     b[2 * p + 1] = __float_as_uint(w.y);
   }
-  if (!(far < 0.4999f && inv < INFINITY)) {  // an infinite reciprocal makes NaN, which the maximum drops
+  if (!(far < 0.49996f && inv < INFINITY)) {  // an infinite reciprocal makes NaN, which the maximum drops
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
       const float2 v = t[p].get();

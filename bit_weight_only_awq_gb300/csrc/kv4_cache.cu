@@ -12,7 +12,7 @@ namespace {
 // two halves of the values.  The floor is HBM's: 8165 tokens of 32 + 32 + 32 heads move 305 MB in 77 us, 3.9 TB/s
 // (74 us when all channels turn, in halves), and are bound by the arithmetic (reductions over a head by shuffles, about
 // twenty operations for a code): without any one of the rotation, the stores or the check for ties it still takes
-// 70 to 73, and reading further ahead changes nothing.  Reading back moves 169 MB in 37 us, 4.5 TB/s.  64 tokens of
+// 70 to 73, and reading further ahead changes nothing.  Reading back moves 169 MB in 34 us, 5.0 TB/s.  64 tokens of
 // 32 + 8 + 8 heads take 4 us.
 constexpr int kAThreads = 256;
 constexpr int kAWarps = kAThreads / 32;
@@ -211,9 +211,28 @@ struct AppendArgs {
   float minus_zero;
 };
 
-// A round is what a warp does at once: 32 / LANES heads of a token.  The rounds of all tokens (each one's queries, then
-// keys, then values) are cut into equal contiguous ranges, one for each warp of a grid that fills the GPU once (a token for
-// each warp instead came to 1.7 waves of warps for 8165 tokens: 80 us instead of 77).
+// A round is what a warp does at once: 32 / LANES heads of a token.  The rounds of all tokens (for the append, each one's
+// queries, then keys, then values) are cut into equal contiguous ranges, one for each warp of a grid that fills the GPU
+// once (a token for each warp instead came to 1.7 waves of warps for 8165 tokens: 80 us instead of 77).
+struct WarpShare {
+  int64_t token;  // the range begins at round `first` of this token
+  int first, rounds;
+};
+__device__ __forceinline__ WarpShare share_of(int64_t total, int rounds) {
+  const int64_t warps = gridDim.x * (int64_t)kAWarps, me = blockIdx.x * (int64_t)kAWarps + threadIdx.x / 32;
+  const int64_t each = total / warps, rest = total - each * warps, begin = me * each + min(me, rest);
+  WarpShare s;
+  s.token = begin / rounds;
+  s.first = (int)(begin - s.token * rounds);
+  s.rounds = (int)each + (me < rest ? 1 : 0);
+  return s;
+}
+// Blocks of a grid for so many rounds.
+unsigned blocks_for(int64_t rounds, int resident) {
+  const int64_t most = resident * (int64_t)device_sm_count(), blocks = (rounds + kAWarps - 1) / kAWarps;
+  return (unsigned)(blocks < most ? blocks : most);
+}
+
 template <int D, bool BF16, Rotation HOW>
 __global__ void __launch_bounds__(kAThreads, kACtas) kv4_append_kernel(const AppendArgs a) {
   // a dependent launched early waits for this grid before it reads what is written here
@@ -222,17 +241,13 @@ __global__ void __launch_bounds__(kAThreads, kACtas) kv4_append_kernel(const App
   const int sub = threadIdx.x % 32 / LANES, lane = threadIdx.x % LANES;
   const int q_rounds = (a.heads + HEADS - 1) / HEADS, kv_rounds = (a.c.kv_heads + HEADS - 1) / HEADS;
   const int rounds = q_rounds + 2 * kv_rounds;
-  const int64_t total = a.T * rounds, warps = gridDim.x * (int64_t)kAWarps, me = blockIdx.x * (int64_t)kAWarps + threadIdx.x / 32;
-  const int64_t begin = me * (total / warps) + min(me, total % warps);
-  int left = (int)(total / warps) + (me < total % warps ? 1 : 0);
-  if (left == 0) return;
-  int64_t t = begin / rounds;
-  int first = (int)(begin - t * rounds);  // the range's first round of token t
+  const WarpShare share = share_of(a.T * rounds, rounds);
+  int64_t t = share.token;
   const int own = sub * D + 8 * lane;     // this lane's place in a round
   const uint4 none = make_uint4(0u, 0u, 0u, 0u);
   auto read = [&](const uint16_t* at, bool in) { return in ? *reinterpret_cast<const uint4*>(at) : none; };
   Turn<LANES, BF16, HOW> turn;
-  for (; left > 0; ++t, first = 0) {
+  for (int left = share.rounds, first = share.first; left > 0; ++t, first = 0) {
     const int last = min(first + left, rounds);
     left -= last - first;
     const int64_t pos = a.rope.rot ? a.rope.positions[t] : 0;
@@ -315,41 +330,68 @@ __device__ __forceinline__ uint32_t two_values(uint32_t pair, float2 sz) {
   return pack2<BF16>(__fadd_rn(sz.y, __fmul_rn(f.x, sz.x)), __fadd_rn(sz.y, __fmul_rn(f.y, sz.x)));
 }
 
+// Rounds cut as in the append; the reads of kGBatch of them are on the way at once (with 8165 tokens of 32 heads: 2 on
+// 6 CTAs an SM 34 us, 4 on 4 35, 8 on 4 38; a CTA for each token, one at a time, 37).
+constexpr int kGBatch = 2, kGCtas = 6;
+
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kAThreads)
+__global__ void __launch_bounds__(kAThreads, kGCtas)
 kv4_gather_kernel(const uint8_t* __restrict__ cache, const int64_t* __restrict__ slots, uint16_t* __restrict__ k,
-                  uint16_t* __restrict__ v, const Kv4Shape c) {
-  constexpr int LANES = D / 8, HEADS = kAThreads / LANES;
-  const int lane = threadIdx.x % LANES;
-  const int64_t t = blockIdx.x;
-  const int64_t slot = slots[t];
-  const bool in = slot >= 0 && slot < c.num_pages * c.page_size;
-  int in_page;
-  const int64_t page = page_of(in ? slot : 0, c.page_size, in_page);
-  const int units = c.page_size / kKv4Unit, token = in_page % kKv4Unit;
-  for (int h = threadIdx.x / LANES; h < c.kv_heads; h += HEADS) {
-    uint4 ko = make_uint4(0u, 0u, 0u, 0u), vo = ko;
-    if (in) {
-      const uint8_t* unit = cache + ((page * c.kv_heads + h) * units + in_page / kKv4Unit) * kv4_unit_bytes(D);
-      const uint2 m = *reinterpret_cast<const uint2*>(unit + kv4_meta_offset(D, token));
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(unit + kv4_key_offset(D, token) + 4 * lane);
-      const uint32_t a = *reinterpret_cast<const uint16_t*>(unit + kv4_value_offset(D, token, 8 * lane));
-      const uint32_t b = *reinterpret_cast<const uint16_t*>(unit + kv4_value_offset(D, token, 8 * lane + 4));
-      const float2 ks = unpack2<false>(m.x), vs = unpack2<false>(m.y);
-      ko = make_uint4(two_values<BF16>(w, ks), two_values<BF16>(w >> 4, ks), two_values<BF16>(w >> 8, ks),
-                      two_values<BF16>(w >> 12, ks));
-      // a half holds its four codes side by side: nibbles 0, 1 and 2, 3 become pairs
-      vo = make_uint4(two_values<BF16>(a | a << 12, vs), two_values<BF16>(a >> 8 | a << 4, vs),
-                      two_values<BF16>(b | b << 12, vs), two_values<BF16>(b >> 8 | b << 4, vs));
+                  uint16_t* __restrict__ v, const Kv4Shape c, int64_t T) {
+  constexpr int LANES = D / 8, HEADS = 32 / LANES;
+  const int sub = threadIdx.x % 32 / LANES, lane = threadIdx.x % LANES;
+  const int rounds = (c.kv_heads + HEADS - 1) / HEADS;
+  const WarpShare mine = share_of(T * rounds, rounds);
+  int64_t t = mine.token;
+  const int units = c.page_size / kKv4Unit;
+  const int64_t head_bytes = units * kv4_unit_bytes(D);
+  for (int left = mine.rounds, first = mine.first; left > 0; ++t, first = 0) {
+    const int last = min(first + left, rounds);
+    left -= last - first;
+    const int64_t slot = slots[t];
+    const bool in = slot >= 0 && slot < c.num_pages * c.page_size;
+    int in_page;
+    const int64_t page = page_of(in ? slot : 0, c.page_size, in_page);
+    const int token = in_page % kKv4Unit;
+    const uint8_t* unit0 = cache + (page * c.kv_heads * units + in_page / kKv4Unit) * kv4_unit_bytes(D);
+    for (int r = first; r < last; r += kGBatch) {
+      uint2 m[kGBatch];
+      uint32_t w[kGBatch], a[kGBatch], b[kGBatch];
+#pragma unroll
+      for (int i = 0; i < kGBatch; ++i) {
+        const int h = (r + i) * HEADS + sub;
+        const uint8_t* unit = unit0 + h * head_bytes;
+        m[i] = make_uint2(0u, 0u);
+        w[i] = a[i] = b[i] = 0u;
+        if (in && r + i < last && h < c.kv_heads) {
+          m[i] = *reinterpret_cast<const uint2*>(unit + kv4_meta_offset(D, token));
+          w[i] = *reinterpret_cast<const uint32_t*>(unit + kv4_key_offset(D, token) + 4 * lane);
+          a[i] = *reinterpret_cast<const uint16_t*>(unit + kv4_value_offset(D, token, 8 * lane));
+          b[i] = *reinterpret_cast<const uint16_t*>(unit + kv4_value_offset(D, token, 8 * lane + 4));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kGBatch; ++i) {
+        const int h = (r + i) * HEADS + sub;
+        if (r + i >= last || h >= c.kv_heads) break;
+        const float2 ks = unpack2<false>(m[i].x), vs = unpack2<false>(m[i].y);
+        const int64_t at = (t * c.kv_heads + h) * D + 8 * lane;
+        // codes 0 with scale and zero 0, of a slot outside the cache, are zeros
+        if (k)
+          *reinterpret_cast<uint4*>(k + at) = make_uint4(two_values<BF16>(w[i], ks), two_values<BF16>(w[i] >> 4, ks),
+                                                         two_values<BF16>(w[i] >> 8, ks), two_values<BF16>(w[i] >> 12, ks));
+        // a half holds its four codes side by side: nibbles 0, 1 and 2, 3 become pairs
+        if (v)
+          *reinterpret_cast<uint4*>(v + at) =
+              make_uint4(two_values<BF16>(a[i] | a[i] << 12, vs), two_values<BF16>(a[i] >> 8 | a[i] << 4, vs),
+                         two_values<BF16>(b[i] | b[i] << 12, vs), two_values<BF16>(b[i] >> 8 | b[i] << 4, vs));
+      }
     }
-    const int64_t at = (t * c.kv_heads + h) * D + 8 * lane;
-    if (k) *reinterpret_cast<uint4*>(k + at) = ko;
-    if (v) *reinterpret_cast<uint4*>(v + at) = vo;
   }
 }
 
 template <int D, bool BF16>
-void run_append(const AppendArgs& a, dim3 grid, cudaStream_t s) {
+void run_append(const AppendArgs& a, unsigned grid, cudaStream_t s) {
   const auto fn = a.rope.rot != D        ? kv4_append_kernel<D, BF16, kAnyRotation>
                   : a.rope.interleaved ? kv4_append_kernel<D, BF16, kNeighbours>
                                        : kv4_append_kernel<D, BF16, kHalves>;
@@ -364,8 +406,7 @@ cudaError_t launch_kv4_append(const uint16_t* q, const uint16_t* k, const uint16
                               int heads, bool bf16, cudaStream_t s) {
   const int at_once = 256 / c.dim;
   const int64_t rounds = T * ((heads + at_once - 1) / at_once + 2 * ((c.kv_heads + at_once - 1) / at_once));
-  const int64_t most = kACtas * (int64_t)device_sm_count(), blocks = (rounds + kAWarps - 1) / kAWarps;
-  const dim3 grid((unsigned)(blocks < most ? blocks : most));
+  const unsigned grid = blocks_for(rounds, kACtas);
   const AppendArgs a{q, k, v, q_stride, k_stride, v_stride, slots, rope, q_out, q_out_stride, cache, c, T, heads, -0.f};
   if (c.dim == 128)
     bf16 ? run_append<128, true>(a, grid, s) : run_append<128, false>(a, grid, s);
@@ -378,7 +419,8 @@ cudaError_t launch_kv4_gather(const uint8_t* cache, const int64_t* slots, uint16
                               int64_t T, bool bf16, cudaStream_t s) {
   const auto fn = c.dim == 128 ? (bf16 ? kv4_gather_kernel<128, true> : kv4_gather_kernel<128, false>)
                                : (bf16 ? kv4_gather_kernel<64, true> : kv4_gather_kernel<64, false>);
-  fn<<<(unsigned)T, kAThreads, 0, s>>>(cache, slots, k, v, c);
+  const int at_once = 256 / c.dim;
+  fn<<<blocks_for(T * ((c.kv_heads + at_once - 1) / at_once), kGCtas), kAThreads, 0, s>>>(cache, slots, k, v, c, T);
   return cudaGetLastError();
 }
 

@@ -60,7 +60,7 @@ __device__ __forceinline__ uint2 codes8(const F2 (&t)[4], float step, float inv)
 // A CTA takes rows in turn and reads each once: a thread keeps t = h w of its V vectors in registers between the
 // reduction and the codes, and has the next row's vectors on the way meanwhile.  The CTA's threads cover the row's K / 8
 // vectors V times.  HBM bound: 8192 x 8192 with the residual moves 470 MB in 72 us, 6.5 TB/s; 4096 x 4096 takes 20.3 us
-// (5.8 TB/s), 8 rows 2.5 us.  7001 x 11016 in bf16 without residual takes 62 us (3.7 TB/s): three bytes an element leave
+// (5.8 TB/s), 8 rows 2.5 us.  7001 x 11016 in bf16 without residual takes 58 us (4.0 TB/s): three bytes an element leave
 // the instructions in front, and a row of 1377 vectors fills eleven warps with a ragged fourth vector.
 template <bool BF16, bool RES, int V, int T, int CTAS>
 __global__ void __launch_bounds__(T, CTAS)
@@ -135,7 +135,8 @@ rmsnorm_kernel(const uint16_t* x, const uint16_t* residual, const uint16_t* __re
     if (xq) {
       // fmaxf drops a NaN, but the sum of squares keeps it, and an infinity too
       const bool finite = sum - sum == 0.f && top - top == 0.f;
-      const float step = __fdiv_rn(top, 127.0f);
+      // top / 127 rounded once: a quotient next to the right one, corrected by its exact remainder (Markstein 1990)
+      const float near = top * (1.f / 127.f), step = fmaf(fmaf(-127.f, near, top), 1.f / 127.f, near);
       const float inv = 1.0f / step;  // infinite for a step below the smallest normal number: exact division then
       if (tid == 0) s_tok[r] = finite ? step * rstd : __uint_as_float(0x7FC00000u);
       const bool codes = finite && step > 0.f;
@@ -172,7 +173,8 @@ cudaError_t launch(const uint16_t* x, const uint16_t* residual, const uint16_t* 
   // Rows that do not fill the GPU get as many threads as they have vectors, up to 1024, so that a row's loads are
   // all in flight at once; many rows get 2 or 4 vectors a thread, and a few CTAs on each SM go through them (a CTA for
   // each row instead: 4096 x 4096 24.4 us).  With 4 vectors two CTAs of 512 threads an SM need 64 registers, which only
-  // the form without a residual has (7001 x 11016: 76 us at one, 64 at two; with a residual 62 against 75).
+  // the form without a residual has (7001 x 11016: 76 us at one, 64 at two; with a residual 62 against 75); two of up to
+  // 384 threads have 80 (7001 x 11016 62 -> 58 us, 4096 x 11008 with a residual 60 -> 52).
   const bool few = M <= 2 * (int64_t)sms;
   const int v = few ? (nvec <= 1024 ? 1 : nvec <= 2048 ? 2 : nvec <= 4096 ? 4 : 8)
                     : (nvec <= 256 ? 1 : nvec <= 1024 ? 2 : nvec <= 4096 ? 4 : 8);
@@ -180,6 +182,7 @@ cudaError_t launch(const uint16_t* x, const uint16_t* residual, const uint16_t* 
   const auto fn = v == 1   ? rmsnorm_kernel<BF16, RES, 1, 1024, 1>
                   : v == 2 ? (threads <= 512 ? rmsnorm_kernel<BF16, RES, 2, 512, 2> : rmsnorm_kernel<BF16, RES, 2, 1024, 1>)
                   : v == 8 ? rmsnorm_kernel<BF16, RES, 8, 1024, 1>
+                  : threads <= 384 ? rmsnorm_kernel<BF16, RES, 4, 384, 2>
                   : threads <= 512 ? rmsnorm_kernel<BF16, RES, 4, 512, RES ? 1 : 2>
                                    : rmsnorm_kernel<BF16, RES, 4, 1024, 1>;
   const int64_t grid = few ? M : (int64_t)sms * 2048 / threads;

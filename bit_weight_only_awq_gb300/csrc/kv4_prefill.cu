@@ -108,6 +108,11 @@ __device__ __forceinline__ void commit(uint32_t bar) {
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Two codes of a word as exact halves u - 8: nibbles 0 and 4 (odd = 0), or 1 and 5.
@@ -162,7 +167,7 @@ __device__ __forceinline__ Job job_of(const Args& a, int row_block, int kv_head,
   return j;
 }
 
-// Floats of a CTA's partial result: output, maximum and sum of every row.
+// Floats of a CTA's partial result: output [channel / 4][row][channel % 4], then maximum and sum of every row.
 __host__ __device__ constexpr long long part_floats(int dim) { return (long long)kRows * (dim + 2); }
 
 template <int D, bool BF16>
@@ -174,6 +179,8 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   volatile int* abort_flag = &abort_word;
+  // the join, launched early, waits for this grid before it reads what is written here
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid / 32, 0), lane = tid % 32;
   // heads of a row block first, then the row blocks from the one that sees the most tokens down: CTAs start in the
   // order of their work, and the short ones fill what the long ones leave
@@ -226,15 +233,32 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
     const bool in = i < job.n;
     const int64_t token = job.begin + i;
     const int head = job.kv_head * a.per + col - i * a.per;
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;  // lanes of a row, rows of a warp at once
+    // chunk c (16 bytes) of row `row` of this row tile's queries, later of its output
+    auto row_at = [&](int row, int c) {
+      return sm + G::kQ + m * G::kQTile + (c / 8) * 16384 + row * 128 + ((c % 8) ^ (row % 8)) * 16;
+    };
     const float sign = a.scale > 0.f ? 1.f : a.scale < 0.f ? -1.f : 0.f;
     const float factor = a.scale == 0.f ? kLog2e : fabsf(a.scale) * kLog2e;
     float qk, qr;
     {
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + token * a.q_stride + head * D);
+      // The warp's rows come into the operand's place as they are, whole rows at once; then a thread scales its own.
+      const int64_t at = in ? token * a.q_stride + head * D : -1;
+      uint4 v[kLanes];
+#pragma unroll
+      for (int k = 0; k < kLanes; ++k) {
+        const int64_t from = __shfl_sync(0xFFFFFFFFu, at, k * kAtOnce + lane / kLanes);
+        v[k] = from >= 0 ? *reinterpret_cast<const uint4*>(a.q + from + 8 * (lane % kLanes)) : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int k = 0; k < kLanes; ++k)
+        sts128(row_at(warp % 4 * 32 + k * kAtOnce + lane / kLanes, lane % kLanes), v[k].x, v[k].y, v[k].z, v[k].w);
+      __syncwarp();
       float top = 0.f, sum = 0.f;
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 v = in ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int c = 0; c < kLanes; ++c) {
+        v[c] = lds128(row_at(r, c));
+        const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           const float2 f = unpack2<BF16>(w[p]);
@@ -245,11 +269,10 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
       // a power of two takes the largest element to [2^10, 2^11): exact in fp16 down to 2^-24 of it
       const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 127);
       const float up = __uint_as_float((uint32_t)(127 + 10 - e) << 23) * sign, up16 = up * 0.0625f;
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 v = in ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-        const float2 f0 = unpack2<BF16>(v.x), f1 = unpack2<BF16>(v.y), f2 = unpack2<BF16>(v.z), f3 = unpack2<BF16>(v.w);
-        sts128(sm + G::kQ + m * G::kQTile + (c / 8) * 16384 + r * 128 + ((c % 8) ^ (r % 8)) * 16,
-               pack2<false>(f0.x * up, f0.y * up), pack2<false>(f1.x * up16, f1.y * up16),
+#pragma unroll
+      for (int c = 0; c < kLanes; ++c) {
+        const float2 f0 = unpack2<BF16>(v[c].x), f1 = unpack2<BF16>(v[c].y), f2 = unpack2<BF16>(v[c].z), f3 = unpack2<BF16>(v[c].w);
+        sts128(row_at(r, c), pack2<false>(f0.x * up, f0.y * up), pack2<false>(f1.x * up16, f1.y * up16),
                pack2<false>(f2.x * up, f2.y * up), pack2<false>(f3.x * up16, f3.y * up16));
       }
       // not 0, which would make a NaN of a masked score, -inf; below that the weights are equal anyway
@@ -412,19 +435,27 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
 #pragma unroll
         for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(o[k]) + z;
         if (splits == 1) {
-          if (in) {
-            uint32_t w[8];
+          uint32_t w[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) w[k] = pack2<BF16>(v[2 * k] * inv, v[2 * k + 1] * inv);
-            uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + c);
-            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-          }
+          for (int k = 0; k < 8; ++k) w[k] = pack2<BF16>(v[2 * k] * inv, v[2 * k + 1] * inv);
+          sts128(row_at(r, c / 8), w[0], w[1], w[2], w[3]);
+          sts128(row_at(r, c / 8 + 1), w[4], w[5], w[6], w[7]);
         } else {
-          float4* dst = reinterpret_cast<float4*>(part + (long long)pr * D + c);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            dst[k] = make_float4(v[4 * k] * unit, v[4 * k + 1] * unit, v[4 * k + 2] * unit, v[4 * k + 3] * unit);
+            reinterpret_cast<float4*>(part)[(c / 4 + k) * kRows + pr] =
+                make_float4(v[4 * k] * unit, v[4 * k + 1] * unit, v[4 * k + 2] * unit, v[4 * k + 3] * unit);
+        }
+      }
+      if (splits == 1) {  // whole rows at once, as the queries came
+        __syncwarp();
+        const int64_t at = in ? row * D : -1;
+#pragma unroll
+        for (int k = 0; k < kLanes; ++k) {
+          const int from = k * kAtOnce + lane / kLanes;
+          const int64_t to = __shfl_sync(0xFFFFFFFFu, at, from);
+          const uint4 x = lds128(row_at(warp % 4 * 32 + from, lane % kLanes));
+          if (to >= 0) *reinterpret_cast<uint4*>(a.out + to + 8 * (lane % kLanes)) = x;
         }
       }
       const float high = top == -INFINITY ? -INFINITY : top * qk;
@@ -608,12 +639,16 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
   }
 }
 
-// The partial results of a row's splits become its output: a warp for each row.
+// The partial results of a row's splits become its output: a CTA for eight rows, a thread for four channels of one.
+constexpr int kJoinRows = 8;
 template <int D, bool BF16>
-__global__ void __launch_bounds__(256) kv4_prefill_join_kernel(const Args a, int splits, const float* __restrict__ parts) {
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int blocks = gridDim.x / (kRows / 8), row_block = blockIdx.x / (kRows / 8);
-  const int pr = blockIdx.x % (kRows / 8) * 8 + warp;
+__global__ void __launch_bounds__(kJoinRows * D / 4)
+kv4_prefill_join_kernel(const Args a, int splits, const float* __restrict__ parts) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int row = threadIdx.x % kJoinRows, c4 = threadIdx.x / kJoinRows;
+  const int blocks = gridDim.x / (kRows / kJoinRows), row_block = blockIdx.x / (kRows / kJoinRows);
+  const int pr = blockIdx.x % (kRows / kJoinRows) * kJoinRows + row;
   const int3 s = read_seq(a, blockIdx.z);
   const int col = row_block * kRows + pr, i = col / a.per;
   if (i >= s.y || s.y * a.per <= a.rows) return;
@@ -621,23 +656,19 @@ __global__ void __launch_bounds__(256) kv4_prefill_join_kernel(const Args a, int
   float top = -INFINITY;
   for (int k = 0; k < splits; ++k) top = fmaxf(top, part[k * part_floats(D) + (long long)kRows * D + pr]);
   const float base = top == -INFINITY ? 0.f : top;
-  float l = 0.f, o[D / 32];
-#pragma unroll
-  for (int c = 0; c < D / 32; ++c) o[c] = 0.f;
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int k = 0; k < splits; ++k) {
     const float* p = part + k * part_floats(D);
     const float f = ex2(p[(long long)kRows * D + pr] - base);
+    const float4 x = reinterpret_cast<const float4*>(p)[c4 * kRows + pr];
     l = fmaf(p[(long long)kRows * D + kRows + pr], f, l);
-    const float* src = p + (long long)pr * D + lane * (D / 32);
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) o[c] = fmaf(src[c], f, o[c]);
+    o = make_float4(fmaf(x.x, f, o.x), fmaf(x.y, f, o.y), fmaf(x.z, f, o.z), fmaf(x.w, f, o.w));
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int64_t row = (int64_t)(s.x + i) * a.heads + blockIdx.y * a.per + col - i * a.per;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + row * D + lane * (D / 32));
-#pragma unroll
-  for (int c = 0; c < D / 64; ++c) dst[c] = pack2<BF16>(o[2 * c] * inv, o[2 * c + 1] * inv);
-  if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
+  const int64_t at = (int64_t)(s.x + i) * a.heads + blockIdx.y * a.per + col - i * a.per;
+  reinterpret_cast<uint2*>(a.out + at * D)[c4] = make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
+  if (a.lse && c4 == 0) a.lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
 }
 
 struct Plan {
@@ -662,14 +693,28 @@ cudaError_t launch(const Kv4AttnArgs& args, int min_rows, float* parts, int* err
   cudaError_t e = set_smem_once(fn, Geo<D>::kSmem);
   if (e != cudaSuccess) return e;
   const Plan p = plan_of(args.T, args.B, args.max_q, args.heads, args.kv_heads);
+  // a split has two tiles at least, as far as the page table tells: a CTA's start and end cost as much as those, and the
+  // join is another launch
+  const int64_t most = (int64_t)args.max_pages * args.page_size, seen = args.window > 0 ? (int64_t)args.window + args.max_q : most;
+  const int64_t tiles = ((seen < most ? seen : most) + kTok - 1) / kTok;
+  const int splits = (int)(p.splits < tiles / 2 ? p.splits : tiles / 2 > 1 ? tiles / 2 : 1);
   Args a = make_args(args);
   a.rows = min_rows;
-  kv4_prefill_kernel<D, BF16><<<dim3((unsigned)a.kv_heads, (unsigned)(p.blocks * p.splits), (unsigned)a.B), kThreads,
-                                Geo<D>::kSmem, s>>>(a, p.splits, parts, err);
+  kv4_prefill_kernel<D, BF16><<<dim3((unsigned)a.kv_heads, (unsigned)(p.blocks * splits), (unsigned)a.B), kThreads, Geo<D>::kSmem,
+                                s>>>(a, splits, parts, err);
   e = cudaGetLastError();
-  if (e != cudaSuccess || p.splits == 1) return e;
-  kv4_prefill_join_kernel<D, BF16><<<dim3((unsigned)(p.blocks * (kRows / 8)), (unsigned)a.kv_heads, (unsigned)a.B), 256, 0, s>>>(
-      a, p.splits, parts);
+  if (e != cudaSuccess || splits == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)(p.blocks * (kRows / kJoinRows)), (unsigned)a.kv_heads, (unsigned)a.B);
+  cfg.blockDim = dim3(kJoinRows * D / 4);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kv4_prefill_join_kernel<D, BF16>, a, splits, (const float*)parts);
+  if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 

@@ -45,8 +45,8 @@ __device__ __forceinline__ long long now_ns() {
 // Bounded wait on an mbarrier phase.  Gives up when `abort` is raised by another
 // thread or after kWaitLimitNs; a timeout records `id` in the device error word
 // and raises `abort`.  Returns true when the phase completed.
-__device__ __noinline__ bool wait_bounded_slow(uint32_t bar, uint32_t parity, volatile int* abort, int* err, int id,
-                                               long long limit_ns = kWaitLimitNs) {
+__device__ __forceinline__ bool wait_bounded_inline(uint32_t bar, uint32_t parity, volatile int* abort, int* err, int id,
+                                                    long long limit_ns = kWaitLimitNs) {
   const long long t0 = now_ns();
   for (uint32_t spin = 1;; ++spin) {
     if (mbar_try(bar, parity)) return true;
@@ -59,6 +59,12 @@ __device__ __noinline__ bool wait_bounded_slow(uint32_t bar, uint32_t parity, vo
       }
     }
   }
+}
+// As a call: its loop takes no place between a kernel's own instructions.  A kernel that shares its registers out among
+// its warps (setmaxnreg) has no calls, and waits inline.
+__device__ __noinline__ bool wait_bounded_slow(uint32_t bar, uint32_t parity, volatile int* abort, int* err, int id,
+                                               long long limit_ns = kWaitLimitNs) {
+  return wait_bounded_inline(bar, parity, abort, err, id, limit_ns);
 }
 // Bounded wait that sleeps `sleep_ns` between polls: for a thread that shares its scheduler with
 // warps that have work and does not need to react within nanoseconds (a copy producer refilling a

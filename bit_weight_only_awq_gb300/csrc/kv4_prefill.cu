@@ -16,8 +16,8 @@
 // so that the rounding of the weights counts by the code's distance from the middle: a third of the error.
 //
 // Roles: warps 0-3 and 4-7 are the softmax of the two row tiles (a thread has a row), warps 8 and 9 issue their
-// products, warp 10 copies units, warps 11-14 turn codes into operands.  While one row tile's softmax runs, the other's products
-// do; a tile's two halves of 64 tokens have an S each, so that a row tile's next scores are there before it is done
+// products, warp 10 copies units, warps 11-14 turn codes into operands.  While one row tile's softmax runs, the other's
+// products do; a tile's two halves of 64 tokens have an S each, so that a row tile's next scores are there before it is done
 // with the present ones.  The output stays in tensor memory; it is rescaled only when a row's maximum has grown by more
 // than 2^8, so the weights are at most 2^8 and enter fp16 as p sv 2^(5 - e), 2^e the largest value scale so far.
 //
@@ -47,7 +47,11 @@ constexpr int kBufs = 4;     // operand buffers of a step's keys, and of its val
 constexpr int kMetas = 6;
 constexpr int kRaw = 3;      // raw slots
 constexpr int kDqThreads = 128;
-constexpr int kThreads = 480;
+constexpr int kThreads = 512;  // the last warp has no work: setmaxnreg wants whole groups of four warps
+// Registers.  At 128 for every thread, the softmax warps have too few to keep enough of a step's 64 scores, scales
+// and zeros under way: the chunk of 2 x 1024 tokens took 138 us, at 160 / 96 and more it takes 121, at 176 / 80 120.
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 176, kOtherRegs = 80;
+static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs, "no more than was launched with");
 constexpr float kGrow = 8.f;  // growth of the maximum (base 2) that rescales the output
 
 template <int D>
@@ -227,6 +231,7 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
   const uint32_t tmem = tmem_slot;  // S of row tile m at column 128 m, O at 256 + 128 m
 
   if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ------------------------------------------------ softmax: a thread has a row
     const int m = warp / 4, r = tid % 128;
     const int col = job.row0 + 128 * m + r, i = col / a.per;
@@ -299,8 +304,8 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
         // the scales and zeros are there with the keys
         const int step = 2 * j + h;
         const uint8_t* meta = smem + G::kMeta + step % kMetas * G::kMetaBytes;
-        ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bars.k_full[step % kBufs]), step / kBufs & 1, abort_flag, err, 622)) &&
-             __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bars.s_full[m][h]), j & 1, abort_flag, err, 621));
+        ok = __all_sync(0xFFFFFFFFu, wait_bounded_inline(smem_u32(&bars.k_full[step % kBufs]), step / kBufs & 1, abort_flag, err, 622)) &&
+             __all_sync(0xFFFFFFFFu, wait_bounded_inline(smem_u32(&bars.s_full[m][h]), j & 1, abort_flag, err, 621));
         if (!ok) break;
         tc_fence_after();
         uint32_t raw[4][16];
@@ -352,7 +357,7 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
           z *= f;
           if (j > 0 || h > 0) {
             // the products into O so far: the last ones, of the half before, may still run
-            ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bars.o_done[m][h ^ 1]), (j - 1 + h) & 1, abort_flag, err, 623));
+            ok = __all_sync(0xFFFFFFFFu, wait_bounded_inline(smem_u32(&bars.o_done[m][h ^ 1]), (j - 1 + h) & 1, abort_flag, err, 623));
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
@@ -413,7 +418,7 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
     // ---- the row's result
     if (ok && count > 0) {
       // the second half's products of the last tile
-      ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bars.o_done[m][1]), (count - 1) & 1, abort_flag, err, 624));
+      ok = __all_sync(0xFFFFFFFFu, wait_bounded_inline(smem_u32(&bars.o_done[m][1]), (count - 1) & 1, abort_flag, err, 624));
       tc_fence_after();
     }
     const float unit = __uint_as_float((uint32_t)(127 + vexp - 5) << 23);
@@ -466,169 +471,172 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
         a.lse[row] = l == 0.f ? -INFINITY : (high + log2f(l * unit)) * kLn2;
       }
     }
-  } else if (warp < 10) {
-    // ------------------------------------------------ products: a warp for each row tile
-    const int m = warp - 8, mine = 2 * job.count[m], steps = 2 * job.total;
-    auto wait = [&](uint64_t& bar, uint32_t parity, int id) {
-      return __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bar), parity, abort_flag, err, id)) != 0;
-    };
-    bool ok = wait(bars.q_full, 0, 611);
-    const uint64_t qa = smem_desc_sw128(sm + G::kQ + m * G::kQTile, 16, 1024);
-    const uint64_t kb = smem_desc_sw128(sm + G::kK, 16, 1024), vb = smem_desc_sw128(sm + G::kV, 16, 1024);
-    // step: 64 tokens; the scores of even and odd steps have an S each
-    auto scores = [&](int step) {
-      const int buf = step % kBufs;
-      ok = ok && wait(bars.k_full[buf], step / kBufs & 1, 612);
-      if (!ok) return;
-      tc_fence_after();
-      if (step < mine) {
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_ss(tmem + 128 * m + step % 2 * kHalf, qa + (uint64_t)((k / 4) * (16384 >> 4) + (k % 4) * 2),
-                 kb + (uint64_t)(buf * (G::kKStep >> 4) + (k / 4) * (kHalf * 128 >> 4) + (k % 4) * 2), G::kIdescS, k > 0 ? 1u : 0u);
-        commit(smem_u32(&bars.s_full[m][step % 2]));
-      }
-      commit(smem_u32(&bars.k_empty[buf]));
-    };
-    for (int step = 0; step < 2 && step < steps; ++step) scores(step);
-    for (int step = 0; step < steps && ok; ++step) {
-      const int buf = step % kBufs;
-      ok = wait(bars.v_full[buf], step / kBufs & 1, 614);
-      if (ok && step < mine) {
-        ok = wait(bars.p_full[m][step % 2], step / 2 & 1, 613);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_ts(tmem + 256 + 128 * m, tmem + 128 * m + step % 2 * kHalf + 8 * k,
-                 vb + (uint64_t)(buf * (G::kVStep >> 4) + k * 2), G::kIdescO, (step | k) ? 1u : 0u);
-        commit(smem_u32(&bars.o_done[m][step % 2]));
-      }
-      if (!ok) break;
-      commit(smem_u32(&bars.v_empty[buf]));
-      // the scores of the step after the next go where these weights were
-      if (step + 2 < steps) scores(step + 2);
-    }
-    // every product has completed before tensor memory is given back
-    commit(smem_u32(&bars.done));
-    volatile int no_abort = 0;
-    wait_bounded(smem_u32(&bars.done), 0, &no_abort, err, 615);
-  } else if (warp == 10) {
-    // ------------------------------------------------ copies: lane u takes unit u of a half tile
-    const int halves = 2 * job.total;
-    int issued = 0;
-    for (int k = 0; k < halves; ++k) {
-      const int st = k % kRaw;
-      const int unit = job.tile0 * (kTok / kKv4Unit) + k * 4 + lane;
-      const bool valid = lane < 4 && unit * kKv4Unit < job.len && (unit + 1) * kKv4Unit > job.lo;
-      const int p = a.page_magic ? (int)__umulhi((uint32_t)unit, a.page_magic) : unit;
-      int64_t page = valid ? a.block_table[blockIdx.z * a.table_stride + p] : 0;
-      if ((uint64_t)page >= (uint64_t)a.num_pages) page = 0;
-      if (k >= kRaw &&
-          !__all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bars.raw_empty[st]), (uint32_t)(k / kRaw - 1) & 1u, abort_flag, err, 601)))
-        break;
-      const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, valid));
-      const uint32_t bar = smem_u32(&bars.raw_full[st]);
-      if (lane == 0) mbar_arrive_tx(bar, n * G::kUnitBytes);
-      __syncwarp();
-      if (valid) {
-        const uint8_t* src = a.cache + ((page * a.kv_heads + job.kv_head) * a.units_page + (unit - p * a.units_page)) * G::kUnitBytes;
-        bulk_load(sm + G::kRawAt + st * G::kRawBytes + lane * G::kUnitStride, src, G::kUnitBytes, bar);
-      }
-      issued = k + 1;
-    }
-    // every copy lands before the CTA ends
-    volatile int no_abort = 0;
-    for (int k = max(0, issued - kRaw); k < issued; ++k)
-      wait_bounded(smem_u32(&bars.raw_full[k % kRaw]), (uint32_t)(k / kRaw) & 1u, &no_abort, err, 602);
   } else {
-    // ------------------------------------------------ operands from codes
-    const int d = tid - 352, w = d / 32;
-    bool ok = true;
-    for (int k = 0; k < 2 * job.total && ok; ++k) {
-      const int st = k % kRaw, buf = k % kBufs;
-      ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bars.raw_full[st]), (uint32_t)(k / kRaw) & 1u, abort_flag, err, 631));
-      if (ok && k >= kBufs)
-        ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bars.k_empty[buf]), (uint32_t)(k / kBufs - 1) & 1u, abort_flag, err, 632));
-      if (!ok) break;
-      const uint8_t* raw = smem + G::kRawAt + st * G::kRawBytes;
-      // scales and zeros as fp32, zeros for tokens outside the sequence: their bytes may be anything
-      if (d < kHalf) {
-        const int at = job.tile0 * kTok + k * kHalf + d;
-        uint2 mt = *reinterpret_cast<const uint2*>(raw + (d / 16) * G::kUnitStride + 16 * D + (d % 16) * 8);
-        if (at < job.lo || at >= job.len) mt = make_uint2(0u, 0u);
-        const float2 ksz = unpack2<false>(mt.x), vsz = unpack2<false>(mt.y);
-        uint8_t* meta = smem + G::kMeta + k % kMetas * G::kMetaBytes;
-        float* f = reinterpret_cast<float*>(meta) + d;
-        f[0] = ksz.x;
-        f[kHalf] = ksz.y;
-        f[2 * kHalf] = vsz.x;
-        f[3 * kHalf] = fmaf(8.f, vsz.x, vsz.y);
-        // the value scales of these 32 tokens are below 2^(that)
-        const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, mt.y & 0x7FFFu);
-        if (lane == 0) *reinterpret_cast<int*>(meta + 4 * kHalf * 4 + 4 * w) = (int)(most >> 10) - 14;
-      }
-      // keys: a word is eight channels of a token, one 16-byte chunk of its row.  A thread has one chunk of every
-      // kPass-th token, so that all its addresses are two bases and constants.
-      {
-        constexpr int kChunks = D / 8, kPass = kDqThreads / kChunks;
-        const int c = d % kChunks, tok = d / kChunks;
-        const uint8_t* src = raw + tok * (D / 2) + 4 * c;
-        const uint32_t dst = sm + G::kK + buf * G::kKStep + (c / 8) * (kHalf * 128) + tok * 128 + ((c % 8) ^ (tok % 8)) * 16;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp < 10) {
+      // ------------------------------------------------ products: a warp for each row tile
+      const int m = warp - 8, mine = 2 * job.count[m], steps = 2 * job.total;
+      auto wait = [&](uint64_t& bar, uint32_t parity, int id) {
+        return __all_sync(0xFFFFFFFFu, wait_bounded_inline(smem_u32(&bar), parity, abort_flag, err, id)) != 0;
+      };
+      bool ok = wait(bars.q_full, 0, 611);
+      const uint64_t qa = smem_desc_sw128(sm + G::kQ + m * G::kQTile, 16, 1024);
+      const uint64_t kb = smem_desc_sw128(sm + G::kK, 16, 1024), vb = smem_desc_sw128(sm + G::kV, 16, 1024);
+      // step: 64 tokens; the scores of even and odd steps have an S each
+      auto scores = [&](int step) {
+        const int buf = step % kBufs;
+        ok = ok && wait(bars.k_full[buf], step / kBufs & 1, 612);
+        if (!ok) return;
+        tc_fence_after();
+        if (step < mine) {
 #pragma unroll
-        for (int i = 0; i < kHalf / kPass; ++i) {
-          const int t = i * kPass;  // a multiple of 8
-          const uint32_t x = *reinterpret_cast<const uint32_t*>(src + (t / 16) * G::kUnitStride + (t % 16) * (D / 2));
-          const uint32_t y = x >> 8;
-          sts128(dst + t * 128, x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u);
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss(tmem + 128 * m + step % 2 * kHalf, qa + (uint64_t)((k / 4) * (16384 >> 4) + (k % 4) * 2),
+                   kb + (uint64_t)(buf * (G::kKStep >> 4) + (k / 4) * (kHalf * 128 >> 4) + (k % 4) * 2), G::kIdescS, k > 0 ? 1u : 0u);
+          commit(smem_u32(&bars.s_full[m][step % 2]));
         }
-      }
-      fence_async();
-      mbar_arrive(smem_u32(&bars.k_full[buf]));
-      if (k >= kBufs) {
-        ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bars.v_empty[buf]), (uint32_t)(k / kBufs - 1) & 1u, abort_flag, err, 633));
+        commit(smem_u32(&bars.k_empty[buf]));
+      };
+      for (int step = 0; step < 2 && step < steps; ++step) scores(step);
+      for (int step = 0; step < steps && ok; ++step) {
+        const int buf = step % kBufs;
+        ok = wait(bars.v_full[buf], step / kBufs & 1, 614);
+        if (ok && step < mine) {
+          ok = wait(bars.p_full[m][step % 2], step / 2 & 1, 613);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ts(tmem + 256 + 128 * m, tmem + 128 * m + step % 2 * kHalf + 8 * k,
+                   vb + (uint64_t)(buf * (G::kVStep >> 4) + k * 2), G::kIdescO, (step | k) ? 1u : 0u);
+          commit(smem_u32(&bars.o_done[m][step % 2]));
+        }
         if (!ok) break;
+        commit(smem_u32(&bars.v_empty[buf]));
+        // the scores of the step after the next go where these weights were
+        if (step + 2 < steps) scores(step + 2);
       }
-      // values: eight tokens of a channel are one chunk of its row.  Thread: eight tokens tc, channels [g D / 8, ...),
-      // a part of its quads; odd eights read their words pair by pair the other way round, so that the reads of
-      // eight lanes fall into different banks.
-      {
-        constexpr int kQuads = D / 32;               // quads of a group of D / 8 channels
-        constexpr int kEach = kQuads / 2;            // of a thread
-        const int tc = lane % 8, s = tc % 2, g = 4 * (w % 2) + lane / 8;
-        const int q0 = ((w / 2) ^ (kEach == 2 ? g % 2 : 0)) * kEach;  // two groups of a half-warp: different banks
-        const uint8_t* src = raw + (tc / 2) * G::kUnitStride + 8 * D + ((s * 8 + g) * 4 * kQuads + q0) * 4;
-        uint32_t x[4][kEach];
+      // every product has completed before tensor memory is given back
+      commit(smem_u32(&bars.done));
+      volatile int no_abort = 0;
+      wait_bounded_inline(smem_u32(&bars.done), 0, &no_abort, err, 615);
+    } else if (warp == 10) {
+      // ------------------------------------------------ copies: lane u takes unit u of a half tile
+      const int halves = 2 * job.total;
+      int issued = 0;
+      for (int k = 0; k < halves; ++k) {
+        const int st = k % kRaw;
+        const int unit = job.tile0 * (kTok / kKv4Unit) + k * 4 + lane;
+        const bool valid = lane < 4 && unit * kKv4Unit < job.len && (unit + 1) * kKv4Unit > job.lo;
+        const int p = a.page_magic ? (int)__umulhi((uint32_t)unit, a.page_magic) : unit;
+        int64_t page = valid ? a.block_table[blockIdx.z * a.table_stride + p] : 0;
+        if ((uint64_t)page >= (uint64_t)a.num_pages) page = 0;
+        if (k >= kRaw &&
+            !__all_sync(0xFFFFFFFFu, wait_bounded_inline(smem_u32(&bars.raw_empty[st]), (uint32_t)(k / kRaw - 1) & 1u, abort_flag, err, 601)))
+          break;
+        const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, valid));
+        const uint32_t bar = smem_u32(&bars.raw_full[st]);
+        if (lane == 0) mbar_arrive_tx(bar, n * G::kUnitBytes);
+        __syncwarp();
+        if (valid) {
+          const uint8_t* src = a.cache + ((page * a.kv_heads + job.kv_head) * a.units_page + (unit - p * a.units_page)) * G::kUnitBytes;
+          bulk_load(sm + G::kRawAt + st * G::kRawBytes + lane * G::kUnitStride, src, G::kUnitBytes, bar);
+        }
+        issued = k + 1;
+      }
+      // every copy lands before the CTA ends
+      volatile int no_abort = 0;
+      for (int k = max(0, issued - kRaw); k < issued; ++k)
+        wait_bounded_inline(smem_u32(&bars.raw_full[k % kRaw]), (uint32_t)(k / kRaw) & 1u, &no_abort, err, 602);
+    } else if (warp < 15) {
+      // ------------------------------------------------ operands from codes
+      const int d = tid - 352, w = d / 32;
+      bool ok = true;
+      for (int k = 0; k < 2 * job.total && ok; ++k) {
+        const int st = k % kRaw, buf = k % kBufs;
+        ok = __all_sync(0xFFFFFFFFu, wait_bounded_inline(smem_u32(&bars.raw_full[st]), (uint32_t)(k / kRaw) & 1u, abort_flag, err, 631));
+        if (ok && k >= kBufs)
+          ok = __all_sync(0xFFFFFFFFu, wait_bounded_inline(smem_u32(&bars.k_empty[buf]), (uint32_t)(k / kBufs - 1) & 1u, abort_flag, err, 632));
+        if (!ok) break;
+        const uint8_t* raw = smem + G::kRawAt + st * G::kRawBytes;
+        // scales and zeros as fp32, zeros for tokens outside the sequence: their bytes may be anything
+        if (d < kHalf) {
+          const int at = job.tile0 * kTok + k * kHalf + d;
+          uint2 mt = *reinterpret_cast<const uint2*>(raw + (d / 16) * G::kUnitStride + 16 * D + (d % 16) * 8);
+          if (at < job.lo || at >= job.len) mt = make_uint2(0u, 0u);
+          const float2 ksz = unpack2<false>(mt.x), vsz = unpack2<false>(mt.y);
+          uint8_t* meta = smem + G::kMeta + k % kMetas * G::kMetaBytes;
+          float* f = reinterpret_cast<float*>(meta) + d;
+          f[0] = ksz.x;
+          f[kHalf] = ksz.y;
+          f[2 * kHalf] = vsz.x;
+          f[3 * kHalf] = fmaf(8.f, vsz.x, vsz.y);
+          // the value scales of these 32 tokens are below 2^(that)
+          const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, mt.y & 0x7FFFu);
+          if (lane == 0) *reinterpret_cast<int*>(meta + 4 * kHalf * 4 + 4 * w) = (int)(most >> 10) - 14;
+        }
+        // keys: a word is eight channels of a token, one 16-byte chunk of its row.  A thread has one chunk of every
+        // kPass-th token, so that all its addresses are two bases and constants.
+        {
+          constexpr int kChunks = D / 8, kPass = kDqThreads / kChunks;
+          const int c = d % kChunks, tok = d / kChunks;
+          const uint8_t* src = raw + tok * (D / 2) + 4 * c;
+          const uint32_t dst = sm + G::kK + buf * G::kKStep + (c / 8) * (kHalf * 128) + tok * 128 + ((c % 8) ^ (tok % 8)) * 16;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const uint8_t* at = src + (t ^ s) * kQuads * 4;
-          if constexpr (kEach == 2) {
-            const uint2 v = *reinterpret_cast<const uint2*>(at);
-            x[t][0] = v.x;
-            x[t][1] = v.y;
-          } else {
-            x[t][0] = *reinterpret_cast<const uint32_t*>(at);
+          for (int i = 0; i < kHalf / kPass; ++i) {
+            const int t = i * kPass;  // a multiple of 8
+            const uint32_t x = *reinterpret_cast<const uint32_t*>(src + (t / 16) * G::kUnitStride + (t % 16) * (D / 2));
+            const uint32_t y = x >> 8;
+            sts128(dst + t * 128, x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u);
           }
         }
-        // channel g D / 8 + 4 (q0 + q) + e: rows of 128 bytes, their chunks swizzled by the channel's last three bits
-        const uint32_t dst = sm + G::kV + buf * G::kVStep + (g * (D / 8) + 4 * q0) * 128 + tc * 16;
-        const uint32_t swap = kEach == 1 ? 64u * (uint32_t)(q0 % 2) : 0u;
+        fence_async();
+        mbar_arrive(smem_u32(&bars.k_full[buf]));
+        if (k >= kBufs) {
+          ok = __all_sync(0xFFFFFFFFu, wait_bounded_inline(smem_u32(&bars.v_empty[buf]), (uint32_t)(k / kBufs - 1) & 1u, abort_flag, err, 633));
+          if (!ok) break;
+        }
+        // values: eight tokens of a channel are one chunk of its row.  Thread: eight tokens tc, channels [g D / 8, ...),
+        // a part of its quads; odd eights read their words pair by pair the other way round, so that the reads of
+        // eight lanes fall into different banks.
+        {
+          constexpr int kQuads = D / 32;               // quads of a group of D / 8 channels
+          constexpr int kEach = kQuads / 2;            // of a thread
+          const int tc = lane % 8, s = tc % 2, g = 4 * (w % 2) + lane / 8;
+          const int q0 = ((w / 2) ^ (kEach == 2 ? g % 2 : 0)) * kEach;  // two groups of a half-warp: different banks
+          const uint8_t* src = raw + (tc / 2) * G::kUnitStride + 8 * D + ((s * 8 + g) * 4 * kQuads + q0) * 4;
+          uint32_t x[4][kEach];
 #pragma unroll
-        for (int q = 0; q < kEach; ++q) {
-          uint32_t y[4];
+          for (int t = 0; t < 4; ++t) {
+            const uint8_t* at = src + (t ^ s) * kQuads * 4;
+            if constexpr (kEach == 2) {
+              const uint2 v = *reinterpret_cast<const uint2*>(at);
+              x[t][0] = v.x;
+              x[t][1] = v.y;
+            } else {
+              x[t][0] = *reinterpret_cast<const uint32_t*>(at);
+            }
+          }
+          // channel g D / 8 + 4 (q0 + q) + e: rows of 128 bytes, their chunks swizzled by the channel's last three bits
+          const uint32_t dst = sm + G::kV + buf * G::kVStep + (g * (D / 8) + 4 * q0) * 128 + tc * 16;
+          const uint32_t swap = kEach == 1 ? 64u * (uint32_t)(q0 % 2) : 0u;
 #pragma unroll
-          for (int t = 0; t < 4; ++t) y[t] = x[t][q] >> 8;
+          for (int q = 0; q < kEach; ++q) {
+            uint32_t y[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const bool v = e / 2 != 0;
-            sts128((dst ^ (uint32_t)((4 * q + e) % 8 * 16) ^ swap) + (4 * q + e) * 128, centred(e % 2, v ? y[0] : x[0][q]),
-                   centred(e % 2, v ? y[1] : x[1][q]), centred(e % 2, v ? y[2] : x[2][q]), centred(e % 2, v ? y[3] : x[3][q]));
+            for (int t = 0; t < 4; ++t) y[t] = x[t][q] >> 8;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const bool v = e / 2 != 0;
+              sts128((dst ^ (uint32_t)((4 * q + e) % 8 * 16) ^ swap) + (4 * q + e) * 128, centred(e % 2, v ? y[0] : x[0][q]),
+                     centred(e % 2, v ? y[1] : x[1][q]), centred(e % 2, v ? y[2] : x[2][q]), centred(e % 2, v ? y[3] : x[3][q]));
+            }
           }
         }
+        fence_async();
+        mbar_arrive(smem_u32(&bars.v_full[buf]));
+        mbar_arrive(smem_u32(&bars.raw_empty[st]));
       }
-      fence_async();
-      mbar_arrive(smem_u32(&bars.v_full[buf]));
-      mbar_arrive(smem_u32(&bars.raw_empty[st]));
     }
   }
   tc_fence_before();
@@ -692,6 +700,12 @@ cudaError_t launch(const Kv4AttnArgs& args, int min_rows, float* parts, int* err
   const void* fn = reinterpret_cast<const void*>(kv4_prefill_kernel<D, BF16>);
   cudaError_t e = set_smem_once(fn, Geo<D>::kSmem);
   if (e != cudaSuccess) return e;
+  // the softmax warps wait for the registers that the others leave: launched with fewer, they would wait for ever
+  static const bool enough = [fn] {
+    cudaFuncAttributes f = {};
+    return cudaFuncGetAttributes(&f, fn) == cudaSuccess && f.numRegs == kLaunchRegs;
+  }();
+  if (!enough) return cudaErrorLaunchOutOfResources;
   const Plan p = plan_of(args.T, args.B, args.max_q, args.heads, args.kv_heads);
   // a split has two tiles at least, as far as the page table tells: a CTA's start and end cost as much as those, and the
   // join is another launch

@@ -414,12 +414,14 @@ def _row_stride(name: str, t, inner: int) -> int:
     """Elements from one row (token) to the next; the `inner` elements of a row are dense."""
     if t.is_contiguous():
         return inner
-    dense = 1
-    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if size != 1 and stride != dense:
-            raise ValueError(f"{name}: heads and channels of a token must be dense")
-        dense *= size
-    return max(t.stride(0), inner) if t.shape[0] <= 1 else t.stride(0)
+    shape, strides = t.shape, t.stride()
+    if strides[-1] != 1 or (len(shape) == 3 and strides[1] != shape[2]):  # else dense, as it mostly is
+        dense = 1
+        for size, stride in zip(reversed(shape[1:]), reversed(strides[1:])):
+            if size != 1 and stride != dense:
+                raise ValueError(f"{name}: heads and channels of a token must be dense")
+            dense *= size
+    return max(strides[0], inner) if shape[0] <= 1 else strides[0]
 
 
 def _rmsnorm_args(name, x, weight, residual, res_out):
@@ -428,10 +430,13 @@ def _rmsnorm_args(name, x, weight, residual, res_out):
     if weight.shape != (K,) or (residual is not None and residual.shape != x.shape) or \
             (res_out is not None and res_out.shape != x.shape):
         raise ValueError(f"{name}: weight [K], residual and res_out [M, K] go with x [M, K]")
-    if residual is not None and res_out is None:
-        res_out = torch.empty((M, K), dtype=x.dtype, device=x.device)
     _need(name, x.dtype, weight, res_out)
-    rs = 0 if residual is None else _row_stride(name, residual, K)
+    if residual is None:
+        rs = 0
+    else:
+        rs = _row_stride(name, residual, K)
+        if res_out is None:
+            res_out = torch.empty((M, K), dtype=x.dtype, device=x.device)
     return M, K, dtype, res_out, _row_stride(name, x, K), rs
 
 
@@ -441,18 +446,21 @@ def w4a8_rmsnorm_quant(x, weight, residual=None, eps: float = 1e-6, res_out=None
     w4a8_gemm takes them; res_out (x + residual) is None without a residual.  `y`, when given, receives the
     normalized rows too.  res_out may be `x` or `residual` itself."""
     M, K, dtype, res_out, xs, rs = _rmsnorm_args("w4a8_rmsnorm_quant", x, weight, residual, res_out)
+    device = x.device
+    if xq is not None or s_tok is not None or y is not None:
+        _need("w4a8_rmsnorm_quant", torch.int8, xq)
+        _need("w4a8_rmsnorm_quant", torch.float32, s_tok)
+        _need("w4a8_rmsnorm_quant", x.dtype, y)
+        if (xq is not None and xq.shape != (M, K)) or (s_tok is not None and s_tok.shape != (M,)) or \
+                (y is not None and y.shape != (M, K)):
+            raise ValueError("w4a8_rmsnorm_quant: xq and y are [M, K], s_tok is [M]")
     if xq is None:
-        xq = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        xq = torch.empty((M, K), dtype=torch.int8, device=device)
     if s_tok is None:
-        s_tok = torch.empty((M,), dtype=torch.float32, device=x.device)
-    _need("w4a8_rmsnorm_quant", torch.int8, xq)
-    _need("w4a8_rmsnorm_quant", torch.float32, s_tok)
-    _need("w4a8_rmsnorm_quant", x.dtype, y)
-    if xq.shape != (M, K) or s_tok.shape != (M,) or (y is not None and y.shape != (M, K)):
-        raise ValueError("w4a8_rmsnorm_quant: xq and y are [M, K], s_tok is [M]")
+        s_tok = torch.empty(M, dtype=torch.float32, device=device)
     _check("w4a8_rmsnorm_quant", lib.w4a8_rmsnorm_quant(_ptr(x), _ptr(residual), _ptr(weight), _ptr(res_out), _ptr(y),
-                                                        _ptr(xq), _ptr(s_tok), M, K, xs, rs, eps, dtype,
-                                                        _raw_stream(stream, x.device)))
+                                                        xq.data_ptr(), s_tok.data_ptr(), M, K, xs, rs, eps, dtype,
+                                                        _raw_stream(stream, device)))
     return xq, s_tok, res_out
 
 
@@ -528,18 +536,21 @@ def kv4_append(cache, k, v, positions, slots, table, q=None, interleaved: bool =
 def kv4_gather(cache, slots, dtype=torch.float16, k=None, v=None, stream=None):
     """The keys and values [T, kv_heads, head_dim] that the cache holds at `slots`."""
     pages, kv_heads, dim, page = _kv4_shape("kv4_gather", cache)
-    T = slots.shape[0]
-    if k is None:
-        k = torch.empty((T, kv_heads, dim), dtype=dtype, device=cache.device)
-    if v is None:
-        v = torch.empty((T, kv_heads, dim), dtype=dtype, device=cache.device)
-    kind = _dtype16("kv4_gather", k, v)
+    shape = (slots.shape[0], kv_heads, dim)
+    device = cache.device
     _need("kv4_gather", torch.int64, slots)
-    _need("kv4_gather", k.dtype, k, v)
-    if k.shape != (T, kv_heads, dim) or v.shape != k.shape:
-        raise ValueError("kv4_gather: k and v are [T, kv_heads, head_dim]")
-    _check("kv4_gather", lib.kv4_gather(_ptr(cache), _ptr(slots), _ptr(k), _ptr(v), pages, T, kv_heads, dim, page,
-                                        kind, _raw_stream(stream, cache.device)))
+    given = k is not None or v is not None
+    if k is None:
+        k = torch.empty(shape, dtype=dtype, device=device)
+    if v is None:
+        v = torch.empty(shape, dtype=dtype, device=device)
+    kind = _dtype16("kv4_gather", k, v)
+    if given:
+        _need("kv4_gather", k.dtype, k, v)
+        if k.shape != shape or v.shape != shape:
+            raise ValueError("kv4_gather: k and v are [T, kv_heads, head_dim]")
+    _check("kv4_gather", lib.kv4_gather(cache.data_ptr(), slots.data_ptr(), k.data_ptr(), v.data_ptr(), pages, shape[0],
+                                        kv_heads, dim, page, kind, _raw_stream(stream, device)))
     return k, v
 
 

@@ -306,8 +306,9 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
         // the scales and zeros are there with the keys
         const int step = 2 * j + h;
         const uint8_t* meta = smem + G::kMeta + step % kMetas * G::kMetaBytes;
-        ok = __all_sync(0xFFFFFFFFu, wait_bounded_inline(smem_u32(&bars.k_full[step % kBufs]), step / kBufs & 1, abort_flag, err, 622)) &&
-             __all_sync(0xFFFFFFFFu, wait_bounded_inline(smem_u32(&bars.s_full[m][h]), j & 1, abort_flag, err, 621));
+        ok = __all_sync(0xFFFFFFFFu,
+                        wait_bounded_inline(smem_u32(&bars.s_full[m][h]), j & 1, abort_flag, err, 621) &&
+                            wait_bounded_inline(smem_u32(&bars.k_full[step % kBufs]), step / kBufs & 1, abort_flag, err, 622));
         if (!ok) break;
         tc_fence_after();
         uint32_t raw[4][16];

@@ -59,8 +59,8 @@ __device__ __forceinline__ uint2 codes8(const F2 (&t)[4], float step, float inv)
 
 // A CTA takes rows in turn and reads each once: a thread keeps t = h w of its V vectors in registers between the
 // reduction and the codes, and has the next row's vectors on the way meanwhile.  The CTA's threads cover the row's K / 8
-// vectors V times.  HBM bound: 8192 x 8192 with the residual moves 470 MB in 72 us, 6.5 TB/s; 4096 x 4096 takes 20.3 us
-// (5.8 TB/s), 8 rows 2.5 us.  7001 x 11016 in bf16 without residual takes 58 us (4.0 TB/s): three bytes an element leave
+// vectors V times.  HBM bound: 8192 x 8192 with the residual moves 470 MB in 72 us, 6.5 TB/s; 4096 x 4096 takes 19.7 us
+// (6.0 TB/s), 8 rows 2.5 us.  7001 x 11016 in bf16 without residual takes 58 us (4.0 TB/s): three bytes an element leave
 // the instructions in front, and a row of 1377 vectors fills eleven warps with a ragged fourth vector.
 template <bool BF16, bool RES, int V, int T, int CTAS>
 __global__ void __launch_bounds__(T, CTAS)

@@ -45,7 +45,8 @@ constexpr int kTok = 128;    // tokens of a tile
 constexpr int kHalf = 64;    // tokens of a raw slot, and of one step of the softmax
 constexpr int kBufs = 4;     // operand buffers of a step's keys, and of its values
 // Scales and zeros of a step stay until its weights are made.  A step's keys are made at the earliest when the values
-// of the one before it are, which is after the weights of five steps before: six buffers.
+// of the one before it are, which is after the weights of five steps before: six buffers.  They have full barriers of
+// their own: the keys' come round again when the products alone have read the keys, before a softmax warp need have looked.
 constexpr int kMetas = 6;
 constexpr int kRaw = 3;      // raw slots
 constexpr int kDqThreads = 128;
@@ -83,8 +84,8 @@ __device__ __forceinline__ void wait_loaded(uint32_t (&r)[16]) {
 }
 
 struct Bars {
-  uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[kBufs], k_empty[kBufs], v_full[kBufs], v_empty[kBufs], s_full[2][2], p_full[2][2],
-      o_done[2][2], q_full, done;
+  uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[kBufs], k_empty[kBufs], v_full[kBufs], v_empty[kBufs], meta_full[kMetas],
+      s_full[2][2], p_full[2][2], o_done[2][2], q_full, done;
 };
 
 // The products and commits are executed by the whole warp, with the same operands in every lane, and issued by
@@ -209,6 +210,7 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
       mbar_init(smem_u32(&bars.k_empty[i]), 2);
       mbar_init(smem_u32(&bars.v_empty[i]), 2);
     }
+    for (int i = 0; i < kMetas; ++i) mbar_init(smem_u32(&bars.meta_full[i]), kHalf);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&bars.s_full[i][0]), 1);
       mbar_init(smem_u32(&bars.s_full[i][1]), 1);
@@ -303,12 +305,11 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         const int j0 = (job.tile0 + j) * kTok + h * kHalf;
-        // the scales and zeros are there with the keys
         const int step = 2 * j + h;
         const uint8_t* meta = smem + G::kMeta + step % kMetas * G::kMetaBytes;
         ok = __all_sync(0xFFFFFFFFu,
                         wait_bounded_inline(smem_u32(&bars.s_full[m][h]), j & 1, abort_flag, err, 621) &&
-                            wait_bounded_inline(smem_u32(&bars.k_full[step % kBufs]), step / kBufs & 1, abort_flag, err, 622));
+                            wait_bounded_inline(smem_u32(&bars.meta_full[step % kMetas]), step / kMetas & 1, abort_flag, err, 622));
         if (!ok) break;
         tc_fence_after();
         uint32_t raw[4][16];
@@ -577,6 +578,7 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
           // the value scales of these 32 tokens are below 2^(that)
           const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, mt.y & 0x7FFFu);
           if (lane == 0) *reinterpret_cast<int*>(meta + 4 * kHalf * 4 + 4 * w) = (int)(most >> 10) - 14;
+          mbar_arrive(smem_u32(&bars.meta_full[k % kMetas]));
         }
         // keys: a word is eight channels of a token, one 16-byte chunk of its row.  A thread has one chunk of every
         // kPass-th token, so that all its addresses are two bases and constants.

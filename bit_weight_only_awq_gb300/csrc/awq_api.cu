@@ -569,7 +569,8 @@ awq_status kv4_gather(const void* cache, const int64_t* slots, uint16_t* k, uint
 
 static bool kv4_attention_shape_ok(int64_t T, int64_t B, int32_t max_q, int32_t heads, int32_t kv_heads, int32_t dim) {
   return T >= 0 && T <= INT32_MAX && B >= 0 && B <= kKv4MaxSeqs && max_q >= 1 && heads >= 1 && heads <= 1024 &&
-         kv_heads >= 1 && heads % kv_heads == 0 && (dim == 64 || dim == 128);
+         kv_heads >= 1 && heads % kv_heads == 0 && (dim == 64 || dim == 128) &&
+         (max_q < T ? max_q : T) * (heads / kv_heads) <= kKv4MaxRows;
 }
 
 size_t kv4_attention_workspace_bytes(int64_t T, int64_t B, int32_t max_q, int32_t heads, int32_t kv_heads,

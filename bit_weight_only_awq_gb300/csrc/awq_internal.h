@@ -143,6 +143,7 @@ cudaError_t launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const ui
 // ---- 4-bit paged cache (kv4_cache.cu, kv4_attention.cu).  Layout of a unit (16 tokens of one head): include/awq.h.
 constexpr int kKv4Unit = 16;
 constexpr int kKv4MaxSeqs = 4096;
+constexpr int64_t kKv4MaxRows = 1 << 30;  // query rows of a cache head and sequence, which are counted in 32 bits
 __host__ __device__ constexpr int kv4_unit_bytes(int dim) { return 16 * dim + 128; }
 // Byte offsets inside a unit: a token's key row, the 16-bit half of value channels 4c..4c+3, the token's four fp16.
 __host__ __device__ constexpr int kv4_key_offset(int dim, int token) { return token * (dim / 2); }

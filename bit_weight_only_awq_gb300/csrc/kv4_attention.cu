@@ -309,9 +309,10 @@ kv4_attention_kernel(const Args a, float* warp_parts, float* cta_parts, int* cou
         at += (long long)use.s.tiles * use.s.groups;
         use.s = seq_of<NT>(a, kept, ++use.b);
       }
-      const int rest = (int)(u0 - at);
-      use.group = rest / use.s.tiles;
-      use.tile = rest - use.group * use.s.tiles;
+      // a sequence may have 2^31 tiles and more; divided in 32 bits where that is enough
+      const unsigned long long rest = (unsigned long long)(u0 - at), tiles = (unsigned)use.s.tiles;
+      use.group = (rest >> 32) == 0 ? (int)((uint32_t)rest / (uint32_t)tiles) : (int)(rest / tiles);
+      use.tile = (int)(rest - use.group * tiles);
     }
     Cursor next = use;  // the tile to be copied next
     const int count = (int)(u1 - u0);
@@ -805,7 +806,6 @@ cudaError_t launch(const Kv4AttnArgs& args, int max_rows, void* ws, int* err, cu
 // tokens, 8 cache heads of 128 channels, here / there: 16 rows 34 / 81, 32 rows 52 / 82, 64 rows 90 / 83; at 16 x 4096,
 // 64 channels: 32 rows 37 / 71, 64 rows 61 / 71.
 int rows_here(int dim) { return dim == 128 ? 48 : 64; }
-constexpr int64_t kPrefillMaxRows = 1 << 20;  // of the other's grid: 4096 row blocks, 16 shares of the cache
 
 // What a call takes: this kernel, with eight or sixteen columns, the other, or each for its sequences.  Sequences of
 // different length (T < B max_q) may be of both kinds: 31 single tokens and 512 of a prompt, 8192 cached each, take 251 us
@@ -817,7 +817,7 @@ struct Route {
 Route route_of(int64_t T, int64_t B, int max_q, int heads, int kv_heads, int dim) {
   const int64_t per = heads / kv_heads, rows = (max_q < T ? max_q : T) * per;
   Route r;
-  r.there = rows > rows_here(dim) && rows <= kPrefillMaxRows;
+  r.there = rows > rows_here(dim);
   r.here = !r.there || (T < B * max_q && per <= rows_here(dim));
   r.nt = (r.there ? per : rows) <= 8 ? 1 : 2;
   return r;

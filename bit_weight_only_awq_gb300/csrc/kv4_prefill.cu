@@ -190,10 +190,11 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid / 32, 0), lane = tid % 32;
   // heads of a row block first, then the row blocks from the one that sees the most tokens down: CTAs start in the
-  // order of their work, and the short ones fill what the long ones leave
-  const int split = blockIdx.y % splits, row_blocks = gridDim.y / splits;
-  const int row_block = row_blocks - 1 - blockIdx.y / splits;
-  const Job job = job_of(a, row_block, blockIdx.x, blockIdx.z, split, splits);
+  // order of their work, and the short ones fill what the long ones leave.  All on the grid's x, the one without a limit.
+  const int place = blockIdx.x / a.kv_heads, kv_head = blockIdx.x - place * a.kv_heads;
+  const int split = place % splits, row_blocks = gridDim.x / a.kv_heads / splits;
+  const int row_block = row_blocks - 1 - place / splits;
+  const Job job = job_of(a, row_block, kv_head, blockIdx.y, split, splits);
   if (job.row0 >= job.n * a.per) return;
   uint8_t* smem = align_smem_1024(smem_raw);
   const uint32_t sm = smem_u32(smem);
@@ -428,7 +429,7 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
     const float unit = __uint_as_float((uint32_t)(127 + vexp - 5) << 23);
     const int64_t row = token * a.heads + head;
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    float* part = parts + ((((long long)blockIdx.z * a.kv_heads + blockIdx.x) * row_blocks + row_block) * splits + split) * part_floats(D);
+    float* part = parts + ((((long long)blockIdx.y * a.kv_heads + kv_head) * row_blocks + row_block) * splits + split) * part_floats(D);
     const int pr = 128 * m + r;
     if (ok) {
 #pragma unroll 1
@@ -533,7 +534,7 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
         const int unit = job.tile0 * (kTok / kKv4Unit) + k * 4 + lane;
         const bool valid = lane < 4 && unit * kKv4Unit < job.len && (unit + 1) * kKv4Unit > job.lo;
         const int p = a.page_magic ? (int)__umulhi((uint32_t)unit, a.page_magic) : unit;
-        int64_t page = valid ? a.block_table[blockIdx.z * a.table_stride + p] : 0;
+        int64_t page = valid ? a.block_table[blockIdx.y * a.table_stride + p] : 0;
         if ((uint64_t)page >= (uint64_t)a.num_pages) page = 0;
         if (k >= kRaw &&
             !__all_sync(0xFFFFFFFFu, wait_bounded_inline(smem_u32(&bars.raw_empty[st]), (uint32_t)(k / kRaw - 1) & 1u, abort_flag, err, 601)))
@@ -719,8 +720,9 @@ cudaError_t launch(const Kv4AttnArgs& args, int min_rows, float* parts, int* err
   const int splits = (int)(p.splits < tiles / 2 ? p.splits : tiles / 2 > 1 ? tiles / 2 : 1);
   Args a = make_args(args);
   a.rows = min_rows;
-  kv4_prefill_kernel<D, BF16><<<dim3((unsigned)a.kv_heads, (unsigned)(p.blocks * splits), (unsigned)a.B), kThreads, Geo<D>::kSmem,
-                                s>>>(a, splits, parts, err);
+  const int64_t ctas = (int64_t)a.kv_heads * p.blocks * splits;
+  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  kv4_prefill_kernel<D, BF16><<<dim3((unsigned)ctas, (unsigned)a.B), kThreads, Geo<D>::kSmem, s>>>(a, splits, parts, err);
   e = cudaGetLastError();
   if (e != cudaSuccess || splits == 1) return e;
   cudaLaunchConfig_t cfg = {};

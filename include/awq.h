@@ -485,7 +485,7 @@ awq_status kv4_gather(const void *cache, const int64_t *slots, uint16_t *k, uint
  * Lengths, q_start and pages are read on the device only, so a captured graph follows them; lengths
  * beyond max_pages * page_size and q_start beyond T are clamped, page numbers outside the cache read
  * page 0: memory-safe, with unspecified results.  heads % kv_heads == 0, B <= 4096, finite scale,
- * 0 <= window, max_pages * page_size <= 2^30.
+ * 0 <= window, max_pages * page_size <= 2^30, min(T, max_q) * heads / kv_heads <= 2^30.
  *
  * The queries enter the tensor cores as fp16 after a power-of-two scaling of each row (exact for fp16 and
  * bf16 down to 2^-24 of the row's largest), the probabilities times the value's scale as fp16, and the

@@ -1,0 +1,76 @@
+"""Attention over the 4-bit cache where a row's neighbours, the cache's signs and the arguments' limits could reach into
+its result.  Bounds: those of test_gpu_kv4_attention, with the largest value taken over the compared rows alone.
+"""
+
+import numpy as np
+import pytest
+
+from oracle import block
+from tests.test_gpu_kv4_attention import Problem, awq  # noqa: F401  (awq is a fixture)
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+def meta_of(p):
+    """float16 [pages, kv_heads, page_size, 4] over the cache: key scale, key zero, value scale, value zero."""
+    meta = p.cache[..., 16 * p.dim:].view(np.float16)
+    return meta.reshape(*p.cache.shape[:2], p.page, 4)
+
+
+def put_meta(p, meta):
+    p.cache[..., 16 * p.dim:] = np.ascontiguousarray(meta.reshape(*p.cache.shape[:3], 64)).view(np.uint8)
+
+
+def check_rows(awq, p, rows, window=0, cache=None):  # noqa: F811
+    """The rows (a boolean for each query token) against float64; `cache` has other values where they do not see."""
+    out, lse = p.run(awq, window)
+    cache = p.cache if cache is None else cache
+    want, want_lse, mag, reach = block.kv4_attention(p.q, cache, p.table, p.lens, p.start, p.scale, window)
+    got, got_lse = out.float().cpu().numpy()[rows], lse.cpu().numpy()[rows]
+    want, want_lse, mag, reach = want[rows], want_lse[rows], mag[rows], reach[rows]
+    assert np.all(np.isfinite(want))
+    delta = reach * (8 + p.dim / 8) * 2.0 ** -23
+    half_ulp = 2.0 ** -8 if p.bf16 else 2.0 ** -11
+    bound = mag * (2 * delta[..., None] + 2.0 ** -11 + 2.0 ** -17) + half_ulp * np.abs(want) + 2.0 ** -24 * (1 + mag.max())
+    worst = np.max(np.abs(got - want) / bound)
+    assert worst <= 1.0, worst
+    empty = np.isneginf(want_lse)
+    assert np.array_equal(np.isneginf(got_lse), empty)
+    assert np.all(np.abs(got_lse - want_lse)[~empty] <= (delta + 2.0 ** -17 + 2.0 ** -22 * np.abs(want_lse))[~empty])
+    assert awq.awq_last_device_error() == 0
+
+
+def test_places_beyond_32_bits(awq):  # noqa: F811
+    """A prompt whose column blocks times tiles of the cache are more than 2^31, and its rows more than 2^20; a window
+    keeps the work small.  Rows all over it against float64 on the pages that they see."""
+    heads, dim, page, T, before, window = 1, 64, 1024, 1_500_001, 37, 100
+    length = T + before
+    assert -(-T // 16) * -(-length // 64) > 2 ** 31
+    pages = -(-length // page)
+    gen = torch.Generator(device="cuda").manual_seed(36)
+    cache = torch.randint(0, 256, (pages, 1, page // 16, 16 * dim + 128), generator=gen, device="cuda", dtype=torch.uint8)
+    meta = cache[..., 16 * dim:].view(torch.float16).unflatten(-1, (16, 2, 2))
+    sigma = torch.exp(0.3 * torch.randn(meta.shape[:-1], generator=gen, device="cuda"))
+    meta[..., 0] = (sigma / 4.6).half()
+    meta[..., 1] = (-7.5 * sigma / 4.6).half()
+    table = torch.randperm(pages, generator=gen, device="cuda").int()[None]
+    q = (2 * torch.randn(T, heads, dim, generator=gen, device="cuda")).half()
+    lens, start = torch.tensor([length], dtype=torch.int32).cuda(), torch.tensor([0, T], dtype=torch.int32).cuda()
+    lse = torch.full((T, heads), 5.0, device="cuda")
+    out = torch.full_like(q, float("nan"))
+    awq.kv4_attention(q, cache, table, lens, q_start=start, max_q=T, window=window, out=out, lse=lse)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    rng = np.random.default_rng(37)
+    for row in [0, 1, 62, 63, 255, 256, T - 1, T - 2, T - 256, 1 << 20, (1 << 20) - 1, *rng.integers(0, T, 60)]:
+        pos = before + int(row)
+        first = max(0, pos - window + 1) // page
+        need = table[0, first:pos // page + 1].long()
+        args = (q[row:row + 1].float().cpu().numpy(), cache[need].cpu().numpy(), np.arange(len(need))[None],
+                np.array([pos + 1 - first * page]), np.array([0, 1]), dim ** -0.5, window)
+        want, want_lse, mag, reach = block.kv4_attention(*args)
+        delta = reach * (8 + dim / 8) * 2.0 ** -23
+        bound = mag * (2 * delta[..., None] + 2.0 ** -11 + 2.0 ** -17) + 2.0 ** -11 * np.abs(want) + 2.0 ** -24 * (1 + mag.max())
+        assert np.all(np.abs(out[row:row + 1].float().cpu().numpy() - want) <= bound), row
+        assert np.all(np.abs(lse[row:row + 1].cpu().numpy() - want_lse) <= delta + 2.0 ** -17 + 2.0 ** -22 * np.abs(want_lse))
+    assert awq.awq_last_device_error() == 0

@@ -604,6 +604,10 @@ def kv4_attention(q, cache, block_table, kv_len, q_start=None, max_q: int = 1, s
     table_stride, inner = block_table.stride()
     if block_table.dtype is not torch.int32 or not block_table.is_cuda or (inner != 1 and max_pages > 1):
         raise TypeError("kv4_attention: block_table is int32 with dense rows, on a GPU")
+    if B <= 1:  # no second row: the stride says nothing
+        table_stride = max_pages
+    elif table_stride < max_pages:
+        raise ValueError("kv4_attention: the rows of block_table overlap (a table made with expand needs a copy)")
     if out is None:
         out = torch.empty(shape, dtype=q.dtype, device=q.device)
     elif out.shape != shape or not out.is_contiguous():
@@ -620,7 +624,7 @@ def kv4_attention(q, cache, block_table, kv_len, q_start=None, max_q: int = 1, s
         workspace = _kv4_workspace(handle, device, kv4_attention_workspace_bytes(T, B, max_q, heads, kv_heads, dim), stream)
     _check("kv4_attention", lib.kv4_attention(
         q.data_ptr(), _row_stride("kv4_attention", q, heads * dim), cache.data_ptr(), block_table.data_ptr(),
-        table_stride if table_stride > max_pages else max_pages, kv_len.data_ptr(), _ptr(q_start), out.data_ptr(),
+        table_stride, kv_len.data_ptr(), _ptr(q_start), out.data_ptr(),
         _ptr(lse), T, B, max_q, heads, kv_heads, dim, pages, page, max_pages, scale, window, dtype,
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle))
     return out

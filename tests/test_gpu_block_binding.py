@@ -1,0 +1,28 @@
+"""What the Python binding of the block operators makes of its arguments: layouts, defaults, workspaces."""
+
+import pytest
+
+from tests.test_gpu_kv4_attention import Problem, awq  # noqa: F401  (awq is a fixture)
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+def operands(p):
+    return (torch.from_numpy(p.q).cuda().half(), *(torch.from_numpy(a).cuda() for a in (p.cache, p.table, p.lens)))
+
+
+def test_tables_whose_rows_overlap_are_refused(awq):  # noqa: F811
+    """Read with another stride, they would name what lies behind them as pages."""
+    p = Problem([150], [1], 4, 2, 64, 16, seed=51)
+    q, cache, table, lens = operands(p)
+    want = awq.kv4_attention(q, cache, table, lens)
+    q3, lens3, width = q.expand(3, -1, -1).contiguous(), lens.expand(3).contiguous(), table.shape[1]
+    for bad in (table.expand(3, -1), table.flatten().as_strided((3, width - 2), (1, 1))):
+        with pytest.raises(ValueError, match="block_table"):
+            awq.kv4_attention(q3, cache, bad, lens3)
+    got = awq.kv4_attention(q3, cache, table.expand(3, -1).contiguous(), lens3)
+    assert torch.equal(got, want.expand(3, -1, -1))
+    # the stride of a single row has no meaning
+    assert torch.equal(awq.kv4_attention(q, cache, table.flatten().as_strided((1, width), (0, 1)), lens), want)
+    assert torch.equal(awq.kv4_attention(q, cache, table[:, :width - 1], lens), want)

@@ -605,6 +605,8 @@ awq_status kv4_attention(const uint16_t* q, int64_t q_stride, const void* cache,
   if (st != AWQ_OK) return st;
   int* err = device_error_ptr();
   if (!err) return AWQ_ECUDA;
+  // one that no sequence can outgrow is none: the kernels' positions less a window stay within 32 bits
+  if (window >= (int64_t)max_pages * page_size) window = 0;
   const Kv4AttnArgs a{q,     q_stride, static_cast<const uint8_t*>(cache), block_table, table_stride, kv_len,
                       q_start, out,    lse,                                T,           (int)B,       max_q,
                       heads, kv_heads, num_pages,                          page_size,   max_pages,    scale,

@@ -74,3 +74,14 @@ def test_places_beyond_32_bits(awq):  # noqa: F811
         assert np.all(np.abs(out[row:row + 1].float().cpu().numpy() - want) <= bound), row
         assert np.all(np.abs(lse[row:row + 1].cpu().numpy() - want_lse) <= delta + 2.0 ** -17 + 2.0 ** -22 * np.abs(want_lse))
     assert awq.awq_last_device_error() == 0
+
+
+@pytest.mark.parametrize("lens,news,heads,kv_heads,dim", [([5, 40], [9, 3], 2, 1, 64), ([60], [140], 8, 2, 128), ([3], [9], 8, 2, 128)])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 4, 1 << 30])
+def test_windows_up_to_the_largest_integer(awq, lens, news, heads, kv_heads, dim, window):  # noqa: F811
+    """A window wider than any sequence hides nothing, also where there are more queries than tokens."""
+    p = Problem(lens, news, heads, kv_heads, dim, 16, seed=31)
+    out, lse = p.run(awq, window)
+    want, want_lse = p.run(awq, 0)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    p.check(awq, window=window)

@@ -492,7 +492,7 @@ kv4_attention_kernel(const Args a, float* warp_parts, float* cta_parts, int* cou
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const float2 key = unpack2<false>(meta[u][r].x);
-          vtop = __vmaxu2(vtop, meta[u][r].y);
+          vtop = max(vtop, meta[u][r].y & 0x7FFFu);  // without its sign: a cache may hold scales of either
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -516,7 +516,7 @@ kv4_attention_kernel(const Args a, float* warp_parts, float* cta_parts, int* cou
       }
 
       // ---- running maximum; the largest value scale, rounded up to a power of two
-      vtop = __reduce_max_sync(0xFFFFFFFFu, vtop & 0x7FFFu);
+      vtop = __reduce_max_sync(0xFFFFFFFFu, vtop);
       const int ve = max(vexp, (int)(vtop >> 10) - 14);
       bool grown = ve != vexp;
       float keep[NT][2];

@@ -85,3 +85,20 @@ def test_windows_up_to_the_largest_integer(awq, lens, news, heads, kv_heads, dim
     want, want_lse = p.run(awq, 0)
     assert torch.equal(out, want) and torch.equal(lse, want_lse)
     p.check(awq, window=window)
+
+
+@pytest.mark.parametrize("new", [1, 3, 12, 70])
+@pytest.mark.parametrize("small", [-0.001, -8.0])
+def test_scales_of_either_sign(awq, new, small):  # noqa: F811
+    """Scales as a cache of the caller's own may have them: every second eight tokens have negative ones, small or large."""
+    p = Problem([200, 90], [new, new], 8, 2, 128, 64, seed=32, q_scale=0.2)
+    meta = meta_of(p).copy()
+    odd = np.arange(p.page) // 8 % 2 == 1
+    for at, scale in ((0, 0.3), (2, 8.0)):
+        meta[..., at] = np.where(np.isnan(meta[..., at]), meta[..., at], np.float16(scale))
+        meta[:, :, odd, at] *= np.float16(small / 8.0)
+        meta[..., at + 1] = np.where(np.isinf(meta[..., at + 1]), meta[..., at + 1], meta[..., at] * np.float16(-7.0))
+    put_meta(p, meta)
+    assert (meta[..., 2] < 0).any() and (meta[..., 2] > 0).any()
+    p.check(awq)
+    p.check(awq, window=33)

@@ -361,7 +361,10 @@ kv4_attention_kernel(const Args a, float* warp_parts, float* cta_parts, int* cou
     float qk[NT][2], qr[NT][2];    // per column: the score's factor (base 2), and sum(q) over it
     int pos[NT][2];                // the last token it sees
     float m[NT][2], l[NT][2], z[NT][2], o[NT][2 * kWords][4];
-    int vexp = 0;                  // probabilities enter fp16 as p sv 2^(13 - vexp)
+    // Per column 13 - e, 2^e above the value scales it has seen: weights enter fp16 as p sv 2^(13 - e), and l, z and o are
+    // in that unit, so a token hidden from a column takes no bits from its weights.  No column's e is below vexp.
+    float lift[NT][2];
+    int vexp = 0;
     int seg0 = 0;                  // the first tile of this warp in the current head
     int kv_head = 0, col0 = 0;
 
@@ -432,6 +435,7 @@ kv4_attention_kernel(const Args a, float* warp_parts, float* cta_parts, int* cou
             pos[n][c] = i < use.s.n ? use.s.len - use.s.n + i : -1;
             m[n][c] = -INFINITY;
             l[n][c] = z[n][c] = 0.f;
+            lift[n][c] = 13.f + 16.f;
           }
 #pragma unroll
           for (int i = 0; i < 2 * kWords; ++i)
@@ -517,8 +521,8 @@ kv4_attention_kernel(const Args a, float* warp_parts, float* cta_parts, int* cou
 
       // ---- running maximum; the largest value scale, rounded up to a power of two
       vtop = __reduce_max_sync(0xFFFFFFFFu, vtop);
-      const int ve = max(vexp, (int)(vtop >> 10) - 14);
-      bool grown = ve != vexp;
+      const int ve = (int)(vtop >> 10) - 14;
+      bool grown = ve > vexp;
       float keep[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -533,31 +537,53 @@ kv4_attention_kernel(const Args a, float* warp_parts, float* cta_parts, int* cou
           m[n][c] = top;
         }
       if (__any_sync(0xFFFFFFFFu, grown)) {
-        const float shrink = __uint_as_float((uint32_t)(127 + vexp - ve) << 23);
-        vexp = ve;
+        int most[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) most[n][0] = most[n][1] = ve;
+        if (__builtin_expect(edge && use.s.n > 1 && ve > vexp, 0)) {
+          // columns of different tokens see different ones of this tile (what no column sees has scale 0); two in a word
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            uint32_t own = 0;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                const uint32_t scale = meta[u][r].y & 0x7FFFu;
+                own = __vmaxu2(own, (s[n][u][2 * r] == -INFINITY ? 0u : scale) | (s[n][u][2 * r + 1] == -INFINITY ? 0u : scale << 16));
+              }
+            own = __vmaxu2(own, __shfl_xor_sync(0xFFFFFFFFu, own, 4));
+            own = __vmaxu2(own, __shfl_xor_sync(0xFFFFFFFFu, own, 8));
+            own = __vmaxu2(own, __shfl_xor_sync(0xFFFFFFFFu, own, 16));
+            most[n][0] = (int)(own >> 10 & 31u) - 14;
+            most[n][1] = (int)(own >> 26) - 14;
+          }
+        } else {
+          vexp = max(vexp, ve);
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const float f = m[n][c] == -INFINITY ? 1.f : ex2((keep[n][c] - m[n][c]) * qk[n][c]);
+            const float to = fminf(lift[n][c], (float)(13 - most[n][c]));
+            const float f = m[n][c] == -INFINITY ? 1.f : ex2(fmaf(keep[n][c] - m[n][c], qk[n][c], to - lift[n][c]));
+            lift[n][c] = to;
             l[n][c] *= f;
             z[n][c] *= f;
 #pragma unroll
             for (int i = 0; i < 2 * kWords; ++i) {
-              o[n][i][c] *= f * shrink;
-              o[n][i][2 + c] *= f * shrink;
+              o[n][i][c] *= f;
+              o[n][i][2 + c] *= f;
             }
           }
       }
 
       // ---- probabilities, and their products with the values' scales as the B operand [token][column]
-      const float vup = __uint_as_float((uint32_t)(127 + 13 - vexp) << 23);
-      const float middle = __uint_as_float((uint32_t)(127 + vexp - 13) << 23) * -8.f;
       float base[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) base[n][c] = m[n][c] == -INFINITY ? 0.f : -m[n][c] * qk[n][c];
+        for (int c = 0; c < 2; ++c) base[n][c] = m[n][c] == -INFINITY ? lift[n][c] : fmaf(-m[n][c], qk[n][c], lift[n][c]);
       uint32_t pf[NT][4][2];
       auto weigh = [&](auto hides) {
 #pragma unroll
@@ -565,7 +591,7 @@ kv4_attention_kernel(const Args a, float* warp_parts, float* cta_parts, int* cou
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             const float2 val = unpack2<false>(meta[u][r].y);
-            const float w = val.x * vup, zero = fmaf(8.f, val.x, val.y);
+            const float zero = fmaf(8.f, val.x, val.y);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               float p[2];
@@ -576,12 +602,12 @@ kv4_attention_kernel(const Args a, float* warp_parts, float* cta_parts, int* cou
                 const bool hidden = decltype(hides)::value && v == -INFINITY;
                 l[n][c] += e;
                 z[n][c] = fmaf(e, hidden ? 0.f : zero, z[n][c]);
-                p[c] = e * (hidden ? 0.f : w);
+                p[c] = e * (hidden ? 0.f : val.x);
               }
               const uint32_t rounded = pack2<false>(p[0], p[1]);
               const float2 back8 = unpack2<false>(rounded);
-              z[n][0] = fmaf(back8.x, middle, z[n][0]);
-              z[n][1] = fmaf(back8.y, middle, z[n][1]);
+              z[n][0] = fmaf(back8.x, -8.f, z[n][0]);
+              z[n][1] = fmaf(back8.y, -8.f, z[n][1]);
               pf[n][u][r] = transpose8x8(rounded);
             }
           }
@@ -619,7 +645,7 @@ kv4_attention_kernel(const Args a, float* warp_parts, float* cta_parts, int* cou
 
       if (last) {
         const bool whole = seg0 == 0 && was.tile + 1 == was.s.tiles;
-        const float back = __uint_as_float((uint32_t)(127 + vexp - 13) << 23) * 16777216.f;
+        constexpr float kBack = 16777216.f;  // codes stood for u 2^-24, or 16 u 2^-24
         float* part = nullptr;
         if (!whole) {
           // the last partial of the range goes where the ring was, an earlier one to global memory
@@ -641,6 +667,7 @@ kv4_attention_kernel(const Args a, float* warp_parts, float* cta_parts, int* cou
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const float ls = col_sum(l[n][c]), zs = col_sum(z[n][c]);
+            const float unit = __uint_as_float((uint32_t)(127 - (int)lift[n][c]) << 23);
             const int col = 8 * n + 2 * t + c;
             // this lane's channels are [g D / 8, (g + 1) D / 8)
             if (whole) {
@@ -653,22 +680,23 @@ kv4_attention_kernel(const Args a, float* warp_parts, float* cta_parts, int* cou
                 uint32_t w[2 * kWords];
 #pragma unroll
                 for (int i = 0; i < 2 * kWords; ++i)
-                  w[i] = pack2<BF16>((o[n][i][c] * back + zs) * inv, (o[n][i][2 + c] * (back * 0.0625f) + zs) * inv);
+                  w[i] = pack2<BF16>((o[n][i][c] * kBack + zs) * inv, (o[n][i][2 + c] * (kBack * 0.0625f) + zs) * inv);
 #pragma unroll
                 for (int i = 0; i < kWords / 2; ++i)
                   reinterpret_cast<uint4*>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-                if (a.lse && g == 0) a.lse[row] = ls == 0.f ? -INFINITY : (m[n][c] * qk[n][c] + log2f(ls)) * kLn2;
+                if (a.lse && g == 0)
+                  a.lse[row] = ls == 0.f ? -INFINITY : (m[n][c] * qk[n][c] + log2f(ls * unit)) * kLn2;
               }
             } else {
               float* dst = part + col * D + g * (D / 8);
 #pragma unroll
               for (int i = 0; i < kWords; ++i)
                 reinterpret_cast<float4*>(dst)[i] =
-                    make_float4(o[n][2 * i][c] * back + zs, o[n][2 * i][2 + c] * (back * 0.0625f) + zs,
-                                o[n][2 * i + 1][c] * back + zs, o[n][2 * i + 1][2 + c] * (back * 0.0625f) + zs);
+                    make_float4((o[n][2 * i][c] * kBack + zs) * unit, (o[n][2 * i][2 + c] * (kBack * 0.0625f) + zs) * unit,
+                                (o[n][2 * i + 1][c] * kBack + zs) * unit, (o[n][2 * i + 1][2 + c] * (kBack * 0.0625f) + zs) * unit);
               if (g == 0) {
                 part[kCols * D + col] = m[n][c] * qk[n][c];
-                part[kCols * D + kCols + col] = ls;
+                part[kCols * D + kCols + col] = ls * unit;
               }
             }
           }

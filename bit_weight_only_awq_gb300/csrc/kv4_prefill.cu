@@ -332,14 +332,21 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
           t[2 * q + 1] = fma2(F2(s4.z, s4.w), F2(__uint_as_float(x[2]), __uint_as_float(x[3])), mul2(F2(z4.z, z4.w), qr2));
         }
         const bool edge = j0 + kHalf > first_pos + 1 || (a.window > 0 && j0 < last_pos + 1 - a.window) || j0 < job.lo;
+        int most = max(ve2.x, ve2.y);
         if (edge) {
+          // a token hidden from this row takes no bits from its weights: the largest scale of those it sees
           const int from = a.window > 0 ? pos - a.window + 1 : 0;
+          float seen = 0.f;
 #pragma unroll
           for (int q = 0; q < 32; ++q) {
             const float2 v = t[q].get();
             const int at = j0 + 2 * q;
-            t[q] = F2(at > pos || at < from ? -INFINITY : v.x, at + 1 > pos || at + 1 < from ? -INFINITY : v.y);
+            const bool no0 = at > pos || at < from, no1 = at + 1 > pos || at + 1 < from;
+            t[q] = F2(no0 ? -INFINITY : v.x, no1 ? -INFINITY : v.y);
+            const float2 s2 = reinterpret_cast<const float2*>(vs)[q];
+            seen = fmaxf(seen, fmaxf(no0 ? 0.f : fabsf(s2.x), no1 ? 0.f : fabsf(s2.y)));
           }
+          most = min((int)(__float_as_uint(seen) >> 23) - 126, 17);  // below 2^most; infinity as in the scales' exponents
         }
         float highs[8] = {top, top, top, top, top, top, top, top};
 #pragma unroll
@@ -352,7 +359,7 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
 #pragma unroll
           for (int k = 0; k < q; ++k) highs[k] = fmaxf(highs[k], highs[k + q]);
         const float high = highs[0];
-        const int ve = max(vexp, max(ve2.x, ve2.y));
+        const int ve = max(vexp, most);
         const bool grown = ve != vexp || (high > top && !((high - top) * qk <= kGrow));
         if (__any_sync(0xFFFFFFFFu, grown)) {
           const float f = (high > top ? ex2((top - high) * qk) : 1.f) * __uint_as_float((uint32_t)(127 + vexp - ve) << 23);

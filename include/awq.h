@@ -491,7 +491,7 @@ awq_status kv4_gather(const void *cache, const int64_t *slots, uint16_t *k, uint
  * bf16 down to 2^-24 of the row's largest), the probabilities times the value's scale as fp16, and the
  * codes as they are, all with fp32 sums; the result does not depend on timing or on other work on the GPU.
  * In fp16 the products of probability (1 for a row's largest) and value scale are held to 2^-30 of the
- * sequence's largest value scale of that head: what is smaller than that counts as nothing.
+ * largest value scale that the query sees of that head: what is smaller than that counts as nothing.
  *
  * Workspace: kv4_attention_workspace_bytes(), same contract as awq_gemv's (zero-filled once, each call
  * leaves its counters at zero, calls that may run concurrently need separate ones).

@@ -102,3 +102,33 @@ def test_scales_of_either_sign(awq, new, small):  # noqa: F811
     assert (meta[..., 2] < 0).any() and (meta[..., 2] > 0).any()
     p.check(awq)
     p.check(awq, window=33)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("heads", [2, 6, 16])
+@pytest.mark.parametrize("new", [2, 5, 120])
+@pytest.mark.parametrize("scale", [np.nan, np.inf, -np.inf, 65504.0])
+def test_a_hidden_scale_takes_no_bits_from_a_row(awq, new, heads, scale, bf16):  # noqa: F811
+    """Value scales near 0.003 beside one that is not finite, or the largest there is: rows that do not see it are as
+    exact as without it, whether it lies after them or has left their window."""
+    p = Problem([200, 150], [new, new], heads, 2, 64, 16, bf16=bf16, seed=33, q_scale=0.5)
+    meta = meta_of(p).copy()
+    meta[..., 2:] = np.where(np.isfinite(meta[..., 2:]), meta[..., 2:] * np.float16(0.01), meta[..., 2:])
+    put_meta(p, meta)
+    check_rows(awq, p, np.ones(2 * new, bool))
+    cache = p.cache.copy()
+    last = meta.copy()
+    last[p.table[0, 199 // 16], :, 199 % 16, 2] = scale
+    put_meta(p, last)
+    rows = np.arange(2 * new) != new - 1
+    check_rows(awq, p, rows, cache=cache)
+    if np.isnan(scale):
+        assert np.isnan(p.run(awq)[0].float().cpu().numpy()[new - 1]).all()
+    # with a window, the oldest token that the first query sees is seen by no other
+    window = 80 - new // 2
+    at = 200 - new - window + 1
+    if at >= 0:
+        first = meta.copy()
+        first[p.table[0, at // 16], :, at % 16, 2] = scale
+        put_meta(p, first)
+        check_rows(awq, p, np.arange(2 * new) != 0, window, cache)

@@ -131,15 +131,15 @@ rmsnorm_kernel(const uint16_t* x, const uint16_t* residual, const uint16_t* __re
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
       }
     }
-    const float rstd = 1.0f / sqrtf(sum / (float)K + eps);
+    const float rstd = 1.0f / sqrtf(sum / (float)K + eps);  // infinite for a row of zeros when eps = 0
     if (xq) {
       // fmaxf drops a NaN, but the sum of squares keeps it, and an infinity too
       const bool finite = sum - sum == 0.f && top - top == 0.f;
       // top / 127 rounded once: a quotient next to the right one, corrected by its exact remainder (Markstein 1990)
       const float near = top * (1.f / 127.f), step = fmaf(fmaf(-127.f, near, top), 1.f / 127.f, near);
       const float inv = 1.0f / step;  // infinite for a step below the smallest normal number: exact division then
-      if (tid == 0) s_tok[r] = finite ? step * rstd : __uint_as_float(0x7FC00000u);
       const bool codes = finite && step > 0.f;
+      if (tid == 0) s_tok[r] = codes ? step * rstd : finite ? 0.f : __uint_as_float(0x7FC00000u);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int i = tid + v * threads;
@@ -149,6 +149,7 @@ rmsnorm_kernel(const uint16_t* x, const uint16_t* residual, const uint16_t* __re
       }
     }
     if (y) {
+      const float by = top == 0.f && sum - sum == 0.f ? 0.f : rstd;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int i = tid + v * threads;
@@ -156,8 +157,8 @@ rmsnorm_kernel(const uint16_t* x, const uint16_t* residual, const uint16_t* __re
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           const float2 a = t[v][p].get();
-          f[2 * p] = a.x * rstd;
-          f[2 * p + 1] = a.y * rstd;
+          f[2 * p] = a.x * by;
+          f[2 * p + 1] = a.y * by;
         }
         if (i < nvec) reinterpret_cast<uint4*>(y + r * (int64_t)K)[i] = narrow8<BF16>(f);
       }

@@ -1,5 +1,5 @@
 // The two 16-bit activation types behind one interface (pairs as packed in memory, widened to fp32 and rounded back),
-// and arithmetic on pairs of fp32 values.
+// arithmetic on pairs of fp32 values, minima and maxima that keep a NaN.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -53,6 +53,18 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
   F2 d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
   return d;
+}
+
+// Minimum and maximum of three that keep a NaN.
+__device__ __forceinline__ float min_nan(float a, float b, float c) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 }  // namespace

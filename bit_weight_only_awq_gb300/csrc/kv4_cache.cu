@@ -117,18 +117,6 @@ struct Turn {
   }
 };
 
-// Minimum and maximum of three that keep a NaN.
-__device__ __forceinline__ float min_nan(float a, float b, float c) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-__device__ __forceinline__ float max_nan(float a, float b, float c) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 // d / 15 rounded once: a quotient next to the right one, corrected by its exact remainder times the rounded reciprocal
 // (Markstein 1990).  An infinite d gives a NaN, which the caller's minimum drops for its bound.
 __device__ __forceinline__ float fifteenth(float d) {

@@ -108,7 +108,7 @@ rmsnorm_kernel(const uint16_t* x, const uint16_t* residual, const uint16_t* __re
         sum2 = fma2(h2, h2, sum2);
         t[v][p] = mul2(h2, F2(w[2 * p], w[2 * p + 1]));
         const float2 a = t[v][p].get();
-        top = fmaxf(top, fmaxf(fabsf(a.x), fabsf(a.y)));
+        top = max_nan(top, fabsf(a.x), fabsf(a.y));
       }
     }
     float sum = sum2.get().x + sum2.get().y;
@@ -116,7 +116,8 @@ rmsnorm_kernel(const uint16_t* x, const uint16_t* residual, const uint16_t* __re
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+      const float other = __shfl_xor_sync(0xFFFFFFFFu, top, o);
+      top = max_nan(top, other, other);
     }
     if ((tid & 31) == 0) part[turn][tid >> 5] = make_float2(sum, top);
     __syncthreads();  // one a row: the other half of `part` is still read by nobody two rows on
@@ -128,12 +129,13 @@ rmsnorm_kernel(const uint16_t* x, const uint16_t* residual, const uint16_t* __re
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        const float other = __shfl_xor_sync(0xFFFFFFFFu, top, o);
+        top = max_nan(top, other, other);
       }
     }
     const float rstd = 1.0f / sqrtf(sum / (float)K + eps);  // infinite for a row of zeros when eps = 0
     if (xq) {
-      // fmaxf drops a NaN, but the sum of squares keeps it, and an infinity too
+      // a row, or a weight, that is not finite shows in the sum of squares, or in the largest product
       const bool finite = sum - sum == 0.f && top - top == 0.f;
       // top / 127 rounded once: a quotient next to the right one, corrected by its exact remainder (Markstein 1990)
       const float near = top * (1.f / 127.f), step = fmaf(fmaf(-127.f, near, top), 1.f / 127.f, near);

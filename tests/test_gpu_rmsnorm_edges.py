@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 from oracle import block
-from tests.test_gpu_rmsnorm import awq, dev, problem, tol  # noqa: F401  (awq is a fixture)
+from tests.test_gpu_rmsnorm import awq, dev, host, problem, tol  # noqa: F401  (awq is a fixture)
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -26,3 +26,18 @@ def test_a_row_of_zeros_without_eps(awq, M, K, bf16):  # noqa: F811
         assert np.all(np.abs(s.cpu().numpy()[other] - scale) <= (tol(K) + 2.0 ** -22) * scale)
         y2, _ = awq.awq_rmsnorm(dev(x, bf16), dev(w, bf16), rt, eps=0.0)
         assert torch.equal(y, y2)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("M,K", [(3, 640), (700, 512), (400, 11016), (2, 16392)])
+@pytest.mark.parametrize("value", [np.nan, np.inf])
+def test_a_weight_that_is_not_finite_shows(awq, M, K, value, bf16):  # noqa: F811
+    """Every row's largest |y| is then not a number, or infinite: a NaN scale and codes 0, as for such a row."""
+    x, r, w = problem(M, K, bf16, 42)
+    w[K - 3] = value
+    x[0, K - 3], r[0, K - 3] = 0, 0  # 0 * inf is a NaN too
+    xq, s, _ = awq.w4a8_rmsnorm_quant(dev(x, bf16), dev(w, bf16), dev(r, bf16))
+    assert torch.isnan(s).all() and not xq.any()
+    y, _ = awq.awq_rmsnorm(dev(x, bf16), dev(w, bf16), dev(r, bf16))
+    bad = ~np.isfinite(host(y))
+    assert bad[:, K - 3].all() and bad.sum() == M

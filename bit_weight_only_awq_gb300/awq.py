@@ -580,14 +580,15 @@ def _kv4_workspace(handle: int, device: torch.device, nbytes: int, stream) -> to
     return ws
 
 
-def kv4_attention(q, cache, block_table, kv_len, q_start=None, max_q: int = 1, scale: float | None = None,
+def kv4_attention(q, cache, block_table, kv_len, q_start=None, max_q: int | None = None, scale: float | None = None,
                   window: int = 0, out=None, lse=None, workspace=None, stream=None):
     """Causal attention of q [T, heads, D] over the cached tokens of each sequence.
 
     block_table int32 [B, max_pages], kv_len int32 [B] (new tokens included).  Without q_start every sequence
     has one query (T = B); with q_start int32 [B + 1] sequence b has the queries q_start[b] .. q_start[b + 1] - 1,
-    at most max_q, which are its last tokens.  scale: 1 / sqrt(D) by default; window: 0 or the number of keys a
-    query looks back over, its own included.  `lse` fp32 [T, heads], when given, receives the log-sum-exp.
+    at most max_q (T by default; a smaller one saves work), which are its last tokens.  scale: 1 / sqrt(D) by
+    default; window: 0 or the number of keys a query looks back over, its own included.  `lse` fp32 [T, heads], when
+    given, receives the log-sum-exp.
     Without `workspace` the calls of a stream share one that grows; a call to be captured in a graph takes one of
     its own (kv4_attention_workspace_bytes, zeroed once).  After awq_last_device_error reports a wait that expired, a
     workspace is zeroed again before its next use, as include/awq.h says of all of them.
@@ -618,6 +619,8 @@ def kv4_attention(q, cache, block_table, kv_len, q_start=None, max_q: int = 1, s
             raise ValueError("kv4_attention: lse is [T, heads]")
     if scale is None:
         scale = dim ** -0.5
+    if max_q is None:
+        max_q = 1 if q_start is None else max(T, 1)
     device = q.device
     handle = _raw_stream(stream, device)
     if workspace is None:

@@ -1,7 +1,9 @@
 """What the Python binding of the block operators makes of its arguments: layouts, defaults, workspaces."""
 
+import numpy as np
 import pytest
 
+from oracle import block
 from tests.test_gpu_kv4_attention import Problem, awq  # noqa: F401  (awq is a fixture)
 
 torch = pytest.importorskip("torch")
@@ -26,3 +28,16 @@ def test_tables_whose_rows_overlap_are_refused(awq):  # noqa: F811
     # the stride of a single row has no meaning
     assert torch.equal(awq.kv4_attention(q, cache, table.flatten().as_strided((1, width), (0, 1)), lens), want)
     assert torch.equal(awq.kv4_attention(q, cache, table[:, :width - 1], lens), want)
+
+
+def test_without_max_q_every_query_is_answered(awq):  # noqa: F811
+    p = Problem([200, 60, 9], [70, 3, 1], 4, 2, 64, 16, seed=34)
+    q, cache, table, lens = operands(p)
+    start = torch.from_numpy(p.start).cuda()
+    out = torch.full_like(q, 7.0)
+    awq.kv4_attention(q, cache, table, lens, q_start=start, out=out)
+    want = block.kv4_attention(p.q, p.cache, p.table, p.lens, p.start, p.scale)[0]
+    assert np.abs(out.float().cpu().numpy() - want).max() < 0.02
+    assert torch.equal(awq.kv4_attention(q, cache, table, lens, q_start=start, max_q=70), out)
+    one = awq.kv4_attention(q[:3], cache, table, lens)  # without q_start one query a sequence
+    assert torch.equal(one, awq.kv4_attention(q[:3], cache, table, lens, max_q=1))

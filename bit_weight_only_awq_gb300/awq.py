@@ -560,19 +560,24 @@ def kv4_attention_workspace_bytes(T: int, B: int, max_q: int, heads: int, kv_hea
 
 
 # One workspace of kv4_attention for each device and stream (calls on one stream may share it), grown on demand, by
-# half at least.  Outgrown ones stay: a graph captured on their stream may still use them.
+# half at least.  Outgrown ones stay.  A captured call never takes it: its graph may run on any stream, beside this
+# one's calls or another graph that holds the same, and a workspace made in the capture would be the graph's memory.
 _kv4_workspaces: dict[tuple, torch.Tensor] = {}
 _kv4_outgrown: list[torch.Tensor] = []
 
 
 def _kv4_workspace(handle: int, device: torch.device, nbytes: int, stream) -> torch.Tensor:
+    if stream is None:
+        capturing = torch.cuda.is_current_stream_capturing()
+    else:
+        with torch.cuda.stream(stream):
+            capturing = torch.cuda.is_current_stream_capturing()
+    if capturing:
+        raise RuntimeError("kv4_attention: a captured call takes a workspace of its own")
     key = (device.index, handle)
     ws = _kv4_workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
-            if torch.cuda.is_current_stream_capturing():
-                # it would belong to the graph's memory, and be zeroed at its replays only
-                raise RuntimeError("kv4_attention: a captured call takes a workspace of its own")
             if ws is not None:
                 _kv4_outgrown.append(ws)
                 nbytes = max(nbytes, ws.numel() + ws.numel() // 2)
@@ -589,8 +594,8 @@ def kv4_attention(q, cache, block_table, kv_len, q_start=None, max_q: int | None
     at most max_q (T by default; a smaller one saves work), which are its last tokens.  scale: 1 / sqrt(D) by
     default; window: 0 or the number of keys a query looks back over, its own included.  `lse` fp32 [T, heads], when
     given, receives the log-sum-exp.
-    Without `workspace` the calls of a stream share one that grows; a call to be captured in a graph takes one of
-    its own (kv4_attention_workspace_bytes, zeroed once).  After awq_last_device_error reports a wait that expired, a
+    Without `workspace` the calls of a stream share one that grows; a call to be captured in a graph needs one of
+    its own (kv4_attention_workspace_bytes, zeroed once) and is refused without.  After awq_last_device_error reports a wait that expired, a
     workspace is zeroed again before its next use, as include/awq.h says of all of them.
     """
     pages, kv_heads, dim, page = _kv4_shape("kv4_attention", cache)

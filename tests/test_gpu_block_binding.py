@@ -41,3 +41,27 @@ def test_without_max_q_every_query_is_answered(awq):  # noqa: F811
     assert torch.equal(awq.kv4_attention(q, cache, table, lens, q_start=start, max_q=70), out)
     one = awq.kv4_attention(q[:3], cache, table, lens)  # without q_start one query a sequence
     assert torch.equal(one, awq.kv4_attention(q[:3], cache, table, lens, max_q=1))
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_a_capture_never_shares_a_workspace(awq, given):  # noqa: F811
+    """A graph that held the stream's workspace could run beside eager calls of that stream, or beside another graph."""
+    p = Problem([500, 300], [1, 1], 8, 2, 128, 64, seed=35, junk=False)
+    q, cache, table, lens = operands(p)
+    out = torch.empty_like(q)
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        want = awq.kv4_attention(q, cache, table, lens)  # the stream has a workspace now
+    torch.cuda.synchronize()
+    with pytest.raises(RuntimeError, match="workspace"):
+        with torch.cuda.graph(graph, stream=stream):
+            out.zero_()
+            awq.kv4_attention(q, cache, table, lens, out=out, stream=stream if given else None)
+    ws = torch.zeros(awq.kv4_attention_workspace_bytes(2, 2, 1, 8, 2, 128), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        awq.kv4_attention(q, cache, table, lens, out=out, workspace=ws, stream=stream if given else None)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)

@@ -554,9 +554,14 @@ def kv4_gather(cache, slots, dtype=torch.float16, k=None, v=None, stream=None):
     return k, v
 
 
-@functools.lru_cache(maxsize=4096)
 def kv4_attention_workspace_bytes(T: int, B: int, max_q: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    """Bytes of a kv4_attention workspace on the current device."""
     return int(lib.kv4_attention_workspace_bytes(T, B, max_q, heads, kv_heads, head_dim))
+
+
+@functools.lru_cache(maxsize=4096)
+def _kv4_workspace_need(device: int, *shape) -> int:
+    return kv4_attention_workspace_bytes(*shape)  # by the device's SM count
 
 
 # One workspace of kv4_attention for each device and stream (calls on one stream may share it), grown on demand, by
@@ -629,7 +634,8 @@ def kv4_attention(q, cache, block_table, kv_len, q_start=None, max_q: int | None
     device = q.device
     handle = _raw_stream(stream, device)
     if workspace is None:
-        workspace = _kv4_workspace(handle, device, kv4_attention_workspace_bytes(T, B, max_q, heads, kv_heads, dim), stream)
+        need = _kv4_workspace_need(device.index, T, B, max_q, heads, kv_heads, dim)
+        workspace = _kv4_workspace(handle, device, need, stream)
     _check("kv4_attention", lib.kv4_attention(
         q.data_ptr(), _row_stride("kv4_attention", q, heads * dim), cache.data_ptr(), block_table.data_ptr(),
         table_stride, kv_len.data_ptr(), _ptr(q_start), out.data_ptr(),

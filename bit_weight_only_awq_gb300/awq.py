@@ -404,6 +404,17 @@ def _raw_stream(stream, device: torch.device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
+_current_device = torch._C._cuda_getDevice
+
+
+def _on_current_gpu(name: str, *tensors) -> None:
+    """The library launches on the current device: all tensors, the caller's workspace among them, are there."""
+    here = _current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"{name}: every tensor is on the current GPU (device {here})")
+
+
 def _need(name: str, dtype, *tensors) -> None:
     for t in tensors:
         if t is not None and (t.dtype is not dtype or not t.is_cuda or not t.is_contiguous()):
@@ -454,6 +465,7 @@ def w4a8_rmsnorm_quant(x, weight, residual=None, eps: float = 1e-6, res_out=None
         if (xq is not None and xq.shape != (M, K)) or (s_tok is not None and s_tok.shape != (M,)) or \
                 (y is not None and y.shape != (M, K)):
             raise ValueError("w4a8_rmsnorm_quant: xq and y are [M, K], s_tok is [M]")
+    _on_current_gpu("w4a8_rmsnorm_quant", x, weight, residual, res_out, y, xq, s_tok)
     if xq is None:
         xq = torch.empty((M, K), dtype=torch.int8, device=device)
     if s_tok is None:
@@ -473,6 +485,7 @@ def awq_rmsnorm(x, weight, residual=None, eps: float = 1e-6, res_out=None, out=N
         _need("awq_rmsnorm", x.dtype, out)
         if out.shape != (M, K):
             raise ValueError("awq_rmsnorm: out is [M, K]")
+    _on_current_gpu("awq_rmsnorm", x, weight, residual, res_out, out)
     _check("awq_rmsnorm", lib.awq_rmsnorm(_ptr(x), _ptr(residual), _ptr(weight), _ptr(res_out), _ptr(out), M, K, xs,
                                           rs, eps, dtype, _raw_stream(stream, x.device)))
     return out, res_out
@@ -525,6 +538,8 @@ def kv4_append(cache, k, v, positions, slots, table, q=None, interleaved: bool =
         _need("kv4_append", torch.int32, positions)
         if positions is None or positions.shape != (T,):
             raise ValueError("kv4_append: positions is [T]")
+        _on_current_gpu("kv4_append", positions, table)
+    _on_current_gpu("kv4_append", cache, k, v, slots, q, q_out)
     _check("kv4_append", lib.kv4_append(
         _ptr(q), _ptr(k), _ptr(v), qs, _row_stride("kv4_append", k, kv_heads * dim),
         _row_stride("kv4_append", v, kv_heads * dim), _ptr(positions),
@@ -549,6 +564,7 @@ def kv4_gather(cache, slots, dtype=torch.float16, k=None, v=None, stream=None):
         _need("kv4_gather", k.dtype, k, v)
         if k.shape != shape or v.shape != shape:
             raise ValueError("kv4_gather: k and v are [T, kv_heads, head_dim]")
+    _on_current_gpu("kv4_gather", cache, slots, k, v)
     _check("kv4_gather", lib.kv4_gather(cache.data_ptr(), slots.data_ptr(), k.data_ptr(), v.data_ptr(), pages, shape[0],
                                         kv_heads, dim, page, kind, _raw_stream(stream, device)))
     return k, v
@@ -631,6 +647,7 @@ def kv4_attention(q, cache, block_table, kv_len, q_start=None, max_q: int | None
         scale = dim ** -0.5
     if max_q is None:
         max_q = 1 if q_start is None else max(T, 1)
+    _on_current_gpu("kv4_attention", q, cache, block_table, kv_len, q_start, out, lse, workspace)
     device = q.device
     handle = _raw_stream(stream, device)
     if workspace is None:

@@ -65,3 +65,22 @@ def test_a_capture_never_shares_a_workspace(awq, given):  # noqa: F811
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_every_entry_point_takes_tensors_of_the_current_gpu_alone(awq, monkeypatch):  # noqa: F811
+    p = Problem([30], [1], 4, 2, 64, 16, seed=36)
+    q, cache, table, lens = operands(p)
+    k, slots, x = q[:, :2].contiguous(), torch.tensor([5]).cuda(), q.view(1, -1)
+    rope = torch.from_numpy(block.rope_table(8, 64)).cuda()
+    calls = {
+        "w4a8_rmsnorm_quant": lambda: awq.w4a8_rmsnorm_quant(x, x[0]), "awq_rmsnorm": lambda: awq.awq_rmsnorm(x, x[0]),
+        "kv4_append": lambda: awq.kv4_append(cache, k, k, slots.int(), slots, rope, q=q),
+        "kv4_gather": lambda: awq.kv4_gather(cache, slots), "kv4_attention": lambda: awq.kv4_attention(q, cache, table, lens)}
+    for call in calls.values():
+        call()
+    with pytest.raises(ValueError, match="current GPU"):  # the library would take the host's address for the device's
+        awq.kv4_attention(q, cache, table, lens, workspace=torch.zeros(1 << 24, dtype=torch.uint8))
+    monkeypatch.setattr(awq, "_current_device", lambda: 1)
+    for name, call in calls.items():
+        with pytest.raises(ValueError, match=f"{name}: every tensor is on the current GPU"):
+            call()

@@ -413,9 +413,9 @@ kv4_attention_kernel(const Args a, float* warp_parts, float* cta_parts, int* cou
           top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
           sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
           sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-          // a power of two takes the largest element to [2^10, 2^11): exact in fp16 down to 2^-24 of it
+          // a power of two takes the largest element to [2^14, 2^15): exact in fp16 down to 2^-24 of it, sixteenths too
           const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 127);
-          const float up = __uint_as_float((uint32_t)(127 + 10 - e) << 23);
+          const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
 #pragma unroll
           for (int i = 0; i < kWords; ++i)
 #pragma unroll
@@ -424,7 +424,7 @@ kv4_attention_kernel(const Args a, float* warp_parts, float* cta_parts, int* cou
               qf[n][2 * i + h][0] = pack2<false>(y[0] * up, y[1] * up);
               qf[n][2 * i + h][1] = pack2<false>(y[2] * up * 0.0625f, y[3] * up * 0.0625f);
             }
-          const float down = __uint_as_float((uint32_t)max(127 + e - 10, 1) << 23) * 16777216.f;
+          const float down = __uint_as_float((uint32_t)max(127 + e - 14, 1) << 23) * 16777216.f;
           // the accumulator's columns of this lane are 2t and 2t + 1
 #pragma unroll
           for (int c = 0; c < 2; ++c) {

@@ -276,9 +276,9 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
           sum += f.x + f.y;
         }
       }
-      // a power of two takes the largest element to [2^10, 2^11): exact in fp16 down to 2^-24 of it
+      // a power of two takes the largest element to [2^14, 2^15): exact in fp16 down to 2^-24 of it, sixteenths too
       const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 127);
-      const float up = __uint_as_float((uint32_t)(127 + 10 - e) << 23) * sign, up16 = up * 0.0625f;
+      const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23) * sign, up16 = up * 0.0625f;
 #pragma unroll
       for (int c = 0; c < kLanes; ++c) {
         const float2 f0 = unpack2<BF16>(v[c].x), f1 = unpack2<BF16>(v[c].y), f2 = unpack2<BF16>(v[c].z), f3 = unpack2<BF16>(v[c].w);
@@ -286,7 +286,7 @@ kv4_prefill_kernel(const Args a, int splits, float* parts, int* err) {
                pack2<false>(f2.x * up, f2.y * up), pack2<false>(f3.x * up16, f3.y * up16));
       }
       // not 0, which would make a NaN of a masked score, -inf; below that the weights are equal anyway
-      qk = fmaxf(__uint_as_float((uint32_t)max(127 + e - 10, 1) << 23) * 16777216.f * factor, FLT_MIN);
+      qk = fmaxf(__uint_as_float((uint32_t)max(127 + e - 14, 1) << 23) * 16777216.f * factor, FLT_MIN);
       qr = sum * (up * 5.9604644775390625e-8f);
     }
     fence_async();

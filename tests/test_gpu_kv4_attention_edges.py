@@ -132,3 +132,33 @@ def test_a_hidden_scale_takes_no_bits_from_a_row(awq, new, heads, scale, bf16): 
         first[p.table[0, at // 16], :, at % 16, 2] = scale
         put_meta(p, first)
         check_rows(awq, p, np.arange(2 * new) != 0, window, cache)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("new", [1, 5, 100])
+def test_small_query_elements_keep_their_bits(awq, new, bf16):  # noqa: F811
+    """Elements of 2^-24 of the row's largest, where the largest meets keys that are 0: the score is theirs alone, and
+    is to be as exact as fp32 sums are."""
+    p = Problem([150], [new], 4, 2, 128, 64, bf16=bf16, seed=38, junk=False)
+    meta = meta_of(p).copy()
+    meta[..., 0], meta[..., 1] = 8.0, 0.0
+    put_meta(p, meta)
+    # channel 0's codes are 0: nibble 0 of the first word of each token's key
+    keys = p.cache[..., :8 * p.dim].reshape(*p.cache.shape[:3], 16, p.dim // 2)
+    keys[..., 0] &= 0xF0
+    p.cache[..., :8 * p.dim] = keys.reshape(*p.cache.shape[:3], 8 * p.dim)
+    rng = np.random.default_rng(39)
+    digits = 2 ** 7 if bf16 else 2 ** 10
+    small = (1 + rng.integers(0, digits, p.q.shape) / digits) * rng.choice([-1, 1], p.q.shape)
+    p.q = (small * 2.0 ** -10).astype(np.float32)
+    p.q[..., 0] = 2.0 ** 14
+    assert np.array_equal(p.q, block.round16(p.q, bf16))
+    p.scale = 1.0
+    out, lse = p.run(awq, scale=1.0)
+    want, want_lse, mag, reach = block.kv4_attention(p.q, p.cache, p.table, p.lens, p.start, 1.0)
+    delta = reach * (8 + p.dim / 8) * 2.0 ** -23
+    assert reach.max() < 40
+    assert np.all(np.abs(lse.cpu().numpy() - want_lse) <= delta + 2.0 ** -17 + 2.0 ** -22 * np.abs(want_lse))
+    half_ulp = 2.0 ** -8 if bf16 else 2.0 ** -11
+    bound = mag * (2 * delta[..., None] + 2.0 ** -11 + 2.0 ** -17) + half_ulp * np.abs(want) + 2.0 ** -24 * (1 + mag.max())
+    assert np.all(np.abs(out.float().cpu().numpy() - want) <= bound)

@@ -27,7 +27,7 @@
 // arrive, always in the order of the tiles, so that results do not depend on timing.
 //
 // Measured, 32 heads on 8: 16 sequences of 32768 tokens 102 us, 5.6 TB/s of cache; 64 sequences of up to 8191 tokens
-// 68 us, 4.2 TB/s; 177 tokens 8.7 us.  A call has 3 us from a CTA's start to its first copies, 3 us to the first tiles, a
+// 70 us, 4.1 TB/s; 177 tokens 9.1 us.  A call has 3 us from a CTA's start to its first copies, 3 us to the first tiles, a
 // body at 6.9 TB/s, SMs that finish over 15 us (the same ones in every run) and 3 to 5 us of joins, so short
 // calls are bound by latency and long ones by HBM with the uneven finish.  A tile takes 1005 instructions of a warp; at
 // 8 sequences of 32768 half of the issue slots are busy.
@@ -47,8 +47,8 @@ namespace {
 constexpr int kTile = 64;    // tokens of a tile: 4 units
 constexpr int kFewParts = 12;
 
-// Eight query columns: twelve warps of 168 registers, three on each sub-partition.  Sixteen: eight warps of 255; twelve
-// spilled (16 columns of 32 x 8192 tokens: 140 us).
+// Eight query columns: twelve warps of 168 registers, three on each sub-partition.  Sixteen: eight warps of 255, which at
+// 128 channels spill 60 bytes (and twelve far more: 16 columns of 32 x 8192 tokens 140 us).
 constexpr int warps_of(int nt) { return nt == 1 ? 12 : 8; }
 
 template <int D, int NT>
@@ -831,13 +831,13 @@ cudaError_t launch(const Kv4AttnArgs& args, int max_rows, void* ws, int* err, cu
 
 // Up to how many query rows of a cache head this kernel takes a sequence; the tcgen05 kernel, which makes operands of a
 // tile once for 256 rows where this one goes over the cache again for every 8 or 16, takes longer ones.  us at 8 x 8192
-// tokens, 8 cache heads of 128 channels, here / there: 16 rows 34 / 81, 32 rows 52 / 82, 64 rows 90 / 83; at 16 x 4096,
-// 64 channels: 32 rows 37 / 71, 64 rows 61 / 71.
+// tokens, 8 cache heads of 128 channels, here / there: 16 rows 33 / 75, 32 rows 52 / 75, 48 rows 72 / 75, 56 rows 91 / 75;
+// at 16 x 4096, 64 channels: 32 rows 39 / 67, 48 rows 53 / 67, 64 rows 66 / 67, 80 rows 80 / 67.
 int rows_here(int dim) { return dim == 128 ? 48 : 64; }
 
 // What a call takes: this kernel, with eight or sixteen columns, the other, or each for its sequences.  Sequences of
-// different length (T < B max_q) may be of both kinds: 31 single tokens and 512 of a prompt, 8192 cached each, take 251 us
-// so, and 413 us on the other kernel alone.
+// different length (T < B max_q) may be of both kinds: 31 single tokens and 512 of a prompt, 8192 cached each, take 256 us
+// so, 395 on this kernel alone and 434 on the other.
 struct Route {
   bool here, there;
   int nt;

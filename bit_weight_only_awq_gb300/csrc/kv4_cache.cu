@@ -10,10 +10,12 @@ namespace {
 
 // Both kernels: D / 8 lanes for each head of a token, eight channels a lane: one 16-byte access, one AWQ word of the keys,
 // two halves of the values.  The floor is HBM's: 8165 tokens of 32 + 32 + 32 heads move 305 MB in 77 us, 3.9 TB/s
-// (74 us when all channels turn, in halves), and are bound by the arithmetic (reductions over a head by shuffles, about
-// twenty operations for a code): without any one of the rotation, the stores or the check for ties it still takes
-// 70 to 73, and reading further ahead changes nothing.  Reading back moves 169 MB in 34 us, 5.0 TB/s.  64 tokens of
-// 32 + 8 + 8 heads take 4 us.
+// (74 us when all channels turn, in halves).  In a capture the warps wait for memory first (long scoreboard 4.4 of an
+// issue's stalls) with 66 % of the issue slots busy; without any one of the rotation, the stores or the check for ties it
+// still takes 70 to 73, and reading further ahead changed nothing.  64 registers, for four CTAs an SM, spill 56 to 60 bytes
+// in the general rotation, 20 to 24 with halves, none with neighbours.  Reading back moves 169 MB in 34 us, 5.0 TB/s,
+// with the same first stall (5.2): a lane's value halves are two bytes each, so a token uses a quarter of the sectors that it
+// touches.  64 tokens of 32 + 8 + 8 heads take 4 us.
 constexpr int kAThreads = 256;
 constexpr int kAWarps = kAThreads / 32;
 constexpr int kACtas = 4;  // resident on an SM

@@ -21,10 +21,11 @@
 // with the present ones.  The output stays in tensor memory; it is rescaled only when a row's maximum has grown by more
 // than 2^8, so the weights are at most 2^8 and enter fp16 as p sv 2^(5 - e), 2^e the largest value scale so far.
 //
-// Measured: 2 x 1024 tokens over 4095 and 2376, 32 heads on 8, 121 us, 751 TFLOP/s (the products alone would take 47 at
-// the library GEMM's rate).  Bound by the softmax warps, two on a sub-partition, and the dependences in their arithmetic: a
-// step of 64 tokens takes a warp 1900 cycles when it is alone on its sub-partition, 2500 beside another.  256 CTAs of 24 to
-// 64 steps on 152 SMs also leave a sixth of the SMs' time unused.  A CTA's start and end cost 6 us.  Slower and left out: two
+// Measured: 2 x 1024 tokens over 4095 and 2376, 32 heads on 8, 122 us, 748 TFLOP/s (the products alone would take 47 at
+// the library GEMM's rate).  A step of 64 tokens takes a softmax warp 1900 cycles when it is alone on its sub-partition,
+// 2500 beside another.  Two things are near their limits in a capture: shared memory, with 0.5 wavefronts a cycle of loads
+// and stores and 0.3 of the products' operands, and the issue slots, 57 % busy between dependences; which of them bounds
+// a step has not been separated.  256 CTAs of 24 to 64 steps on 152 SMs also leave a sixth of the SMs' time unused.  A CTA's start and end cost 6 us.  Slower and left out: two
 // threads for a row (176 us against 159), threads with a row of both row tiles (196 against 161), one product warp for
 // both row tiles (180 against 161), weights made with the maximum of the steps before, in one pass (147 against 121).
 #include <cfloat>

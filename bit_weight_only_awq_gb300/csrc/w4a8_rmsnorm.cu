@@ -60,8 +60,11 @@ __device__ __forceinline__ uint2 codes8(const F2 (&t)[4], float step, float inv)
 // A CTA takes rows in turn and reads each once: a thread keeps t = h w of its V vectors in registers between the
 // reduction and the codes, and has the next row's vectors on the way meanwhile.  The CTA's threads cover the row's K / 8
 // vectors V times.  HBM bound: 8192 x 8192 with the residual moves 470 MB in 72 us, 6.5 TB/s; 4096 x 4096 takes 19.7 us
-// (6.0 TB/s), 8 rows 2.5 us.  7001 x 11016 in bf16 without residual takes 58 us (4.0 TB/s): three bytes an element leave
-// the instructions in front, and a row of 1377 vectors fills eleven warps with a ragged fourth vector.
+// (6.0 TB/s), 8 rows 2.5 us.  7001 x 11016 in bf16 without residual takes 58 us (4.0 TB/s): in a capture 62 % of the issue
+// slots are busy and DRAM 42 %, with dependences between instructions the first stall (1.8 of an issue's), and a row
+// of 1377 vectors fills eleven warps with a ragged fourth vector.  Registers: V = 4 spills 40 to 64 bytes at two CTAs (none
+// in threads of 384 without a residual, none at one CTA of 512), 52 to 440 at 1024 threads, V = 8 532 to 1004; rows wider
+// than 16384 have only those two (1024 x 28672 with a residual 58 us, 4.0 TB/s).
 template <bool BF16, bool RES, int V, int T, int CTAS>
 __global__ void __launch_bounds__(T, CTAS)
 rmsnorm_kernel(const uint16_t* x, const uint16_t* residual, const uint16_t* __restrict__ weight, uint16_t* res_out,

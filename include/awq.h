@@ -407,7 +407,8 @@ typedef enum { AWQ_FP16 = 0, AWQ_BF16 = 1 } awq_dtype;
  * res_out [M, K] dense (output; NULL to skip; may be x or residual itself when that is dense);
  * y [M, K] dense (the norm's rows, rounded once; NULL to skip); xq int8 [M, K]; s_tok fp32 [M].
  * A row of zeros gets s_tok = 0, codes 0 and y = 0, also with eps = 0; a row that holds a NaN or an infinity,
- * in h or in its products with w, gets s_tok = NaN and codes 0, so that the product shows it.  K % 8 == 0, 8 <= K <= 65536,
+ * in h or in its products with w, gets s_tok = NaN and codes 0, so that the product shows it; so does one
+ * whose sum of squares is beyond fp32 (bf16 elements past 1e19).  K % 8 == 0, 8 <= K <= 65536,
  * strides % 8 == 0 and >= K, eps >= 0.  M = 0 is a no-op.
  */
 awq_status w4a8_rmsnorm_quant(const uint16_t *x, const uint16_t *residual, const uint16_t *weight,

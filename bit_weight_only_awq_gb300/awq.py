@@ -67,6 +67,19 @@ _SIGS = {
     "kv4_attention_workspace_bytes": (_sz, [_i64, _i64, _i32, _i32, _i32, _i32]),
     "kv4_attention": (_i32, [_p, _i64, _p, _p, _i64, _p, _p, _p, _p, _i64, _i64, _i32, _i32, _i32, _i32, _i64, _i32,
                              _i32, _f32, _i32, _i32, _p, _sz, _p]),
+    "awq_moe_plan": (_i32, [_p, _i64, _i32, _p, _p, _p, _p]),
+    "awq_moe_route": (_i32, [_p, _i64, _i64, _i32, _i32, _i32, _i32, _p, _p, _p, _p, _p, _p]),
+    "awq_moe_prepacked_bytes": (_sz, [_i32, _i64, _i64, _i32]),
+    "awq_moe_prepack": (_i32, [_p, _p, _p, _i32, _i64, _i64, _i32, _i32, _p, _sz, _p]),
+    "awq_moe_unprepack": (_i32, [_p, _i32, _i64, _i64, _i32, _p, _p, _p, _p]),
+    "awq_moe_gemm_workspace_bytes": (_sz, [_i64, _i32, _i64, _i64, _i32]),
+    "awq_moe_gemm": (_i32, [_p, _i64, _i64, _p, _p, _p, _i32, _p, _i64, _i32, _i64, _i64, _i32, _i32, _p, _sz, _p]),
+    "awq_moe_combine": (_i32, [_p, _p, _p, _p, _i64, _p, _i64, _i32, _i64, _i64, _i32, _p]),
+    "awq_fp8_quant_act": (_i32, [_p, _i64, _p, _p, _i64, _i64, _i32, _p]),
+    "awq_fp8_gemm_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "awq_fp8_gemm": (_i32, [_p, _p, _p, _p, _p, _i64, _i64, _i64, _i32, _p, _sz, _p]),
+    "awq_fp8_linear_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "awq_fp8_linear": (_i32, [_p, _i64, _p, _p, _p, _i64, _i64, _i64, _i32, _p, _sz, _p]),
     "awq_last_device_error": (_i32, [ctypes.POINTER(_i32)]),
     "awq_selftest_wait_timeout": (_i32, [_i64, _p]),
 }
@@ -658,6 +671,307 @@ def kv4_attention(q, cache, block_table, kv_len, q_start=None, max_q: int | None
         table_stride, kv_len.data_ptr(), _ptr(q_start), out.data_ptr(),
         _ptr(lse), T, B, max_q, heads, kv_heads, dim, pages, page, max_pages, scale, window, dtype,
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle))
+    return out
+
+
+# ---- the feed-forward layer with experts, fp8 linear layers
+
+# Workspaces of the grouped product and the fp8 layers: one for each device and stream, as for kv4_attention.
+_layer_workspaces: dict[tuple, torch.Tensor] = {}
+_layer_outgrown: list[torch.Tensor] = []
+
+
+def _capturing(stream) -> bool:
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
+def _layer_workspace(name: str, handle: int, device: torch.device, nbytes: int, stream) -> torch.Tensor:
+    if _capturing(stream):
+        raise RuntimeError(f"{name}: a captured call takes a workspace of its own")
+    key = (device.index, handle)
+    ws = _layer_workspaces.get(key)
+    if ws is None or ws.numel() < nbytes:
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
+            if ws is not None:
+                _layer_outgrown.append(ws)
+                nbytes = max(nbytes, ws.numel() + ws.numel() // 2)
+            ws = _layer_workspaces[key] = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+    return ws
+
+
+@functools.lru_cache(maxsize=4096)
+def _layer_workspace_need(device: int, query: str, *shape) -> int:
+    return int(getattr(lib, query)(*shape))  # by the device's SM count
+
+
+class MoePlan:
+    """Rows of a layer with experts in the experts' order (awq_moe_plan): `offsets` int32 [experts + 1], `order` int32
+    [R], `place` int32 [R], with R = tokens * top_k; the tensors that include/awq.h describes."""
+
+    def __init__(self, offsets: torch.Tensor, order: torch.Tensor, place: torch.Tensor, top_k: int):
+        self.offsets, self.order, self.place, self.top_k = offsets, order, place, top_k
+
+    @property
+    def rows(self) -> int:
+        return self.order.shape[0]
+
+    @property
+    def experts(self) -> int:
+        return self.offsets.shape[0] - 1
+
+
+def _new_plan(rows: int, experts: int, top_k: int, device) -> MoePlan:
+    # one allocation, each part 16-byte aligned
+    first, wide = (experts + 4) // 4 * 4, (rows + 3) // 4 * 4
+    buf = torch.empty(first + 2 * wide, dtype=torch.int32, device=device)
+    return MoePlan(buf[: experts + 1], buf[first : first + rows], buf[first + wide : first + wide + rows], top_k)
+
+
+def awq_moe_plan(ids: torch.Tensor, experts: int, stream=None) -> MoePlan:
+    """The plan of a router of one's own: ids int32 [T, top_k], each in [0, experts) or a choice without a row."""
+    if ids.dim() != 2:
+        raise ValueError("awq_moe_plan: ids is [T, top_k]")
+    _need("awq_moe_plan", torch.int32, ids)
+    _on_current_gpu("awq_moe_plan", ids)
+    T, top_k = ids.shape
+    plan = _new_plan(T * top_k, experts, top_k, ids.device)
+    _check("awq_moe_plan", lib.awq_moe_plan(ids.data_ptr(), T * top_k, experts, plan.offsets.data_ptr(),
+                                            plan.order.data_ptr(), plan.place.data_ptr(),
+                                            _raw_stream(stream, ids.device)))
+    return plan
+
+
+_LOGITS = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+
+
+def awq_moe_route(logits: torch.Tensor, top_k: int, normalize: bool = True, stream=None):
+    """Softmax and top_k of a router's logits [T, experts] (fp16, bf16 or fp32): (weights fp32 [T, top_k], ids int32
+    [T, top_k], their MoePlan).  normalize: a token's weights sum to 1."""
+    T, experts = logits.shape
+    kind = _LOGITS.get(logits.dtype)
+    if kind is None or not logits.is_cuda:
+        raise TypeError("awq_moe_route takes fp16, bf16 or fp32 logits on a GPU")
+    _on_current_gpu("awq_moe_route", logits)
+    device = logits.device
+    if not 1 <= top_k <= experts:
+        raise AwqError("awq_moe_route", -1)
+    weights = torch.empty((T, top_k), dtype=torch.float32, device=device)
+    ids = torch.empty((T, top_k), dtype=torch.int32, device=device)
+    plan = _new_plan(T * top_k, experts, top_k, device)
+    _check("awq_moe_route", lib.awq_moe_route(
+        logits.data_ptr(), _row_stride("awq_moe_route", logits, experts), T, experts, top_k, int(normalize), kind,
+        ids.data_ptr(), weights.data_ptr(), plan.offsets.data_ptr(), plan.order.data_ptr(), plan.place.data_ptr(),
+        _raw_stream(stream, device)))
+    return weights, ids, plan
+
+
+class MoeWeights:
+    """Prepared weights of a layer's experts (awq_moe_prepack): the device bytes, the sizes and the scales' type."""
+
+    def __init__(self, data: torch.Tensor, experts: int, K: int, N: int, gated: bool, dtype: torch.dtype):
+        self.data, self.experts, self.K, self.N, self.gated, self.dtype = data, experts, K, N, gated, dtype
+
+    @property
+    def outputs(self) -> int:
+        """Columns that awq_moe_gemm writes."""
+        return self.N // 2 if self.gated else self.N
+
+
+def awq_moe_prepack(qweight, qzeros, scales, gated: bool = False, group_size: int = GROUP_SIZE, stream=None) -> MoeWeights:
+    """Lays the experts' AWQ weights out for awq_moe_gemm: qweight int32 [experts, K, N/8], qzeros int32 [experts,
+    K/128, N/8] or None (symmetric), scales fp16 or bf16 [experts, K/128, N].  gated: the columns are gate's, then
+    up's, and the product gives silu(gate) * up.  The originals are not needed afterwards (awq_moe_unprepack)."""
+    experts, K, nw = qweight.shape
+    N = nw * 8
+    _dtype16("awq_moe_prepack", scales)
+    _need("awq_moe_prepack", torch.int32, qweight, qzeros)
+    _need("awq_moe_prepack", scales.dtype, scales)
+    if scales.shape != (experts, K // GROUP_SIZE, N) or (qzeros is not None and qzeros.shape != (experts, K // GROUP_SIZE, nw)):
+        raise ValueError("awq_moe_prepack: scales [experts, K / 128, N], qzeros [experts, K / 128, N / 8]")
+    _on_current_gpu("awq_moe_prepack", qweight, qzeros, scales)
+    nbytes = int(lib.awq_moe_prepacked_bytes(experts, K, N, int(gated)))
+    if nbytes == 0:
+        raise AwqError("awq_moe_prepack", -1)
+    data = torch.empty(nbytes, dtype=torch.uint8, device=qweight.device)
+    _check("awq_moe_prepack", lib.awq_moe_prepack(_ptr(qweight), _ptr(qzeros), _ptr(scales), experts, K, N, group_size,
+                                                  int(gated), _ptr(data), nbytes, _raw_stream(stream, qweight.device)))
+    return MoeWeights(data, experts, K, N, bool(gated), scales.dtype)
+
+
+def awq_moe_unprepack(weights: MoeWeights, with_zeros: bool = True, stream=None):
+    """The AWQ (qweight, qzeros or None, scales) that `weights` was made from."""
+    w, dev = weights, weights.data.device
+    _on_current_gpu("awq_moe_unprepack", w.data)
+    qweight = torch.empty((w.experts, w.K, w.N // 8), dtype=torch.int32, device=dev)
+    qzeros = torch.empty((w.experts, w.K // GROUP_SIZE, w.N // 8), dtype=torch.int32, device=dev) if with_zeros else None
+    scales = torch.empty((w.experts, w.K // GROUP_SIZE, w.N), dtype=w.dtype, device=dev)
+    _check("awq_moe_unprepack", lib.awq_moe_unprepack(_ptr(w.data), w.experts, w.K, w.N, int(w.gated), _ptr(qweight),
+                                                      _ptr(qzeros), _ptr(scales), _raw_stream(stream, dev)))
+    return qweight, qzeros, scales
+
+
+def awq_moe_gemm_workspace_bytes(rows: int, weights: MoeWeights) -> int:
+    """Bytes of an awq_moe_gemm workspace on the current device."""
+    return int(lib.awq_moe_gemm_workspace_bytes(rows, weights.experts, weights.K, weights.N, int(weights.gated)))
+
+
+def awq_moe_gemm(x, weights: MoeWeights, plan: MoePlan, gather: bool = False, out=None, workspace=None, stream=None):
+    """Every expert's rows times its weights: [plan.rows, weights.outputs].  x holds the rows in the plan's order, or with
+    `gather` the tokens that the plan was made for.  Rows that no expert has are not written.  Workspaces as for
+    kv4_attention: the calls of a stream share one, a captured call takes one of its own (awq_moe_gemm_workspace_bytes,
+    zeroed once)."""
+    rows, K = plan.rows, weights.K
+    dtype = _dtype16("awq_moe_gemm", x, out)
+    if x.dtype is not weights.dtype:
+        raise TypeError("awq_moe_gemm: x and the weights' scales have one type")
+    if x.dim() != 2 or x.shape[1] != K or plan.experts != weights.experts or \
+            x.shape[0] * (plan.top_k if gather else 1) != rows:
+        raise ValueError("awq_moe_gemm: x is [rows, K] ([tokens, K] with gather), plan and weights have the same experts")
+    device = x.device
+    if out is None:
+        out = torch.empty((rows, weights.outputs), dtype=x.dtype, device=device)
+    elif out.shape != (rows, weights.outputs) or not out.is_contiguous():
+        raise ValueError("awq_moe_gemm: out is dense, [rows, outputs]")
+    _on_current_gpu("awq_moe_gemm", x, weights.data, plan.offsets, plan.order, out, workspace)
+    handle = _raw_stream(stream, device)
+    if workspace is None:
+        need = _layer_workspace_need(device.index, "awq_moe_gemm_workspace_bytes", rows, weights.experts, K, weights.N,
+                                     int(weights.gated))
+        workspace = _layer_workspace("awq_moe_gemm", handle, device, need, stream)
+    _check("awq_moe_gemm", lib.awq_moe_gemm(
+        x.data_ptr(), _row_stride("awq_moe_gemm", x, K), x.shape[0], weights.data.data_ptr(), plan.offsets.data_ptr(),
+        plan.order.data_ptr() if gather else None, plan.top_k, out.data_ptr(), rows, weights.experts, K, weights.N,
+        int(weights.gated), dtype, workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle))
+    return out
+
+
+def awq_moe_combine(y, plan: MoePlan, weights, residual=None, out=None, stream=None):
+    """Each token's rows of y [plan.rows, H], weighted (weights fp32 [T, top_k]) and added up, to `residual` [T, H] where
+    one is given: [T, H].  out may be residual itself."""
+    T, top_k = weights.shape
+    H = y.shape[1]
+    dtype = _dtype16("awq_moe_combine", y, residual, out)
+    _need("awq_moe_combine", y.dtype, y, out)
+    _need("awq_moe_combine", torch.float32, weights)
+    if y.shape != (plan.rows, H) or top_k != plan.top_k or T * top_k != plan.rows or \
+            (residual is not None and residual.shape != (T, H)) or (out is not None and out.shape != (T, H)):
+        raise ValueError("awq_moe_combine: y [rows, H], weights [T, top_k], residual and out [T, H] go with the plan")
+    _on_current_gpu("awq_moe_combine", y, plan.place, weights, residual, out)
+    if out is None:
+        out = torch.empty((T, H), dtype=y.dtype, device=y.device)
+    rs = 0 if residual is None else _row_stride("awq_moe_combine", residual, H)
+    _check("awq_moe_combine", lib.awq_moe_combine(y.data_ptr(), plan.place.data_ptr(), weights.data_ptr(), _ptr(residual),
+                                                  rs, out.data_ptr(), T, top_k, H, plan.rows, dtype,
+                                                  _raw_stream(stream, y.device)))
+    return out
+
+
+def awq_moe(x, up: MoeWeights, down: MoeWeights, weights, plan: MoePlan, residual=None, out=None, workspace=None, stream=None):
+    """A sparse feed-forward layer: x [T, K] through every token's experts, down(silu(gate) * up), weighted and added up
+    (to `residual` where one is given).  `up` is gated, `down` plain; weights and plan from awq_moe_route.  A captured
+    call takes a workspace of the larger of the two products' sizes."""
+    if not up.gated or down.gated or down.K != up.outputs:
+        raise ValueError("awq_moe: up is gated, down is plain, and down takes up's outputs")
+    h = awq_moe_gemm(x, up, plan, gather=True, workspace=workspace, stream=stream)
+    y = awq_moe_gemm(h, down, plan, workspace=workspace, stream=stream)
+    return awq_moe_combine(y, plan, weights, residual=residual, out=out, stream=stream)
+
+
+FP8_BLOCK = 128
+
+
+def _fp8_weights(name, wq, s_w):
+    N, K = wq.shape
+    _need(name, torch.float8_e4m3fn, wq)
+    _need(name, torch.float32, s_w)
+    if s_w.shape != (-(-N // FP8_BLOCK), -(-K // FP8_BLOCK)):
+        raise ValueError(f"{name}: wq is [N, K], s_w [N / 128, K / 128] rounded up")
+    return N, K
+
+
+def awq_fp8_quant_act(x, xq=None, s_x=None, stream=None):
+    """e4m3 codes [M, K] of 16-bit x [M, K] and their fp32 scales [K / 128, M], one for each token and 128 channels."""
+    M, K = x.shape
+    dtype = _dtype16("awq_fp8_quant_act", x)
+    groups = -(-K // FP8_BLOCK)
+    if xq is None:
+        xq = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=x.device)
+    if s_x is None:
+        s_x = torch.empty((groups, M), dtype=torch.float32, device=x.device)
+    _need("awq_fp8_quant_act", torch.float8_e4m3fn, xq)
+    _need("awq_fp8_quant_act", torch.float32, s_x)
+    if xq.shape != (M, K) or s_x.shape != (groups, M):
+        raise ValueError("awq_fp8_quant_act: xq is [M, K], s_x [K / 128, M]")
+    _on_current_gpu("awq_fp8_quant_act", x, xq, s_x)
+    _check("awq_fp8_quant_act", lib.awq_fp8_quant_act(x.data_ptr(), _row_stride("awq_fp8_quant_act", x, K), xq.data_ptr(),
+                                                      s_x.data_ptr(), M, K, dtype, _raw_stream(stream, x.device)))
+    return xq, s_x
+
+
+def awq_fp8_gemm_workspace_bytes(M: int, K: int, N: int) -> int:
+    """Bytes of an awq_fp8_gemm workspace on the current device."""
+    return int(lib.awq_fp8_gemm_workspace_bytes(M, K, N))
+
+
+def awq_fp8_linear_workspace_bytes(M: int, K: int, N: int) -> int:
+    """Bytes of an awq_fp8_linear workspace on the current device."""
+    return int(lib.awq_fp8_linear_workspace_bytes(M, K, N))
+
+
+def _fp8_out(name, out, M, N, dtype, device):
+    if out is None:
+        return torch.empty((M, N), dtype=dtype, device=device)
+    if out.shape != (M, N) or not out.is_contiguous() or out.dtype is not dtype or not out.is_cuda:
+        raise ValueError(f"{name}: out is dense, [M, N], of the output's type")
+    return out
+
+
+def awq_fp8_gemm(xq, s_x, wq, s_w, dtype=torch.float16, out=None, workspace=None, stream=None):
+    """e4m3 codes xq [M, K] with s_x [K / 128, M] times wq [N, K] with s_w [N / 128, K / 128]: [M, N] of `dtype` (fp16 or
+    bf16).  Workspaces as for awq_moe_gemm."""
+    M, K = xq.shape
+    N, wk = _fp8_weights("awq_fp8_gemm", wq, s_w)
+    _need("awq_fp8_gemm", torch.float8_e4m3fn, xq)
+    _need("awq_fp8_gemm", torch.float32, s_x)
+    kind = _DTYPES.get(dtype)
+    if kind is None:
+        raise TypeError("awq_fp8_gemm: outputs are fp16 or bf16")
+    if wk != K or s_x.shape != (-(-K // FP8_BLOCK), M):
+        raise ValueError("awq_fp8_gemm: xq [M, K] and s_x [K / 128, M] go with wq [N, K]")
+    device = xq.device
+    out = _fp8_out("awq_fp8_gemm", out, M, N, dtype, device)
+    _on_current_gpu("awq_fp8_gemm", xq, s_x, wq, s_w, out, workspace)
+    handle = _raw_stream(stream, device)
+    if workspace is None:
+        need = _layer_workspace_need(device.index, "awq_fp8_gemm_workspace_bytes", M, K, N)
+        workspace = _layer_workspace("awq_fp8_gemm", handle, device, need, stream)
+    _check("awq_fp8_gemm", lib.awq_fp8_gemm(xq.data_ptr(), s_x.data_ptr(), wq.data_ptr(), s_w.data_ptr(), out.data_ptr(), M,
+                                            K, N, kind, workspace.data_ptr(),
+                                            workspace.numel() * workspace.element_size(), handle))
+    return out
+
+
+def awq_fp8_linear(x, wq, s_w, out=None, workspace=None, stream=None):
+    """16-bit x [M, K] through a layer of e4m3 weights wq [N, K], s_w [N / 128, K / 128]: quantization and product in one
+    call, [M, N] in x's type.  Workspaces as for awq_moe_gemm (awq_fp8_linear_workspace_bytes)."""
+    M, K = x.shape
+    kind = _dtype16("awq_fp8_linear", x)
+    N, wk = _fp8_weights("awq_fp8_linear", wq, s_w)
+    if wk != K:
+        raise ValueError("awq_fp8_linear: x is [M, K], wq [N, K]")
+    device = x.device
+    out = _fp8_out("awq_fp8_linear", out, M, N, x.dtype, device)
+    _on_current_gpu("awq_fp8_linear", x, wq, s_w, out, workspace)
+    handle = _raw_stream(stream, device)
+    if workspace is None:
+        need = _layer_workspace_need(device.index, "awq_fp8_linear_workspace_bytes", M, K, N)
+        workspace = _layer_workspace("awq_fp8_linear", handle, device, need, stream)
+    _check("awq_fp8_linear", lib.awq_fp8_linear(x.data_ptr(), _row_stride("awq_fp8_linear", x, K), wq.data_ptr(),
+                                                s_w.data_ptr(), out.data_ptr(), M, K, N, kind, workspace.data_ptr(),
+                                                workspace.numel() * workspace.element_size(), handle))
     return out
 
 

@@ -614,6 +614,185 @@ awq_status kv4_attention(const uint16_t* q, int64_t q_stride, const void* cache,
   return from_cuda(launch_kv4_attention(a, head_dim, dtype == AWQ_BF16, workspace, err, (cudaStream_t)stream));
 }
 
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+static bool is_dtype(awq_dtype d) { return d == AWQ_FP16 || d == AWQ_BF16; }
+
+awq_status awq_moe_plan(const int32_t* ids, int64_t R, int32_t experts, int32_t* offsets, int32_t* order, int32_t* place,
+                        awq_stream_t stream) {
+  if (R < 0 || R > kMoeMaxRows || experts < 1 || experts > kMoeMaxExperts) return AWQ_EINVAL;
+  if (!offsets || (R > 0 && (!ids || !order || !place))) return AWQ_ENULL;
+  if (!aligned4(ids) || !aligned4(offsets) || !aligned4(order) || !aligned4(place)) return AWQ_EALIGN;
+  awq_status st = check_arch();
+  if (st != AWQ_OK) return st;
+  return from_cuda(launch_moe_plan(ids, R, experts, offsets, order, place, (cudaStream_t)stream));
+}
+
+awq_status awq_moe_route(const void* logits, int64_t logits_stride, int64_t T, int32_t experts, int32_t top_k,
+                         int32_t normalize, awq_logits_type type, int32_t* ids, float* weights, int32_t* offsets,
+                         int32_t* order, int32_t* place, awq_stream_t stream) {
+  if (experts < 1 || experts > kMoeMaxExperts || top_k < 1 || top_k > experts || top_k > kMoeMaxTopK || T < 0 ||
+      T > kMoeMaxRows / top_k || logits_stride < experts ||
+      (type != AWQ_LOGITS_FP16 && type != AWQ_LOGITS_BF16 && type != AWQ_LOGITS_FP32))
+    return AWQ_EINVAL;
+  if (T > 0 && (!logits || !ids || !weights)) return AWQ_ENULL;
+  if (T > 0 && ((offsets != nullptr) != (order != nullptr) || (offsets != nullptr) != (place != nullptr))) return AWQ_ENULL;
+  const uintptr_t element = type == AWQ_LOGITS_FP32 ? 4 : 2;
+  if ((reinterpret_cast<uintptr_t>(logits) & (element - 1)) != 0 || !aligned4(ids) || !aligned4(weights) ||
+      !aligned4(offsets) || !aligned4(order) || !aligned4(place))
+    return AWQ_EALIGN;
+  if (T == 0 && !offsets) return AWQ_OK;
+  awq_status st = check_arch();
+  if (st != AWQ_OK) return st;
+  return from_cuda(launch_moe_route(logits, logits_stride, T, experts, top_k, normalize != 0, (int)type, ids, weights,
+                                    offsets, order, place, (cudaStream_t)stream));
+}
+
+static bool moe_shape_ok(int32_t experts, int64_t K, int64_t N, int32_t gated) {
+  return experts >= 1 && experts <= kMoeMaxExperts && K >= kGroup && K <= kMoeMaxSize && K % kGroup == 0 && N >= 1 &&
+         N <= kMoeMaxSize && N % (gated ? 64 : 32) == 0;
+}
+
+size_t awq_moe_prepacked_bytes(int32_t experts, int64_t K, int64_t N, int32_t gated) {
+  if (!moe_shape_ok(experts, K, N, gated)) return 0;
+  return (size_t)experts * (size_t)moe_tiles(N, gated != 0) * (size_t)(K / kGroup) * kMoeUnitBytes;
+}
+
+awq_status awq_moe_prepack(const int32_t* qweight, const int32_t* qzeros, const uint16_t* scales, int32_t experts, int64_t K,
+                           int64_t N, int32_t group_size, int32_t gated, void* packed, size_t packed_bytes,
+                           awq_stream_t stream) {
+  const size_t need = awq_moe_prepacked_bytes(experts, K, N, gated);
+  if (need == 0 || group_size != kGroup || packed_bytes < need) return AWQ_EINVAL;
+  if (!qweight || !scales || !packed) return AWQ_ENULL;
+  if (!aligned16(qweight) || !aligned16(qzeros) || !aligned16(scales) || !aligned16(packed)) return AWQ_EALIGN;
+  awq_status st = check_arch();
+  if (st != AWQ_OK) return st;
+  return from_cuda(launch_moe_prepack(reinterpret_cast<const uint32_t*>(qweight), reinterpret_cast<const uint32_t*>(qzeros),
+                                      scales, experts, K, N, gated != 0, static_cast<uint8_t*>(packed),
+                                      (cudaStream_t)stream));
+}
+
+awq_status awq_moe_unprepack(const void* packed, int32_t experts, int64_t K, int64_t N, int32_t gated, int32_t* qweight,
+                             int32_t* qzeros, uint16_t* scales, awq_stream_t stream) {
+  if (!moe_shape_ok(experts, K, N, gated)) return AWQ_EINVAL;
+  if (!qweight || !scales || !packed) return AWQ_ENULL;
+  if (!aligned16(qweight) || !aligned16(qzeros) || !aligned16(scales) || !aligned16(packed)) return AWQ_EALIGN;
+  awq_status st = check_arch();
+  if (st != AWQ_OK) return st;
+  return from_cuda(launch_moe_unprepack(static_cast<const uint8_t*>(packed), experts, K, N, gated != 0,
+                                        reinterpret_cast<uint32_t*>(qweight), reinterpret_cast<uint32_t*>(qzeros), scales,
+                                        (cudaStream_t)stream));
+}
+
+size_t awq_moe_gemm_workspace_bytes(int64_t R, int32_t experts, int64_t K, int64_t N, int32_t gated) {
+  if (R < 1 || R > kMoeMaxRows || !moe_shape_ok(experts, K, N, gated)) return 0;
+  return moe_gemm_workspace(R, experts, K, N, gated != 0);
+}
+
+awq_status awq_moe_gemm(const uint16_t* x, int64_t x_stride, int64_t x_rows, const void* packed, const int32_t* offsets,
+                        const int32_t* order, int32_t top_k, uint16_t* y, int64_t R, int32_t experts, int64_t K, int64_t N,
+                        int32_t gated, awq_dtype dtype, void* workspace, size_t workspace_bytes, awq_stream_t stream) {
+  if (R < 0 || R > kMoeMaxRows || x_rows < 0 || x_rows > kMoeMaxRows || !moe_shape_ok(experts, K, N, gated) ||
+      x_stride < K || x_stride % 8 != 0 || !is_dtype(dtype) || (order && (top_k < 1 || top_k > kMoeMaxTopK)))
+    return AWQ_EINVAL;
+  if (R == 0) return AWQ_OK;
+  if (!packed || !offsets || !y || !x) return AWQ_ENULL;
+  if (!aligned16(x) || !aligned16(packed) || !aligned16(y) || !aligned4(offsets) || !aligned4(order)) return AWQ_EALIGN;
+  awq_status st = check_workspace(moe_gemm_workspace(R, experts, K, N, gated != 0), workspace, workspace_bytes);
+  if (st != AWQ_OK) return st;
+  st = check_arch();
+  if (st != AWQ_OK) return st;
+  int* err = device_error_ptr();
+  if (!err) return AWQ_ECUDA;
+  const MoeGemmArgs a{x, x_stride, x_rows, static_cast<const uint8_t*>(packed), offsets, order, order ? top_k : 1,
+                      y, R,        experts, K, N, (int)moe_tiles(N, gated != 0)};
+  return from_cuda(launch_moe_gemm(a, gated != 0, dtype == AWQ_BF16, workspace, err, (cudaStream_t)stream));
+}
+
+awq_status awq_moe_combine(const uint16_t* y, const int32_t* place, const float* weights, const uint16_t* residual,
+                           int64_t res_stride, uint16_t* out, int64_t T, int32_t top_k, int64_t H, int64_t R,
+                           awq_dtype dtype, awq_stream_t stream) {
+  if (top_k < 1 || top_k > kMoeMaxTopK || T < 0 || T > kMoeMaxRows / top_k || R < 0 || R > kMoeMaxRows || H < 8 ||
+      H > kMoeMaxSize || H % 8 != 0 || !is_dtype(dtype))
+    return AWQ_EINVAL;
+  if (residual && (res_stride < H || res_stride % 8 != 0)) return AWQ_EINVAL;
+  if (T == 0) return AWQ_OK;
+  if ((R > 0 && !y) || !place || !weights || !out) return AWQ_ENULL;
+  if (!aligned16(y) || !aligned16(residual) || !aligned16(out) || !aligned4(place) || !aligned4(weights)) return AWQ_EALIGN;
+  awq_status st = check_arch();
+  if (st != AWQ_OK) return st;
+  return from_cuda(launch_moe_combine(y, place, weights, residual, res_stride, out, T, top_k, H, R, dtype == AWQ_BF16,
+                                      (cudaStream_t)stream));
+}
+
+// ---- e4m3 linear layers
+
+static bool fp8_shape_ok(int64_t M, int64_t K, int64_t N) {
+  return M >= 0 && M <= kMoeMaxRows && K >= 16 && K <= kMoeMaxSize && K % 16 == 0 && N >= 8 && N <= kMoeMaxSize && N % 8 == 0;
+}
+
+awq_status awq_fp8_quant_act(const uint16_t* x, int64_t x_stride, uint8_t* xq, float* s_x, int64_t M, int64_t K,
+                             awq_dtype dtype, awq_stream_t stream) {
+  if (!fp8_shape_ok(M, K, 8) || x_stride < K || x_stride % 8 != 0 || !is_dtype(dtype)) return AWQ_EINVAL;
+  if (M == 0) return AWQ_OK;
+  if (!x || !xq || !s_x) return AWQ_ENULL;
+  if (!aligned16(x) || !aligned16(xq) || !aligned4(s_x)) return AWQ_EALIGN;
+  awq_status st = check_arch();
+  if (st != AWQ_OK) return st;
+  return from_cuda(launch_fp8_quant(x, x_stride, xq, s_x, M, K, dtype == AWQ_BF16, (cudaStream_t)stream));
+}
+
+size_t awq_fp8_gemm_workspace_bytes(int64_t M, int64_t K, int64_t N) {
+  return fp8_shape_ok(M, K, N) && M > 0 ? fp8_gemm_workspace(M, K, N) : 0;
+}
+
+awq_status awq_fp8_gemm(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w, uint16_t* y, int64_t M,
+                        int64_t K, int64_t N, awq_dtype dtype, void* workspace, size_t workspace_bytes,
+                        awq_stream_t stream) {
+  if (!fp8_shape_ok(M, K, N) || !is_dtype(dtype)) return AWQ_EINVAL;
+  if (M == 0) return AWQ_OK;
+  if (!xq || !s_x || !wq || !s_w || !y) return AWQ_ENULL;
+  if (!aligned16(xq) || !aligned16(wq) || !aligned16(y) || !aligned4(s_x) || !aligned4(s_w)) return AWQ_EALIGN;
+  awq_status st = check_workspace(fp8_gemm_workspace(M, K, N), workspace, workspace_bytes);
+  if (st != AWQ_OK) return st;
+  st = check_arch();
+  if (st != AWQ_OK) return st;
+  int* err = device_error_ptr();
+  if (!err) return AWQ_ECUDA;
+  return from_cuda(launch_fp8_gemm(Fp8GemmArgs{xq, s_x, wq, s_w, y, M, K, N}, dtype == AWQ_BF16, workspace, err,
+                                   (cudaStream_t)stream));
+}
+
+// The product's own workspace, whose counters no other call's codes may fall on, then codes and scales.
+static size_t fp8_codes_offset(int64_t M, int64_t K, int64_t N) {
+  const size_t own = align256(fp8_gemm_workspace(M, K, N));
+  return own < kCounterBytes ? kCounterBytes : own;
+}
+size_t awq_fp8_linear_workspace_bytes(int64_t M, int64_t K, int64_t N) {
+  if (!fp8_shape_ok(M, K, N) || M == 0) return 0;
+  return fp8_codes_offset(M, K, N) + align256((size_t)M * (size_t)K) + (size_t)M * (size_t)((K + kGroup - 1) / kGroup) * 4;
+}
+
+awq_status awq_fp8_linear(const uint16_t* x, int64_t x_stride, const uint8_t* wq, const float* s_w, uint16_t* y, int64_t M,
+                          int64_t K, int64_t N, awq_dtype dtype, void* workspace, size_t workspace_bytes,
+                          awq_stream_t stream) {
+  if (!fp8_shape_ok(M, K, N) || x_stride < K || x_stride % 8 != 0 || !is_dtype(dtype)) return AWQ_EINVAL;
+  if (M == 0) return AWQ_OK;
+  if (!x || !wq || !s_w || !y) return AWQ_ENULL;
+  if (!aligned16(x) || !aligned16(wq) || !aligned16(y) || !aligned4(s_w)) return AWQ_EALIGN;
+  awq_status st = check_workspace(awq_fp8_linear_workspace_bytes(M, K, N), workspace, workspace_bytes);
+  if (st != AWQ_OK) return st;
+  st = check_arch();
+  if (st != AWQ_OK) return st;
+  int* err = device_error_ptr();
+  if (!err) return AWQ_ECUDA;
+  uint8_t* xq = static_cast<uint8_t*>(workspace) + fp8_codes_offset(M, K, N);
+  float* s_x = reinterpret_cast<float*>(xq + align256((size_t)M * (size_t)K));
+  const cudaStream_t s = (cudaStream_t)stream;
+  const bool bf16 = dtype == AWQ_BF16;
+  if (launch_fp8_quant(x, x_stride, xq, s_x, M, K, bf16, s) != cudaSuccess) return AWQ_ECUDA;
+  return from_cuda(launch_fp8_gemm(Fp8GemmArgs{xq, s_x, wq, s_w, y, M, K, N}, bf16, workspace, err, s));
+}
+
 awq_status awq_last_device_error(int32_t* code) {
   if (!code) return AWQ_ENULL;
   *code = 0;

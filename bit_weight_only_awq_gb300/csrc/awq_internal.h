@@ -197,4 +197,58 @@ size_t kv4_prefill_workspace(int64_t T, int64_t B, int max_q, int heads, int kv_
 cudaError_t launch_kv4_prefill(const Kv4AttnArgs& a, int min_rows, int dim, bool bf16, void* ws, int* err, cudaStream_t s);
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, int dim, bool bf16, void* ws, int* err, cudaStream_t s);
 
+// ---- router, plan and combination of a layer with experts (moe_route.cu)
+constexpr int kMoeMaxExperts = 512, kMoeMaxTopK = 32;
+constexpr int64_t kMoeMaxRows = 1 << 30;
+constexpr int64_t kMoeMaxSize = 1 << 20;  // K and N
+cudaError_t launch_moe_plan(const int32_t* ids, int64_t R, int experts, int32_t* offsets, int32_t* order, int32_t* place,
+                            cudaStream_t s);
+cudaError_t launch_moe_route(const void* logits, int64_t stride, int64_t T, int experts, int top_k, bool normalize, int type,
+                             int32_t* ids, float* weights, int32_t* offsets, int32_t* order, int32_t* place,
+                             cudaStream_t s);
+cudaError_t launch_moe_combine(const uint16_t* y, const int32_t* place, const float* weights, const uint16_t* residual,
+                               int64_t res_stride, uint16_t* out, int64_t T, int top_k, int64_t H, int64_t R, bool bf16,
+                               cudaStream_t s);
+
+// ---- prepared weights of the experts (moe_pack.cu) and the grouped product on them (moe_gemm.cu).  Layout of a unit (256
+// columns x 128 rows): include/awq.h.
+constexpr int kMoeZeroOffset = 16384, kMoeScaleOffset = kMoeZeroOffset + 128, kMoeUnitBytes = kMoeScaleOffset + 512;
+static_assert(kMoeUnitBytes == 17024 && kMoeUnitBytes % 16 == 0, "codes | zero points | scales");
+// Byte of rows 32 chunk .. + 31 of column c (0..255).
+__host__ __device__ constexpr int moe_code_offset(int c, int chunk) { return ((c >> 7) * 4 + chunk) * 2048 + (c & 127) * 16; }
+inline int64_t moe_tiles(int64_t N, bool gated) { return gated ? (N / 2 + 127) / 128 : (N + 255) / 256; }
+cudaError_t launch_moe_prepack(const uint32_t* qw, const uint32_t* qz, const uint16_t* sc, int experts, int64_t K, int64_t N,
+                               bool gated, uint8_t* packed, cudaStream_t s);
+cudaError_t launch_moe_unprepack(const uint8_t* packed, int experts, int64_t K, int64_t N, bool gated, uint32_t* qw,
+                                 uint32_t* qz, uint16_t* sc, cudaStream_t s);
+struct MoeGemmArgs {
+  const uint16_t* x;
+  int64_t x_stride, x_rows;
+  const uint8_t* packed;
+  const int32_t* offsets;
+  const int32_t* order;  // nullptr: x holds rows
+  int top_k;
+  uint16_t* y;
+  int64_t R;
+  int experts;
+  int64_t K, N;  // N: both halves when gated
+  int tiles;
+};
+size_t moe_gemm_workspace(int64_t R, int experts, int64_t K, int64_t N, bool gated);
+cudaError_t launch_moe_gemm(const MoeGemmArgs& a, bool gated, bool bf16, void* ws, int* err, cudaStream_t s);
+
+// ---- e4m3 linear layers with scales for blocks of 128 (fp8_linear.cu)
+cudaError_t launch_fp8_quant(const uint16_t* x, int64_t x_stride, uint8_t* xq, float* s_x, int64_t M, int64_t K, bool bf16,
+                             cudaStream_t s);
+struct Fp8GemmArgs {
+  const uint8_t* xq;
+  const float* s_x;
+  const uint8_t* wq;
+  const float* s_w;
+  uint16_t* y;
+  int64_t M, K, N;
+};
+size_t fp8_gemm_workspace(int64_t M, int64_t K, int64_t N);
+cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, bool bf16, void* ws, int* err, cudaStream_t s);
+
 }  // namespace awq

@@ -1,0 +1,240 @@
+// The router of a layer with experts: softmax and top_k of each token, the plan that puts the chosen rows in the experts'
+// order, and the weighted sum of a token's rows.
+//
+// Bound by latency: 8191 tokens' fp32 logits over 128 experts are 4 MB.  A warp has a token; its lanes hold the logits
+// in registers, as keys whose order as whole numbers is the logits' order, and every choice is one reduction of keys and
+// one ballot for the lowest expert among equals.
+#include <type_traits>
+
+#include "awq_internal.h"
+#include "awq_types.cuh"
+
+namespace awq {
+namespace {
+
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+
+// A float as a key: larger for a larger value, equal for 0 and -0, above all others for a NaN.  0 is no value's key.
+__device__ __forceinline__ uint32_t key_of(float v) {
+  if (v != v) return 0xFFFFFFFFu;
+  const uint32_t u = __float_as_uint(v + 0.f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t key) {
+  if (key == 0xFFFFFFFFu) return __uint_as_float(0x7FFFFFFFu);
+  return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+}
+
+template <int TYPE>
+__device__ __forceinline__ float read_logit(const void* p, int64_t i) {
+  if constexpr (TYPE == 2) return static_cast<const float*>(p)[i];
+  else if constexpr (TYPE == 1) return __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
+  else return __half2float(static_cast<const __half*>(p)[i]);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(kAll, v, d);
+  return v;
+}
+
+// One token, by one warp: choice j's expert and weight end up in lane j.
+template <int TYPE, int L>
+__device__ __forceinline__ void route_token(const void* logits, int64_t at, int experts, int top_k, bool normalize, int lane,
+                                            int& id, float& weight) {
+  uint32_t key[L];
+#pragma unroll
+  for (int l = 0; l < L; ++l) {
+    const int e = lane + 32 * l;
+    key[l] = e < experts ? key_of(read_logit<TYPE>(logits, at + e)) : 0u;
+  }
+  uint32_t most = 0u;
+#pragma unroll
+  for (int l = 0; l < L; ++l) most = max(most, key[l]);
+  const float top = value_of(__reduce_max_sync(kAll, most));
+  float sum = 0.f;
+  if (!normalize) {
+#pragma unroll
+    for (int l = 0; l < L; ++l)
+      if (key[l] != 0u) sum += expf(value_of(key[l]) - top);
+    sum = warp_sum(sum);
+  }
+  id = 0;
+  float mine = 0.f;
+  for (int j = 0; j < top_k; ++j) {
+    uint32_t best = 0u;
+    int where = 0;
+#pragma unroll
+    for (int l = 0; l < L; ++l)
+      if (key[l] > best) {
+        best = key[l];
+        where = l;
+      }
+    const uint32_t k = __reduce_max_sync(kAll, best);
+    const int e = (int)__reduce_min_sync(kAll, best == k ? (uint32_t)(lane + 32 * where) : kAll);
+#pragma unroll
+    for (int l = 0; l < L; ++l)
+      if (lane + 32 * l == e) key[l] = 0u;
+    if (lane == j) {
+      id = e;
+      mine = expf(value_of(k) - top);
+    }
+  }
+  if (normalize) sum = warp_sum(mine);
+  // a row of nothing but -inf has no weights; a NaN or +inf makes `top - top` NaN, and every weight with it
+  weight = top == -INFINITY ? 0.f : mine / sum;
+  if (!(top - top == 0.f) && top != -INFINITY) weight = __uint_as_float(0x7FFFFFFFu);
+}
+
+// Class of a position: its expert, or `experts` for an id that is none.
+__device__ __forceinline__ int class_of(int id, int experts) { return (unsigned)id < (unsigned)experts ? id : experts; }
+
+// The warp's positions [begin, end) (multiples of 32 apart): how many are of a class below e, and of class e.
+__device__ __forceinline__ void count_class(const int32_t* ids, int begin, int end, int e, int experts, int lane, int& below,
+                                            int& equal) {
+  below = equal = 0;
+#pragma unroll 4
+  for (int i = begin; i < end; i += 32) {
+    const int c = i + lane < end ? class_of(ids[i + lane], experts) : experts + 1;
+    below += __popc(__ballot_sync(kAll, c < e));
+    equal += __popc(__ballot_sync(kAll, c == e));
+  }
+}
+// Writes the rows of class e among them, from row `row` on.
+__device__ __forceinline__ void place_class(const int32_t* ids, int begin, int end, int e, int experts, int lane, int row,
+                                            int32_t* order, int32_t* place) {
+#pragma unroll 4
+  for (int i = begin; i < end; i += 32) {
+    const bool in = i + lane < end && class_of(ids[i + lane], experts) == e;
+    const uint32_t votes = __ballot_sync(kAll, in);
+    if (in) {
+      const int r = row + __popc(votes & ((1u << lane) - 1u));
+      order[r] = e < experts ? i + lane : -1;
+      place[i + lane] = e < experts ? r : -1;
+    }
+    row += __popc(votes);
+  }
+}
+
+// A CTA for each class (expert, and "none"): counts what comes before its rows, then writes them.
+__global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ ids, int R, int experts,
+                                                    int32_t* __restrict__ offsets, int32_t* __restrict__ order,
+                                                    int32_t* __restrict__ place) {
+  __shared__ int s_below[32], s_equal[32];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, e = blockIdx.x;
+  const int share = (int)(((int64_t)R + 1023) / 1024 * 32);
+  const int begin = (int)min((int64_t)R, (int64_t)warp * share), end = (int)min((int64_t)R, (int64_t)(warp + 1) * share);
+  int below, equal;
+  count_class(ids, begin, end, e, experts, lane, below, equal);
+  if (lane == 0) {
+    s_below[warp] = below;
+    s_equal[warp] = equal;
+  }
+  __syncthreads();
+  int row = s_below[lane], before = lane < warp ? s_equal[lane] : 0;
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) {
+    row += __shfl_xor_sync(kAll, row, d);
+    before += __shfl_xor_sync(kAll, before, d);
+  }
+  if (threadIdx.x == 0) offsets[e] = row;
+  place_class(ids, begin, end, e, experts, lane, row + before, order, place);
+}
+
+template <int TYPE, int L>
+__global__ void __launch_bounds__(256) route_kernel(const void* __restrict__ logits, int64_t stride, int T, int experts,
+                                                    int top_k, int normalize, int32_t* __restrict__ ids,
+                                                    float* __restrict__ weights) {
+  const int lane = threadIdx.x % 32;
+  const int64_t t = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+  if (t >= T) return;
+  int id;
+  float weight;
+  route_token<TYPE, L>(logits, t * stride, experts, top_k, normalize != 0, lane, id, weight);
+  if (lane < top_k) {
+    ids[t * top_k + lane] = id;
+    weights[t * top_k + lane] = weight;
+  }
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(256) combine_kernel(const uint16_t* __restrict__ y, const int32_t* __restrict__ place,
+                                                      const float* __restrict__ weights, const uint16_t* residual,
+                                                      int64_t res_stride, uint16_t* out, int64_t T, int top_k, int64_t H,
+                                                      int64_t R) {
+  const int64_t vec = H / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= T * vec) return;
+  const int64_t t = i / vec, c = (i - t * vec) * 8;
+  float sum[8];
+#pragma unroll
+  for (int p = 0; p < 8; ++p) sum[p] = 0.f;
+  if (residual) {
+    const uint4 v = *reinterpret_cast<const uint4*>(residual + t * res_stride + c);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const float2 f = unpack2<BF16>(w[p]);
+      sum[2 * p] = f.x;
+      sum[2 * p + 1] = f.y;
+    }
+  }
+#pragma unroll 4
+  for (int j = 0; j < top_k; ++j) {
+    const int r = place[t * top_k + j];
+    if (r < 0 || r >= R) continue;
+    const float weight = weights[t * top_k + j];
+    const uint4 v = *reinterpret_cast<const uint4*>(y + r * H + c);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const float2 f = unpack2<BF16>(w[p]);
+      sum[2 * p] = fmaf(weight, f.x, sum[2 * p]);
+      sum[2 * p + 1] = fmaf(weight, f.y, sum[2 * p + 1]);
+    }
+  }
+  *reinterpret_cast<uint4*>(out + t * H + c) = make_uint4(pack2<BF16>(sum[0], sum[1]), pack2<BF16>(sum[2], sum[3]),
+                                                          pack2<BF16>(sum[4], sum[5]), pack2<BF16>(sum[6], sum[7]));
+}
+
+}  // namespace
+
+cudaError_t launch_moe_plan(const int32_t* ids, int64_t R, int experts, int32_t* offsets, int32_t* order, int32_t* place,
+                            cudaStream_t s) {
+  plan_kernel<<<experts + 1, 1024, 0, s>>>(ids, (int)R, experts, offsets, order, place);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_moe_route(const void* logits, int64_t stride, int64_t T, int experts, int top_k, bool normalize, int type,
+                             int32_t* ids, float* weights, int32_t* offsets, int32_t* order, int32_t* place,
+                             cudaStream_t s) {
+  if (T > 0) {
+    auto launch = [&](auto kernel) {
+      kernel<<<(unsigned)((T + 7) / 8), 256, 0, s>>>(logits, stride, (int)T, experts, top_k, normalize, ids, weights);
+      return cudaGetLastError();
+    };
+    auto by_size = [&](auto t) {
+      constexpr int kType = decltype(t)::value;
+      return experts <= 32    ? launch(route_kernel<kType, 1>)
+             : experts <= 64  ? launch(route_kernel<kType, 2>)
+             : experts <= 128 ? launch(route_kernel<kType, 4>)
+             : experts <= 256 ? launch(route_kernel<kType, 8>)
+                              : launch(route_kernel<kType, 16>);
+    };
+    const cudaError_t e = type == 0   ? by_size(std::integral_constant<int, 0>{})
+                          : type == 1 ? by_size(std::integral_constant<int, 1>{})
+                                      : by_size(std::integral_constant<int, 2>{});
+    if (e != cudaSuccess) return e;
+  }
+  return offsets ? launch_moe_plan(ids, T * top_k, experts, offsets, order, place, s) : cudaSuccess;
+}
+
+cudaError_t launch_moe_combine(const uint16_t* y, const int32_t* place, const float* weights, const uint16_t* residual,
+                               int64_t res_stride, uint16_t* out, int64_t T, int top_k, int64_t H, int64_t R, bool bf16,
+                               cudaStream_t s) {
+  const int64_t threads = T * (H / 8);
+  (bf16 ? combine_kernel<true> : combine_kernel<false>)<<<(unsigned)((threads + 255) / 256), 256, 0, s>>>(
+      y, place, weights, residual, res_stride, out, T, top_k, H, R);
+  return cudaGetLastError();
+}
+
+}  // namespace awq

@@ -508,6 +508,125 @@ awq_status kv4_attention(const uint16_t *q, int64_t q_stride, const void *cache,
                          awq_stream_t stream);
 
 /*
+ * The feed-forward layer with experts
+ * -----------------------------------
+ * A router chooses top_k of `experts` layers for each token; every chosen (token, expert) is a row.  The plan puts
+ * the R = T * top_k rows in the experts' order, the grouped product multiplies each expert's rows by that expert's
+ * 4-bit weights, and the combination adds the rows of a token up again.  A position is t * top_k + j, token t's
+ * choice j.  Lengths are read on the device only, so a captured graph follows the routing.
+ * The pages describe none of this; its layers are the group-wise 4-bit layers of the entry points above.
+ *
+ * awq_moe_plan -- offsets int32 [experts + 1]: rows of expert e are offsets[e] .. offsets[e + 1] - 1; order int32 [R]:
+ * the position of each row, those of one expert in ascending order; place int32 [R]: the row of each position.
+ * A position whose id is outside [0, experts) has no row: its place is -1, and order is -1 from offsets[experts]
+ * on.  ids int32 [R].  0 <= R <= 2^30, 1 <= experts <= 512; all pointers 4-byte aligned.  R = 0 writes offsets only.
+ */
+awq_status awq_moe_plan(const int32_t *ids, int64_t R, int32_t experts, int32_t *offsets, int32_t *order,
+                        int32_t *place, awq_stream_t stream);
+
+/* Type of the router's logits. */
+typedef enum { AWQ_LOGITS_FP16 = 0, AWQ_LOGITS_BF16 = 1, AWQ_LOGITS_FP32 = 2 } awq_logits_type;
+
+/*
+ * awq_moe_route -- softmax over a token's logits, its top_k experts in descending order (of equals the lowest
+ * first) and, unless offsets, order and place are all NULL, their plan.
+ *   p_e = exp(l_e - max l) / sum exp(l - max l);  weights[t, j] = p_id, divided by the chosen p's sum if normalize != 0
+ * all in fp32.  logits [T, experts] with row stride logits_stride (elements) and of the given type; ids int32
+ * [T, top_k]; weights fp32 [T, top_k].  A logit of -inf is an expert that gets weight 0; a row of nothing else gets
+ * weights 0.  A row that holds a NaN or +inf gets NaN weights.  The ids are distinct and valid in every case (a NaN
+ * counts as the largest).  1 <= experts <= 512, 1 <= top_k <= min(experts, 32), T * top_k <= 2^30.
+ */
+awq_status awq_moe_route(const void *logits, int64_t logits_stride, int64_t T, int32_t experts, int32_t top_k,
+                         int32_t normalize, awq_logits_type type, int32_t *ids, float *weights, int32_t *offsets,
+                         int32_t *order, int32_t *place, awq_stream_t stream);
+
+/*
+ * Prepared weights of the experts.  The grouped product reads its weights from a copy laid out for it, made once
+ * when the layer is loaded: codes, zero points and scales of the AWQ layers, rearranged.  A tile is 256 columns: of
+ * a plain layer columns 256 j .. 256 j + 255; of a gated one (N = 2 I columns, gate first) gate columns 128 j .. + 127
+ * and the same columns of up.  For each expert, tile and 128-row group (in this order) one 17024-byte unit:
+ *   - codes: [half b: 2][chunk c: 4][column n: 128][word w: 4] uint32, nibble i of a word the code of column
+ *     128 b + n of the tile and row 32 c + 8 w + map[i], map = [0, 2, 4, 6, 1, 3, 5, 7];
+ *   - zero points: [column: 256] nibbles, the even column in the low half of a byte;
+ *   - scales: [column: 256], 16 bits.
+ * Columns beyond the layer hold code 0, zero point 0 and scale 0.
+ *
+ * awq_moe_prepacked_bytes -- experts * tiles * (K / 128) * 17024; 0 for a shape outside K % 128 == 0, N % 32 == 0
+ * (N % 64 == 0 when gated), K, N >= 1, K, N <= 2^20, 1 <= experts <= 512.
+ *
+ * awq_moe_prepack -- writes that copy of qweight int32 [experts, K, N/8], qzeros int32 [experts, K/128, N/8] (NULL:
+ * symmetric, z = 8), scales 16-bit [experts, K/128, N] (fp16 or bf16).  group_size == 128.  AWQ_EINVAL where
+ * packed_bytes is below the size needed.  awq_moe_unprepack is the inverse (qzeros may be NULL).
+ */
+size_t awq_moe_prepacked_bytes(int32_t experts, int64_t K, int64_t N, int32_t gated);
+awq_status awq_moe_prepack(const int32_t *qweight, const int32_t *qzeros, const uint16_t *scales, int32_t experts,
+                           int64_t K, int64_t N, int32_t group_size, int32_t gated, void *packed,
+                           size_t packed_bytes, awq_stream_t stream);
+awq_status awq_moe_unprepack(const void *packed, int32_t experts, int64_t K, int64_t N, int32_t gated,
+                             int32_t *qweight, int32_t *qzeros, uint16_t *scales, awq_stream_t stream);
+
+/*
+ * awq_moe_gemm -- the products of all experts, each with its rows, in one call:
+ *   a[r] = x[src(r)] W_e,  W = RN16((q - z) s),  y[r] = RN16(a[r]), or gated RN16(silu(gate) * up) with
+ *   (gate, up) the two halves of a[r] and silu(v) = v / (1 + exp(-v)); sums, silu and product in fp32
+ * for the rows r of every expert e, offsets[e] <= r < offsets[e + 1].  src(r) = order[r] / top_k where order is given
+ * (x holds tokens), r where it is NULL (x holds rows).  x 16-bit [x_rows, K] with row stride x_stride, y [R, N] dense,
+ * [R, N / 2] when gated; packed from awq_moe_prepack with the same sizes.  Rows of y outside every expert's are not
+ * written.  Offsets are clamped to [0, R] and never run backwards; a src outside [0, x_rows) reads as zeros.
+ * The result does not depend on timing: split sums are added in a fixed order.
+ * x_stride % 8 == 0 and >= K, R and x_rows <= 2^30; sizes otherwise as for awq_moe_prepack.  R = 0 is a no-op.
+ * Workspace: awq_moe_gemm_workspace_bytes(), same contract as awq_gemv's; its CTAs wait (bounded) for one another's
+ * partial sums, so the call assumes that they can all be resident at once.
+ */
+size_t awq_moe_gemm_workspace_bytes(int64_t R, int32_t experts, int64_t K, int64_t N, int32_t gated);
+awq_status awq_moe_gemm(const uint16_t *x, int64_t x_stride, int64_t x_rows, const void *packed,
+                        const int32_t *offsets, const int32_t *order, int32_t top_k, uint16_t *y, int64_t R,
+                        int32_t experts, int64_t K, int64_t N, int32_t gated, awq_dtype dtype, void *workspace,
+                        size_t workspace_bytes, awq_stream_t stream);
+
+/*
+ * awq_moe_combine -- out[t] = RN16(residual[t] + sum_j weights[t, j] * y[place[t, j]]), j in ascending order, in fp32.
+ * y 16-bit [R, H] dense; place int32, weights fp32 [T, top_k]; residual 16-bit [T, H] with row stride res_stride, or
+ * NULL; out [T, H] dense (may be residual itself when that is dense).  A choice whose place is outside [0, R) adds
+ * nothing.  H % 8 == 0, 1 <= top_k <= 32, T * top_k and R <= 2^30.  T = 0 is a no-op.
+ */
+awq_status awq_moe_combine(const uint16_t *y, const int32_t *place, const float *weights, const uint16_t *residual,
+                           int64_t res_stride, uint16_t *out, int64_t T, int32_t top_k, int64_t H, int64_t R,
+                           awq_dtype dtype, awq_stream_t stream);
+
+/*
+ * Linear layers in 8-bit floating point
+ * -------------------------------------
+ * Weights e4m3 [N, K] (row-major: K dense) with an fp32 scale for each block of 128 x 128, s_w [ceil(N / 128),
+ * ceil(K / 128)]; activations e4m3 [M, K] with an fp32 scale for each token and 128 channels, s_x [ceil(K / 128), M].
+ * The last blocks may be cut short.  e4m3 has no infinities: the largest value is 448, 0x7F and 0xFF are NaN.
+ * The pages describe none of this.
+ *
+ * awq_fp8_quant_act -- s_x = RN32(max|x| / 448) over a token's 128 channels, xq = e4m3(RN32(x / s_x)), to nearest
+ * even.  Channels that are all zero get scale 0 and codes 0; channels with a NaN or an infinity get a NaN scale and
+ * codes 0, so that the product shows it.  x 16-bit [M, K] with row stride x_stride; K % 16 == 0, 16 <= K <= 2^20,
+ * x_stride % 8 == 0 and >= K, 0 <= M <= 2^30.
+ *
+ * awq_fp8_gemm -- y[m, n] = RN16(sum_g s_x[g, m] s_w[n / 128, g] sum_{k in block g} xq[m, k] wq[n, k]), sums in fp32:
+ * the products of one block on the tensor cores, the blocks' sums scaled and added in registers.  y [M, N] dense,
+ * fp16 or bf16; N % 8 == 0, 8 <= N <= 2^20.  Workspace: awq_fp8_gemm_workspace_bytes(), contract and residency as for
+ * awq_moe_gemm's.  M = 0 is a no-op.
+ *
+ * awq_fp8_linear -- both in one call, from 16-bit activations; the codes and their scales live in the workspace
+ * (awq_fp8_linear_workspace_bytes()).  Bit-identical to the two calls.
+ */
+awq_status awq_fp8_quant_act(const uint16_t *x, int64_t x_stride, uint8_t *xq, float *s_x, int64_t M, int64_t K,
+                             awq_dtype dtype, awq_stream_t stream);
+size_t awq_fp8_gemm_workspace_bytes(int64_t M, int64_t K, int64_t N);
+awq_status awq_fp8_gemm(const uint8_t *xq, const float *s_x, const uint8_t *wq, const float *s_w, uint16_t *y,
+                        int64_t M, int64_t K, int64_t N, awq_dtype dtype, void *workspace, size_t workspace_bytes,
+                        awq_stream_t stream);
+size_t awq_fp8_linear_workspace_bytes(int64_t M, int64_t K, int64_t N);
+awq_status awq_fp8_linear(const uint16_t *x, int64_t x_stride, const uint8_t *wq, const float *s_w, uint16_t *y,
+                          int64_t M, int64_t K, int64_t N, awq_dtype dtype, void *workspace,
+                          size_t workspace_bytes, awq_stream_t stream);
+
+/*
  * awq_last_device_error -- reads and clears the device-side error word of the
  * current device (synchronous: waits for the device).  *code receives 0 when
  * no bounded wait expired since the last read, else the id of the wait that

@@ -34,3 +34,4 @@ from .awq_oracle import (  # noqa: F401
     prepack_gemv,
 )
 from . import block_oracle as block  # noqa: F401,E402  (the operators between the linear layers)
+from . import layer_oracle as layer  # noqa: F401,E402  (the layer with experts, fp8 linear layers)

@@ -73,8 +73,8 @@ _SIGS = {
     "awq_moe_prepack": (_i32, [_p, _p, _p, _i32, _i64, _i64, _i32, _i32, _p, _sz, _p]),
     "awq_moe_unprepack": (_i32, [_p, _i32, _i64, _i64, _i32, _p, _p, _p, _p]),
     "awq_moe_gemm_workspace_bytes": (_sz, [_i64, _i32, _i64, _i64, _i32]),
-    "awq_moe_gemm": (_i32, [_p, _i64, _i64, _p, _p, _p, _i32, _p, _i64, _i32, _i64, _i64, _i32, _i32, _p, _sz, _p]),
-    "awq_moe_combine": (_i32, [_p, _p, _p, _p, _i64, _p, _i64, _i32, _i64, _i64, _i32, _p]),
+    "awq_moe_gemm": (_i32, [_p, _i64, _i64, _p, _p, _p, _i32, _p, _i32, _i64, _i32, _i64, _i64, _i32, _i32, _p, _sz, _p]),
+    "awq_moe_combine": (_i32, [_p, _i32, _p, _p, _p, _i64, _p, _i64, _i32, _i64, _i64, _i32, _p]),
     "awq_fp8_quant_act": (_i32, [_p, _i64, _p, _p, _i64, _i64, _i32, _p]),
     "awq_fp8_gemm_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "awq_fp8_gemm": (_i32, [_p, _p, _p, _p, _p, _i64, _i64, _i64, _i32, _p, _sz, _p]),
@@ -818,13 +818,18 @@ def awq_moe_gemm_workspace_bytes(rows: int, weights: MoeWeights) -> int:
     return int(lib.awq_moe_gemm_workspace_bytes(rows, weights.experts, weights.K, weights.N, int(weights.gated)))
 
 
-def awq_moe_gemm(x, weights: MoeWeights, plan: MoePlan, gather: bool = False, out=None, workspace=None, stream=None):
-    """Every expert's rows times its weights: [plan.rows, weights.outputs].  x holds the rows in the plan's order, or with
-    `gather` the tokens that the plan was made for.  Rows that no expert has are not written.  Workspaces as for
-    kv4_attention: the calls of a stream share one, a captured call takes one of its own (awq_moe_gemm_workspace_bytes,
-    zeroed once)."""
+def awq_moe_gemm(x, weights: MoeWeights, plan: MoePlan, gather: bool = False, out_dtype=None, out=None, workspace=None,
+                 stream=None):
+    """Every expert's rows times its weights: [plan.rows, weights.outputs] in x's type, or fp32 with out_dtype (or `out`) so.
+    x holds the rows in the plan's order, or with `gather` the tokens that the plan was made for.  Rows that no expert
+    has are not written.  Workspaces as for kv4_attention: the calls of a stream share one, a captured call takes one
+    of its own (awq_moe_gemm_workspace_bytes, zeroed once)."""
     rows, K = plan.rows, weights.K
-    dtype = _dtype16("awq_moe_gemm", x, out)
+    dtype = _dtype16("awq_moe_gemm", x)
+    if out_dtype is None:
+        out_dtype = x.dtype if out is None else out.dtype
+    if (out_dtype is not x.dtype and out_dtype is not torch.float32) or (out is not None and out.dtype is not out_dtype):
+        raise TypeError("awq_moe_gemm: the output has x's type or is fp32")
     if x.dtype is not weights.dtype:
         raise TypeError("awq_moe_gemm: x and the weights' scales have one type")
     if x.dim() != 2 or x.shape[1] != K or plan.experts != weights.experts or \
@@ -832,7 +837,7 @@ def awq_moe_gemm(x, weights: MoeWeights, plan: MoePlan, gather: bool = False, ou
         raise ValueError("awq_moe_gemm: x is [rows, K] ([tokens, K] with gather), plan and weights have the same experts")
     device = x.device
     if out is None:
-        out = torch.empty((rows, weights.outputs), dtype=x.dtype, device=device)
+        out = torch.empty((rows, weights.outputs), dtype=out_dtype, device=device)
     elif out.shape != (rows, weights.outputs) or not out.is_contiguous():
         raise ValueError("awq_moe_gemm: out is dense, [rows, outputs]")
     _on_current_gpu("awq_moe_gemm", x, weights.data, plan.offsets, plan.order, out, workspace)
@@ -843,28 +848,33 @@ def awq_moe_gemm(x, weights: MoeWeights, plan: MoePlan, gather: bool = False, ou
         workspace = _layer_workspace("awq_moe_gemm", handle, device, need, stream)
     _check("awq_moe_gemm", lib.awq_moe_gemm(
         x.data_ptr(), _row_stride("awq_moe_gemm", x, K), x.shape[0], weights.data.data_ptr(), plan.offsets.data_ptr(),
-        plan.order.data_ptr() if gather else None, plan.top_k, out.data_ptr(), rows, weights.experts, K, weights.N,
-        int(weights.gated), dtype, workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle))
+        plan.order.data_ptr() if gather else None, plan.top_k, out.data_ptr(), int(out_dtype is torch.float32), rows,
+        weights.experts, K, weights.N, int(weights.gated), dtype, workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle))
     return out
 
 
-def awq_moe_combine(y, plan: MoePlan, weights, residual=None, out=None, stream=None):
+def awq_moe_combine(y, plan: MoePlan, weights, residual=None, dtype=None, out=None, stream=None):
     """Each token's rows of y [plan.rows, H], weighted (weights fp32 [T, top_k]) and added up, to `residual` [T, H] where
-    one is given: [T, H].  out may be residual itself."""
+    one is given: [T, H] in `dtype`, that of out, residual or y by default (y may be fp32).  out may be residual itself."""
     T, top_k = weights.shape
     H = y.shape[1]
-    dtype = _dtype16("awq_moe_combine", y, residual, out)
-    _need("awq_moe_combine", y.dtype, y, out)
+    if dtype is None:
+        dtype = (out if out is not None else residual if residual is not None else y).dtype
+    kind = _DTYPES.get(dtype)
+    if kind is None or y.dtype not in (dtype, torch.float32) or (residual is not None and (residual.dtype is not dtype or not residual.is_cuda)):
+        raise TypeError("awq_moe_combine: residual and output are fp16 or bf16, y is of their type or fp32, on a GPU")
+    _need("awq_moe_combine", y.dtype, y)
+    _need("awq_moe_combine", dtype, out)
     _need("awq_moe_combine", torch.float32, weights)
     if y.shape != (plan.rows, H) or top_k != plan.top_k or T * top_k != plan.rows or \
             (residual is not None and residual.shape != (T, H)) or (out is not None and out.shape != (T, H)):
         raise ValueError("awq_moe_combine: y [rows, H], weights [T, top_k], residual and out [T, H] go with the plan")
     _on_current_gpu("awq_moe_combine", y, plan.place, weights, residual, out)
     if out is None:
-        out = torch.empty((T, H), dtype=y.dtype, device=y.device)
+        out = torch.empty((T, H), dtype=dtype, device=y.device)
     rs = 0 if residual is None else _row_stride("awq_moe_combine", residual, H)
-    _check("awq_moe_combine", lib.awq_moe_combine(y.data_ptr(), plan.place.data_ptr(), weights.data_ptr(), _ptr(residual),
-                                                  rs, out.data_ptr(), T, top_k, H, plan.rows, dtype,
+    _check("awq_moe_combine", lib.awq_moe_combine(y.data_ptr(), int(y.dtype is torch.float32), plan.place.data_ptr(), weights.data_ptr(),
+                                                  _ptr(residual), rs, out.data_ptr(), T, top_k, H, plan.rows, kind,
                                                   _raw_stream(stream, y.device)))
     return out
 
@@ -876,8 +886,8 @@ def awq_moe(x, up: MoeWeights, down: MoeWeights, weights, plan: MoePlan, residua
     if not up.gated or down.gated or down.K != up.outputs:
         raise ValueError("awq_moe: up is gated, down is plain, and down takes up's outputs")
     h = awq_moe_gemm(x, up, plan, gather=True, workspace=workspace, stream=stream)
-    y = awq_moe_gemm(h, down, plan, workspace=workspace, stream=stream)
-    return awq_moe_combine(y, plan, weights, residual=residual, out=out, stream=stream)
+    y = awq_moe_gemm(h, down, plan, out_dtype=torch.float32, workspace=workspace, stream=stream)
+    return awq_moe_combine(y, plan, weights, residual=residual, dtype=x.dtype, out=out, stream=stream)
 
 
 FP8_BLOCK = 128

@@ -689,9 +689,10 @@ size_t awq_moe_gemm_workspace_bytes(int64_t R, int32_t experts, int64_t K, int64
 }
 
 awq_status awq_moe_gemm(const uint16_t* x, int64_t x_stride, int64_t x_rows, const void* packed, const int32_t* offsets,
-                        const int32_t* order, int32_t top_k, uint16_t* y, int64_t R, int32_t experts, int64_t K, int64_t N,
-                        int32_t gated, awq_dtype dtype, void* workspace, size_t workspace_bytes, awq_stream_t stream) {
-  if (R < 0 || R > kMoeMaxRows || x_rows < 0 || x_rows > kMoeMaxRows || !moe_shape_ok(experts, K, N, gated) ||
+                        const int32_t* order, int32_t top_k, void* y, int32_t y_fp32, int64_t R, int32_t experts, int64_t K,
+                        int64_t N, int32_t gated, awq_dtype dtype, void* workspace, size_t workspace_bytes,
+                        awq_stream_t stream) {
+  if (R < 0 || R > kMoeMaxRows || x_rows < (R > 0 ? 1 : 0) || x_rows > kMoeMaxRows || !moe_shape_ok(experts, K, N, gated) ||
       x_stride < K || x_stride % 8 != 0 || !is_dtype(dtype) || (order && (top_k < 1 || top_k > kMoeMaxTopK)))
     return AWQ_EINVAL;
   if (R == 0) return AWQ_OK;
@@ -705,10 +706,10 @@ awq_status awq_moe_gemm(const uint16_t* x, int64_t x_stride, int64_t x_rows, con
   if (!err) return AWQ_ECUDA;
   const MoeGemmArgs a{x, x_stride, x_rows, static_cast<const uint8_t*>(packed), offsets, order, order ? top_k : 1,
                       y, R,        experts, K, N, (int)moe_tiles(N, gated != 0)};
-  return from_cuda(launch_moe_gemm(a, gated != 0, dtype == AWQ_BF16, workspace, err, (cudaStream_t)stream));
+  return from_cuda(launch_moe_gemm(a, gated != 0, y_fp32 != 0, dtype == AWQ_BF16, workspace, err, (cudaStream_t)stream));
 }
 
-awq_status awq_moe_combine(const uint16_t* y, const int32_t* place, const float* weights, const uint16_t* residual,
+awq_status awq_moe_combine(const void* y, int32_t y_fp32, const int32_t* place, const float* weights, const uint16_t* residual,
                            int64_t res_stride, uint16_t* out, int64_t T, int32_t top_k, int64_t H, int64_t R,
                            awq_dtype dtype, awq_stream_t stream) {
   if (top_k < 1 || top_k > kMoeMaxTopK || T < 0 || T > kMoeMaxRows / top_k || R < 0 || R > kMoeMaxRows || H < 8 ||
@@ -720,7 +721,7 @@ awq_status awq_moe_combine(const uint16_t* y, const int32_t* place, const float*
   if (!aligned16(y) || !aligned16(residual) || !aligned16(out) || !aligned4(place) || !aligned4(weights)) return AWQ_EALIGN;
   awq_status st = check_arch();
   if (st != AWQ_OK) return st;
-  return from_cuda(launch_moe_combine(y, place, weights, residual, res_stride, out, T, top_k, H, R, dtype == AWQ_BF16,
+  return from_cuda(launch_moe_combine(y, y_fp32 != 0, place, weights, residual, res_stride, out, T, top_k, H, R, dtype == AWQ_BF16,
                                       (cudaStream_t)stream));
 }
 

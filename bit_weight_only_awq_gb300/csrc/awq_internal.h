@@ -206,7 +206,7 @@ cudaError_t launch_moe_plan(const int32_t* ids, int64_t R, int experts, int32_t*
 cudaError_t launch_moe_route(const void* logits, int64_t stride, int64_t T, int experts, int top_k, bool normalize, int type,
                              int32_t* ids, float* weights, int32_t* offsets, int32_t* order, int32_t* place,
                              cudaStream_t s);
-cudaError_t launch_moe_combine(const uint16_t* y, const int32_t* place, const float* weights, const uint16_t* residual,
+cudaError_t launch_moe_combine(const void* y, bool wide, const int32_t* place, const float* weights, const uint16_t* residual,
                                int64_t res_stride, uint16_t* out, int64_t T, int top_k, int64_t H, int64_t R, bool bf16,
                                cudaStream_t s);
 
@@ -228,14 +228,15 @@ struct MoeGemmArgs {
   const int32_t* offsets;
   const int32_t* order;  // nullptr: x holds rows
   int top_k;
-  uint16_t* y;
+  void* y;
   int64_t R;
   int experts;
   int64_t K, N;  // N: both halves when gated
   int tiles;
 };
 size_t moe_gemm_workspace(int64_t R, int experts, int64_t K, int64_t N, bool gated);
-cudaError_t launch_moe_gemm(const MoeGemmArgs& a, bool gated, bool bf16, void* ws, int* err, cudaStream_t s);
+// wide: y in fp32
+cudaError_t launch_moe_gemm(const MoeGemmArgs& a, bool gated, bool wide, bool bf16, void* ws, int* err, cudaStream_t s);
 
 // ---- e4m3 linear layers with scales for blocks of 128 (fp8_linear.cu)
 cudaError_t launch_fp8_quant(const uint16_t* x, int64_t x_stride, uint8_t* xq, float* s_x, int64_t M, int64_t K, bool bf16,

@@ -1,102 +1,597 @@
-// Products grouped by expert on prepared 4-bit weights (layout: include/awq.h).
+// Products grouped by expert on prepared 4-bit weights (layout: include/awq.h), on the 5th-generation tensor cores.
 //
-// y[r, n] = sum_k x[src(r), k] RN16((q[k, n] - z) s) over an expert's rows; gated: silu(gate) * up.
-// A CTA has 256 columns and 8 rows of one expert; a thread has one column of each half.
+// y[r, n] = sum_g s[g, n] sum_{k in g} x[src(r), k] (q[k, n] - z[g, n]) over an expert's rows; gated: silu(gate) * up.
+// The weights enter the products as the integers q - z, exact in fp16 and bf16; each group of 128 rows has a sum of its
+// own in tensor memory, which is scaled and added to the running sum in fp32 registers, where a column's scale is one
+// register of its lane.  So no weight is rounded, and a code costs one operation less than with its scale on it.
+//
+// A CTA works on tiles of 256 columns x up to 128 rows of one expert:
+//   D[column][row] = A B,  A = weights, in tensor memory (128 columns x 64 k at once), B = rows of x, K-major in shared
+//   memory.  Weights in shared memory would cost it 192 bytes a cycle at the full rate of the products; so it moves
+//   64 (the operand B) and what the copies bring.
+// Roles: warps 0-7 add the groups' sums up and write results (a thread has one column of each half and 64 rows: gate and up of a
+// gated layer meet in it), warps 8-15 turn codes into operands (a thread has a column), warp 16 issues the products,
+// warp 17 copies weights (one 17 KB unit a group), warp 18 rows of x (four rows an instruction, in any order).
+// The three sums in tensor memory and the operands' four pieces go round, so that the products need not wait for either.
+//
+// Tiles are dealt out to a persistent grid in whole rounds; what is left over is cut evenly along K, and a tile that several
+// CTAs share is finished by the one that has its first group, which adds the others' sums in their order.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "awq_host.h"
 #include "awq_internal.h"
+#include "awq_ptx.cuh"
 #include "awq_types.cuh"
 
 namespace awq {
 namespace {
 
-constexpr int kRows = 8;
+constexpr int kBT = 128;        // rows of a tile
+constexpr int kXStages = 4, kXBytes = kBT * 256;  // a group's rows: two blocks of 64 k, 128 bytes a row, swizzled
+constexpr int kQStages = 5;
+constexpr int kSums = 3;        // sums in tensor memory, kBT columns each
+constexpr int kScaleSlots = 4;  // groups whose scales are kept, see below
+constexpr int kACol = kSums * kBT;  // operands in tensor memory: [half][piece] of 32 columns
+constexpr int kThreads = 640, kSumThreads = 256;
+// Registers: 96 a thread at launch; the last group of four warps has one without work (setmaxnreg wants whole groups).
+constexpr int kLaunchRegs = 96, kSumRegs = 168, kCodeRegs = 56, kOtherRegs = 32;
+static_assert(256 * kSumRegs + 256 * kCodeRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "no more than was launched with");
+constexpr int kMinUnits = 4;    // groups that a CTA gets at least of what is cut along K
 
-template <bool BF16>
-__device__ __forceinline__ float round16(float v) {
-  return unpack2<BF16>(pack2<BF16>(v, 0.f)).x;
+// Shared memory: rows of x | units | scales | tables
+constexpr int kQAt = kXStages * kXBytes, kScaleAt = kQAt + kQStages * kMoeUnitBytes;
+constexpr int kTableAt = kScaleAt + kScaleSlots * 256 * 4;
+constexpr int kSmem = kTableAt + 2 * (kMoeMaxExperts + 1) * 4 + 1024;
+static_assert(kSmem <= 227 * 1024 - 1024, "shared memory");
+// a CTA's part of a shared tile: a sum for each of a summing thread's columns and rows
+constexpr size_t kPartBytes = (size_t)kSumThreads * 128 * 4;
+
+struct Bars {
+  uint64_t x_full[kXStages], x_empty[kXStages], q_full[kQStages], q_empty[kQStages], a_full[2][2], a_empty[2][2],
+      d_full[kSums], d_empty[kSums], s_full[kScaleSlots], join, done;
+};
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
 }
-template <bool BF16>
-__device__ __forceinline__ float widen(uint16_t v) {
-  return unpack2<BF16>((uint32_t)v).x;
+// A in tensor memory: a lane for each column of the weights, two k a column of it.  Executed by the whole warp with
+// uniform operands, issued by the lane that elect.sync chooses (always the same).
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n elect.sync _|q, 0xFFFFFFFF;\n setp.ne.b32 p, %4, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xFFFFFFFF;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
+      : "memory");
+}
+// Four rows of a tensor map whose box is one row high, 64 k each.
+__device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap* map, int col, const int (&r)[4], uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, "
+      "%6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(col), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar)
+      : "memory");
 }
 
-template <bool BF16, bool GATED>
-__global__ void __launch_bounds__(128) moe_gemm_simple(const MoeGemmArgs a) {
-  __shared__ float xs[kRows][128];
-  __shared__ int where[3];  // expert, first row, rows
-  const int tid = threadIdx.x;
-  if (tid == 0) {
-    int item = blockIdx.y, end = 0;
-    where[0] = -1;
-    for (int e = 0; e < a.experts; ++e) {
-      const int begin = max(end, min(a.offsets[e], (int)a.R));
-      end = max(begin, min(a.offsets[e + 1], (int)a.R));
-      const int items = (end - begin + kRows - 1) / kRows;
-      if (item < items) {
-        where[0] = e;
-        where[1] = begin + item * kRows;
-        where[2] = min(kRows, end - where[1]);
-        break;
-      }
-      item -= items;
-    }
-  }
-  __syncthreads();
-  const int e = where[0], r0 = where[1], rows = where[2];
-  if (e < 0) return;
-  const int groups = (int)(a.K / 128), tile = blockIdx.x;
-  float acc[2][kRows] = {};
-  for (int g = 0; g < groups; ++g) {
-    __syncthreads();
-    for (int r = 0; r < kRows; ++r) {
-      int64_t src = r < rows ? (a.order ? (a.order[r0 + r] < 0 ? -1 : a.order[r0 + r] / a.top_k) : r0 + r) : -1;
-      if (src >= a.x_rows) src = -1;
-      xs[r][tid] = src >= 0 ? widen<BF16>(a.x[src * a.x_stride + g * 128 + tid]) : 0.f;
-    }
-    __syncthreads();
-    const uint8_t* unit = a.packed + (((int64_t)e * a.tiles + tile) * groups + g) * kMoeUnitBytes;
-    for (int b = 0; b < 2; ++b) {
-      const int n = b * 128 + tid;
-      const float z = (float)(unit[kMoeZeroOffset + n / 2] >> (4 * (n & 1)) & 15);
-      const float s = widen<BF16>(*reinterpret_cast<const uint16_t*>(unit + kMoeScaleOffset + 2 * n));
-      for (int c = 0; c < 4; ++c) {
-        const uint4 v = *reinterpret_cast<const uint4*>(unit + moe_code_offset(n, c));
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        for (int q = 0; q < 4; ++q)
-          for (int i = 0; i < 8; ++i) {
-            const float weight = round16<BF16>(((float)(w[q] >> (4 * i) & 15u) - z) * s);
-            const int k = 32 * c + 8 * q + order_map(i);
+// Four registers of operand (k pairs 0..3) from a word of eight codes.
+template <bool BF16>
+__device__ __forceinline__ void operands(uint32_t w, uint32_t z, uint32_t z16, uint32_t (&o)[16], int at) {
+  if constexpr (BF16) {  // 128 + q less 128 + z, exact
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) acc[b][r] = fmaf(weight, xs[r][k], acc[b][r]);
+    for (int i = 0; i < 4; ++i)
+      asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(o[at + i]) : "r"((w >> (4 * i) & 0x000F000Fu) | 0x43004300u), "r"(z));
+  } else {  // 1024 + q less 1024 + z; (1024 + 16 q) / 16 less 64 + z: exact
+    const uint32_t v = w >> 8;
+    const uint32_t h[4] = {(w & 0x000F000Fu) | 0x64006400u, (w & 0x00F000F0u) | 0x64006400u, (v & 0x000F000Fu) | 0x64006400u,
+                           (v & 0x00F000F0u) | 0x64006400u};
+    const __half2 sixteenth = __float2half2_rn(0.0625f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 a = *reinterpret_cast<const __half2*>(&h[i]);
+      const __half2 r = i & 1 ? __hfma2(a, sixteenth, *reinterpret_cast<const __half2*>(&z16))
+                              : __hsub2(a, *reinterpret_cast<const __half2*>(&z));
+      o[at + i] = *reinterpret_cast<const uint32_t*>(&r);
+    }
+  }
+}
+
+// What a CTA works on, in order: parts of tiles, groups g0 .. g1 - 1 of each.
+struct Walk {
+  int grid, me, groups, rounds, tiles;  // whole rounds of tiles; the tiles that are left
+  int round, u, u1;
+  long long units;
+  int ctas;
+  __device__ __forceinline__ Walk(int total, int groups_) : grid(gridDim.x), me(blockIdx.x), groups(groups_) {
+    rounds = total % grid == 0 ? total / grid : max(0, total / grid - 1);
+    tiles = total - rounds * grid;
+    units = (long long)tiles * groups;
+    ctas = (int)max(1ll, min((long long)grid, units / kMinUnits));
+    round = 0;
+    u = me < ctas ? begin_of(me) : 0;
+    u1 = me < ctas ? begin_of(me + 1) : 0;
+  }
+  __device__ __forceinline__ int begin_of(int cta) const { return (int)(units * cta / ctas); }
+  __device__ __forceinline__ bool next(int& tile, int& g0, int& g1) {
+    if (round < rounds) {
+      tile = me + grid * round++;
+      g0 = 0;
+      g1 = groups;
+      return true;
+    }
+    if (u >= u1) return false;
+    const int t = u / groups;
+    g0 = u - t * groups;
+    g1 = min(groups, g0 + u1 - u);
+    tile = rounds * grid + t;
+    u += g1 - g0;
+    return true;
+  }
+};
+
+struct Tile {
+  int expert, pair, row, rows;  // rows of y: row .. row + rows - 1
+};
+// Tables: first row of each expert, and items (row tiles) before it.  Within an expert the items of a column pair are
+// neighbours, so that the CTAs of one time share weights.
+__device__ __forceinline__ Tile find_tile(const int* first, const int* items, int experts, int pairs, int t) {
+  int lo = 0, hi = experts;  // the last expert with items[lo] * pairs <= t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (items[mid] * pairs <= t) lo = mid;
+    else hi = mid;
+  }
+  const int n = items[lo + 1] - items[lo], local = t - items[lo] * pairs, count = first[lo + 1] - first[lo];
+  const int pair = local / n, item = local - pair * n;
+  const int share = ((count + n - 1) / n + 15) / 16 * 16;  // rows even out over an expert's items
+  return Tile{lo, pair, first[lo] + item * share, min(share, count - item * share)};
+}
+
+template <bool BF16, bool GATED, bool WIDE>
+__global__ void __launch_bounds__(kThreads, 1)
+moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, int* flags, float* parts, int* err) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Bars bars;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_word, s_ok;
+  volatile int* abort_flag = &abort_word;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid / 32, 0), lane = tid % 32;
+  uint8_t* smem = align_smem_1024(smem_raw);
+  const uint32_t sm = smem_u32(smem);
+  int* first = reinterpret_cast<int*>(smem + kTableAt);
+  int* items = first + kMoeMaxExperts + 1;
+  const int groups = (int)(a.K / 128);
+
+  if (tid == 0) {
+    abort_word = 0;
+    for (int i = 0; i < kXStages; ++i) {
+      mbar_init(smem_u32(&bars.x_full[i]), 1);
+      mbar_init(smem_u32(&bars.x_empty[i]), 1);
+    }
+    for (int i = 0; i < kQStages; ++i) {
+      mbar_init(smem_u32(&bars.q_full[i]), 1);
+      mbar_init(smem_u32(&bars.q_empty[i]), 8);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&bars.a_full[i / 2][i % 2]), 4);
+      mbar_init(smem_u32(&bars.a_empty[i / 2][i % 2]), 1);
+    }
+    for (int i = 0; i < kSums; ++i) {
+      mbar_init(smem_u32(&bars.d_full[i]), 1);
+      mbar_init(smem_u32(&bars.d_empty[i]), 8);
+    }
+    for (int i = 0; i < kScaleSlots; ++i) mbar_init(smem_u32(&bars.s_full[i]), 8);
+    mbar_init(smem_u32(&bars.join), kSumThreads / 32);
+    mbar_init(smem_u32(&bars.done), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 16) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (warp == 0) {
+    // offsets held to [0, R] and made to run forwards, and the items before each expert
+    int row = 0, item = 0;
+    for (int e0 = 0; e0 <= a.experts; e0 += 32) {
+      const int e = e0 + lane;
+      int v = e <= a.experts ? min(max(a.offsets[e], 0), (int)a.R) : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+        if (lane >= d) v = max(v, o);
+      }
+      v = max(v, row);
+      int before = __shfl_up_sync(0xFFFFFFFFu, v, 1);
+      if (lane == 0) before = row;
+      if (e0 == 0 && lane == 0) before = v;  // rows before the first expert's are nobody's
+      int n = e <= a.experts ? (v - before + kBT - 1) / kBT : 0;  // items of expert e - 1
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, n, d);
+        if (lane >= d) n += o;
+      }
+      if (e <= a.experts) {
+        first[e] = v;
+        items[e] = item + n;
+      }
+      row = __shfl_sync(0xFFFFFFFFu, v, 31);
+      item += __shfl_sync(0xFFFFFFFFu, n, 31);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const int pairs = a.tiles;
+  Walk walk(items[a.experts] * pairs, groups);
+  int tile, g0, g1;
+  bool ok = true;
+
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
+    // ------------------------------------------------ running sums: column n of each half, rows 64 wg .. + 63
+    const int wg = warp / 4, n = warp % 4 * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16) + 64 * wg;
+    const float* scales = reinterpret_cast<const float*>(smem + kScaleAt);
+    int d = 0, slot = 0;
+    uint32_t d_phase = 0, slot_phase = 0, join_phase = 0;
+    // all summing warps, or false: a wait that gives up elsewhere must not leave this one waiting
+    auto join = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars.join));
+      const bool all = __all_sync(0xFFFFFFFFu, wait_bounded_inline(smem_u32(&bars.join), join_phase, abort_flag, err, 704));
+      join_phase ^= 1u;
+      return all;
+    };
+    while (ok && walk.next(tile, g0, g1)) {
+      const Tile t = find_tile(first, items, a.experts, pairs, tile);
+      const int mine = min(max(t.rows - 64 * wg, 0), 64);  // of this thread's rows
+      F2 acc[2][32];
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) acc[b][i] = F2(0.f, 0.f);
+      for (int g = g0; g < g1 && ok; ++g) {
+        ok = __all_sync(0xFFFFFFFFu, wait_bounded_inline(smem_u32(&bars.s_full[slot]), slot_phase, abort_flag, err, 701));
+        if (!ok) break;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const float s = scales[slot * 256 + b * 128 + n];
+          const F2 s2(s, s);
+          ok = __all_sync(0xFFFFFFFFu, wait_bounded_inline(smem_u32(&bars.d_full[d]), d_phase, abort_flag, err, 702));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < 4; c += 2) {
+            if (16 * c < mine) {
+              uint32_t v[2][16];
+              tmem_ld16_nowait(lanes + d * kBT + 16 * c, v[0]);
+              tmem_ld16_nowait(lanes + d * kBT + 16 * c + 16, v[1]);
+              asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  asm volatile("" : "+r"(v[h][2 * i]), "+r"(v[h][2 * i + 1]));  // not used before the wait
+                  F2& s0 = acc[b][8 * (c + h) + i];
+                  s0 = fma2(F2(__uint_as_float(v[h][2 * i]), __uint_as_float(v[h][2 * i + 1])), s2, s0);
+                }
+            }
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars.d_empty[d]));
+          if (++d == kSums) {
+            d = 0;
+            d_phase ^= 1u;
+          }
+        }
+        if (++slot == kScaleSlots) {
+          slot = 0;
+          slot_phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      if (g0 > 0) {
+        // another CTA has the tile's first group: this one's sums go to it
+        F2* part = reinterpret_cast<F2*>(parts) + (size_t)walk.me * (kPartBytes / 8) + tid;
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (2 * i < mine) __stcg(reinterpret_cast<unsigned long long*>(part + (b * 32 + i) * kSumThreads), acc[b][i].v);
+        __threadfence();
+        ok = join();
+        if (ok && tid == 0) atomicExch(flags + walk.me, 1);
+        continue;
+      }
+      if (g1 < groups) {
+        // the others' sums, in the order of their groups
+        const int end = (tile - walk.rounds * walk.grid + 1) * groups;
+        for (int q = walk.me + 1; q < walk.ctas && walk.begin_of(q) < end && ok; ++q) {
+          if (tid == 0) {
+            const long long t0 = now_ns();
+            int seen = 0;
+            for (uint32_t spin = 1;; ++spin) {
+              asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(seen) : "l"(flags + q) : "memory");
+              if (seen) break;
+              if ((spin & 255u) == 0) {
+                if (*abort_flag) break;
+                if (now_ns() - t0 > kWaitLimitNs) {
+                  if (err) atomicExch(err, 703);
+                  *abort_flag = 1;
+                  break;
+                }
+              }
+            }
+            s_ok = seen;
+          }
+          ok = join() && s_ok != 0;
+          if (ok) {
+            __threadfence();
+            const F2* part = reinterpret_cast<const F2*>(parts) + (size_t)q * (kPartBytes / 8) + tid;
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (2 * i < mine) {
+                  F2 o;
+                  o.v = __ldcg(reinterpret_cast<const unsigned long long*>(part + (b * 32 + i) * kSumThreads));
+                  acc[b][i] = add2(acc[b][i], o);
+                }
+          }
+          ok = ok && join();
+          if (ok && tid == 0) atomicExch(flags + q, 0);
+        }
+        if (!ok) break;
+      }
+      const int64_t outs = GATED ? a.N / 2 : a.N;
+#pragma unroll
+      for (int b = 0; b < (GATED ? 1 : 2); ++b) {
+        const int64_t col = GATED ? (int64_t)t.pair * 128 + n : (int64_t)t.pair * 256 + b * 128 + n;
+        const bool in = col < outs;
+        using Out = typename std::conditional<WIDE, float, uint16_t>::type;
+        Out* p = static_cast<Out*>(a.y) + (int64_t)(t.row + 64 * wg) * outs + col;
+        const int rows = in ? mine : 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          float2 v = acc[b][i].get();
+          if constexpr (GATED) {
+            const float2 u = acc[1][i].get();
+            if (2 * i < rows) {
+              v.x = __fdividef(v.x, 1.f + expf(-v.x)) * u.x;
+              v.y = __fdividef(v.y, 1.f + expf(-v.y)) * u.y;
+            }
+          }
+          const uint32_t w = pack2<BF16>(v.x, v.y);
+          if (2 * i < rows) {
+            if constexpr (WIDE) *p = v.x;
+            else *p = (uint16_t)w;
+          }
+          p += outs;
+          if (2 * i + 1 < rows) {
+            if constexpr (WIDE) *p = v.y;
+            else *p = (uint16_t)(w >> 16);
+          }
+          p += outs;
+          asm volatile("" : "+l"(p));  // one address at a time, not 64 made ahead
+        }
       }
     }
-  }
-  const int64_t out = GATED ? a.N / 2 : a.N;
-  for (int r = 0; r < rows; ++r) {
-    if (GATED) {
-      const int64_t n = (int64_t)tile * 128 + tid;
-      const float v = acc[0][r] / (1.f + expf(-acc[0][r])) * acc[1][r];
-      if (n < out) a.y[(int64_t)(r0 + r) * out + n] = (uint16_t)pack2<BF16>(v, 0.f);
-    } else {
-      for (int b = 0; b < 2; ++b) {
-        const int64_t n = (int64_t)tile * 256 + b * 128 + tid;
-        if (n < out) a.y[(int64_t)(r0 + r) * out + n] = (uint16_t)pack2<BF16>(acc[b][r], 0.f);
+  } else if (warp < 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCodeRegs));
+    // ------------------------------------------------ operands: column n of half b
+    const int b = (warp - 8) / 4, n = warp % 4 * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16) + kACol + 64 * b;
+    int q = 0, slot = 0;
+    uint32_t q_phase = 0, a_phase = 1;
+    while (ok && walk.next(tile, g0, g1)) {
+      for (int g = g0; g < g1 && ok; ++g) {
+        ok = __all_sync(0xFFFFFFFFu, wait_bounded_inline(smem_u32(&bars.q_full[q]), q_phase, abort_flag, err, 711));
+        if (!ok) break;
+        const uint8_t* unit = smem + kQAt + q * kMoeUnitBytes;
+        const uint32_t codes = sm + kQAt + q * kMoeUnitBytes + b * 8192 + n * 16;
+        const int c = b * 128 + n;
+        const uint32_t z = unit[kMoeZeroOffset + c / 2] >> (4 * (c & 1)) & 15u;
+        const uint16_t raw = *reinterpret_cast<const uint16_t*>(unit + kMoeScaleOffset + 2 * c);
+        // A slot comes round again four groups later, when the products of the group before that have been issued, and
+        // those waited for the sums of at least the group after this one's to have been taken out.
+        reinterpret_cast<float*>(smem + kScaleAt)[slot * 256 + c] = unpack2<BF16>(raw).x;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.s_full[slot]));
+        uint32_t zz, z16 = 0u;
+        if constexpr (BF16) {
+          zz = (z | z << 16) | 0x43004300u;
+        } else {
+          zz = (z | z << 16) | 0x64006400u;
+          const __half2 h = __float2half2_rn(-64.f - (float)z);
+          z16 = *reinterpret_cast<const uint32_t*>(&h);
+        }
+#pragma unroll
+        for (int piece = 0; piece < 2; ++piece) {
+          const uint4 w0 = lds128(codes + (2 * piece) * 2048), w1 = lds128(codes + (2 * piece + 1) * 2048);
+          if (piece == 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars.q_empty[q]));
+          }
+          ok = __all_sync(0xFFFFFFFFu, wait_bounded_inline(smem_u32(&bars.a_empty[b][piece]), a_phase, abort_flag, err, 712));
+          if (!ok) break;
+          tc_fence_after();
+          uint32_t o[16];
+          operands<BF16>(w0.x, zz, z16, o, 0);
+          operands<BF16>(w0.y, zz, z16, o, 4);
+          operands<BF16>(w0.z, zz, z16, o, 8);
+          operands<BF16>(w0.w, zz, z16, o, 12);
+          tmem_st16(lanes + 32 * piece, o);
+          operands<BF16>(w1.x, zz, z16, o, 0);
+          operands<BF16>(w1.y, zz, z16, o, 4);
+          operands<BF16>(w1.z, zz, z16, o, 8);
+          operands<BF16>(w1.w, zz, z16, o, 12);
+          tmem_st16(lanes + 32 * piece + 16, o);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars.a_full[b][piece]));
+        }
+        a_phase ^= 1u;
+        if (++q == kQStages) {
+          q = 0;
+          q_phase ^= 1u;
+        }
+        if (++slot == kScaleSlots) slot = 0;
       }
     }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 16) {
+      // ------------------------------------------------ products
+      const uint64_t bdesc0 = smem_desc_sw128(sm, 16, 1024);
+      int x = 0, d = 0;
+      uint32_t x_phase = 0, d_phase = 1, a_phase = 0;
+      while (ok && walk.next(tile, g0, g1)) {
+        const Tile t = find_tile(first, items, a.experts, pairs, tile);
+        const uint32_t idesc = (1u << 4) | (BF16 ? (1u << 7) | (1u << 10) : 0u) | ((uint32_t)((t.rows + 15) / 16 * 2) << 17) |
+                               (8u << 24);
+        for (int g = g0; g < g1 && ok; ++g) {
+          ok = wait_bounded_inline(smem_u32(&bars.x_full[x]), x_phase, abort_flag, err, 721);
+#pragma unroll 1
+          for (int b = 0; b < 2 && ok; ++b) {
+            ok = wait_bounded_inline(smem_u32(&bars.d_empty[d]), d_phase, abort_flag, err, 722);
+#pragma unroll 1
+            for (int piece = 0; piece < 2 && ok; ++piece) {
+              ok = __all_sync(0xFFFFFFFFu, ok && wait_bounded_inline(smem_u32(&bars.a_full[b][piece]), a_phase, abort_flag, err, 723));
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t bd = bdesc0 + (uint64_t)((x * kXBytes + piece * (kXBytes / 2)) >> 4);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_ts(tmem + d * kBT, tmem + kACol + 64 * b + 32 * piece + 8 * k, bd + 2 * k, idesc, (piece | k) ? 1u : 0u);
+              commit(smem_u32(&bars.a_empty[b][piece]));
+            }
+            if (!ok) break;
+            commit(smem_u32(&bars.d_full[d]));
+            if (++d == kSums) {
+              d = 0;
+              d_phase ^= 1u;
+            }
+          }
+          if (!ok) break;
+          commit(smem_u32(&bars.x_empty[x]));
+          a_phase ^= 1u;
+          if (++x == kXStages) {
+            x = 0;
+            x_phase ^= 1u;
+          }
+        }
+      }
+      commit(smem_u32(&bars.done));  // arrives once every product has completed
+      volatile int no_abort = 0;
+      wait_bounded_inline(smem_u32(&bars.done), 0, &no_abort, err, 724);
+    } else if (warp == 17) {
+      // ------------------------------------------------ copies of weights
+      if (lane == 0) {
+        int q = 0, issued = 0;
+        uint32_t q_phase = 1;
+        while (ok && walk.next(tile, g0, g1)) {
+          const Tile t = find_tile(first, items, a.experts, pairs, tile);
+          const uint8_t* src = a.packed + ((int64_t)t.expert * pairs + t.pair) * groups * kMoeUnitBytes;
+          for (int g = g0; g < g1; ++g) {
+            ok = wait_bounded_inline(smem_u32(&bars.q_empty[q]), q_phase, abort_flag, err, 731);
+            if (!ok) break;
+            mbar_arrive_tx(smem_u32(&bars.q_full[q]), kMoeUnitBytes);
+            bulk_load(sm + kQAt + q * kMoeUnitBytes, src + (int64_t)g * kMoeUnitBytes, kMoeUnitBytes, smem_u32(&bars.q_full[q]));
+            ++issued;
+            if (++q == kQStages) {
+              q = 0;
+              q_phase ^= 1u;
+            }
+          }
+        }
+        // never leave the CTA with copies in flight
+        volatile int no_abort = 0;
+        for (int j = max(0, issued - kQStages); j < issued; ++j)
+          wait_bounded_inline(smem_u32(&bars.q_full[j % kQStages]), (uint32_t)(j / kQStages) & 1u, &no_abort, err, 732);
+      }
+    } else if (warp == 18) {
+      // ------------------------------------------------ copies of rows: lane l has rows 4 l .. 4 l + 3 of the tile
+      int x = 0, issued = 0;
+      uint32_t x_phase = 1;
+      while (ok && walk.next(tile, g0, g1)) {
+        const Tile t = find_tile(first, items, a.experts, pairs, tile);
+        int r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = t.row + min(4 * lane + i, t.rows - 1);
+          const int src = a.order ? a.order[row] / a.top_k : row;
+          r[i] = src >= 0 && src < a.x_rows ? src : 0;
+        }
+        const int fours = (t.rows + 3) / 4;
+        for (int g = g0; g < g1; ++g) {
+          ok = __all_sync(0xFFFFFFFFu, wait_bounded_inline(smem_u32(&bars.x_empty[x]), x_phase, abort_flag, err, 741));
+          if (!ok) break;
+          const uint32_t bar = smem_u32(&bars.x_full[x]);
+          if (lane == 0) mbar_arrive_tx(bar, (uint32_t)fours * 1024u);
+          __syncwarp();
+          if (lane < fours) {
+            gather4(sm + x * kXBytes + lane * 512, &tm_x, g * 128, r, bar);
+            gather4(sm + x * kXBytes + kXBytes / 2 + lane * 512, &tm_x, g * 128 + 64, r, bar);
+          }
+          ++issued;
+          if (++x == kXStages) {
+            x = 0;
+            x_phase ^= 1u;
+          }
+        }
+      }
+      volatile int no_abort = 0;
+      for (int j = max(0, issued - kXStages); j < issued; ++j)
+        wait_bounded_inline(smem_u32(&bars.x_full[j % kXStages]), (uint32_t)(j / kXStages) & 1u, &no_abort, err, 742);
+    }
   }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 16) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+  }
+}
+
+template <bool BF16>
+cudaError_t launch(const MoeGemmArgs& a, bool gated, bool wide, void* ws, int* err, cudaStream_t s) {
+  CUtensorMap tm;
+  if (!make_map_2d(&tm, BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.x, (uint64_t)a.K,
+                   (uint64_t)a.x_rows, 64, 1, CU_TENSOR_MAP_SWIZZLE_128B, (uint64_t)a.x_stride))
+    return cudaErrorInvalidValue;
+  const auto fn = gated ? (wide ? moe_gemm_kernel<BF16, true, true> : moe_gemm_kernel<BF16, true, false>)
+                        : (wide ? moe_gemm_kernel<BF16, false, true> : moe_gemm_kernel<BF16, false, false>);
+  const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(fn), kSmem);
+  if (e != cudaSuccess) return e;
+  int* flags = static_cast<int*>(ws);
+  float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kCounterBytes);
+  fn<<<device_sm_count(), kThreads, kSmem, s>>>(tm, a, flags, parts, err);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t moe_gemm_workspace(int64_t, int, int64_t, int64_t, bool) { return 0; }
+size_t moe_gemm_workspace(int64_t, int, int64_t, int64_t, bool) {
+  return kCounterBytes + (size_t)device_sm_count() * kPartBytes;
+}
 
-cudaError_t launch_moe_gemm(const MoeGemmArgs& a, bool gated, bool bf16, void*, int*, cudaStream_t s) {
-  const int64_t items = a.R / kRows + (a.experts < a.R ? a.experts : a.R);
-  const dim3 grid((unsigned)a.tiles, (unsigned)items);
-  const auto fn = bf16 ? (gated ? moe_gemm_simple<true, true> : moe_gemm_simple<true, false>)
-                       : (gated ? moe_gemm_simple<false, true> : moe_gemm_simple<false, false>);
-  fn<<<grid, 128, 0, s>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_moe_gemm(const MoeGemmArgs& a, bool gated, bool wide, bool bf16, void* ws, int* err, cudaStream_t s) {
+  return bf16 ? launch<true>(a, gated, wide, ws, err, s) : launch<false>(a, gated, wide, ws, err, s);
 }
 
 }  // namespace awq

@@ -157,8 +157,9 @@ __global__ void __launch_bounds__(256) route_kernel(const void* __restrict__ log
   }
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(256) combine_kernel(const uint16_t* __restrict__ y, const int32_t* __restrict__ place,
+// WIDE: y in fp32.
+template <bool BF16, bool WIDE>
+__global__ void __launch_bounds__(256) combine_kernel(const void* __restrict__ y, const int32_t* __restrict__ place,
                                                       const float* __restrict__ weights, const uint16_t* residual,
                                                       int64_t res_stride, uint16_t* out, int64_t T, int top_k, int64_t H,
                                                       int64_t R) {
@@ -183,14 +184,24 @@ __global__ void __launch_bounds__(256) combine_kernel(const uint16_t* __restrict
     const int r = place[t * top_k + j];
     if (r < 0 || r >= R) continue;
     const float weight = weights[t * top_k + j];
-    const uint4 v = *reinterpret_cast<const uint4*>(y + r * H + c);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float f[8];
+    if constexpr (WIDE) {
+      const float4* v = reinterpret_cast<const float4*>(static_cast<const float*>(y) + r * H + c);
+      const float4 lo = v[0], hi = v[1];
+      f[0] = lo.x, f[1] = lo.y, f[2] = lo.z, f[3] = lo.w;
+      f[4] = hi.x, f[5] = hi.y, f[6] = hi.z, f[7] = hi.w;
+    } else {
+      const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(y) + r * H + c);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const float2 f = unpack2<BF16>(w[p]);
-      sum[2 * p] = fmaf(weight, f.x, sum[2 * p]);
-      sum[2 * p + 1] = fmaf(weight, f.y, sum[2 * p + 1]);
+      for (int p = 0; p < 4; ++p) {
+        const float2 u = unpack2<BF16>(w[p]);
+        f[2 * p] = u.x;
+        f[2 * p + 1] = u.y;
+      }
     }
+#pragma unroll
+    for (int p = 0; p < 8; ++p) sum[p] = fmaf(weight, f[p], sum[p]);
   }
   *reinterpret_cast<uint4*>(out + t * H + c) = make_uint4(pack2<BF16>(sum[0], sum[1]), pack2<BF16>(sum[2], sum[3]),
                                                           pack2<BF16>(sum[4], sum[5]), pack2<BF16>(sum[6], sum[7]));
@@ -228,12 +239,13 @@ cudaError_t launch_moe_route(const void* logits, int64_t stride, int64_t T, int 
   return offsets ? launch_moe_plan(ids, T * top_k, experts, offsets, order, place, s) : cudaSuccess;
 }
 
-cudaError_t launch_moe_combine(const uint16_t* y, const int32_t* place, const float* weights, const uint16_t* residual,
+cudaError_t launch_moe_combine(const void* y, bool wide, const int32_t* place, const float* weights, const uint16_t* residual,
                                int64_t res_stride, uint16_t* out, int64_t T, int top_k, int64_t H, int64_t R, bool bf16,
                                cudaStream_t s) {
   const int64_t threads = T * (H / 8);
-  (bf16 ? combine_kernel<true> : combine_kernel<false>)<<<(unsigned)((threads + 255) / 256), 256, 0, s>>>(
-      y, place, weights, residual, res_stride, out, T, top_k, H, R);
+  const auto fn = bf16 ? (wide ? combine_kernel<true, true> : combine_kernel<true, false>)
+                       : (wide ? combine_kernel<false, true> : combine_kernel<false, false>);
+  fn<<<(unsigned)((threads + 255) / 256), 256, 0, s>>>(y, place, weights, residual, res_stride, out, T, top_k, H, R);
   return cudaGetLastError();
 }
 

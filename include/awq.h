@@ -567,32 +567,35 @@ awq_status awq_moe_unprepack(const void *packed, int32_t experts, int64_t K, int
 
 /*
  * awq_moe_gemm -- the products of all experts, each with its rows, in one call:
- *   a[r] = x[src(r)] W_e,  W = RN16((q - z) s),  y[r] = RN16(a[r]), or gated RN16(silu(gate) * up) with
- *   (gate, up) the two halves of a[r] and silu(v) = v / (1 + exp(-v)); sums, silu and product in fp32
+ *   a[r] = x[src(r)] W_e,  W = (q - z) s,  y[r] = a[r], or gated silu(gate) * up with (gate, up) the two halves of a[r]
+ *   and silu(v) = v / (1 + exp(-v))
  * for the rows r of every expert e, offsets[e] <= r < offsets[e + 1].  src(r) = order[r] / top_k where order is given
  * (x holds tokens), r where it is NULL (x holds rows).  x 16-bit [x_rows, K] with row stride x_stride, y [R, N] dense,
- * [R, N / 2] when gated; packed from awq_moe_prepack with the same sizes.  Rows of y outside every expert's are not
- * written.  Offsets are clamped to [0, R] and never run backwards; a src outside [0, x_rows) reads as zeros.
- * The result does not depend on timing: split sums are added in a fixed order.
- * x_stride % 8 == 0 and >= K, R and x_rows <= 2^30; sizes otherwise as for awq_moe_prepack.  R = 0 is a no-op.
+ * [R, N / 2] when gated, rounded once: to x's type, or fp32 if y_fp32 != 0 (what awq_moe_combine adds up unrounded);
+ * packed from awq_moe_prepack with the same sizes and scales of x's type.  The codes q - z enter the products as
+ * they are (no weight is rounded); a group's sum is scaled and added in fp32.  Rows of y outside every expert's are not
+ * written.  Offsets are clamped to [0, R] and never run backwards, a src outside [0, x_rows) reads row 0: memory-safe,
+ * with unspecified results.  The result does not depend on timing: split sums are added in a fixed order.
+ * x_stride % 8 == 0 and >= K, 1 <= x_rows <= 2^30, R <= 2^30; sizes otherwise as for awq_moe_prepack.  R = 0 is a no-op.
  * Workspace: awq_moe_gemm_workspace_bytes(), same contract as awq_gemv's; its CTAs wait (bounded) for one another's
  * partial sums, so the call assumes that they can all be resident at once.
  */
 size_t awq_moe_gemm_workspace_bytes(int64_t R, int32_t experts, int64_t K, int64_t N, int32_t gated);
 awq_status awq_moe_gemm(const uint16_t *x, int64_t x_stride, int64_t x_rows, const void *packed,
-                        const int32_t *offsets, const int32_t *order, int32_t top_k, uint16_t *y, int64_t R,
-                        int32_t experts, int64_t K, int64_t N, int32_t gated, awq_dtype dtype, void *workspace,
-                        size_t workspace_bytes, awq_stream_t stream);
+                        const int32_t *offsets, const int32_t *order, int32_t top_k, void *y, int32_t y_fp32,
+                        int64_t R, int32_t experts, int64_t K, int64_t N, int32_t gated, awq_dtype dtype,
+                        void *workspace, size_t workspace_bytes, awq_stream_t stream);
 
 /*
  * awq_moe_combine -- out[t] = RN16(residual[t] + sum_j weights[t, j] * y[place[t, j]]), j in ascending order, in fp32.
- * y 16-bit [R, H] dense; place int32, weights fp32 [T, top_k]; residual 16-bit [T, H] with row stride res_stride, or
- * NULL; out [T, H] dense (may be residual itself when that is dense).  A choice whose place is outside [0, R) adds
- * nothing.  H % 8 == 0, 1 <= top_k <= 32, T * top_k and R <= 2^30.  T = 0 is a no-op.
+ * y [R, H] dense, of out's type or fp32 (y_fp32 != 0); place int32, weights fp32 [T, top_k]; residual 16-bit [T, H] with
+ * row stride res_stride, or NULL; out 16-bit [T, H] dense (may be residual itself when that is dense).  A choice whose
+ * place is outside [0, R) adds nothing.  8 <= H <= 2^20, H % 8 == 0, 1 <= top_k <= 32, T * top_k and R <= 2^30.  T = 0
+ * is a no-op.
  */
-awq_status awq_moe_combine(const uint16_t *y, const int32_t *place, const float *weights, const uint16_t *residual,
-                           int64_t res_stride, uint16_t *out, int64_t T, int32_t top_k, int64_t H, int64_t R,
-                           awq_dtype dtype, awq_stream_t stream);
+awq_status awq_moe_combine(const void *y, int32_t y_fp32, const int32_t *place, const float *weights,
+                           const uint16_t *residual, int64_t res_stride, uint16_t *out, int64_t T, int32_t top_k,
+                           int64_t H, int64_t R, awq_dtype dtype, awq_stream_t stream);
 
 /*
  * Linear layers in 8-bit floating point

@@ -10,7 +10,6 @@ from __future__ import annotations
 import numpy as np
 
 from .awq_oracle import AWQ_ORDER, unpack
-from .block_oracle import round16
 
 f32 = np.float32
 
@@ -48,12 +47,12 @@ def plan(ids, experts: int):
 
 # ---- weights
 
-def dequantize(qweight, qzeros, scales, bf16: bool):
-    """float32 [K, N] of one layer: RN16((q - z) s); scales float32 [K / 128, N]."""
+def dequantize(qweight, qzeros, scales):
+    """float64 [K, N] of one layer: (q - z) s, exact; scales float32 [K / 128, N]."""
     q = unpack(qweight).astype(np.int32)
     z = np.full((scales.shape[0], q.shape[1]), 8, np.int32) if qzeros is None else unpack(qzeros).astype(np.int32)
     rep = np.repeat(np.arange(scales.shape[0]), 128)
-    return round16((q - z[rep]).astype(f32) * scales[rep].astype(f32), bf16)
+    return (q - z[rep]).astype(np.float64) * scales[rep].astype(np.float64)
 
 
 def prepack(qweight, qzeros, scale_bits, gated: bool) -> np.ndarray:

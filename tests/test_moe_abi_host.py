@@ -78,11 +78,11 @@ def test_prepack_sizes_and_refusals(lib):
 
 def _gemm(lib, x=FAKE, xs=256, xr=8, packed=FAKE, offsets=FAKE, order=FAKE, top_k=2, y=FAKE, R=16, experts=4, K=256, N=512,
           gated=0, dtype=0, ws=FAKE, wsb=1 << 40):
-    return lib.awq_moe_gemm(x, xs, xr, packed, offsets, order, top_k, y, R, experts, K, N, gated, dtype, ws, wsb, None)
+    return lib.awq_moe_gemm(x, xs, xr, packed, offsets, order, top_k, y, 0, R, experts, K, N, gated, dtype, ws, wsb, None)
 
 
 def test_gemm_refusals(lib):
-    for bad in ({"R": -1}, {"R": 2 ** 30 + 1}, {"xr": -1}, {"xr": 2 ** 30 + 1}, {"K": 200}, {"N": 500}, {"N": 96, "gated": 1},
+    for bad in ({"R": -1}, {"R": 2 ** 30 + 1}, {"xr": 0}, {"xr": 2 ** 30 + 1}, {"K": 200}, {"N": 500}, {"N": 96, "gated": 1},
                 {"xs": 248}, {"xs": 260}, {"dtype": 2}, {"top_k": 0}, {"top_k": 33}, {"experts": 0}, {"experts": 513}):
         assert _gemm(lib, **bad) == EINVAL, bad
     for name in ("x", "packed", "offsets", "y"):
@@ -101,7 +101,7 @@ def test_gemm_refusals(lib):
 
 def test_combine_refusals(lib):
     def call(y=FAKE, place=FAKE, w=FAKE, res=FAKE, rs=64, out=FAKE, T=3, k=2, H=64, R=6, dtype=0):
-        return lib.awq_moe_combine(y, place, w, res, rs, out, T, k, H, R, dtype, None)
+        return lib.awq_moe_combine(y, 1, place, w, res, rs, out, T, k, H, R, dtype, None)
 
     for bad in ({"k": 0}, {"k": 33}, {"T": -1}, {"R": -1}, {"H": 60}, {"H": 0}, {"rs": 56}, {"rs": 68}, {"dtype": 5}):
         assert call(**bad) == EINVAL, bad

@@ -5,18 +5,18 @@
 // own in tensor memory, which is scaled and added to the running sum in fp32 registers, where a column's scale is one
 // register of its lane.  So no weight is rounded, and a code costs one operation less than with its scale on it.
 //
-// A CTA works on tiles of 256 columns x up to 128 rows of one expert:
+// A CTA works on tiles of 256 columns x up to BT rows of one expert:
 //   D[column][row] = A B,  A = weights, in tensor memory (128 columns x 64 k at once), B = rows of x, K-major in shared
 //   memory.  Weights in shared memory would cost it 192 bytes a cycle at the full rate of the products; so it moves
 //   64 (the operand B) and what the copies bring.
-// Roles: warps 0-7 add the groups' sums up and write results (a thread has one column of each half and 64 rows: gate and up of a
-// gated layer meet in it), warps 8-15 turn codes into operands (a thread has a column), warp 16 issues the products,
-// warp 17 copies weights (one 17 KB unit a group), warp 18 rows of x (four rows an instruction, in any order).
-// The three sums in tensor memory and the operands' four pieces go round, so that the products need not wait for either.
+// Roles: warps 0-7 add the groups' sums up and write results (a thread has one column of each half and BT / 2 rows: gate and up
+// of a gated layer meet in it), warps 8-15 turn codes into operands (a thread has a column), warp 16 issues the products,
+// warp 17 copies weights (one 17 KB unit a group), warps 18 and 19 rows of x (in any order; four rows of a tensor map an
+// instruction, tile::gather4, took 30 cycles each: 484 us against 273 without them at 32008 rows over 126 experts).
+// Sums and operand pieces in tensor memory go round, so that the products need not wait for either.
 //
 // Tiles are dealt out to a persistent grid in whole rounds; what is left over is cut evenly along K, and a tile that several
 // CTAs share is finished by the one that has its first group, which adds the others' sums in their order.
-#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -30,29 +30,38 @@
 namespace awq {
 namespace {
 
-constexpr int kBT = 128;        // rows of a tile
-constexpr int kXStages = 4, kXBytes = kBT * 256;  // a group's rows: two blocks of 64 k, 128 bytes a row, swizzled
-constexpr int kQStages = 5;
-constexpr int kSums = 3;        // sums in tensor memory, kBT columns each
-constexpr int kScaleSlots = 4;  // groups whose scales are kept, see below
-constexpr int kACol = kSums * kBT;  // operands in tensor memory: [half][piece] of 32 columns
+constexpr int kPieces = 4;      // operand pieces of a half in tensor memory, 32 columns (64 k) each: two groups
+constexpr int kACol = 256;      // operands in tensor memory: [half][piece]; the sums come before
+constexpr int kScaleSlots = 8;  // groups whose scales are kept, see below
 constexpr int kThreads = 640, kSumThreads = 256;
-// Registers: 96 a thread at launch; the last group of four warps has one without work (setmaxnreg wants whole groups).
+// Registers: 96 a thread at launch.
 constexpr int kLaunchRegs = 96, kSumRegs = 168, kCodeRegs = 56, kOtherRegs = 32;
 static_assert(256 * kSumRegs + 256 * kCodeRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "no more than was launched with");
 constexpr int kMinUnits = 4;    // groups that a CTA gets at least of what is cut along K
 
-// Shared memory: rows of x | units | scales | tables
-constexpr int kQAt = kXStages * kXBytes, kScaleAt = kQAt + kQStages * kMoeUnitBytes;
-constexpr int kTableAt = kScaleAt + kScaleSlots * 256 * 4;
-constexpr int kSmem = kTableAt + 2 * (kMoeMaxExperts + 1) * 4 + 1024;
-static_assert(kSmem <= 227 * 1024 - 1024, "shared memory");
-// a CTA's part of a shared tile: a sum for each of a summing thread's columns and rows
-constexpr size_t kPartBytes = (size_t)kSumThreads * 128 * 4;
+// Tiles of up to BT rows.
+template <int BT>
+struct Geo {
+  static constexpr int kSums = BT == 128 ? 2 : 4;        // sums in tensor memory, BT columns each
+  static constexpr int kXBytes = BT * 256;               // a group's rows: two blocks of 64 k, 128 bytes a row, swizzled
+  static constexpr int kXStages = 4, kXAhead = 2;        // copies under way before one is waited for
+  static constexpr int kQStages = BT == 128 ? 5 : 8;
+  // shared memory: rows of x | units | scales | expert tables | sources of rows
+  static constexpr int kQAt = kXStages * kXBytes, kScaleAt = kQAt + kQStages * kMoeUnitBytes;
+  static constexpr int kTableAt = kScaleAt + kScaleSlots * 256 * 4;
+  static constexpr int kSourceAt = kTableAt + 2 * (kMoeMaxExperts + 1) * 4;
+  static constexpr int kSmem = kSourceAt + BT * 4 + 1024;
+  static constexpr int kPairs = BT / 4;                  // pairs of rows of a summing thread, in each half
+  // a CTA's part of a shared tile: a sum for each of a summing thread's columns and rows
+  static constexpr size_t kPartBytes = (size_t)kSumThreads * BT * 4;
+  static_assert(kSums * BT <= kACol && kSmem <= 227 * 1024 - 1024, "tensor memory, shared memory");
+  static_assert(kScaleSlots >= 5 + kSums / 2, "scales");
+};
 
+template <int BT>
 struct Bars {
-  uint64_t x_full[kXStages], x_empty[kXStages], q_full[kQStages], q_empty[kQStages], a_full[2][2], a_empty[2][2],
-      d_full[kSums], d_empty[kSums], s_full[kScaleSlots], join, done;
+  uint64_t x_full[Geo<BT>::kXStages], x_empty[Geo<BT>::kXStages], q_full[Geo<BT>::kQStages], q_empty[Geo<BT>::kQStages],
+      a_full[2][kPieces], a_empty[2][kPieces], d_full[Geo<BT>::kSums], d_empty[Geo<BT>::kSums], s_full[kScaleSlots], join, done;
 };
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -75,13 +84,12 @@ __device__ __forceinline__ void commit(uint32_t bar) {
       " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
       : "memory");
 }
-// Four rows of a tensor map whose box is one row high, 64 k each.
-__device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap* map, int col, const int (&r)[4], uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, "
-      "%6}], [%7];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(col), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar)
-      : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// The first look comes before the clock is read for the limit.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort, int* err, int id) {
+  return mbar_try(bar, parity) || wait_bounded_inline(bar, parity, abort, err, id);
 }
 
 // Four registers of operand (k pairs 0..3) from a word of eight codes.
@@ -144,6 +152,7 @@ struct Tile {
 };
 // Tables: first row of each expert, and items (row tiles) before it.  Within an expert the items of a column pair are
 // neighbours, so that the CTAs of one time share weights.
+template <int BT>
 __device__ __forceinline__ Tile find_tile(const int* first, const int* items, int experts, int pairs, int t) {
   int lo = 0, hi = experts;  // the last expert with items[lo] * pairs <= t
   while (hi - lo > 1) {
@@ -157,36 +166,37 @@ __device__ __forceinline__ Tile find_tile(const int* first, const int* items, in
   return Tile{lo, pair, first[lo] + item * share, min(share, count - item * share)};
 }
 
-template <bool BF16, bool GATED, bool WIDE>
+template <int BT, bool BF16, bool GATED, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1)
-moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, int* flags, float* parts, int* err) {
+moe_gemm_kernel(const MoeGemmArgs a, int* flags, float* parts, int* err) {
+  using G = Geo<BT>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ Bars bars;
+  __shared__ Bars<BT> bars;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word, s_ok;
   volatile int* abort_flag = &abort_word;
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid / 32, 0), lane = tid % 32;
   uint8_t* smem = align_smem_1024(smem_raw);
   const uint32_t sm = smem_u32(smem);
-  int* first = reinterpret_cast<int*>(smem + kTableAt);
+  int* first = reinterpret_cast<int*>(smem + G::kTableAt);
   int* items = first + kMoeMaxExperts + 1;
   const int groups = (int)(a.K / 128);
 
-  if (tid == 0) {
+  if (tid == 32) {
     abort_word = 0;
-    for (int i = 0; i < kXStages; ++i) {
-      mbar_init(smem_u32(&bars.x_full[i]), 1);
+    for (int i = 0; i < G::kXStages; ++i) {
+      mbar_init(smem_u32(&bars.x_full[i]), 2);
       mbar_init(smem_u32(&bars.x_empty[i]), 1);
     }
-    for (int i = 0; i < kQStages; ++i) {
+    for (int i = 0; i < G::kQStages; ++i) {
       mbar_init(smem_u32(&bars.q_full[i]), 1);
       mbar_init(smem_u32(&bars.q_empty[i]), 8);
     }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(smem_u32(&bars.a_full[i / 2][i % 2]), 4);
-      mbar_init(smem_u32(&bars.a_empty[i / 2][i % 2]), 1);
+    for (int i = 0; i < 2 * kPieces; ++i) {
+      mbar_init(smem_u32(&bars.a_full[0][i]), 4);
+      mbar_init(smem_u32(&bars.a_empty[0][i]), 1);
     }
-    for (int i = 0; i < kSums; ++i) {
+    for (int i = 0; i < G::kSums; ++i) {
       mbar_init(smem_u32(&bars.d_full[i]), 1);
       mbar_init(smem_u32(&bars.d_empty[i]), 8);
     }
@@ -214,9 +224,8 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
       }
       v = max(v, row);
       int before = __shfl_up_sync(0xFFFFFFFFu, v, 1);
-      if (lane == 0) before = row;
-      if (e0 == 0 && lane == 0) before = v;  // rows before the first expert's are nobody's
-      int n = e <= a.experts ? (v - before + kBT - 1) / kBT : 0;  // items of expert e - 1
+      if (lane == 0) before = e0 == 0 ? v : row;  // rows before the first expert's are nobody's
+      int n = e <= a.experts ? (v - before + BT - 1) / BT : 0;  // items of expert e - 1
 #pragma unroll
       for (int d = 1; d < 32; d *= 2) {
         const int o = __shfl_up_sync(0xFFFFFFFFu, n, d);
@@ -241,59 +250,68 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
-    // ------------------------------------------------ running sums: column n of each half, rows 64 wg .. + 63
+    // ------------------------------------------------ running sums: column n of each half, rows BT / 2 wg ..
     const int wg = warp / 4, n = warp % 4 * 32 + lane;
-    const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16) + 64 * wg;
-    const float* scales = reinterpret_cast<const float*>(smem + kScaleAt);
+    const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16) + BT / 2 * wg;
+    const float* scales = reinterpret_cast<const float*>(smem + G::kScaleAt);
     int d = 0, slot = 0;
     uint32_t d_phase = 0, slot_phase = 0, join_phase = 0;
     // all summing warps, or false: a wait that gives up elsewhere must not leave this one waiting
     auto join = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars.join));
-      const bool all = __all_sync(0xFFFFFFFFu, wait_bounded_inline(smem_u32(&bars.join), join_phase, abort_flag, err, 704));
+      const bool all = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.join), join_phase, abort_flag, err, 704));
       join_phase ^= 1u;
       return all;
     };
     while (ok && walk.next(tile, g0, g1)) {
-      const Tile t = find_tile(first, items, a.experts, pairs, tile);
-      const int mine = min(max(t.rows - 64 * wg, 0), 64);  // of this thread's rows
-      F2 acc[2][32];
+      const Tile t = find_tile<BT>(first, items, a.experts, pairs, tile);
+      const int mine = min(max(t.rows - BT / 2 * wg, 0), BT / 2);  // of this thread's rows
+      F2 acc[2][G::kPairs];
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) acc[b][i] = F2(0.f, 0.f);
+        for (int i = 0; i < G::kPairs; ++i) acc[b][i] = F2(0.f, 0.f);
       for (int g = g0; g < g1 && ok; ++g) {
-        ok = __all_sync(0xFFFFFFFFu, wait_bounded_inline(smem_u32(&bars.s_full[slot]), slot_phase, abort_flag, err, 701));
+        ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.s_full[slot]), slot_phase, abort_flag, err, 701));
         if (!ok) break;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const float s = scales[slot * 256 + b * 128 + n];
           const F2 s2(s, s);
-          ok = __all_sync(0xFFFFFFFFu, wait_bounded_inline(smem_u32(&bars.d_full[d]), d_phase, abort_flag, err, 702));
+          ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.d_full[d]), d_phase, abort_flag, err, 702));
           if (!ok) break;
           tc_fence_after();
+          if constexpr (BT == 16) {
+            if (mine > 0) {
+              float v[8];
+              tmem_ld8(lanes + d * BT, v);
 #pragma unroll
-          for (int c = 0; c < 4; c += 2) {
-            if (16 * c < mine) {
-              uint32_t v[2][16];
-              tmem_ld16_nowait(lanes + d * kBT + 16 * c, v[0]);
-              tmem_ld16_nowait(lanes + d * kBT + 16 * c + 16, v[1]);
-              asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+              for (int i = 0; i < 4; ++i) acc[b][i] = fma2(F2(v[2 * i], v[2 * i + 1]), s2, acc[b][i]);
+            }
+          } else {
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
+            for (int c = 0; c < G::kPairs / 8; c += 2) {
+              if (16 * c < mine) {
+                uint32_t v[2][16];
+                tmem_ld16_nowait(lanes + d * BT + 16 * c, v[0]);
+                tmem_ld16_nowait(lanes + d * BT + 16 * c + 16, v[1]);
+                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  asm volatile("" : "+r"(v[h][2 * i]), "+r"(v[h][2 * i + 1]));  // not used before the wait
-                  F2& s0 = acc[b][8 * (c + h) + i];
-                  s0 = fma2(F2(__uint_as_float(v[h][2 * i]), __uint_as_float(v[h][2 * i + 1])), s2, s0);
-                }
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) {
+                    asm volatile("" : "+r"(v[h][2 * i]), "+r"(v[h][2 * i + 1]));  // not used before the wait
+                    F2& s0 = acc[b][8 * (c + h) + i];
+                    s0 = fma2(F2(__uint_as_float(v[h][2 * i]), __uint_as_float(v[h][2 * i + 1])), s2, s0);
+                  }
+              }
             }
           }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&bars.d_empty[d]));
-          if (++d == kSums) {
+          if (++d == G::kSums) {
             d = 0;
             d_phase ^= 1u;
           }
@@ -306,67 +324,73 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
       if (!ok) break;
       if (g0 > 0) {
         // another CTA has the tile's first group: this one's sums go to it
-        F2* part = reinterpret_cast<F2*>(parts) + (size_t)walk.me * (kPartBytes / 8) + tid;
+        F2* part = reinterpret_cast<F2*>(parts) + (size_t)walk.me * (G::kPartBytes / 8) + tid;
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (2 * i < mine) __stcg(reinterpret_cast<unsigned long long*>(part + (b * 32 + i) * kSumThreads), acc[b][i].v);
+          for (int i = 0; i < G::kPairs; ++i)
+            if (2 * i < mine) __stcg(reinterpret_cast<unsigned long long*>(part + (b * G::kPairs + i) * kSumThreads), acc[b][i].v);
         __threadfence();
         ok = join();
         if (ok && tid == 0) atomicExch(flags + walk.me, 1);
         continue;
       }
       if (g1 < groups) {
-        // the others' sums, in the order of their groups
+        // the others' sums, in the order of their groups; the lanes of one warp wait for all of them at once
         const int end = (tile - walk.rounds * walk.grid + 1) * groups;
-        for (int q = walk.me + 1; q < walk.ctas && walk.begin_of(q) < end && ok; ++q) {
-          if (tid == 0) {
+        int last = walk.me + 1;
+        while (last < walk.ctas && walk.begin_of(last) < end) ++last;
+        if (warp == 0) {
+          bool seen = true;
+          for (int q = walk.me + 1 + lane; q < last && seen; q += 32) {
             const long long t0 = now_ns();
-            int seen = 0;
             for (uint32_t spin = 1;; ++spin) {
-              asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(seen) : "l"(flags + q) : "memory");
-              if (seen) break;
+              int v;
+              asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(flags + q) : "memory");
+              if (v) break;
               if ((spin & 255u) == 0) {
-                if (*abort_flag) break;
-                if (now_ns() - t0 > kWaitLimitNs) {
+                if (*abort_flag) seen = false;
+                else if (now_ns() - t0 > kWaitLimitNs) {
                   if (err) atomicExch(err, 703);
                   *abort_flag = 1;
-                  break;
+                  seen = false;
                 }
+                if (!seen) break;
               }
             }
-            s_ok = seen;
           }
-          ok = join() && s_ok != 0;
-          if (ok) {
-            __threadfence();
-            const F2* part = reinterpret_cast<const F2*>(parts) + (size_t)q * (kPartBytes / 8) + tid;
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (2 * i < mine) {
-                  F2 o;
-                  o.v = __ldcg(reinterpret_cast<const unsigned long long*>(part + (b * 32 + i) * kSumThreads));
-                  acc[b][i] = add2(acc[b][i], o);
-                }
-          }
-          ok = ok && join();
-          if (ok && tid == 0) atomicExch(flags + q, 0);
+          seen = __all_sync(0xFFFFFFFFu, seen);
+          __threadfence();
+          if (lane == 0) s_ok = seen;
         }
+        ok = join() && s_ok != 0;
         if (!ok) break;
+        for (int q = walk.me + 1; q < last; ++q) {
+          const F2* part = reinterpret_cast<const F2*>(parts) + (size_t)q * (G::kPartBytes / 8) + tid;
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int i = 0; i < G::kPairs; ++i)
+              if (2 * i < mine) {
+                F2 o;
+                o.v = __ldcg(reinterpret_cast<const unsigned long long*>(part + (b * G::kPairs + i) * kSumThreads));
+                acc[b][i] = add2(acc[b][i], o);
+              }
+        }
+        ok = join();
+        if (!ok) break;
+        if (warp == 0)
+          for (int q = walk.me + 1 + lane; q < last; q += 32) atomicExch(flags + q, 0);
       }
       const int64_t outs = GATED ? a.N / 2 : a.N;
 #pragma unroll
       for (int b = 0; b < (GATED ? 1 : 2); ++b) {
         const int64_t col = GATED ? (int64_t)t.pair * 128 + n : (int64_t)t.pair * 256 + b * 128 + n;
-        const bool in = col < outs;
         using Out = typename std::conditional<WIDE, float, uint16_t>::type;
-        Out* p = static_cast<Out*>(a.y) + (int64_t)(t.row + 64 * wg) * outs + col;
-        const int rows = in ? mine : 0;
+        Out* p = static_cast<Out*>(a.y) + (int64_t)(t.row + BT / 2 * wg) * outs + col;
+        const int rows = col < outs ? mine : 0;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
+        for (int i = 0; i < G::kPairs; ++i) {
           float2 v = acc[b][i].get();
           if constexpr (GATED) {
             const float2 u = acc[1][i].get();
@@ -386,7 +410,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
             else *p = (uint16_t)(w >> 16);
           }
           p += outs;
-          asm volatile("" : "+l"(p));  // one address at a time, not 64 made ahead
+          asm volatile("" : "+l"(p));  // one address at a time, not all made ahead
         }
       }
     }
@@ -394,21 +418,23 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCodeRegs));
     // ------------------------------------------------ operands: column n of half b
     const int b = (warp - 8) / 4, n = warp % 4 * 32 + lane;
-    const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16) + kACol + 64 * b;
-    int q = 0, slot = 0;
+    const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16) + kACol + 32 * kPieces * b;
+    int q = 0, slot = 0, piece = 0;
     uint32_t q_phase = 0, a_phase = 1;
     while (ok && walk.next(tile, g0, g1)) {
       for (int g = g0; g < g1 && ok; ++g) {
-        ok = __all_sync(0xFFFFFFFFu, wait_bounded_inline(smem_u32(&bars.q_full[q]), q_phase, abort_flag, err, 711));
+        ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.q_full[q]), q_phase, abort_flag, err, 711));
         if (!ok) break;
-        const uint8_t* unit = smem + kQAt + q * kMoeUnitBytes;
-        const uint32_t codes = sm + kQAt + q * kMoeUnitBytes + b * 8192 + n * 16;
+        const uint8_t* unit = smem + G::kQAt + q * kMoeUnitBytes;
+        const uint32_t codes = sm + G::kQAt + q * kMoeUnitBytes + b * 8192 + n * 16;
         const int c = b * 128 + n;
         const uint32_t z = unit[kMoeZeroOffset + c / 2] >> (4 * (c & 1)) & 15u;
         const uint16_t raw = *reinterpret_cast<const uint16_t*>(unit + kMoeScaleOffset + 2 * c);
-        // A slot comes round again four groups later, when the products of the group before that have been issued, and
-        // those waited for the sums of at least the group after this one's to have been taken out.
-        reinterpret_cast<float*>(smem + kScaleAt)[slot * 256 + c] = unpack2<BF16>(raw).x;
+        uint4 w0 = lds128(codes), w1 = lds128(codes + 2048);
+        // Scales are written to a slot again 8 groups later.  By then the pieces of the group before were free, so the
+        // products of the group three back were done, and those waited until the sums of at least half kSums groups
+        // before them had been taken out, scales read.
+        reinterpret_cast<float*>(smem + G::kScaleAt)[slot * 256 + c] = unpack2<BF16>(raw).x;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars.s_full[slot]));
         uint32_t zz, z16 = 0u;
@@ -420,33 +446,46 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
           z16 = *reinterpret_cast<const uint32_t*>(&h);
         }
 #pragma unroll
-        for (int piece = 0; piece < 2; ++piece) {
-          const uint4 w0 = lds128(codes + (2 * piece) * 2048), w1 = lds128(codes + (2 * piece + 1) * 2048);
-          if (piece == 1) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars.q_empty[q]));
-          }
-          ok = __all_sync(0xFFFFFFFFu, wait_bounded_inline(smem_u32(&bars.a_empty[b][piece]), a_phase, abort_flag, err, 712));
-          if (!ok) break;
-          tc_fence_after();
+        for (int half = 0; half < 2; ++half) {
           uint32_t o[16];
           operands<BF16>(w0.x, zz, z16, o, 0);
           operands<BF16>(w0.y, zz, z16, o, 4);
           operands<BF16>(w0.z, zz, z16, o, 8);
           operands<BF16>(w0.w, zz, z16, o, 12);
+          if (half == 1) {
+            // the first half's stores had the time of these operations to arrive
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars.a_full[b][piece - 1]));
+          }
+          ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.a_empty[b][piece]), a_phase, abort_flag, err, 712));
+          if (!ok) break;
+          tc_fence_after();
           tmem_st16(lanes + 32 * piece, o);
           operands<BF16>(w1.x, zz, z16, o, 0);
           operands<BF16>(w1.y, zz, z16, o, 4);
           operands<BF16>(w1.z, zz, z16, o, 8);
           operands<BF16>(w1.w, zz, z16, o, 12);
+          if (half == 0) {
+            w0 = lds128(codes + 4096);
+            w1 = lds128(codes + 6144);
+          }
           tmem_st16(lanes + 32 * piece + 16, o);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&bars.a_full[b][piece]));
+          ++piece;
         }
-        a_phase ^= 1u;
-        if (++q == kQStages) {
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.q_empty[q]));
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.a_full[b][piece - 1]));
+        if (piece == kPieces) {
+          piece = 0;
+          a_phase ^= 1u;
+        }
+        if (++q == G::kQStages) {
           q = 0;
           q_phase ^= 1u;
         }
@@ -458,39 +497,44 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
     if (warp == 16) {
       // ------------------------------------------------ products
       const uint64_t bdesc0 = smem_desc_sw128(sm, 16, 1024);
-      int x = 0, d = 0;
+      int x = 0, d = 0, piece = 0;
       uint32_t x_phase = 0, d_phase = 1, a_phase = 0;
       while (ok && walk.next(tile, g0, g1)) {
-        const Tile t = find_tile(first, items, a.experts, pairs, tile);
+        const Tile t = find_tile<BT>(first, items, a.experts, pairs, tile);
         const uint32_t idesc = (1u << 4) | (BF16 ? (1u << 7) | (1u << 10) : 0u) | ((uint32_t)((t.rows + 15) / 16 * 2) << 17) |
                                (8u << 24);
         for (int g = g0; g < g1 && ok; ++g) {
-          ok = wait_bounded_inline(smem_u32(&bars.x_full[x]), x_phase, abort_flag, err, 721);
+          ok = wait_for(smem_u32(&bars.x_full[x]), x_phase, abort_flag, err, 721);
 #pragma unroll 1
           for (int b = 0; b < 2 && ok; ++b) {
-            ok = wait_bounded_inline(smem_u32(&bars.d_empty[d]), d_phase, abort_flag, err, 722);
+            ok = wait_for(smem_u32(&bars.d_empty[d]), d_phase, abort_flag, err, 722);
 #pragma unroll 1
-            for (int piece = 0; piece < 2 && ok; ++piece) {
-              ok = __all_sync(0xFFFFFFFFu, ok && wait_bounded_inline(smem_u32(&bars.a_full[b][piece]), a_phase, abort_flag, err, 723));
+            for (int half = 0; half < 2 && ok; ++half) {
+              ok = __all_sync(0xFFFFFFFFu, ok && wait_for(smem_u32(&bars.a_full[b][piece + half]), a_phase, abort_flag, err, 723));
               if (!ok) break;
               tc_fence_after();
-              const uint64_t bd = bdesc0 + (uint64_t)((x * kXBytes + piece * (kXBytes / 2)) >> 4);
+              const uint64_t bd = bdesc0 + (uint64_t)((x * G::kXBytes + half * (G::kXBytes / 2)) >> 4);
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                mma_ts(tmem + d * kBT, tmem + kACol + 64 * b + 32 * piece + 8 * k, bd + 2 * k, idesc, (piece | k) ? 1u : 0u);
-              commit(smem_u32(&bars.a_empty[b][piece]));
+                mma_ts(tmem + d * BT, tmem + kACol + 32 * (kPieces * b + piece + half) + 8 * k, bd + 2 * k, idesc,
+                       (half | k) ? 1u : 0u);
+              commit(smem_u32(&bars.a_empty[b][piece + half]));
             }
             if (!ok) break;
             commit(smem_u32(&bars.d_full[d]));
-            if (++d == kSums) {
+            if (++d == G::kSums) {
               d = 0;
               d_phase ^= 1u;
             }
           }
           if (!ok) break;
           commit(smem_u32(&bars.x_empty[x]));
-          a_phase ^= 1u;
-          if (++x == kXStages) {
+          piece += 2;
+          if (piece == kPieces) {
+            piece = 0;
+            a_phase ^= 1u;
+          }
+          if (++x == G::kXStages) {
             x = 0;
             x_phase ^= 1u;
           }
@@ -498,22 +542,22 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
       }
       commit(smem_u32(&bars.done));  // arrives once every product has completed
       volatile int no_abort = 0;
-      wait_bounded_inline(smem_u32(&bars.done), 0, &no_abort, err, 724);
+      wait_for(smem_u32(&bars.done), 0, &no_abort, err, 724);
     } else if (warp == 17) {
       // ------------------------------------------------ copies of weights
       if (lane == 0) {
         int q = 0, issued = 0;
         uint32_t q_phase = 1;
         while (ok && walk.next(tile, g0, g1)) {
-          const Tile t = find_tile(first, items, a.experts, pairs, tile);
+          const Tile t = find_tile<BT>(first, items, a.experts, pairs, tile);
           const uint8_t* src = a.packed + ((int64_t)t.expert * pairs + t.pair) * groups * kMoeUnitBytes;
           for (int g = g0; g < g1; ++g) {
-            ok = wait_bounded_inline(smem_u32(&bars.q_empty[q]), q_phase, abort_flag, err, 731);
+            ok = wait_for(smem_u32(&bars.q_empty[q]), q_phase, abort_flag, err, 731);
             if (!ok) break;
             mbar_arrive_tx(smem_u32(&bars.q_full[q]), kMoeUnitBytes);
-            bulk_load(sm + kQAt + q * kMoeUnitBytes, src + (int64_t)g * kMoeUnitBytes, kMoeUnitBytes, smem_u32(&bars.q_full[q]));
+            bulk_load(sm + G::kQAt + q * kMoeUnitBytes, src + (int64_t)g * kMoeUnitBytes, kMoeUnitBytes, smem_u32(&bars.q_full[q]));
             ++issued;
-            if (++q == kQStages) {
+            if (++q == G::kQStages) {
               q = 0;
               q_phase ^= 1u;
             }
@@ -521,43 +565,54 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
         }
         // never leave the CTA with copies in flight
         volatile int no_abort = 0;
-        for (int j = max(0, issued - kQStages); j < issued; ++j)
-          wait_bounded_inline(smem_u32(&bars.q_full[j % kQStages]), (uint32_t)(j / kQStages) & 1u, &no_abort, err, 732);
+        for (int j = max(0, issued - G::kQStages); j < issued; ++j)
+          wait_for(smem_u32(&bars.q_full[j % G::kQStages]), (uint32_t)(j / G::kQStages) & 1u, &no_abort, err, 732);
       }
-    } else if (warp == 18) {
-      // ------------------------------------------------ copies of rows: lane l has rows 4 l .. 4 l + 3 of the tile
-      int x = 0, issued = 0;
+    } else {
+      // ------------------------------------------------ copies of rows: half a warp has a row, warp wx rows 4 i + 2 wx, + 1
+      const int wx = warp - 18, upper = lane / 16, chunk = lane % 16;
+      int* source = reinterpret_cast<int*>(smem + G::kSourceAt) + wx * (BT / 2);
+      const uint32_t dst0 = sm + (chunk / 8) * (G::kXBytes / 2);
+      int x = 0, issued = 0, shown = 0;
       uint32_t x_phase = 1;
+      auto show = [&]() {  // a stage whose copies have arrived
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.x_full[shown % G::kXStages]));
+        ++shown;
+      };
       while (ok && walk.next(tile, g0, g1)) {
-        const Tile t = find_tile(first, items, a.experts, pairs, tile);
-        int r[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = t.row + min(4 * lane + i, t.rows - 1);
+        const Tile t = find_tile<BT>(first, items, a.experts, pairs, tile);
+        __syncwarp();
+        for (int i = lane; i < BT / 2; i += 32) {
+          const int row = t.row + min(i / 2 * 4 + 2 * wx + i % 2, t.rows - 1);
           const int src = a.order ? a.order[row] / a.top_k : row;
-          r[i] = src >= 0 && src < a.x_rows ? src : 0;
+          source[i] = src >= 0 && src < a.x_rows ? src : 0;
         }
-        const int fours = (t.rows + 3) / 4;
+        __syncwarp();
+        const int steps = (t.rows + 3) / 4;
         for (int g = g0; g < g1; ++g) {
-          ok = __all_sync(0xFFFFFFFFu, wait_bounded_inline(smem_u32(&bars.x_empty[x]), x_phase, abort_flag, err, 741));
+          ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.x_empty[x]), x_phase, abort_flag, err, 741));
           if (!ok) break;
-          const uint32_t bar = smem_u32(&bars.x_full[x]);
-          if (lane == 0) mbar_arrive_tx(bar, (uint32_t)fours * 1024u);
-          __syncwarp();
-          if (lane < fours) {
-            gather4(sm + x * kXBytes + lane * 512, &tm_x, g * 128, r, bar);
-            gather4(sm + x * kXBytes + kXBytes / 2 + lane * 512, &tm_x, g * 128 + 64, r, bar);
+          const uint16_t* from = a.x + g * 128 + chunk * 8;
+#pragma unroll 4
+          for (int i = 0; i < steps; ++i) {
+            const int row = 4 * i + 2 * wx + upper;
+            cp_async16(dst0 + x * G::kXBytes + row * 128 + ((chunk ^ row) & 7) * 16, from + source[2 * i + upper] * a.x_stride);
           }
-          ++issued;
-          if (++x == kXStages) {
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          if (++issued - shown > G::kXAhead) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(G::kXAhead) : "memory");
+            show();
+          }
+          if (++x == G::kXStages) {
             x = 0;
             x_phase ^= 1u;
           }
         }
       }
-      volatile int no_abort = 0;
-      for (int j = max(0, issued - kXStages); j < issued; ++j)
-        wait_bounded_inline(smem_u32(&bars.x_full[j % kXStages]), (uint32_t)(j / kXStages) & 1u, &no_abort, err, 742);
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      while (shown < issued) show();
     }
   }
   tc_fence_before();
@@ -568,30 +623,36 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
   }
 }
 
-template <bool BF16>
+template <int BT, bool BF16>
 cudaError_t launch(const MoeGemmArgs& a, bool gated, bool wide, void* ws, int* err, cudaStream_t s) {
-  CUtensorMap tm;
-  if (!make_map_2d(&tm, BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.x, (uint64_t)a.K,
-                   (uint64_t)a.x_rows, 64, 1, CU_TENSOR_MAP_SWIZZLE_128B, (uint64_t)a.x_stride))
-    return cudaErrorInvalidValue;
-  const auto fn = gated ? (wide ? moe_gemm_kernel<BF16, true, true> : moe_gemm_kernel<BF16, true, false>)
-                        : (wide ? moe_gemm_kernel<BF16, false, true> : moe_gemm_kernel<BF16, false, false>);
-  const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(fn), kSmem);
+  const auto fn = gated ? (wide ? moe_gemm_kernel<BT, BF16, true, true> : moe_gemm_kernel<BT, BF16, true, false>)
+                        : (wide ? moe_gemm_kernel<BT, BF16, false, true> : moe_gemm_kernel<BT, BF16, false, false>);
+  const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(fn), Geo<BT>::kSmem);
   if (e != cudaSuccess) return e;
   int* flags = static_cast<int*>(ws);
   float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kCounterBytes);
-  fn<<<device_sm_count(), kThreads, kSmem, s>>>(tm, a, flags, parts, err);
+  fn<<<device_sm_count(), kThreads, Geo<BT>::kSmem, s>>>(a, flags, parts, err);
   return cudaGetLastError();
+}
+
+// Rows of a tile: by the rows that an expert has on average, as their distribution is known on the device only.
+int tile_rows(int64_t R, int experts) {
+  const double mean = (double)R / experts;
+  return R <= 16 || mean <= 4 ? 16 : mean <= 40 ? 64 : 128;
 }
 
 }  // namespace
 
-size_t moe_gemm_workspace(int64_t, int, int64_t, int64_t, bool) {
-  return kCounterBytes + (size_t)device_sm_count() * kPartBytes;
+size_t moe_gemm_workspace(int64_t R, int experts, int64_t, int64_t, bool) {
+  return kCounterBytes + (size_t)device_sm_count() * kSumThreads * (size_t)tile_rows(R, experts) * 4;
 }
 
 cudaError_t launch_moe_gemm(const MoeGemmArgs& a, bool gated, bool wide, bool bf16, void* ws, int* err, cudaStream_t s) {
-  return bf16 ? launch<true>(a, gated, wide, ws, err, s) : launch<false>(a, gated, wide, ws, err, s);
+  const int bt = tile_rows(a.R, a.experts);
+  const auto fn = bt == 16   ? (bf16 ? launch<16, true> : launch<16, false>)
+                  : bt == 64 ? (bf16 ? launch<64, true> : launch<64, false>)
+                             : (bf16 ? launch<128, true> : launch<128, false>);
+  return fn(a, gated, wide, ws, err, s);
 }
 
 }  // namespace awq

@@ -27,15 +27,17 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// Row-major [outer][inner] tensor of elem_bytes-sized elements at `base`, copied in boxes of
-// box_outer x box_inner with swizzle `sw`, 256-byte L2 promotion, zero fill out of bounds.
+// Row-major [outer][inner] tensor of elem_bytes-sized elements at `base`, rows `stride` elements apart
+// (0: inner), copied in boxes of box_outer x box_inner with swizzle `sw`, 256-byte L2 promotion, zero
+// fill out of bounds.
 // A descriptor depends only on these arguments, so a small per-thread cache returns the one
 // encoded for an identical argument set.
 inline bool make_map_2d(CUtensorMap* map, CUtensorMapDataType dt, int elem_bytes, const void* base, uint64_t inner,
-                        uint64_t outer, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw) {
+                        uint64_t outer, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw,
+                        uint64_t stride = 0) {
   struct Key {
     const void* base;
-    uint64_t inner, outer;
+    uint64_t inner, outer, stride;
     uint32_t box_inner, box_outer;
     int32_t dt, elem_bytes, sw, pad;
   };
@@ -50,6 +52,7 @@ inline bool make_map_2d(CUtensorMap* map, CUtensorMapDataType dt, int elem_bytes
   key.base = base;
   key.inner = inner;
   key.outer = outer;
+  key.stride = stride ? stride : inner;
   key.box_inner = box_inner;
   key.box_outer = box_outer;
   key.dt = (int32_t)dt;
@@ -66,7 +69,7 @@ inline bool make_map_2d(CUtensorMap* map, CUtensorMapDataType dt, int elem_bytes
   const auto fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[2] = {inner, outer};
-  const cuuint64_t strides[1] = {inner * (uint64_t)elem_bytes};
+  const cuuint64_t strides[1] = {key.stride * (uint64_t)elem_bytes};
   const cuuint32_t box[2] = {box_inner, box_outer};
   const cuuint32_t estr[2] = {1, 1};
   if (fn(map, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,

@@ -9,14 +9,17 @@
 //   D[column][row] = A B,  A = weights, in tensor memory (128 columns x 64 k at once), B = rows of x, K-major in shared
 //   memory.  Weights in shared memory would cost it 192 bytes a cycle at the full rate of the products; so it moves
 //   64 (the operand B) and what the copies bring.
-// Roles: warps 0-7 add the groups' sums up and write results (a thread has one column of each half and BT / 2 rows: gate and up
-// of a gated layer meet in it), warps 8-15 turn codes into operands (a thread has a column), warp 16 issues the products,
-// warp 17 copies weights (one 17 KB unit a group), warps 18 and 19 rows of x (in any order; four rows of a tensor map an
-// instruction, tile::gather4, took 30 cycles each: 484 us against 273 without them at 32008 rows over 126 experts).
-// Sums and operand pieces in tensor memory go round, so that the products need not wait for either.
+// Roles: warps 0-15 add the groups' sums up and write results (a thread has one column of each half and BT / 4 rows: gate and
+// up of a gated layer meet in it), warps 16-23 turn codes into operands (a thread has a column), warp 24 issues the
+// products, warp 25 copies weights (one 17 KB unit a group), warps 26 and 27 rows of x.
+// Sums and operands in tensor memory go round, so that the products need not wait for either.
+// Rows of x come in any order.  Tiles of 128 rows want 32 KB of them a group, which only whole boxes of neighbouring rows
+// bring in time: they are put in order first (at 32008 rows over 126 experts 484 us with four rows an instruction,
+// tile::gather4, and 406 with 16 bytes a thread against 273 without any copies).  Smaller tiles copy 16 bytes a thread.
 //
 // Tiles are dealt out to a persistent grid in whole rounds; what is left over is cut evenly along K, and a tile that several
 // CTAs share is finished by the one that has its first group, which adds the others' sums in their order.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -30,14 +33,16 @@
 namespace awq {
 namespace {
 
-constexpr int kPieces = 4;      // operand pieces of a half in tensor memory, 32 columns (64 k) each: two groups
-constexpr int kACol = 256;      // operands in tensor memory: [half][piece]; the sums come before
+constexpr int kABufs = 2;       // operands of a half in tensor memory: two groups, 64 columns (128 k) each
+constexpr int kACol = 256;      // they come behind the sums
 constexpr int kScaleSlots = 8;  // groups whose scales are kept, see below
-constexpr int kThreads = 640, kSumThreads = 256;
-// Registers: 96 a thread at launch.
-constexpr int kLaunchRegs = 96, kSumRegs = 168, kCodeRegs = 56, kOtherRegs = 32;
-static_assert(256 * kSumRegs + 256 * kCodeRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "no more than was launched with");
+constexpr int kSumWarps = 16, kSumThreads = kSumWarps * 32, kCodeWarp = kSumWarps, kMmaWarp = kCodeWarp + 8;
+constexpr int kThreads = kSumThreads + 256 + 128;
+// Registers: 72 a thread at launch.
+constexpr int kLaunchRegs = 72, kSumRegs = 88, kCodeRegs = 56, kOtherRegs = 40;
+static_assert(kSumThreads * kSumRegs + 256 * kCodeRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "no more than was launched with");
 constexpr int kMinUnits = 4;    // groups that a CTA gets at least of what is cut along K
+constexpr int kBoxRows = 32;    // rows of a box of x
 
 // Tiles of up to BT rows.
 template <int BT>
@@ -45,15 +50,16 @@ struct Geo {
   static constexpr int kSums = BT == 128 ? 2 : 4;        // sums in tensor memory, BT columns each
   static constexpr int kXBytes = BT * 256;               // a group's rows: two blocks of 64 k, 128 bytes a row, swizzled
   static constexpr int kXStages = 4, kXAhead = 2;        // copies under way before one is waited for
+  static constexpr bool kBoxes = BT == 128;              // rows in order, copied in boxes
   static constexpr int kQStages = BT == 128 ? 5 : 8;
   // shared memory: rows of x | units | scales | expert tables | sources of rows
   static constexpr int kQAt = kXStages * kXBytes, kScaleAt = kQAt + kQStages * kMoeUnitBytes;
   static constexpr int kTableAt = kScaleAt + kScaleSlots * 256 * 4;
   static constexpr int kSourceAt = kTableAt + 2 * (kMoeMaxExperts + 1) * 4;
   static constexpr int kSmem = kSourceAt + BT * 4 + 1024;
-  static constexpr int kPairs = BT / 4;                  // pairs of rows of a summing thread, in each half
+  static constexpr int kRows = BT / 4, kPairs = BT / 8;  // rows of a summing thread, and pairs of them, in each half
   // a CTA's part of a shared tile: a sum for each of a summing thread's columns and rows
-  static constexpr size_t kPartBytes = (size_t)kSumThreads * BT * 4;
+  static constexpr size_t kPartBytes = (size_t)kSumThreads * 2 * kRows * 4;
   static_assert(kSums * BT <= kACol && kSmem <= 227 * 1024 - 1024, "tensor memory, shared memory");
   static_assert(kScaleSlots >= 5 + kSums / 2, "scales");
 };
@@ -61,7 +67,7 @@ struct Geo {
 template <int BT>
 struct Bars {
   uint64_t x_full[Geo<BT>::kXStages], x_empty[Geo<BT>::kXStages], q_full[Geo<BT>::kQStages], q_empty[Geo<BT>::kQStages],
-      a_full[2][kPieces], a_empty[2][kPieces], d_full[Geo<BT>::kSums], d_empty[Geo<BT>::kSums], s_full[kScaleSlots], join, done;
+      a_full[2][kABufs], a_empty[2][kABufs], d_full[Geo<BT>::kSums], d_empty[Geo<BT>::kSums], s_full[kScaleSlots], join, done;
 };
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -69,13 +75,27 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
-// A in tensor memory: a lane for each column of the weights, two k a column of it.  Executed by the whole warp with
-// uniform operands, issued by the lane that elect.sync chooses (always the same).
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// The products of one half and group, 128 k in steps of 16, into a fresh sum.  A in tensor memory: a lane for each column
+// of the weights, two k a column of it; B: two blocks of 64 k.  Executed by the whole warp with uniform operands, issued by
+// the lane that elect.sync chooses (always the same); one choice for all eight, which with one each took 60 cycles a product.
+__device__ __forceinline__ void mma_group(uint32_t d, uint32_t a, uint64_t b0, uint64_t b1, uint32_t idesc) {
   asm volatile(
-      "{\n .reg .pred p, q;\n elect.sync _|q, 0xFFFFFFFF;\n setp.ne.b32 p, %4, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n .reg .pred q, no, yes;\n .reg .b32 a1, a2, a3, a4, a5, a6, a7;\n .reg .b64 b01, b02, b03, b11, b12, b13;\n"
+      " setp.ne.b32 no, 0, 0;\n setp.eq.b32 yes, 0, 0;\n"
+      " add.u32 a1, %1, 8;\n add.u32 a2, %1, 16;\n add.u32 a3, %1, 24;\n add.u32 a4, %1, 32;\n add.u32 a5, %1, 40;\n"
+      " add.u32 a6, %1, 48;\n add.u32 a7, %1, 56;\n"
+      " add.u64 b01, %2, 2;\n add.u64 b02, %2, 4;\n add.u64 b03, %2, 6;\n"
+      " add.u64 b11, %3, 2;\n add.u64 b12, %3, 4;\n add.u64 b13, %3, 6;\n"
+      " elect.sync _|q, 0xFFFFFFFF;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, no;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b01, %4, yes;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b02, %4, yes;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b03, %4, yes;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a4], %3, %4, yes;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a5], b11, %4, yes;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a6], b12, %4, yes;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a7], b13, %4, yes;\n}\n" ::"r"(d),
+      "r"(a), "l"(b0), "l"(b1), "r"(idesc)
       : "memory");
 }
 __device__ __forceinline__ void commit(uint32_t bar) {
@@ -84,9 +104,32 @@ __device__ __forceinline__ void commit(uint32_t bar) {
       " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
       : "memory");
 }
+__device__ __forceinline__ void commit2(uint32_t bar0, uint32_t bar1) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xFFFFFFFF;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n}\n" ::"r"(bar0), "r"(bar1)
+      : "memory");
+}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+// Waits for this thread's tensor memory loads; `r` is not used before.
+__device__ __forceinline__ void wait_loaded(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr)
+               : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]) : : "memory");
+}
+
 // The first look comes before the clock is read for the limit.
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort, int* err, int id) {
   return mbar_try(bar, parity) || wait_bounded_inline(bar, parity, abort, err, id);
@@ -168,7 +211,7 @@ __device__ __forceinline__ Tile find_tile(const int* first, const int* items, in
 
 template <int BT, bool BF16, bool GATED, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1)
-moe_gemm_kernel(const MoeGemmArgs a, int* flags, float* parts, int* err) {
+moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, int* flags, float* parts, int* err) {
   using G = Geo<BT>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Bars<BT> bars;
@@ -185,28 +228,28 @@ moe_gemm_kernel(const MoeGemmArgs a, int* flags, float* parts, int* err) {
   if (tid == 32) {
     abort_word = 0;
     for (int i = 0; i < G::kXStages; ++i) {
-      mbar_init(smem_u32(&bars.x_full[i]), 2);
+      mbar_init(smem_u32(&bars.x_full[i]), G::kBoxes ? 1 : 2);
       mbar_init(smem_u32(&bars.x_empty[i]), 1);
     }
     for (int i = 0; i < G::kQStages; ++i) {
       mbar_init(smem_u32(&bars.q_full[i]), 1);
       mbar_init(smem_u32(&bars.q_empty[i]), 8);
     }
-    for (int i = 0; i < 2 * kPieces; ++i) {
+    for (int i = 0; i < 2 * kABufs; ++i) {
       mbar_init(smem_u32(&bars.a_full[0][i]), 4);
       mbar_init(smem_u32(&bars.a_empty[0][i]), 1);
     }
     for (int i = 0; i < G::kSums; ++i) {
       mbar_init(smem_u32(&bars.d_full[i]), 1);
-      mbar_init(smem_u32(&bars.d_empty[i]), 8);
+      mbar_init(smem_u32(&bars.d_empty[i]), kSumWarps);
     }
     for (int i = 0; i < kScaleSlots; ++i) mbar_init(smem_u32(&bars.s_full[i]), 8);
-    mbar_init(smem_u32(&bars.join), kSumThreads / 32);
+    mbar_init(smem_u32(&bars.join), kSumWarps);
     mbar_init(smem_u32(&bars.done), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
-  if (warp == 16) {
+  if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(512u)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -248,11 +291,11 @@ moe_gemm_kernel(const MoeGemmArgs a, int* flags, float* parts, int* err) {
   int tile, g0, g1;
   bool ok = true;
 
-  if (warp < 8) {
+  if (warp < kSumWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
-    // ------------------------------------------------ running sums: column n of each half, rows BT / 2 wg ..
+    // ------------------------------------------------ running sums: column n of each half, rows BT / 4 wg ..
     const int wg = warp / 4, n = warp % 4 * 32 + lane;
-    const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16) + BT / 2 * wg;
+    const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16) + G::kRows * wg;
     const float* scales = reinterpret_cast<const float*>(smem + G::kScaleAt);
     int d = 0, slot = 0;
     uint32_t d_phase = 0, slot_phase = 0, join_phase = 0;
@@ -264,9 +307,15 @@ moe_gemm_kernel(const MoeGemmArgs a, int* flags, float* parts, int* err) {
       join_phase ^= 1u;
       return all;
     };
+    // a sum is in registers
+    auto take = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars.d_empty[d]));
+    };
     while (ok && walk.next(tile, g0, g1)) {
       const Tile t = find_tile<BT>(first, items, a.experts, pairs, tile);
-      const int mine = min(max(t.rows - BT / 2 * wg, 0), BT / 2);  // of this thread's rows
+      const int mine = min(max(t.rows - G::kRows * wg, 0), G::kRows);  // of this thread's rows
       F2 acc[2][G::kPairs];
 #pragma unroll
       for (int b = 0; b < 2; ++b)
@@ -283,34 +332,29 @@ moe_gemm_kernel(const MoeGemmArgs a, int* flags, float* parts, int* err) {
           if (!ok) break;
           tc_fence_after();
           if constexpr (BT == 16) {
+            uint32_t v[4];
+            if (mine > 0) tmem_ld4(lanes + d * BT, v);
+            take();
             if (mine > 0) {
-              float v[8];
-              tmem_ld8(lanes + d * BT, v);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) acc[b][i] = fma2(F2(v[2 * i], v[2 * i + 1]), s2, acc[b][i]);
+              acc[b][0] = fma2(F2(__uint_as_float(v[0]), __uint_as_float(v[1])), s2, acc[b][0]);
+              acc[b][1] = fma2(F2(__uint_as_float(v[2]), __uint_as_float(v[3])), s2, acc[b][1]);
             }
           } else {
 #pragma unroll
-            for (int c = 0; c < G::kPairs / 8; c += 2) {
+            for (int c = 0; c < G::kRows / 16; ++c) {
+              uint32_t v[16];
               if (16 * c < mine) {
-                uint32_t v[2][16];
-                tmem_ld16_nowait(lanes + d * BT + 16 * c, v[0]);
-                tmem_ld16_nowait(lanes + d * BT + 16 * c + 16, v[1]);
-                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                tmem_ld16_nowait(lanes + d * BT + 16 * c, v);
+                wait_loaded(v);
+              }
+              if (c == G::kRows / 16 - 1) take();
+              if (16 * c < mine) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                  for (int i = 0; i < 8; ++i) {
-                    asm volatile("" : "+r"(v[h][2 * i]), "+r"(v[h][2 * i + 1]));  // not used before the wait
-                    F2& s0 = acc[b][8 * (c + h) + i];
-                    s0 = fma2(F2(__uint_as_float(v[h][2 * i]), __uint_as_float(v[h][2 * i + 1])), s2, s0);
-                  }
+                for (int i = 0; i < 8; ++i)
+                  acc[b][8 * c + i] = fma2(F2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s2, acc[b][8 * c + i]);
               }
             }
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&bars.d_empty[d]));
           if (++d == G::kSums) {
             d = 0;
             d_phase ^= 1u;
@@ -387,7 +431,7 @@ moe_gemm_kernel(const MoeGemmArgs a, int* flags, float* parts, int* err) {
       for (int b = 0; b < (GATED ? 1 : 2); ++b) {
         const int64_t col = GATED ? (int64_t)t.pair * 128 + n : (int64_t)t.pair * 256 + b * 128 + n;
         using Out = typename std::conditional<WIDE, float, uint16_t>::type;
-        Out* p = static_cast<Out*>(a.y) + (int64_t)(t.row + BT / 2 * wg) * outs + col;
+        Out* p = static_cast<Out*>(a.y) + (int64_t)(t.row + G::kRows * wg) * outs + col;
         const int rows = col < outs ? mine : 0;
 #pragma unroll
         for (int i = 0; i < G::kPairs; ++i) {
@@ -414,15 +458,15 @@ moe_gemm_kernel(const MoeGemmArgs a, int* flags, float* parts, int* err) {
         }
       }
     }
-  } else if (warp < 16) {
+  } else if (warp < kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCodeRegs));
     // ------------------------------------------------ operands: column n of half b
-    const int b = (warp - 8) / 4, n = warp % 4 * 32 + lane;
-    const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16) + kACol + 32 * kPieces * b;
-    int q = 0, slot = 0, piece = 0;
+    const int b = (warp - kCodeWarp) / 4, n = warp % 4 * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16) + kACol + 64 * kABufs * b;
+    int q = 0, slot = 0, buf = 0;
     uint32_t q_phase = 0, a_phase = 1;
     while (ok && walk.next(tile, g0, g1)) {
-      for (int g = g0; g < g1 && ok; ++g) {
+      for (int g = g0; g < g1; ++g) {
         ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.q_full[q]), q_phase, abort_flag, err, 711));
         if (!ok) break;
         const uint8_t* unit = smem + G::kQAt + q * kMoeUnitBytes;
@@ -430,9 +474,9 @@ moe_gemm_kernel(const MoeGemmArgs a, int* flags, float* parts, int* err) {
         const int c = b * 128 + n;
         const uint32_t z = unit[kMoeZeroOffset + c / 2] >> (4 * (c & 1)) & 15u;
         const uint16_t raw = *reinterpret_cast<const uint16_t*>(unit + kMoeScaleOffset + 2 * c);
-        uint4 w0 = lds128(codes), w1 = lds128(codes + 2048);
-        // Scales are written to a slot again 8 groups later.  By then the pieces of the group before were free, so the
-        // products of the group three back were done, and those waited until the sums of at least half kSums groups
+        uint4 w = lds128(codes);
+        // Scales are written to a slot again 8 groups later.  By then the operands of the group before were written, so
+        // the products of the group three back were done, and those waited until the sums of at least half kSums groups
         // before them had been taken out, scales read.
         reinterpret_cast<float*>(smem + G::kScaleAt)[slot * 256 + c] = unpack2<BF16>(raw).x;
         __syncwarp();
@@ -446,43 +490,32 @@ moe_gemm_kernel(const MoeGemmArgs a, int* flags, float* parts, int* err) {
           z16 = *reinterpret_cast<const uint32_t*>(&h);
         }
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        for (int chunk = 0; chunk < 4; ++chunk) {
           uint32_t o[16];
-          operands<BF16>(w0.x, zz, z16, o, 0);
-          operands<BF16>(w0.y, zz, z16, o, 4);
-          operands<BF16>(w0.z, zz, z16, o, 8);
-          operands<BF16>(w0.w, zz, z16, o, 12);
-          if (half == 1) {
-            // the first half's stores had the time of these operations to arrive
-            tmem_wait_st();
-            tc_fence_before();
+          operands<BF16>(w.x, zz, z16, o, 0);
+          operands<BF16>(w.y, zz, z16, o, 4);
+          operands<BF16>(w.z, zz, z16, o, 8);
+          operands<BF16>(w.w, zz, z16, o, 12);
+          if (chunk < 3) {
+            w = lds128(codes + 2048 * (chunk + 1));
+          } else {
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars.a_full[b][piece - 1]));
+            if (lane == 0) mbar_arrive(smem_u32(&bars.q_empty[q]));  // all codes are in registers
           }
-          ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.a_empty[b][piece]), a_phase, abort_flag, err, 712));
-          if (!ok) break;
-          tc_fence_after();
-          tmem_st16(lanes + 32 * piece, o);
-          operands<BF16>(w1.x, zz, z16, o, 0);
-          operands<BF16>(w1.y, zz, z16, o, 4);
-          operands<BF16>(w1.z, zz, z16, o, 8);
-          operands<BF16>(w1.w, zz, z16, o, 12);
-          if (half == 0) {
-            w0 = lds128(codes + 4096);
-            w1 = lds128(codes + 6144);
+          if (chunk == 0) {
+            ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.a_empty[b][buf]), a_phase, abort_flag, err, 712));
+            if (!ok) break;
+            tc_fence_after();
           }
-          tmem_st16(lanes + 32 * piece + 16, o);
-          ++piece;
+          tmem_st16(lanes + 64 * buf + 16 * chunk, o);
         }
         if (!ok) break;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars.q_empty[q]));
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars.a_full[b][piece - 1]));
-        if (piece == kPieces) {
-          piece = 0;
+        if (lane == 0) mbar_arrive(smem_u32(&bars.a_full[b][buf]));
+        if (++buf == kABufs) {
+          buf = 0;
           a_phase ^= 1u;
         }
         if (++q == G::kQStages) {
@@ -494,10 +527,10 @@ moe_gemm_kernel(const MoeGemmArgs a, int* flags, float* parts, int* err) {
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == 16) {
+    if (warp == kMmaWarp) {
       // ------------------------------------------------ products
       const uint64_t bdesc0 = smem_desc_sw128(sm, 16, 1024);
-      int x = 0, d = 0, piece = 0;
+      int x = 0, d = 0, buf = 0;
       uint32_t x_phase = 0, d_phase = 1, a_phase = 0;
       while (ok && walk.next(tile, g0, g1)) {
         const Tile t = find_tile<BT>(first, items, a.experts, pairs, tile);
@@ -505,23 +538,15 @@ moe_gemm_kernel(const MoeGemmArgs a, int* flags, float* parts, int* err) {
                                (8u << 24);
         for (int g = g0; g < g1 && ok; ++g) {
           ok = wait_for(smem_u32(&bars.x_full[x]), x_phase, abort_flag, err, 721);
+          const uint64_t bd = bdesc0 + (uint64_t)((x * G::kXBytes) >> 4);
 #pragma unroll 1
-          for (int b = 0; b < 2 && ok; ++b) {
-            ok = wait_for(smem_u32(&bars.d_empty[d]), d_phase, abort_flag, err, 722);
-#pragma unroll 1
-            for (int half = 0; half < 2 && ok; ++half) {
-              ok = __all_sync(0xFFFFFFFFu, ok && wait_for(smem_u32(&bars.a_full[b][piece + half]), a_phase, abort_flag, err, 723));
-              if (!ok) break;
-              tc_fence_after();
-              const uint64_t bd = bdesc0 + (uint64_t)((x * G::kXBytes + half * (G::kXBytes / 2)) >> 4);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_ts(tmem + d * BT, tmem + kACol + 32 * (kPieces * b + piece + half) + 8 * k, bd + 2 * k, idesc,
-                       (half | k) ? 1u : 0u);
-              commit(smem_u32(&bars.a_empty[b][piece + half]));
-            }
+          for (int b = 0; b < 2; ++b) {
+            ok = __all_sync(0xFFFFFFFFu, ok && wait_for(smem_u32(&bars.d_empty[d]), d_phase, abort_flag, err, 722) &&
+                                             wait_for(smem_u32(&bars.a_full[b][buf]), a_phase, abort_flag, err, 723));
             if (!ok) break;
-            commit(smem_u32(&bars.d_full[d]));
+            tc_fence_after();
+            mma_group(tmem + d * BT, tmem + kACol + 64 * (kABufs * b + buf), bd, bd + (uint64_t)(G::kXBytes >> 5), idesc);
+            commit2(smem_u32(&bars.d_full[d]), smem_u32(&bars.a_empty[b][buf]));
             if (++d == G::kSums) {
               d = 0;
               d_phase ^= 1u;
@@ -529,9 +554,8 @@ moe_gemm_kernel(const MoeGemmArgs a, int* flags, float* parts, int* err) {
           }
           if (!ok) break;
           commit(smem_u32(&bars.x_empty[x]));
-          piece += 2;
-          if (piece == kPieces) {
-            piece = 0;
+          if (++buf == kABufs) {
+            buf = 0;
             a_phase ^= 1u;
           }
           if (++x == G::kXStages) {
@@ -543,7 +567,7 @@ moe_gemm_kernel(const MoeGemmArgs a, int* flags, float* parts, int* err) {
       commit(smem_u32(&bars.done));  // arrives once every product has completed
       volatile int no_abort = 0;
       wait_for(smem_u32(&bars.done), 0, &no_abort, err, 724);
-    } else if (warp == 17) {
+    } else if (warp == kMmaWarp + 1) {
       // ------------------------------------------------ copies of weights
       if (lane == 0) {
         int q = 0, issued = 0;
@@ -568,9 +592,38 @@ moe_gemm_kernel(const MoeGemmArgs a, int* flags, float* parts, int* err) {
         for (int j = max(0, issued - G::kQStages); j < issued; ++j)
           wait_for(smem_u32(&bars.q_full[j % G::kQStages]), (uint32_t)(j / G::kQStages) & 1u, &no_abort, err, 732);
       }
+    } else if constexpr (G::kBoxes) {
+      // ------------------------------------------------ copies of rows, boxes of 32 rows x 64 k
+      if (warp == kMmaWarp + 2 && lane == 0) {
+        int x = 0, issued = 0;
+        uint32_t x_phase = 1;
+        while (ok && walk.next(tile, g0, g1)) {
+          const Tile t = find_tile<BT>(first, items, a.experts, pairs, tile);
+          const int boxes = (t.rows + kBoxRows - 1) / kBoxRows;
+          for (int g = g0; g < g1; ++g) {
+            ok = wait_for(smem_u32(&bars.x_empty[x]), x_phase, abort_flag, err, 743);
+            if (!ok) break;
+            const uint32_t bar = smem_u32(&bars.x_full[x]);
+            mbar_arrive_tx(bar, (uint32_t)(boxes * kBoxRows * 256));
+            for (int i = 0; i < boxes; ++i) {
+              const uint32_t dst = sm + x * G::kXBytes + i * (kBoxRows * 128);
+              tma_load_2d(dst, &tm_x, g * 128, t.row + i * kBoxRows, bar);
+              tma_load_2d(dst + G::kXBytes / 2, &tm_x, g * 128 + 64, t.row + i * kBoxRows, bar);
+            }
+            ++issued;
+            if (++x == G::kXStages) {
+              x = 0;
+              x_phase ^= 1u;
+            }
+          }
+        }
+        volatile int no_abort = 0;
+        for (int j = max(0, issued - G::kXStages); j < issued; ++j)
+          wait_for(smem_u32(&bars.x_full[j % G::kXStages]), (uint32_t)(j / G::kXStages) & 1u, &no_abort, err, 744);
+      }
     } else {
       // ------------------------------------------------ copies of rows: half a warp has a row, warp wx rows 4 i + 2 wx, + 1
-      const int wx = warp - 18, upper = lane / 16, chunk = lane % 16;
+      const int wx = warp - kMmaWarp - 2, upper = lane / 16, chunk = lane % 16;
       int* source = reinterpret_cast<int*>(smem + G::kSourceAt) + wx * (BT / 2);
       const uint32_t dst0 = sm + (chunk / 8) * (G::kXBytes / 2);
       int x = 0, issued = 0, shown = 0;
@@ -617,22 +670,21 @@ moe_gemm_kernel(const MoeGemmArgs a, int* flags, float* parts, int* err) {
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 16) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
   }
 }
 
-template <int BT, bool BF16>
-cudaError_t launch(const MoeGemmArgs& a, bool gated, bool wide, void* ws, int* err, cudaStream_t s) {
-  const auto fn = gated ? (wide ? moe_gemm_kernel<BT, BF16, true, true> : moe_gemm_kernel<BT, BF16, true, false>)
-                        : (wide ? moe_gemm_kernel<BT, BF16, false, true> : moe_gemm_kernel<BT, BF16, false, false>);
-  const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(fn), Geo<BT>::kSmem);
-  if (e != cudaSuccess) return e;
-  int* flags = static_cast<int*>(ws);
-  float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kCounterBytes);
-  fn<<<device_sm_count(), kThreads, Geo<BT>::kSmem, s>>>(a, flags, parts, err);
-  return cudaGetLastError();
+// Rows of x in the plan's order, 16 bytes a thread.
+__global__ void __launch_bounds__(256) moe_order_kernel(const MoeGemmArgs a, uint16_t* out) {
+  const int vec = (int)(a.K / 8), rows = min(max(a.offsets[a.experts], 0), (int)a.R);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)rows * vec; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / vec;
+    const int src = a.order[r] / a.top_k;
+    const int64_t from = src >= 0 && src < a.x_rows ? src * a.x_stride : 0;
+    reinterpret_cast<uint4*>(out)[i] = *reinterpret_cast<const uint4*>(a.x + from + (i - r * vec) * 8);
+  }
 }
 
 // Rows of a tile: by the rows that an expert has on average, as their distribution is known on the device only.
@@ -640,11 +692,43 @@ int tile_rows(int64_t R, int experts) {
   const double mean = (double)R / experts;
   return R <= 16 || mean <= 4 ? 16 : mean <= 40 ? 64 : 128;
 }
+// Workspace: flags | parts of shared tiles | rows in order
+size_t parts_bytes(int bt) { return align256((size_t)device_sm_count() * kSumThreads * (size_t)bt / 2 * 4); }
+
+template <int BT, bool BF16>
+cudaError_t launch(MoeGemmArgs a, bool gated, bool wide, void* ws, int* err, cudaStream_t s) {
+  using G = Geo<BT>;
+  const auto fn = gated ? (wide ? moe_gemm_kernel<BT, BF16, true, true> : moe_gemm_kernel<BT, BF16, true, false>)
+                        : (wide ? moe_gemm_kernel<BT, BF16, false, true> : moe_gemm_kernel<BT, BF16, false, false>);
+  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(fn), G::kSmem);
+  if (e != cudaSuccess) return e;
+  int* flags = static_cast<int*>(ws);
+  float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kCounterBytes);
+  CUtensorMap tm = {};
+  if (G::kBoxes) {
+    if (a.order) {
+      uint16_t* rows = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(parts) + parts_bytes(BT));
+      moe_order_kernel<<<device_sm_count() * 8, 256, 0, s>>>(a, rows);
+      e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+      a.x = rows;
+      a.x_rows = a.R;
+      a.x_stride = a.K;
+      a.order = nullptr;
+    }
+    if (!make_map_2d(&tm, BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.x, (uint64_t)a.K,
+                     (uint64_t)a.x_rows, 64, kBoxRows, CU_TENSOR_MAP_SWIZZLE_128B, (uint64_t)a.x_stride))
+      return cudaErrorInvalidValue;
+  }
+  fn<<<device_sm_count(), kThreads, G::kSmem, s>>>(tm, a, flags, parts, err);
+  return cudaGetLastError();
+}
 
 }  // namespace
 
-size_t moe_gemm_workspace(int64_t R, int experts, int64_t, int64_t, bool) {
-  return kCounterBytes + (size_t)device_sm_count() * kSumThreads * (size_t)tile_rows(R, experts) * 4;
+size_t moe_gemm_workspace(int64_t R, int experts, int64_t K, int64_t, bool gated) {
+  const int bt = tile_rows(R, experts);
+  return kCounterBytes + parts_bytes(bt) + (bt == 128 ? (size_t)R * (size_t)K * 2 : 0);
 }
 
 cudaError_t launch_moe_gemm(const MoeGemmArgs& a, bool gated, bool wide, bool bf16, void* ws, int* err, cudaStream_t s) {

@@ -43,13 +43,14 @@ constexpr int kLaunchRegs = 72, kSumRegs = 88, kCodeRegs = 56, kOtherRegs = 40;
 static_assert(kSumThreads * kSumRegs + 256 * kCodeRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "no more than was launched with");
 constexpr int kMinUnits = 4;    // groups that a CTA gets at least of what is cut along K
 constexpr int kBoxRows = 32;    // rows of a box of x
+constexpr int kXAhead = 2;      // groups of rows copied 16 bytes a thread that are under way before one is waited for
 
 // Tiles of up to BT rows.
 template <int BT>
 struct Geo {
   static constexpr int kSums = BT == 128 ? 2 : 4;        // sums in tensor memory, BT columns each
   static constexpr int kXBytes = BT * 256;               // a group's rows: two blocks of 64 k, 128 bytes a row, swizzled
-  static constexpr int kXStages = 4, kXAhead = 2;        // copies under way before one is waited for
+  static constexpr int kXStages = 4;
   static constexpr bool kBoxes = BT == 128;              // rows in order, copied in boxes
   static constexpr int kQStages = BT == 128 ? 5 : 8;
   // shared memory: rows of x | units | scales | expert tables | sources of rows
@@ -135,26 +136,28 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile
   return mbar_try(bar, parity) || wait_bounded_inline(bar, parity, abort, err, id);
 }
 
-// Four registers of operand (k pairs 0..3) from a word of eight codes.
+// Operands (q - z) 2^-kDown, exact, of a word of eight codes: k pairs 0..3.  A masked nibble is a subnormal 16-bit number, q or
+// 16 q of the smallest (in bf16 16 q reaches the lowest bit of the exponent, where numbers are still as far apart); one
+// multiplication and addition gives it its size and takes the zero point off.  One AND and one fma for two codes: 315
+// cycles a group for eight warps, where exponents put in by AND and OR took 670.
 template <bool BF16>
-__device__ __forceinline__ void operands(uint32_t w, uint32_t z, uint32_t z16, uint32_t (&o)[16], int at) {
-  if constexpr (BF16) {  // 128 + q less 128 + z, exact
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(o[at + i]) : "r"((w >> (4 * i) & 0x000F000Fu) | 0x43004300u), "r"(z));
-  } else {  // 1024 + q less 1024 + z; (1024 + 16 q) / 16 less 64 + z: exact
-    const uint32_t v = w >> 8;
-    const uint32_t h[4] = {(w & 0x000F000Fu) | 0x64006400u, (w & 0x00F000F0u) | 0x64006400u, (v & 0x000F000Fu) | 0x64006400u,
-                           (v & 0x00F000F0u) | 0x64006400u};
-    const __half2 sixteenth = __float2half2_rn(0.0625f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __half2 a = *reinterpret_cast<const __half2*>(&h[i]);
-      const __half2 r = i & 1 ? __hfma2(a, sixteenth, *reinterpret_cast<const __half2*>(&z16))
-                              : __hsub2(a, *reinterpret_cast<const __half2*>(&z));
-      o[at + i] = *reinterpret_cast<const uint32_t*>(&r);
-    }
-  }
+constexpr int kDown = BF16 ? 7 : 10;
+template <bool BF16>
+__device__ __forceinline__ uint32_t fma16(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  if constexpr (BF16) asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  else asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+template <bool BF16>
+__device__ __forceinline__ void operands(uint32_t w, uint32_t z, uint32_t (&o)[16], int at) {
+  constexpr uint32_t kOne = BF16 ? 0x7E807E80u : 0x74007400u;        // 2^126, 2^14
+  constexpr uint32_t kSixteenth = BF16 ? 0x7C807C80u : 0x64006400u;  // 2^122, 2^10
+  const uint32_t v = w >> 8;
+  o[at] = fma16<BF16>(w & 0x000F000Fu, kOne, z);
+  o[at + 1] = fma16<BF16>(w & 0x00F000F0u, kSixteenth, z);
+  o[at + 2] = fma16<BF16>(v & 0x000F000Fu, kOne, z);
+  o[at + 3] = fma16<BF16>(v & 0x00F000F0u, kSixteenth, z);
 }
 
 // What a CTA works on, in order: parts of tiles, groups g0 .. g1 - 1 of each.
@@ -478,24 +481,18 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
         // Scales are written to a slot again 8 groups later.  By then the operands of the group before were written, so
         // the products of the group three back were done, and those waited until the sums of at least half kSums groups
         // before them had been taken out, scales read.
-        reinterpret_cast<float*>(smem + G::kScaleAt)[slot * 256 + c] = unpack2<BF16>(raw).x;
+        reinterpret_cast<float*>(smem + G::kScaleAt)[slot * 256 + c] = unpack2<BF16>(raw).x * (float)(1 << kDown<BF16>);
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars.s_full[slot]));
-        uint32_t zz, z16 = 0u;
-        if constexpr (BF16) {
-          zz = (z | z << 16) | 0x43004300u;
-        } else {
-          zz = (z | z << 16) | 0x64006400u;
-          const __half2 h = __float2half2_rn(-64.f - (float)z);
-          z16 = *reinterpret_cast<const uint32_t*>(&h);
-        }
+        const float zf = (float)z * (-1.f / (1 << kDown<BF16>));
+        const uint32_t zz = pack2<BF16>(zf, zf);
 #pragma unroll
         for (int chunk = 0; chunk < 4; ++chunk) {
           uint32_t o[16];
-          operands<BF16>(w.x, zz, z16, o, 0);
-          operands<BF16>(w.y, zz, z16, o, 4);
-          operands<BF16>(w.z, zz, z16, o, 8);
-          operands<BF16>(w.w, zz, z16, o, 12);
+          operands<BF16>(w.x, zz, o, 0);
+          operands<BF16>(w.y, zz, o, 4);
+          operands<BF16>(w.z, zz, o, 8);
+          operands<BF16>(w.w, zz, o, 12);
           if (chunk < 3) {
             w = lds128(codes + 2048 * (chunk + 1));
           } else {
@@ -654,8 +651,8 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
             cp_async16(dst0 + x * G::kXBytes + row * 128 + ((chunk ^ row) & 7) * 16, from + source[2 * i + upper] * a.x_stride);
           }
           asm volatile("cp.async.commit_group;" ::: "memory");
-          if (++issued - shown > G::kXAhead) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(G::kXAhead) : "memory");
+          if (++issued - shown > kXAhead) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kXAhead) : "memory");
             show();
           }
           if (++x == G::kXStages) {

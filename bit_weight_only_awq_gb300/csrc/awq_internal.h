@@ -214,8 +214,11 @@ cudaError_t launch_moe_combine(const void* y, bool wide, const int32_t* place, c
 // columns x 128 rows): include/awq.h.
 constexpr int kMoeZeroOffset = 16384, kMoeScaleOffset = kMoeZeroOffset + 128, kMoeUnitBytes = kMoeScaleOffset + 512;
 static_assert(kMoeUnitBytes == 17024 && kMoeUnitBytes % 16 == 0, "codes | zero points | scales");
-// Byte of rows 32 chunk .. + 31 of column c (0..255).
-__host__ __device__ constexpr int moe_code_offset(int c, int chunk) { return ((c >> 7) * 4 + chunk) * 2048 + (c & 127) * 16; }
+// Byte of rows 32 chunk .. + 31 of column c (0..255), and the place of word w (eight rows) among them.
+__host__ __device__ constexpr int moe_code_offset(int c, int chunk) {
+  return ((c >> 7) * 4 + chunk) * 2048 + ((c & 127) ^ (2 * chunk)) * 16;
+}
+__host__ __device__ constexpr int moe_word_place(int w, int chunk) { return w ^ (chunk >> 1); }
 inline int64_t moe_tiles(int64_t N, bool gated) { return gated ? (N / 2 + 127) / 128 : (N + 255) / 256; }
 cudaError_t launch_moe_prepack(const uint32_t* qw, const uint32_t* qz, const uint16_t* sc, int experts, int64_t K, int64_t N,
                                bool gated, uint8_t* packed, cudaStream_t s);

@@ -29,6 +29,7 @@
 #include "awq_internal.h"
 #include "awq_ptx.cuh"
 #include "awq_types.cuh"
+#include "moe_gemm.cuh"
 
 namespace awq {
 namespace {
@@ -36,12 +37,6 @@ namespace {
 constexpr int kABufs = 2;       // operands of a half in tensor memory: two groups, 64 columns (128 k) each
 constexpr int kACol = 256;      // they come behind the sums
 constexpr int kScaleSlots = 8;  // groups whose scales are kept, see below
-constexpr int kSumWarps = 16, kSumThreads = kSumWarps * 32, kCodeWarp = kSumWarps, kMmaWarp = kCodeWarp + 8;
-constexpr int kThreads = kSumThreads + 256 + 128;
-// Registers: 72 a thread at launch.
-constexpr int kLaunchRegs = 72, kSumRegs = 88, kCodeRegs = 56, kOtherRegs = 40;
-static_assert(kSumThreads * kSumRegs + 256 * kCodeRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "no more than was launched with");
-constexpr int kMinUnits = 4;    // groups that a CTA gets at least of what is cut along K
 constexpr int kBoxRows = 32;    // rows of a box of x
 constexpr int kXAhead = 2;      // groups of rows copied 16 bytes a thread that are under way before one is waited for
 
@@ -51,6 +46,15 @@ struct Geo {
   static constexpr int kSums = BT == 128 ? 2 : 4;        // sums in tensor memory, BT columns each
   static constexpr int kXBytes = BT * 256;               // a group's rows: two blocks of 64 k, 128 bytes a row, swizzled
   static constexpr int kXStages = 4;
+  // warps that add up, then eight that make operands, then products and copies
+  static constexpr int kSumWarps = BT == 64 ? 8 : 16;
+  static constexpr int kCodeWarp = kSumWarps, kMmaWarp = kCodeWarp + 8;
+  static constexpr int kSumThreads = kSumWarps * 32, kThreads = (kMmaWarp + 4) * 32;
+  // registers of a thread: at launch, then by role
+  static constexpr int kLaunchRegs = BT == 64 ? 96 : 72, kSumRegs = BT == 64 ? 128 : 88,
+                       kCodeRegs = BT == 64 ? 72 : 56, kOtherRegs = BT == 64 ? 72 : 40;
+  static_assert(kSumThreads * kSumRegs + 256 * kCodeRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs &&
+                kThreads * kLaunchRegs <= 65536, "no more than was launched with");
   static constexpr bool kBoxes = BT == 128;              // rows in order, copied in boxes
   static constexpr int kQStages = BT == 128 ? 5 : 8;
   // shared memory: rows of x | units | scales | expert tables | sources of rows
@@ -58,9 +62,9 @@ struct Geo {
   static constexpr int kTableAt = kScaleAt + kScaleSlots * 256 * 4;
   static constexpr int kSourceAt = kTableAt + 2 * (kMoeMaxExperts + 1) * 4;
   static constexpr int kSmem = kSourceAt + BT * 4 + 1024;
-  static constexpr int kRows = BT / 4, kPairs = BT / 8;  // rows of a summing thread, and pairs of them, in each half
+  static constexpr int kRows = BT / (kSumWarps / 4), kPairs = kRows / 2;  // rows of a summing thread, and pairs of them, in each half
   // a CTA's part of a shared tile: a sum for each of a summing thread's columns and rows
-  static constexpr size_t kPartBytes = (size_t)kSumThreads * 2 * kRows * 4;
+  static constexpr size_t kPartBytes = (size_t)256 * BT * 4;
   static_assert(kSums * BT <= kACol && kSmem <= 227 * 1024 - 1024, "tensor memory, shared memory");
   static_assert(kScaleSlots >= 5 + kSums / 2, "scales");
 };
@@ -123,97 +127,14 @@ __device__ __forceinline__ void wait_loaded(uint32_t (&r)[16]) {
                :
                : "memory");
 }
-__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(taddr)
-               : "memory");
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]) : : "memory");
-}
 
 // The first look comes before the clock is read for the limit.
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort, int* err, int id) {
   return mbar_try(bar, parity) || wait_bounded_inline(bar, parity, abort, err, id);
 }
 
-// Operands (q - z) 2^-kDown, exact, of a word of eight codes: k pairs 0..3.  A masked nibble is a subnormal 16-bit number, q or
-// 16 q of the smallest (in bf16 16 q reaches the lowest bit of the exponent, where numbers are still as far apart); one
-// multiplication and addition gives it its size and takes the zero point off.  One AND and one fma for two codes: 315
-// cycles a group for eight warps, where exponents put in by AND and OR took 670.
-template <bool BF16>
-constexpr int kDown = BF16 ? 7 : 10;
-template <bool BF16>
-__device__ __forceinline__ uint32_t fma16(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  if constexpr (BF16) asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  else asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-template <bool BF16>
-__device__ __forceinline__ void operands(uint32_t w, uint32_t z, uint32_t (&o)[16], int at) {
-  constexpr uint32_t kOne = BF16 ? 0x7E807E80u : 0x74007400u;        // 2^126, 2^14
-  constexpr uint32_t kSixteenth = BF16 ? 0x7C807C80u : 0x64006400u;  // 2^122, 2^10
-  const uint32_t v = w >> 8;
-  o[at] = fma16<BF16>(w & 0x000F000Fu, kOne, z);
-  o[at + 1] = fma16<BF16>(w & 0x00F000F0u, kSixteenth, z);
-  o[at + 2] = fma16<BF16>(v & 0x000F000Fu, kOne, z);
-  o[at + 3] = fma16<BF16>(v & 0x00F000F0u, kSixteenth, z);
-}
-
-// What a CTA works on, in order: parts of tiles, groups g0 .. g1 - 1 of each.
-struct Walk {
-  int grid, me, groups, rounds, tiles;  // whole rounds of tiles; the tiles that are left
-  int round, u, u1;
-  long long units;
-  int ctas;
-  __device__ __forceinline__ Walk(int total, int groups_) : grid(gridDim.x), me(blockIdx.x), groups(groups_) {
-    rounds = total % grid == 0 ? total / grid : max(0, total / grid - 1);
-    tiles = total - rounds * grid;
-    units = (long long)tiles * groups;
-    ctas = (int)max(1ll, min((long long)grid, units / kMinUnits));
-    round = 0;
-    u = me < ctas ? begin_of(me) : 0;
-    u1 = me < ctas ? begin_of(me + 1) : 0;
-  }
-  __device__ __forceinline__ int begin_of(int cta) const { return (int)(units * cta / ctas); }
-  __device__ __forceinline__ bool next(int& tile, int& g0, int& g1) {
-    if (round < rounds) {
-      tile = me + grid * round++;
-      g0 = 0;
-      g1 = groups;
-      return true;
-    }
-    if (u >= u1) return false;
-    const int t = u / groups;
-    g0 = u - t * groups;
-    g1 = min(groups, g0 + u1 - u);
-    tile = rounds * grid + t;
-    u += g1 - g0;
-    return true;
-  }
-};
-
-struct Tile {
-  int expert, pair, row, rows;  // rows of y: row .. row + rows - 1
-};
-// Tables: first row of each expert, and items (row tiles) before it.  Within an expert the items of a column pair are
-// neighbours, so that the CTAs of one time share weights.
-template <int BT>
-__device__ __forceinline__ Tile find_tile(const int* first, const int* items, int experts, int pairs, int t) {
-  int lo = 0, hi = experts;  // the last expert with items[lo] * pairs <= t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (items[mid] * pairs <= t) lo = mid;
-    else hi = mid;
-  }
-  const int n = items[lo + 1] - items[lo], local = t - items[lo] * pairs, count = first[lo + 1] - first[lo];
-  const int pair = local / n, item = local - pair * n;
-  const int share = ((count + n - 1) / n + 15) / 16 * 16;  // rows even out over an expert's items
-  return Tile{lo, pair, first[lo] + item * share, min(share, count - item * share)};
-}
-
 template <int BT, bool BF16, bool GATED, bool WIDE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Geo<BT>::kThreads, 1)
 moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, int* flags, float* parts, int* err) {
   using G = Geo<BT>;
   extern __shared__ uint8_t smem_raw[];
@@ -244,47 +165,20 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
     }
     for (int i = 0; i < G::kSums; ++i) {
       mbar_init(smem_u32(&bars.d_full[i]), 1);
-      mbar_init(smem_u32(&bars.d_empty[i]), kSumWarps);
+      mbar_init(smem_u32(&bars.d_empty[i]), G::kSumWarps);
     }
     for (int i = 0; i < kScaleSlots; ++i) mbar_init(smem_u32(&bars.s_full[i]), 8);
-    mbar_init(smem_u32(&bars.join), kSumWarps);
+    mbar_init(smem_u32(&bars.join), G::kSumWarps);
     mbar_init(smem_u32(&bars.done), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
-  if (warp == kMmaWarp) {
+  if (warp == G::kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(512u)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  if (warp == 0) {
-    // offsets held to [0, R] and made to run forwards, and the items before each expert
-    int row = 0, item = 0;
-    for (int e0 = 0; e0 <= a.experts; e0 += 32) {
-      const int e = e0 + lane;
-      int v = e <= a.experts ? min(max(a.offsets[e], 0), (int)a.R) : 0;
-#pragma unroll
-      for (int d = 1; d < 32; d *= 2) {
-        const int o = __shfl_up_sync(0xFFFFFFFFu, v, d);
-        if (lane >= d) v = max(v, o);
-      }
-      v = max(v, row);
-      int before = __shfl_up_sync(0xFFFFFFFFu, v, 1);
-      if (lane == 0) before = e0 == 0 ? v : row;  // rows before the first expert's are nobody's
-      int n = e <= a.experts ? (v - before + BT - 1) / BT : 0;  // items of expert e - 1
-#pragma unroll
-      for (int d = 1; d < 32; d *= 2) {
-        const int o = __shfl_up_sync(0xFFFFFFFFu, n, d);
-        if (lane >= d) n += o;
-      }
-      if (e <= a.experts) {
-        first[e] = v;
-        items[e] = item + n;
-      }
-      row = __shfl_sync(0xFFFFFFFFu, v, 31);
-      item += __shfl_sync(0xFFFFFFFFu, n, 31);
-    }
-  }
+  if (warp == 0) expert_tables<BT>(a, lane, first, items);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -294,9 +188,9 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
   int tile, g0, g1;
   bool ok = true;
 
-  if (warp < kSumWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
-    // ------------------------------------------------ running sums: column n of each half, rows BT / 4 wg ..
+  if (warp < G::kSumWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::kSumRegs));
+    // ------------------------------------------------ running sums: column n of each half, rows kRows wg ..
     const int wg = warp / 4, n = warp % 4 * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16) + G::kRows * wg;
     const float* scales = reinterpret_cast<const float*>(smem + G::kScaleAt);
@@ -334,28 +228,18 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
           ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.d_full[d]), d_phase, abort_flag, err, 702));
           if (!ok) break;
           tc_fence_after();
-          if constexpr (BT == 16) {
-            uint32_t v[4];
-            if (mine > 0) tmem_ld4(lanes + d * BT, v);
-            take();
-            if (mine > 0) {
-              acc[b][0] = fma2(F2(__uint_as_float(v[0]), __uint_as_float(v[1])), s2, acc[b][0]);
-              acc[b][1] = fma2(F2(__uint_as_float(v[2]), __uint_as_float(v[3])), s2, acc[b][1]);
+#pragma unroll
+          for (int c = 0; c < G::kRows / 16; ++c) {
+            uint32_t v[16];
+            if (16 * c < mine) {
+              tmem_ld16_nowait(lanes + d * BT + 16 * c, v);
+              wait_loaded(v);
             }
-          } else {
+            if (c == G::kRows / 16 - 1) take();
+            if (16 * c < mine) {
 #pragma unroll
-            for (int c = 0; c < G::kRows / 16; ++c) {
-              uint32_t v[16];
-              if (16 * c < mine) {
-                tmem_ld16_nowait(lanes + d * BT + 16 * c, v);
-                wait_loaded(v);
-              }
-              if (c == G::kRows / 16 - 1) take();
-              if (16 * c < mine) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  acc[b][8 * c + i] = fma2(F2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s2, acc[b][8 * c + i]);
-              }
+              for (int i = 0; i < 8; ++i)
+                acc[b][8 * c + i] = fma2(F2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s2, acc[b][8 * c + i]);
             }
           }
           if (++d == G::kSums) {
@@ -376,7 +260,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
         for (int b = 0; b < 2; ++b)
 #pragma unroll
           for (int i = 0; i < G::kPairs; ++i)
-            if (2 * i < mine) __stcg(reinterpret_cast<unsigned long long*>(part + (b * G::kPairs + i) * kSumThreads), acc[b][i].v);
+            if (2 * i < mine) __stcg(reinterpret_cast<unsigned long long*>(part + (b * G::kPairs + i) * G::kSumThreads), acc[b][i].v);
         __threadfence();
         ok = join();
         if (ok && tid == 0) atomicExch(flags + walk.me, 1);
@@ -388,26 +272,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
         int last = walk.me + 1;
         while (last < walk.ctas && walk.begin_of(last) < end) ++last;
         if (warp == 0) {
-          bool seen = true;
-          for (int q = walk.me + 1 + lane; q < last && seen; q += 32) {
-            const long long t0 = now_ns();
-            for (uint32_t spin = 1;; ++spin) {
-              int v;
-              asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(flags + q) : "memory");
-              if (v) break;
-              if ((spin & 255u) == 0) {
-                if (*abort_flag) seen = false;
-                else if (now_ns() - t0 > kWaitLimitNs) {
-                  if (err) atomicExch(err, 703);
-                  *abort_flag = 1;
-                  seen = false;
-                }
-                if (!seen) break;
-              }
-            }
-          }
-          seen = __all_sync(0xFFFFFFFFu, seen);
-          __threadfence();
+          const bool seen = wait_flags(flags, walk.me + 1, last, lane, abort_flag, err, 703);
           if (lane == 0) s_ok = seen;
         }
         ok = join() && s_ok != 0;
@@ -420,7 +285,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
             for (int i = 0; i < G::kPairs; ++i)
               if (2 * i < mine) {
                 F2 o;
-                o.v = __ldcg(reinterpret_cast<const unsigned long long*>(part + (b * G::kPairs + i) * kSumThreads));
+                o.v = __ldcg(reinterpret_cast<const unsigned long long*>(part + (b * G::kPairs + i) * G::kSumThreads));
                 acc[b][i] = add2(acc[b][i], o);
               }
         }
@@ -442,8 +307,8 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
           if constexpr (GATED) {
             const float2 u = acc[1][i].get();
             if (2 * i < rows) {
-              v.x = __fdividef(v.x, 1.f + expf(-v.x)) * u.x;
-              v.y = __fdividef(v.y, 1.f + expf(-v.y)) * u.y;
+              v.x = silu_times(v.x, u.x);
+              v.y = silu_times(v.y, u.y);
             }
           }
           const uint32_t w = pack2<BF16>(v.x, v.y);
@@ -461,10 +326,10 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
         }
       }
     }
-  } else if (warp < kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCodeRegs));
+  } else if (warp < G::kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kCodeRegs));
     // ------------------------------------------------ operands: column n of half b
-    const int b = (warp - kCodeWarp) / 4, n = warp % 4 * 32 + lane;
+    const int b = (warp - G::kCodeWarp) / 4, n = warp % 4 * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16) + kACol + 64 * kABufs * b;
     int q = 0, slot = 0, buf = 0;
     uint32_t q_phase = 0, a_phase = 1;
@@ -473,11 +338,11 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
         ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.q_full[q]), q_phase, abort_flag, err, 711));
         if (!ok) break;
         const uint8_t* unit = smem + G::kQAt + q * kMoeUnitBytes;
-        const uint32_t codes = sm + G::kQAt + q * kMoeUnitBytes + b * 8192 + n * 16;
+        const uint32_t codes = sm + G::kQAt + q * kMoeUnitBytes;
         const int c = b * 128 + n;
         const uint32_t z = unit[kMoeZeroOffset + c / 2] >> (4 * (c & 1)) & 15u;
         const uint16_t raw = *reinterpret_cast<const uint16_t*>(unit + kMoeScaleOffset + 2 * c);
-        uint4 w = lds128(codes);
+        uint4 w = lds128(codes + moe_code_offset(c, 0));
         // Scales are written to a slot again 8 groups later.  By then the operands of the group before were written, so
         // the products of the group three back were done, and those waited until the sums of at least half kSums groups
         // before them had been taken out, scales read.
@@ -489,12 +354,12 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
 #pragma unroll
         for (int chunk = 0; chunk < 4; ++chunk) {
           uint32_t o[16];
-          operands<BF16>(w.x, zz, o, 0);
-          operands<BF16>(w.y, zz, o, 4);
-          operands<BF16>(w.z, zz, o, 8);
-          operands<BF16>(w.w, zz, o, 12);
+          operands<BF16>(w.x, zz, o, 4 * moe_word_place(0, chunk));
+          operands<BF16>(w.y, zz, o, 4 * moe_word_place(1, chunk));
+          operands<BF16>(w.z, zz, o, 4 * moe_word_place(2, chunk));
+          operands<BF16>(w.w, zz, o, 4 * moe_word_place(3, chunk));
           if (chunk < 3) {
-            w = lds128(codes + 2048 * (chunk + 1));
+            w = lds128(codes + moe_code_offset(c, chunk + 1));
           } else {
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bars.q_empty[q]));  // all codes are in registers
@@ -523,8 +388,8 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kOtherRegs));
+    if (warp == G::kMmaWarp) {
       // ------------------------------------------------ products
       const uint64_t bdesc0 = smem_desc_sw128(sm, 16, 1024);
       int x = 0, d = 0, buf = 0;
@@ -564,7 +429,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
       commit(smem_u32(&bars.done));  // arrives once every product has completed
       volatile int no_abort = 0;
       wait_for(smem_u32(&bars.done), 0, &no_abort, err, 724);
-    } else if (warp == kMmaWarp + 1) {
+    } else if (warp == G::kMmaWarp + 1) {
       // ------------------------------------------------ copies of weights
       if (lane == 0) {
         int q = 0, issued = 0;
@@ -591,7 +456,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
       }
     } else if constexpr (G::kBoxes) {
       // ------------------------------------------------ copies of rows, boxes of 32 rows x 64 k
-      if (warp == kMmaWarp + 2 && lane == 0) {
+      if (warp == G::kMmaWarp + 2 && lane == 0) {
         int x = 0, issued = 0;
         uint32_t x_phase = 1;
         while (ok && walk.next(tile, g0, g1)) {
@@ -620,7 +485,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
       }
     } else {
       // ------------------------------------------------ copies of rows: half a warp has a row, warp wx rows 4 i + 2 wx, + 1
-      const int wx = warp - kMmaWarp - 2, upper = lane / 16, chunk = lane % 16;
+      const int wx = warp - G::kMmaWarp - 2, upper = lane / 16, chunk = lane % 16;
       int* source = reinterpret_cast<int*>(smem + G::kSourceAt) + wx * (BT / 2);
       const uint32_t dst0 = sm + (chunk / 8) * (G::kXBytes / 2);
       int x = 0, issued = 0, shown = 0;
@@ -636,8 +501,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
         __syncwarp();
         for (int i = lane; i < BT / 2; i += 32) {
           const int row = t.row + min(i / 2 * 4 + 2 * wx + i % 2, t.rows - 1);
-          const int src = a.order ? a.order[row] / a.top_k : row;
-          source[i] = src >= 0 && src < a.x_rows ? src : 0;
+          source[i] = source_row(a, row);
         }
         __syncwarp();
         const int steps = (t.rows + 3) / 4;
@@ -667,7 +531,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == G::kMmaWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
   }
@@ -678,19 +542,17 @@ __global__ void __launch_bounds__(256) moe_order_kernel(const MoeGemmArgs a, uin
   const int vec = (int)(a.K / 8), rows = min(max(a.offsets[a.experts], 0), (int)a.R);
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)rows * vec; i += (int64_t)gridDim.x * 256) {
     const int64_t r = i / vec;
-    const int src = a.order[r] / a.top_k;
-    const int64_t from = src >= 0 && src < a.x_rows ? src * a.x_stride : 0;
-    reinterpret_cast<uint4*>(out)[i] = *reinterpret_cast<const uint4*>(a.x + from + (i - r * vec) * 8);
+    reinterpret_cast<uint4*>(out)[i] = *reinterpret_cast<const uint4*>(a.x + source_row(a, (int)r) * a.x_stride + (i - r * vec) * 8);
   }
 }
 
 // Rows of a tile: by the rows that an expert has on average, as their distribution is known on the device only.
 int tile_rows(int64_t R, int experts) {
   const double mean = (double)R / experts;
-  return R <= 16 || mean <= 4 ? 16 : mean <= 40 ? 64 : 128;
+  return R <= 16 || mean <= 4 ? kMoeGemvRows : mean <= 40 ? 64 : 128;
 }
 // Workspace: flags | parts of shared tiles | rows in order
-size_t parts_bytes(int bt) { return align256((size_t)device_sm_count() * kSumThreads * (size_t)bt / 2 * 4); }
+size_t parts_bytes(int bt) { return align256((size_t)device_sm_count() * 256 * (size_t)bt * 4); }
 
 template <int BT, bool BF16>
 cudaError_t launch(MoeGemmArgs a, bool gated, bool wide, void* ws, int* err, cudaStream_t s) {
@@ -717,7 +579,7 @@ cudaError_t launch(MoeGemmArgs a, bool gated, bool wide, void* ws, int* err, cud
                      (uint64_t)a.x_rows, 64, kBoxRows, CU_TENSOR_MAP_SWIZZLE_128B, (uint64_t)a.x_stride))
       return cudaErrorInvalidValue;
   }
-  fn<<<device_sm_count(), kThreads, G::kSmem, s>>>(tm, a, flags, parts, err);
+  fn<<<device_sm_count(), G::kThreads, G::kSmem, s>>>(tm, a, flags, parts, err);
   return cudaGetLastError();
 }
 
@@ -730,9 +592,10 @@ size_t moe_gemm_workspace(int64_t R, int experts, int64_t K, int64_t, bool gated
 
 cudaError_t launch_moe_gemm(const MoeGemmArgs& a, bool gated, bool wide, bool bf16, void* ws, int* err, cudaStream_t s) {
   const int bt = tile_rows(a.R, a.experts);
-  const auto fn = bt == 16   ? (bf16 ? launch<16, true> : launch<16, false>)
-                  : bt == 64 ? (bf16 ? launch<64, true> : launch<64, false>)
-                             : (bf16 ? launch<128, true> : launch<128, false>);
+  if (bt == kMoeGemvRows)
+    return launch_moe_gemv(a, gated, wide, bf16, static_cast<int*>(ws),
+                           reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kCounterBytes), err, s);
+  const auto fn = bt == 64 ? (bf16 ? launch<64, true> : launch<64, false>) : (bf16 ? launch<128, true> : launch<128, false>);
   return fn(a, gated, wide, ws, err, s);
 }
 

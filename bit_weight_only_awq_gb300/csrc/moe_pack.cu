@@ -1,7 +1,7 @@
 // The experts' weights laid out for the grouped product (layout: include/awq.h), and back.
 //
 // A thread has 32 rows of one packed word, which is 32 rows of 8 columns: in the prepared copy 16 consecutive bytes of
-// each column, the 8 columns next to one another, so its writes are 128 bytes in one piece.
+// each column, the 8 columns next to one another in some order, so its writes are 128 bytes in one piece.
 #include "awq_internal.h"
 
 namespace awq {
@@ -26,7 +26,6 @@ __global__ void __launch_bounds__(128) moe_prepack_kernel(const uint32_t* __rest
   const int w = threadIdx.x % 32, chunk = threadIdx.x / 32;
   const int64_t col = moe_column(tile, 8 * w, N, gated), nw = N / 8;  // eight columns lie on one side of every border
   const uint32_t* src = qw + ((int64_t)e * K + g * 128 + chunk * 32) * nw + col / 8;
-  uint4* dst = reinterpret_cast<uint4*>(unit + moe_code_offset(8 * w, chunk));
   uint32_t out[8][4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -42,7 +41,9 @@ __global__ void __launch_bounds__(128) moe_prepack_kernel(const uint32_t* __rest
     }
   }
 #pragma unroll
-  for (int c = 0; c < 8; ++c) dst[c] = make_uint4(out[c][0], out[c][1], out[c][2], out[c][3]);
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<uint4*>(unit + moe_code_offset(8 * w + c, chunk)) =
+        chunk < 2 ? make_uint4(out[c][0], out[c][1], out[c][2], out[c][3]) : make_uint4(out[c][1], out[c][0], out[c][3], out[c][2]);  // moe_word_place
   if (chunk == 0) {
     const uint32_t word = col < 0 ? 0u : qz ? qz[((int64_t)e * groups + g) * nw + col / 8] : 0x88888888u;
     uint32_t z = 0u;
@@ -65,15 +66,14 @@ __global__ void __launch_bounds__(128) moe_unprepack_kernel(const uint8_t* __res
   const int64_t col = moe_column(tile, 8 * w, N, gated), nw = N / 8;
   if (col < 0) return;
   uint32_t* dst = qw + ((int64_t)e * K + g * 128 + chunk * 32) * nw + col / 8;
-  const uint4* src = reinterpret_cast<const uint4*>(unit + moe_code_offset(8 * w, chunk));
   uint32_t in[8][4];
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
-    const uint4 v = src[c];
-    in[c][0] = v.x;
-    in[c][1] = v.y;
-    in[c][2] = v.z;
-    in[c][3] = v.w;
+    const uint4 v = *reinterpret_cast<const uint4*>(unit + moe_code_offset(8 * w + c, chunk));
+    in[c][0] = chunk < 2 ? v.x : v.y;
+    in[c][1] = chunk < 2 ? v.y : v.x;
+    in[c][2] = chunk < 2 ? v.z : v.w;
+    in[c][3] = chunk < 2 ? v.w : v.z;
   }
 #pragma unroll
   for (int q = 0; q < 4; ++q)

@@ -545,8 +545,9 @@ awq_status awq_moe_route(const void *logits, int64_t logits_stride, int64_t T, i
  * when the layer is loaded: codes, zero points and scales of the AWQ layers, rearranged.  A tile is 256 columns: of
  * a plain layer columns 256 j .. 256 j + 255; of a gated one (N = 2 I columns, gate first) gate columns 128 j .. + 127
  * and the same columns of up.  For each expert, tile and 128-row group (in this order) one 17024-byte unit:
- *   - codes: [half b: 2][chunk c: 4][column n: 128][word w: 4] uint32, nibble i of a word the code of column
- *     128 b + n of the tile and row 32 c + 8 w + map[i], map = [0, 2, 4, 6, 1, 3, 5, 7];
+ *   - codes: [half b: 2][chunk c: 4][place p: 128][place q: 4] uint32, nibble i of a word the code of column
+ *     128 b + (p ^ 2 c) of the tile and row 32 c + 8 (q ^ c / 2) + map[i], map = [0, 2, 4, 6, 1, 3, 5, 7] (the places of
+ *     columns and words keep the reads of both kernels free of bank conflicts);
  *   - zero points: [column: 256] nibbles, the even column in the low half of a byte;
  *   - scales: [column: 256], 16 bits.
  * Columns beyond the layer hold code 0, zero point 0 and scale 0.

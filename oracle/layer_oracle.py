@@ -78,12 +78,13 @@ def prepack(qweight, qzeros, scale_bits, gated: bool) -> np.ndarray:
                     unit = out[e, j, g]
                     codes = q[128 * g:128 * g + 128, n]
                     for chunk in range(4):
-                        at = (c // 128) * 8192 + chunk * 2048 + (c % 128) * 16
+                        at = (c // 128) * 8192 + chunk * 2048 + ((c % 128) ^ (2 * chunk)) * 16
                         for w in range(4):
                             word = 0
                             for i in range(8):
                                 word |= int(codes[32 * chunk + 8 * w + AWQ_ORDER[i]]) << (4 * i)
-                            unit[at + 4 * w:at + 4 * w + 4] = np.frombuffer(np.uint32(word).tobytes(), np.uint8)
+                            p = w ^ (chunk // 2)
+                            unit[at + 4 * p:at + 4 * p + 4] = np.frombuffer(np.uint32(word).tobytes(), np.uint8)
                     unit[16384 + c // 2] |= int(z[g, n]) << (4 * (c % 2))
                     unit[16512 + 2 * c:16512 + 2 * c + 2] = np.frombuffer(np.uint16(scale_bits[e, g, n]).tobytes(), np.uint8)
     return out

@@ -173,8 +173,8 @@ def test_oracle_prepack_holds_the_layer():
     assert p.shape == (2, 1, 1, 17024)
     from oracle import unpack
     q = unpack(qw[1])
-    # column 3 of up (layer column 35), row 77 = chunk 2, word 1, k 5 of 8: nibble 6 of the AWQ order
-    word = p[1, 0, 0, 8192 + 2 * 2048 + 3 * 16 + 4:][:4].copy().view(np.uint32)[0]
+    # column 3 of up (layer column 35), row 77 = chunk 2, word 1, k 5 of 8: place 3 ^ 4, word place 1 ^ 1, nibble 6 of the order
+    word = p[1, 0, 0, 8192 + 2 * 2048 + 7 * 16 + 0:][:4].copy().view(np.uint32)[0]
     assert word >> (4 * 6) & 15 == q[77, 35]
     assert p[1, 0, 0, 16384 + 64 + 1] >> 4 == 8 and p[1, 0, 0, 16384 + 20] == 0
     assert p[1, 0, 0, 16512 + 2 * (128 + 3):][:2].copy().view(np.uint16)[0] == sc[1, 0, 35]

@@ -9,10 +9,11 @@
 //   D[column][row] = A B,  A = weights, in tensor memory (128 columns x 64 k at once), B = rows of x, K-major in shared
 //   memory.  Weights in shared memory would cost it 192 bytes a cycle at the full rate of the products; so it moves
 //   64 (the operand B) and what the copies bring.
-// Roles: warps 0-15 add the groups' sums up and write results (a thread has one column of each half and BT / 4 rows: gate and
-// up of a gated layer meet in it), warps 16-23 turn codes into operands (a thread has a column), warp 24 issues the
-// products, warp 25 copies weights (one 17 KB unit a group), warps 26 and 27 rows of x.
-// Sums and operands in tensor memory go round, so that the products need not wait for either.
+// Roles: the first warps add the groups' sums up and write results (a thread has one column of each half and some rows: gate and
+// up of a gated layer meet in it), eight warps turn codes into operands (a thread has a column), then come a warp that issues the
+// products, one that copies weights (one 17 KB unit a group) and two for rows of x.
+// Sums and operands in tensor memory go round, so that the products need not wait for either.  A step of the products is a half
+// of a group in tiles of 128 rows and a whole group in smaller ones; whoever waits for its products waits on one barrier.
 // Rows of x come in any order.  Tiles of 128 rows want 32 KB of them a group, which only whole boxes of neighbouring rows
 // bring in time: they are put in order first (at 32008 rows over 126 experts 484 us with four rows an instruction,
 // tile::gather4, and 406 with 16 bytes a thread against 273 without any copies).  Smaller tiles copy 16 bytes a thread.
@@ -29,50 +30,53 @@
 #include "awq_internal.h"
 #include "awq_ptx.cuh"
 #include "awq_types.cuh"
-#include "moe_gemm.cuh"
 
 namespace awq {
 namespace {
 
-constexpr int kABufs = 2;       // operands of a half in tensor memory: two groups, 64 columns (128 k) each
-constexpr int kACol = 256;      // they come behind the sums
 constexpr int kScaleSlots = 8;  // groups whose scales are kept, see below
+constexpr int kRing = 4;        // groups whose products' barriers and rows are kept
 constexpr int kBoxRows = 32;    // rows of a box of x
 constexpr int kXAhead = 2;      // groups of rows copied 16 bytes a thread that are under way before one is waited for
 
 // Tiles of up to BT rows.
 template <int BT>
 struct Geo {
-  static constexpr int kSums = BT == 128 ? 2 : 4;        // sums in tensor memory, BT columns each
+  static constexpr int kSteps = BT == 128 ? 2 : 1;       // steps of a group, each of 2 / kSteps halves
+  static constexpr int kSumCols = BT * 2 / kSteps;       // columns of a step's sums
+  static constexpr int kSums = BT == 16 ? 4 : 2;         // steps whose sums are kept in tensor memory
+  static constexpr int kACol = kSums * kSumCols;         // operands come behind them: [half][buffer] of 64 columns (128 k)
+  static constexpr int kABufs = BT == 16 ? 3 : 2;        // groups whose operands are kept
   static constexpr int kXBytes = BT * 256;               // a group's rows: two blocks of 64 k, 128 bytes a row, swizzled
-  static constexpr int kXStages = 4;
+  static constexpr bool kBoxes = BT == 128;              // rows in order, copied in boxes
+  static constexpr int kQStages = BT == 128 ? 5 : BT == 64 ? 8 : 10;
   // warps that add up, then eight that make operands, then products and copies
-  static constexpr int kSumWarps = BT == 64 ? 8 : 16;
+  static constexpr int kSumWarps = BT == 16 ? 4 : 8;
   static constexpr int kCodeWarp = kSumWarps, kMmaWarp = kCodeWarp + 8;
   static constexpr int kSumThreads = kSumWarps * 32, kThreads = (kMmaWarp + 4) * 32;
   // registers of a thread: at launch, then by role
-  static constexpr int kLaunchRegs = BT == 64 ? 96 : 72, kSumRegs = BT == 64 ? 128 : 88,
-                       kCodeRegs = BT == 64 ? 72 : 56, kOtherRegs = BT == 64 ? 72 : 40;
+  static constexpr int kLaunchRegs = BT == 16 ? 128 : 96, kSumRegs = BT == 16 ? 128 : BT == 64 ? 128 : 168,
+                       kCodeRegs = BT == 16 ? 128 : BT == 64 ? 72 : 56, kOtherRegs = BT == 16 ? 128 : BT == 64 ? 72 : 32;
   static_assert(kSumThreads * kSumRegs + 256 * kCodeRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs &&
                 kThreads * kLaunchRegs <= 65536, "no more than was launched with");
-  static constexpr bool kBoxes = BT == 128;              // rows in order, copied in boxes
-  static constexpr int kQStages = BT == 128 ? 5 : 8;
   // shared memory: rows of x | units | scales | expert tables | sources of rows
-  static constexpr int kQAt = kXStages * kXBytes, kScaleAt = kQAt + kQStages * kMoeUnitBytes;
+  static constexpr int kQAt = kRing * kXBytes, kScaleAt = kQAt + kQStages * kMoeUnitBytes;
   static constexpr int kTableAt = kScaleAt + kScaleSlots * 256 * 4;
   static constexpr int kSourceAt = kTableAt + 2 * (kMoeMaxExperts + 1) * 4;
   static constexpr int kSmem = kSourceAt + BT * 4 + 1024;
   static constexpr int kRows = BT / (kSumWarps / 4), kPairs = kRows / 2;  // rows of a summing thread, and pairs of them, in each half
+  static constexpr int kAtOnce = BT == 64 ? 2 : 1;       // loads of 16 columns of sums at once
   // a CTA's part of a shared tile: a sum for each of a summing thread's columns and rows
   static constexpr size_t kPartBytes = (size_t)256 * BT * 4;
-  static_assert(kSums * BT <= kACol && kSmem <= 227 * 1024 - 1024, "tensor memory, shared memory");
-  static_assert(kScaleSlots >= 5 + kSums / 2, "scales");
+  static_assert(kACol + 2 * kABufs * 64 <= 512 && kSmem <= 227 * 1024 - 1024, "tensor memory, shared memory");
+  static_assert(kABufs <= kRing && kSums <= kRing * kSteps, "barriers of products");
+  static_assert(kScaleSlots >= kABufs + kSums / kSteps + 1, "scales");
 };
 
 template <int BT>
 struct Bars {
-  uint64_t x_full[Geo<BT>::kXStages], x_empty[Geo<BT>::kXStages], q_full[Geo<BT>::kQStages], q_empty[Geo<BT>::kQStages],
-      a_full[2][kABufs], a_empty[2][kABufs], d_full[Geo<BT>::kSums], d_empty[Geo<BT>::kSums], s_full[kScaleSlots], join, done;
+  uint64_t x_full[kRing], q_full[Geo<BT>::kQStages], q_empty[Geo<BT>::kQStages],
+      a_full[Geo<BT>::kABufs][Geo<BT>::kSteps], done[kRing][Geo<BT>::kSteps], d_empty[Geo<BT>::kSums], join, end;
 };
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -109,13 +113,6 @@ __device__ __forceinline__ void commit(uint32_t bar) {
       " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void commit2(uint32_t bar0, uint32_t bar1) {
-  asm volatile(
-      "{\n .reg .pred q;\n elect.sync _|q, 0xFFFFFFFF;\n"
-      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n"
-      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n}\n" ::"r"(bar0), "r"(bar1)
-      : "memory");
-}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -132,6 +129,147 @@ __device__ __forceinline__ void wait_loaded(uint32_t (&r)[16]) {
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort, int* err, int id) {
   return mbar_try(bar, parity) || wait_bounded_inline(bar, parity, abort, err, id);
 }
+
+// Operands (q - z) 2^-kDown, exact, of a word of eight codes: k pairs 0..3.  A masked nibble is a subnormal 16-bit number, q or
+// 16 q of the smallest (in bf16 16 q reaches the lowest bit of the exponent, where numbers are still as far apart); one
+// multiplication and addition gives it its size and takes the zero point off.  One AND and one fma for two codes: 315
+// cycles a group for eight warps, where exponents put in by AND and OR took 670.
+template <bool BF16>
+constexpr int kDown = BF16 ? 7 : 10;
+template <bool BF16>
+__device__ __forceinline__ uint32_t fma16(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  if constexpr (BF16) asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  else asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+template <bool BF16>
+__device__ __forceinline__ void operands(uint32_t w, uint32_t z, uint32_t* o, int at) {
+  constexpr uint32_t kOne = BF16 ? 0x7E807E80u : 0x74007400u;        // 2^126, 2^14
+  constexpr uint32_t kSixteenth = BF16 ? 0x7C807C80u : 0x64006400u;  // 2^122, 2^10
+  const uint32_t v = w >> 8;
+  o[at] = fma16<BF16>(w & 0x000F000Fu, kOne, z);
+  o[at + 1] = fma16<BF16>(w & 0x00F000F0u, kSixteenth, z);
+  o[at + 2] = fma16<BF16>(v & 0x000F000Fu, kOne, z);
+  o[at + 3] = fma16<BF16>(v & 0x00F000F0u, kSixteenth, z);
+}
+
+constexpr int kMinUnits = 4;  // groups that a CTA gets at least of what is cut along K
+
+// What a CTA works on, in order: parts of tiles, groups g0 .. g1 - 1 of each.
+struct Walk {
+  int grid, me, groups, rounds, tiles;  // whole rounds of tiles; the tiles that are left
+  int round, u, u1;
+  long long units;
+  int ctas;
+  __device__ __forceinline__ Walk(int total, int groups_) : grid(gridDim.x), me(blockIdx.x), groups(groups_) {
+    rounds = total % grid == 0 ? total / grid : max(0, total / grid - 1);
+    tiles = total - rounds * grid;
+    units = (long long)tiles * groups;
+    ctas = (int)max(1ll, min((long long)grid, units / kMinUnits));
+    round = 0;
+    u = me < ctas ? begin_of(me) : 0;
+    u1 = me < ctas ? begin_of(me + 1) : 0;
+  }
+  __device__ __forceinline__ int begin_of(int cta) const { return (int)(units * cta / ctas); }
+  __device__ __forceinline__ bool next(int& tile, int& g0, int& g1) {
+    if (round < rounds) {
+      tile = me + grid * round++;
+      g0 = 0;
+      g1 = groups;
+      return true;
+    }
+    if (u >= u1) return false;
+    const int t = u / groups;
+    g0 = u - t * groups;
+    g1 = min(groups, g0 + u1 - u);
+    tile = rounds * grid + t;
+    u += g1 - g0;
+    return true;
+  }
+};
+
+struct Tile {
+  int expert, pair, row, rows;  // rows of y: row .. row + rows - 1
+};
+// Tables: first row of each expert, and items (row tiles) before it.  Within an expert the items of a column pair are
+// neighbours, so that the CTAs of one time share weights.
+template <int BT>
+__device__ __forceinline__ Tile find_tile(const int* first, const int* items, int experts, int pairs, int t) {
+  int lo = 0, hi = experts;  // the last expert with items[lo] * pairs <= t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (items[mid] * pairs <= t) lo = mid;
+    else hi = mid;
+  }
+  const int n = items[lo + 1] - items[lo], local = t - items[lo] * pairs, count = first[lo + 1] - first[lo];
+  const int pair = local / n, item = local - pair * n;
+  const int share = ((count + n - 1) / n + 15) / 16 * 16;  // rows even out over an expert's items
+  return Tile{lo, pair, first[lo] + item * share, min(share, count - item * share)};
+}
+
+// Tables of the experts, by one warp: offsets held to [0, R] and made to run forwards, and the items before each expert.
+template <int BT>
+__device__ __forceinline__ void expert_tables(const MoeGemmArgs& a, int lane, int* first, int* items) {
+  int row = 0, item = 0;
+  for (int e0 = 0; e0 <= a.experts; e0 += 32) {
+    const int e = e0 + lane;
+    int v = e <= a.experts ? min(max(a.offsets[e], 0), (int)a.R) : 0;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+      if (lane >= d) v = max(v, o);
+    }
+    v = max(v, row);
+    int before = __shfl_up_sync(0xFFFFFFFFu, v, 1);
+    if (lane == 0) before = e0 == 0 ? v : row;  // rows before the first expert's are nobody's
+    int n = e <= a.experts ? (v - before + BT - 1) / BT : 0;  // items of expert e - 1
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, n, d);
+      if (lane >= d) n += o;
+    }
+    if (e <= a.experts) {
+      first[e] = v;
+      items[e] = item + n;
+    }
+    row = __shfl_sync(0xFFFFFFFFu, v, 31);
+    item += __shfl_sync(0xFFFFFFFFu, n, 31);
+  }
+}
+
+// A source row of x for row `row` of the plan's order; one that makes no sense reads row 0.
+__device__ __forceinline__ int source_row(const MoeGemmArgs& a, int row) {
+  const int src = a.order ? a.order[row] / a.top_k : row;
+  return src >= 0 && src < a.x_rows ? src : 0;
+}
+
+// The calling warp's lanes wait for flags [from, to), all at once.
+__device__ __forceinline__ bool wait_flags(const int* flags, int from, int to, int lane, volatile int* abort, int* err, int id) {
+  bool seen = true;
+  for (int q = from + lane; q < to && seen; q += 32) {
+    const long long t0 = now_ns();
+    for (uint32_t spin = 1;; ++spin) {
+      int v;
+      asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(flags + q) : "memory");
+      if (v) break;
+      if ((spin & 255u) == 0) {
+        if (*abort) seen = false;
+        else if (now_ns() - t0 > kWaitLimitNs) {
+          if (err) atomicExch(err, id);
+          *abort = 1;
+          seen = false;
+        }
+        if (!seen) break;
+      }
+    }
+  }
+  seen = __all_sync(0xFFFFFFFFu, seen);
+  __threadfence();
+  return seen;
+}
+
+__device__ __forceinline__ float silu_times(float gate, float up) { return __fdividef(gate, 1.f + expf(-gate)) * up; }
 
 template <int BT, bool BF16, bool GATED, bool WIDE>
 __global__ void __launch_bounds__(Geo<BT>::kThreads, 1)
@@ -151,25 +289,18 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
 
   if (tid == 32) {
     abort_word = 0;
-    for (int i = 0; i < G::kXStages; ++i) {
+    for (int i = 0; i < kRing; ++i) {
       mbar_init(smem_u32(&bars.x_full[i]), G::kBoxes ? 1 : 2);
-      mbar_init(smem_u32(&bars.x_empty[i]), 1);
+      for (int h = 0; h < G::kSteps; ++h) mbar_init(smem_u32(&bars.done[i][h]), 1);
     }
     for (int i = 0; i < G::kQStages; ++i) {
       mbar_init(smem_u32(&bars.q_full[i]), 1);
       mbar_init(smem_u32(&bars.q_empty[i]), 8);
     }
-    for (int i = 0; i < 2 * kABufs; ++i) {
-      mbar_init(smem_u32(&bars.a_full[0][i]), 4);
-      mbar_init(smem_u32(&bars.a_empty[0][i]), 1);
-    }
-    for (int i = 0; i < G::kSums; ++i) {
-      mbar_init(smem_u32(&bars.d_full[i]), 1);
-      mbar_init(smem_u32(&bars.d_empty[i]), G::kSumWarps);
-    }
-    for (int i = 0; i < kScaleSlots; ++i) mbar_init(smem_u32(&bars.s_full[i]), 8);
+    for (int i = 0; i < G::kABufs * G::kSteps; ++i) mbar_init(smem_u32(&bars.a_full[0][i]), 8 / G::kSteps);
+    for (int i = 0; i < G::kSums; ++i) mbar_init(smem_u32(&bars.d_empty[i]), G::kSumWarps);
     mbar_init(smem_u32(&bars.join), G::kSumWarps);
-    mbar_init(smem_u32(&bars.done), 1);
+    mbar_init(smem_u32(&bars.end), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -189,13 +320,13 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
   bool ok = true;
 
   if (warp < G::kSumWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::kSumRegs));
+    if constexpr (G::kSumRegs > G::kLaunchRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::kSumRegs));
     // ------------------------------------------------ running sums: column n of each half, rows kRows wg ..
     const int wg = warp / 4, n = warp % 4 * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16) + G::kRows * wg;
     const float* scales = reinterpret_cast<const float*>(smem + G::kScaleAt);
-    int d = 0, slot = 0;
-    uint32_t d_phase = 0, slot_phase = 0, join_phase = 0;
+    int d = 0, count = 0;  // count: groups so far, of this CTA
+    uint32_t join_phase = 0;
     // all summing warps, or false: a wait that gives up elsewhere must not leave this one waiting
     auto join = [&]() {
       __syncwarp();
@@ -218,38 +349,42 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
       for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int i = 0; i < G::kPairs; ++i) acc[b][i] = F2(0.f, 0.f);
-      for (int g = g0; g < g1 && ok; ++g) {
-        ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.s_full[slot]), slot_phase, abort_flag, err, 701));
-        if (!ok) break;
+      for (int g = g0; g < g1 && ok; ++g, ++count) {
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const float s = scales[slot * 256 + b * 128 + n];
-          const F2 s2(s, s);
-          ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.d_full[d]), d_phase, abort_flag, err, 702));
+        for (int step = 0; step < G::kSteps; ++step) {
+          ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.done[count % kRing][step]), (uint32_t)(count / kRing) & 1u,
+                                                abort_flag, err, 702));
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < G::kRows / 16; ++c) {
-            uint32_t v[16];
-            if (16 * c < mine) {
-              tmem_ld16_nowait(lanes + d * BT + 16 * c, v);
-              wait_loaded(v);
-            }
-            if (c == G::kRows / 16 - 1) take();
-            if (16 * c < mine) {
+          for (int bb = 0; bb < 2 / G::kSteps; ++bb) {
+            const int b = G::kSteps == 2 ? step : bb;
+            const float s = scales[count % kScaleSlots * 256 + b * 128 + n];
+            const F2 s2(s, s);
+            const uint32_t from = lanes + d * G::kSumCols + bb * BT;
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                acc[b][8 * c + i] = fma2(F2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s2, acc[b][8 * c + i]);
+            for (int c = 0; c < G::kRows / 16; c += G::kAtOnce) {
+              uint32_t v[G::kAtOnce][16];
+              const bool any = 16 * c < mine;
+              if (any) {
+#pragma unroll
+                for (int h = 0; h < G::kAtOnce; ++h) tmem_ld16_nowait(from + 16 * (c + h), v[h]);
+#pragma unroll
+                for (int h = 0; h < G::kAtOnce; ++h) wait_loaded(v[h]);
+              }
+              if (bb == 2 / G::kSteps - 1 && c + G::kAtOnce == G::kRows / 16) take();
+              if (any) {
+#pragma unroll
+                for (int h = 0; h < G::kAtOnce; ++h)
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) {
+                    F2& to = acc[b][8 * (c + h) + i];
+                    to = fma2(F2(__uint_as_float(v[h][2 * i]), __uint_as_float(v[h][2 * i + 1])), s2, to);
+                  }
+              }
             }
           }
-          if (++d == G::kSums) {
-            d = 0;
-            d_phase ^= 1u;
-          }
-        }
-        if (++slot == kScaleSlots) {
-          slot = 0;
-          slot_phase ^= 1u;
+          if (++d == G::kSums) d = 0;
         }
       }
       if (!ok) break;
@@ -327,28 +462,22 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
       }
     }
   } else if (warp < G::kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kCodeRegs));
+    if constexpr (G::kCodeRegs < G::kLaunchRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kCodeRegs));
     // ------------------------------------------------ operands: column n of half b
     const int b = (warp - G::kCodeWarp) / 4, n = warp % 4 * 32 + lane;
-    const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16) + kACol + 64 * kABufs * b;
-    int q = 0, slot = 0, buf = 0;
-    uint32_t q_phase = 0, a_phase = 1;
+    const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16) + G::kACol + 64 * G::kABufs * b;
+    const int step = G::kSteps == 2 ? b : 0, c = b * 128 + n;
+    int q = 0, buf = 0, count = 0;
+    uint32_t q_phase = 0;
     while (ok && walk.next(tile, g0, g1)) {
-      for (int g = g0; g < g1; ++g) {
+      for (int g = g0; g < g1; ++g, ++count) {
         ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.q_full[q]), q_phase, abort_flag, err, 711));
         if (!ok) break;
         const uint8_t* unit = smem + G::kQAt + q * kMoeUnitBytes;
         const uint32_t codes = sm + G::kQAt + q * kMoeUnitBytes;
-        const int c = b * 128 + n;
+        uint4 w = lds128(codes + moe_code_offset(c, 0));
         const uint32_t z = unit[kMoeZeroOffset + c / 2] >> (4 * (c & 1)) & 15u;
         const uint16_t raw = *reinterpret_cast<const uint16_t*>(unit + kMoeScaleOffset + 2 * c);
-        uint4 w = lds128(codes + moe_code_offset(c, 0));
-        // Scales are written to a slot again 8 groups later.  By then the operands of the group before were written, so
-        // the products of the group three back were done, and those waited until the sums of at least half kSums groups
-        // before them had been taken out, scales read.
-        reinterpret_cast<float*>(smem + G::kScaleAt)[slot * 256 + c] = unpack2<BF16>(raw).x * (float)(1 << kDown<BF16>);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars.s_full[slot]));
         const float zf = (float)z * (-1.f / (1 << kDown<BF16>));
         const uint32_t zz = pack2<BF16>(zf, zf);
 #pragma unroll
@@ -358,77 +487,74 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
           operands<BF16>(w.y, zz, o, 4 * moe_word_place(1, chunk));
           operands<BF16>(w.z, zz, o, 4 * moe_word_place(2, chunk));
           operands<BF16>(w.w, zz, o, 4 * moe_word_place(3, chunk));
-          if (chunk < 3) {
-            w = lds128(codes + moe_code_offset(c, chunk + 1));
-          } else {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars.q_empty[q]));  // all codes are in registers
-          }
-          if (chunk == 0) {
-            ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.a_empty[b][buf]), a_phase, abort_flag, err, 712));
+          if (chunk < 3) w = lds128(codes + moe_code_offset(c, chunk + 1));
+          if (chunk == 0 && count >= G::kABufs) {
+            // the products that read this buffer last
+            const int last = count - G::kABufs;
+            ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.done[last % kRing][step]), (uint32_t)(last / kRing) & 1u,
+                                                  abort_flag, err, 712));
             if (!ok) break;
             tc_fence_after();
           }
           tmem_st16(lanes + 64 * buf + 16 * chunk, o);
         }
         if (!ok) break;
+        // Scales for the sums.  A slot is written again 8 groups later: the products of kABufs groups back are done, which
+        // waited until the sums of the steps kSums before them had been taken out, their scales read.
+        reinterpret_cast<float*>(smem + G::kScaleAt)[count % kScaleSlots * 256 + c] = unpack2<BF16>(raw).x * (float)(1 << kDown<BF16>);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.q_empty[q]));  // all codes are in registers
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars.a_full[b][buf]));
-        if (++buf == kABufs) {
-          buf = 0;
-          a_phase ^= 1u;
-        }
+        if (lane == 0) mbar_arrive(smem_u32(&bars.a_full[buf][step]));
+        if (++buf == G::kABufs) buf = 0;
         if (++q == G::kQStages) {
           q = 0;
           q_phase ^= 1u;
         }
-        if (++slot == kScaleSlots) slot = 0;
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kOtherRegs));
+    if constexpr (G::kOtherRegs < G::kLaunchRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kOtherRegs));
     if (warp == G::kMmaWarp) {
       // ------------------------------------------------ products
       const uint64_t bdesc0 = smem_desc_sw128(sm, 16, 1024);
-      int x = 0, d = 0, buf = 0;
-      uint32_t x_phase = 0, d_phase = 1, a_phase = 0;
+      int d = 0, buf = 0, count = 0;
+      uint32_t d_phase = 1, a_phase = 0;
       while (ok && walk.next(tile, g0, g1)) {
         const Tile t = find_tile<BT>(first, items, a.experts, pairs, tile);
         const uint32_t idesc = (1u << 4) | (BF16 ? (1u << 7) | (1u << 10) : 0u) | ((uint32_t)((t.rows + 15) / 16 * 2) << 17) |
                                (8u << 24);
-        for (int g = g0; g < g1 && ok; ++g) {
-          ok = wait_for(smem_u32(&bars.x_full[x]), x_phase, abort_flag, err, 721);
+        for (int g = g0; g < g1 && ok; ++g, ++count) {
+          const int x = count % kRing;
+          ok = wait_for(smem_u32(&bars.x_full[x]), (uint32_t)(count / kRing) & 1u, abort_flag, err, 721);
           const uint64_t bd = bdesc0 + (uint64_t)((x * G::kXBytes) >> 4);
 #pragma unroll 1
-          for (int b = 0; b < 2; ++b) {
+          for (int step = 0; step < G::kSteps; ++step) {
             ok = __all_sync(0xFFFFFFFFu, ok && wait_for(smem_u32(&bars.d_empty[d]), d_phase, abort_flag, err, 722) &&
-                                             wait_for(smem_u32(&bars.a_full[b][buf]), a_phase, abort_flag, err, 723));
+                                             wait_for(smem_u32(&bars.a_full[buf][step]), a_phase, abort_flag, err, 723));
             if (!ok) break;
             tc_fence_after();
-            mma_group(tmem + d * BT, tmem + kACol + 64 * (kABufs * b + buf), bd, bd + (uint64_t)(G::kXBytes >> 5), idesc);
-            commit2(smem_u32(&bars.d_full[d]), smem_u32(&bars.a_empty[b][buf]));
+#pragma unroll
+            for (int bb = 0; bb < 2 / G::kSteps; ++bb)
+              mma_group(tmem + d * G::kSumCols + bb * BT, tmem + G::kACol + 64 * (G::kABufs * (step + bb) + buf), bd,
+                        bd + (uint64_t)(G::kXBytes >> 5), idesc);
+            commit(smem_u32(&bars.done[x][step]));
             if (++d == G::kSums) {
               d = 0;
               d_phase ^= 1u;
             }
           }
-          if (!ok) break;
-          commit(smem_u32(&bars.x_empty[x]));
-          if (++buf == kABufs) {
+          if (++buf == G::kABufs) {
             buf = 0;
             a_phase ^= 1u;
           }
-          if (++x == G::kXStages) {
-            x = 0;
-            x_phase ^= 1u;
-          }
         }
       }
-      commit(smem_u32(&bars.done));  // arrives once every product has completed
+      commit(smem_u32(&bars.end));  // arrives once every product has completed
       volatile int no_abort = 0;
-      wait_for(smem_u32(&bars.done), 0, &no_abort, err, 724);
+      wait_for(smem_u32(&bars.end), 0, &no_abort, err, 724);
     } else if (warp == G::kMmaWarp + 1) {
       // ------------------------------------------------ copies of weights
       if (lane == 0) {
@@ -457,14 +583,16 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
     } else if constexpr (G::kBoxes) {
       // ------------------------------------------------ copies of rows, boxes of 32 rows x 64 k
       if (warp == G::kMmaWarp + 2 && lane == 0) {
-        int x = 0, issued = 0;
-        uint32_t x_phase = 1;
+        int count = 0;
         while (ok && walk.next(tile, g0, g1)) {
           const Tile t = find_tile<BT>(first, items, a.experts, pairs, tile);
           const int boxes = (t.rows + kBoxRows - 1) / kBoxRows;
-          for (int g = g0; g < g1; ++g) {
-            ok = wait_for(smem_u32(&bars.x_empty[x]), x_phase, abort_flag, err, 743);
-            if (!ok) break;
+          for (int g = g0; g < g1; ++g, ++count) {
+            const int x = count % kRing;
+            if (count >= kRing) {
+              ok = wait_for(smem_u32(&bars.done[x][G::kSteps - 1]), (uint32_t)(count / kRing - 1) & 1u, abort_flag, err, 743);
+              if (!ok) break;
+            }
             const uint32_t bar = smem_u32(&bars.x_full[x]);
             mbar_arrive_tx(bar, (uint32_t)(boxes * kBoxRows * 256));
             for (int i = 0; i < boxes; ++i) {
@@ -472,28 +600,22 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
               tma_load_2d(dst, &tm_x, g * 128, t.row + i * kBoxRows, bar);
               tma_load_2d(dst + G::kXBytes / 2, &tm_x, g * 128 + 64, t.row + i * kBoxRows, bar);
             }
-            ++issued;
-            if (++x == G::kXStages) {
-              x = 0;
-              x_phase ^= 1u;
-            }
           }
         }
         volatile int no_abort = 0;
-        for (int j = max(0, issued - G::kXStages); j < issued; ++j)
-          wait_for(smem_u32(&bars.x_full[j % G::kXStages]), (uint32_t)(j / G::kXStages) & 1u, &no_abort, err, 744);
+        for (int j = max(0, count - kRing); j < count; ++j)
+          wait_for(smem_u32(&bars.x_full[j % kRing]), (uint32_t)(j / kRing) & 1u, &no_abort, err, 744);
       }
     } else {
       // ------------------------------------------------ copies of rows: half a warp has a row, warp wx rows 4 i + 2 wx, + 1
       const int wx = warp - G::kMmaWarp - 2, upper = lane / 16, chunk = lane % 16;
       int* source = reinterpret_cast<int*>(smem + G::kSourceAt) + wx * (BT / 2);
       const uint32_t dst0 = sm + (chunk / 8) * (G::kXBytes / 2);
-      int x = 0, issued = 0, shown = 0;
-      uint32_t x_phase = 1;
+      int issued = 0, shown = 0;
       auto show = [&]() {  // a stage whose copies have arrived
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars.x_full[shown % G::kXStages]));
+        if (lane == 0) mbar_arrive(smem_u32(&bars.x_full[shown % kRing]));
         ++shown;
       };
       while (ok && walk.next(tile, g0, g1)) {
@@ -506,8 +628,12 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
         __syncwarp();
         const int steps = (t.rows + 3) / 4;
         for (int g = g0; g < g1; ++g) {
-          ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.x_empty[x]), x_phase, abort_flag, err, 741));
-          if (!ok) break;
+          const int x = issued % kRing;
+          if (issued >= kRing) {
+            ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.done[x][G::kSteps - 1]), (uint32_t)(issued / kRing - 1) & 1u,
+                                                  abort_flag, err, 741));
+            if (!ok) break;
+          }
           const uint16_t* from = a.x + g * 128 + chunk * 8;
 #pragma unroll 4
           for (int i = 0; i < steps; ++i) {
@@ -518,10 +644,6 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
           if (++issued - shown > kXAhead) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kXAhead) : "memory");
             show();
-          }
-          if (++x == G::kXStages) {
-            x = 0;
-            x_phase ^= 1u;
           }
         }
       }
@@ -549,7 +671,7 @@ __global__ void __launch_bounds__(256) moe_order_kernel(const MoeGemmArgs a, uin
 // Rows of a tile: by the rows that an expert has on average, as their distribution is known on the device only.
 int tile_rows(int64_t R, int experts) {
   const double mean = (double)R / experts;
-  return R <= 16 || mean <= 4 ? kMoeGemvRows : mean <= 40 ? 64 : 128;
+  return R <= 16 || mean <= 4 ? 16 : mean <= 40 ? 64 : 128;
 }
 // Workspace: flags | parts of shared tiles | rows in order
 size_t parts_bytes(int bt) { return align256((size_t)device_sm_count() * 256 * (size_t)bt * 4); }
@@ -592,10 +714,9 @@ size_t moe_gemm_workspace(int64_t R, int experts, int64_t K, int64_t, bool gated
 
 cudaError_t launch_moe_gemm(const MoeGemmArgs& a, bool gated, bool wide, bool bf16, void* ws, int* err, cudaStream_t s) {
   const int bt = tile_rows(a.R, a.experts);
-  if (bt == kMoeGemvRows)
-    return launch_moe_gemv(a, gated, wide, bf16, static_cast<int*>(ws),
-                           reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kCounterBytes), err, s);
-  const auto fn = bt == 64 ? (bf16 ? launch<64, true> : launch<64, false>) : (bf16 ? launch<128, true> : launch<128, false>);
+  const auto fn = bt == 16   ? (bf16 ? launch<16, true> : launch<16, false>)
+                  : bt == 64 ? (bf16 ? launch<64, true> : launch<64, false>)
+                             : (bf16 ? launch<128, true> : launch<128, false>);
   return fn(a, gated, wide, ws, err, s);
 }
 

@@ -241,7 +241,7 @@ size_t moe_gemm_workspace(int64_t R, int experts, int64_t K, int64_t N, bool gat
 // wide: y in fp32
 cudaError_t launch_moe_gemm(const MoeGemmArgs& a, bool gated, bool wide, bool bf16, void* ws, int* err, cudaStream_t s);
 
-// ---- e4m3 linear layers with scales for blocks of 128 (fp8_linear.cu)
+// ---- e4m3 linear layers with scales for blocks of 128 (fp8_quant.cu, fp8_gemm.cu)
 cudaError_t launch_fp8_quant(const uint16_t* x, int64_t x_stride, uint8_t* xq, float* s_x, int64_t M, int64_t K, bool bf16,
                              cudaStream_t s);
 struct Fp8GemmArgs {

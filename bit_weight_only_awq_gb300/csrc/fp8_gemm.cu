@@ -1,0 +1,372 @@
+// Product of e4m3 activations and weights with scales for blocks of 128, on the 5th-generation tensor cores.
+//
+// y[m, n] = sum_g s_x[g, m] s_w[n / 128, g] sum_{k in block g} xq[m, k] wq[n, k].
+// Each block of 128 k has a sum of its own in tensor memory (fp32; its products are exact), which is multiplied by the
+// two scales and added to the running sum in fp32 registers: a column of the tile is a token, so the factor s_x s_w is one
+// of BT numbers in shared memory, the same for all lanes.
+//
+// A CTA works on tiles of 128 outputs x up to BT tokens: D[output][token] = A B with A = weights and B = codes, both K-major in
+// shared memory, tcgen05.mma kind::f8f6f4.  Roles: the first warps add up and write results (a thread has an output and BT or BT / 2
+// tokens), then come a warp that issues the products, one that copies both operands (one 128-byte row of each a block) and one that
+// makes the factors.  The persistent grid and sums that cross CTAs are those of the grouped product.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "awq_host.h"
+#include "awq_internal.h"
+#include "awq_ptx.cuh"
+#include "awq_types.cuh"
+#include "layer_common.cuh"
+
+namespace awq {
+namespace {
+
+constexpr int kOut = 128, kABytes = kOut * 128;  // outputs of a tile; bytes of a block's weights
+
+template <int BT>
+struct Geo {
+  static constexpr int kBytes = kABytes + BT * 128;     // a stage: weights | codes
+  static constexpr int kStages = BT == 256 ? 4 : BT == 64 ? 8 : 11;
+  static constexpr int kSums = BT == 256 ? 2 : 4;       // blocks whose sums are kept in tensor memory, BT columns each
+  // A factor's slot is written again when the products kStages before it are done; those waited for the sums kSums
+  // further back to be taken out.
+  static constexpr int kSlots = kStages + kSums;
+  static constexpr int kBoxRows = BT < 64 ? BT : 64;
+  static constexpr int kSumWarps = BT == 256 ? 8 : 4, kMmaWarp = kSumWarps;
+  static constexpr int kSumThreads = kSumWarps * 32, kThreads = (kMmaWarp + 4) * 32;
+  // registers of a thread: at launch, then by role (256 tokens: 128 sums and 64 loaded ones)
+  static constexpr int kLaunchRegs = BT == 256 ? 168 : 248, kSumRegs = BT == 256 ? 216 : 248, kOtherRegs = BT == 256 ? 72 : 248;
+  static_assert(kSumThreads * kSumRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs && kThreads * kLaunchRegs <= 65536,
+                "no more than was launched with");
+  static constexpr int kRows = BT / (kSumWarps / 4), kPairs = kRows / 2;  // tokens of a summing thread, and pairs of them
+  static constexpr int kAtOnce = BT == 64 ? 4 : 1;                       // loads of 16 columns at once
+  static constexpr int kFactorAt = kStages * kBytes, kSmem = kFactorAt + kSlots * BT * 4 + 1024;
+  static constexpr int kTmem = kSums * BT < 64 ? 64 : kSums * BT;
+  static constexpr size_t kPartBytes = (size_t)kOut * BT * 4;
+  static_assert(kSmem <= 227 * 1024 - 1024 && kTmem <= 512, "shared memory, tensor memory");
+};
+
+template <int BT>
+struct Bars {
+  uint64_t full[Geo<BT>::kStages], done[Geo<BT>::kStages], d_empty[Geo<BT>::kSums], join, end;
+};
+
+// The products of one block, 128 k in steps of 32, into a fresh sum.
+__device__ __forceinline__ void mma_block(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n .reg .pred q, no, yes;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n"
+      " setp.ne.b32 no, 0, 0;\n setp.eq.b32 yes, 0, 0;\n"
+      " add.u64 a1, %1, 2;\n add.u64 a2, %1, 4;\n add.u64 a3, %1, 6;\n add.u64 b1, %2, 2;\n add.u64 b2, %2, 4;\n add.u64 b3, %2, 6;\n"
+      " elect.sync _|q, 0xFFFFFFFF;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, no;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, yes;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, yes;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, yes;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc)
+      : "memory");
+}
+
+// Tokens of a tile: they even out over the token tiles.
+struct Tile {
+  int n, row, rows;  // block of outputs; tokens row .. row + rows - 1
+};
+__device__ __forceinline__ Tile find_tile(int tile, int m_tiles, int M) {
+  const int n = tile / m_tiles, m = tile - n * m_tiles;
+  const int share = ((M + m_tiles - 1) / m_tiles + 15) / 16 * 16;
+  return Tile{n, m * share, min(share, M - m * share)};
+}
+
+template <int BT, bool BF16>
+__global__ void __launch_bounds__(Geo<BT>::kThreads, 1)
+fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const Fp8GemmArgs a,
+                int m_tiles, int tiles, int* flags, float* parts, int* err) {
+  using G = Geo<BT>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Bars<BT> bars;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_word, s_ok;
+  volatile int* abort_flag = &abort_word;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid / 32, 0), lane = tid % 32;
+  uint8_t* smem = align_smem_1024(smem_raw);
+  const uint32_t sm = smem_u32(smem);
+  const int blocks = (int)((a.K + 127) / 128), M = (int)a.M;
+
+  if (tid == 0) {
+    abort_word = 0;
+    for (int i = 0; i < G::kStages; ++i) {
+      mbar_init(smem_u32(&bars.full[i]), 2);  // the copies and the factors
+      mbar_init(smem_u32(&bars.done[i]), 1);
+    }
+    for (int i = 0; i < G::kSums; ++i) mbar_init(smem_u32(&bars.d_empty[i]), G::kSumWarps);
+    mbar_init(smem_u32(&bars.join), G::kSumWarps);
+    mbar_init(smem_u32(&bars.end), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == G::kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                 "r"((uint32_t)G::kTmem)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  Walk walk(tiles, blocks);
+  int tile, g0, g1, count = 0;  // count: blocks so far, of this CTA
+  bool ok = true;
+
+  if (warp < G::kSumWarps) {
+    if constexpr (G::kSumRegs > G::kLaunchRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::kSumRegs));
+    // ------------------------------------------------ running sums: output n, tokens kRows wg ..
+    const int wg = warp / 4, n = warp % 4 * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16) + G::kRows * wg;
+    int d = 0, stage = 0, slot = 0;
+    uint32_t phase = 0, join_phase = 0;
+    // all summing warps, or false: a wait that gives up elsewhere must not leave this one waiting
+    auto join = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars.join));
+      const bool all = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.join), join_phase, abort_flag, err, 804));
+      join_phase ^= 1u;
+      return all;
+    };
+    while (ok && walk.next(tile, g0, g1)) {
+      const Tile t = find_tile(tile, m_tiles, M);
+      const int mine = min(max(t.rows - G::kRows * wg, 0), G::kRows);  // of this thread's tokens
+      F2 acc[G::kPairs];
+#pragma unroll
+      for (int i = 0; i < G::kPairs; ++i) acc[i] = F2(0.f, 0.f);
+      for (int g = g0; g < g1 && ok; ++g) {
+        ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.done[stage]), phase, abort_flag, err, 802));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t factors = sm + G::kFactorAt + (slot * BT + G::kRows * wg) * 4;
+#pragma unroll
+        for (int c = 0; c < G::kRows / 16; c += G::kAtOnce) {
+          uint32_t v[G::kAtOnce][16];
+          const bool any = 16 * c < mine;
+          if (any) {
+#pragma unroll
+            for (int h = 0; h < G::kAtOnce; ++h) tmem_ld16_nowait(lanes + d * BT + 16 * (c + h), v[h]);
+#pragma unroll
+            for (int h = 0; h < G::kAtOnce; ++h) wait_loaded(v[h]);
+          }
+          if (c + G::kAtOnce == G::kRows / 16) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars.d_empty[d]));  // the sum is in registers
+          }
+          if (any) {
+#pragma unroll
+            for (int h = 0; h < G::kAtOnce; ++h)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float4 f;
+                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
+                             : "r"(factors + (16 * (c + h) + 4 * i) * 4));
+                F2& s0 = acc[8 * (c + h) + 2 * i];
+                F2& s1 = acc[8 * (c + h) + 2 * i + 1];
+                s0 = fma2(F2(__uint_as_float(v[h][4 * i]), __uint_as_float(v[h][4 * i + 1])), F2(f.x, f.y), s0);
+                s1 = fma2(F2(__uint_as_float(v[h][4 * i + 2]), __uint_as_float(v[h][4 * i + 3])), F2(f.z, f.w), s1);
+              }
+          }
+        }
+        if (++d == G::kSums) d = 0;
+        if (++slot == G::kSlots) slot = 0;
+        if (++stage == G::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      if (g0 > 0) {
+        // another CTA has the tile's first block: this one's sums go to it
+        F2* part = reinterpret_cast<F2*>(parts) + (size_t)walk.me * (G::kPartBytes / 8) + tid;
+#pragma unroll
+        for (int i = 0; i < G::kPairs; ++i)
+          if (2 * i < mine) __stcg(reinterpret_cast<unsigned long long*>(part + i * G::kSumThreads), acc[i].v);
+        __threadfence();
+        ok = join();
+        if (ok && tid == 0) atomicExch(flags + walk.me, 1);
+        continue;
+      }
+      if (g1 < blocks) {
+        // the others' sums, in the order of their blocks; the lanes of one warp wait for all of them at once
+        const int end = (tile - walk.rounds * walk.grid + 1) * blocks;
+        int last = walk.me + 1;
+        while (last < walk.ctas && walk.begin_of(last) < end) ++last;
+        if (warp == 0) {
+          const bool seen = wait_flags(flags, walk.me + 1, last, lane, abort_flag, err, 803);
+          if (lane == 0) s_ok = seen;
+        }
+        ok = join() && s_ok != 0;
+        if (!ok) break;
+        for (int q = walk.me + 1; q < last; ++q) {
+          const F2* part = reinterpret_cast<const F2*>(parts) + (size_t)q * (G::kPartBytes / 8) + tid;
+#pragma unroll
+          for (int i = 0; i < G::kPairs; ++i)
+            if (2 * i < mine) {
+              F2 o;
+              o.v = __ldcg(reinterpret_cast<const unsigned long long*>(part + i * G::kSumThreads));
+              acc[i] = add2(acc[i], o);
+            }
+        }
+        ok = join();
+        if (!ok) break;
+        if (warp == 0)
+          for (int q = walk.me + 1 + lane; q < last; q += 32) atomicExch(flags + q, 0);
+      }
+      // Two neighbouring lanes swap one of a pair of tokens each, so that a lane writes two outputs of one token.
+      const int64_t col = (int64_t)t.n * kOut + (n & ~1);
+      const bool odd = lane & 1;
+      uint16_t* p = a.y + (int64_t)(t.row + G::kRows * wg + odd) * a.N + col;
+      const int rows = col < a.N ? mine - odd : 0;  // N is even
+#pragma unroll
+      for (int i = 0; i < G::kPairs; ++i) {
+        const float2 v = acc[i].get();
+        const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? v.x : v.y, 1);
+        const uint32_t w = odd ? pack2<BF16>(got, v.y) : pack2<BF16>(v.x, got);
+        if (2 * i < rows) *reinterpret_cast<uint32_t*>(p) = w;
+        p += 2 * a.N;
+        asm volatile("" : "+l"(p));  // one address at a time, not all made ahead
+      }
+    }
+  } else {
+    if constexpr (G::kOtherRegs < G::kLaunchRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kOtherRegs));
+    if (warp == G::kMmaWarp) {
+      // ------------------------------------------------ products
+      const uint64_t desc0 = smem_desc_sw128(sm, 16, 1024);
+      int d = 0, stage = 0;
+      uint32_t phase = 0, d_phase = 1;
+      while (ok && walk.next(tile, g0, g1)) {
+        const Tile t = find_tile(tile, m_tiles, M);
+        const uint32_t idesc = (1u << 4) | ((uint32_t)((t.rows + 15) / 16 * 2) << 17) | (8u << 24);  // e4m3 x e4m3, fp32 sums
+        for (int g = g0; g < g1; ++g) {
+          ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.full[stage]), phase, abort_flag, err, 821) &&
+                                           wait_for(smem_u32(&bars.d_empty[d]), d_phase, abort_flag, err, 822));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t at = desc0 + (uint64_t)((stage * G::kBytes) >> 4);
+          mma_block(tmem + d * BT, at, at + (uint64_t)(kABytes >> 4), idesc);
+          commit(smem_u32(&bars.done[stage]));
+          if (++d == G::kSums) {
+            d = 0;
+            d_phase ^= 1u;
+          }
+          if (++stage == G::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      commit(smem_u32(&bars.end));  // arrives once every product has completed
+      volatile int no_abort = 0;
+      wait_for(smem_u32(&bars.end), 0, &no_abort, err, 824);
+    } else if (warp == G::kMmaWarp + 1) {
+      // ------------------------------------------------ copies of weights and codes
+      if (lane == 0) {
+        int stage = 0;
+        uint32_t phase = 1;
+        while (ok && walk.next(tile, g0, g1)) {
+          const Tile t = find_tile(tile, m_tiles, M);
+          const int boxes = (t.rows + G::kBoxRows - 1) / G::kBoxRows;
+          for (int g = g0; g < g1; ++g, ++count) {
+            ok = wait_for(smem_u32(&bars.done[stage]), phase, abort_flag, err, 831);
+            if (!ok) break;
+            const uint32_t bar = smem_u32(&bars.full[stage]), to = sm + stage * G::kBytes;
+            mbar_arrive_tx(bar, (uint32_t)(kABytes + boxes * G::kBoxRows * 128));
+            tma_load_2d(to, &tm_w, g * 128, t.n * kOut, bar);
+            for (int i = 0; i < boxes; ++i)
+              tma_load_2d(to + kABytes + i * G::kBoxRows * 128, &tm_x, g * 128, t.row + i * G::kBoxRows, bar);
+            if (++stage == G::kStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+        }
+        // never leave the CTA with copies in flight
+        volatile int no_abort = 0;
+        for (int j = max(0, count - G::kStages); j < count; ++j)
+          wait_for(smem_u32(&bars.full[j % G::kStages]), (uint32_t)(j / G::kStages) & 1u, &no_abort, err, 832);
+      }
+    } else if (warp == G::kMmaWarp + 2) {
+      // ------------------------------------------------ factors s_x s_w of a block's tokens
+      int stage = 0, slot = 0;
+      uint32_t phase = 1;
+      float* factors = reinterpret_cast<float*>(smem + G::kFactorAt);
+      while (ok && walk.next(tile, g0, g1)) {
+        const Tile t = find_tile(tile, m_tiles, M);
+        const float* s_w = a.s_w + (int64_t)t.n * blocks;
+        for (int g = g0; g < g1; ++g) {
+          float f[(BT + 31) / 32];
+          const float w = __ldg(s_w + g);
+          const float* s_x = a.s_x + (int64_t)g * a.M + t.row;
+#pragma unroll
+          for (int i = 0; i < (BT + 31) / 32; ++i) f[i] = lane + 32 * i < t.rows ? __ldg(s_x + lane + 32 * i) * w : 0.f;
+          ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.done[stage]), phase, abort_flag, err, 841));
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < (BT + 31) / 32; ++i)
+            if (lane + 32 * i < BT) factors[slot * BT + lane + 32 * i] = f[i];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars.full[stage]));  // no product starts without them: `done` cannot run two rounds ahead
+          if (++slot == G::kSlots) slot = 0;
+          if (++stage == G::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == G::kMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)G::kTmem) : "memory");
+  }
+}
+
+int tile_tokens(int64_t M) { return M <= 16 ? 16 : M <= 64 ? 64 : 256; }
+
+template <int BT, bool BF16>
+cudaError_t launch(const Fp8GemmArgs& a, void* ws, int* err, cudaStream_t s) {
+  using G = Geo<BT>;
+  const auto fn = fp8_gemm_kernel<BT, BF16>;
+  const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(fn), G::kSmem);
+  if (e != cudaSuccess) return e;
+  CUtensorMap tw, tx;
+  if (!make_map_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.wq, (uint64_t)a.K, (uint64_t)a.N, 128, kOut,
+                   CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.xq, (uint64_t)a.K, (uint64_t)a.M, 128, G::kBoxRows,
+                   CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  const int m_tiles = (int)((a.M + BT - 1) / BT);
+  const int64_t tiles = (a.N + kOut - 1) / kOut * m_tiles;
+  if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+  int* flags = static_cast<int*>(ws);
+  float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kCounterBytes);
+  fn<<<device_sm_count(), G::kThreads, G::kSmem, s>>>(tw, tx, a, m_tiles, (int)tiles, flags, parts, err);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// flags | parts of shared tiles
+size_t fp8_gemm_workspace(int64_t M, int64_t, int64_t) {
+  return kCounterBytes + (size_t)device_sm_count() * kOut * (size_t)tile_tokens(M) * 4;
+}
+
+cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, bool bf16, void* ws, int* err, cudaStream_t s) {
+  const int bt = tile_tokens(a.M);
+  const auto fn = bt == 16   ? (bf16 ? launch<16, true> : launch<16, false>)
+                  : bt == 64 ? (bf16 ? launch<64, true> : launch<64, false>)
+                             : (bf16 ? launch<256, true> : launch<256, false>);
+  return fn(a, ws, err, s);
+}
+
+}  // namespace awq

@@ -1,6 +1,4 @@
-// Linear layers on e4m3 operands with scales for blocks of 128.
-#include <cuda_fp8.h>
-
+// Activations in e4m3 with a scale for each token and 128 channels.
 #include "awq_internal.h"
 #include "awq_types.cuh"
 
@@ -52,44 +50,6 @@ __global__ void __launch_bounds__(256) fp8_quant_kernel(const uint16_t* __restri
   if (m < M && lane == 0) s_x[(int64_t)g * M + m] = scale;
 }
 
-__device__ __forceinline__ float e4m3_value(uint8_t v) {
-  __nv_fp8_e4m3 f;
-  f.__x = v;
-  return (float)f;
-}
-
-constexpr int kRows = 8;
-
-// A CTA has 128 outputs and 8 tokens, a thread one output.
-template <bool BF16>
-__global__ void __launch_bounds__(128) fp8_gemm_simple(const Fp8GemmArgs a) {
-  __shared__ float xs[kRows][128];
-  const int tid = threadIdx.x;
-  const int64_t n = (int64_t)blockIdx.x * 128 + tid, m0 = (int64_t)blockIdx.y * kRows;
-  const int groups = (int)((a.K + 127) / 128);
-  float acc[kRows] = {};
-  for (int g = 0; g < groups; ++g) {
-    const int count = (int)min((int64_t)128, a.K - g * 128);
-    __syncthreads();
-    for (int r = 0; r < kRows; ++r)
-      xs[r][tid] = m0 + r < a.M && tid < count ? e4m3_value(a.xq[(m0 + r) * a.K + g * 128 + tid]) : 0.f;
-    __syncthreads();
-    if (n >= a.N) continue;
-    float sum[kRows] = {};
-    for (int k = 0; k < count; ++k) {
-      const float w = e4m3_value(a.wq[n * a.K + g * 128 + k]);
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) sum[r] = fmaf(w, xs[r][k], sum[r]);
-    }
-    const float sw = a.s_w[n / 128 * groups + g];
-    for (int r = 0; r < kRows; ++r)
-      if (m0 + r < a.M) acc[r] = fmaf(sum[r], a.s_x[(int64_t)g * a.M + m0 + r] * sw, acc[r]);
-  }
-  if (n >= a.N) return;
-  for (int r = 0; r < kRows; ++r)
-    if (m0 + r < a.M) a.y[(m0 + r) * a.N + n] = (uint16_t)pack2<BF16>(acc[r], 0.f);
-}
-
 }  // namespace
 
 cudaError_t launch_fp8_quant(const uint16_t* x, int64_t x_stride, uint8_t* xq, float* s_x, int64_t M, int64_t K, bool bf16,
@@ -98,14 +58,6 @@ cudaError_t launch_fp8_quant(const uint16_t* x, int64_t x_stride, uint8_t* xq, f
   const int64_t blocks = (M * groups * 16 + 255) / 256;
   (bf16 ? fp8_quant_kernel<true> : fp8_quant_kernel<false>)<<<(unsigned)blocks, 256, 0, s>>>(x, x_stride, xq, s_x, M, (int)K,
                                                                                             groups);
-  return cudaGetLastError();
-}
-
-size_t fp8_gemm_workspace(int64_t, int64_t, int64_t) { return 0; }
-
-cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, bool bf16, void*, int*, cudaStream_t s) {
-  const dim3 grid((unsigned)((a.N + 127) / 128), (unsigned)((a.M + kRows - 1) / kRows));
-  (bf16 ? fp8_gemm_simple<true> : fp8_gemm_simple<false>)<<<grid, 128, 0, s>>>(a);
   return cudaGetLastError();
 }
 

@@ -1,0 +1,94 @@
+// What the tensor-memory products of the layer with experts and of the fp8 layers share: waits, a CTA's share of the work and
+// the flags of sums that cross CTAs.
+#pragma once
+
+#include "awq_internal.h"
+#include "awq_ptx.cuh"
+
+namespace awq {
+namespace {
+
+// Waits for this thread's tensor memory loads; `r` is not used before.
+__device__ __forceinline__ void wait_loaded(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
+// The first look comes before the clock is read for the limit.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort, int* err, int id) {
+  return mbar_try(bar, parity) || wait_bounded_inline(bar, parity, abort, err, id);
+}
+
+// Arrives on `bar` once the products issued before have completed; executed by the whole warp, issued by the lane that
+// elect.sync chooses (always the same, which issued the products).
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xFFFFFFFF;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
+      : "memory");
+}
+constexpr int kMinUnits = 4;  // groups that a CTA gets at least of what is cut along K
+
+// What a CTA works on, in order: parts of tiles, groups g0 .. g1 - 1 of each.
+struct Walk {
+  int grid, me, groups, rounds, tiles;  // whole rounds of tiles; the tiles that are left
+  int round, u, u1;
+  long long units;
+  int ctas;
+  __device__ __forceinline__ Walk(int total, int groups_) : grid(gridDim.x), me(blockIdx.x), groups(groups_) {
+    rounds = total % grid == 0 ? total / grid : max(0, total / grid - 1);
+    tiles = total - rounds * grid;
+    units = (long long)tiles * groups;
+    ctas = (int)max(1ll, min((long long)grid, units / kMinUnits));
+    round = 0;
+    u = me < ctas ? begin_of(me) : 0;
+    u1 = me < ctas ? begin_of(me + 1) : 0;
+  }
+  __device__ __forceinline__ int begin_of(int cta) const { return (int)(units * cta / ctas); }
+  __device__ __forceinline__ bool next(int& tile, int& g0, int& g1) {
+    if (round < rounds) {
+      tile = me + grid * round++;
+      g0 = 0;
+      g1 = groups;
+      return true;
+    }
+    if (u >= u1) return false;
+    const int t = u / groups;
+    g0 = u - t * groups;
+    g1 = min(groups, g0 + u1 - u);
+    tile = rounds * grid + t;
+    u += g1 - g0;
+    return true;
+  }
+};
+
+// The calling warp's lanes wait for flags [from, to), all at once.
+__device__ __forceinline__ bool wait_flags(const int* flags, int from, int to, int lane, volatile int* abort, int* err, int id) {
+  bool seen = true;
+  for (int q = from + lane; q < to && seen; q += 32) {
+    const long long t0 = now_ns();
+    for (uint32_t spin = 1;; ++spin) {
+      int v;
+      asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(flags + q) : "memory");
+      if (v) break;
+      if ((spin & 255u) == 0) {
+        if (*abort) seen = false;
+        else if (now_ns() - t0 > kWaitLimitNs) {
+          if (err) atomicExch(err, id);
+          *abort = 1;
+          seen = false;
+        }
+        if (!seen) break;
+      }
+    }
+  }
+  seen = __all_sync(0xFFFFFFFFu, seen);
+  __threadfence();
+  return seen;
+}
+
+}  // namespace
+}  // namespace awq

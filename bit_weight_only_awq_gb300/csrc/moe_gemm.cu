@@ -30,6 +30,7 @@
 #include "awq_internal.h"
 #include "awq_ptx.cuh"
 #include "awq_types.cuh"
+#include "layer_common.cuh"
 
 namespace awq {
 namespace {
@@ -107,29 +108,9 @@ __device__ __forceinline__ void mma_group(uint32_t d, uint32_t a, uint64_t b0, u
       "r"(a), "l"(b0), "l"(b1), "r"(idesc)
       : "memory");
 }
-__device__ __forceinline__ void commit(uint32_t bar) {
-  asm volatile(
-      "{\n .reg .pred q;\n elect.sync _|q, 0xFFFFFFFF;\n"
-      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
-      : "memory");
-}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-// Waits for this thread's tensor memory loads; `r` is not used before.
-__device__ __forceinline__ void wait_loaded(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :
-               : "memory");
-}
-
-// The first look comes before the clock is read for the limit.
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort, int* err, int id) {
-  return mbar_try(bar, parity) || wait_bounded_inline(bar, parity, abort, err, id);
-}
-
 // Operands (q - z) 2^-kDown, exact, of a word of eight codes: k pairs 0..3.  A masked nibble is a subnormal 16-bit number, q or
 // 16 q of the smallest (in bf16 16 q reaches the lowest bit of the exponent, where numbers are still as far apart); one
 // multiplication and addition gives it its size and takes the zero point off.  One AND and one fma for two codes: 315
@@ -153,41 +134,6 @@ __device__ __forceinline__ void operands(uint32_t w, uint32_t z, uint32_t* o, in
   o[at + 2] = fma16<BF16>(v & 0x000F000Fu, kOne, z);
   o[at + 3] = fma16<BF16>(v & 0x00F000F0u, kSixteenth, z);
 }
-
-constexpr int kMinUnits = 4;  // groups that a CTA gets at least of what is cut along K
-
-// What a CTA works on, in order: parts of tiles, groups g0 .. g1 - 1 of each.
-struct Walk {
-  int grid, me, groups, rounds, tiles;  // whole rounds of tiles; the tiles that are left
-  int round, u, u1;
-  long long units;
-  int ctas;
-  __device__ __forceinline__ Walk(int total, int groups_) : grid(gridDim.x), me(blockIdx.x), groups(groups_) {
-    rounds = total % grid == 0 ? total / grid : max(0, total / grid - 1);
-    tiles = total - rounds * grid;
-    units = (long long)tiles * groups;
-    ctas = (int)max(1ll, min((long long)grid, units / kMinUnits));
-    round = 0;
-    u = me < ctas ? begin_of(me) : 0;
-    u1 = me < ctas ? begin_of(me + 1) : 0;
-  }
-  __device__ __forceinline__ int begin_of(int cta) const { return (int)(units * cta / ctas); }
-  __device__ __forceinline__ bool next(int& tile, int& g0, int& g1) {
-    if (round < rounds) {
-      tile = me + grid * round++;
-      g0 = 0;
-      g1 = groups;
-      return true;
-    }
-    if (u >= u1) return false;
-    const int t = u / groups;
-    g0 = u - t * groups;
-    g1 = min(groups, g0 + u1 - u);
-    tile = rounds * grid + t;
-    u += g1 - g0;
-    return true;
-  }
-};
 
 struct Tile {
   int expert, pair, row, rows;  // rows of y: row .. row + rows - 1
@@ -242,31 +188,6 @@ __device__ __forceinline__ void expert_tables(const MoeGemmArgs& a, int lane, in
 __device__ __forceinline__ int source_row(const MoeGemmArgs& a, int row) {
   const int src = a.order ? a.order[row] / a.top_k : row;
   return src >= 0 && src < a.x_rows ? src : 0;
-}
-
-// The calling warp's lanes wait for flags [from, to), all at once.
-__device__ __forceinline__ bool wait_flags(const int* flags, int from, int to, int lane, volatile int* abort, int* err, int id) {
-  bool seen = true;
-  for (int q = from + lane; q < to && seen; q += 32) {
-    const long long t0 = now_ns();
-    for (uint32_t spin = 1;; ++spin) {
-      int v;
-      asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(flags + q) : "memory");
-      if (v) break;
-      if ((spin & 255u) == 0) {
-        if (*abort) seen = false;
-        else if (now_ns() - t0 > kWaitLimitNs) {
-          if (err) atomicExch(err, id);
-          *abort = 1;
-          seen = false;
-        }
-        if (!seen) break;
-      }
-    }
-  }
-  seen = __all_sync(0xFFFFFFFFu, seen);
-  __threadfence();
-  return seen;
 }
 
 __device__ __forceinline__ float silu_times(float gate, float up) { return __fdividef(gate, 1.f + expf(-gate)) * up; }

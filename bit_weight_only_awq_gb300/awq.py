@@ -723,13 +723,6 @@ class MoePlan:
         return self.offsets.shape[0] - 1
 
 
-def _new_plan(rows: int, experts: int, top_k: int, device) -> MoePlan:
-    # one allocation, each part 16-byte aligned
-    first, wide = (experts + 4) // 4 * 4, (rows + 3) // 4 * 4
-    buf = torch.empty(first + 2 * wide, dtype=torch.int32, device=device)
-    return MoePlan(buf[: experts + 1], buf[first : first + rows], buf[first + wide : first + wide + rows], top_k)
-
-
 def awq_moe_plan(ids: torch.Tensor, experts: int, stream=None) -> MoePlan:
     """The plan of a router of one's own: ids int32 [T, top_k], each in [0, experts) or a choice without a row."""
     if ids.dim() != 2:
@@ -737,11 +730,15 @@ def awq_moe_plan(ids: torch.Tensor, experts: int, stream=None) -> MoePlan:
     _need("awq_moe_plan", torch.int32, ids)
     _on_current_gpu("awq_moe_plan", ids)
     T, top_k = ids.shape
-    plan = _new_plan(T * top_k, experts, top_k, ids.device)
-    _check("awq_moe_plan", lib.awq_moe_plan(ids.data_ptr(), T * top_k, experts, plan.offsets.data_ptr(),
-                                            plan.order.data_ptr(), plan.place.data_ptr(),
-                                            _raw_stream(stream, ids.device)))
-    return plan
+    rows, device = T * top_k, ids.device
+    if experts < 1:
+        raise AwqError("awq_moe_plan", -1)
+    buf = torch.empty(experts + 1 + 2 * rows, dtype=torch.int32, device=device)  # one allocation for the plan
+    at = buf.data_ptr()
+    order = at + 4 * (experts + 1)
+    _check("awq_moe_plan", lib.awq_moe_plan(ids.data_ptr(), rows, experts, at, order, order + 4 * rows,
+                                            _raw_stream(stream, device)))
+    return MoePlan(*buf.split_with_sizes((experts + 1, rows, rows)), top_k)
 
 
 _LOGITS = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
@@ -758,14 +755,17 @@ def awq_moe_route(logits: torch.Tensor, top_k: int, normalize: bool = True, stre
     device = logits.device
     if not 1 <= top_k <= experts:
         raise AwqError("awq_moe_route", -1)
-    weights = torch.empty((T, top_k), dtype=torch.float32, device=device)
-    ids = torch.empty((T, top_k), dtype=torch.int32, device=device)
-    plan = _new_plan(T * top_k, experts, top_k, device)
+    rows = T * top_k
+    buf = torch.empty(experts + 1 + 4 * rows, dtype=torch.int32, device=device)  # one allocation for all that it returns
+    ids = buf.data_ptr()
+    weights = ids + 4 * rows
+    offsets = weights + 4 * rows
+    order = offsets + 4 * (experts + 1)
     _check("awq_moe_route", lib.awq_moe_route(
-        logits.data_ptr(), _row_stride("awq_moe_route", logits, experts), T, experts, top_k, int(normalize), kind,
-        ids.data_ptr(), weights.data_ptr(), plan.offsets.data_ptr(), plan.order.data_ptr(), plan.place.data_ptr(),
-        _raw_stream(stream, device)))
-    return weights, ids, plan
+        logits.data_ptr(), _row_stride("awq_moe_route", logits, experts), T, experts, top_k, int(normalize), kind, ids,
+        weights, offsets, order, order + 4 * rows, _raw_stream(stream, device)))
+    ids, weights, offsets, order, place = buf.split_with_sizes((rows, rows, experts + 1, rows, rows))
+    return weights.view(torch.float32).view(T, top_k), ids.view(T, top_k), MoePlan(offsets, order, place, top_k)
 
 
 class MoeWeights:
@@ -881,13 +881,47 @@ def awq_moe_combine(y, plan: MoePlan, weights, residual=None, dtype=None, out=No
 
 def awq_moe(x, up: MoeWeights, down: MoeWeights, weights, plan: MoePlan, residual=None, out=None, workspace=None, stream=None):
     """A sparse feed-forward layer: x [T, K] through every token's experts, down(silu(gate) * up), weighted and added up
-    (to `residual` where one is given).  `up` is gated, `down` plain; weights and plan from awq_moe_route.  A captured
-    call takes a workspace of the larger of the two products' sizes."""
+    (to `residual` where one is given): awq_moe_gemm, awq_moe_gemm and awq_moe_combine.  `up` is gated, `down` plain;
+    weights and plan from awq_moe_route.  Between the products the activations have x's type, between down and the sum they
+    are fp32.  A captured call takes a workspace of the larger of the two products' sizes."""
+    name = "awq_moe"
     if not up.gated or down.gated or down.K != up.outputs:
         raise ValueError("awq_moe: up is gated, down is plain, and down takes up's outputs")
-    h = awq_moe_gemm(x, up, plan, gather=True, workspace=workspace, stream=stream)
-    y = awq_moe_gemm(h, down, plan, out_dtype=torch.float32, workspace=workspace, stream=stream)
-    return awq_moe_combine(y, plan, weights, residual=residual, dtype=x.dtype, out=out, stream=stream)
+    dtype = _dtype16(name, x, residual, out)
+    device, rows, experts, top_k = x.device, plan.rows, plan.experts, plan.top_k
+    if x.dtype is not up.dtype or x.dtype is not down.dtype:
+        raise TypeError("awq_moe: x and the weights' scales have one type")
+    T, H = x.shape[0], down.N
+    _need(name, torch.float32, weights)
+    _need(name, x.dtype, out)
+    if x.shape != (T, up.K) or weights.shape != (T, top_k) or T * top_k != rows or up.experts != experts or \
+            down.experts != experts or (residual is not None and residual.shape != (T, H)) or \
+            (out is not None and out.shape != (T, H)):
+        raise ValueError("awq_moe: x [T, K], weights [T, top_k], residual and out [T, H] go with the layers and the plan")
+    _on_current_gpu(name, x, up.data, down.data, weights, plan.offsets, plan.order, plan.place, residual, out, workspace)
+    handle = _raw_stream(stream, device)
+    if workspace is None:
+        query = "awq_moe_gemm_workspace_bytes"
+        need = max(_layer_workspace_need(device.index, query, rows, experts, up.K, up.N, 1),
+                   _layer_workspace_need(device.index, query, rows, experts, down.K, down.N, 0))
+        workspace = _layer_workspace(name, handle, device, need, stream)
+    ws, nbytes, offsets = workspace.data_ptr(), workspace.numel() * workspace.element_size(), plan.offsets.data_ptr()
+    h = torch.empty((rows, down.K), dtype=x.dtype, device=device)
+    y = torch.empty((rows, H), dtype=torch.float32, device=device)
+    if out is None:
+        out = torch.empty((T, H), dtype=x.dtype, device=device)
+    if stream is not None:
+        for t in (h, y, out):  # made on the current stream, used on another
+            t.record_stream(stream)
+    _check(name, lib.awq_moe_gemm(x.data_ptr(), _row_stride(name, x, up.K), T, up.data.data_ptr(), offsets,
+                                  plan.order.data_ptr(), top_k, h.data_ptr(), 0, rows, experts, up.K, up.N, 1, dtype, ws,
+                                  nbytes, handle))
+    _check(name, lib.awq_moe_gemm(h.data_ptr(), down.K, rows, down.data.data_ptr(), offsets, None, 1, y.data_ptr(), 1, rows,
+                                  experts, down.K, H, 0, dtype, ws, nbytes, handle))
+    _check(name, lib.awq_moe_combine(y.data_ptr(), 1, plan.place.data_ptr(), weights.data_ptr(), _ptr(residual),
+                                     0 if residual is None else _row_stride(name, residual, H), out.data_ptr(), T, top_k, H,
+                                     rows, dtype, handle))
+    return out
 
 
 FP8_BLOCK = 128

@@ -105,4 +105,21 @@ inline cudaError_t set_smem_once(const void* func, int bytes) {
   return cudaSuccess;
 }
 
+// Launches with programmatic dependent launch: the kernel may become resident while the one before it in the stream still
+// runs, and waits for it (griddepcontrol.wait) before it touches what that one may have written.
+template <typename... P, typename... A>
+inline cudaError_t launch_dependent(void (*fn)(P...), dim3 grid, int threads, int smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, P(args)...);
+}
+
 }  // namespace awq

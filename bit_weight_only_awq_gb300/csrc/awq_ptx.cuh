@@ -122,6 +122,13 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
+// Waits for the kernel before this one in the stream, then lets the next one become resident: in this order what the next
+// one reads before its own wait is as old as the kernels before this one.
+__device__ __forceinline__ void wait_then_release_dependents() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---- tcgen05 (5th-generation tensor cores, tensor memory)
 
 // Shared-memory matrix descriptor, 128-byte swizzle: start, leading / stride byte offsets.

@@ -230,6 +230,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  wait_then_release_dependents();
   if (warp == 0) expert_tables<BT>(a, lane, first, items);
   tc_fence_before();
   __syncthreads();
@@ -582,6 +583,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
 
 // Rows of x in the plan's order, 16 bytes a thread.
 __global__ void __launch_bounds__(256) moe_order_kernel(const MoeGemmArgs a, uint16_t* out) {
+  wait_then_release_dependents();
   const int vec = (int)(a.K / 8), rows = min(max(a.offsets[a.experts], 0), (int)a.R);
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)rows * vec; i += (int64_t)gridDim.x * 256) {
     const int64_t r = i / vec;
@@ -610,8 +612,7 @@ cudaError_t launch(MoeGemmArgs a, bool gated, bool wide, void* ws, int* err, cud
   if (G::kBoxes) {
     if (a.order) {
       uint16_t* rows = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(parts) + parts_bytes(BT));
-      moe_order_kernel<<<device_sm_count() * 8, 256, 0, s>>>(a, rows);
-      e = cudaGetLastError();
+      e = launch_dependent(moe_order_kernel, dim3(device_sm_count() * 8), 256, 0, s, a, rows);
       if (e != cudaSuccess) return e;
       a.x = rows;
       a.x_rows = a.R;
@@ -622,8 +623,7 @@ cudaError_t launch(MoeGemmArgs a, bool gated, bool wide, void* ws, int* err, cud
                      (uint64_t)a.x_rows, 64, kBoxRows, CU_TENSOR_MAP_SWIZZLE_128B, (uint64_t)a.x_stride))
       return cudaErrorInvalidValue;
   }
-  fn<<<device_sm_count(), G::kThreads, G::kSmem, s>>>(tm, a, flags, parts, err);
-  return cudaGetLastError();
+  return launch_dependent(fn, dim3(device_sm_count()), G::kThreads, G::kSmem, s, tm, a, flags, parts, err);
 }
 
 }  // namespace

@@ -6,7 +6,9 @@
 // one ballot for the lowest expert among equals.
 #include <type_traits>
 
+#include "awq_host.h"
 #include "awq_internal.h"
+#include "awq_ptx.cuh"
 #include "awq_types.cuh"
 
 namespace awq {
@@ -122,6 +124,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ 
                                                     int32_t* __restrict__ place) {
   __shared__ int s_below[32], s_equal[32];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, e = blockIdx.x;
+  wait_then_release_dependents();
   const int share = (int)(((int64_t)R + 1023) / 1024 * 32);
   const int begin = (int)min((int64_t)R, (int64_t)warp * share), end = (int)min((int64_t)R, (int64_t)(warp + 1) * share);
   int below, equal;
@@ -147,6 +150,7 @@ __global__ void __launch_bounds__(256) route_kernel(const void* __restrict__ log
                                                     float* __restrict__ weights) {
   const int lane = threadIdx.x % 32;
   const int64_t t = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+  wait_then_release_dependents();
   if (t >= T) return;
   int id;
   float weight;
@@ -157,6 +161,54 @@ __global__ void __launch_bounds__(256) route_kernel(const void* __restrict__ log
   }
 }
 
+// Few tokens: one CTA routes them and makes the plan from ids in shared memory.  3 tokens over 8 experts: one launch instead of
+// two, which is most of such a call.
+constexpr int kFewRows = 2048, kFewTokens = 256;
+template <int TYPE, int L>
+__global__ void __launch_bounds__(1024) route_few_kernel(const void* __restrict__ logits, int64_t stride, int T, int experts,
+                                                         int top_k, int normalize, int32_t* __restrict__ ids,
+                                                         float* __restrict__ weights, int32_t* __restrict__ offsets,
+                                                         int32_t* __restrict__ order, int32_t* __restrict__ place) {
+  __shared__ int32_t s_ids[kFewRows];
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, R = T * top_k;
+  wait_then_release_dependents();
+  for (int t = warp; t < T; t += 32) {
+    int id;
+    float weight;
+    route_token<TYPE, L>(logits, t * stride, experts, top_k, normalize != 0, lane, id, weight);
+    if (lane < top_k) {
+      ids[t * top_k + lane] = id;
+      weights[t * top_k + lane] = weight;
+      s_ids[t * top_k + lane] = id;
+    }
+  }
+  __syncthreads();
+  if (R <= 256) {
+    // a row's place is the number of rows that come before it, an expert's offset the number of rows of lower ones
+    if (tid < R) {
+      const int id = s_ids[tid];
+      int before = 0;
+      for (int q = 0; q < R; ++q) {
+        const int other = s_ids[q];
+        before += other < id || (other == id && q < tid);
+      }
+      order[before] = tid;
+      place[tid] = before;
+    } else if (tid >= 256 && tid - 256 <= experts) {
+      int below = 0;
+      for (int q = 0; q < R; ++q) below += s_ids[q] < tid - 256;
+      offsets[tid - 256] = below;
+    }
+    return;
+  }
+  for (int e = warp; e <= experts; e += 32) {
+    int below, equal;
+    count_class(s_ids, 0, R, e, experts, lane, below, equal);
+    if (lane == 0) offsets[e] = below;
+    place_class(s_ids, 0, R, e, experts, lane, below, order, place);
+  }
+}
+
 // WIDE: y in fp32.
 template <bool BF16, bool WIDE>
 __global__ void __launch_bounds__(256) combine_kernel(const void* __restrict__ y, const int32_t* __restrict__ place,
@@ -164,6 +216,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const void* __restrict__ y
                                                       int64_t res_stride, uint16_t* out, int64_t T, int top_k, int64_t H,
                                                       int64_t R) {
   const int64_t vec = H / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  wait_then_release_dependents();
   if (i >= T * vec) return;
   const int64_t t = i / vec, c = (i - t * vec) * 8;
   float sum[8];
@@ -211,30 +264,33 @@ __global__ void __launch_bounds__(256) combine_kernel(const void* __restrict__ y
 
 cudaError_t launch_moe_plan(const int32_t* ids, int64_t R, int experts, int32_t* offsets, int32_t* order, int32_t* place,
                             cudaStream_t s) {
-  plan_kernel<<<experts + 1, 1024, 0, s>>>(ids, (int)R, experts, offsets, order, place);
-  return cudaGetLastError();
+  return launch_dependent(plan_kernel, dim3(experts + 1), 1024, 0, s, ids, (int)R, experts, offsets, order, place);
 }
 
 cudaError_t launch_moe_route(const void* logits, int64_t stride, int64_t T, int experts, int top_k, bool normalize, int type,
                              int32_t* ids, float* weights, int32_t* offsets, int32_t* order, int32_t* place,
                              cudaStream_t s) {
+  const bool few = offsets && T <= kFewTokens && T * top_k <= kFewRows;
+  auto by_size = [&](auto kType, auto kL) {
+    constexpr int TYPE = decltype(kType)::value, L = decltype(kL)::value;
+    if (few)
+      return launch_dependent(route_few_kernel<TYPE, L>, dim3(1), 1024, 0, s, logits, stride, (int)T, experts, top_k,
+                              (int)normalize, ids, weights, offsets, order, place);
+    return launch_dependent(route_kernel<TYPE, L>, dim3((unsigned)((T + 7) / 8)), 256, 0, s, logits, stride, (int)T, experts,
+                            top_k, (int)normalize, ids, weights);
+  };
+  auto by_type = [&](auto t) {
+    return experts <= 32    ? by_size(t, std::integral_constant<int, 1>{})
+           : experts <= 64  ? by_size(t, std::integral_constant<int, 2>{})
+           : experts <= 128 ? by_size(t, std::integral_constant<int, 4>{})
+           : experts <= 256 ? by_size(t, std::integral_constant<int, 8>{})
+                            : by_size(t, std::integral_constant<int, 16>{});
+  };
   if (T > 0) {
-    auto launch = [&](auto kernel) {
-      kernel<<<(unsigned)((T + 7) / 8), 256, 0, s>>>(logits, stride, (int)T, experts, top_k, normalize, ids, weights);
-      return cudaGetLastError();
-    };
-    auto by_size = [&](auto t) {
-      constexpr int kType = decltype(t)::value;
-      return experts <= 32    ? launch(route_kernel<kType, 1>)
-             : experts <= 64  ? launch(route_kernel<kType, 2>)
-             : experts <= 128 ? launch(route_kernel<kType, 4>)
-             : experts <= 256 ? launch(route_kernel<kType, 8>)
-                              : launch(route_kernel<kType, 16>);
-    };
-    const cudaError_t e = type == 0   ? by_size(std::integral_constant<int, 0>{})
-                          : type == 1 ? by_size(std::integral_constant<int, 1>{})
-                                      : by_size(std::integral_constant<int, 2>{});
-    if (e != cudaSuccess) return e;
+    const cudaError_t e = type == 0   ? by_type(std::integral_constant<int, 0>{})
+                          : type == 1 ? by_type(std::integral_constant<int, 1>{})
+                                      : by_type(std::integral_constant<int, 2>{});
+    if (e != cudaSuccess || few) return e;
   }
   return offsets ? launch_moe_plan(ids, T * top_k, experts, offsets, order, place, s) : cudaSuccess;
 }
@@ -245,8 +301,8 @@ cudaError_t launch_moe_combine(const void* y, bool wide, const int32_t* place, c
   const int64_t threads = T * (H / 8);
   const auto fn = bf16 ? (wide ? combine_kernel<true, true> : combine_kernel<true, false>)
                        : (wide ? combine_kernel<false, true> : combine_kernel<false, false>);
-  fn<<<(unsigned)((threads + 255) / 256), 256, 0, s>>>(y, place, weights, residual, res_stride, out, T, top_k, H, R);
-  return cudaGetLastError();
+  return launch_dependent(fn, dim3((unsigned)((threads + 255) / 256)), 256, 0, s, y, place, weights, residual, res_stride, out,
+                          T, top_k, H, R);
 }
 
 }  // namespace awq

@@ -756,16 +756,15 @@ def awq_moe_route(logits: torch.Tensor, top_k: int, normalize: bool = True, stre
     if not 1 <= top_k <= experts:
         raise AwqError("awq_moe_route", -1)
     rows = T * top_k
-    buf = torch.empty(experts + 1 + 4 * rows, dtype=torch.int32, device=device)  # one allocation for all that it returns
-    ids = buf.data_ptr()
-    weights = ids + 4 * rows
-    offsets = weights + 4 * rows
-    order = offsets + 4 * (experts + 1)
+    weights = torch.empty((T, top_k), dtype=torch.float32, device=device)
+    buf = torch.empty(experts + 1 + 3 * rows, dtype=torch.int32, device=device)  # one allocation for the whole numbers
+    offsets = buf.data_ptr()
+    ids = offsets + 4 * (experts + 1)
     _check("awq_moe_route", lib.awq_moe_route(
         logits.data_ptr(), _row_stride("awq_moe_route", logits, experts), T, experts, top_k, int(normalize), kind, ids,
-        weights, offsets, order, order + 4 * rows, _raw_stream(stream, device)))
-    ids, weights, offsets, order, place = buf.split_with_sizes((rows, rows, experts + 1, rows, rows))
-    return weights.view(torch.float32).view(T, top_k), ids.view(T, top_k), MoePlan(offsets, order, place, top_k)
+        weights.data_ptr(), offsets, ids + 4 * rows, ids + 8 * rows, _raw_stream(stream, device)))
+    offsets, ids, order, place = buf.split_with_sizes((experts + 1, rows, rows, rows))
+    return weights, ids.view(T, top_k), MoePlan(offsets, order, place, top_k)
 
 
 class MoeWeights:

@@ -6,9 +6,10 @@
 // of BT numbers in shared memory, the same for all lanes.
 //
 // A CTA works on tiles of 128 outputs x up to BT tokens: D[output][token] = A B with A = weights and B = codes, both K-major in
-// shared memory, tcgen05.mma kind::f8f6f4.  Roles: the first warps add up and write results (a thread has an output and BT or BT / 2
-// tokens), then come a warp that issues the products, one that copies both operands (one 128-byte row of each a block) and one that
-// makes the factors.  The persistent grid and sums that cross CTAs are those of the grouped product.
+// shared memory, tcgen05.mma kind::f8f6f4.  Roles: the first warps add up and write results (a thread has an output and some of the
+// tokens), then come a warp that issues the products, one that copies the operands (128 bytes of a row a block) and two that make
+// the factors, or with up to 16 tokens given in 16 bits the codes too: a layer of few tokens is one launch.  The persistent
+// grid and sums that cross CTAs are those of the grouped product.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -16,7 +17,7 @@
 #include "awq_host.h"
 #include "awq_internal.h"
 #include "awq_ptx.cuh"
-#include "awq_types.cuh"
+#include "fp8_common.cuh"
 #include "layer_common.cuh"
 
 namespace awq {
@@ -33,14 +34,14 @@ struct Geo {
   // further back to be taken out.
   static constexpr int kSlots = kStages + kSums;
   static constexpr int kBoxRows = BT < 64 ? BT : 64;
-  static constexpr int kSumWarps = BT == 256 ? 8 : 4, kMmaWarp = kSumWarps;
+  static constexpr int kSumWarps = BT == 16 ? 4 : 16, kMmaWarp = kSumWarps;
   static constexpr int kSumThreads = kSumWarps * 32, kThreads = (kMmaWarp + 4) * 32;
-  // registers of a thread: at launch, then by role (256 tokens: 128 sums and 64 loaded ones)
-  static constexpr int kLaunchRegs = BT == 256 ? 168 : 248, kSumRegs = BT == 256 ? 216 : 248, kOtherRegs = BT == 256 ? 72 : 248;
+  // registers of a thread: at launch, then by role (256 tokens: 64 sums)
+  static constexpr int kLaunchRegs = BT == 16 ? 248 : 96, kSumRegs = BT == 16 ? 248 : BT == 64 ? 96 : 104,
+                       kOtherRegs = BT == 16 ? 248 : BT == 64 ? 96 : 64;
   static_assert(kSumThreads * kSumRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs && kThreads * kLaunchRegs <= 65536,
                 "no more than was launched with");
   static constexpr int kRows = BT / (kSumWarps / 4), kPairs = kRows / 2;  // tokens of a summing thread, and pairs of them
-  static constexpr int kAtOnce = BT == 64 ? 4 : 1;                       // loads of 16 columns at once
   static constexpr int kFactorAt = kStages * kBytes, kSmem = kFactorAt + kSlots * BT * 4 + 1024;
   static constexpr int kTmem = kSums * BT < 64 ? 64 : kSums * BT;
   static constexpr size_t kPartBytes = (size_t)kOut * BT * 4;
@@ -77,7 +78,8 @@ __device__ __forceinline__ Tile find_tile(int tile, int m_tiles, int M) {
   return Tile{n, m * share, min(share, M - m * share)};
 }
 
-template <int BT, bool BF16>
+// QUANT: the activations are 16-bit, quantized here.
+template <int BT, bool BF16, bool QUANT>
 __global__ void __launch_bounds__(Geo<BT>::kThreads, 1)
 fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const Fp8GemmArgs a,
                 int m_tiles, int tiles, int* flags, float* parts, int* err) {
@@ -95,7 +97,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
   if (tid == 0) {
     abort_word = 0;
     for (int i = 0; i < G::kStages; ++i) {
-      mbar_init(smem_u32(&bars.full[i]), 2);  // the copies and the factors
+      mbar_init(smem_u32(&bars.full[i]), QUANT ? 3 : 2);  // the copies and the factors
       mbar_init(smem_u32(&bars.done[i]), 1);
     }
     for (int i = 0; i < G::kSums; ++i) mbar_init(smem_u32(&bars.d_empty[i]), G::kSumWarps);
@@ -110,6 +112,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  wait_then_release_dependents();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -145,33 +148,29 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
         tc_fence_after();
         const uint32_t factors = sm + G::kFactorAt + (slot * BT + G::kRows * wg) * 4;
 #pragma unroll
-        for (int c = 0; c < G::kRows / 16; c += G::kAtOnce) {
-          uint32_t v[G::kAtOnce][16];
+        for (int c = 0; c < G::kRows / 16; ++c) {
+          uint32_t v[16];
           const bool any = 16 * c < mine;
           if (any) {
-#pragma unroll
-            for (int h = 0; h < G::kAtOnce; ++h) tmem_ld16_nowait(lanes + d * BT + 16 * (c + h), v[h]);
-#pragma unroll
-            for (int h = 0; h < G::kAtOnce; ++h) wait_loaded(v[h]);
+            tmem_ld16_nowait(lanes + d * BT + 16 * c, v);
+            wait_loaded(v);
           }
-          if (c + G::kAtOnce == G::kRows / 16) {
+          if (c + 1 == G::kRows / 16) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bars.d_empty[d]));  // the sum is in registers
           }
           if (any) {
 #pragma unroll
-            for (int h = 0; h < G::kAtOnce; ++h)
-#pragma unroll
               for (int i = 0; i < 4; ++i) {
                 float4 f;
                 asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                              : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
-                             : "r"(factors + (16 * (c + h) + 4 * i) * 4));
-                F2& s0 = acc[8 * (c + h) + 2 * i];
-                F2& s1 = acc[8 * (c + h) + 2 * i + 1];
-                s0 = fma2(F2(__uint_as_float(v[h][4 * i]), __uint_as_float(v[h][4 * i + 1])), F2(f.x, f.y), s0);
-                s1 = fma2(F2(__uint_as_float(v[h][4 * i + 2]), __uint_as_float(v[h][4 * i + 3])), F2(f.z, f.w), s1);
+                             : "r"(factors + (16 * c + 4 * i) * 4));
+                F2& s0 = acc[8 * c + 2 * i];
+                F2& s1 = acc[8 * c + 2 * i + 1];
+                s0 = fma2(F2(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])), F2(f.x, f.y), s0);
+                s1 = fma2(F2(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])), F2(f.z, f.w), s1);
               }
           }
         }
@@ -278,9 +277,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
             ok = wait_for(smem_u32(&bars.done[stage]), phase, abort_flag, err, 831);
             if (!ok) break;
             const uint32_t bar = smem_u32(&bars.full[stage]), to = sm + stage * G::kBytes;
-            mbar_arrive_tx(bar, (uint32_t)(kABytes + boxes * G::kBoxRows * 128));
+            mbar_arrive_tx(bar, (uint32_t)(kABytes + (QUANT ? 0 : boxes * G::kBoxRows * 128)));
             tma_load_2d(to, &tm_w, g * 128, t.n * kOut, bar);
-            for (int i = 0; i < boxes; ++i)
+            for (int i = 0; !QUANT && i < boxes; ++i)
               tma_load_2d(to + kABytes + i * G::kBoxRows * 128, &tm_x, g * 128, t.row + i * G::kBoxRows, bar);
             if (++stage == G::kStages) {
               stage = 0;
@@ -293,31 +292,115 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
         for (int j = max(0, count - G::kStages); j < count; ++j)
           wait_for(smem_u32(&bars.full[j % G::kStages]), (uint32_t)(j / G::kStages) & 1u, &no_abort, err, 832);
       }
-    } else if (warp == G::kMmaWarp + 2) {
-      // ------------------------------------------------ factors s_x s_w of a block's tokens
-      int stage = 0, slot = 0;
-      uint32_t phase = 1;
+    } else {
+      // ------------------------------------------------ factors s_x s_w of a block's tokens, and the codes if need be
+      // What a block needs is read kAhead blocks before; `ahead` is the walk that far on.
+      constexpr int kAhead = 4;
       float* factors = reinterpret_cast<float*>(smem + G::kFactorAt);
-      while (ok && walk.next(tile, g0, g1)) {
-        const Tile t = find_tile(tile, m_tiles, M);
-        const float* s_w = a.s_w + (int64_t)t.n * blocks;
-        for (int g = g0; g < g1; ++g) {
-          float f[(BT + 31) / 32];
-          const float w = __ldg(s_w + g);
-          const float* s_x = a.s_x + (int64_t)g * a.M + t.row;
+      int stage = 0, slot = 0, tile_a, a0 = 0, a1 = 0;
+      uint32_t phase = 1;
+      Walk ahead = walk;
+      Tile ta = {0, 0, 0};
+      auto more = [&]() {  // the next block of `ahead` is a0 of tile ta
+        if (a0 < a1) return true;
+        if (!ahead.next(tile_a, a0, a1)) return false;
+        ta = find_tile(tile_a, m_tiles, M);
+        return true;
+      };
+      if constexpr (QUANT) {
+        const int w = warp - G::kMmaWarp - 2, half = lane / 16, sub = lane % 16;  // rows 8 w + 2 i + half
+        struct Block {
+          uint4 x[4];
+          float s_w;
+          bool in;
+        } ring[kAhead];
+        auto read = [&](Block& b) {
+          b.in = more();
+          if (!b.in) return;
+          b.s_w = __ldg(a.s_w + (int64_t)ta.n * blocks + a0);
+          const int k = a0 * 128 + sub * 8;
 #pragma unroll
-          for (int i = 0; i < (BT + 31) / 32; ++i) f[i] = lane + 32 * i < t.rows ? __ldg(s_x + lane + 32 * i) * w : 0.f;
-          ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.done[stage]), phase, abort_flag, err, 841));
-          if (!ok) break;
+          for (int i = 0; i < 4; ++i) {
+            const int row = 8 * w + 2 * i + half;
+            b.x[i] = row < M && k < (int)a.K ? *reinterpret_cast<const uint4*>(a.x + row * a.x_stride + k) : make_uint4(0u, 0u, 0u, 0u);
+          }
+          ++a0;
+        };
 #pragma unroll
-          for (int i = 0; i < (BT + 31) / 32; ++i)
-            if (lane + 32 * i < BT) factors[slot * BT + lane + 32 * i] = f[i];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&bars.full[stage]));  // no product starts without them: `done` cannot run two rounds ahead
-          if (++slot == G::kSlots) slot = 0;
-          if (++stage == G::kStages) {
-            stage = 0;
-            phase ^= 1u;
+        for (int j = 0; j < kAhead; ++j) read(ring[j]);
+        while (ok) {
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j) {
+            if (!ring[j].in || !ok) {
+              ok = false;
+              break;
+            }
+            uint2 codes[4];
+            float scale[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (8 * w + 2 * i < M) codes[i] = quantize8<BF16>(ring[j].x[i], scale[i]);
+            }
+            const float s_w = ring[j].s_w;
+            read(ring[j]);
+            ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.done[stage]), phase, abort_flag, err, 842));
+            if (!ok) break;
+            uint8_t* to = smem + stage * G::kBytes + kABytes;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (8 * w + 2 * i < M) {
+                const int row = 8 * w + 2 * i + half;
+                *reinterpret_cast<uint2*>(to + row * 128 + (((sub / 2) ^ (row & 7)) << 4) + sub % 2 * 8) = codes[i];
+                if (sub == 0) factors[slot * BT + row] = scale[i] * s_w;
+              }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars.full[stage]));
+            if (++slot == G::kSlots) slot = 0;
+            if (++stage == G::kStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+        }
+      } else if (warp == G::kMmaWarp + 2) {
+        constexpr int kEach = (BT + 31) / 32;  // factors of a lane
+        struct Block {
+          float f[kEach];
+          bool in;
+        } ring[kAhead];
+        auto read = [&](Block& b) {
+          b.in = more();
+          if (!b.in) return;
+          const float w = __ldg(a.s_w + (int64_t)ta.n * blocks + a0);
+          const float* s_x = a.s_x + (int64_t)a0 * a.M + ta.row;
+#pragma unroll
+          for (int i = 0; i < kEach; ++i) b.f[i] = lane + 32 * i < ta.rows ? s_x[lane + 32 * i] * w : 0.f;
+          ++a0;
+        };
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) read(ring[j]);
+        while (ok) {
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j) {
+            if (!ring[j].in || !ok) {
+              ok = false;
+              break;
+            }
+            ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.done[stage]), phase, abort_flag, err, 841));
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i)
+              if (lane + 32 * i < BT) factors[slot * BT + lane + 32 * i] = ring[j].f[i];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars.full[stage]));  // no product starts without them: `done` cannot run two rounds ahead
+            read(ring[j]);
+            if (++slot == G::kSlots) slot = 0;
+            if (++stage == G::kStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
         }
       }
@@ -333,25 +416,24 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
 
 int tile_tokens(int64_t M) { return M <= 16 ? 16 : M <= 64 ? 64 : 256; }
 
-template <int BT, bool BF16>
+template <int BT, bool BF16, bool QUANT = false>
 cudaError_t launch(const Fp8GemmArgs& a, void* ws, int* err, cudaStream_t s) {
   using G = Geo<BT>;
-  const auto fn = fp8_gemm_kernel<BT, BF16>;
+  const auto fn = fp8_gemm_kernel<BT, BF16, QUANT>;
   const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(fn), G::kSmem);
   if (e != cudaSuccess) return e;
-  CUtensorMap tw, tx;
+  CUtensorMap tw, tx = {};
   if (!make_map_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.wq, (uint64_t)a.K, (uint64_t)a.N, 128, kOut,
                    CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_map_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.xq, (uint64_t)a.K, (uint64_t)a.M, 128, G::kBoxRows,
-                   CU_TENSOR_MAP_SWIZZLE_128B))
+      (!QUANT && !make_map_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.xq, (uint64_t)a.K, (uint64_t)a.M, 128, G::kBoxRows,
+                              CU_TENSOR_MAP_SWIZZLE_128B)))
     return cudaErrorInvalidValue;
   const int m_tiles = (int)((a.M + BT - 1) / BT);
   const int64_t tiles = (a.N + kOut - 1) / kOut * m_tiles;
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
   int* flags = static_cast<int*>(ws);
   float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kCounterBytes);
-  fn<<<device_sm_count(), G::kThreads, G::kSmem, s>>>(tw, tx, a, m_tiles, (int)tiles, flags, parts, err);
-  return cudaGetLastError();
+  return launch_dependent(fn, dim3(device_sm_count()), G::kThreads, G::kSmem, s, tw, tx, a, m_tiles, (int)tiles, flags, parts, err);
 }
 
 }  // namespace
@@ -363,6 +445,7 @@ size_t fp8_gemm_workspace(int64_t M, int64_t, int64_t) {
 
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, bool bf16, void* ws, int* err, cudaStream_t s) {
   const int bt = tile_tokens(a.M);
+  if (a.x) return bf16 ? launch<16, true, true>(a, ws, err, s) : launch<16, false, true>(a, ws, err, s);
   const auto fn = bt == 16   ? (bf16 ? launch<16, true> : launch<16, false>)
                   : bt == 64 ? (bf16 ? launch<64, true> : launch<64, false>)
                              : (bf16 ? launch<256, true> : launch<256, false>);

@@ -2,14 +2,17 @@
 //
 // y[m, n] = sum_g s_x[g, m] s_w[n / 128, g] sum_{k in block g} xq[m, k] wq[n, k].
 // Each block of 128 k has a sum of its own in tensor memory (fp32; its products are exact), which is multiplied by the
-// two scales and added to the running sum in fp32 registers: a column of the tile is a token, so the factor s_x s_w is one
-// of BT numbers in shared memory, the same for all lanes.
+// two scales and added to the running sum in fp32 registers.
 //
-// A CTA works on tiles of 128 outputs x up to BT tokens: D[output][token] = A B with A = weights and B = codes, both K-major in
-// shared memory, tcgen05.mma kind::f8f6f4.  Roles: the first warps add up and write results (a thread has an output and some of the
-// tokens), then come a warp that issues the products, one that copies the operands (128 bytes of a row a block) and two that make
-// the factors, or with up to 16 tokens given in 16 bits the codes too: a layer of few tokens is one launch.  The persistent
-// grid and sums that cross CTAs are those of the grouped product.
+// Two forms of tcgen05.mma kind::f8f6f4, both operands K-major in shared memory:
+//   up to 64 tokens, D[output][token]: 128 outputs x up to 16 or 64 tokens; a column's factor s_x s_w is one of these numbers in
+//     shared memory, the same for all lanes;
+//   more tokens, D[token][output]: 128 tokens x 256 outputs; a lane has a token, whose factor is one register (the first form with
+//     256 tokens spent its time on loading factors: 574 us against TODO for 4096 tokens through 4096 x 28672).
+// Roles: the first warps add up and write results (a thread has a lane of D and some of its columns), then come a warp that issues
+// the products, one that copies the operands (128 bytes of a row a block) and two that make the first form's factors, or with up to
+// 16 tokens given in 16 bits the codes too: a layer of few tokens is one launch.  The persistent grid and sums that cross CTAs are
+// those of the grouped product.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -23,34 +26,39 @@
 namespace awq {
 namespace {
 
-constexpr int kOut = 128, kABytes = kOut * 128;  // outputs of a tile; bytes of a block's weights
+constexpr int kLanes = 128, kABytes = kLanes * 128;  // lanes of D; bytes of a block of their operand
 
+// BT: columns of D, tokens up to 64, outputs at 256.
 template <int BT>
 struct Geo {
-  static constexpr int kBytes = kABytes + BT * 128;     // a stage: weights | codes
+  static constexpr bool kTokenLanes = BT == 256;
+  static constexpr int kBytes = kABytes + BT * 128;     // a stage: the lanes' operand | the columns'
   static constexpr int kStages = BT == 256 ? 4 : BT == 64 ? 8 : 11;
   static constexpr int kSums = BT == 256 ? 2 : 4;       // blocks whose sums are kept in tensor memory, BT columns each
+  // 256 columns are two halves with products and barriers of their own: the sums of one are taken out during the products of
+  // the other, and each has its own block of weights.
+  static constexpr int kHalves = BT == 256 ? 2 : 1, kHalf = BT / kHalves;
   // A factor's slot is written again when the products kStages before it are done; those waited for the sums kSums
   // further back to be taken out.
   static constexpr int kSlots = kStages + kSums;
   static constexpr int kBoxRows = BT < 64 ? BT : 64;
   static constexpr int kSumWarps = BT == 16 ? 4 : 16, kMmaWarp = kSumWarps;
   static constexpr int kSumThreads = kSumWarps * 32, kThreads = (kMmaWarp + 4) * 32;
-  // registers of a thread: at launch, then by role (256 tokens: 64 sums)
+  // registers of a thread: at launch, then by role (256 columns: 64 sums)
   static constexpr int kLaunchRegs = BT == 16 ? 248 : 96, kSumRegs = BT == 16 ? 248 : BT == 64 ? 96 : 104,
                        kOtherRegs = BT == 16 ? 248 : BT == 64 ? 96 : 64;
   static_assert(kSumThreads * kSumRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs && kThreads * kLaunchRegs <= 65536,
                 "no more than was launched with");
-  static constexpr int kRows = BT / (kSumWarps / 4), kPairs = kRows / 2;  // tokens of a summing thread, and pairs of them
-  static constexpr int kFactorAt = kStages * kBytes, kSmem = kFactorAt + kSlots * BT * 4 + 1024;
+  static constexpr int kRows = BT / (kSumWarps / 4), kPairs = kRows / 2;  // columns of a summing thread, and pairs of them
+  static constexpr int kFactorAt = kStages * kBytes, kSmem = kFactorAt + (kTokenLanes ? 0 : kSlots * BT * 4) + 1024;
   static constexpr int kTmem = kSums * BT < 64 ? 64 : kSums * BT;
-  static constexpr size_t kPartBytes = (size_t)kOut * BT * 4;
+  static constexpr size_t kPartBytes = (size_t)kLanes * BT * 4;
   static_assert(kSmem <= 227 * 1024 - 1024 && kTmem <= 512, "shared memory, tensor memory");
 };
 
 template <int BT>
 struct Bars {
-  uint64_t full[Geo<BT>::kStages], done[Geo<BT>::kStages], d_empty[Geo<BT>::kSums], join, end;
+  uint64_t full[Geo<BT>::kStages], done[Geo<BT>::kStages][Geo<BT>::kHalves], d_empty[Geo<BT>::kSums][Geo<BT>::kHalves], join, end;
 };
 
 // The products of one block, 128 k in steps of 32, into a fresh sum.
@@ -68,20 +76,23 @@ __device__ __forceinline__ void mma_block(uint32_t d, uint64_t a, uint64_t b, ui
       : "memory");
 }
 
-// Tokens of a tile: they even out over the token tiles.
+// Rows of the two operands that a tile has: `lane`.. (128 of them) and `col` .. col + cols - 1.
 struct Tile {
-  int n, row, rows;  // block of outputs; tokens row .. row + rows - 1
+  int lane, col, cols;
 };
-__device__ __forceinline__ Tile find_tile(int tile, int m_tiles, int M) {
+// Token tiles are neighbours; in the first form tokens even out over them.
+template <int BT>
+__device__ __forceinline__ Tile find_tile(int tile, int m_tiles, const Fp8GemmArgs& a) {
   const int n = tile / m_tiles, m = tile - n * m_tiles;
-  const int share = ((M + m_tiles - 1) / m_tiles + 15) / 16 * 16;
-  return Tile{n, m * share, min(share, M - m * share)};
+  if constexpr (Geo<BT>::kTokenLanes) return Tile{m * kLanes, n * BT, min(BT, (int)a.N - n * BT)};
+  const int M = (int)a.M, share = ((M + m_tiles - 1) / m_tiles + 15) / 16 * 16;
+  return Tile{n * kLanes, m * share, min(share, M - m * share)};
 }
 
 // QUANT: the activations are 16-bit, quantized here.
 template <int BT, bool BF16, bool QUANT>
 __global__ void __launch_bounds__(Geo<BT>::kThreads, 1)
-fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const Fp8GemmArgs a,
+fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_lanes, const __grid_constant__ CUtensorMap tm_cols, const Fp8GemmArgs a,
                 int m_tiles, int tiles, int* flags, float* parts, int* err) {
   using G = Geo<BT>;
   extern __shared__ uint8_t smem_raw[];
@@ -97,10 +108,10 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
   if (tid == 0) {
     abort_word = 0;
     for (int i = 0; i < G::kStages; ++i) {
-      mbar_init(smem_u32(&bars.full[i]), QUANT ? 3 : 2);  // the copies and the factors
-      mbar_init(smem_u32(&bars.done[i]), 1);
+      mbar_init(smem_u32(&bars.full[i]), QUANT ? 3 : G::kTokenLanes ? 1 : 2);  // the copies and the factors
+      for (int h = 0; h < G::kHalves; ++h) mbar_init(smem_u32(&bars.done[i][h]), 1);
     }
-    for (int i = 0; i < G::kSums; ++i) mbar_init(smem_u32(&bars.d_empty[i]), G::kSumWarps);
+    for (int i = 0; i < G::kSums * G::kHalves; ++i) mbar_init(smem_u32(&bars.d_empty[0][i]), G::kSumWarps / G::kHalves);
     mbar_init(smem_u32(&bars.join), G::kSumWarps);
     mbar_init(smem_u32(&bars.end), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -123,8 +134,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
 
   if (warp < G::kSumWarps) {
     if constexpr (G::kSumRegs > G::kLaunchRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::kSumRegs));
-    // ------------------------------------------------ running sums: output n, tokens kRows wg ..
-    const int wg = warp / 4, n = warp % 4 * 32 + lane;
+    // ------------------------------------------------ running sums: lane n of D, columns kRows wg ..
+    const int wg = warp / 4, n = warp % 4 * 32 + lane, half = wg * G::kRows / G::kHalf;
     const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16) + G::kRows * wg;
     int d = 0, stage = 0, slot = 0;
     uint32_t phase = 0, join_phase = 0;
@@ -137,13 +148,29 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
       return all;
     };
     while (ok && walk.next(tile, g0, g1)) {
-      const Tile t = find_tile(tile, m_tiles, M);
-      const int mine = min(max(t.rows - G::kRows * wg, 0), G::kRows);  // of this thread's tokens
+      const Tile t = find_tile<BT>(tile, m_tiles, a);
+      const int mine = min(max(t.cols - G::kRows * wg, 0), G::kRows);  // of this thread's columns
       F2 acc[G::kPairs];
 #pragma unroll
       for (int i = 0; i < G::kPairs; ++i) acc[i] = F2(0.f, 0.f);
+      // token lanes: the factor, read a block ahead
+      const float* s_x = a.s_x + min(t.lane + n, M - 1);
+      const float* s_w = a.s_w + (int64_t)min(t.col / 128 + half, (int)((a.N + 127) / 128) - 1) * blocks;
+      float next_x = 0.f, next_w = 0.f;
+      if constexpr (G::kTokenLanes) {
+        next_x = s_x[(int64_t)g0 * a.M];
+        next_w = __ldg(s_w + g0);
+      }
       for (int g = g0; g < g1 && ok; ++g) {
-        ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.done[stage]), phase, abort_flag, err, 802));
+        const float f = next_x * next_w;
+        const F2 f2(f, f);
+        if constexpr (G::kTokenLanes) {
+          if (g + 1 < g1) {
+            next_x = s_x[(int64_t)(g + 1) * a.M];
+            next_w = __ldg(s_w + g + 1);
+          }
+        }
+        ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.done[stage][half]), phase, abort_flag, err, 802));
         if (!ok) break;
         tc_fence_after();
         const uint32_t factors = sm + G::kFactorAt + (slot * BT + G::kRows * wg) * 4;
@@ -158,9 +185,13 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
           if (c + 1 == G::kRows / 16) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars.d_empty[d]));  // the sum is in registers
+            if (lane == 0) mbar_arrive(smem_u32(&bars.d_empty[d][half]));  // the sum is in registers
           }
-          if (any) {
+          if (any && G::kTokenLanes) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              acc[8 * c + i] = fma2(F2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2, acc[8 * c + i]);
+          } else if (any) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 float4 f;
@@ -219,19 +250,31 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
         if (warp == 0)
           for (int q = walk.me + 1 + lane; q < last; q += 32) atomicExch(flags + q, 0);
       }
-      // Two neighbouring lanes swap one of a pair of tokens each, so that a lane writes two outputs of one token.
-      const int64_t col = (int64_t)t.n * kOut + (n & ~1);
-      const bool odd = lane & 1;
-      uint16_t* p = a.y + (int64_t)(t.row + G::kRows * wg + odd) * a.N + col;
-      const int rows = col < a.N ? mine - odd : 0;  // N is even
+      if constexpr (G::kTokenLanes) {
+        const int m = t.lane + n;
+        uint16_t* p = a.y + (int64_t)m * a.N + t.col + G::kRows * wg;
 #pragma unroll
-      for (int i = 0; i < G::kPairs; ++i) {
-        const float2 v = acc[i].get();
-        const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? v.x : v.y, 1);
-        const uint32_t w = odd ? pack2<BF16>(got, v.y) : pack2<BF16>(v.x, got);
-        if (2 * i < rows) *reinterpret_cast<uint32_t*>(p) = w;
-        p += 2 * a.N;
-        asm volatile("" : "+l"(p));  // one address at a time, not all made ahead
+        for (int i = 0; i < G::kPairs; i += 4) {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] = pack2<BF16>(acc[i + j].get().x, acc[i + j].get().y);
+          if (m < M && 2 * i < mine) *reinterpret_cast<uint4*>(p + 2 * i) = make_uint4(w[0], w[1], w[2], w[3]);  // N % 8 == 0
+        }
+      } else {
+        // Two neighbouring lanes swap one of a pair of tokens each, so that a lane writes two outputs of one token.
+        const int64_t col = (int64_t)t.lane + (n & ~1);
+        const bool odd = lane & 1;
+        uint16_t* p = a.y + (int64_t)(t.col + G::kRows * wg + odd) * a.N + col;
+        const int rows = col < a.N ? mine - odd : 0;  // N is even
+#pragma unroll
+        for (int i = 0; i < G::kPairs; ++i) {
+          const float2 v = acc[i].get();
+          const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? v.x : v.y, 1);
+          const uint32_t w = odd ? pack2<BF16>(got, v.y) : pack2<BF16>(v.x, got);
+          if (2 * i < rows) *reinterpret_cast<uint32_t*>(p) = w;
+          p += 2 * a.N;
+          asm volatile("" : "+l"(p));  // one address at a time, not all made ahead
+        }
       }
     }
   } else {
@@ -242,16 +285,22 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
       int d = 0, stage = 0;
       uint32_t phase = 0, d_phase = 1;
       while (ok && walk.next(tile, g0, g1)) {
-        const Tile t = find_tile(tile, m_tiles, M);
-        const uint32_t idesc = (1u << 4) | ((uint32_t)((t.rows + 15) / 16 * 2) << 17) | (8u << 24);  // e4m3 x e4m3, fp32 sums
-        for (int g = g0; g < g1; ++g) {
-          ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.full[stage]), phase, abort_flag, err, 821) &&
-                                           wait_for(smem_u32(&bars.d_empty[d]), d_phase, abort_flag, err, 822));
-          if (!ok) break;
-          tc_fence_after();
+        const Tile t = find_tile<BT>(tile, m_tiles, a);
+        const int columns = (t.cols + 15) / 16 * 16;
+        for (int g = g0; g < g1 && ok; ++g) {
+          ok = wait_for(smem_u32(&bars.full[stage]), phase, abort_flag, err, 821);
           const uint64_t at = desc0 + (uint64_t)((stage * G::kBytes) >> 4);
-          mma_block(tmem + d * BT, at, at + (uint64_t)(kABytes >> 4), idesc);
-          commit(smem_u32(&bars.done[stage]));
+#pragma unroll 1
+          for (int h = 0; h < G::kHalves; ++h) {
+            ok = __all_sync(0xFFFFFFFFu, ok && wait_for(smem_u32(&bars.d_empty[d][h]), d_phase, abort_flag, err, 822));
+            if (!ok) break;
+            tc_fence_after();
+            const int some = min(columns - h * G::kHalf, G::kHalf);
+            const uint32_t idesc = (1u << 4) | ((uint32_t)(some / 8) << 17) | (8u << 24);  // e4m3 x e4m3, fp32 sums
+            if (some > 0)
+              mma_block(tmem + d * BT + h * G::kHalf, at, at + (uint64_t)((kABytes + h * G::kHalf * 128) >> 4), idesc);
+            commit(smem_u32(&bars.done[stage][h]));
+          }
           if (++d == G::kSums) {
             d = 0;
             d_phase ^= 1u;
@@ -271,16 +320,16 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
         int stage = 0;
         uint32_t phase = 1;
         while (ok && walk.next(tile, g0, g1)) {
-          const Tile t = find_tile(tile, m_tiles, M);
-          const int boxes = (t.rows + G::kBoxRows - 1) / G::kBoxRows;
+          const Tile t = find_tile<BT>(tile, m_tiles, a);
+          const int boxes = (t.cols + G::kBoxRows - 1) / G::kBoxRows;
           for (int g = g0; g < g1; ++g, ++count) {
-            ok = wait_for(smem_u32(&bars.done[stage]), phase, abort_flag, err, 831);
+            ok = wait_for(smem_u32(&bars.done[stage][G::kHalves - 1]), phase, abort_flag, err, 831);
             if (!ok) break;
             const uint32_t bar = smem_u32(&bars.full[stage]), to = sm + stage * G::kBytes;
             mbar_arrive_tx(bar, (uint32_t)(kABytes + (QUANT ? 0 : boxes * G::kBoxRows * 128)));
-            tma_load_2d(to, &tm_w, g * 128, t.n * kOut, bar);
+            tma_load_2d(to, &tm_lanes, g * 128, t.lane, bar);
             for (int i = 0; !QUANT && i < boxes; ++i)
-              tma_load_2d(to + kABytes + i * G::kBoxRows * 128, &tm_x, g * 128, t.row + i * G::kBoxRows, bar);
+              tma_load_2d(to + kABytes + i * G::kBoxRows * 128, &tm_cols, g * 128, t.col + i * G::kBoxRows, bar);
             if (++stage == G::kStages) {
               stage = 0;
               phase ^= 1u;
@@ -292,7 +341,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
         for (int j = max(0, count - G::kStages); j < count; ++j)
           wait_for(smem_u32(&bars.full[j % G::kStages]), (uint32_t)(j / G::kStages) & 1u, &no_abort, err, 832);
       }
-    } else {
+    } else if constexpr (!G::kTokenLanes) {
       // ------------------------------------------------ factors s_x s_w of a block's tokens, and the codes if need be
       // What a block needs is read kAhead blocks before; `ahead` is the walk that far on.
       constexpr int kAhead = 4;
@@ -304,7 +353,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
       auto more = [&]() {  // the next block of `ahead` is a0 of tile ta
         if (a0 < a1) return true;
         if (!ahead.next(tile_a, a0, a1)) return false;
-        ta = find_tile(tile_a, m_tiles, M);
+        ta = find_tile<BT>(tile_a, m_tiles, a);
         return true;
       };
       if constexpr (QUANT) {
@@ -317,7 +366,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
         auto read = [&](Block& b) {
           b.in = more();
           if (!b.in) return;
-          b.s_w = __ldg(a.s_w + (int64_t)ta.n * blocks + a0);
+          b.s_w = __ldg(a.s_w + (int64_t)(ta.lane / kLanes) * blocks + a0);
           const int k = a0 * 128 + sub * 8;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -343,7 +392,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
             }
             const float s_w = ring[j].s_w;
             read(ring[j]);
-            ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.done[stage]), phase, abort_flag, err, 842));
+            ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.done[stage][G::kHalves - 1]), phase, abort_flag, err, 842));
             if (!ok) break;
             uint8_t* to = smem + stage * G::kBytes + kABytes;
 #pragma unroll
@@ -373,10 +422,10 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
         auto read = [&](Block& b) {
           b.in = more();
           if (!b.in) return;
-          const float w = __ldg(a.s_w + (int64_t)ta.n * blocks + a0);
-          const float* s_x = a.s_x + (int64_t)a0 * a.M + ta.row;
+          const float w = __ldg(a.s_w + (int64_t)(ta.lane / kLanes) * blocks + a0);
+          const float* s_x = a.s_x + (int64_t)a0 * a.M + ta.col;
 #pragma unroll
-          for (int i = 0; i < kEach; ++i) b.f[i] = lane + 32 * i < ta.rows ? s_x[lane + 32 * i] * w : 0.f;
+          for (int i = 0; i < kEach; ++i) b.f[i] = lane + 32 * i < ta.cols ? s_x[lane + 32 * i] * w : 0.f;
           ++a0;
         };
 #pragma unroll
@@ -388,7 +437,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
               ok = false;
               break;
             }
-            ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.done[stage]), phase, abort_flag, err, 841));
+            ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.done[stage][G::kHalves - 1]), phase, abort_flag, err, 841));
             if (!ok) break;
 #pragma unroll
             for (int i = 0; i < kEach; ++i)
@@ -414,7 +463,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
   }
 }
 
-int tile_tokens(int64_t M) { return M <= 16 ? 16 : M <= 64 ? 64 : 256; }
+int tile_columns(int64_t M) { return M <= kFp8FewTokens ? 16 : M <= 64 ? 64 : 256; }
 
 template <int BT, bool BF16, bool QUANT = false>
 cudaError_t launch(const Fp8GemmArgs& a, void* ws, int* err, cudaStream_t s) {
@@ -422,29 +471,31 @@ cudaError_t launch(const Fp8GemmArgs& a, void* ws, int* err, cudaStream_t s) {
   const auto fn = fp8_gemm_kernel<BT, BF16, QUANT>;
   const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(fn), G::kSmem);
   if (e != cudaSuccess) return e;
+  // the operand of the lanes in one box, that of the columns in boxes of up to 64 rows
+  const auto map = [&](CUtensorMap* tm, const uint8_t* p, int64_t rows, bool lanes) {
+    return make_map_2d(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p, (uint64_t)a.K, (uint64_t)rows, 128, lanes ? kLanes : G::kBoxRows,
+                       CU_TENSOR_MAP_SWIZZLE_128B);
+  };
   CUtensorMap tw, tx = {};
-  if (!make_map_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.wq, (uint64_t)a.K, (uint64_t)a.N, 128, kOut,
-                   CU_TENSOR_MAP_SWIZZLE_128B) ||
-      (!QUANT && !make_map_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.xq, (uint64_t)a.K, (uint64_t)a.M, 128, G::kBoxRows,
-                              CU_TENSOR_MAP_SWIZZLE_128B)))
-    return cudaErrorInvalidValue;
-  const int m_tiles = (int)((a.M + BT - 1) / BT);
-  const int64_t tiles = (a.N + kOut - 1) / kOut * m_tiles;
-  if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+  if (!map(&tw, a.wq, a.N, !G::kTokenLanes) || (!QUANT && !map(&tx, a.xq, a.M, G::kTokenLanes))) return cudaErrorInvalidValue;
+  const int64_t m_tiles = (a.M + (G::kTokenLanes ? kLanes : BT) - 1) / (G::kTokenLanes ? kLanes : BT);
+  const int64_t n_tiles = (a.N + (G::kTokenLanes ? BT : kLanes) - 1) / (G::kTokenLanes ? BT : kLanes);
+  if (n_tiles * m_tiles > INT32_MAX) return cudaErrorInvalidValue;
   int* flags = static_cast<int*>(ws);
   float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kCounterBytes);
-  return launch_dependent(fn, dim3(device_sm_count()), G::kThreads, G::kSmem, s, tw, tx, a, m_tiles, (int)tiles, flags, parts, err);
+  return launch_dependent(fn, dim3(device_sm_count()), G::kThreads, G::kSmem, s, G::kTokenLanes ? tx : tw,
+                          G::kTokenLanes ? tw : tx, a, (int)m_tiles, (int)(n_tiles * m_tiles), flags, parts, err);
 }
 
 }  // namespace
 
 // flags | parts of shared tiles
 size_t fp8_gemm_workspace(int64_t M, int64_t, int64_t) {
-  return kCounterBytes + (size_t)device_sm_count() * kOut * (size_t)tile_tokens(M) * 4;
+  return kCounterBytes + (size_t)device_sm_count() * kLanes * (size_t)tile_columns(M) * 4;
 }
 
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, bool bf16, void* ws, int* err, cudaStream_t s) {
-  const int bt = tile_tokens(a.M);
+  const int bt = tile_columns(a.M);
   if (a.x) return bf16 ? launch<16, true, true>(a, ws, err, s) : launch<16, false, true>(a, ws, err, s);
   const auto fn = bt == 16   ? (bf16 ? launch<16, true> : launch<16, false>)
                   : bt == 64 ? (bf16 ? launch<64, true> : launch<64, false>)

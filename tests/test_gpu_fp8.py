@@ -60,6 +60,32 @@ def test_quant(awq, M, K, bf16):
     assert np.array_equal(codes(xq), want_q)
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+def test_quant_at_the_borders_of_codes_and_of_the_range(awq, bf16):
+    """Every ratio of two 16-bit significands near the borders between codes, largest values from the smallest to the
+    largest, scales that are subnormal."""
+    rng = np.random.default_rng(1)
+    table = layer.e4m3_values()[:127]
+    tops = np.exp2(rng.integers(-20, 15, 400)) * (1 + rng.integers(0, 128 if bf16 else 1024, 400) / (128 if bf16 else 1024))
+    if bf16:
+        tops[:120] = np.exp2(rng.integers(-133, -90, 120)) * (1 + rng.integers(0, 128, 120) / 128)
+        tops[120:160] = np.exp2(rng.integers(100, 127, 40))
+    else:
+        tops[:40] = rng.integers(1, 64, 40) * 2.0 ** -24
+    tops = round16(tops.astype(np.float32), bf16)
+    border = (table[1:] + table[:-1]) / 2
+    x = np.empty((400, 128), np.float32)
+    with np.errstate(over="ignore", under="ignore"):
+        for r in range(400):
+            pick = rng.choice(border, 127)
+            x[r, 0] = tops[r]
+            x[r, 1:] = round16((pick / 448 * np.float64(tops[r]) * rng.choice([-1, 1], 127)).astype(np.float32), bf16)
+    want_q, want_s = layer.fp8_quant(x)
+    xq, s_x = awq.awq_fp8_quant_act(dev16(x, bf16))
+    assert np.array_equal(s_x.cpu().numpy(), want_s)
+    assert np.array_equal(codes(xq), want_q)
+
+
 class Problem:
     def __init__(self, M, K, N, seed=0):
         rng = np.random.default_rng(seed)

@@ -11,12 +11,12 @@
 //   64 (the operand B) and what the copies bring.
 // Roles: the first warps add the groups' sums up and write results (a thread has one column of each half and some rows: gate and
 // up of a gated layer meet in it), eight warps turn codes into operands (a thread has a column), then come a warp that issues the
-// products, one that copies weights (one 17 KB unit a group) and two for rows of x.
+// products, one that copies weights (one 17 KB unit a group) and one that copies rows of x.
 // Sums and operands in tensor memory go round, so that the products need not wait for either.  A step of the products is a half
 // of a group in tiles of 128 rows and a whole group in smaller ones; whoever waits for its products waits on one barrier.
-// Rows of x come in any order.  Tiles of 128 rows want 32 KB of them a group, which only whole boxes of neighbouring rows
-// bring in time: they are put in order first (at 32008 rows over 126 experts 484 us with four rows an instruction,
-// tile::gather4, and 406 with 16 bytes a thread against 273 without any copies).  Smaller tiles copy 16 bytes a thread.
+// Rows of x come in any order.  Up to 16 of them are copied four an instruction (tile::gather4, about 30 cycles each); more,
+// 32 KB a group with 128, are put in order first and copied in boxes of neighbouring rows (at 32008 rows over 126 experts
+// 484 us with four rows an instruction, 406 with 16 bytes a thread, 273 without any copies, each on that day's kernel).
 //
 // Tiles are dealt out to a persistent grid in whole rounds; what is left over is cut evenly along K, and a tile that several
 // CTAs share is finished by the one that has its first group, which adds the others' sums in their order.
@@ -38,7 +38,6 @@ namespace {
 constexpr int kScaleSlots = 8;  // groups whose scales are kept, see below
 constexpr int kRing = 4;        // groups whose products' barriers and rows are kept
 constexpr int kBoxRows = 32;    // rows of a box of x
-constexpr int kXAhead = 2;      // groups of rows copied 16 bytes a thread that are under way before one is waited for
 
 // Tiles of up to BT rows.
 template <int BT>
@@ -49,7 +48,7 @@ struct Geo {
   static constexpr int kACol = kSums * kSumCols;         // operands come behind them: [half][buffer] of 64 columns (128 k)
   static constexpr int kABufs = BT == 16 ? 3 : 2;        // groups whose operands are kept
   static constexpr int kXBytes = BT * 256;               // a group's rows: two blocks of 64 k, 128 bytes a row, swizzled
-  static constexpr bool kBoxes = BT == 128;              // rows in order, copied in boxes
+  static constexpr bool kBoxes = BT > 16;                // rows in order, copied in boxes; else four rows in any order at once
   static constexpr int kQStages = BT == 128 ? 5 : BT == 64 ? 8 : 10;
   // warps that add up, then eight that make operands, then products and copies
   static constexpr int kSumWarps = BT == 16 ? 4 : 8;
@@ -60,11 +59,10 @@ struct Geo {
                        kCodeRegs = BT == 16 ? 128 : BT == 64 ? 72 : 56, kOtherRegs = BT == 16 ? 128 : BT == 64 ? 72 : 32;
   static_assert(kSumThreads * kSumRegs + 256 * kCodeRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs &&
                 kThreads * kLaunchRegs <= 65536, "no more than was launched with");
-  // shared memory: rows of x | units | scales | expert tables | sources of rows
+  // shared memory: rows of x | units | scales | expert tables
   static constexpr int kQAt = kRing * kXBytes, kScaleAt = kQAt + kQStages * kMoeUnitBytes;
   static constexpr int kTableAt = kScaleAt + kScaleSlots * 256 * 4;
-  static constexpr int kSourceAt = kTableAt + 2 * (kMoeMaxExperts + 1) * 4;
-  static constexpr int kSmem = kSourceAt + BT * 4 + 1024;
+  static constexpr int kSmem = kTableAt + 2 * (kMoeMaxExperts + 1) * 4 + 1024;
   static constexpr int kRows = BT / (kSumWarps / 4), kPairs = kRows / 2;  // rows of a summing thread, and pairs of them, in each half
   static constexpr int kAtOnce = BT == 64 ? 2 : 1;       // loads of 16 columns of sums at once
   // a CTA's part of a shared tile: a sum for each of a summing thread's columns and rows
@@ -108,9 +106,15 @@ __device__ __forceinline__ void mma_group(uint32_t d, uint32_t a, uint64_t b0, u
       "r"(a), "l"(b0), "l"(b1), "r"(idesc)
       : "memory");
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// Four rows, 64 k each, of a tensor map whose box is one row high.
+__device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap* map, int col, const int (&r)[4], uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, "
+      "%6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(col), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar)
+      : "memory");
 }
+
 // Operands (q - z) 2^-kDown, exact, of a word of eight codes: k pairs 0..3.  A masked nibble is a subnormal 16-bit number, q or
 // 16 q of the smallest (in bf16 16 q reaches the lowest bit of the exponent, where numbers are still as far apart); one
 // multiplication and addition gives it its size and takes the zero point off.  One AND and one fma for two codes: 315
@@ -211,7 +215,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
   if (tid == 32) {
     abort_word = 0;
     for (int i = 0; i < kRing; ++i) {
-      mbar_init(smem_u32(&bars.x_full[i]), G::kBoxes ? 1 : 2);
+      mbar_init(smem_u32(&bars.x_full[i]), 1);
       for (int h = 0; h < G::kSteps; ++h) mbar_init(smem_u32(&bars.done[i][h]), 1);
     }
     for (int i = 0; i < G::kQStages; ++i) {
@@ -528,49 +532,34 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
         for (int j = max(0, count - kRing); j < count; ++j)
           wait_for(smem_u32(&bars.x_full[j % kRing]), (uint32_t)(j / kRing) & 1u, &no_abort, err, 744);
       }
-    } else {
-      // ------------------------------------------------ copies of rows: half a warp has a row, warp wx rows 4 i + 2 wx, + 1
-      const int wx = warp - G::kMmaWarp - 2, upper = lane / 16, chunk = lane % 16;
-      int* source = reinterpret_cast<int*>(smem + G::kSourceAt) + wx * (BT / 2);
-      const uint32_t dst0 = sm + (chunk / 8) * (G::kXBytes / 2);
-      int issued = 0, shown = 0;
-      auto show = [&]() {  // a stage whose copies have arrived
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars.x_full[shown % kRing]));
-        ++shown;
-      };
+    } else if (warp == G::kMmaWarp + 2) {
+      // ------------------------------------------------ copies of rows: lane l has rows 4 l .. 4 l + 3
+      int count = 0;
       while (ok && walk.next(tile, g0, g1)) {
         const Tile t = find_tile<BT>(first, items, a.experts, pairs, tile);
-        __syncwarp();
-        for (int i = lane; i < BT / 2; i += 32) {
-          const int row = t.row + min(i / 2 * 4 + 2 * wx + i % 2, t.rows - 1);
-          source[i] = source_row(a, row);
-        }
-        __syncwarp();
-        const int steps = (t.rows + 3) / 4;
-        for (int g = g0; g < g1; ++g) {
-          const int x = issued % kRing;
-          if (issued >= kRing) {
-            ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.done[x][G::kSteps - 1]), (uint32_t)(issued / kRing - 1) & 1u,
+        int r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = source_row(a, t.row + min(4 * lane + i, t.rows - 1));
+        const int fours = (t.rows + 3) / 4;
+        for (int g = g0; g < g1; ++g, ++count) {
+          const int x = count % kRing;
+          if (count >= kRing) {
+            ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.done[x][G::kSteps - 1]), (uint32_t)(count / kRing - 1) & 1u,
                                                   abort_flag, err, 741));
             if (!ok) break;
           }
-          const uint16_t* from = a.x + g * 128 + chunk * 8;
-#pragma unroll 4
-          for (int i = 0; i < steps; ++i) {
-            const int row = 4 * i + 2 * wx + upper;
-            cp_async16(dst0 + x * G::kXBytes + row * 128 + ((chunk ^ row) & 7) * 16, from + source[2 * i + upper] * a.x_stride);
-          }
-          asm volatile("cp.async.commit_group;" ::: "memory");
-          if (++issued - shown > kXAhead) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(kXAhead) : "memory");
-            show();
+          const uint32_t bar = smem_u32(&bars.x_full[x]), dst = sm + x * G::kXBytes + lane * 512;
+          if (lane == 0) mbar_arrive_tx(bar, (uint32_t)fours * 1024u);
+          __syncwarp();
+          if (lane < fours) {
+            gather4(dst, &tm_x, g * 128, r, bar);
+            gather4(dst + G::kXBytes / 2, &tm_x, g * 128 + 64, r, bar);
           }
         }
       }
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-      while (shown < issued) show();
+      volatile int no_abort = 0;
+      for (int j = max(0, count - kRing); j < count; ++j)
+        wait_for(smem_u32(&bars.x_full[j % kRing]), (uint32_t)(j / kRing) & 1u, &no_abort, err, 742);
     }
   }
   tc_fence_before();
@@ -608,21 +597,19 @@ cudaError_t launch(MoeGemmArgs a, bool gated, bool wide, void* ws, int* err, cud
   if (e != cudaSuccess) return e;
   int* flags = static_cast<int*>(ws);
   float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kCounterBytes);
-  CUtensorMap tm = {};
-  if (G::kBoxes) {
-    if (a.order) {
-      uint16_t* rows = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(parts) + parts_bytes(BT));
-      e = launch_dependent(moe_order_kernel, dim3(device_sm_count() * 8), 256, 0, s, a, rows);
-      if (e != cudaSuccess) return e;
-      a.x = rows;
-      a.x_rows = a.R;
-      a.x_stride = a.K;
-      a.order = nullptr;
-    }
-    if (!make_map_2d(&tm, BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.x, (uint64_t)a.K,
-                     (uint64_t)a.x_rows, 64, kBoxRows, CU_TENSOR_MAP_SWIZZLE_128B, (uint64_t)a.x_stride))
-      return cudaErrorInvalidValue;
+  if (G::kBoxes && a.order) {
+    uint16_t* rows = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(parts) + parts_bytes(BT));
+    e = launch_dependent(moe_order_kernel, dim3(device_sm_count() * 8), 256, 0, s, a, rows);
+    if (e != cudaSuccess) return e;
+    a.x = rows;
+    a.x_rows = a.R;
+    a.x_stride = a.K;
+    a.order = nullptr;
   }
+  CUtensorMap tm;
+  if (!make_map_2d(&tm, BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.x, (uint64_t)a.K,
+                   (uint64_t)a.x_rows, 64, G::kBoxes ? kBoxRows : 1, CU_TENSOR_MAP_SWIZZLE_128B, (uint64_t)a.x_stride))
+    return cudaErrorInvalidValue;
   return launch_dependent(fn, dim3(device_sm_count()), G::kThreads, G::kSmem, s, tm, a, flags, parts, err);
 }
 
@@ -630,7 +617,7 @@ cudaError_t launch(MoeGemmArgs a, bool gated, bool wide, void* ws, int* err, cud
 
 size_t moe_gemm_workspace(int64_t R, int experts, int64_t K, int64_t, bool gated) {
   const int bt = tile_rows(R, experts);
-  return kCounterBytes + parts_bytes(bt) + (bt == 128 ? (size_t)R * (size_t)K * 2 : 0);
+  return kCounterBytes + parts_bytes(bt) + (bt > 16 ? (size_t)R * (size_t)K * 2 : 0);
 }
 
 cudaError_t launch_moe_gemm(const MoeGemmArgs& a, bool gated, bool wide, bool bf16, void* ws, int* err, cudaStream_t s) {

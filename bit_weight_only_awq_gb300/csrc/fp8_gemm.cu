@@ -357,65 +357,64 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_lanes, const __grid_const
         return true;
       };
       if constexpr (QUANT) {
-        const int w = warp - G::kMmaWarp - 2, half = lane / 16, sub = lane % 16;  // rows 8 w + 2 i + half
-        struct Block {
-          uint4 x[4];
-          float s_w;
-          bool in;
-        } ring[kAhead];
-        auto read = [&](Block& b) {
-          b.in = more();
-          if (!b.in) return;
-          b.s_w = __ldg(a.s_w + (int64_t)(ta.lane / kLanes) * blocks + a0);
-          const int k = a0 * 128 + sub * 8;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = 8 * w + 2 * i + half;
-            b.x[i] = row < M && k < (int)a.K ? *reinterpret_cast<const uint4*>(a.x + row * a.x_stride + k) : make_uint4(0u, 0u, 0u, 0u);
-          }
-          ++a0;
-        };
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) read(ring[j]);
-        // kAhead blocks at once: one fence makes all their codes visible to the products (a fence for each block cost 0.5 us)
-        while (ok && ring[0].in) {
-          int at = stage;
-          uint32_t ph = phase;
-          int blocks_now = 0;
+        // kAhead blocks at once, their (block, token) pairs dealt out to the four half warps, so that few tokens are not many
+        // rounds; one fence makes all their codes visible to the products.  Loops, not unrolled: a call of one token runs through
+        // here three times, and code that has to be fetched first costs more than it does (19 us unrolled, TODO so).
+        const int w = warp - G::kMmaWarp - 2, sub = lane % 16, item = 2 * w + lane / 16;
+        const int lg = M <= 1 ? 0 : 32 - __clz(M - 1), rounds = 1 << lg;  // tokens padded to a power of two
+        while (ok) {
+          int block[kAhead], out[kAhead], n = 0;
 #pragma unroll
           for (int j = 0; j < kAhead; ++j) {
-            if (!ring[j].in || !ok) continue;
-            ++blocks_now;
-            uint2 codes[4];
-            float scale[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (8 * w + 2 * i < M) codes[i] = quantize8<BF16>(ring[j].x[i], scale[i]);
-            }
-            const float s_w = ring[j].s_w;
-            read(ring[j]);
-            ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.done[at][0]), ph, abort_flag, err, 842));
-            if (!ok) continue;
-            uint8_t* to = smem + at * G::kBytes + kABytes;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (8 * w + 2 * i < M) {
-                const int row = 8 * w + 2 * i + half;
-                *reinterpret_cast<uint2*>(to + row * 128 + (((sub / 2) ^ (row & 7)) << 4) + sub % 2 * 8) = codes[i];
-                if (sub == 0) factors[slot * BT + row] = scale[i] * s_w;
-              }
-            }
-            if (++slot == G::kSlots) slot = 0;
-            if (++at == G::kStages) {
-              at = 0;
-              ph ^= 1u;
+            block[j] = out[j] = 0;
+            if (more()) {
+              block[j] = a0++;
+              out[j] = ta.lane / kLanes;
+              ++n;
             }
           }
+          if (n == 0) break;
+          uint4 x;
+          float s_w;
+          auto read = [&](int p) {
+            const int it = 4 * p + item, j = it >> lg, row = it & (rounds - 1);
+            const int g = j == 0 ? block[0] : j == 1 ? block[1] : j == 2 ? block[2] : block[3];
+            const int o = j == 0 ? out[0] : j == 1 ? out[1] : j == 2 ? out[2] : out[3];
+            const int k = g * 128 + sub * 8;
+            x = row < M && k < (int)a.K ? *reinterpret_cast<const uint4*>(a.x + row * a.x_stride + k) : make_uint4(0u, 0u, 0u, 0u);
+            s_w = __ldg(a.s_w + (int64_t)o * blocks + g);
+          };
+          read(0);
+#pragma unroll 1
+          for (int j = 0; j < n && ok; ++j) {
+            const int at = stage + j;
+            ok = wait_for(smem_u32(&bars.done[at < G::kStages ? at : at - G::kStages][0]), at < G::kStages ? phase : phase ^ 1u,
+                          abort_flag, err, 842);
+          }
+          ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
+#pragma unroll 1
+          for (int p = 0; p < rounds; ++p) {
+            const uint4 now = x;
+            const float w_now = s_w;
+            if (p + 1 < rounds) read(p + 1);
+            float scale;
+            const uint2 codes = quantize8<BF16>(now, scale);
+            const int it = 4 * p + item, j = it >> lg, row = it & (rounds - 1);
+            if (j < n && row < M) {
+              const int at = stage + j < G::kStages ? stage + j : stage + j - G::kStages;
+              const int sl = slot + j < G::kSlots ? slot + j : slot + j - G::kSlots;
+              *reinterpret_cast<uint2*>(smem + at * G::kBytes + kABytes + row * 128 + (((sub / 2) ^ (row & 7)) << 4) + sub % 2 * 8) =
+                  codes;
+              if (sub == 0) factors[sl * BT + row] = scale * w_now;
+            }
+          }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
-          for (int j = 0; j < blocks_now; ++j) {
+#pragma unroll 1
+          for (int j = 0; j < n; ++j) {
             if (lane == 0) mbar_arrive(smem_u32(&bars.full[stage]));
+            if (++slot == G::kSlots) slot = 0;
             if (++stage == G::kStages) {
               stage = 0;
               phase ^= 1u;

@@ -32,22 +32,28 @@ __device__ __forceinline__ void commit(uint32_t bar) {
 }
 constexpr int kMinUnits = 4;  // groups that a CTA gets at least of what is cut along K
 
-// What a CTA works on, in order: parts of tiles, groups g0 .. g1 - 1 of each.
+// What a CTA works on, in order: parts of tiles, groups g0 .. g1 - 1 of each.  Counts stay within 32 bits: fewer than 2 grid
+// tiles are cut along K, each of at most 8192 groups.
 struct Walk {
-  int grid, me, groups, rounds, tiles;  // whole rounds of tiles; the tiles that are left
+  int grid, me, groups, rounds;  // whole rounds of tiles; what is left is cut
   int round, u, u1;
-  long long units;
-  int ctas;
+  int ctas, share, longer;  // CTAs that have some of it: `share` groups each, the first `longer` of them one more
   __device__ __forceinline__ Walk(int total, int groups_) : grid(gridDim.x), me(blockIdx.x), groups(groups_) {
-    rounds = total % grid == 0 ? total / grid : max(0, total / grid - 1);
-    tiles = total - rounds * grid;
-    units = (long long)tiles * groups;
-    ctas = (int)max(1ll, min((long long)grid, units / kMinUnits));
+    rounds = total / grid;
+    int tiles = total - rounds * grid;
+    if (tiles > 0 && rounds > 0) {
+      --rounds;
+      tiles += grid;
+    }
+    const int units = tiles * groups;
+    ctas = max(1, min(grid, units / kMinUnits));
+    share = units / ctas;
+    longer = units - share * ctas;
     round = 0;
     u = me < ctas ? begin_of(me) : 0;
     u1 = me < ctas ? begin_of(me + 1) : 0;
   }
-  __device__ __forceinline__ int begin_of(int cta) const { return (int)(units * cta / ctas); }
+  __device__ __forceinline__ int begin_of(int cta) const { return cta * share + min(cta, longer); }
   __device__ __forceinline__ bool next(int& tile, int& g0, int& g1) {
     if (round < rounds) {
       tile = me + grid * round++;

@@ -758,12 +758,11 @@ def awq_moe_route(logits: torch.Tensor, top_k: int, normalize: bool = True, stre
     rows = T * top_k
     weights = torch.empty((T, top_k), dtype=torch.float32, device=device)
     buf = torch.empty(experts + 1 + 3 * rows, dtype=torch.int32, device=device)  # one allocation for the whole numbers
-    offsets = buf.data_ptr()
-    ids = offsets + 4 * (experts + 1)
+    ids = buf.data_ptr()  # first: 16-byte aligned, which the plan's kernel reads fastest
     _check("awq_moe_route", lib.awq_moe_route(
         logits.data_ptr(), _row_stride("awq_moe_route", logits, experts), T, experts, top_k, int(normalize), kind, ids,
-        weights.data_ptr(), offsets, ids + 4 * rows, ids + 8 * rows, _raw_stream(stream, device)))
-    offsets, ids, order, place = buf.split_with_sizes((experts + 1, rows, rows, rows))
+        weights.data_ptr(), ids + 12 * rows, ids + 4 * rows, ids + 8 * rows, _raw_stream(stream, device)))
+    ids, order, place, offsets = buf.split_with_sizes((rows, rows, rows, experts + 1))
     return weights, ids.view(T, top_k), MoePlan(offsets, order, place, top_k)
 
 

@@ -570,13 +570,22 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
   }
 }
 
-// Rows of x in the plan's order, 16 bytes a thread.
+// Rows of x in the plan's order, a warp for each (32008 x 2048: 35 us with a thread for 16 bytes, each looking its row up, TODO so).
 __global__ void __launch_bounds__(256) moe_order_kernel(const MoeGemmArgs a, uint16_t* out) {
   wait_then_release_dependents();
-  const int vec = (int)(a.K / 8), rows = min(max(a.offsets[a.experts], 0), (int)a.R);
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)rows * vec; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / vec;
-    reinterpret_cast<uint4*>(out)[i] = *reinterpret_cast<const uint4*>(a.x + source_row(a, (int)r) * a.x_stride + (i - r * vec) * 8);
+  const int vec = (int)(a.K / 8), rows = min(max(a.offsets[a.experts], 0), (int)a.R), lane = threadIdx.x % 32;
+  for (int r = (int)(blockIdx.x * 8 + threadIdx.x / 32); r < rows; r += (int)gridDim.x * 8) {
+    const uint4* from = reinterpret_cast<const uint4*>(a.x + source_row(a, r) * a.x_stride);
+    uint4* to = reinterpret_cast<uint4*>(out + (int64_t)r * a.K);
+    for (int i0 = 0; i0 < vec; i0 += 256) {
+      uint4 v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i0 + 32 * j + lane < vec) v[j] = from[i0 + 32 * j + lane];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i0 + 32 * j + lane < vec) to[i0 + 32 * j + lane] = v[j];
+    }
   }
 }
 

@@ -91,30 +91,59 @@ __device__ __forceinline__ void route_token(const void* logits, int64_t at, int 
 // Class of a position: its expert, or `experts` for an id that is none.
 __device__ __forceinline__ int class_of(int id, int experts) { return (unsigned)id < (unsigned)experts ? id : experts; }
 
-// The warp's positions [begin, end) (multiples of 32 apart): how many are of a class below e, and of class e.
-__device__ __forceinline__ void count_class(const int32_t* ids, int begin, int end, int e, int experts, int lane, int& below,
-                                            int& equal) {
-  below = equal = 0;
-#pragma unroll 4
-  for (int i = begin; i < end; i += 32) {
-    const int c = i + lane < end ? class_of(ids[i + lane], experts) : experts + 1;
-    below += __popc(__ballot_sync(kAll, c < e));
-    equal += __popc(__ballot_sync(kAll, c == e));
+// Four ids from position i on; `none` beyond the end.
+__device__ __forceinline__ void read4(const int32_t* ids, int i, int end, bool aligned, int experts, int (&c)[4]) {
+  constexpr int kBeyond = 0x7FFFFFFF;
+  if (aligned && i + 4 <= end) {
+    const int4 v = *reinterpret_cast<const int4*>(ids + i);
+    c[0] = class_of(v.x, experts), c[1] = class_of(v.y, experts), c[2] = class_of(v.z, experts), c[3] = class_of(v.w, experts);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[j] = i + j < end ? class_of(ids[i + j], experts) : kBeyond;
   }
 }
-// Writes the rows of class e among them, from row `row` on.
-__device__ __forceinline__ void place_class(const int32_t* ids, int begin, int end, int e, int experts, int lane, int row,
-                                            int32_t* order, int32_t* place) {
+// The warp's positions [begin, end): how many are of a class below e, and of class e.  A lane reads four neighbours.
+__device__ __forceinline__ void count_class(const int32_t* ids, int begin, int end, bool aligned, int e, int experts, int lane,
+                                            int& below, int& equal) {
+  int b = 0, q = 0;
 #pragma unroll 4
-  for (int i = begin; i < end; i += 32) {
-    const bool in = i + lane < end && class_of(ids[i + lane], experts) == e;
-    const uint32_t votes = __ballot_sync(kAll, in);
-    if (in) {
-      const int r = row + __popc(votes & ((1u << lane) - 1u));
-      order[r] = e < experts ? i + lane : -1;
-      place[i + lane] = e < experts ? r : -1;
+  for (int i = begin + 4 * lane; i < end; i += 128) {
+    int c[4];
+    read4(ids, i, end, aligned, experts, c);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      b += c[j] < e;
+      q += c[j] == e;
     }
-    row += __popc(votes);
+  }
+  below = __reduce_add_sync(kAll, b);
+  equal = __reduce_add_sync(kAll, q);
+}
+// Writes the rows of class e among them, from row `row` on.
+__device__ __forceinline__ void place_class(const int32_t* ids, int begin, int end, bool aligned, int e, int experts, int lane,
+                                            int row, int32_t* order, int32_t* place) {
+  const uint32_t before = (1u << lane) - 1u;
+#pragma unroll 4
+  for (int i0 = begin; i0 < end; i0 += 128) {
+    const int i = i0 + 4 * lane;
+    int c[4];
+    read4(ids, i, end, aligned, experts, c);
+    uint32_t votes[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) votes[j] = __ballot_sync(kAll, c[j] == e);
+    int r = row;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      r += __popc(votes[j] & before);
+      row += __popc(votes[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c[j] == e) {
+        order[r] = e < experts ? i + j : -1;
+        place[i + j] = e < experts ? r : -1;
+        ++r;
+      }
   }
 }
 
@@ -125,10 +154,11 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ 
   __shared__ int s_below[32], s_equal[32];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, e = blockIdx.x;
   wait_then_release_dependents();
-  const int share = (int)(((int64_t)R + 1023) / 1024 * 32);
+  const int share = (int)(((int64_t)R + 4095) / 4096 * 128);
+  const bool aligned = (reinterpret_cast<uintptr_t>(ids) & 15u) == 0;
   const int begin = (int)min((int64_t)R, (int64_t)warp * share), end = (int)min((int64_t)R, (int64_t)(warp + 1) * share);
   int below, equal;
-  count_class(ids, begin, end, e, experts, lane, below, equal);
+  count_class(ids, begin, end, aligned, e, experts, lane, below, equal);
   if (lane == 0) {
     s_below[warp] = below;
     s_equal[warp] = equal;
@@ -141,7 +171,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ 
     before += __shfl_xor_sync(kAll, before, d);
   }
   if (threadIdx.x == 0) offsets[e] = row;
-  place_class(ids, begin, end, e, experts, lane, row + before, order, place);
+  place_class(ids, begin, end, aligned, e, experts, lane, row + before, order, place);
 }
 
 template <int TYPE, int L>
@@ -169,7 +199,7 @@ __global__ void __launch_bounds__(1024) route_few_kernel(const void* __restrict_
                                                          int top_k, int normalize, int32_t* __restrict__ ids,
                                                          float* __restrict__ weights, int32_t* __restrict__ offsets,
                                                          int32_t* __restrict__ order, int32_t* __restrict__ place) {
-  __shared__ int32_t s_ids[kFewRows];
+  __shared__ __align__(16) int32_t s_ids[kFewRows];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, R = T * top_k;
   wait_then_release_dependents();
   for (int t = warp; t < T; t += 32) {
@@ -203,9 +233,9 @@ __global__ void __launch_bounds__(1024) route_few_kernel(const void* __restrict_
   }
   for (int e = warp; e <= experts; e += 32) {
     int below, equal;
-    count_class(s_ids, 0, R, e, experts, lane, below, equal);
+    count_class(s_ids, 0, R, true, e, experts, lane, below, equal);
     if (lane == 0) offsets[e] = below;
-    place_class(s_ids, 0, R, e, experts, lane, below, order, place);
+    place_class(s_ids, 0, R, true, e, experts, lane, below, order, place);
   }
 }
 

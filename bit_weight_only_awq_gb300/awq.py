@@ -75,6 +75,8 @@ _SIGS = {
     "awq_moe_gemm_workspace_bytes": (_sz, [_i64, _i32, _i64, _i64, _i32]),
     "awq_moe_gemm": (_i32, [_p, _i64, _i64, _p, _p, _p, _i32, _p, _i32, _i64, _i32, _i64, _i64, _i32, _i32, _p, _sz, _p]),
     "awq_moe_combine": (_i32, [_p, _i32, _p, _p, _p, _i64, _p, _i64, _i32, _i64, _i64, _i32, _p]),
+    "awq_moe_workspace_bytes": (_sz, [_i64, _i32, _i32, _i64, _i64, _i64]),
+    "awq_moe": (_i32, [_p, _i64, _p, _p, _p, _p, _p, _p, _p, _i64, _p, _i64, _i32, _i32, _i64, _i64, _i64, _i32, _p, _sz, _p]),
     "awq_fp8_quant_act": (_i32, [_p, _i64, _p, _p, _i64, _i64, _i32, _p]),
     "awq_fp8_gemm_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "awq_fp8_gemm": (_i32, [_p, _p, _p, _p, _p, _i64, _i64, _i64, _i32, _p, _sz, _p]),
@@ -877,11 +879,16 @@ def awq_moe_combine(y, plan: MoePlan, weights, residual=None, dtype=None, out=No
     return out
 
 
+def awq_moe_workspace_bytes(tokens: int, top_k: int, up: MoeWeights, down: MoeWeights) -> int:
+    """Bytes of an awq_moe workspace on the current device."""
+    return int(lib.awq_moe_workspace_bytes(tokens, top_k, up.experts, up.K, down.K, down.N))
+
+
 def awq_moe(x, up: MoeWeights, down: MoeWeights, weights, plan: MoePlan, residual=None, out=None, workspace=None, stream=None):
     """A sparse feed-forward layer: x [T, K] through every token's experts, down(silu(gate) * up), weighted and added up
     (to `residual` where one is given): awq_moe_gemm, awq_moe_gemm and awq_moe_combine.  `up` is gated, `down` plain;
     weights and plan from awq_moe_route.  Between the products the activations have x's type, between down and the sum they
-    are fp32.  A captured call takes a workspace of the larger of the two products' sizes."""
+    are fp32.  Workspaces as for awq_moe_gemm (awq_moe_workspace_bytes)."""
     name = "awq_moe"
     if not up.gated or down.gated or down.K != up.outputs:
         raise ValueError("awq_moe: up is gated, down is plain, and down takes up's outputs")
@@ -899,26 +906,15 @@ def awq_moe(x, up: MoeWeights, down: MoeWeights, weights, plan: MoePlan, residua
     _on_current_gpu(name, x, up.data, down.data, weights, plan.offsets, plan.order, plan.place, residual, out, workspace)
     handle = _raw_stream(stream, device)
     if workspace is None:
-        query = "awq_moe_gemm_workspace_bytes"
-        need = max(_layer_workspace_need(device.index, query, rows, experts, up.K, up.N, 1),
-                   _layer_workspace_need(device.index, query, rows, experts, down.K, down.N, 0))
+        need = _layer_workspace_need(device.index, "awq_moe_workspace_bytes", T, top_k, experts, up.K, down.K, H)
         workspace = _layer_workspace(name, handle, device, need, stream)
-    ws, nbytes, offsets = workspace.data_ptr(), workspace.numel() * workspace.element_size(), plan.offsets.data_ptr()
-    h = torch.empty((rows, down.K), dtype=x.dtype, device=device)
-    y = torch.empty((rows, H), dtype=torch.float32, device=device)
     if out is None:
         out = torch.empty((T, H), dtype=x.dtype, device=device)
-    if stream is not None:
-        for t in (h, y, out):  # made on the current stream, used on another
-            t.record_stream(stream)
-    _check(name, lib.awq_moe_gemm(x.data_ptr(), _row_stride(name, x, up.K), T, up.data.data_ptr(), offsets,
-                                  plan.order.data_ptr(), top_k, h.data_ptr(), 0, rows, experts, up.K, up.N, 1, dtype, ws,
-                                  nbytes, handle))
-    _check(name, lib.awq_moe_gemm(h.data_ptr(), down.K, rows, down.data.data_ptr(), offsets, None, 1, y.data_ptr(), 1, rows,
-                                  experts, down.K, H, 0, dtype, ws, nbytes, handle))
-    _check(name, lib.awq_moe_combine(y.data_ptr(), 1, plan.place.data_ptr(), weights.data_ptr(), _ptr(residual),
-                                     0 if residual is None else _row_stride(name, residual, H), out.data_ptr(), T, top_k, H,
-                                     rows, dtype, handle))
+    _check(name, lib.awq_moe(
+        x.data_ptr(), _row_stride(name, x, up.K), up.data.data_ptr(), down.data.data_ptr(), plan.offsets.data_ptr(),
+        plan.order.data_ptr(), plan.place.data_ptr(), weights.data_ptr(), _ptr(residual),
+        0 if residual is None else _row_stride(name, residual, H), out.data_ptr(), T, top_k, experts, up.K, down.K, H, dtype,
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle))
     return out
 
 

@@ -705,7 +705,7 @@ awq_status awq_moe_gemm(const uint16_t* x, int64_t x_stride, int64_t x_rows, con
   int* err = device_error_ptr();
   if (!err) return AWQ_ECUDA;
   const MoeGemmArgs a{x, x_stride, x_rows, static_cast<const uint8_t*>(packed), offsets, order, order ? top_k : 1,
-                      y, R,        experts, K, N, (int)moe_tiles(N, gated != 0)};
+                      y, R,        experts, K, N, (int)moe_tiles(N, gated != 0), false};
   return from_cuda(launch_moe_gemm(a, gated != 0, y_fp32 != 0, dtype == AWQ_BF16, workspace, err, (cudaStream_t)stream));
 }
 
@@ -723,6 +723,60 @@ awq_status awq_moe_combine(const void* y, int32_t y_fp32, const int32_t* place, 
   if (st != AWQ_OK) return st;
   return from_cuda(launch_moe_combine(y, y_fp32 != 0, place, weights, residual, res_stride, out, T, top_k, H, R, dtype == AWQ_BF16,
                                       (cudaStream_t)stream));
+}
+
+// Workspace of the whole layer: what the products need | rows between up and down | rows between down and the sum.
+struct MoeLayout {
+  size_t product, rows, bytes;
+};
+static bool moe_layout(int64_t T, int32_t top_k, int32_t experts, int64_t K, int64_t inner, int64_t H, MoeLayout& l) {
+  if (top_k < 1 || top_k > kMoeMaxTopK || T < 0 || T > kMoeMaxRows / top_k || inner < 1 || inner > kMoeMaxSize / 2 ||
+      !moe_shape_ok(experts, K, 2 * inner, 1) || !moe_shape_ok(experts, inner, H, 0))
+    return false;
+  const int64_t R = T * top_k;
+  const size_t up = moe_gemm_workspace(R, experts, K, 2 * inner, true), down = moe_gemm_workspace(R, experts, inner, H, false);
+  l.product = align256(up > down ? up : down);
+  l.rows = align256((size_t)R * (size_t)inner * 2);
+  l.bytes = l.product + l.rows + (size_t)R * (size_t)H * 4;
+  return true;
+}
+
+size_t awq_moe_workspace_bytes(int64_t T, int32_t top_k, int32_t experts, int64_t K, int64_t inner, int64_t H) {
+  MoeLayout l;
+  return moe_layout(T, top_k, experts, K, inner, H, l) && T > 0 ? l.bytes : 0;
+}
+
+awq_status awq_moe(const uint16_t* x, int64_t x_stride, const void* up, const void* down, const int32_t* offsets,
+                   const int32_t* order, const int32_t* place, const float* weights, const uint16_t* residual,
+                   int64_t res_stride, uint16_t* out, int64_t T, int32_t top_k, int32_t experts, int64_t K, int64_t inner,
+                   int64_t H, awq_dtype dtype, void* workspace, size_t workspace_bytes, awq_stream_t stream) {
+  MoeLayout l;
+  if (!moe_layout(T, top_k, experts, K, inner, H, l) || x_stride < K || x_stride % 8 != 0 || !is_dtype(dtype)) return AWQ_EINVAL;
+  if (residual && (res_stride < H || res_stride % 8 != 0)) return AWQ_EINVAL;
+  if (T == 0) return AWQ_OK;
+  if (!x || !up || !down || !offsets || !order || !place || !weights || !out) return AWQ_ENULL;
+  if (!aligned16(x) || !aligned16(up) || !aligned16(down) || !aligned16(residual) || !aligned16(out) || !aligned4(offsets) ||
+      !aligned4(order) || !aligned4(place) || !aligned4(weights))
+    return AWQ_EALIGN;
+  awq_status st = check_workspace(l.bytes, workspace, workspace_bytes);
+  if (st != AWQ_OK) return st;
+  st = check_arch();
+  if (st != AWQ_OK) return st;
+  int* err = device_error_ptr();
+  if (!err) return AWQ_ECUDA;
+  const cudaStream_t s = (cudaStream_t)stream;
+  const bool bf16 = dtype == AWQ_BF16;
+  const int64_t R = T * top_k;
+  uint16_t* h = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + l.product);
+  float* y = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + l.product + l.rows);
+  const MoeGemmArgs first{x, x_stride, T, static_cast<const uint8_t*>(up), offsets, order, top_k,
+                          h, R,        experts, K, 2 * inner, (int)moe_tiles(2 * inner, true), false};
+  if (launch_moe_gemm(first, true, false, bf16, workspace, err, s) != cudaSuccess) return AWQ_ECUDA;
+  // up has waited for what wrote the plan: down reads it, and its weights, while up runs
+  const MoeGemmArgs second{h, inner, R, static_cast<const uint8_t*>(down), offsets, nullptr, 1,
+                           y, R,     experts, inner, H, (int)moe_tiles(H, false), true};
+  if (launch_moe_gemm(second, false, true, bf16, workspace, err, s) != cudaSuccess) return AWQ_ECUDA;
+  return from_cuda(launch_moe_combine(y, true, place, weights, residual, res_stride, out, T, top_k, H, R, bf16, s));
 }
 
 // ---- e4m3 linear layers

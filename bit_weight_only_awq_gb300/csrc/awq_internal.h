@@ -236,6 +236,8 @@ struct MoeGemmArgs {
   int experts;
   int64_t K, N;  // N: both halves when gated
   int tiles;
+  // The kernel before this one in the stream has waited for what wrote offsets (and weights): they may be read while it runs.
+  bool early;
 };
 size_t moe_gemm_workspace(int64_t R, int experts, int64_t K, int64_t N, bool gated);
 // wide: y in fp32

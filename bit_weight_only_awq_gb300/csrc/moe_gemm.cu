@@ -234,7 +234,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  wait_then_release_dependents();
+  if (!a.early) wait_then_release_dependents();
   if (warp == 0) expert_tables<BT>(a, lane, first, items);
   tc_fence_before();
   __syncthreads();
@@ -262,6 +262,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
       return all;
     };
     // a sum is in registers
+    if (a.early) wait_then_release_dependents();
     auto take = [&]() {
       tc_fence_before();
       __syncwarp();
@@ -509,6 +510,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
     } else if constexpr (G::kBoxes) {
       // ------------------------------------------------ copies of rows, boxes of 32 rows x 64 k
       if (warp == G::kMmaWarp + 2 && lane == 0) {
+        if (a.early) asm volatile("griddepcontrol.wait;" ::: "memory");
         int count = 0;
         while (ok && walk.next(tile, g0, g1)) {
           const Tile t = find_tile<BT>(first, items, a.experts, pairs, tile);
@@ -535,6 +537,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
     } else if (warp == G::kMmaWarp + 2) {
       // ------------------------------------------------ copies of rows: lane l has rows 4 l .. 4 l + 3
       int count = 0;
+      if (a.early) asm volatile("griddepcontrol.wait;" ::: "memory");
       while (ok && walk.next(tile, g0, g1)) {
         const Tile t = find_tile<BT>(first, items, a.experts, pairs, tile);
         int r[4];

@@ -599,6 +599,19 @@ awq_status awq_moe_combine(const void *y, int32_t y_fp32, const int32_t *place, 
                            int64_t H, int64_t R, awq_dtype dtype, awq_stream_t stream);
 
 /*
+ * awq_moe -- the whole sparse feed-forward layer: awq_moe_gemm of x [T, K] (row stride x_stride) with the gated `up`
+ * (experts x [K, 2 inner]), awq_moe_gemm of its rows with `down` (experts x [inner, H]) in fp32, awq_moe_combine.  The rows
+ * between up and down have x's type; the results are those of the three calls.  Plan and weights as from awq_moe_route.
+ * Workspace: awq_moe_workspace_bytes(), which holds the rows between the products too; contract as for awq_moe_gemm's.
+ */
+size_t awq_moe_workspace_bytes(int64_t T, int32_t top_k, int32_t experts, int64_t K, int64_t inner, int64_t H);
+awq_status awq_moe(const uint16_t *x, int64_t x_stride, const void *up, const void *down, const int32_t *offsets,
+                   const int32_t *order, const int32_t *place, const float *weights, const uint16_t *residual,
+                   int64_t res_stride, uint16_t *out, int64_t T, int32_t top_k, int32_t experts, int64_t K,
+                   int64_t inner, int64_t H, awq_dtype dtype, void *workspace, size_t workspace_bytes,
+                   awq_stream_t stream);
+
+/*
  * Linear layers in 8-bit floating point
  * -------------------------------------
  * Weights e4m3 [N, K] (row-major: K dense) with an fp32 scale for each block of 128 x 128, s_w [ceil(N / 128),

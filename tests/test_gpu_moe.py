@@ -350,6 +350,10 @@ def test_layer(awq, T, E, k, K, inner, bf16):
     want, tol = reference_layer(up, down, x.float().numpy(), ids.cpu().numpy(), host(weights), bf16)
     assert np.all(np.abs(host(out) - want) <= tol), np.max(np.abs(host(out) - want) / tol)
     assert torch.equal(out, awq.awq_moe(x.cuda(), w_up, w_down, weights, plan))
+    # the three calls that it is made of
+    h = awq.awq_moe_gemm(x.cuda(), w_up, plan, gather=True)
+    y = awq.awq_moe_gemm(h, w_down, plan, out_dtype=torch.float32)
+    assert torch.equal(out, awq.awq_moe_combine(y, plan, weights, dtype=x.dtype))
 
 
 def test_layer_in_a_graph_follows_the_routing(awq):
@@ -361,8 +365,7 @@ def test_layer_in_a_graph_follows_the_routing(awq):
         weights, _, plan = awq.awq_moe_route(logits, k)
         return awq.awq_moe(x, up, down, weights, plan, workspace=workspace)
 
-    need = max(awq.awq_moe_gemm_workspace_bytes(T * k, w) for w in (up, down))
-    ws = torch.zeros(max(need, 256), dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(awq.awq_moe_workspace_bytes(T, k, up, down), dtype=torch.uint8, device="cuda")
     pass_()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):

@@ -114,6 +114,27 @@ def test_combine_refusals(lib):
     assert call(T=0, y=None, place=None) == 0
 
 
+def test_layer_refusals(lib):
+    def call(x=FAKE, xs=256, up=FAKE, down=FAKE, offsets=FAKE, order=FAKE, place=FAKE, w=FAKE, res=FAKE, rs=320, out=FAKE, T=6,
+             k=2, E=4, K=256, inner=384, H=320, dtype=0, ws=FAKE, wsb=1 << 40):
+        return lib.awq_moe(x, xs, up, down, offsets, order, place, w, res, rs, out, T, k, E, K, inner, H, dtype, ws, wsb, None)
+
+    for bad in ({"xs": 248}, {"xs": 260}, {"rs": 312}, {"rs": 324}, {"T": -1}, {"T": 2 ** 29 + 1}, {"k": 0}, {"k": 33}, {"E": 0},
+                {"E": 513}, {"K": 250}, {"inner": 96}, {"inner": 0}, {"inner": 2 ** 62}, {"H": 300}, {"dtype": 3}):
+        assert call(**bad) == EINVAL, bad
+    for name in ("x", "up", "down", "offsets", "order", "place", "w", "out"):
+        assert call(**{name: None}) == ENULL, name
+    for name in ("x", "up", "down", "res", "out"):
+        assert call(**{name: OFF}) == EALIGN, name
+    for name in ("offsets", "order", "place", "w"):
+        assert call(**{name: FAKE + 2}) == EALIGN, name
+    assert call(T=0, x=None, out=None) == 0
+    need = lib.awq_moe_workspace_bytes(6, 2, 4, 256, 384, 320)
+    assert need >= lib.awq_moe_gemm_workspace_bytes(12, 4, 256, 768, 1) + 12 * 384 * 2 + 12 * 320 * 4
+    assert call(ws=None) == EWORKSPACE and call(wsb=need - 1) == EWORKSPACE and call(ws=FAKE + 16) == EALIGN
+    assert lib.awq_moe_workspace_bytes(6, 2, 4, 256, 100, 320) == 0
+
+
 def test_fp8_refusals(lib):
     q = lib.awq_fp8_quant_act  # x, stride, xq, s_x, M, K, dtype, stream
     for bad in ((4, 4100, 4104, 0), (4, 8, 8, 0), (-1, 64, 64, 0), (4, 64, 56, 0), (4, 64, 68, 0), (4, 64, 64, 2),

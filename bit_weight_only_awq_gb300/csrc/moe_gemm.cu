@@ -395,18 +395,27 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
     const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16) + G::kACol + 64 * G::kABufs * b;
     const int step = G::kSteps == 2 ? b : 0, c = b * 128 + n;
     int q = 0, buf = 0, count = 0;
-    uint32_t q_phase = 0;
+    uint32_t q_phase = 0, z = 0u;
+    uint16_t raw = 0;
+    uint4 w;
+    bool have = false;  // the first codes of the next group are in registers
+    auto start = [&]() {
+      const uint8_t* unit = smem + G::kQAt + q * kMoeUnitBytes;
+      w = lds128(sm + G::kQAt + q * kMoeUnitBytes + moe_code_offset(c, 0));
+      z = unit[kMoeZeroOffset + c / 2];
+      raw = *reinterpret_cast<const uint16_t*>(unit + kMoeScaleOffset + 2 * c);
+    };
     while (ok && walk.next(tile, g0, g1)) {
       for (int g = g0; g < g1; ++g, ++count) {
-        ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.q_full[q]), q_phase, abort_flag, err, 711));
-        if (!ok) break;
-        const uint8_t* unit = smem + G::kQAt + q * kMoeUnitBytes;
+        if (!have) {
+          ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.q_full[q]), q_phase, abort_flag, err, 711));
+          if (!ok) break;
+          start();
+        }
         const uint32_t codes = sm + G::kQAt + q * kMoeUnitBytes;
-        uint4 w = lds128(codes + moe_code_offset(c, 0));
-        const uint32_t z = unit[kMoeZeroOffset + c / 2] >> (4 * (c & 1)) & 15u;
-        const uint16_t raw = *reinterpret_cast<const uint16_t*>(unit + kMoeScaleOffset + 2 * c);
-        const float zf = (float)z * (-1.f / (1 << kDown<BF16>));
-        const uint32_t zz = pack2<BF16>(zf, zf);
+        const uint32_t zn = z >> (4 * (c & 1)) & 15u;
+        const uint32_t zz = fma16<BF16>(zn | zn << 16, BF16 ? 0xFE80FE80u : 0xF400F400u, 0u);  // -z 2^-kDown
+        const float scale = unpack2<BF16>(raw).x * (float)(1 << kDown<BF16>);
 #pragma unroll
         for (int chunk = 0; chunk < 4; ++chunk) {
           uint32_t o[16];
@@ -428,18 +437,21 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
         if (!ok) break;
         // Scales for the sums.  A slot is written again 8 groups later: the products of kABufs groups back are done, which
         // waited until the sums of the steps kSums before them had been taken out, their scales read.
-        reinterpret_cast<float*>(smem + G::kScaleAt)[count % kScaleSlots * 256 + c] = unpack2<BF16>(raw).x * (float)(1 << kDown<BF16>);
+        reinterpret_cast<float*>(smem + G::kScaleAt)[count % kScaleSlots * 256 + c] = scale;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars.q_empty[q]));  // all codes are in registers
+        if (++q == G::kQStages) {
+          q = 0;
+          q_phase ^= 1u;
+        }
+        // the next group's first codes, if they are there, while the stores arrive
+        have = g + 1 < g1 && __all_sync(0xFFFFFFFFu, mbar_try(smem_u32(&bars.q_full[q]), q_phase));
+        if (have) start();
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars.a_full[buf][step]));
         if (++buf == G::kABufs) buf = 0;
-        if (++q == G::kQStages) {
-          q = 0;
-          q_phase ^= 1u;
-        }
       }
     }
   } else {

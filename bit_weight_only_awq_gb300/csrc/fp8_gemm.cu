@@ -35,9 +35,6 @@ struct Geo {
   static constexpr int kBytes = kABytes + BT * 128;     // a stage: the lanes' operand | the columns'
   static constexpr int kStages = BT == 256 ? 4 : BT == 64 ? 8 : 11;
   static constexpr int kSums = BT == 256 ? 2 : 4;       // blocks whose sums are kept in tensor memory, BT columns each
-  // 256 columns are two halves with products and barriers of their own: the sums of one are taken out during the products of
-  // the other, and each has its own block of weights.
-  static constexpr int kHalves = BT == 256 ? 2 : 1, kHalf = BT / kHalves;
   // A factor's slot is written again when the products kStages before it are done; those waited for the sums kSums
   // further back to be taken out.
   static constexpr int kSlots = kStages + kSums;
@@ -45,8 +42,8 @@ struct Geo {
   static constexpr int kSumWarps = BT == 16 ? 4 : 16, kMmaWarp = kSumWarps;
   static constexpr int kSumThreads = kSumWarps * 32, kThreads = (kMmaWarp + 4) * 32;
   // registers of a thread: at launch, then by role (256 columns: 64 sums)
-  static constexpr int kLaunchRegs = BT == 16 ? 248 : 96, kSumRegs = BT == 16 ? 248 : BT == 64 ? 96 : 104,
-                       kOtherRegs = BT == 16 ? 248 : BT == 64 ? 96 : 64;
+  static constexpr int kLaunchRegs = BT == 16 ? 248 : 96, kSumRegs = BT == 16 ? 248 : BT == 64 ? 96 : 112,
+                       kOtherRegs = BT == 16 ? 248 : BT == 64 ? 96 : 32;
   static_assert(kSumThreads * kSumRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs && kThreads * kLaunchRegs <= 65536,
                 "no more than was launched with");
   static constexpr int kRows = BT / (kSumWarps / 4), kPairs = kRows / 2;  // columns of a summing thread, and pairs of them
@@ -58,7 +55,7 @@ struct Geo {
 
 template <int BT>
 struct Bars {
-  uint64_t full[Geo<BT>::kStages], done[Geo<BT>::kStages][Geo<BT>::kHalves], d_empty[Geo<BT>::kSums][Geo<BT>::kHalves], join, end;
+  uint64_t full[Geo<BT>::kStages], done[Geo<BT>::kStages], d_empty[Geo<BT>::kSums], join, end;
 };
 
 // The products of one block, 128 k in steps of 32, into a fresh sum.
@@ -109,9 +106,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_lanes, const __grid_const
     abort_word = 0;
     for (int i = 0; i < G::kStages; ++i) {
       mbar_init(smem_u32(&bars.full[i]), QUANT ? 3 : G::kTokenLanes ? 1 : 2);  // the copies and the factors
-      for (int h = 0; h < G::kHalves; ++h) mbar_init(smem_u32(&bars.done[i][h]), 1);
+      mbar_init(smem_u32(&bars.done[i]), 1);
     }
-    for (int i = 0; i < G::kSums * G::kHalves; ++i) mbar_init(smem_u32(&bars.d_empty[0][i]), G::kSumWarps / G::kHalves);
+    for (int i = 0; i < G::kSums; ++i) mbar_init(smem_u32(&bars.d_empty[i]), G::kSumWarps);
     mbar_init(smem_u32(&bars.join), G::kSumWarps);
     mbar_init(smem_u32(&bars.end), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -135,7 +132,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_lanes, const __grid_const
   if (warp < G::kSumWarps) {
     if constexpr (G::kSumRegs > G::kLaunchRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::kSumRegs));
     // ------------------------------------------------ running sums: lane n of D, columns kRows wg ..
-    const int wg = warp / 4, n = warp % 4 * 32 + lane, half = wg * G::kRows / G::kHalf;
+    const int wg = warp / 4, n = warp % 4 * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16) + G::kRows * wg;
     int d = 0, stage = 0, slot = 0;
     uint32_t phase = 0, join_phase = 0;
@@ -154,23 +151,23 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_lanes, const __grid_const
 #pragma unroll
       for (int i = 0; i < G::kPairs; ++i) acc[i] = F2(0.f, 0.f);
       // token lanes: the factor, read a block ahead
-      const float* s_x = a.s_x + min(t.lane + n, M - 1);
-      const float* s_w = a.s_w + (int64_t)min(t.col / 128 + half, (int)((a.N + 127) / 128) - 1) * blocks;
+      const float* s_x = a.s_x + (int64_t)g0 * a.M + min(t.lane + n, M - 1);
+      const float* s_w = a.s_w + (int64_t)min(t.col / 128 + wg * G::kRows / 128, (int)((a.N + 127) / 128) - 1) * blocks + g0;
       float next_x = 0.f, next_w = 0.f;
       if constexpr (G::kTokenLanes) {
-        next_x = s_x[(int64_t)g0 * a.M];
-        next_w = __ldg(s_w + g0);
+        next_x = *s_x;
+        next_w = __ldg(s_w);
       }
       for (int g = g0; g < g1 && ok; ++g) {
         const float f = next_x * next_w;
         const F2 f2(f, f);
         if constexpr (G::kTokenLanes) {
           if (g + 1 < g1) {
-            next_x = s_x[(int64_t)(g + 1) * a.M];
-            next_w = __ldg(s_w + g + 1);
+            next_x = *(s_x += a.M);
+            next_w = __ldg(++s_w);
           }
         }
-        ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.done[stage][half]), phase, abort_flag, err, 802));
+        ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.done[stage]), phase, abort_flag, err, 802));
         if (!ok) break;
         tc_fence_after();
         const uint32_t factors = sm + G::kFactorAt + (slot * BT + G::kRows * wg) * 4;
@@ -185,7 +182,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_lanes, const __grid_const
           if (c + 1 == G::kRows / 16) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars.d_empty[d][half]));  // the sum is in registers
+            if (lane == 0) mbar_arrive(smem_u32(&bars.d_empty[d]));  // the sum is in registers
           }
           if (any && G::kTokenLanes) {
 #pragma unroll
@@ -286,21 +283,16 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_lanes, const __grid_const
       uint32_t phase = 0, d_phase = 1;
       while (ok && walk.next(tile, g0, g1)) {
         const Tile t = find_tile<BT>(tile, m_tiles, a);
-        const int columns = (t.cols + 15) / 16 * 16;
-        for (int g = g0; g < g1 && ok; ++g) {
-          ok = wait_for(smem_u32(&bars.full[stage]), phase, abort_flag, err, 821);
-          const uint64_t at = desc0 + (uint64_t)((stage * G::kBytes) >> 4);
+        const uint32_t idesc = (1u << 4) | ((uint32_t)((t.cols + 15) / 16 * 2) << 17) | (8u << 24);  // e4m3 x e4m3, fp32 sums
 #pragma unroll 1
-          for (int h = 0; h < G::kHalves; ++h) {
-            ok = __all_sync(0xFFFFFFFFu, ok && wait_for(smem_u32(&bars.d_empty[d][h]), d_phase, abort_flag, err, 822));
-            if (!ok) break;
-            tc_fence_after();
-            const int some = min(columns - h * G::kHalf, G::kHalf);
-            const uint32_t idesc = (1u << 4) | ((uint32_t)(some / 8) << 17) | (8u << 24);  // e4m3 x e4m3, fp32 sums
-            if (some > 0)
-              mma_block(tmem + d * BT + h * G::kHalf, at, at + (uint64_t)((kABytes + h * G::kHalf * 128) >> 4), idesc);
-            commit(smem_u32(&bars.done[stage][h]));
-          }
+        for (int g = g0; g < g1; ++g) {
+          ok = wait_for(smem_u32(&bars.full[stage]), phase, abort_flag, err, 821);
+          ok = __all_sync(0xFFFFFFFFu, ok && wait_for(smem_u32(&bars.d_empty[d]), d_phase, abort_flag, err, 822));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t at = desc0 + (uint64_t)((stage * G::kBytes) >> 4);
+          mma_block(tmem + d * BT, at, at + (uint64_t)(kABytes >> 4), idesc);
+          commit(smem_u32(&bars.done[stage]));
           if (++d == G::kSums) {
             d = 0;
             d_phase ^= 1u;
@@ -323,7 +315,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_lanes, const __grid_const
           const Tile t = find_tile<BT>(tile, m_tiles, a);
           const int boxes = (t.cols + G::kBoxRows - 1) / G::kBoxRows;
           for (int g = g0; g < g1; ++g, ++count) {
-            ok = wait_for(smem_u32(&bars.done[stage][G::kHalves - 1]), phase, abort_flag, err, 831);
+            ok = wait_for(smem_u32(&bars.done[stage]), phase, abort_flag, err, 831);
             if (!ok) break;
             const uint32_t bar = smem_u32(&bars.full[stage]), to = sm + stage * G::kBytes;
             mbar_arrive_tx(bar, (uint32_t)(kABytes + (QUANT ? 0 : boxes * G::kBoxRows * 128)));
@@ -388,7 +380,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_lanes, const __grid_const
 #pragma unroll 1
           for (int j = 0; j < n && ok; ++j) {
             const int at = stage + j;
-            ok = wait_for(smem_u32(&bars.done[at < G::kStages ? at : at - G::kStages][0]), at < G::kStages ? phase : phase ^ 1u,
+            ok = wait_for(smem_u32(&bars.done[at < G::kStages ? at : at - G::kStages]), at < G::kStages ? phase : phase ^ 1u,
                           abort_flag, err, 842);
           }
           ok = __all_sync(0xFFFFFFFFu, ok);
@@ -445,7 +437,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_lanes, const __grid_const
               ok = false;
               break;
             }
-            ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.done[stage][G::kHalves - 1]), phase, abort_flag, err, 841));
+            ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.done[stage]), phase, abort_flag, err, 841));
             if (!ok) break;
 #pragma unroll
             for (int i = 0; i < kEach; ++i)

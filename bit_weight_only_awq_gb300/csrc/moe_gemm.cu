@@ -10,10 +10,12 @@
 //   memory.  Weights in shared memory would cost it 192 bytes a cycle at the full rate of the products; so it moves
 //   64 (the operand B) and what the copies bring.
 // Roles: the first warps add the groups' sums up and write results (a thread has one column of each half and some rows: gate and
-// up of a gated layer meet in it), eight warps turn codes into operands (a thread has a column), then come a warp that issues the
+// up of a gated layer meet in it), eight warps turn codes into operands (a thread has a column), then come those that issue the
 // products, one that copies weights (one 17 KB unit a group) and one that copies rows of x.
 // Sums and operands in tensor memory go round, so that the products need not wait for either.  A step of the products is a half
-// of a group in tiles of 128 rows and a whole group in smaller ones; whoever waits for its products waits on one barrier.
+// of a group in tiles of 128 rows, each half's issued by a warp of its own (one warp for both: 1530 and 706 us for gate and up, and
+// down, of 8192 rows over 8 experts, against 1440 and 668), and a whole group in smaller ones, by one warp (two: 147 and 81 us
+// for 192 rows, against 130 and 76); whoever waits for its products waits on one barrier.
 // Rows of x come in any order.  Up to 16 of them are copied four an instruction (tile::gather4, about 30 cycles each); more,
 // 32 KB a group with 128, are put in order first and copied in boxes of neighbouring rows (at 32008 rows over 126 experts
 // 484 us with four rows an instruction, 406 with 16 bytes a thread, 273 without any copies, each on that day's kernel).
@@ -44,8 +46,8 @@ template <int BT>
 struct Geo {
   static constexpr int kSteps = BT == 128 ? 2 : 1;       // steps of a group, each of 2 / kSteps halves
   static constexpr int kSumCols = BT * 2 / kSteps;       // columns of a step's sums
-  static constexpr int kSums = BT == 16 ? 4 : 2;         // steps whose sums are kept in tensor memory
-  static constexpr int kACol = kSums * kSumCols;         // operands come behind them: [half][buffer] of 64 columns (128 k)
+  static constexpr int kSums = BT == 16 ? 4 : BT == 64 ? 2 : 1;  // groups whose sums are kept in tensor memory
+  static constexpr int kACol = kSums * kSteps * kSumCols;  // operands come behind them: [half][buffer] of 64 columns (128 k)
   static constexpr int kABufs = BT == 16 ? 3 : 2;        // groups whose operands are kept
   static constexpr int kXBytes = BT * 256;               // a group's rows: two blocks of 64 k, 128 bytes a row, swizzled
   static constexpr bool kBoxes = BT > 16;                // rows in order, copied in boxes; else four rows in any order at once
@@ -68,14 +70,15 @@ struct Geo {
   // a CTA's part of a shared tile: a sum for each of a summing thread's columns and rows
   static constexpr size_t kPartBytes = (size_t)256 * BT * 4;
   static_assert(kACol + 2 * kABufs * 64 <= 512 && kSmem <= 227 * 1024 - 1024, "tensor memory, shared memory");
-  static_assert(kABufs <= kRing && kSums <= kRing * kSteps, "barriers of products");
-  static_assert(kScaleSlots >= kABufs + kSums / kSteps + 1, "scales");
+  static_assert(kABufs <= kRing && kSums <= kRing, "barriers of products");
+  static_assert(kBoxes || kSteps == 1, "rows copied four at a time wait for one step's products");
+  static_assert(kScaleSlots >= kABufs + kSums + 1, "scales");
 };
 
 template <int BT>
 struct Bars {
   uint64_t x_full[kRing], q_full[Geo<BT>::kQStages], q_empty[Geo<BT>::kQStages],
-      a_full[Geo<BT>::kABufs][Geo<BT>::kSteps], done[kRing][Geo<BT>::kSteps], d_empty[Geo<BT>::kSums], join, end;
+      a_full[Geo<BT>::kABufs][Geo<BT>::kSteps], done[kRing][Geo<BT>::kSteps], d_empty[Geo<BT>::kSums][Geo<BT>::kSteps], join, end;
 };
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -223,9 +226,9 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
       mbar_init(smem_u32(&bars.q_empty[i]), 8);
     }
     for (int i = 0; i < G::kABufs * G::kSteps; ++i) mbar_init(smem_u32(&bars.a_full[0][i]), 8 / G::kSteps);
-    for (int i = 0; i < G::kSums; ++i) mbar_init(smem_u32(&bars.d_empty[i]), G::kSumWarps);
+    for (int i = 0; i < G::kSums * G::kSteps; ++i) mbar_init(smem_u32(&bars.d_empty[0][i]), G::kSumWarps);
     mbar_init(smem_u32(&bars.join), G::kSumWarps);
-    mbar_init(smem_u32(&bars.end), 1);
+    mbar_init(smem_u32(&bars.end), G::kSteps);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -263,10 +266,10 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
     };
     // a sum is in registers
     if (a.early) wait_then_release_dependents();
-    auto take = [&]() {
+    auto take = [&](int step) {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars.d_empty[d]));
+      if (lane == 0) mbar_arrive(smem_u32(&bars.d_empty[d][step]));
     };
     while (ok && walk.next(tile, g0, g1)) {
       const Tile t = find_tile<BT>(first, items, a.experts, pairs, tile);
@@ -288,7 +291,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
             const int b = G::kSteps == 2 ? step : bb;
             const float s = scales[count % kScaleSlots * 256 + b * 128 + n];
             const F2 s2(s, s);
-            const uint32_t from = lanes + d * G::kSumCols + bb * BT;
+            const uint32_t from = lanes + (d * G::kSteps + step) * G::kSumCols + bb * BT;
 #pragma unroll
             for (int c = 0; c < G::kRows / 16; c += G::kAtOnce) {
               uint32_t v[G::kAtOnce][16];
@@ -299,7 +302,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
 #pragma unroll
                 for (int h = 0; h < G::kAtOnce; ++h) wait_loaded(v[h]);
               }
-              if (bb == 2 / G::kSteps - 1 && c + G::kAtOnce == G::kRows / 16) take();
+              if (bb == 2 / G::kSteps - 1 && c + G::kAtOnce == G::kRows / 16) take(step);
               if (any) {
 #pragma unroll
                 for (int h = 0; h < G::kAtOnce; ++h)
@@ -311,8 +314,8 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
               }
             }
           }
-          if (++d == G::kSums) d = 0;
         }
+        if (++d == G::kSums) d = 0;
       }
       if (!ok) break;
       if (g0 > 0) {
@@ -456,8 +459,9 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
     }
   } else {
     if constexpr (G::kOtherRegs < G::kLaunchRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kOtherRegs));
-    if (warp == G::kMmaWarp) {
-      // ------------------------------------------------ products
+    if (warp < G::kMmaWarp + G::kSteps) {
+      // ------------------------------------------------ products of a step; each step's warp has sums of its own
+      const int step = warp - G::kMmaWarp;
       const uint64_t bdesc0 = smem_desc_sw128(sm, 16, 1024);
       int d = 0, buf = 0, count = 0;
       uint32_t d_phase = 1, a_phase = 0;
@@ -465,25 +469,23 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
         const Tile t = find_tile<BT>(first, items, a.experts, pairs, tile);
         const uint32_t idesc = (1u << 4) | (BF16 ? (1u << 7) | (1u << 10) : 0u) | ((uint32_t)((t.rows + 15) / 16 * 2) << 17) |
                                (8u << 24);
-        for (int g = g0; g < g1 && ok; ++g, ++count) {
+#pragma unroll 1
+        for (int g = g0; g < g1; ++g, ++count) {
           const int x = count % kRing;
           ok = wait_for(smem_u32(&bars.x_full[x]), (uint32_t)(count / kRing) & 1u, abort_flag, err, 721);
+          ok = __all_sync(0xFFFFFFFFu, ok && wait_for(smem_u32(&bars.d_empty[d][step]), d_phase, abort_flag, err, 722) &&
+                                           wait_for(smem_u32(&bars.a_full[buf][step]), a_phase, abort_flag, err, 723));
+          if (!ok) break;
+          tc_fence_after();
           const uint64_t bd = bdesc0 + (uint64_t)((x * G::kXBytes) >> 4);
-#pragma unroll 1
-          for (int step = 0; step < G::kSteps; ++step) {
-            ok = __all_sync(0xFFFFFFFFu, ok && wait_for(smem_u32(&bars.d_empty[d]), d_phase, abort_flag, err, 722) &&
-                                             wait_for(smem_u32(&bars.a_full[buf][step]), a_phase, abort_flag, err, 723));
-            if (!ok) break;
-            tc_fence_after();
 #pragma unroll
-            for (int bb = 0; bb < 2 / G::kSteps; ++bb)
-              mma_group(tmem + d * G::kSumCols + bb * BT, tmem + G::kACol + 64 * (G::kABufs * (step + bb) + buf), bd,
-                        bd + (uint64_t)(G::kXBytes >> 5), idesc);
-            commit(smem_u32(&bars.done[x][step]));
-            if (++d == G::kSums) {
-              d = 0;
-              d_phase ^= 1u;
-            }
+          for (int bb = 0; bb < 2 / G::kSteps; ++bb)
+            mma_group(tmem + (d * G::kSteps + step) * G::kSumCols + bb * BT, tmem + G::kACol + 64 * (G::kABufs * (step + bb) + buf), bd,
+                      bd + (uint64_t)(G::kXBytes >> 5), idesc);
+          commit(smem_u32(&bars.done[x][step]));
+          if (++d == G::kSums) {
+            d = 0;
+            d_phase ^= 1u;
           }
           if (++buf == G::kABufs) {
             buf = 0;
@@ -491,10 +493,10 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
           }
         }
       }
-      commit(smem_u32(&bars.end));  // arrives once every product has completed
+      commit(smem_u32(&bars.end));  // arrives once every product of this warp has completed
       volatile int no_abort = 0;
       wait_for(smem_u32(&bars.end), 0, &no_abort, err, 724);
-    } else if (warp == G::kMmaWarp + 1) {
+    } else if (warp == G::kMmaWarp + G::kSteps) {
       // ------------------------------------------------ copies of weights
       if (lane == 0) {
         int q = 0, issued = 0;
@@ -521,7 +523,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
       }
     } else if constexpr (G::kBoxes) {
       // ------------------------------------------------ copies of rows, boxes of 32 rows x 64 k
-      if (warp == G::kMmaWarp + 2 && lane == 0) {
+      if (warp == G::kMmaWarp + G::kSteps + 1 && lane == 0) {
         if (a.early) asm volatile("griddepcontrol.wait;" ::: "memory");
         int count = 0;
         while (ok && walk.next(tile, g0, g1)) {
@@ -530,7 +532,8 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
           for (int g = g0; g < g1; ++g, ++count) {
             const int x = count % kRing;
             if (count >= kRing) {
-              ok = wait_for(smem_u32(&bars.done[x][G::kSteps - 1]), (uint32_t)(count / kRing - 1) & 1u, abort_flag, err, 743);
+              for (int h = 0; h < G::kSteps && ok; ++h)
+                ok = wait_for(smem_u32(&bars.done[x][h]), (uint32_t)(count / kRing - 1) & 1u, abort_flag, err, 743);
               if (!ok) break;
             }
             const uint32_t bar = smem_u32(&bars.x_full[x]);
@@ -546,7 +549,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
         for (int j = max(0, count - kRing); j < count; ++j)
           wait_for(smem_u32(&bars.x_full[j % kRing]), (uint32_t)(j / kRing) & 1u, &no_abort, err, 744);
       }
-    } else if (warp == G::kMmaWarp + 2) {
+    } else if (warp == G::kMmaWarp + G::kSteps + 1) {
       // ------------------------------------------------ copies of rows: lane l has rows 4 l .. 4 l + 3
       int count = 0;
       if (a.early) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -559,8 +562,8 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
         for (int g = g0; g < g1; ++g, ++count) {
           const int x = count % kRing;
           if (count >= kRing) {
-            ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.done[x][G::kSteps - 1]), (uint32_t)(count / kRing - 1) & 1u,
-                                                  abort_flag, err, 741));
+            ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.done[x][0]), (uint32_t)(count / kRing - 1) & 1u, abort_flag, err,
+                                                  741));
             if (!ok) break;
           }
           const uint32_t bar = smem_u32(&bars.x_full[x]), dst = sm + x * G::kXBytes + lane * 512;

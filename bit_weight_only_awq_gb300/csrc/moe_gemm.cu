@@ -57,8 +57,8 @@ struct Geo {
   static constexpr int kCodeWarp = kSumWarps, kMmaWarp = kCodeWarp + 8;
   static constexpr int kSumThreads = kSumWarps * 32, kThreads = (kMmaWarp + 4) * 32;
   // registers of a thread: at launch, then by role
-  static constexpr int kLaunchRegs = BT == 16 ? 128 : 96, kSumRegs = BT == 16 ? 128 : BT == 64 ? 128 : 168,
-                       kCodeRegs = BT == 16 ? 128 : BT == 64 ? 72 : 56, kOtherRegs = BT == 16 ? 128 : BT == 64 ? 72 : 32;
+  static constexpr int kLaunchRegs = BT == 16 ? 128 : 96, kSumRegs = BT == 16 ? 128 : BT == 64 ? 128 : 176,
+                       kCodeRegs = BT == 16 ? 128 : BT == 64 ? 72 : 48, kOtherRegs = BT == 16 ? 128 : BT == 64 ? 72 : 32;
   static_assert(kSumThreads * kSumRegs + 256 * kCodeRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs &&
                 kThreads * kLaunchRegs <= 65536, "no more than was launched with");
   // shared memory: rows of x | units | scales | expert tables

@@ -273,6 +273,37 @@ def test_gemm_with_offsets_that_make_no_sense_stays_in_bounds(awq):
         assert (out[20:] == 7.0).all() and awq.awq_last_device_error() == 0
 
 
+def test_gemm_and_combine_beyond_32_bits(awq):
+    """More than 2^31 elements of y: the last rows are those of a call of their own."""
+    E, K, N, rows = 2, 128, 8192, 270000
+    w = Experts(E, K, N, seed=1).pack(awq)
+    x = torch.randn(rows, K, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").half()
+
+    def plan_of(*counts):
+        offsets = torch.tensor([0, counts[0], sum(counts)], dtype=torch.int32, device="cuda")
+        order = torch.arange(sum(counts), dtype=torch.int32, device="cuda")
+        return awq.MoePlan(offsets, order, order, 1)
+
+    y = awq.awq_moe_gemm(x, w, plan_of(1000, rows - 1000), out_dtype=torch.float32)
+    last = awq.awq_moe_gemm(x[-300:].contiguous(), w, plan_of(0, 300), out_dtype=torch.float32)
+    assert y.numel() > 2 ** 31 and torch.equal(y[-300:], last)
+    ones = torch.ones(rows, 1, device="cuda")
+    out = awq.awq_moe_combine(y, plan_of(1000, rows - 1000), ones, dtype=torch.float16)
+    assert torch.equal(out[-300:], last.half())
+
+
+def test_choices_of_one_expert_twice(awq):
+    """A router of one's own may choose an expert twice for a token: two rows, added up."""
+    p = Experts(3, 128, 64, seed=1)
+    ids = dev(np.array([[2, 2], [0, 2]], np.int32))
+    plan = awq.awq_moe_plan(ids, 3)
+    x = dev16(np.random.default_rng(1).normal(size=(2, 128)), False)
+    y = awq.awq_moe_gemm(x, p.pack(awq), plan, gather=True)
+    assert torch.equal(y[1], y[2])
+    out = awq.awq_moe_combine(y, plan, torch.full((2, 2), 0.5, device="cuda"))
+    assert torch.equal(out[0], y[1])
+
+
 # ---- combination
 
 @pytest.mark.parametrize("T,k,H", [(1, 1, 8), (3, 2, 64), (70, 8, 520), (33, 5, 4096), (5, 32, 16)])
@@ -382,6 +413,32 @@ def test_layer_in_a_graph_follows_the_routing(awq):
         with torch.cuda.graph(torch.cuda.CUDAGraph()):
             pass_()
     torch.cuda.synchronize()
+    assert awq.awq_last_device_error() == 0
+
+
+def test_two_graphs_of_the_layer_at_once(awq):
+    """Captured calls have workspaces of their own: their graphs may run side by side."""
+    T, E, k, K, inner = 24, 8, 2, 512, 256
+    up, down = Experts(E, K, 2 * inner, seed=1).pack(awq, True), Experts(E, inner, K, seed=2).pack(awq)
+    xs = [torch.randn(T, K, generator=torch.Generator(device="cuda").manual_seed(i), device="cuda").half() for i in range(2)]
+    logits = torch.randn(T, E, generator=torch.Generator(device="cuda").manual_seed(9), device="cuda")
+    weights, _, plan = awq.awq_moe_route(logits, k)
+    want = [awq.awq_moe(x, up, down, weights, plan) for x in xs]
+    graphs, outs, spaces = [], [], []
+    for x in xs:
+        spaces.append(torch.zeros(awq.awq_moe_workspace_bytes(T, k, up, down), dtype=torch.uint8, device="cuda"))
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(awq.awq_moe(x, up, down, weights, plan, workspace=spaces[-1]))
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(5):
+        torch.cuda.synchronize()
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        awq.awq_moe(xs[0], up, down, weights, plan)  # and the shared workspace's call beside them
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
     assert awq.awq_last_device_error() == 0
 
 

@@ -36,8 +36,8 @@ struct Geo {
   static constexpr int kStages = BT == 256 ? 4 : BT == 64 ? 8 : 11;
   static constexpr int kSums = BT == 256 ? 2 : 4;       // blocks whose sums are kept in tensor memory, BT columns each
   // A factor's slot is written again when the products kStages before it are done; those waited for the sums kSums
-  // further back to be taken out.
-  static constexpr int kSlots = kStages + kSums;
+  // further back to be taken out, and the factors of the block before these had been read by then.
+  static constexpr int kSlots = kStages + kSums + 1;
   static constexpr int kBoxRows = BT < 64 ? BT : 64;
   static constexpr int kSumWarps = BT == 16 ? 4 : 16, kMmaWarp = kSumWarps;
   static constexpr int kSumThreads = kSumWarps * 32, kThreads = (kMmaWarp + 4) * 32;
@@ -328,10 +328,10 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_lanes, const __grid_const
             }
           }
         }
-        // never leave the CTA with copies in flight
+        // never leave the CTA with copies in flight; one limit is enough for all, where factors are missing after an abort
         volatile int no_abort = 0;
         for (int j = max(0, count - G::kStages); j < count; ++j)
-          wait_for(smem_u32(&bars.full[j % G::kStages]), (uint32_t)(j / G::kStages) & 1u, &no_abort, err, 832);
+          if (!wait_for(smem_u32(&bars.full[j % G::kStages]), (uint32_t)(j / G::kStages) & 1u, &no_abort, err, 832)) break;
       }
     } else if constexpr (!G::kTokenLanes) {
       // ------------------------------------------------ factors s_x s_w of a block's tokens, and the codes if need be

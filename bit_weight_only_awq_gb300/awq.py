@@ -714,7 +714,19 @@ class MoePlan:
     [R], `place` int32 [R], with R = tokens * top_k; the tensors that include/awq.h describes."""
 
     def __init__(self, offsets: torch.Tensor, order: torch.Tensor, place: torch.Tensor, top_k: int):
+        for t in (offsets, order, place):
+            if t.dtype is not torch.int32 or t.dim() != 1 or not t.is_contiguous():
+                raise TypeError("MoePlan: offsets, order and place are dense vectors of int32")
+        if offsets.shape[0] < 2 or place.shape != order.shape or top_k < 1 or order.shape[0] % top_k:
+            raise ValueError("MoePlan: offsets [experts + 1], order and place [tokens * top_k]")
         self.offsets, self.order, self.place, self.top_k = offsets, order, place, top_k
+
+    @classmethod
+    def _of(cls, offsets, order, place, top_k) -> "MoePlan":
+        """From parts of one buffer, which need no checks."""
+        plan = cls.__new__(cls)
+        plan.offsets, plan.order, plan.place, plan.top_k = offsets, order, place, top_k
+        return plan
 
     @property
     def rows(self) -> int:
@@ -740,7 +752,7 @@ def awq_moe_plan(ids: torch.Tensor, experts: int, stream=None) -> MoePlan:
     order = at + 4 * (experts + 1)
     _check("awq_moe_plan", lib.awq_moe_plan(ids.data_ptr(), rows, experts, at, order, order + 4 * rows,
                                             _raw_stream(stream, device)))
-    return MoePlan(*buf.split_with_sizes((experts + 1, rows, rows)), top_k)
+    return MoePlan._of(*buf.split_with_sizes((experts + 1, rows, rows)), top_k)
 
 
 _LOGITS = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
@@ -765,13 +777,17 @@ def awq_moe_route(logits: torch.Tensor, top_k: int, normalize: bool = True, stre
         logits.data_ptr(), _row_stride("awq_moe_route", logits, experts), T, experts, top_k, int(normalize), kind, ids,
         weights.data_ptr(), ids + 12 * rows, ids + 4 * rows, ids + 8 * rows, _raw_stream(stream, device)))
     ids, order, place, offsets = buf.split_with_sizes((rows, rows, rows, experts + 1))
-    return weights, ids.view(T, top_k), MoePlan(offsets, order, place, top_k)
+    return weights, ids.view(T, top_k), MoePlan._of(offsets, order, place, top_k)
 
 
 class MoeWeights:
     """Prepared weights of a layer's experts (awq_moe_prepack): the device bytes, the sizes and the scales' type."""
 
     def __init__(self, data: torch.Tensor, experts: int, K: int, N: int, gated: bool, dtype: torch.dtype):
+        if data.dtype is not torch.uint8 or dtype not in _DTYPES or not data.is_contiguous():
+            raise TypeError("MoeWeights: dense uint8 bytes, scales of fp16 or bf16")
+        if data.numel() == 0 or data.numel() != lib.awq_moe_prepacked_bytes(experts, K, N, int(gated)):
+            raise ValueError("MoeWeights: the bytes are not those of a prepared layer of this size")
         self.data, self.experts, self.K, self.N, self.gated, self.dtype = data, experts, K, N, gated, dtype
 
     @property

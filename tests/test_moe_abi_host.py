@@ -168,6 +168,27 @@ def test_fp8_refusals(lib):
 
 # ---- the oracle
 
+def test_plans_and_weights_of_other_sizes_are_refused(lib):
+    import torch
+    from bit_weight_only_awq_gb300 import awq
+    i32 = lambda n: torch.zeros(n, dtype=torch.int32)
+    assert awq.MoePlan(i32(5), i32(6), i32(6), 2).rows == 6
+    for bad in ((i32(5).long(), i32(6), i32(6), 2), (i32(5), i32(12)[::2], i32(6), 2), (i32(5), i32(6), i32((6, 1)), 2)):
+        with pytest.raises(TypeError):
+            awq.MoePlan(*bad)
+    for bad in ((i32(1), i32(6), i32(6), 2), (i32(5), i32(6), i32(5), 2), (i32(5), i32(6), i32(6), 4), (i32(5), i32(6), i32(6), 0)):
+        with pytest.raises(ValueError):
+            awq.MoePlan(*bad)
+    data = torch.zeros(2 * 17024, dtype=torch.uint8)
+    assert awq.MoeWeights(data, 2, 128, 256, True, torch.float16).outputs == 128
+    for bad in ((data, 2, 256, 256, False), (data[:-1], 2, 128, 256, False), (data[:0], 2, 128, 100, False)):
+        with pytest.raises(ValueError):
+            awq.MoeWeights(*bad, torch.float16)
+    for bad in ((data.char(), torch.float16), (data, torch.float32)):
+        with pytest.raises(TypeError):
+            awq.MoeWeights(bad[0], 2, 128, 256, False, bad[1])
+
+
 def test_oracle_plan_and_route_by_hand():
     offsets, order, place = layer.plan([[2, 0], [0, 9], [2, -1]], 3)
     assert offsets.tolist() == [0, 2, 2, 4] and order.tolist() == [1, 2, 0, 4, -1, -1] and place.tolist() == [2, 0, 1, -1, 3, -1]

@@ -47,7 +47,8 @@ struct Geo {
   static_assert(kSumThreads * kSumRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs && kThreads * kLaunchRegs <= 65536,
                 "no more than was launched with");
   static constexpr int kRows = BT / (kSumWarps / 4), kPairs = kRows / 2;  // columns of a summing thread, and pairs of them
-  static constexpr int kFactorAt = kStages * kBytes, kSmem = kFactorAt + (kTokenLanes ? 0 : kSlots * BT * 4) + 1024;
+  // behind the stages: factors, or for token lanes 2 KB of each summing warp, through which rows of results leave
+  static constexpr int kFactorAt = kStages * kBytes, kSmem = kFactorAt + (kTokenLanes ? kSumWarps * 2048 : kSlots * BT * 4) + 1024;
   static constexpr int kTmem = kSums * BT < 64 ? 64 : kSums * BT;
   static constexpr size_t kPartBytes = (size_t)kLanes * BT * 4;
   static_assert(kSmem <= 227 * 1024 - 1024 && kTmem <= 512, "shared memory, tensor memory");
@@ -248,14 +249,28 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_lanes, const __grid_const
           for (int q = walk.me + 1 + lane; q < last; q += 32) atomicExch(flags + q, 0);
       }
       if constexpr (G::kTokenLanes) {
-        const int m = t.lane + n;
-        uint16_t* p = a.y + (int64_t)m * a.N + t.col + G::kRows * wg;
+        // 32 columns of the warp's 32 tokens at once go through shared memory, so that four lanes write 64 bytes of a row
+        // (each lane its own row's 16 bytes: TODO).  16-byte piece c of row r is at c ^ (r / 2) % 4: no bank conflicts.
+        uint8_t* own = smem + G::kFactorAt + warp * 2048;
+        const int row = lane / 4, piece = lane % 4, m = t.lane + warp % 4 * 32 + row;
+        uint16_t* p = a.y + (int64_t)m * a.N + t.col + G::kRows * wg + 8 * piece;
 #pragma unroll
-        for (int i = 0; i < G::kPairs; i += 4) {
-          uint32_t w[4];
+        for (int h = 0; h < G::kRows / 32; ++h) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) w[j] = pack2<BF16>(acc[i + j].get().x, acc[i + j].get().y);
-          if (m < M && 2 * i < mine) *reinterpret_cast<uint4*>(p + 2 * i) = make_uint4(w[0], w[1], w[2], w[3]);  // N % 8 == 0
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = pack2<BF16>(acc[16 * h + 4 * i + j].get().x, acc[16 * h + 4 * i + j].get().y);
+            *reinterpret_cast<uint4*>(own + lane * 64 + ((i ^ (lane / 2 & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4*>(own + (row + 8 * i) * 64 + ((piece ^ (row / 2 & 3)) << 4));
+            if (m + 8 * i < M && 32 * h + 8 * piece < mine)  // N % 8 == 0
+              *reinterpret_cast<uint4*>(p + (int64_t)(8 * i) * a.N + 32 * h) = v;
+          }
+          __syncwarp();
         }
       } else {
         // Two neighbouring lanes swap one of a pair of tokens each, so that a lane writes two outputs of one token.

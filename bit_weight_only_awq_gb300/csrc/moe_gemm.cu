@@ -197,7 +197,7 @@ __device__ __forceinline__ int source_row(const MoeGemmArgs& a, int row) {
   return src >= 0 && src < a.x_rows ? src : 0;
 }
 
-__device__ __forceinline__ float silu_times(float gate, float up) { return __fdividef(gate, 1.f + expf(-gate)) * up; }
+__device__ __forceinline__ float silu_times(float gate, float up) { return __fdividef(gate, 1.f + __expf(-gate)) * up; }
 
 template <int BT, bool BF16, bool GATED, bool WIDE>
 __global__ void __launch_bounds__(Geo<BT>::kThreads, 1)
@@ -359,35 +359,43 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
         if (warp == 0)
           for (int q = walk.me + 1 + lane; q < last; q += 32) atomicExch(flags + q, 0);
       }
+      // Two neighbouring lanes swap one of a pair of rows each, so that a lane writes two columns of one row.  Whether a column
+      // exists is the same for all lanes: there are multiples of 32.
       const int64_t outs = GATED ? a.N / 2 : a.N;
+      const bool odd = lane & 1;
+      using Out = typename std::conditional<WIDE, float2, uint32_t>::type;
 #pragma unroll
       for (int b = 0; b < (GATED ? 1 : 2); ++b) {
         const int64_t col = GATED ? (int64_t)t.pair * 128 + n : (int64_t)t.pair * 256 + b * 128 + n;
-        using Out = typename std::conditional<WIDE, float, uint16_t>::type;
-        Out* p = static_cast<Out*>(a.y) + (int64_t)(t.row + G::kRows * wg) * outs + col;
+        Out* p = static_cast<Out*>(a.y) + ((int64_t)(t.row + G::kRows * wg + odd) * outs + col - odd) / 2;
         const int rows = col < outs ? mine : 0;
 #pragma unroll
-        for (int i = 0; i < G::kPairs; ++i) {
-          float2 v = acc[b][i].get();
-          if constexpr (GATED) {
-            const float2 u = acc[1][i].get();
-            if (2 * i < rows) {
-              v.x = silu_times(v.x, u.x);
-              v.y = silu_times(v.y, u.y);
+        for (int c = 0; c < G::kPairs; c += 4) {
+          if (2 * c >= rows) break;
+          // eight rows at once, those beyond the tile's among them: one after another, each waits for its exponential
+          float2 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            v[i] = acc[b][c + i].get();
+            if constexpr (GATED) {
+              const float2 u = acc[1][c + i].get();
+              v[i] = make_float2(silu_times(v[i].x, u.x), silu_times(v[i].y, u.y));
             }
           }
-          const uint32_t w = pack2<BF16>(v.x, v.y);
-          if (2 * i < rows) {
-            if constexpr (WIDE) *p = v.x;
-            else *p = (uint16_t)w;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            Out w;
+            if constexpr (WIDE) {
+              const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[i].x : v[i].y, 1);
+              w = odd ? make_float2(got, v[i].y) : make_float2(v[i].x, got);
+            } else {
+              const uint32_t own = pack2<BF16>(v[i].x, v[i].y), got = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
+              w = __byte_perm(own, got, odd ? 0x3276 : 0x5410);
+            }
+            if (2 * (c + i) + odd < rows) *p = w;
+            p += outs;
+            asm volatile("" : "+l"(p));  // one address at a time, not all made ahead
           }
-          p += outs;
-          if (2 * i + 1 < rows) {
-            if constexpr (WIDE) *p = v.y;
-            else *p = (uint16_t)(w >> 16);
-          }
-          p += outs;
-          asm volatile("" : "+l"(p));  // one address at a time, not all made ahead
         }
       }
     }

@@ -844,7 +844,7 @@ awq_status awq_fp8_linear(const uint16_t* x, int64_t x_stride, const uint8_t* wq
   float* s_x = reinterpret_cast<float*>(xq + align256((size_t)M * (size_t)K));
   const cudaStream_t s = (cudaStream_t)stream;
   const bool bf16 = dtype == AWQ_BF16;
-  if (M <= kFp8FewTokens)
+  if (M <= kFp8FusedTokens)
     return from_cuda(launch_fp8_gemm(Fp8GemmArgs{x, x_stride, nullptr, nullptr, wq, s_w, y, M, K, N}, bf16, workspace, err, s));
   if (launch_fp8_quant(x, x_stride, xq, s_x, M, K, bf16, s) != cudaSuccess) return AWQ_ECUDA;
   return from_cuda(launch_fp8_gemm(Fp8GemmArgs{nullptr, 0, xq, s_x, wq, s_w, y, M, K, N}, bf16, workspace, err, s));

@@ -246,7 +246,9 @@ cudaError_t launch_moe_gemm(const MoeGemmArgs& a, bool gated, bool wide, bool bf
 // ---- e4m3 linear layers with scales for blocks of 128 (fp8_quant.cu, fp8_gemm.cu)
 cudaError_t launch_fp8_quant(const uint16_t* x, int64_t x_stride, uint8_t* xq, float* s_x, int64_t M, int64_t K, bool bf16,
                              cudaStream_t s);
-constexpr int kFp8FewTokens = 16;  // up to these the product quantizes its activations itself
+// Up to these the product quantizes its activations itself (4096 x 6144: 11.0 us against 12.6 for one token, 11.8 against 12.6
+// for two, 16.7 against 12.6 for three: every CTA quantizes all of them).
+constexpr int kFp8FusedTokens = 2;
 struct Fp8GemmArgs {
   const uint16_t* x;  // 16-bit activations of few tokens; nullptr: codes and scales are given
   int64_t x_stride;

@@ -5,14 +5,20 @@
 // two scales and added to the running sum in fp32 registers.
 //
 // Two forms of tcgen05.mma kind::f8f6f4, both operands K-major in shared memory:
-//   up to 64 tokens, D[output][token]: 128 outputs x up to 16 or 64 tokens; a column's factor s_x s_w is one of these numbers in
+//   few tokens, or so many that tiles of 64 suffice, D[output][token]: 128 outputs x up to 16 or 64 tokens; a column's factor s_x s_w is one of these numbers in
 //     shared memory, the same for all lanes;
 //   more tokens, D[token][output]: 128 tokens x 256 outputs; a lane has a token, whose factor is one register (the first form with
-//     256 tokens spent its time on loading factors: 574 us against TODO for 4096 tokens through 4096 x 28672).
+//     256 tokens spent its time on loading factors: 574 us against 460 for 4096 tokens through 4096 x 28672).
 // Roles: the first warps add up and write results (a thread has a lane of D and some of its columns), then come a warp that issues
-// the products, one that copies the operands (128 bytes of a row a block) and two that make the first form's factors, or with up to
-// 16 tokens given in 16 bits the codes too: a layer of few tokens is one launch.  The persistent grid and sums that cross CTAs are
+// the products, one that copies the operands (128 bytes of a row a block) and two that make the first form's factors, or for one or
+// two tokens given in 16 bits the codes too: such a layer is one launch.  The persistent grid and sums that cross CTAs are
 // those of the grouped product.
+//
+// Measured: 4096 tokens through 4096 x 28672 in 399 us, 2410 TFLOP/s.  A block's products take 517 cycles, the sums of its 128 x 256
+// numbers by 16 warps about 570, its 48 KB of operands 768 at 64 bytes a cycle; all three at once 1020.  None of them alone is
+// the limit: without the sums 362 us, without the copies 375, without the stores 378; without all three and the products 245,
+// the barriers' round trips between the roles.  48 tokens through 14336 x 4096: 20 us, 3 TB/s, bound by those round trips too;
+// one token through 4096 x 6144: 11 us, of which 3.7 are its bytes.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -28,7 +34,7 @@ namespace {
 
 constexpr int kLanes = 128, kABytes = kLanes * 128;  // lanes of D; bytes of a block of their operand
 
-// BT: columns of D, tokens up to 64, outputs at 256.
+// BT: columns of D, tokens at 16 and 64, outputs at 256.
 template <int BT>
 struct Geo {
   static constexpr bool kTokenLanes = BT == 256;
@@ -250,7 +256,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_lanes, const __grid_const
       }
       if constexpr (G::kTokenLanes) {
         // 32 columns of the warp's 32 tokens at once go through shared memory, so that four lanes write 64 bytes of a row
-        // (each lane its own row's 16 bytes: TODO).  16-byte piece c of row r is at c ^ (r / 2) % 4: no bank conflicts.
+        // (each lane its own row's 16 bytes: 466 us against 399 for 4096 tokens through 4096 x 28672).  16-byte piece c of row r is at c ^ (r / 2) % 4: no bank conflicts.
         uint8_t* own = smem + G::kFactorAt + warp * 2048;
         const int row = lane / 4, piece = lane % 4, m = t.lane + warp % 4 * 32 + row;
         uint16_t* p = a.y + (int64_t)m * a.N + t.col + G::kRows * wg + 8 * piece;
@@ -366,7 +372,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_lanes, const __grid_const
       if constexpr (QUANT) {
         // kAhead blocks at once, their (block, token) pairs dealt out to the four half warps, so that few tokens are not many
         // rounds; one fence makes all their codes visible to the products.  Loops, not unrolled: a call of one token runs through
-        // here three times, and code that has to be fetched first costs more than it does (19 us unrolled, TODO so).
+        // here three times, and code that has to be fetched first costs more than it does (19 us unrolled, 12 so).
         const int w = warp - G::kMmaWarp - 2, sub = lane % 16, item = 2 * w + lane / 16;
         const int lg = M <= 1 ? 0 : 32 - __clz(M - 1), rounds = 1 << lg;  // tokens padded to a power of two
         while (ok) {
@@ -478,7 +484,17 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_lanes, const __grid_const
   }
 }
 
-int tile_columns(int64_t M) { return M <= kFp8FewTokens ? 16 : M <= 64 ? 64 : 256; }
+// 16 or 64 token columns (4096 x 28672: 16 tokens 28.7 and 30.0 us, 24 tokens 40.2 and 29.7), or 256 output columns.  Above 64
+// tokens the form that is expected to be faster, both in microseconds, fitted to 80 to 768 tokens, 1024 to 28672 outputs and 2048
+// to 14336 inputs: a block of a CTA takes 0.37 and 0.53; the larger tiles, where they are few, are joined from many CTAs' parts
+// of 131 KB (64 and 256 columns, 4096 x 4096: 128 tokens 15.1 and 33.1, 512 tokens 27.9 and 27.4, 768 tokens 38.2 and 28.2;
+// 4096 x 28672: 64 tokens 30.5 and 37.2, 80 tokens 44.1 and 38.2).
+int tile_columns(int64_t M, int64_t K, int64_t N) {
+  if (M <= 64) return M <= 16 ? 16 : 64;
+  const double blocks = (double)((K + 127) / 128) / device_sm_count();
+  const double small = (double)((M + 63) / 64) * (double)((N + 127) / 128), large = (double)((M + 127) / 128) * (double)((N + 255) / 256);
+  return 10 + 0.37 * small * blocks <= 15 + 320 / large + 0.53 * large * blocks ? 64 : 256;
+}
 
 template <int BT, bool BF16, bool QUANT = false>
 cudaError_t launch(const Fp8GemmArgs& a, void* ws, int* err, cudaStream_t s) {
@@ -505,12 +521,12 @@ cudaError_t launch(const Fp8GemmArgs& a, void* ws, int* err, cudaStream_t s) {
 }  // namespace
 
 // flags | parts of shared tiles
-size_t fp8_gemm_workspace(int64_t M, int64_t, int64_t) {
-  return kCounterBytes + (size_t)device_sm_count() * kLanes * (size_t)tile_columns(M) * 4;
+size_t fp8_gemm_workspace(int64_t M, int64_t K, int64_t N) {
+  return kCounterBytes + (size_t)device_sm_count() * kLanes * (size_t)tile_columns(M, K, N) * 4;
 }
 
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, bool bf16, void* ws, int* err, cudaStream_t s) {
-  const int bt = tile_columns(a.M);
+  const int bt = tile_columns(a.M, a.K, a.N);
   if (a.x) return bf16 ? launch<16, true, true>(a, ws, err, s) : launch<16, false, true>(a, ws, err, s);
   const auto fn = bt == 16   ? (bf16 ? launch<16, true> : launch<16, false>)
                   : bt == 64 ? (bf16 ? launch<64, true> : launch<64, false>)

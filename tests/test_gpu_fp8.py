@@ -111,7 +111,8 @@ def check(got, want, mag, K, bf16):
 
 @pytest.mark.parametrize("M,K,N", [(1, 16, 8), (1, 128, 128), (2, 144, 136), (5, 4096, 256), (16, 272, 1032), (17, 512, 128),
                                    (31, 1040, 264), (33, 640, 520), (64, 256, 4096), (65, 384, 72), (128, 1024, 512),
-                                   (130, 2048, 248), (257, 528, 1160), (300, 128, 2056), (1, 14336, 512), (700, 1296, 400)])
+                                   (130, 2048, 248), (257, 528, 1160), (300, 128, 2056), (1, 14336, 512), (700, 1296, 400),
+                                   (601, 1040, 8200), (384, 16384, 2040), (515, 4112, 4096)])
 @pytest.mark.parametrize("bf16", [False, True])
 def test_gemm(awq, M, K, N, bf16):
     p = Problem(M, K, N, seed=M + K + N)
@@ -136,7 +137,8 @@ def test_gemm_scales_of_blocks(awq):
     assert y[:, 128:].all() and y[7].all() and not y[:7, :128].any() and not y[8:, :128].any()
 
 
-@pytest.mark.parametrize("M,K,N", [(0, 64, 64), (1, 4096, 512), (19, 1040, 1000), (200, 512, 384)])
+@pytest.mark.parametrize("M,K,N", [(0, 64, 64), (1, 4096, 512), (19, 1040, 1000), (200, 512, 384), (2, 1040, 1000), (3, 272, 264),
+                                   (16, 1024, 136), (601, 1040, 8200)])
 @pytest.mark.parametrize("bf16", [False, True])
 def test_linear_is_quant_and_gemm(awq, M, K, N, bf16):
     p = Problem(max(M, 1), K, N, seed=3)

@@ -76,7 +76,7 @@ def test_plan(awq, T, k, E):
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("T,E,k", [(0, 8, 2), (1, 1, 1), (1, 8, 2), (7, 8, 8), (33, 33, 32), (513, 60, 4), (900, 128, 8),
-                                   (100, 160, 6), (70, 512, 8), (257, 300, 10)])
+                                   (100, 160, 6), (70, 512, 8), (257, 300, 10), (16, 512, 8), (32, 100, 4), (32, 8, 5), (4, 400, 32), (5, 400, 32)])
 def test_route(awq, dtype, T, E, k):
     gen = torch.Generator().manual_seed(T + E)
     logits = (2.0 * torch.randn(T, E, generator=gen)).to(dtype)

@@ -203,6 +203,8 @@ __device__ __forceinline__ int source_row(const MoeGemmArgs& a, int row) {
   return src >= 0 && src < a.x_rows ? src : 0;
 }
 
+// The approximate exponential is off by 2 + 1.2 |gate| units in the last place: where that is much, silu is small against the error
+// that gate has from its own sum.  expf: 16 us more of 1427 for 8192 rows of 14336 columns.
 __device__ __forceinline__ float silu_times(float gate, float up) { return __fdividef(gate, 1.f + __expf(-gate)) * up; }
 
 template <int BT, bool BF16, bool GATED, bool WIDE>

@@ -17,8 +17,8 @@
 // Measured: 4096 tokens through 4096 x 28672 in 399 us, 2410 TFLOP/s.  A block's products take 517 cycles, the sums of its 128 x 256
 // numbers by 16 warps about 570, its 48 KB of operands 768 at 64 bytes a cycle; all three at once 1020.  None of them alone is
 // the limit: without the sums 362 us, without the copies 375, without the stores 378; without all three and the products 245,
-// the barriers' round trips between the roles.  48 tokens through 14336 x 4096: 20 us, 3 TB/s, bound by those round trips too;
-// one token through 4096 x 6144: 11 us, of which 3.7 are its bytes.
+// the barriers' round trips between the roles.  48 tokens through 14336 x 4096: 19 us, 3.2 TB/s, bound by those round trips too;
+// one token through 4096 x 6144: 10.5 us, of which 3.7 are its bytes.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -62,7 +62,7 @@ struct Geo {
 
 template <int BT>
 struct Bars {
-  uint64_t full[Geo<BT>::kStages], done[Geo<BT>::kStages], d_empty[Geo<BT>::kSums], join, end;
+  uint64_t full[Geo<BT>::kStages], done[Geo<BT>::kStages], d_empty[Geo<BT>::kSums], end;
 };
 
 // The products of one block, 128 k in steps of 32, into a fresh sum.
@@ -102,7 +102,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_lanes, const __grid_const
   extern __shared__ uint8_t smem_raw[];
   __shared__ Bars<BT> bars;
   __shared__ uint32_t tmem_slot;
-  __shared__ int abort_word, s_ok;
+  __shared__ int abort_word;
   volatile int* abort_flag = &abort_word;
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid / 32, 0), lane = tid % 32;
   uint8_t* smem = align_smem_1024(smem_raw);
@@ -116,7 +116,6 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_lanes, const __grid_const
       mbar_init(smem_u32(&bars.done[i]), 1);
     }
     for (int i = 0; i < G::kSums; ++i) mbar_init(smem_u32(&bars.d_empty[i]), G::kSumWarps);
-    mbar_init(smem_u32(&bars.join), G::kSumWarps);
     mbar_init(smem_u32(&bars.end), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -142,15 +141,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_lanes, const __grid_const
     const int wg = warp / 4, n = warp % 4 * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16) + G::kRows * wg;
     int d = 0, stage = 0, slot = 0;
-    uint32_t phase = 0, join_phase = 0;
-    // all summing warps, or false: a wait that gives up elsewhere must not leave this one waiting
-    auto join = [&]() {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars.join));
-      const bool all = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.join), join_phase, abort_flag, err, 804));
-      join_phase ^= 1u;
-      return all;
-    };
+    uint32_t phase = 0;
     while (ok && walk.next(tile, g0, g1)) {
       const Tile t = find_tile<BT>(tile, m_tiles, a);
       const int mine = min(max(t.cols - G::kRows * wg, 0), G::kRows);  // of this thread's columns
@@ -223,21 +214,15 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_lanes, const __grid_const
 #pragma unroll
         for (int i = 0; i < G::kPairs; ++i)
           if (2 * i < mine) __stcg(reinterpret_cast<unsigned long long*>(part + i * G::kSumThreads), acc[i].v);
-        __threadfence();
-        ok = join();
-        if (ok && tid == 0) atomicExch(flags + walk.me, 1);
+        raise_flag(flags + walk.me * G::kSumWarps + warp, lane);
         continue;
       }
       if (g1 < blocks) {
-        // the others' sums, in the order of their blocks; the lanes of one warp wait for all of them at once
+        // the others' sums, in the order of their blocks; a warp's lanes wait for all of them at once
         const int end = (tile - walk.rounds * walk.grid + 1) * blocks;
         int last = walk.me + 1;
         while (last < walk.ctas && walk.begin_of(last) < end) ++last;
-        if (warp == 0) {
-          const bool seen = wait_flags(flags, walk.me + 1, last, lane, abort_flag, err, 803);
-          if (lane == 0) s_ok = seen;
-        }
-        ok = join() && s_ok != 0;
+        ok = wait_flags(flags + warp, G::kSumWarps, walk.me + 1, last, lane, abort_flag, err, 803);
         if (!ok) break;
         for (int q = walk.me + 1; q < last; ++q) {
           const F2* part = reinterpret_cast<const F2*>(parts) + (size_t)q * (G::kPartBytes / 8) + tid;
@@ -249,10 +234,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_lanes, const __grid_const
               acc[i] = add2(acc[i], o);
             }
         }
-        ok = join();
-        if (!ok) break;
-        if (warp == 0)
-          for (int q = walk.me + 1 + lane; q < last; q += 32) atomicExch(flags + q, 0);
+        __syncwarp();
+        for (int q = walk.me + 1 + lane; q < last; q += 32) flags[q * G::kSumWarps + warp] = 0;
       }
       if constexpr (G::kTokenLanes) {
         // 32 columns of the warp's 32 tokens at once go through shared memory, so that four lanes write 64 bytes of a row

@@ -23,11 +23,12 @@
 // Tiles are dealt out to a persistent grid in whole rounds; what is left over is cut evenly along K, and a tile that several
 // CTAs share is finished by the one that has its first group, which adds the others' sums in their order.
 //
-// Measured (gate and up, then down): 8192 rows over 8 experts, 4096 x 2 x 14336 and back, 1427 and 720 us, 1348 and 1335 TFLOP/s:
-// a group takes 1790 cycles of which the products are 1024; the rest are hand-overs between the roles and, in the first, the
-// epilogue (1390 without it).  2 rows of one token: 36 and 22 us, 3.4 TB/s, at 1100 cycles a group: issue slots 52 % busy, operands
-// 315 cycles, the rest their hand-over and the 8 us of start and joins.  192 rows over 8 experts: 132 and 78 us, 3.7 TB/s.
-// 32008 rows over 126 experts, 2048 x 2 x 768: 231 and 145 us, of which 27 put rows in order and 12 and 31 are the epilogue.
+// Measured (gate and up, then down): 8192 rows over 8 experts, 4096 x 2 x 14336 and back, 1405 and 714 us, 1369 and 1347 TFLOP/s:
+// a group takes 1770 cycles of which the products are 1024; the rest are hand-overs between the roles and, in the first, the
+// epilogue (37 us).  2 rows of one token: 34 and 21 us, 3.6 TB/s, at 1050 cycles a group: issue slots 52 % busy, operands
+// 315 cycles, the rest their hand-over (750 a group with no work but theirs) and the 7 us of start and joins.  192 rows over 8
+// experts: 129 and 75 us, 3.8 TB/s.  32008 rows over 126 experts, 2048 x 2 x 768: 228 and 144 us, of which 27 put rows in order and 12
+// and 31 are the epilogue.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -84,7 +85,7 @@ struct Geo {
 template <int BT>
 struct Bars {
   uint64_t x_full[kRing], q_full[Geo<BT>::kQStages], q_empty[Geo<BT>::kQStages],
-      a_full[Geo<BT>::kABufs][Geo<BT>::kSteps], done[kRing][Geo<BT>::kSteps], d_empty[Geo<BT>::kSums][Geo<BT>::kSteps], join, end;
+      a_full[Geo<BT>::kABufs][Geo<BT>::kSteps], done[kRing][Geo<BT>::kSteps], d_empty[Geo<BT>::kSums][Geo<BT>::kSteps], end;
 };
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -214,7 +215,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
   extern __shared__ uint8_t smem_raw[];
   __shared__ Bars<BT> bars;
   __shared__ uint32_t tmem_slot;
-  __shared__ int abort_word, s_ok;
+  __shared__ int abort_word;
   volatile int* abort_flag = &abort_word;
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid / 32, 0), lane = tid % 32;
   uint8_t* smem = align_smem_1024(smem_raw);
@@ -235,7 +236,6 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
     }
     for (int i = 0; i < G::kABufs * G::kSteps; ++i) mbar_init(smem_u32(&bars.a_full[0][i]), 8 / G::kSteps);
     for (int i = 0; i < G::kSums * G::kSteps; ++i) mbar_init(smem_u32(&bars.d_empty[0][i]), G::kSumWarps);
-    mbar_init(smem_u32(&bars.join), G::kSumWarps);
     mbar_init(smem_u32(&bars.end), G::kSteps);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -263,18 +263,8 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
     const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16) + G::kRows * wg;
     const float* scales = reinterpret_cast<const float*>(smem + G::kScaleAt);
     int d = 0, count = 0;  // count: groups so far, of this CTA
-    uint32_t join_phase = 0;
-    // all summing warps, or false: a wait that gives up elsewhere must not leave this one waiting
-    auto join = [&]() {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars.join));
-      const bool all = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&bars.join), join_phase, abort_flag, err, 704));
-      join_phase ^= 1u;
-      return all;
-    };
-    // a sum is in registers
     if (a.early) wait_then_release_dependents();
-    auto take = [&](int step) {
+    auto take = [&](int step) {  // a sum is in registers
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars.d_empty[d][step]));
@@ -334,21 +324,15 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
 #pragma unroll
           for (int i = 0; i < G::kPairs; ++i)
             if (2 * i < mine) __stcg(reinterpret_cast<unsigned long long*>(part + (b * G::kPairs + i) * G::kSumThreads), acc[b][i].v);
-        __threadfence();
-        ok = join();
-        if (ok && tid == 0) atomicExch(flags + walk.me, 1);
+        raise_flag(flags + walk.me * G::kSumWarps + warp, lane);
         continue;
       }
       if (g1 < groups) {
-        // the others' sums, in the order of their groups; the lanes of one warp wait for all of them at once
+        // the others' sums, in the order of their groups; a warp's lanes wait for all of them at once
         const int end = (tile - walk.rounds * walk.grid + 1) * groups;
         int last = walk.me + 1;
         while (last < walk.ctas && walk.begin_of(last) < end) ++last;
-        if (warp == 0) {
-          const bool seen = wait_flags(flags, walk.me + 1, last, lane, abort_flag, err, 703);
-          if (lane == 0) s_ok = seen;
-        }
-        ok = join() && s_ok != 0;
+        ok = wait_flags(flags + warp, G::kSumWarps, walk.me + 1, last, lane, abort_flag, err, 703);
         if (!ok) break;
         for (int q = walk.me + 1; q < last; ++q) {
           const F2* part = reinterpret_cast<const F2*>(parts) + (size_t)q * (G::kPartBytes / 8) + tid;
@@ -362,10 +346,8 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const MoeGemmArgs a, i
                 acc[b][i] = add2(acc[b][i], o);
               }
         }
-        ok = join();
-        if (!ok) break;
-        if (warp == 0)
-          for (int q = walk.me + 1 + lane; q < last; q += 32) atomicExch(flags + q, 0);
+        __syncwarp();
+        for (int q = walk.me + 1 + lane; q < last; q += 32) flags[q * G::kSumWarps + warp] = 0;
       }
       // Two neighbouring lanes swap one of a pair of rows each, so that a lane writes two columns of one row.  Whether a column
       // exists is the same for all lanes: there are multiples of 32.

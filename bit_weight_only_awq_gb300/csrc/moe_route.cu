@@ -147,8 +147,8 @@ __device__ __forceinline__ void place_class(const int32_t* ids, int begin, int e
   }
 }
 
-// A CTA for each class (expert, and "none"): counts what comes before its rows, then writes them.  65528 ids of 128 experts: 15.6 us, bound
-// by every CTA's reading all ids twice, 68 MB from L2; kept in registers in between, 16 bits each, they spill: 15.1.
+// A CTA for each class (expert, and "none"): counts what comes before its rows, then writes them.  Every CTA
+// looks at all ids twice (8192 of 128 experts: 4.9 us, where the form for many rows takes 8.0).
 __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ ids, int R, int experts,
                                                     int32_t* __restrict__ offsets, int32_t* __restrict__ order,
                                                     int32_t* __restrict__ place) {
@@ -173,6 +173,106 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ 
   }
   if (threadIdx.x == 0) offsets[e] = row;
   place_class(ids, begin, end, aligned, e, experts, lane, row + before, order, place);
+}
+
+// Many rows: one cluster of CTAs, each warp with a stretch of positions of its own.  The warps count their classes in shared memory, sums
+// over the warps of a CTA, the CTAs (through distributed shared memory) and the lower classes give each warp the first row of each
+// class, and the warps go over their stretch again, 32 positions at once in order.  Every id is read twice, not twice a class; bound by
+// the steps' latency (5 us without any rows to speak of) and 8 SMs.
+constexpr int kPlanCtas = 8, kPlanWarps = 32;
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanWarps * 32)
+plan_many_kernel(const int32_t* __restrict__ ids, int R, int experts, int32_t* __restrict__ offsets, int32_t* __restrict__ order,
+                 int32_t* __restrict__ place) {
+  extern __shared__ int s_counts[];  // [warp][class] | this CTA's sums of classes | first rows
+  __shared__ int s_warp[kPlanWarps];
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, rank = blockIdx.x, classes = experts + 1;
+  int* mine = s_counts + warp * classes;
+  int* sums = s_counts + kPlanWarps * classes;
+  int* first = sums + classes;
+  wait_then_release_dependents();
+  for (int c = lane; c < classes; c += 32) mine[c] = 0;
+  __syncwarp();
+  constexpr int kStretches = kPlanCtas * kPlanWarps;
+  const int64_t share = ((int64_t)R + kStretches * 128 - 1) / (kStretches * 128) * 128, at = (int64_t)(rank * kPlanWarps + warp) * share;
+  const int begin = (int)min((int64_t)R, at), end = (int)min((int64_t)R, at + share);
+  const bool aligned = (reinterpret_cast<uintptr_t>(ids) & 15u) == 0;
+#pragma unroll 2
+  for (int i = begin + 4 * lane; i < end; i += 128) {
+    int c[4];
+    read4(ids, i, end, aligned, experts, c);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c[j] < classes) atomicAdd(mine + c[j], 1);
+  }
+  __syncthreads();
+  if (tid < classes) {
+    int sum = 0;
+#pragma unroll 8
+    for (int w = 0; w < kPlanWarps; ++w) {
+      const int n = s_counts[w * classes + tid];
+      s_counts[w * classes + tid] = sum;
+      sum += n;
+    }
+    sums[tid] = sum;
+  }
+  cluster_sync();
+  int before = 0, all = 0;  // of class `tid`: in the CTAs before this one, in all
+  if (tid < classes) {
+    const uint32_t own = smem_u32(sums + tid);
+#pragma unroll
+    for (int r = 0; r < kPlanCtas; ++r) {
+      uint32_t there;
+      int n;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(own), "r"(r));
+      asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(n) : "r"(there) : "memory");
+      before += r < rank ? n : 0;
+      all += n;
+    }
+  }
+  int row = all;  // sums of the classes up to this one, of the warp's
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int o = __shfl_up_sync(kAll, row, d);
+    if (lane >= d) row += o;
+  }
+  if (lane == 31) s_warp[warp] = row;
+  __syncthreads();
+  int lower = lane < warp ? s_warp[lane] : 0;
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) lower += __shfl_xor_sync(kAll, lower, d);
+  row += lower - all;
+  if (tid < classes) {
+    first[tid] = row + before;
+    if (rank == 0) offsets[tid] = row;
+  }
+  __syncthreads();
+  const uint32_t left = (1u << lane) - 1u;
+  const int bits = 32 - __clz(classes);
+  int id = begin + lane < end ? ids[begin + lane] : 0;
+  for (int i0 = begin; i0 < end; i0 += 32) {
+    const int i = i0 + lane, c = i < end ? class_of(id, experts) : classes;
+    if (i + 32 < end) id = ids[i + 32];
+    uint32_t same = kAll;  // lanes of the same class, bit by bit (__match_any_sync takes the
+    // longer the more there are: 14.6 us against 11.1 for 65528 ids of 128 experts)
+#pragma unroll 4
+    for (int b = 0; b < bits; ++b) {
+      const uint32_t set = __ballot_sync(kAll, c >> b & 1);
+      same &= c >> b & 1 ? set : ~set;
+    }
+    int r = 0;
+    if (c < classes) r = first[c] + mine[c] + __popc(same & left);
+    __syncwarp();
+    if (c < classes) {
+      if ((same & left) == 0u) mine[c] += __popc(same);
+      order[r] = c < experts ? i : -1;
+      place[i] = c < experts ? r : -1;
+    }
+    __syncwarp();
+  }
+  cluster_sync();  // the others may still read this CTA's sums
 }
 
 template <int TYPE, int L>
@@ -285,8 +385,18 @@ __global__ void __launch_bounds__(256) combine_kernel(const void* __restrict__ y
 
 }  // namespace
 
+// us of a CTA a class and of one cluster: 16384 ids of 128 experts 5.9 and 8.0, all of one expert 12.3 and 6.9; 32768 of 512 experts
+// 19.2 and 9.0; 65528 of 128 15.2 and 11.1, of one 41.3 and 10.0; 2^20 of 256 experts 258 and 104.
+constexpr int64_t kPlanFewRows = 16384;
 cudaError_t launch_moe_plan(const int32_t* ids, int64_t R, int experts, int32_t* offsets, int32_t* order, int32_t* place,
                             cudaStream_t s) {
+  if (R > kPlanFewRows) {
+    const int smem = (kPlanWarps + 2) * (experts + 1) * (int)sizeof(int);
+    const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(plan_many_kernel),
+                                        (kPlanWarps + 2) * (kMoeMaxExperts + 1) * (int)sizeof(int));
+    if (e != cudaSuccess) return e;
+    return launch_dependent(plan_many_kernel, dim3(kPlanCtas), kPlanWarps * 32, smem, s, ids, (int)R, experts, offsets, order, place);
+  }
   return launch_dependent(plan_kernel, dim3(experts + 1), 1024, 0, s, ids, (int)R, experts, offsets, order, place);
 }
 

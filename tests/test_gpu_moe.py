@@ -56,7 +56,8 @@ def host(t):
 # ---- plan
 
 @pytest.mark.parametrize("T,k,E", [(0, 2, 4), (1, 1, 1), (1, 2, 8), (3, 5, 7), (64, 8, 512), (333, 4, 60), (1025, 1, 3),
-                                   (1000, 9, 129), (4100, 8, 16), (8192, 8, 20), (8193, 8, 5), (70001, 1, 3)])
+                                   (1000, 9, 129), (4100, 8, 16), (8192, 8, 20), (8193, 8, 5), (70001, 1, 3), (16385, 1, 512),
+                                   (9000, 2, 300), (40000, 8, 1)])
 def test_plan(awq, T, k, E):
     rng = np.random.default_rng(T + k + E)
     ids = rng.integers(0, E, (T, k)).astype(np.int32)

@@ -723,7 +723,7 @@ class MoePlan:
 
     @classmethod
     def _of(cls, offsets, order, place, top_k) -> "MoePlan":
-        """From parts of one buffer, which need no checks."""
+        """From tensors made here, which need no checks."""
         plan = cls.__new__(cls)
         plan.offsets, plan.order, plan.place, plan.top_k = offsets, order, place, top_k
         return plan
@@ -737,6 +737,12 @@ class MoePlan:
         return self.offsets.shape[0] - 1
 
 
+def _plan_tensors(experts: int, rows: int, device):
+    # allocations of their own: parts of one cost the host more (a router's call 21 us against 15)
+    return (torch.empty(experts + 1, dtype=torch.int32, device=device), torch.empty(rows, dtype=torch.int32, device=device),
+            torch.empty(rows, dtype=torch.int32, device=device))
+
+
 def awq_moe_plan(ids: torch.Tensor, experts: int, stream=None) -> MoePlan:
     """The plan of a router of one's own: ids int32 [T, top_k], each in [0, experts) or a choice without a row."""
     if ids.dim() != 2:
@@ -747,12 +753,10 @@ def awq_moe_plan(ids: torch.Tensor, experts: int, stream=None) -> MoePlan:
     rows, device = T * top_k, ids.device
     if experts < 1:
         raise AwqError("awq_moe_plan", -1)
-    buf = torch.empty(experts + 1 + 2 * rows, dtype=torch.int32, device=device)  # one allocation for the plan
-    at = buf.data_ptr()
-    order = at + 4 * (experts + 1)
-    _check("awq_moe_plan", lib.awq_moe_plan(ids.data_ptr(), rows, experts, at, order, order + 4 * rows,
+    offsets, order, place = _plan_tensors(experts, rows, device)
+    _check("awq_moe_plan", lib.awq_moe_plan(ids.data_ptr(), rows, experts, offsets.data_ptr(), order.data_ptr(), place.data_ptr(),
                                             _raw_stream(stream, device)))
-    return MoePlan._of(*buf.split_with_sizes((experts + 1, rows, rows)), top_k)
+    return MoePlan._of(offsets, order, place, top_k)
 
 
 _LOGITS = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
@@ -771,13 +775,12 @@ def awq_moe_route(logits: torch.Tensor, top_k: int, normalize: bool = True, stre
         raise AwqError("awq_moe_route", -1)
     rows = T * top_k
     weights = torch.empty((T, top_k), dtype=torch.float32, device=device)
-    buf = torch.empty(experts + 1 + 3 * rows, dtype=torch.int32, device=device)  # one allocation for the whole numbers
-    ids = buf.data_ptr()  # first: 16-byte aligned, which the plan's kernel reads fastest
+    ids = torch.empty((T, top_k), dtype=torch.int32, device=device)
+    offsets, order, place = _plan_tensors(experts, rows, device)
     _check("awq_moe_route", lib.awq_moe_route(
-        logits.data_ptr(), _row_stride("awq_moe_route", logits, experts), T, experts, top_k, int(normalize), kind, ids,
-        weights.data_ptr(), ids + 12 * rows, ids + 4 * rows, ids + 8 * rows, _raw_stream(stream, device)))
-    ids, order, place, offsets = buf.split_with_sizes((rows, rows, rows, experts + 1))
-    return weights, ids.view(T, top_k), MoePlan._of(offsets, order, place, top_k)
+        logits.data_ptr(), _row_stride("awq_moe_route", logits, experts), T, experts, top_k, int(normalize), kind, ids.data_ptr(),
+        weights.data_ptr(), offsets.data_ptr(), order.data_ptr(), place.data_ptr(), _raw_stream(stream, device)))
+    return weights, ids, MoePlan._of(offsets, order, place, top_k)
 
 
 class MoeWeights:

@@ -13,6 +13,7 @@ import ctypes
 import functools
 import os
 import re
+import threading
 
 import torch
 
@@ -120,6 +121,16 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream
 
 
+# A call may be several launches that hand data on through its workspace, and the interpreter runs other threads
+# meanwhile: whoever takes a workspace that other calls share keeps its lock from the taking to the last launch.
+_locks: dict[tuple, threading.Lock] = {}
+
+
+def _lock_of(*key) -> threading.Lock:
+    lock = _locks.get(key)
+    return lock if lock is not None else _locks.setdefault(key, threading.Lock())
+
+
 # One zero-filled workspace per device, grown on demand.  The library leaves its tile
 # counters at zero after every call, so reuse on one stream needs no re-zeroing.
 _workspaces: dict[int, torch.Tensor] = {}
@@ -134,6 +145,19 @@ def device_workspace(nbytes: int, device: torch.device) -> torch.Tensor | None:
         ws = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
         _workspaces[idx] = ws
     return ws
+
+
+def _call_with_workspace(name, fn, workspace, need: int, stream, device: torch.device, *args) -> None:
+    """fn(*args, workspace, its bytes, stream); without a workspace the device's own, under its lock."""
+    if workspace is not None:
+        _check(name, fn(*args, _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+        return
+    if need == 0:
+        _check(name, fn(*args, None, 0, _stream(stream)))
+        return
+    with _lock_of("device", device.index):
+        ws = device_workspace(need, device)
+        _check(name, fn(*args, _ptr(ws), ws.numel(), _stream(stream)))
 
 
 def awq_workspace_bytes(op: int, M: int, K: int, N: int, split_k: int = 0) -> int:
@@ -202,12 +226,9 @@ def _gemm_like(name, op, x, qweight, qzeros, scales, group_size, split_k, out, w
     N = qweight.shape[1] * 8
     if out is None:
         out = torch.empty((M, N), dtype=x.dtype, device=x.device)
-    if ws is None:
-        ws = device_workspace(_workspace_need(op, M, K, N, split_k, x.device), x.device)
-    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
-    fn = getattr(lib, name)
-    _check(name, fn(_ptr(x), _ptr(qweight), _ptr(qzeros), _ptr(scales), _ptr(out), M, K, N, group_size,
-                    split_k, _ptr(ws), nbytes, _stream(stream)))
+    need = 0 if ws is not None else _workspace_need(op, M, K, N, split_k, x.device)
+    _call_with_workspace(name, getattr(lib, name), ws, need, stream, x.device, _ptr(x), _ptr(qweight), _ptr(qzeros),
+                         _ptr(scales), _ptr(out), M, K, N, group_size, split_k)
     return out
 
 
@@ -269,11 +290,9 @@ def awq_gemv_prepacked(x, packed: Prepacked, split_k: int = 0, out=None, workspa
         raise ValueError("x has K columns different from the prepared layer's")
     if out is None:
         out = torch.empty((M, N), dtype=torch.float16, device=x.device)
-    ws = workspace if workspace is not None else \
-        device_workspace(_workspace_need(OP_GEMV_PREPACKED, M, K, N, split_k, x.device), x.device)
-    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
-    _check("awq_gemv_prepacked", lib.awq_gemv_prepacked(_ptr(x), _ptr(packed.data), _ptr(out), M, K, N, split_k,
-                                                        _ptr(ws), nbytes, _stream(stream)))
+    need = 0 if workspace is not None else _workspace_need(OP_GEMV_PREPACKED, M, K, N, split_k, x.device)
+    _call_with_workspace("awq_gemv_prepacked", lib.awq_gemv_prepacked, workspace, need, stream, x.device, _ptr(x),
+                         _ptr(packed.data), _ptr(out), M, K, N, split_k)
     return out
 
 
@@ -339,10 +358,8 @@ def w4a8_gemm(xq, s_tok, wq, s_ch, split_k: int = 0, out=None, acc_out=None, wor
     if out is None:
         out = torch.empty((M, N), dtype=torch.float16, device=xq.device)
     need = awq_workspace_bytes(OP_W4A8_GEMM, M, K, N, split_k)
-    ws = workspace if workspace is not None else device_workspace(need, xq.device)
-    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
-    _check("w4a8_gemm", lib.w4a8_gemm(_ptr(xq), _ptr(s_tok), _ptr(wq), _ptr(s_ch), _ptr(out), _ptr(acc_out), M, K,
-                                      N, split_k, _ptr(ws), nbytes, _stream(stream)))
+    _call_with_workspace("w4a8_gemm", lib.w4a8_gemm, workspace, need, stream, xq.device, _ptr(xq), _ptr(s_tok),
+                         _ptr(wq), _ptr(s_ch), _ptr(out), _ptr(acc_out), M, K, N, split_k)
     return out
 
 
@@ -356,10 +373,8 @@ def w4a8_linear(x, wq, s_ch, split_k: int = 0, out=None, acc_out=None, xq_out=No
     if s_tok is None:
         s_tok = torch.empty((M,), dtype=torch.float32, device=x.device)
     need = awq_workspace_bytes(OP_W4A8_GEMM, M, K, N, split_k)
-    ws = workspace if workspace is not None else device_workspace(need, x.device)
-    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
-    _check("w4a8_linear", lib.w4a8_linear(_ptr(x), _ptr(wq), _ptr(s_ch), _ptr(out), _ptr(acc_out), _ptr(xq_out),
-                                          _ptr(s_tok), M, K, N, split_k, _ptr(ws), nbytes, _stream(stream)))
+    _call_with_workspace("w4a8_linear", lib.w4a8_linear, workspace, need, stream, x.device, _ptr(x), _ptr(wq),
+                         _ptr(s_ch), _ptr(out), _ptr(acc_out), _ptr(xq_out), _ptr(s_tok), M, K, N, split_k)
     return out, s_tok
 
 
@@ -371,11 +386,8 @@ def w4a8_gemm_grouped(xq, s_tok, wq, s3, s2, split_k: int = 0, out=None, acc_out
     if out is None:
         out = torch.empty((M, N), dtype=torch.float16, device=xq.device)
     need = awq_workspace_bytes(OP_W4A8_GROUPED, M, K, N, split_k)
-    ws = workspace if workspace is not None else device_workspace(need, xq.device)
-    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
-    _check("w4a8_gemm_grouped", lib.w4a8_gemm_grouped(_ptr(xq), _ptr(s_tok), _ptr(wq), _ptr(s3), _ptr(s2), _ptr(out),
-                                                      _ptr(acc_out), M, K, N, GROUP_SIZE, split_k, _ptr(ws), nbytes,
-                                                      _stream(stream)))
+    _call_with_workspace("w4a8_gemm_grouped", lib.w4a8_gemm_grouped, workspace, need, stream, xq.device, _ptr(xq),
+                         _ptr(s_tok), _ptr(wq), _ptr(s3), _ptr(s2), _ptr(out), _ptr(acc_out), M, K, N, GROUP_SIZE, split_k)
     return out
 
 
@@ -389,11 +401,9 @@ def w4a8_linear_grouped(x, wq, s3, s2, split_k: int = 0, out=None, acc_out=None,
     if s_tok is None:
         s_tok = torch.empty((M,), dtype=torch.float32, device=x.device)
     need = awq_workspace_bytes(OP_W4A8_GROUPED, M, K, N, split_k)
-    ws = workspace if workspace is not None else device_workspace(need, x.device)
-    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
-    _check("w4a8_linear_grouped", lib.w4a8_linear_grouped(_ptr(x), _ptr(wq), _ptr(s3), _ptr(s2), _ptr(out),
-                                                          _ptr(acc_out), _ptr(xq_out), _ptr(s_tok), M, K, N,
-                                                          GROUP_SIZE, split_k, _ptr(ws), nbytes, _stream(stream)))
+    _call_with_workspace("w4a8_linear_grouped", lib.w4a8_linear_grouped, workspace, need, stream, x.device, _ptr(x),
+                         _ptr(wq), _ptr(s3), _ptr(s2), _ptr(out), _ptr(acc_out), _ptr(xq_out), _ptr(s_tok), M, K, N, GROUP_SIZE,
+                         split_k)
     return out, s_tok
 
 
@@ -595,11 +605,26 @@ def _kv4_workspace_need(device: int, *shape) -> int:
     return kv4_attention_workspace_bytes(*shape)  # by the device's SM count
 
 
-# One workspace of kv4_attention for each device and stream (calls on one stream may share it), grown on demand, by
-# half at least.  Outgrown ones stay.  A captured call never takes it: its graph may run on any stream, beside this
+# One workspace of kv4_attention for each device and stream (calls on one stream may share it, under its lock), grown on
+# demand, by half at least.  Outgrown ones stay.  A captured call never takes it: its graph may run on any stream, beside this
 # one's calls or another graph that holds the same, and a workspace made in the capture would be the graph's memory.
 _kv4_workspaces: dict[tuple, torch.Tensor] = {}
 _kv4_outgrown: list[torch.Tensor] = []
+
+
+def _stream_key(device: torch.device, handle: int) -> tuple:
+    """What the calls that share a workspace have in common.  Handle 2 is each thread's own default stream."""
+    return (device.index, handle) if handle != 2 else (device.index, handle, threading.get_ident())
+
+
+def _call_on_stream(name, fn, workspace, shared, device: torch.device, handle: int, *args) -> None:
+    """fn(*args, workspace, its bytes, handle); without a workspace the stream's own, shared(), under its lock."""
+    if workspace is not None:
+        _check(name, fn(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle))
+        return
+    with _lock_of(*_stream_key(device, handle)):
+        ws = shared()
+        _check(name, fn(*args, ws.data_ptr(), ws.numel(), handle))
 
 
 def _kv4_workspace(handle: int, device: torch.device, nbytes: int, stream) -> torch.Tensor:
@@ -610,7 +635,7 @@ def _kv4_workspace(handle: int, device: torch.device, nbytes: int, stream) -> to
             capturing = torch.cuda.is_current_stream_capturing()
     if capturing:
         raise RuntimeError("kv4_attention: a captured call takes a workspace of its own")
-    key = (device.index, handle)
+    key = _stream_key(device, handle)
     ws = _kv4_workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
@@ -665,20 +690,21 @@ def kv4_attention(q, cache, block_table, kv_len, q_start=None, max_q: int | None
     _on_current_gpu("kv4_attention", q, cache, block_table, kv_len, q_start, out, lse, workspace)
     device = q.device
     handle = _raw_stream(stream, device)
-    if workspace is None:
-        need = _kv4_workspace_need(device.index, T, B, max_q, heads, kv_heads, dim)
-        workspace = _kv4_workspace(handle, device, need, stream)
-    _check("kv4_attention", lib.kv4_attention(
+
+    def shared():
+        return _kv4_workspace(handle, device, _kv4_workspace_need(device.index, T, B, max_q, heads, kv_heads, dim), stream)
+
+    _call_on_stream(
+        "kv4_attention", lib.kv4_attention, workspace, shared, device, handle,
         q.data_ptr(), _row_stride("kv4_attention", q, heads * dim), cache.data_ptr(), block_table.data_ptr(),
         table_stride, kv_len.data_ptr(), _ptr(q_start), out.data_ptr(),
-        _ptr(lse), T, B, max_q, heads, kv_heads, dim, pages, page, max_pages, scale, window, dtype,
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle))
+        _ptr(lse), T, B, max_q, heads, kv_heads, dim, pages, page, max_pages, scale, window, dtype)
     return out
 
 
 # ---- the feed-forward layer with experts, fp8 linear layers
 
-# Workspaces of the grouped product and the fp8 layers: one for each device and stream, as for kv4_attention.
+# Workspaces of the grouped product and the fp8 layers: one for each device and stream, under its lock, as for kv4_attention.
 _layer_workspaces: dict[tuple, torch.Tensor] = {}
 _layer_outgrown: list[torch.Tensor] = []
 
@@ -693,7 +719,7 @@ def _capturing(stream) -> bool:
 def _layer_workspace(name: str, handle: int, device: torch.device, nbytes: int, stream) -> torch.Tensor:
     if _capturing(stream):
         raise RuntimeError(f"{name}: a captured call takes a workspace of its own")
-    key = (device.index, handle)
+    key = _stream_key(device, handle)
     ws = _layer_workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
@@ -707,6 +733,12 @@ def _layer_workspace(name: str, handle: int, device: torch.device, nbytes: int, 
 @functools.lru_cache(maxsize=4096)
 def _layer_workspace_need(device: int, query: str, *shape) -> int:
     return int(getattr(lib, query)(*shape))  # by the device's SM count
+
+
+def _layer_share(name: str, handle: int, device: torch.device, stream, *shape):
+    """The stream's workspace for a call of this shape, for _call_on_stream."""
+    return lambda: _layer_workspace(name, handle, device, _layer_workspace_need(device.index, name + "_workspace_bytes", *shape),
+                                    stream)
 
 
 class MoePlan:
@@ -841,8 +873,8 @@ def awq_moe_gemm(x, weights: MoeWeights, plan: MoePlan, gather: bool = False, ou
                  stream=None):
     """Every expert's rows times its weights: [plan.rows, weights.outputs] in x's type, or fp32 with out_dtype (or `out`) so.
     x holds the rows in the plan's order, or with `gather` the tokens that the plan was made for.  Rows that no expert
-    has are not written.  Workspaces as for kv4_attention: the calls of a stream share one, a captured call takes one
-    of its own (awq_moe_gemm_workspace_bytes, zeroed once)."""
+    has are not written.  Workspaces as for kv4_attention: the calls of a stream share one, from any thread, a captured call
+    takes one of its own (awq_moe_gemm_workspace_bytes, zeroed once); a workspace that is passed serves one call at a time."""
     rows, K = plan.rows, weights.K
     dtype = _dtype16("awq_moe_gemm", x)
     if out_dtype is None:
@@ -861,14 +893,12 @@ def awq_moe_gemm(x, weights: MoeWeights, plan: MoePlan, gather: bool = False, ou
         raise ValueError("awq_moe_gemm: out is dense, [rows, outputs]")
     _on_current_gpu("awq_moe_gemm", x, weights.data, plan.offsets, plan.order, out, workspace)
     handle = _raw_stream(stream, device)
-    if workspace is None:
-        need = _layer_workspace_need(device.index, "awq_moe_gemm_workspace_bytes", rows, weights.experts, K, weights.N,
-                                     int(weights.gated))
-        workspace = _layer_workspace("awq_moe_gemm", handle, device, need, stream)
-    _check("awq_moe_gemm", lib.awq_moe_gemm(
+    _call_on_stream(
+        "awq_moe_gemm", lib.awq_moe_gemm, workspace,
+        _layer_share("awq_moe_gemm", handle, device, stream, rows, weights.experts, K, weights.N, int(weights.gated)), device, handle,
         x.data_ptr(), _row_stride("awq_moe_gemm", x, K), x.shape[0], weights.data.data_ptr(), plan.offsets.data_ptr(),
         plan.order.data_ptr() if gather else None, plan.top_k, out.data_ptr(), int(out_dtype is torch.float32), rows,
-        weights.experts, K, weights.N, int(weights.gated), dtype, workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle))
+        weights.experts, K, weights.N, int(weights.gated), dtype)
     return out
 
 
@@ -924,16 +954,13 @@ def awq_moe(x, up: MoeWeights, down: MoeWeights, weights, plan: MoePlan, residua
         raise ValueError("awq_moe: x [T, K], weights [T, top_k], residual and out [T, H] go with the layers and the plan")
     _on_current_gpu(name, x, up.data, down.data, weights, plan.offsets, plan.order, plan.place, residual, out, workspace)
     handle = _raw_stream(stream, device)
-    if workspace is None:
-        need = _layer_workspace_need(device.index, "awq_moe_workspace_bytes", T, top_k, experts, up.K, down.K, H)
-        workspace = _layer_workspace(name, handle, device, need, stream)
     if out is None:
         out = torch.empty((T, H), dtype=x.dtype, device=device)
-    _check(name, lib.awq_moe(
+    _call_on_stream(
+        name, lib.awq_moe, workspace, _layer_share(name, handle, device, stream, T, top_k, experts, up.K, down.K, H), device, handle,
         x.data_ptr(), _row_stride(name, x, up.K), up.data.data_ptr(), down.data.data_ptr(), plan.offsets.data_ptr(),
         plan.order.data_ptr(), plan.place.data_ptr(), weights.data_ptr(), _ptr(residual),
-        0 if residual is None else _row_stride(name, residual, H), out.data_ptr(), T, top_k, experts, up.K, down.K, H, dtype,
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle))
+        0 if residual is None else _row_stride(name, residual, H), out.data_ptr(), T, top_k, experts, up.K, down.K, H, dtype)
     return out
 
 
@@ -1002,12 +1029,8 @@ def awq_fp8_gemm(xq, s_x, wq, s_w, dtype=torch.float16, out=None, workspace=None
     out = _fp8_out("awq_fp8_gemm", out, M, N, dtype, device)
     _on_current_gpu("awq_fp8_gemm", xq, s_x, wq, s_w, out, workspace)
     handle = _raw_stream(stream, device)
-    if workspace is None:
-        need = _layer_workspace_need(device.index, "awq_fp8_gemm_workspace_bytes", M, K, N)
-        workspace = _layer_workspace("awq_fp8_gemm", handle, device, need, stream)
-    _check("awq_fp8_gemm", lib.awq_fp8_gemm(xq.data_ptr(), s_x.data_ptr(), wq.data_ptr(), s_w.data_ptr(), out.data_ptr(), M,
-                                            K, N, kind, workspace.data_ptr(),
-                                            workspace.numel() * workspace.element_size(), handle))
+    _call_on_stream("awq_fp8_gemm", lib.awq_fp8_gemm, workspace, _layer_share("awq_fp8_gemm", handle, device, stream, M, K, N),
+                    device, handle, xq.data_ptr(), s_x.data_ptr(), wq.data_ptr(), s_w.data_ptr(), out.data_ptr(), M, K, N, kind)
     return out
 
 
@@ -1023,12 +1046,9 @@ def awq_fp8_linear(x, wq, s_w, out=None, workspace=None, stream=None):
     out = _fp8_out("awq_fp8_linear", out, M, N, x.dtype, device)
     _on_current_gpu("awq_fp8_linear", x, wq, s_w, out, workspace)
     handle = _raw_stream(stream, device)
-    if workspace is None:
-        need = _layer_workspace_need(device.index, "awq_fp8_linear_workspace_bytes", M, K, N)
-        workspace = _layer_workspace("awq_fp8_linear", handle, device, need, stream)
-    _check("awq_fp8_linear", lib.awq_fp8_linear(x.data_ptr(), _row_stride("awq_fp8_linear", x, K), wq.data_ptr(),
-                                                s_w.data_ptr(), out.data_ptr(), M, K, N, kind, workspace.data_ptr(),
-                                                workspace.numel() * workspace.element_size(), handle))
+    _call_on_stream("awq_fp8_linear", lib.awq_fp8_linear, workspace, _layer_share("awq_fp8_linear", handle, device, stream, M, K, N),
+                    device, handle, x.data_ptr(), _row_stride("awq_fp8_linear", x, K), wq.data_ptr(), s_w.data_ptr(), out.data_ptr(),
+                    M, K, N, kind)
     return out
 
 

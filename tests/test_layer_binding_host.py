@@ -1,0 +1,171 @@
+"""Host-side behaviour of the Python binding that no GPU is needed for: workspaces that calls share.
+
+The library is replaced by a stand-in and the checks of devices are taken out, so that tensors may be the host's.
+"""
+
+import threading
+import time
+import types
+
+import pytest
+
+from bit_weight_only_awq_gb300 import build as awq_build
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def awq():
+    awq_build.build()
+    from bit_weight_only_awq_gb300 import awq as mod
+    return mod
+
+
+class Library:
+    """Calls that take a while, as several launches do, and the workspaces that are in use at once."""
+
+    def __init__(self):
+        self.lock, self.inside, self.shared, self.calls = threading.Lock(), [], [], 0
+
+    def __getattr__(self, name):
+        if name.endswith("_bytes"):
+            return lambda *shape: 256
+
+        def call(*args):
+            workspace, stream = args[-3], args[-1]
+            with self.lock:
+                self.calls += 1
+                if workspace in self.inside:
+                    self.shared.append((name, stream))
+                self.inside.append(workspace)
+            time.sleep(0.01)
+            with self.lock:
+                self.inside.remove(workspace)
+            return 0
+
+        return call
+
+
+@pytest.fixture
+def on_host(awq, monkeypatch):
+    """The binding with the stand-in and two streams' workspaces in host memory; the stream of a thread is its own choice."""
+    library, stream = Library(), threading.local()
+    spaces = {handle: torch.zeros(256, dtype=torch.uint8) for handle in (7, 8)}
+    monkeypatch.setattr(awq, "lib", library)
+    for check in ("_need", "_on_current_gpu"):
+        monkeypatch.setattr(awq, check, lambda *a: None)
+    monkeypatch.setattr(awq, "_dtype16", lambda *a: 0)
+    monkeypatch.setattr(awq, "_fp8_out", lambda name, out, M, N, dtype, device: torch.zeros(M, N))
+    monkeypatch.setattr(awq, "_raw_stream", lambda s, device: stream.handle)
+    monkeypatch.setattr(awq, "_stream", lambda s: stream.handle)
+    monkeypatch.setattr(awq, "_layer_workspace", lambda name, handle, device, nbytes, s: spaces[handle])
+    monkeypatch.setattr(awq, "_kv4_workspace", lambda handle, device, nbytes, s: spaces[handle])
+    monkeypatch.setattr(awq, "device_workspace", lambda nbytes, device: spaces[7])
+    monkeypatch.setattr(awq, "_kv4_shape", lambda name, cache: (4, 2, 64, 16))
+    return types.SimpleNamespace(library=library, stream=stream, spaces=spaces)
+
+
+def layers(awq):
+    x, ids = torch.zeros(4, 128), torch.zeros(4, dtype=torch.int32)
+    plan = awq.MoePlan._of(torch.zeros(3, dtype=torch.int32), ids, ids, 1)
+    up, down = (types.SimpleNamespace(data=x, experts=2, K=128, N=n, gated=g, dtype=x.dtype, outputs=128)
+                for n, g in ((256, True), (128, False)))
+    table = types.SimpleNamespace(shape=(4, 1), stride=lambda: (1, 1), dtype=torch.int32, is_cuda=True, data_ptr=lambda: 0)
+    wq, s_w, s_x = torch.zeros(128, 128), torch.zeros(1, 1), torch.zeros(1, 4)
+    return {
+        "awq_fp8_linear": lambda **kw: awq.awq_fp8_linear(x, wq, s_w, **kw),
+        "awq_fp8_gemm": lambda **kw: awq.awq_fp8_gemm(x, s_x, wq, s_w, **kw),
+        "awq_moe_gemm": lambda **kw: awq.awq_moe_gemm(x, down, plan, **kw),
+        "awq_moe": lambda **kw: awq.awq_moe(x, up, down, torch.zeros(4, 1), plan, **kw),
+        "kv4_attention": lambda **kw: awq.kv4_attention(torch.zeros(4, 2, 64), x, table, ids, **kw),
+        "w4a8_linear": lambda **kw: awq.w4a8_linear(x, torch.zeros(128, 16), None, **kw),
+    }
+
+
+NAMES = ("awq_fp8_linear", "awq_fp8_gemm", "awq_moe_gemm", "awq_moe", "kv4_attention", "w4a8_linear")
+
+
+def run_threads(work):
+    failed = []
+
+    def guarded(i):
+        try:
+            work(i)
+        except BaseException as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=guarded, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_threads_of_one_stream_use_its_workspace_one_after_another(awq, on_host, name):
+    call = layers(awq)[name]
+
+    def work(i):
+        on_host.stream.handle = 7
+        for _ in range(5):
+            call()
+
+    run_threads(work)
+    assert on_host.library.calls == 10 and on_host.library.shared == []
+
+
+def test_different_operators_of_one_stream_do_not_mix(awq, on_host):
+    calls = layers(awq)
+
+    def work(i):
+        on_host.stream.handle = 7
+        for _ in range(5):
+            calls[("awq_moe", "awq_fp8_linear")[i]]()
+
+    run_threads(work)
+    assert on_host.library.calls == 10 and on_host.library.shared == []
+
+
+def test_other_streams_and_given_workspaces_do_not_wait(awq, on_host):
+    """A lock is one stream's: another's calls go on while it is held, and so do calls with a workspace of their own."""
+    call, entered, leave = layers(awq)["awq_fp8_linear"], threading.Event(), threading.Event()
+    real = on_host.library
+
+    def slow(*args):
+        if args[-1] == 7 and args[-3] == on_host.spaces[7].data_ptr():
+            entered.set()
+            assert leave.wait(30)
+        return 0
+
+    awq.lib = types.SimpleNamespace(awq_fp8_linear=slow, awq_fp8_linear_workspace_bytes=real.awq_fp8_linear_workspace_bytes)
+
+    def work(i):
+        if i == 0:
+            on_host.stream.handle = 7
+            call()
+            return
+        try:
+            assert entered.wait(30)
+            on_host.stream.handle = 8
+            call()
+            on_host.stream.handle = 7
+            call(workspace=torch.zeros(256, dtype=torch.uint8))
+        finally:
+            leave.set()
+
+    run_threads(work)
+
+
+def test_each_threads_default_stream_is_another(awq):
+    """Handle 2 names the stream of whichever thread asks."""
+    device, keys = torch.device("cuda", 0), []
+    barrier = threading.Barrier(2)
+
+    def work(i):
+        barrier.wait()
+        keys.append((awq._stream_key(device, 2), awq._stream_key(device, 5)))
+        barrier.wait()
+
+    run_threads(work)
+    assert keys[0][0] != keys[1][0] and keys[0][1] == keys[1][1] == (0, 5)

@@ -656,8 +656,8 @@ def kv4_attention(q, cache, block_table, kv_len, q_start=None, max_q: int | None
     default; window: 0 or the number of keys a query looks back over, its own included.  `lse` fp32 [T, heads], when
     given, receives the log-sum-exp.
     Without `workspace` the calls of a stream share one that grows; a call to be captured in a graph needs one of
-    its own (kv4_attention_workspace_bytes, zeroed once) and is refused without.  After awq_last_device_error reports a wait that expired, a
-    workspace is zeroed again before its next use, as include/awq.h says of all of them.
+    its own (kv4_attention_workspace_bytes, zeroed once) and is refused without.  After awq_last_device_error reports a wait
+    that expired, a workspace of one's own is zeroed again before its next use, as include/awq.h says of all of them.
     """
     pages, kv_heads, dim, page = _kv4_shape("kv4_attention", cache)
     shape = q.shape
@@ -1052,11 +1052,28 @@ def awq_fp8_linear(x, wq, s_w, out=None, workspace=None, stream=None):
     return out
 
 
+def _renew_workspaces(device: int) -> None:
+    """A call whose wait expired leaves its workspace's counters and flags as they were then.  Streams' workspaces are
+    let go of (no graph holds them, and a call that has one still keeps it); the device's, which graphs may hold, is zeroed."""
+    for pool in (_kv4_workspaces, _layer_workspaces):
+        for key in [key for key in list(pool) if key[0] == device]:
+            pool.pop(key, None)
+    with _lock_of("device", device):
+        if device in _workspaces:
+            _workspaces[device].zero_()
+            torch.cuda.current_stream(device).synchronize()
+
+
 def awq_last_device_error() -> int:
+    """The id of the last bounded wait that expired on the current device, 0 for none, and clears it; waits for the
+    device.  After an id the results since the last reading may be wrong; the workspaces that the binding keeps are
+    made anew, those of the caller's own are the caller's to zero."""
     code = _i32(0)
     status = lib.awq_last_device_error(ctypes.byref(code))
     if status not in (0, -5):
         raise AwqError("awq_last_device_error", status)
+    if code.value:
+        _renew_workspaces(_current_device())
     return int(code.value)
 
 

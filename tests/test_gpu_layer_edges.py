@@ -66,3 +66,24 @@ def test_threads_on_one_stream(awq, tokens):  # noqa: F811
         t.join()
     assert not wrong, wrong[:4]
     assert awq.awq_last_device_error() == 0
+
+
+def test_stale_flags_do_not_outlive_the_report_of_an_expired_wait(awq):  # noqa: F811
+    """A wait that expired may leave any flags behind.  Here nothing runs while all of a stream's shared workspaces are
+    filled with ones, and an unrelated wait expires; calls whose tiles several CTAs share come after the report."""
+    layers = Layers(awq, 6)
+    _, _, wq, s_w = Problem(1, 14336, 512, seed=4).on_gpu()
+    deep = normal(20, 14336, seed=5)
+    calls = [lambda: layers.experts(layers.x(0)), lambda: layers.fp8(layers.x(0)), lambda: awq.awq_fp8_linear(deep, wq, s_w)]
+    want = [call() for call in calls]
+    torch.cuda.synchronize()
+    spaces = list(awq._layer_workspaces.values())
+    assert spaces
+    for ws in spaces:
+        ws.fill_(1)
+    torch.cuda.synchronize()
+    awq.awq_selftest_wait_timeout(1_000_000)
+    assert awq.awq_last_device_error() != 0
+    for _ in range(3):
+        assert all(torch.equal(call(), w) for call, w in zip(calls, want))
+    assert awq.awq_last_device_error() == 0

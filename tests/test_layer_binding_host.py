@@ -169,3 +169,32 @@ def test_each_threads_default_stream_is_another(awq):
 
     run_threads(work)
     assert keys[0][0] != keys[1][0] and keys[0][1] == keys[1][1] == (0, 5)
+
+
+def test_workspaces_are_made_anew_after_an_expired_wait(awq, monkeypatch):
+    """What the wait's call left in its flags must not reach the next one; other devices' and other errors' do not matter."""
+    code = [0]
+
+    def last_error(p):
+        p._obj.value = code[0]
+        return -5 if code[0] else 0
+
+    def dirty():
+        return torch.ones(8, dtype=torch.uint8)
+
+    waited = []
+    monkeypatch.setattr(awq, "lib", types.SimpleNamespace(awq_last_device_error=last_error))
+    monkeypatch.setattr(awq, "_current_device", lambda: 0)
+    monkeypatch.setattr(awq.torch.cuda, "current_stream",
+                        lambda device: types.SimpleNamespace(synchronize=lambda: waited.append(device)))
+    pools = {"_kv4_workspaces": {(0, 5): dirty(), (1, 5): dirty()},
+             "_layer_workspaces": {(0, 5): dirty(), (0, 2, 99): dirty(), (1, 5): dirty()},
+             "_workspaces": {0: dirty(), 1: dirty()}}
+    for name, pool in pools.items():
+        monkeypatch.setattr(awq, name, pool)
+    graphs = pools["_workspaces"][0]  # a captured graph of the dense layers keeps this address
+    assert awq.awq_last_device_error() == 0 and len(pools["_layer_workspaces"]) == 3 and graphs.all()
+    code[0] = 703
+    assert awq.awq_last_device_error() == 703
+    assert list(pools["_kv4_workspaces"]) == [(1, 5)] and list(pools["_layer_workspaces"]) == [(1, 5)]
+    assert pools["_workspaces"][0] is graphs and not graphs.any() and pools["_workspaces"][1].all() and waited == [0]

@@ -5,6 +5,9 @@ CUDA kernels.  PyTorch provides device memory (outputs and workspaces allocated
 here when the caller passes none) and the current CUDA stream.  Importing this
 module loads the library and raises ImportError when it has not been built;
 there is no fallback path.
+
+A call with `stream=` runs there: its operands are ready on that stream and stay until it is past
+the call, and the current stream waits for it before it uses the results.
 """
 
 from __future__ import annotations
@@ -177,10 +180,21 @@ def _workspace_need(op: int, M: int, K: int, N: int, split_k: int, device: torch
     return need
 
 
+def _empty(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
+    """Memory for a result that is written on `stream` (None: the current one).  It is that stream's, so that nothing queued
+    elsewhere still reads what the memory held before, and stays until the current stream, which will use it, is past it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def awq_pack(q: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     rows, n = q.shape
     if out is None:
-        out = torch.empty((rows, n // 8), dtype=torch.int32, device=q.device)
+        out = _empty((rows, n // 8), torch.int32, q.device, stream)
     _check("awq_pack", lib.awq_pack(_ptr(q), rows, n, _ptr(out), _stream(stream)))
     return out
 
@@ -188,7 +202,7 @@ def awq_pack(q: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> t
 def awq_unpack(packed: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     rows, nw = packed.shape
     if out is None:
-        out = torch.empty((rows, nw * 8), dtype=torch.uint8, device=packed.device)
+        out = _empty((rows, nw * 8), torch.uint8, packed.device, stream)
     _check("awq_unpack", lib.awq_unpack(_ptr(packed), rows, nw * 8, _ptr(out), _stream(stream)))
     return out
 
@@ -199,7 +213,7 @@ ORDER_OLD, ORDER_NEW = 0, 1
 def awq_pack_order(q: torch.Tensor, order: int, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     rows, n = q.shape
     if out is None:
-        out = torch.empty((rows, n // 8), dtype=torch.int32, device=q.device)
+        out = _empty((rows, n // 8), torch.int32, q.device, stream)
     _check("awq_pack_order", lib.awq_pack_order(_ptr(q), rows, n, order, _ptr(out), _stream(stream)))
     return out
 
@@ -207,7 +221,7 @@ def awq_pack_order(q: torch.Tensor, order: int, out: torch.Tensor | None = None,
 def awq_unpack_order(packed: torch.Tensor, order: int, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     rows, nw = packed.shape
     if out is None:
-        out = torch.empty((rows, nw * 8), dtype=torch.uint8, device=packed.device)
+        out = _empty((rows, nw * 8), torch.uint8, packed.device, stream)
     _check("awq_unpack_order", lib.awq_unpack_order(_ptr(packed), rows, nw * 8, order, _ptr(out), _stream(stream)))
     return out
 
@@ -215,7 +229,7 @@ def awq_unpack_order(packed: torch.Tensor, order: int, out: torch.Tensor | None 
 def awq_dequant(qweight, qzeros, scales, group_size: int = GROUP_SIZE, out=None, stream=None) -> torch.Tensor:
     K, nw = qweight.shape
     if out is None:
-        out = torch.empty((K, nw * 8), dtype=torch.float16, device=qweight.device)
+        out = _empty((K, nw * 8), torch.float16, qweight.device, stream)
     _check("awq_dequant", lib.awq_dequant(_ptr(qweight), _ptr(qzeros), _ptr(scales), K, nw * 8, group_size,
                                           _ptr(out), _stream(stream)))
     return out
@@ -225,7 +239,7 @@ def _gemm_like(name, op, x, qweight, qzeros, scales, group_size, split_k, out, w
     M, K = x.shape
     N = qweight.shape[1] * 8
     if out is None:
-        out = torch.empty((M, N), dtype=x.dtype, device=x.device)
+        out = _empty((M, N), x.dtype, x.device, stream)
     need = 0 if ws is not None else _workspace_need(op, M, K, N, split_k, x.device)
     _call_with_workspace(name, getattr(lib, name), ws, need, stream, x.device, _ptr(x), _ptr(qweight), _ptr(qzeros),
                          _ptr(scales), _ptr(out), M, K, N, group_size, split_k)
@@ -246,7 +260,7 @@ def awq_gemv_noalloc(x, qweight, qzeros, scales, group_size: int = GROUP_SIZE, s
     M, K = x.shape
     N = qweight.shape[1] * 8
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float16, device=x.device)
+        out = _empty((M, N), torch.float16, x.device, stream)
     _check("awq_gemv_noalloc", lib.awq_gemv_noalloc(_ptr(x), _ptr(qweight), _ptr(qzeros), _ptr(scales), _ptr(out),
                                                     M, K, N, group_size, split_k, _stream(stream)))
     return out
@@ -265,7 +279,7 @@ def awq_prepack_gemv(qweight, qzeros, scales, group_size: int = GROUP_SIZE, stre
     nbytes = int(lib.awq_prepacked_bytes(K, N))
     if nbytes == 0:
         raise AwqError("awq_prepack_gemv", -1)
-    data = torch.empty(nbytes, dtype=torch.uint8, device=qweight.device)
+    data = _empty(nbytes, torch.uint8, qweight.device, stream)
     _check("awq_prepack_gemv", lib.awq_prepack_gemv(_ptr(qweight), _ptr(qzeros), _ptr(scales), K, N, group_size,
                                                     _ptr(data), nbytes, _stream(stream)))
     return Prepacked(data, K, N)
@@ -275,9 +289,9 @@ def awq_unprepack_gemv(packed: Prepacked, with_zeros: bool = True, stream=None):
     """The AWQ (qweight, qzeros or None, scales) that `packed` was made from."""
     K, N = packed.K, packed.N
     dev = packed.data.device
-    qweight = torch.empty((K, N // 8), dtype=torch.int32, device=dev)
-    qzeros = torch.empty((K // GROUP_SIZE, N // 8), dtype=torch.int32, device=dev) if with_zeros else None
-    scales = torch.empty((K // GROUP_SIZE, N), dtype=torch.float16, device=dev)
+    qweight = _empty((K, N // 8), torch.int32, dev, stream)
+    qzeros = _empty((K // GROUP_SIZE, N // 8), torch.int32, dev, stream) if with_zeros else None
+    scales = _empty((K // GROUP_SIZE, N), torch.float16, dev, stream)
     _check("awq_unprepack_gemv", lib.awq_unprepack_gemv(_ptr(packed.data), K, N, _ptr(qweight), _ptr(qzeros),
                                                         _ptr(scales), _stream(stream)))
     return qweight, qzeros, scales
@@ -289,7 +303,7 @@ def awq_gemv_prepacked(x, packed: Prepacked, split_k: int = 0, out=None, workspa
     if K != packed.K:
         raise ValueError("x has K columns different from the prepared layer's")
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float16, device=x.device)
+        out = _empty((M, N), torch.float16, x.device, stream)
     need = 0 if workspace is not None else _workspace_need(OP_GEMV_PREPACKED, M, K, N, split_k, x.device)
     _call_with_workspace("awq_gemv_prepacked", lib.awq_gemv_prepacked, workspace, need, stream, x.device, _ptr(x),
                          _ptr(packed.data), _ptr(out), M, K, N, split_k)
@@ -311,7 +325,7 @@ def awq_dequant_bf16(qweight, qzeros, scales, group_size: int = GROUP_SIZE, out=
     _need_bf16(scales)
     K, nw = qweight.shape
     if out is None:
-        out = torch.empty((K, nw * 8), dtype=torch.bfloat16, device=qweight.device)
+        out = _empty((K, nw * 8), torch.bfloat16, qweight.device, stream)
     _check("awq_dequant_bf16", lib.awq_dequant_bf16(_ptr(qweight), _ptr(qzeros), _ptr(scales), K, nw * 8,
                                                     group_size, _ptr(out), _stream(stream)))
     return out
@@ -345,9 +359,9 @@ def awq_linear(x, qweight, qzeros, scales, group_size: int = GROUP_SIZE, **kw) -
 def w4a8_quant_act(x, xq=None, s_tok=None, stream=None):
     M, K = x.shape
     if xq is None:
-        xq = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        xq = _empty((M, K), torch.int8, x.device, stream)
     if s_tok is None:
-        s_tok = torch.empty((M,), dtype=torch.float32, device=x.device)
+        s_tok = _empty((M,), torch.float32, x.device, stream)
     _check("w4a8_quant_act", lib.w4a8_quant_act(_ptr(x), _ptr(xq), _ptr(s_tok), M, K, _stream(stream)))
     return xq, s_tok
 
@@ -356,7 +370,7 @@ def w4a8_gemm(xq, s_tok, wq, s_ch, split_k: int = 0, out=None, acc_out=None, wor
     M, K = xq.shape
     N = wq.shape[1] * 8
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float16, device=xq.device)
+        out = _empty((M, N), torch.float16, xq.device, stream)
     need = awq_workspace_bytes(OP_W4A8_GEMM, M, K, N, split_k)
     _call_with_workspace("w4a8_gemm", lib.w4a8_gemm, workspace, need, stream, xq.device, _ptr(xq), _ptr(s_tok),
                          _ptr(wq), _ptr(s_ch), _ptr(out), _ptr(acc_out), M, K, N, split_k)
@@ -369,9 +383,9 @@ def w4a8_linear(x, wq, s_ch, split_k: int = 0, out=None, acc_out=None, xq_out=No
     M, K = x.shape
     N = wq.shape[1] * 8
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float16, device=x.device)
+        out = _empty((M, N), torch.float16, x.device, stream)
     if s_tok is None:
-        s_tok = torch.empty((M,), dtype=torch.float32, device=x.device)
+        s_tok = _empty((M,), torch.float32, x.device, stream)
     need = awq_workspace_bytes(OP_W4A8_GEMM, M, K, N, split_k)
     _call_with_workspace("w4a8_linear", lib.w4a8_linear, workspace, need, stream, x.device, _ptr(x), _ptr(wq),
                          _ptr(s_ch), _ptr(out), _ptr(acc_out), _ptr(xq_out), _ptr(s_tok), M, K, N, split_k)
@@ -384,7 +398,7 @@ def w4a8_gemm_grouped(xq, s_tok, wq, s3, s2, split_k: int = 0, out=None, acc_out
     M, K = xq.shape
     N = wq.shape[1] * 8
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float16, device=xq.device)
+        out = _empty((M, N), torch.float16, xq.device, stream)
     need = awq_workspace_bytes(OP_W4A8_GROUPED, M, K, N, split_k)
     _call_with_workspace("w4a8_gemm_grouped", lib.w4a8_gemm_grouped, workspace, need, stream, xq.device, _ptr(xq),
                          _ptr(s_tok), _ptr(wq), _ptr(s3), _ptr(s2), _ptr(out), _ptr(acc_out), M, K, N, GROUP_SIZE, split_k)
@@ -397,9 +411,9 @@ def w4a8_linear_grouped(x, wq, s3, s2, split_k: int = 0, out=None, acc_out=None,
     M, K = x.shape
     N = wq.shape[1] * 8
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float16, device=x.device)
+        out = _empty((M, N), torch.float16, x.device, stream)
     if s_tok is None:
-        s_tok = torch.empty((M,), dtype=torch.float32, device=x.device)
+        s_tok = _empty((M,), torch.float32, x.device, stream)
     need = awq_workspace_bytes(OP_W4A8_GROUPED, M, K, N, split_k)
     _call_with_workspace("w4a8_linear_grouped", lib.w4a8_linear_grouped, workspace, need, stream, x.device, _ptr(x),
                          _ptr(wq), _ptr(s3), _ptr(s2), _ptr(out), _ptr(acc_out), _ptr(xq_out), _ptr(s_tok), M, K, N, GROUP_SIZE,
@@ -460,7 +474,7 @@ def _row_stride(name: str, t, inner: int) -> int:
     return max(strides[0], inner) if shape[0] <= 1 else strides[0]
 
 
-def _rmsnorm_args(name, x, weight, residual, res_out):
+def _rmsnorm_args(name, x, weight, residual, res_out, stream):
     M, K = x.shape
     dtype = _dtype16(name, x, weight, residual, res_out)
     if weight.shape != (K,) or (residual is not None and residual.shape != x.shape) or \
@@ -472,7 +486,7 @@ def _rmsnorm_args(name, x, weight, residual, res_out):
     else:
         rs = _row_stride(name, residual, K)
         if res_out is None:
-            res_out = torch.empty((M, K), dtype=x.dtype, device=x.device)
+            res_out = _empty((M, K), x.dtype, x.device, stream)
     return M, K, dtype, res_out, _row_stride(name, x, K), rs
 
 
@@ -481,7 +495,7 @@ def w4a8_rmsnorm_quant(x, weight, residual=None, eps: float = 1e-6, res_out=None
     """Residual addition, RMS norm and int8 codes of x [M, K]: (xq, s_tok, res_out), the first two as
     w4a8_gemm takes them; res_out (x + residual) is None without a residual.  `y`, when given, receives the
     normalized rows too.  res_out may be `x` or `residual` itself."""
-    M, K, dtype, res_out, xs, rs = _rmsnorm_args("w4a8_rmsnorm_quant", x, weight, residual, res_out)
+    M, K, dtype, res_out, xs, rs = _rmsnorm_args("w4a8_rmsnorm_quant", x, weight, residual, res_out, stream)
     device = x.device
     if xq is not None or s_tok is not None or y is not None:
         _need("w4a8_rmsnorm_quant", torch.int8, xq)
@@ -492,9 +506,9 @@ def w4a8_rmsnorm_quant(x, weight, residual=None, eps: float = 1e-6, res_out=None
             raise ValueError("w4a8_rmsnorm_quant: xq and y are [M, K], s_tok is [M]")
     _on_current_gpu("w4a8_rmsnorm_quant", x, weight, residual, res_out, y, xq, s_tok)
     if xq is None:
-        xq = torch.empty((M, K), dtype=torch.int8, device=device)
+        xq = _empty((M, K), torch.int8, device, stream)
     if s_tok is None:
-        s_tok = torch.empty(M, dtype=torch.float32, device=device)
+        s_tok = _empty(M, torch.float32, device, stream)
     _check("w4a8_rmsnorm_quant", lib.w4a8_rmsnorm_quant(_ptr(x), _ptr(residual), _ptr(weight), _ptr(res_out), _ptr(y),
                                                         xq.data_ptr(), s_tok.data_ptr(), M, K, xs, rs, eps, dtype,
                                                         _raw_stream(stream, device)))
@@ -503,9 +517,9 @@ def w4a8_rmsnorm_quant(x, weight, residual=None, eps: float = 1e-6, res_out=None
 
 def awq_rmsnorm(x, weight, residual=None, eps: float = 1e-6, res_out=None, out=None, stream=None):
     """Residual addition and RMS norm of x [M, K] in its own type: (y, res_out), for the W4A16 layers."""
-    M, K, dtype, res_out, xs, rs = _rmsnorm_args("awq_rmsnorm", x, weight, residual, res_out)
+    M, K, dtype, res_out, xs, rs = _rmsnorm_args("awq_rmsnorm", x, weight, residual, res_out, stream)
     if out is None:
-        out = torch.empty((M, K), dtype=x.dtype, device=x.device)
+        out = _empty((M, K), x.dtype, x.device, stream)
     else:
         _need("awq_rmsnorm", x.dtype, out)
         if out.shape != (M, K):
@@ -552,7 +566,7 @@ def kv4_append(cache, k, v, positions, slots, table, q=None, interleaved: bool =
         if q.shape != (T, heads, dim):
             raise ValueError("kv4_append: q is [T, heads, head_dim]")
         if q_out is None:
-            q_out = torch.empty((T, heads, dim), dtype=q.dtype, device=q.device)
+            q_out = _empty((T, heads, dim), q.dtype, q.device, stream)
         elif q_out.shape != q.shape:
             raise ValueError("kv4_append: q_out has another shape than q")
         inner = heads * dim
@@ -581,9 +595,9 @@ def kv4_gather(cache, slots, dtype=torch.float16, k=None, v=None, stream=None):
     _need("kv4_gather", torch.int64, slots)
     given = k is not None or v is not None
     if k is None:
-        k = torch.empty(shape, dtype=dtype, device=device)
+        k = _empty(shape, dtype, device, stream)
     if v is None:
-        v = torch.empty(shape, dtype=dtype, device=device)
+        v = _empty(shape, dtype, device, stream)
     kind = _dtype16("kv4_gather", k, v)
     if given:
         _need("kv4_gather", k.dtype, k, v)
@@ -676,7 +690,7 @@ def kv4_attention(q, cache, block_table, kv_len, q_start=None, max_q: int | None
     elif table_stride < max_pages:
         raise ValueError("kv4_attention: the rows of block_table overlap (a table made with expand needs a copy)")
     if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        out = _empty(shape, q.dtype, q.device, stream)
     elif out.shape != shape or not out.is_contiguous():
         raise ValueError("kv4_attention: out is dense and has q's shape")
     if lse is not None:
@@ -769,10 +783,10 @@ class MoePlan:
         return self.offsets.shape[0] - 1
 
 
-def _plan_tensors(experts: int, rows: int, device):
+def _plan_tensors(experts: int, rows: int, device, stream):
     # allocations of their own: parts of one cost the host more (a router's call 21 us against 15)
-    return (torch.empty(experts + 1, dtype=torch.int32, device=device), torch.empty(rows, dtype=torch.int32, device=device),
-            torch.empty(rows, dtype=torch.int32, device=device))
+    return (_empty(experts + 1, torch.int32, device, stream), _empty(rows, torch.int32, device, stream),
+            _empty(rows, torch.int32, device, stream))
 
 
 def awq_moe_plan(ids: torch.Tensor, experts: int, stream=None) -> MoePlan:
@@ -785,7 +799,7 @@ def awq_moe_plan(ids: torch.Tensor, experts: int, stream=None) -> MoePlan:
     rows, device = T * top_k, ids.device
     if experts < 1:
         raise AwqError("awq_moe_plan", -1)
-    offsets, order, place = _plan_tensors(experts, rows, device)
+    offsets, order, place = _plan_tensors(experts, rows, device, stream)
     _check("awq_moe_plan", lib.awq_moe_plan(ids.data_ptr(), rows, experts, offsets.data_ptr(), order.data_ptr(), place.data_ptr(),
                                             _raw_stream(stream, device)))
     return MoePlan._of(offsets, order, place, top_k)
@@ -806,9 +820,9 @@ def awq_moe_route(logits: torch.Tensor, top_k: int, normalize: bool = True, stre
     if not 1 <= top_k <= experts:
         raise AwqError("awq_moe_route", -1)
     rows = T * top_k
-    weights = torch.empty((T, top_k), dtype=torch.float32, device=device)
-    ids = torch.empty((T, top_k), dtype=torch.int32, device=device)
-    offsets, order, place = _plan_tensors(experts, rows, device)
+    weights = _empty((T, top_k), torch.float32, device, stream)
+    ids = _empty((T, top_k), torch.int32, device, stream)
+    offsets, order, place = _plan_tensors(experts, rows, device, stream)
     _check("awq_moe_route", lib.awq_moe_route(
         logits.data_ptr(), _row_stride("awq_moe_route", logits, experts), T, experts, top_k, int(normalize), kind, ids.data_ptr(),
         weights.data_ptr(), offsets.data_ptr(), order.data_ptr(), place.data_ptr(), _raw_stream(stream, device)))
@@ -846,7 +860,7 @@ def awq_moe_prepack(qweight, qzeros, scales, gated: bool = False, group_size: in
     nbytes = int(lib.awq_moe_prepacked_bytes(experts, K, N, int(gated)))
     if nbytes == 0:
         raise AwqError("awq_moe_prepack", -1)
-    data = torch.empty(nbytes, dtype=torch.uint8, device=qweight.device)
+    data = _empty(nbytes, torch.uint8, qweight.device, stream)
     _check("awq_moe_prepack", lib.awq_moe_prepack(_ptr(qweight), _ptr(qzeros), _ptr(scales), experts, K, N, group_size,
                                                   int(gated), _ptr(data), nbytes, _raw_stream(stream, qweight.device)))
     return MoeWeights(data, experts, K, N, bool(gated), scales.dtype)
@@ -856,9 +870,9 @@ def awq_moe_unprepack(weights: MoeWeights, with_zeros: bool = True, stream=None)
     """The AWQ (qweight, qzeros or None, scales) that `weights` was made from."""
     w, dev = weights, weights.data.device
     _on_current_gpu("awq_moe_unprepack", w.data)
-    qweight = torch.empty((w.experts, w.K, w.N // 8), dtype=torch.int32, device=dev)
-    qzeros = torch.empty((w.experts, w.K // GROUP_SIZE, w.N // 8), dtype=torch.int32, device=dev) if with_zeros else None
-    scales = torch.empty((w.experts, w.K // GROUP_SIZE, w.N), dtype=w.dtype, device=dev)
+    qweight = _empty((w.experts, w.K, w.N // 8), torch.int32, dev, stream)
+    qzeros = _empty((w.experts, w.K // GROUP_SIZE, w.N // 8), torch.int32, dev, stream) if with_zeros else None
+    scales = _empty((w.experts, w.K // GROUP_SIZE, w.N), w.dtype, dev, stream)
     _check("awq_moe_unprepack", lib.awq_moe_unprepack(_ptr(w.data), w.experts, w.K, w.N, int(w.gated), _ptr(qweight),
                                                       _ptr(qzeros), _ptr(scales), _raw_stream(stream, dev)))
     return qweight, qzeros, scales
@@ -888,7 +902,7 @@ def awq_moe_gemm(x, weights: MoeWeights, plan: MoePlan, gather: bool = False, ou
         raise ValueError("awq_moe_gemm: x is [rows, K] ([tokens, K] with gather), plan and weights have the same experts")
     device = x.device
     if out is None:
-        out = torch.empty((rows, weights.outputs), dtype=out_dtype, device=device)
+        out = _empty((rows, weights.outputs), out_dtype, device, stream)
     elif out.shape != (rows, weights.outputs) or not out.is_contiguous():
         raise ValueError("awq_moe_gemm: out is dense, [rows, outputs]")
     _on_current_gpu("awq_moe_gemm", x, weights.data, plan.offsets, plan.order, out, workspace)
@@ -920,7 +934,7 @@ def awq_moe_combine(y, plan: MoePlan, weights, residual=None, dtype=None, out=No
         raise ValueError("awq_moe_combine: y [rows, H], weights [T, top_k], residual and out [T, H] go with the plan")
     _on_current_gpu("awq_moe_combine", y, plan.place, weights, residual, out)
     if out is None:
-        out = torch.empty((T, H), dtype=dtype, device=y.device)
+        out = _empty((T, H), dtype, y.device, stream)
     rs = 0 if residual is None else _row_stride("awq_moe_combine", residual, H)
     _check("awq_moe_combine", lib.awq_moe_combine(y.data_ptr(), int(y.dtype is torch.float32), plan.place.data_ptr(), weights.data_ptr(),
                                                   _ptr(residual), rs, out.data_ptr(), T, top_k, H, plan.rows, kind,
@@ -955,7 +969,7 @@ def awq_moe(x, up: MoeWeights, down: MoeWeights, weights, plan: MoePlan, residua
     _on_current_gpu(name, x, up.data, down.data, weights, plan.offsets, plan.order, plan.place, residual, out, workspace)
     handle = _raw_stream(stream, device)
     if out is None:
-        out = torch.empty((T, H), dtype=x.dtype, device=device)
+        out = _empty((T, H), x.dtype, device, stream)
     _call_on_stream(
         name, lib.awq_moe, workspace, _layer_share(name, handle, device, stream, T, top_k, experts, up.K, down.K, H), device, handle,
         x.data_ptr(), _row_stride(name, x, up.K), up.data.data_ptr(), down.data.data_ptr(), plan.offsets.data_ptr(),
@@ -982,9 +996,9 @@ def awq_fp8_quant_act(x, xq=None, s_x=None, stream=None):
     dtype = _dtype16("awq_fp8_quant_act", x)
     groups = -(-K // FP8_BLOCK)
     if xq is None:
-        xq = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=x.device)
+        xq = _empty((M, K), torch.float8_e4m3fn, x.device, stream)
     if s_x is None:
-        s_x = torch.empty((groups, M), dtype=torch.float32, device=x.device)
+        s_x = _empty((groups, M), torch.float32, x.device, stream)
     _need("awq_fp8_quant_act", torch.float8_e4m3fn, xq)
     _need("awq_fp8_quant_act", torch.float32, s_x)
     if xq.shape != (M, K) or s_x.shape != (groups, M):
@@ -1005,9 +1019,9 @@ def awq_fp8_linear_workspace_bytes(M: int, K: int, N: int) -> int:
     return int(lib.awq_fp8_linear_workspace_bytes(M, K, N))
 
 
-def _fp8_out(name, out, M, N, dtype, device):
+def _fp8_out(name, out, M, N, dtype, device, stream):
     if out is None:
-        return torch.empty((M, N), dtype=dtype, device=device)
+        return _empty((M, N), dtype, device, stream)
     if out.shape != (M, N) or not out.is_contiguous() or out.dtype is not dtype or not out.is_cuda:
         raise ValueError(f"{name}: out is dense, [M, N], of the output's type")
     return out
@@ -1026,7 +1040,7 @@ def awq_fp8_gemm(xq, s_x, wq, s_w, dtype=torch.float16, out=None, workspace=None
     if wk != K or s_x.shape != (-(-K // FP8_BLOCK), M):
         raise ValueError("awq_fp8_gemm: xq [M, K] and s_x [K / 128, M] go with wq [N, K]")
     device = xq.device
-    out = _fp8_out("awq_fp8_gemm", out, M, N, dtype, device)
+    out = _fp8_out("awq_fp8_gemm", out, M, N, dtype, device, stream)
     _on_current_gpu("awq_fp8_gemm", xq, s_x, wq, s_w, out, workspace)
     handle = _raw_stream(stream, device)
     _call_on_stream("awq_fp8_gemm", lib.awq_fp8_gemm, workspace, _layer_share("awq_fp8_gemm", handle, device, stream, M, K, N),
@@ -1043,7 +1057,7 @@ def awq_fp8_linear(x, wq, s_w, out=None, workspace=None, stream=None):
     if wk != K:
         raise ValueError("awq_fp8_linear: x is [M, K], wq [N, K]")
     device = x.device
-    out = _fp8_out("awq_fp8_linear", out, M, N, x.dtype, device)
+    out = _fp8_out("awq_fp8_linear", out, M, N, x.dtype, device, stream)
     _on_current_gpu("awq_fp8_linear", x, wq, s_w, out, workspace)
     handle = _raw_stream(stream, device)
     _call_on_stream("awq_fp8_linear", lib.awq_fp8_linear, workspace, _layer_share("awq_fp8_linear", handle, device, stream, M, K, N),

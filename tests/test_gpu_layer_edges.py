@@ -87,3 +87,75 @@ def test_stale_flags_do_not_outlive_the_report_of_an_expired_wait(awq):  # noqa:
     for _ in range(3):
         assert all(torch.equal(call(), w) for call, w in zip(calls, want))
     assert awq.awq_last_device_error() == 0
+
+
+def tensors(result):
+    if result is None or torch.is_tensor(result):
+        return [] if result is None else [result]
+    if isinstance(result, tuple):
+        return [t for r in result for t in tensors(r)]
+    return [v for v in vars(result).values() if torch.is_tensor(v)]  # plans, prepared weights
+
+
+def prepared_calls(awq, name):  # noqa: F811
+    """Two calls of an operator, whose operands exist."""
+    layers = Layers(awq, 40)
+    weights, plan, w_up = layers.weights, layers.plan, layers.up
+    e = Experts(1, 512, 256, seed=7)
+    dense = [torch.from_numpy(a).cuda() for a in (e.qw[0], e.qz[0])]
+    words = torch.randint(-2 ** 31, 2 ** 31, (2, 256, 16), dtype=torch.int32, device="cuda")
+    ones = torch.ones(4, 40, device="cuda")
+    operands = {
+        "awq_moe_plan": lambda x: ((x[:, :2] > 0).int(), 8),
+        "awq_moe_route": lambda x: (x[:, :8].float(), 2),
+        "awq_moe_prepack": lambda x: (words, None, x[:4, :128].reshape(2, 2, 128).contiguous()),
+        "awq_moe_unprepack": lambda x: (w_up,),
+        "awq_moe_gemm": lambda x: (x, w_up, plan, True),
+        "awq_moe_combine": lambda x: (x.repeat(2, 1), plan, weights),
+        "awq_moe": lambda x: (x, layers.up, layers.down, weights, plan),
+        "awq_fp8_quant_act": lambda x: (x,),
+        "awq_fp8_gemm": lambda x: (x.to(torch.float8_e4m3fn), ones, layers.wq, layers.s_w),
+        "awq_fp8_linear": lambda x: (x, layers.wq, layers.s_w),
+        "awq_gemm": lambda x: (x, *dense, x[:4, :256].contiguous()),
+        "awq_rmsnorm": lambda x: (x, x[0]),
+        "w4a8_quant_act": lambda x: (x,),
+    }[name]
+    fn = getattr(awq, name)
+    return [lambda stream=None, args=operands(normal(40, 512, seed=seed)): fn(*args, stream=stream) for seed in (1, 2)]
+
+
+NAMES = ("awq_moe_plan", "awq_moe_route", "awq_moe_prepack", "awq_moe_unprepack", "awq_moe_gemm", "awq_moe_combine", "awq_moe",
+         "awq_fp8_quant_act", "awq_fp8_gemm", "awq_fp8_linear", "awq_gemm", "awq_rmsnorm", "w4a8_quant_act")
+
+
+def as_bytes(result):
+    return [t.view(torch.uint8).flatten() for t in tensors(result)]
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_results_for_another_stream(awq, name):  # noqa: F811
+    """A result's memory is neither what the current stream has yet to read nor given away while it has the result to read."""
+    first, second = prepared_calls(awq, name)
+    side = torch.cuda.Stream()
+    want = [t.clone() for t in as_bytes(first())]
+    for call in (first, second):  # the side's workspace, the kernels
+        call(side)
+    seen, old = [torch.zeros_like(w) for w in want], [torch.full_like(w, 7) for w in want]
+    torch.cuda.synchronize()
+
+    torch.cuda._sleep(40_000_000)  # about 20 ms
+    for s in seen:
+        s.copy_(old.pop(0))  # freed here, read later
+    got = first(side)
+    torch.cuda.synchronize()
+    assert all((s == 7).all() for s in seen)
+    assert all(torch.equal(g, w) for g, w in zip(as_bytes(got), want))
+
+    torch.cuda._sleep(40_000_000)
+    for s, t in zip(seen, as_bytes(got)):
+        s.copy_(t)
+    del got, t
+    got = second(side)  # may not take the memory yet
+    torch.cuda.synchronize()
+    assert all(torch.equal(s, w) for s, w in zip(seen, want))
+    assert awq.awq_last_device_error() == 0

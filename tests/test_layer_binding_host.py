@@ -1,4 +1,4 @@
-"""Host-side behaviour of the Python binding that no GPU is needed for: workspaces that calls share.
+"""Host-side behaviour of the Python binding that no GPU is needed for: workspaces that calls share, streams of results.
 
 The library is replaced by a stand-in and the checks of devices are taken out, so that tensors may be the host's.
 """
@@ -49,20 +49,20 @@ class Library:
 @pytest.fixture
 def on_host(awq, monkeypatch):
     """The binding with the stand-in and two streams' workspaces in host memory; the stream of a thread is its own choice."""
-    library, stream = Library(), threading.local()
+    library, stream, fp8_out = Library(), threading.local(), awq._fp8_out
     spaces = {handle: torch.zeros(256, dtype=torch.uint8) for handle in (7, 8)}
     monkeypatch.setattr(awq, "lib", library)
     for check in ("_need", "_on_current_gpu"):
         monkeypatch.setattr(awq, check, lambda *a: None)
     monkeypatch.setattr(awq, "_dtype16", lambda *a: 0)
-    monkeypatch.setattr(awq, "_fp8_out", lambda name, out, M, N, dtype, device: torch.zeros(M, N))
+    monkeypatch.setattr(awq, "_fp8_out", lambda name, out, M, N, *rest: torch.zeros(M, N))
     monkeypatch.setattr(awq, "_raw_stream", lambda s, device: stream.handle)
     monkeypatch.setattr(awq, "_stream", lambda s: stream.handle)
     monkeypatch.setattr(awq, "_layer_workspace", lambda name, handle, device, nbytes, s: spaces[handle])
     monkeypatch.setattr(awq, "_kv4_workspace", lambda handle, device, nbytes, s: spaces[handle])
     monkeypatch.setattr(awq, "device_workspace", lambda nbytes, device: spaces[7])
     monkeypatch.setattr(awq, "_kv4_shape", lambda name, cache: (4, 2, 64, 16))
-    return types.SimpleNamespace(library=library, stream=stream, spaces=spaces)
+    return types.SimpleNamespace(library=library, stream=stream, spaces=spaces, fp8_out=fp8_out)
 
 
 def layers(awq):
@@ -198,3 +198,38 @@ def test_workspaces_are_made_anew_after_an_expired_wait(awq, monkeypatch):
     assert awq.awq_last_device_error() == 703
     assert list(pools["_kv4_workspaces"]) == [(1, 5)] and list(pools["_layer_workspaces"]) == [(1, 5)]
     assert pools["_workspaces"][0] is graphs and not graphs.any() and pools["_workspaces"][1].all() and waited == [0]
+
+
+@pytest.mark.parametrize("name", ["awq_fp8_linear", "awq_fp8_gemm", "awq_moe_gemm", "awq_moe", "w4a8_linear"])
+def test_results_for_a_given_stream_are_that_streams(awq, on_host, monkeypatch, name):
+    """Memory of another stream may have readers there still; the current stream, which gets the result, is noted."""
+    side, entered, made, noted = object(), [], [], []
+
+    class On:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            entered.append(self.stream)
+
+        def __exit__(self, *_):
+            entered.pop()
+
+    class Result(torch.Tensor):
+        def record_stream(self, stream):
+            noted.append(stream)
+
+    real = torch.empty
+
+    def empty(*a, **kw):
+        made.append(list(entered))
+        return real(*a, **kw).as_subclass(Result)
+
+    on_host.stream.handle = 7
+    call = layers(awq)[name]
+    monkeypatch.setattr(awq, "_fp8_out", on_host.fp8_out)
+    monkeypatch.setattr(awq.torch, "empty", empty)
+    monkeypatch.setattr(awq.torch.cuda, "stream", On)
+    monkeypatch.setattr(awq.torch.cuda, "current_stream", lambda device=None: "current")
+    call(stream=side)
+    assert made and all(streams == [side] for streams in made) and noted == ["current"] * len(made)

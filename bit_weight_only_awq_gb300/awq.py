@@ -1050,7 +1050,7 @@ def awq_fp8_gemm(xq, s_x, wq, s_w, dtype=torch.float16, out=None, workspace=None
 
 def awq_fp8_linear(x, wq, s_w, out=None, workspace=None, stream=None):
     """16-bit x [M, K] through a layer of e4m3 weights wq [N, K], s_w [N / 128, K / 128]: quantization and product in one
-    call, [M, N] in x's type.  Workspaces as for awq_moe_gemm (awq_fp8_linear_workspace_bytes)."""
+    call, [M, N] in x's type; out may be x itself.  Workspaces as for awq_moe_gemm (awq_fp8_linear_workspace_bytes)."""
     M, K = x.shape
     kind = _dtype16("awq_fp8_linear", x)
     N, wk = _fp8_weights("awq_fp8_linear", wq, s_w)

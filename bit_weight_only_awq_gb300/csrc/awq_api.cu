@@ -616,6 +616,12 @@ awq_status kv4_attention(const uint16_t* q, int64_t q_stride, const void* cache,
 
 static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 static bool is_dtype(awq_dtype d) { return d == AWQ_FP16 || d == AWQ_BF16; }
+// Whether `bytes` from p on share any with n rows of row_bytes each, `stride` bytes apart (>= row_bytes), from `rows` on.
+static bool overlaps(const void* p, int64_t bytes, const void* rows, int64_t n, int64_t row_bytes, int64_t stride) {
+  const int64_t begin = (int64_t)(reinterpret_cast<uintptr_t>(p) - reinterpret_cast<uintptr_t>(rows)), end = begin + bytes;
+  const int64_t first = begin < row_bytes ? 0 : (begin - row_bytes) / stride + 1;  // the first row that ends behind `begin`
+  return first < n && first * stride < end;
+}
 
 awq_status awq_moe_plan(const int32_t* ids, int64_t R, int32_t experts, int32_t* offsets, int32_t* order, int32_t* place,
                         awq_stream_t stream) {
@@ -844,7 +850,8 @@ awq_status awq_fp8_linear(const uint16_t* x, int64_t x_stride, const uint8_t* wq
   float* s_x = reinterpret_cast<float*>(xq + align256((size_t)M * (size_t)K));
   const cudaStream_t s = (cudaStream_t)stream;
   const bool bf16 = dtype == AWQ_BF16;
-  if (M <= kFp8FusedTokens)
+  // the form of few tokens reads x to the end of the launch that writes y
+  if (M <= kFp8FusedTokens && !overlaps(y, M * N * 2, x, M, K * 2, x_stride * 2))
     return from_cuda(launch_fp8_gemm(Fp8GemmArgs{x, x_stride, nullptr, nullptr, wq, s_w, y, M, K, N}, bf16, workspace, err, s));
   if (launch_fp8_quant(x, x_stride, xq, s_x, M, K, bf16, s) != cudaSuccess) return AWQ_ECUDA;
   return from_cuda(launch_fp8_gemm(Fp8GemmArgs{nullptr, 0, xq, s_x, wq, s_w, y, M, K, N}, bf16, workspace, err, s));

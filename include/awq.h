@@ -630,7 +630,8 @@ awq_status awq_moe(const uint16_t *x, int64_t x_stride, const void *up, const vo
  * awq_moe_gemm's.  M = 0 is a no-op.
  *
  * awq_fp8_linear -- both in one call, from 16-bit activations; the codes and their scales live in the workspace
- * (awq_fp8_linear_workspace_bytes()).  Bit-identical to the two calls.
+ * (awq_fp8_linear_workspace_bytes()).  Bit-identical to the two calls.  y may share memory with x, whose codes are then made
+ * before anything is written.
  */
 awq_status awq_fp8_quant_act(const uint16_t *x, int64_t x_stride, uint8_t *xq, float *s_x, int64_t M, int64_t K,
                              awq_dtype dtype, awq_stream_t stream);

@@ -159,3 +159,25 @@ def test_results_for_another_stream(awq, name):  # noqa: F811
     torch.cuda.synchronize()
     assert all(torch.equal(s, w) for s, w in zip(seen, want))
     assert awq.awq_last_device_error() == 0
+
+
+@pytest.mark.parametrize("tokens,K", [(1, 24576), (2, 24576), (1, 4096), (2, 1024), (3, 4096), (40, 1024), (300, 1024)])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_fp8_layer_in_place(awq, tokens, K, bf16):  # noqa: F811
+    """out=x.  192 tiles of 24576 channels over fewer SMs: results are written while other CTAs still have channels to read."""
+    gen = torch.Generator(device="cuda").manual_seed(K)
+    wq = torch.randn(K, K, generator=gen, device="cuda").mul_(100).clamp_(-448, 448).to(torch.float8_e4m3fn)
+    s_w = torch.rand(-(-K // 128), -(-K // 128), generator=gen, device="cuda") * 1e-4
+    wide = normal(tokens + 2, K + 16, seed=tokens, dtype=torch.bfloat16 if bf16 else torch.float16)
+    x = wide[1:-1, :K]
+    want = awq.awq_fp8_linear(x, wq, s_w)
+    dense = x.clone(memory_format=torch.contiguous_format)
+    assert awq.awq_fp8_linear(dense, wq, s_w, out=dense) is dense and torch.equal(dense, want)
+    # rows that cross: out begins where the first row of x does, or ends where the last one ends
+    for first in (wide.flatten()[K + 16:], wide.flatten()[(tokens + 1) * (K + 16) - 16 - tokens * K:]):
+        keep = wide.clone()
+        out = first[: tokens * K].view(tokens, K)
+        awq.awq_fp8_linear(x, wq, s_w, out=out)
+        assert torch.equal(out, want)
+        wide.copy_(keep)
+    assert awq.awq_last_device_error() == 0

@@ -706,6 +706,7 @@ awq_status awq_moe_gemm(const uint16_t* x, int64_t x_stride, int64_t x_rows, con
   if (!aligned16(x) || !aligned16(packed) || !aligned16(y) || !aligned4(offsets) || !aligned4(order)) return AWQ_EALIGN;
   awq_status st = check_workspace(moe_gemm_workspace(R, experts, K, N, gated != 0), workspace, workspace_bytes);
   if (st != AWQ_OK) return st;
+  if (overlaps(y, R * (gated ? N / 2 : N) * (y_fp32 ? 4 : 2), x, x_rows, K * 2, x_stride * 2)) return AWQ_EINVAL;
   st = check_arch();
   if (st != AWQ_OK) return st;
   int* err = device_error_ptr();
@@ -713,6 +714,11 @@ awq_status awq_moe_gemm(const uint16_t* x, int64_t x_stride, int64_t x_rows, con
   const MoeGemmArgs a{x, x_stride, x_rows, static_cast<const uint8_t*>(packed), offsets, order, order ? top_k : 1,
                       y, R,        experts, K, N, (int)moe_tiles(N, gated != 0), false};
   return from_cuda(launch_moe_gemm(a, gated != 0, y_fp32 != 0, dtype == AWQ_BF16, workspace, err, (cudaStream_t)stream));
+}
+
+// Results [T, H] may be the residual itself, piece by piece, or have no memory in common with it.
+static bool may_add_to(const uint16_t* out, const uint16_t* residual, int64_t T, int64_t H, int64_t res_stride) {
+  return !residual || (out == residual && (res_stride == H || T == 1)) || !overlaps(out, T * H * 2, residual, T, H * 2, res_stride * 2);
 }
 
 awq_status awq_moe_combine(const void* y, int32_t y_fp32, const int32_t* place, const float* weights, const uint16_t* residual,
@@ -725,6 +731,8 @@ awq_status awq_moe_combine(const void* y, int32_t y_fp32, const int32_t* place, 
   if (T == 0) return AWQ_OK;
   if ((R > 0 && !y) || !place || !weights || !out) return AWQ_ENULL;
   if (!aligned16(y) || !aligned16(residual) || !aligned16(out) || !aligned4(place) || !aligned4(weights)) return AWQ_EALIGN;
+  if (overlaps(out, T * H * 2, y, R, H * (y_fp32 ? 4 : 2), H * (y_fp32 ? 4 : 2)) || !may_add_to(out, residual, T, H, res_stride))
+    return AWQ_EINVAL;
   awq_status st = check_arch();
   if (st != AWQ_OK) return st;
   return from_cuda(launch_moe_combine(y, y_fp32 != 0, place, weights, residual, res_stride, out, T, top_k, H, R, dtype == AWQ_BF16,
@@ -766,6 +774,7 @@ awq_status awq_moe(const uint16_t* x, int64_t x_stride, const void* up, const vo
     return AWQ_EALIGN;
   awq_status st = check_workspace(l.bytes, workspace, workspace_bytes);
   if (st != AWQ_OK) return st;
+  if (!may_add_to(out, residual, T, H, res_stride)) return AWQ_EINVAL;
   st = check_arch();
   if (st != AWQ_OK) return st;
   int* err = device_error_ptr();
@@ -797,6 +806,7 @@ awq_status awq_fp8_quant_act(const uint16_t* x, int64_t x_stride, uint8_t* xq, f
   if (M == 0) return AWQ_OK;
   if (!x || !xq || !s_x) return AWQ_ENULL;
   if (!aligned16(x) || !aligned16(xq) || !aligned4(s_x)) return AWQ_EALIGN;
+  if (overlaps(xq, M * K, x, M, K * 2, x_stride * 2)) return AWQ_EINVAL;
   awq_status st = check_arch();
   if (st != AWQ_OK) return st;
   return from_cuda(launch_fp8_quant(x, x_stride, xq, s_x, M, K, dtype == AWQ_BF16, (cudaStream_t)stream));
@@ -815,6 +825,7 @@ awq_status awq_fp8_gemm(const uint8_t* xq, const float* s_x, const uint8_t* wq, 
   if (!aligned16(xq) || !aligned16(wq) || !aligned16(y) || !aligned4(s_x) || !aligned4(s_w)) return AWQ_EALIGN;
   awq_status st = check_workspace(fp8_gemm_workspace(M, K, N), workspace, workspace_bytes);
   if (st != AWQ_OK) return st;
+  if (overlaps(y, M * N * 2, xq, M, K, K)) return AWQ_EINVAL;
   st = check_arch();
   if (st != AWQ_OK) return st;
   int* err = device_error_ptr();

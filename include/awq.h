@@ -514,6 +514,8 @@ awq_status kv4_attention(const uint16_t *q, int64_t q_stride, const void *cache,
  * the R = T * top_k rows in the experts' order, the grouped product multiplies each expert's rows by that expert's
  * 4-bit weights, and the combination adds the rows of a token up again.  A position is t * top_k + j, token t's
  * choice j.  Lengths are read on the device only, so a captured graph follows the routing.
+ * What a call writes shares no memory with what it reads, unless its comment says so: with activations, rows or a
+ * residual of its own AWQ_EINVAL, otherwise undefined.
  * The pages describe none of this; its layers are the group-wise 4-bit layers of the entry points above.
  *
  * awq_moe_plan -- offsets int32 [experts + 1]: rows of expert e are offsets[e] .. offsets[e + 1] - 1; order int32 [R]:
@@ -602,6 +604,7 @@ awq_status awq_moe_combine(const void *y, int32_t y_fp32, const int32_t *place, 
  * awq_moe -- the whole sparse feed-forward layer: awq_moe_gemm of x [T, K] (row stride x_stride) with the gated `up`
  * (experts x [K, 2 inner]), awq_moe_gemm of its rows with `down` (experts x [inner, H]) in fp32, awq_moe_combine.  The rows
  * between up and down have x's type; the results are those of the three calls.  Plan and weights as from awq_moe_route.
+ * out may share memory with x, which is read before anything is written, and may be the residual as for awq_moe_combine.
  * Workspace: awq_moe_workspace_bytes(), which holds the rows between the products too; contract as for awq_moe_gemm's.
  */
 size_t awq_moe_workspace_bytes(int64_t T, int32_t top_k, int32_t experts, int64_t K, int64_t inner, int64_t H);
@@ -616,7 +619,7 @@ awq_status awq_moe(const uint16_t *x, int64_t x_stride, const void *up, const vo
  * -------------------------------------
  * Weights e4m3 [N, K] (row-major: K dense) with an fp32 scale for each block of 128 x 128, s_w [ceil(N / 128),
  * ceil(K / 128)]; activations e4m3 [M, K] with an fp32 scale for each token and 128 channels, s_x [ceil(K / 128), M].
- * The last blocks may be cut short.  e4m3 has no infinities: the largest value is 448, 0x7F and 0xFF are NaN.
+ * The last blocks may be cut short.  Overlap: as above.  e4m3 has no infinities: the largest value is 448, 0x7F and 0xFF are NaN.
  * The pages describe none of this.
  *
  * awq_fp8_quant_act -- s_x = RN32(max|x| / 448) over a token's 128 channels, xq = e4m3(RN32(x / s_x)), to nearest

@@ -181,3 +181,26 @@ def test_fp8_layer_in_place(awq, tokens, K, bf16):  # noqa: F811
         assert torch.equal(out, want)
         wide.copy_(keep)
     assert awq.awq_last_device_error() == 0
+
+
+@pytest.mark.parametrize("tokens", [1, 40, 700])
+def test_layer_with_experts_in_place(awq, tokens):  # noqa: F811
+    """out=x, and out=x with x the residual too."""
+    layers = Layers(awq, tokens)
+    x = layers.x(1)
+    want, added = layers.experts(x), layers.experts(x, residual=x)
+    for residual, result in ((False, want), (True, added)):
+        own = x.clone()
+        assert layers.experts(own, residual=own if residual else None, out=own) is own and torch.equal(own, result)
+
+
+def test_results_over_operands_are_refused(awq):  # noqa: F811
+    layers = Layers(awq, 40)
+    rows = normal(80, 256, seed=1)
+    wide = normal(40, 520, seed=2)
+    square = Experts(8, 256, 256, seed=5).pack(awq)
+    for bad in (lambda: awq.awq_moe_gemm(rows, square, layers.plan, out=rows),
+                lambda: awq.awq_moe_combine(rows, layers.plan, layers.weights, out=rows[:40]),
+                lambda: layers.experts(layers.x(0), residual=wide[:, :512], out=wide.flatten()[: 40 * 512].view(40, 512))):
+        with pytest.raises(awq.AwqError):
+            bad()

@@ -8,6 +8,8 @@ import threading
 import numpy as np
 import pytest
 
+from oracle import layer as oracle_layer
+from oracle.block_oracle import round16
 from tests.test_gpu_fp8 import Problem, dev16
 from tests.test_gpu_moe import Experts, awq  # noqa: F401  (awq is a fixture)
 
@@ -204,3 +206,41 @@ def test_results_over_operands_are_refused(awq):  # noqa: F811
                 lambda: layers.experts(layers.x(0), residual=wide[:, :512], out=wide.flatten()[: 40 * 512].view(40, 512))):
         with pytest.raises(awq.AwqError):
             bad()
+
+
+@pytest.mark.parametrize("wide", [True, False])
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("rows", [5, 200, 700])
+def test_silu_over_its_range(awq, rows, bf16, wide):  # noqa: F811
+    """Gates and ups that are exact in fp32 (one channel, scales that are powers of two), from -104 to 104 and 0.
+
+    e = exp(-|g|) is off by 2 units of 2^-23 (expf) or 2 + 1.173 |g| (the approximate one), which counts once in g e and at most
+    half in 1 + e; the products, the sum and the division add 4 roundings of 2^-24 (the approximate division 2 units): 2.5 2^-22 in
+    fp32, (7 + 1.8 |g|) 2^-23 for 16 bits.  Where e is subnormal its error is at most 2^-148, times |g u|."""
+    I = 64
+    qw, qz = np.zeros((1, 128, 2 * I), np.uint8), np.zeros((1, 1, 2 * I // 8), np.int32)
+    qw[0, 0, :I], qw[0, 0, I:] = 1 + np.arange(I) % 13, 1 + np.arange(I) % 7
+    words = awq.awq_pack(torch.from_numpy(qw.reshape(128, 2 * I)).cuda()).view(1, 128, 2 * I // 8)
+    scales = np.ones((1, 1, 2 * I), np.float32)
+    scales[0, 0, :I] = 2.0 ** -(np.arange(I) % 4)
+    scales[0, 0, I:] = 2.0 ** (np.arange(I) % 5 - 2)
+    x = np.zeros((rows, 128), np.float32)
+    x[:, 0] = round16(np.random.default_rng(rows).uniform(-8, 8, rows).astype(np.float32), bf16)
+    x[:3, 0] = 0, 7.375, -7.375
+    dtype = torch.bfloat16 if bf16 else torch.float16
+    w = awq.awq_moe_prepack(words, torch.from_numpy(qz).cuda(), torch.from_numpy(scales).to(dtype).cuda(), gated=True)
+    order = torch.arange(rows, dtype=torch.int32, device="cuda")
+    plan = awq.MoePlan(torch.tensor([0, rows], dtype=torch.int32, device="cuda"), order, order, 1)
+    y = awq.awq_moe_gemm(torch.from_numpy(x).to(dtype).cuda(), w, plan, out_dtype=torch.float32 if wide else None)
+    a = x[:, :1].astype(np.float64) * (qw[0, 0] * scales[0, 0]).astype(np.float64)
+    g, u = a[:, :I], a[:, I:]
+    want = oracle_layer.silu(g) * u
+    tol = 2.0 ** -148 * np.abs(g * u)
+    if wide:
+        tol += 2.5 * 2.0 ** -22 * np.abs(want) + 2.0 ** -149
+    else:
+        half, least = (2.0 ** -8, 2.0 ** -134) if bf16 else (2.0 ** -11, 2.0 ** -25)
+        tol += (7 + 1.8 * np.abs(g)) * 2.0 ** -23 * np.abs(want)
+        tol += half * (np.abs(want) + tol) + least
+    err = np.abs(y.double().cpu().numpy() - want)
+    assert g.min() < -88 and np.all(err <= tol), np.max(err / np.maximum(tol, 2.0 ** -1000))

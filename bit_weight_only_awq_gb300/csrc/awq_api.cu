@@ -691,7 +691,7 @@ awq_status awq_moe_unprepack(const void* packed, int32_t experts, int64_t K, int
 
 size_t awq_moe_gemm_workspace_bytes(int64_t R, int32_t experts, int64_t K, int64_t N, int32_t gated) {
   if (R < 1 || R > kMoeMaxRows || !moe_shape_ok(experts, K, N, gated)) return 0;
-  return moe_gemm_workspace(R, experts, K, N, gated != 0);
+  return moe_gemm_workspace(R, experts, K, true);
 }
 
 awq_status awq_moe_gemm(const uint16_t* x, int64_t x_stride, int64_t x_rows, const void* packed, const int32_t* offsets,
@@ -704,7 +704,7 @@ awq_status awq_moe_gemm(const uint16_t* x, int64_t x_stride, int64_t x_rows, con
   if (R == 0) return AWQ_OK;
   if (!packed || !offsets || !y || !x) return AWQ_ENULL;
   if (!aligned16(x) || !aligned16(packed) || !aligned16(y) || !aligned4(offsets) || !aligned4(order)) return AWQ_EALIGN;
-  awq_status st = check_workspace(moe_gemm_workspace(R, experts, K, N, gated != 0), workspace, workspace_bytes);
+  awq_status st = check_workspace(moe_gemm_workspace(R, experts, K, true), workspace, workspace_bytes);
   if (st != AWQ_OK) return st;
   if (overlaps(y, R * (gated ? N / 2 : N) * (y_fp32 ? 4 : 2), x, x_rows, K * 2, x_stride * 2)) return AWQ_EINVAL;
   st = check_arch();
@@ -748,7 +748,7 @@ static bool moe_layout(int64_t T, int32_t top_k, int32_t experts, int64_t K, int
       !moe_shape_ok(experts, K, 2 * inner, 1) || !moe_shape_ok(experts, inner, H, 0))
     return false;
   const int64_t R = T * top_k;
-  const size_t up = moe_gemm_workspace(R, experts, K, 2 * inner, true), down = moe_gemm_workspace(R, experts, inner, H, false);
+  const size_t up = moe_gemm_workspace(R, experts, K, true), down = moe_gemm_workspace(R, experts, inner, false);
   l.product = align256(up > down ? up : down);
   l.rows = align256((size_t)R * (size_t)inner * 2);
   l.bytes = l.product + l.rows + (size_t)R * (size_t)H * 4;

@@ -239,7 +239,7 @@ struct MoeGemmArgs {
   // The kernel before this one in the stream has waited for what wrote offsets (and weights): they may be read while it runs.
   bool early;
 };
-size_t moe_gemm_workspace(int64_t R, int experts, int64_t K, int64_t N, bool gated);
+size_t moe_gemm_workspace(int64_t R, int experts, int64_t K, bool tokens);  // tokens: order is given
 // wide: y in fp32
 cudaError_t launch_moe_gemm(const MoeGemmArgs& a, bool gated, bool wide, bool bf16, void* ws, int* err, cudaStream_t s);
 

@@ -620,7 +620,7 @@ int tile_rows(int64_t R, int experts) {
   const double mean = (double)R / experts;
   return R <= 16 || mean <= 8 ? 16 : mean <= 80 ? 64 : 128;
 }
-// Workspace: flags | parts of shared tiles | rows in order
+// Workspace: flags | parts of shared tiles | rows in order, where x holds tokens
 size_t parts_bytes(int bt) { return align256((size_t)device_sm_count() * 256 * (size_t)bt * 4); }
 
 template <int BT, bool BF16>
@@ -650,9 +650,9 @@ cudaError_t launch(MoeGemmArgs a, bool gated, bool wide, void* ws, int* err, cud
 
 }  // namespace
 
-size_t moe_gemm_workspace(int64_t R, int experts, int64_t K, int64_t, bool gated) {
+size_t moe_gemm_workspace(int64_t R, int experts, int64_t K, bool tokens) {
   const int bt = tile_rows(R, experts);
-  return kCounterBytes + parts_bytes(bt) + (bt > 16 ? (size_t)R * (size_t)K * 2 : 0);
+  return kCounterBytes + parts_bytes(bt) + (tokens && bt > 16 ? (size_t)R * (size_t)K * 2 : 0);
 }
 
 cudaError_t launch_moe_gemm(const MoeGemmArgs& a, bool gated, bool wide, bool bf16, void* ws, int* err, cudaStream_t s) {

@@ -1,4 +1,5 @@
-"""Host-side checks of the C ABI of the layers with experts and the e4m3 layers: memory that results share with operands.
+"""Host-side checks of the C ABI of the layers with experts and the e4m3 layers: memory that results share with operands,
+sizes of workspaces.
 
 No address is dereferenced: the refusals come before anything is launched, and what is not refused ends at the check for the
 GPU, which is why these run where there is none.
@@ -77,3 +78,14 @@ def test_e4m3_calls_refuse_operands_under_their_results(lib):
     assert f(A, B, B, B, A + 4 * 256, 4, 256, 128, 0, *SPACE, None) == TAKEN
     # x of a whole layer may be overwritten
     assert lib.awq_fp8_linear(A, 256, B, B, A, 4, 256, 256, 0, *SPACE, None) == TAKEN
+
+
+def test_a_layers_workspace_has_rows_in_order_for_up_alone(lib):
+    """down finds its rows in order: 235 MB less for 8192 rows of 14336 channels."""
+    for T, k, E, K, inner, H in ((4096, 2, 8, 4096, 14336, 4096), (4001, 8, 128, 2048, 768, 2048), (100, 2, 8, 256, 1024, 320)):
+        R = T * k
+        up = lib.awq_moe_gemm_workspace_bytes(R, E, K, 2 * inner, 1)
+        parts = up - R * K * 2
+        assert 0 < parts < 1 << 25
+        aligned = lambda n: (n + 255) // 256 * 256
+        assert lib.awq_moe_workspace_bytes(T, k, E, K, inner, H) == aligned(up) + aligned(R * inner * 2) + R * H * 4

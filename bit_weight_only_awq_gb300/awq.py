@@ -641,22 +641,30 @@ def _call_on_stream(name, fn, workspace, shared, device: torch.device, handle: i
         _check(name, fn(*args, ws.data_ptr(), ws.numel(), handle))
 
 
-def _kv4_workspace(handle: int, device: torch.device, nbytes: int, stream) -> torch.Tensor:
+def _stream_workspace(pool: dict, name: str, handle: int, device: torch.device, nbytes: int, stream) -> torch.Tensor:
+    """The workspace that `pool` has for the stream, made or grown where it is too small."""
     if stream is None:
         capturing = torch.cuda.is_current_stream_capturing()
     else:
         with torch.cuda.stream(stream):
             capturing = torch.cuda.is_current_stream_capturing()
     if capturing:
-        raise RuntimeError("kv4_attention: a captured call takes a workspace of its own")
+        raise RuntimeError(f"{name}: a captured call takes a workspace of its own")
     key = _stream_key(device, handle)
-    ws = _kv4_workspaces.get(key)
+    ws = pool.get(key)
     if ws is None or ws.numel() < nbytes:
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
             if ws is not None:
-                _kv4_outgrown.append(ws)
                 nbytes = max(nbytes, ws.numel() + ws.numel() // 2)
-            ws = _kv4_workspaces[key] = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+            ws = pool[key] = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+    return ws
+
+
+def _kv4_workspace(handle: int, device: torch.device, nbytes: int, stream) -> torch.Tensor:
+    before = _kv4_workspaces.get(_stream_key(device, handle))
+    ws = _stream_workspace(_kv4_workspaces, "kv4_attention", handle, device, nbytes, stream)
+    if before is not None and ws is not before:
+        _kv4_outgrown.append(before)
     return ws
 
 
@@ -719,29 +727,12 @@ def kv4_attention(q, cache, block_table, kv_len, q_start=None, max_q: int | None
 # ---- the feed-forward layer with experts, fp8 linear layers
 
 # Workspaces of the grouped product and the fp8 layers: one for each device and stream, under its lock, as for kv4_attention.
+# An outgrown one goes back to its stream, whose calls alone have used it (a long prompt's are some hundred megabytes).
 _layer_workspaces: dict[tuple, torch.Tensor] = {}
-_layer_outgrown: list[torch.Tensor] = []
-
-
-def _capturing(stream) -> bool:
-    if stream is None:
-        return torch.cuda.is_current_stream_capturing()
-    with torch.cuda.stream(stream):
-        return torch.cuda.is_current_stream_capturing()
 
 
 def _layer_workspace(name: str, handle: int, device: torch.device, nbytes: int, stream) -> torch.Tensor:
-    if _capturing(stream):
-        raise RuntimeError(f"{name}: a captured call takes a workspace of its own")
-    key = _stream_key(device, handle)
-    ws = _layer_workspaces.get(key)
-    if ws is None or ws.numel() < nbytes:
-        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
-            if ws is not None:
-                _layer_outgrown.append(ws)
-                nbytes = max(nbytes, ws.numel() + ws.numel() // 2)
-            ws = _layer_workspaces[key] = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
-    return ws
+    return _stream_workspace(_layer_workspaces, name, handle, device, nbytes, stream)
 
 
 @functools.lru_cache(maxsize=4096)

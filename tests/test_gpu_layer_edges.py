@@ -244,3 +244,22 @@ def test_silu_over_its_range(awq, rows, bf16, wide):  # noqa: F811
         tol += half * (np.abs(want) + tol) + least
     err = np.abs(y.double().cpu().numpy() - want)
     assert g.min() < -88 and np.all(err <= tol), np.max(err / np.maximum(tol, 2.0 ** -1000))
+
+
+def test_growing_workspaces_while_calls_are_queued(awq):  # noqa: F811
+    """Outgrown memory goes back to its stream: what is queued there before still has it."""
+    small, large = Layers(awq, 20), Layers(awq, 3000)
+    for stream in (torch.cuda.current_stream(), torch.cuda.Stream()):
+        with torch.cuda.stream(stream):
+            xs, xl = small.x(0), large.x(1)
+            want = small.experts(xs), large.experts(xl), small.fp8(xs)
+            torch.cuda.synchronize()
+            awq._layer_workspaces.clear()
+            torch.cuda._sleep(20_000_000)
+            first = small.experts(xs)
+            got = first, large.experts(xl), small.fp8(xs)
+            junk = [torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
+            torch.cuda.synchronize()
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
+        del junk
+    assert awq.awq_last_device_error() == 0

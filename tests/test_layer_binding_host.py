@@ -3,9 +3,11 @@
 The library is replaced by a stand-in and the checks of devices are taken out, so that tensors may be the host's.
 """
 
+import contextlib
 import threading
 import time
 import types
+import weakref
 
 import pytest
 
@@ -233,3 +235,19 @@ def test_results_for_a_given_stream_are_that_streams(awq, on_host, monkeypatch, 
     monkeypatch.setattr(awq.torch.cuda, "current_stream", lambda device=None: "current")
     call(stream=side)
     assert made and all(streams == [side] for streams in made) and noted == ["current"] * len(made)
+
+
+def test_an_outgrown_workspace_of_the_layers_is_given_back(awq, monkeypatch):
+    """Each length of prompt would keep one of its own otherwise."""
+    monkeypatch.setattr(awq, "_layer_workspaces", {})
+    monkeypatch.setattr(awq.torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(awq.torch.cuda, "current_stream", lambda device=None: None)
+    monkeypatch.setattr(awq.torch.cuda, "stream", lambda stream: contextlib.nullcontext())
+    host, made = torch.device("cpu"), []
+    for nbytes in (1 << 20, 100, 5 << 20, 6 << 20, 7 << 20, 40 << 20):  # 6 MB make it 7.5
+        ws = awq._layer_workspace("awq_moe", 7, host, nbytes, None)
+        assert ws.numel() >= nbytes and not ws.any()
+        if not made or made[-1]() is not ws:
+            made.append(weakref.ref(ws))
+        del ws
+    assert [ref() is None for ref in made] == [True, True, True, False]

@@ -353,11 +353,12 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_lanes, const __grid_const
         return true;
       };
       if constexpr (QUANT) {
-        // kAhead blocks at once, their (block, token) pairs dealt out to the four half warps, so that few tokens are not many
-        // rounds; one fence makes all their codes visible to the products.  Loops, not unrolled: a call of one token runs through
-        // here three times, and code that has to be fetched first costs more than it does (19 us unrolled, 12 so).
+        // kAhead blocks at once, their (block, token) pairs dealt out to the four half warps in one round for a token; one fence
+        // makes all their codes visible to the products.  Loops, not unrolled: a call of one token runs through here three
+        // times, and code that has to be fetched first costs more than it does (19 us unrolled, 12 so).
         const int w = warp - G::kMmaWarp - 2, sub = lane % 16, item = 2 * w + lane / 16;
-        const int lg = M <= 1 ? 0 : 32 - __clz(M - 1), rounds = 1 << lg;  // tokens padded to a power of two
+        static_assert(kFp8FusedTokens == 2, "one or two tokens, an even share of a block's items for each");
+        const int lg = M - 1, rounds = M;
         while (ok) {
           int block[kAhead], out[kAhead], n = 0;
 #pragma unroll

@@ -13,22 +13,22 @@
 // up of a gated layer meet in it), eight warps turn codes into operands (a thread has a column), then come those that issue the
 // products, one that copies weights (one 17 KB unit a group) and one that copies rows of x.
 // Sums and operands in tensor memory go round, so that the products need not wait for either.  A step of the products is a half
-// of a group in tiles of 128 rows, each half's issued by a warp of its own (one warp for both: 1530 and 706 us for gate and up, and
-// down, of 8192 rows over 8 experts, against 1440 and 668), and a whole group in smaller ones, by one warp (two: 147 and 81 us
-// for 192 rows, against 130 and 76); whoever waits for its products waits on one barrier.
+// of a group in tiles of 128 rows, each half's issued by a warp of its own (one warp for both took 6 % longer for 8192 rows over
+// 8 experts), and a whole group in smaller ones, by one warp (two took 13 and 7 % longer for up and down of 192 rows); whoever
+// waits for its products waits on one barrier.
 // Rows of x come in any order.  Up to 16 of them are copied four an instruction (tile::gather4, about 30 cycles each); more,
-// 32 KB a group with 128, are put in order first and copied in boxes of neighbouring rows (at 32008 rows over 126 experts
-// 484 us with four rows an instruction, 406 with 16 bytes a thread, 273 without any copies, each on that day's kernel).
+// 32 KB a group with 128, are put in order first and copied in boxes of neighbouring rows (at 32008 rows over 126 experts an
+// earlier form took 484 us with four rows an instruction, 406 with 16 bytes a thread, 273 without any copies).
 //
 // Tiles are dealt out to a persistent grid in whole rounds; what is left over is cut evenly along K, and a tile that several
 // CTAs share is finished by the one that has its first group, which adds the others' sums in their order.
 //
-// Measured (gate and up, then down): 8192 rows over 8 experts, 4096 x 2 x 14336 and back, 1405 and 714 us, 1369 and 1347 TFLOP/s:
-// a group takes 1770 cycles of which the products are 1024; the rest are hand-overs between the roles and, in the first, the
-// epilogue (37 us).  2 rows of one token: 34 and 21 us, 3.6 TB/s, at 1050 cycles a group: issue slots 52 % busy, operands
-// 315 cycles, the rest their hand-over (750 a group with no work but theirs) and the 7 us of start and joins.  192 rows over 8
-// experts: 129 and 75 us, 3.8 TB/s.  32008 rows over 126 experts, 2048 x 2 x 768: 228 and 144 us, of which 27 put rows in order and 12
-// and 31 are the epilogue.
+// Measured in graphs, inputs out of L2 (gate and up, then down): 8192 rows over 8 experts, 4096 x 2 x 14336 and back, 1410 and
+// 720 us, 1365 and 1335 TFLOP/s: a group takes 1770 cycles of which the products are 1024; the rest are hand-overs between the roles
+// and, in the first, the epilogue (37 us).  2 rows of one token: 34 and 21 us, 3.6 TB/s, at 1050 cycles a group: issue slots 54 %
+// busy, operands 315 cycles, the rest their hand-over (750 a group with no work but theirs) and the 7 us of start and joins.  192 rows
+// over 8 experts: 129 and 75 us, 3.8 TB/s.  32008 rows over 126 experts, 2048 x 2 x 768: 230 and 144 us, of which 27 put rows in order
+// and 12 and 31 are the epilogue.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -612,7 +612,8 @@ __global__ void __launch_bounds__(256) moe_order_kernel(const MoeGemmArgs a, uin
   }
 }
 
-// Rows of a tile: by the rows that an expert has on average, as their distribution is known on the device only.  Tiles of 16, 64
+// Rows of a tile: by the rows that an expert has on average, choices without an expert counted, as more is known on the device
+// only; a hot expert among idle ones, or a rank that holds few of the experts, gets tiles that are small or large for it.  Tiles of 16, 64
 // and 128 rows, us: 8 experts of 4096 x 2 x 14336, 8 rows of each 118, 121, 135; 12 rows 133, 123, 138; 60 rows 452, 189, 199; 128
 // experts of 2048 x 2 x 768, 8 rows 60, 61, 67; 12 rows 71, 64, 73; 80 rows 270, 118, 120; 64 experts of 2048 x 2 x 1408, 100 rows 301,
 // 121, 111.

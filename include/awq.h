@@ -581,7 +581,10 @@ awq_status awq_moe_unprepack(const void *packed, int32_t experts, int64_t K, int
  * with unspecified results.  The result does not depend on timing: split sums are added in a fixed order.
  * x_stride % 8 == 0 and >= K, 1 <= x_rows <= 2^30, R <= 2^30; sizes otherwise as for awq_moe_prepack.  R = 0 is a no-op.
  * Workspace: awq_moe_gemm_workspace_bytes(), same contract as awq_gemv's; its CTAs wait (bounded) for one another's
- * partial sums, so the call assumes that they can all be resident at once.
+ * partial sums.  They need not all be resident at once: a CTA waits only for those of higher index, which publish theirs before
+ * they wait themselves.  But each has to get there within the 2 s that a wait lasts, so nothing else may hold the SMs for long.
+ * fp32 sums of a group are formed before its scale: bf16 rows whose 128 products |x (q - z)| 2^-7 add up beyond 2^128, and bf16
+ * scales of 2^121 and more, overflow.
  */
 size_t awq_moe_gemm_workspace_bytes(int64_t R, int32_t experts, int64_t K, int64_t N, int32_t gated);
 awq_status awq_moe_gemm(const uint16_t *x, int64_t x_stride, int64_t x_rows, const void *packed,
@@ -603,7 +606,8 @@ awq_status awq_moe_combine(const void *y, int32_t y_fp32, const int32_t *place, 
 /*
  * awq_moe -- the whole sparse feed-forward layer: awq_moe_gemm of x [T, K] (row stride x_stride) with the gated `up`
  * (experts x [K, 2 inner]), awq_moe_gemm of its rows with `down` (experts x [inner, H]) in fp32, awq_moe_combine.  The rows
- * between up and down have x's type; the results are those of the three calls.  Plan and weights as from awq_moe_route.
+ * between up and down have x's type, as those of any two layers have: in fp16 one beyond 65504 becomes infinite, and its token's
+ * results infinite or NaN.  The results are those of the three calls.  Plan and weights as from awq_moe_route.
  * out may share memory with x, which is read before anything is written, and may be the residual as for awq_moe_combine.
  * Workspace: awq_moe_workspace_bytes(), which holds the rows between the products too; contract as for awq_moe_gemm's.
  */
@@ -627,7 +631,8 @@ awq_status awq_moe(const uint16_t *x, int64_t x_stride, const void *up, const vo
  * codes 0, so that the product shows it.  x 16-bit [M, K] with row stride x_stride; K % 16 == 0, 16 <= K <= 2^20,
  * x_stride % 8 == 0 and >= K, 0 <= M <= 2^30.
  *
- * awq_fp8_gemm -- y[m, n] = RN16(sum_g s_x[g, m] s_w[n / 128, g] sum_{k in block g} xq[m, k] wq[n, k]), sums in fp32:
+ * awq_fp8_gemm -- y[m, n] = RN16(sum_g s_x[g, m] s_w[n / 128, g] sum_{k in block g} xq[m, k] wq[n, k]), sums in fp32,
+ * as the product s_x s_w is, which has fewer bits below 2^-126 and none below 2^-150:
  * the products of one block on the tensor cores, the blocks' sums scaled and added in registers.  y [M, N] dense,
  * fp16 or bf16; N % 8 == 0, 8 <= N <= 2^20.  Workspace: awq_fp8_gemm_workspace_bytes(), contract and residency as for
  * awq_moe_gemm's.  M = 0 is a no-op.

@@ -263,3 +263,15 @@ def test_growing_workspaces_while_calls_are_queued(awq):  # noqa: F811
         assert all(torch.equal(g, w) for g, w in zip(got, want))
         del junk
     assert awq.awq_last_device_error() == 0
+
+
+@pytest.mark.parametrize("tokens", [4, 60, 900])
+def test_rows_between_up_and_down_beyond_fp16_show_in_their_token_alone(awq, tokens):  # noqa: F811
+    layers = Layers(awq, tokens)
+    x = layers.x(3)
+    want = layers.experts(x)
+    x[2] = torch.where(x[2] < 0, -30000.0, 30000.0)
+    got = layers.experts(x)
+    assert not got[2].isfinite().any()
+    others = torch.arange(tokens, device="cuda") != 2
+    assert got[others].isfinite().all() and torch.equal(got[others], want[others])

@@ -125,13 +125,14 @@ def _stream(stream) -> int | None:
 
 
 # A call may be several launches that hand data on through its workspace, and the interpreter runs other threads
-# meanwhile: whoever takes a workspace that other calls share keeps its lock from the taking to the last launch.
-_locks: dict[tuple, threading.Lock] = {}
+# meanwhile: whoever takes a workspace that other calls share keeps its lock from the taking to the last launch.  A
+# signal handler or finalizer that calls from within the taking has all its launches before the first of this call.
+_locks: dict[tuple, threading.RLock] = {}
 
 
-def _lock_of(*key) -> threading.Lock:
+def _lock_of(*key) -> threading.RLock:
     lock = _locks.get(key)
-    return lock if lock is not None else _locks.setdefault(key, threading.Lock())
+    return lock if lock is not None else _locks.setdefault(key, threading.RLock())
 
 
 # One zero-filled workspace per device, grown on demand.  The library leaves its tile

@@ -52,7 +52,7 @@ class Library:
 def on_host(awq, monkeypatch):
     """The binding with the stand-in and two streams' workspaces in host memory; the stream of a thread is its own choice."""
     library, stream, fp8_out = Library(), threading.local(), awq._fp8_out
-    spaces = {handle: torch.zeros(256, dtype=torch.uint8) for handle in (7, 8)}
+    spaces = {handle: torch.zeros(256, dtype=torch.uint8) for handle in (7, 8, 9)}
     monkeypatch.setattr(awq, "lib", library)
     for check in ("_need", "_on_current_gpu"):
         monkeypatch.setattr(awq, check, lambda *a: None)
@@ -171,6 +171,24 @@ def test_each_threads_default_stream_is_another(awq):
 
     run_threads(work)
     assert keys[0][0] != keys[1][0] and keys[0][1] == keys[1][1] == (0, 5)
+
+
+def test_a_call_from_within_the_taking_of_a_workspace_goes_first(awq, on_host, monkeypatch):
+    """As a signal handler or a finalizer makes it, on the thread that holds the lock."""
+    call, taking, inner = layers(awq)["awq_fp8_linear"], awq._layer_workspace, []
+
+    def interrupted(*args):
+        if not inner:
+            inner.append(on_host.library.calls)
+            call()
+            inner.append(on_host.library.calls)
+        return taking(*args)
+
+    monkeypatch.setattr(awq, "_layer_workspace", interrupted)
+    done = threading.Thread(target=lambda: (setattr(on_host.stream, "handle", 9), call()), daemon=True)
+    done.start()
+    done.join(20)
+    assert not done.is_alive() and inner == [0, 1] and on_host.library.calls == 2
 
 
 def test_workspaces_are_made_anew_after_an_expired_wait(awq, monkeypatch):

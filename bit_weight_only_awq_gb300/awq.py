@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import itertools
 import os
 import re
 import threading
@@ -627,9 +628,21 @@ _kv4_workspaces: dict[tuple, torch.Tensor] = {}
 _kv4_outgrown: list[torch.Tensor] = []
 
 
+class _Thread(threading.local):
+    """A number for each thread.  That of one that has ended, whose stream may still be busy, is not given out again."""
+
+    numbers = itertools.count()
+
+    def __init__(self):
+        self.number = next(_Thread.numbers)
+
+
+_thread = _Thread()
+
+
 def _stream_key(device: torch.device, handle: int) -> tuple:
     """What the calls that share a workspace have in common.  Handle 2 is each thread's own default stream."""
-    return (device.index, handle) if handle != 2 else (device.index, handle, threading.get_ident())
+    return (device.index, handle) if handle != 2 else (device.index, handle, _thread.number)
 
 
 def _call_on_stream(name, fn, workspace, shared, device: torch.device, handle: int, *args) -> None:

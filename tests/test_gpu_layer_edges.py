@@ -275,3 +275,100 @@ def test_rows_between_up_and_down_beyond_fp16_show_in_their_token_alone(awq, tok
     assert not got[2].isfinite().any()
     others = torch.arange(tokens, device="cuda") != 2
     assert got[others].isfinite().all() and torch.equal(got[others], want[others])
+
+
+@pytest.mark.parametrize("tokens", [1, 2, 40, 60, 300, 900])
+def test_graphs_of_every_form(awq, tokens):  # noqa: F811
+    """Captured with a workspace of its own and replayed on other inputs: rows four at a time and in order, tiles of all heights,
+    codes inside the product and before it."""
+    layers = Layers(awq, tokens)
+    x, out = layers.x(0), torch.empty(tokens, 512, dtype=torch.float16, device="cuda")
+    spaces = [torch.zeros(n, dtype=torch.uint8, device="cuda") for n in
+              (awq.awq_moe_workspace_bytes(tokens, 2, layers.up, layers.down), awq.awq_fp8_linear_workspace_bytes(tokens, 512, 512))]
+    layers.fp8(layers.experts(x))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layers.fp8(layers.experts(x, workspace=spaces[0]), workspace=spaces[1], out=out)
+    for i in range(1, 4):
+        x.copy_(layers.x(i))
+        graph.replay()
+        assert torch.equal(out, layers.fp8(layers.experts(layers.x(i))))
+    assert awq.awq_last_device_error() == 0
+
+
+def fp8_reference(awq, x, wq, s_w):  # noqa: F811
+    """float64 product of the codes that x quantizes to, and its magnitudes."""
+    xq, s_x = awq.awq_fp8_quant_act(x)
+    (m, k), n = x.shape, wq.shape[0]
+    a = xq.double() * s_x.double().t().repeat_interleave(128, 1)[:, :k]
+    w = wq.double() * s_w.double().repeat_interleave(128, 0)[:n].repeat_interleave(128, 1)[:, :k]
+    return a @ w.t(), a.abs() @ w.abs().t()
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 16, 8), (2, 16, 8), (3, 16, 8), (1, 2 ** 20, 8), (2, 2 ** 20, 8), (70, 2 ** 20, 8), (1, 16, 2 ** 20),
+                                   (20, 16, 2 ** 20), (200, 16, 2 ** 20), (2 ** 22 + 5, 16, 8)])
+def test_e4m3_layer_at_the_ends_of_its_sizes(awq, M, K, N):  # noqa: F811
+    """The bound of the operator's own test: (27 + K / 128) 2^-23 of the magnitudes and half a step."""
+    gen = torch.Generator(device="cuda").manual_seed(M + K + N)
+    x = torch.randn(M, K, generator=gen, device="cuda").half()
+    wq = torch.randn(N, K, generator=gen, device="cuda").mul_(100).clamp_(-448, 448).to(torch.float8_e4m3fn)
+    s_w = (0.5 + torch.rand(-(-N // 128), -(-K // 128), generator=gen, device="cuda")) * 1e-3 / K ** 0.5
+    y = awq.awq_fp8_linear(x, wq, s_w)
+    rows = torch.arange(M, device="cuda") if M < 1000 else torch.tensor([0, 1, M // 2, 2 ** 22 - 1, 2 ** 22, M - 1], device="cuda")
+    want, mag = fp8_reference(awq, x[rows], wq, s_w)
+    err = (27 + K / 128) * 2.0 ** -23 * mag
+    tol = err + 2.0 ** -11 * (want.abs() + err) + 2.0 ** -25
+    off = (y[rows].double() - want).abs()
+    assert (off <= tol).all(), (off / tol).max()
+    assert awq.awq_last_device_error() == 0
+
+
+@pytest.mark.parametrize("rows,K,N", [(1, 2 ** 20, 32), (20, 2 ** 20, 64), (90, 2 ** 20, 32), (1, 128, 2 ** 20), (40, 128, 2 ** 20),
+                                      (200, 128, 2 ** 20)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_grouped_product_at_the_ends_of_its_sizes(awq, rows, K, N, gated):  # noqa: F811
+    """(8 + K / 8) 2^-23 of the magnitudes, silu's share and half a step, as in the operator's own test."""
+    if gated and N % 64:
+        N = 64
+    gen = torch.Generator(device="cuda").manual_seed(rows + N)
+    words = torch.randint(-2 ** 31, 2 ** 31, (1, K, N // 8), generator=gen, device="cuda", dtype=torch.int32)
+    scales = (0.2 / K ** 0.5 * (0.5 + torch.rand(1, K // 128, N, generator=gen, device="cuda"))).half()
+    w = awq.awq_moe_prepack(words, None, scales, gated=gated)
+    x = torch.randn(rows, K, generator=gen, device="cuda").half()
+    order = torch.arange(rows, dtype=torch.int32, device="cuda")
+    y = awq.awq_moe_gemm(x, w, awq.MoePlan(torch.tensor([0, rows], dtype=torch.int32, device="cuda"), order, order, 1))
+    shift = torch.tensor([0, 16, 4, 20, 8, 24, 12, 28], dtype=torch.int32, device="cuda")
+    a, mag = (torch.zeros(rows, N, dtype=torch.float64, device="cuda") for _ in range(2))
+    step = max(1, 2 ** 26 // N // 128) * 128
+    for k in range(0, K, step):
+        q = (((words[0, k : k + step, :, None] >> shift) & 15).flatten(-2) - 8).double()
+        q *= scales[0, k // 128 : (k + step) // 128].double().repeat_interleave(128, 0)[: q.shape[0]]
+        part = x[:, k : k + step].double()
+        a += part @ q
+        mag += part.abs() @ q.abs()
+    err = (8 + K / 8) * 2.0 ** -23 * mag
+    if gated:
+        (g, u), (dg, du) = a.chunk(2, dim=1), err.chunk(2, dim=1)
+        s = g * torch.sigmoid(g)
+        a = s * u
+        err = 1.1 * u.abs() * dg + (s.abs() + 1.1 * dg) * du + 2.0 ** -20 * a.abs()
+    tol = err + 2.0 ** -11 * (a.abs() + err) + 2.0 ** -25
+    off = (y.double() - a).abs()
+    assert (off <= tol).all(), (off / tol).max()
+    assert awq.awq_last_device_error() == 0
+
+
+def test_plan_of_many_rows(awq):  # noqa: F811
+    R, E = 2 ** 26 + 77, 200
+    ids = torch.randint(-1, E + 1, (R, 1), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda", dtype=torch.int32)
+    plan = awq.awq_moe_plan(ids, E)
+    flat = torch.where((ids >= 0) & (ids < E), ids, E).flatten()
+    order = torch.sort(flat, stable=True).indices.int()
+    n = int((flat < E).sum())
+    count = torch.bincount(flat, minlength=E + 1)
+    assert torch.equal(plan.offsets.long(), torch.cat((count.new_zeros(1), count[:E].cumsum(0))))
+    assert torch.equal(plan.order[:n], order[:n]) and (plan.order[n:] == -1).all()
+    place = torch.full((R,), -1, dtype=torch.int32, device="cuda")
+    place[order[:n].long()] = torch.arange(n, dtype=torch.int32, device="cuda")
+    assert torch.equal(plan.place, place)

@@ -118,6 +118,8 @@ awq_status awq_dequant(const int32_t *qweight, const int32_t *qzeros, const uint
  * (cudaMemsetAsync); every call that completes leaves its tile counters at
  * zero again, so consecutive calls on one stream can reuse it without
  * re-zeroing.  Calls that may run concurrently need separate workspaces.
+ * A call may be several launches that hand data on through the workspace, so host threads that
+ * share one on a stream must not enter their calls at the same time.
  * After AWQ_ETIMEOUT, zero the workspace again before reusing it.
  */
 size_t awq_workspace_bytes(awq_op op, int64_t M, int64_t K, int64_t N, int32_t split_k);
